@@ -70,9 +70,12 @@ extern "C" {
 
 typedef struct specdec_ctx* specdec_handle_t;
 
-/* dtype of target_logits (draft_probs are always float32) */
+/* dtype of target_logits (draft_probs are always float32): F32 or BF16; the
+ * cache's operators take BF16 and F16 rows and BF16, F16 and E4M3 caches */
 #define SPECDEC_F32 0
 #define SPECDEC_BF16 1
+#define SPECDEC_F16 2
+#define SPECDEC_E4M3 3
 
 /* status codes */
 #define SPECDEC_OK 0
@@ -89,7 +92,10 @@ typedef struct specdec_ctx* specdec_handle_t;
 #define SPECDEC_DEVERR_BAD_CU 2u
 #define SPECDEC_DEVERR_CAPACITY 4u
 #define SPECDEC_DEVERR_TIMEOUT 8u
-#define SPECDEC_DEVERR_BAD_TREE 16u   /* specdec_tree_verify: a node's parent is not an earlier node */
+#define SPECDEC_DEVERR_BAD_TREE 16u   /* a node's parent is not an earlier node, an accepted path does not rise, or
+                                         a tree is larger than SPECDEC_MAX_TREE_NODES (attention) */
+#define SPECDEC_DEVERR_BAD_CACHE 32u  /* a length, slot, page or position outside the cache, its page table or the
+                                         rotary table */
 
 /* execution paths (specdec_set_path); AUTO picks per call */
 #define SPECDEC_PATH_AUTO 0
@@ -240,6 +246,166 @@ int specdec_tree_verify(specdec_handle_t h, const void* target_logits, int dtype
                         const int32_t* node_parent, const int32_t* cu_num_nodes, int B, int V,
                         float T, uint64_t seed, uint64_t request_offset, int32_t* out_tokens,
                         int32_t* out_num_accepted, int32_t* out_path, void* stream);
+
+/* ---- verification from given random numbers --------------------------------
+ * The chain verification of specdec_rejection_sample for callers that hold
+ * probabilities and draw their own random numbers (an engine with one generator
+ * for all of its sampling, a replay of a recorded step): same batch layout, same
+ * outputs, no generator and no softmax.
+ *   target_probs     device float32 rows of V probabilities, target_row_stride
+ *                    elements apart (>= V), N_t = n_draft_positions + B rows
+ *   draft_probs      device float32 rows, draft_row_stride apart, N_d rows; NULL:
+ *                    a one-hot drafter, q_i = [v == x_i] (no row is read)
+ *   draft_ids        device [N_d] int32 (may be NULL when N_d == 0)
+ *   accept_uniforms  device [N_d] float32 r_i in [0, 1) (may be NULL when N_d == 0)
+ *   sample_uniforms  device [B] float32 s_b in [0, 1)
+ *   n_draft_positions N_d = cu[B]: the rows that the arrays hold
+ * Draft i is accepted iff r_i < min(1, p_i(x_i) / q_i(x_i)), decided exactly
+ * (r_i < 1 and the 48-bit product r_i q_i(x_i) < p_i(x_i); an id outside [0, V)
+ * is rejected and sets SPECDEC_DEVERR_BAD_DRAFT_ID).  The extra token is the
+ * inverse of the cumulative weights in index order: the first v with
+ * sum_{j <= v} w(j) > s_b sum_j w(j), w = max(0, p_n - q_n) after a rejection
+ * (p_n where that is 0 everywhere) and w = p_gamma for the bonus, in sums held
+ * to about 2^-48 of the total.  Entries that are not above 0 (NaN among them)
+ * weigh nothing; a row without weight gives token 0.  Rows are not normalised.
+ * out_tokens [N_t] and out_num_accepted [B] as in specdec_rejection_sample;
+ * a request whose cu range is malformed or passes N_d writes nothing
+ * (SPECDEC_DEVERR_BAD_CU).  One launch, no workspace: calls on one handle may
+ * overlap on several streams. */
+int specdec_rejection_sample_given(specdec_handle_t h, const float* target_probs,
+                                   int64_t target_row_stride, const float* draft_probs,
+                                   int64_t draft_row_stride, const int32_t* draft_ids,
+                                   const int32_t* cu_num_draft_tokens,
+                                   const float* accept_uniforms, const float* sample_uniforms,
+                                   int B, int V, int64_t n_draft_positions, int32_t* out_tokens,
+                                   int32_t* out_num_accepted, void* stream);
+
+/* ---- the paged key/value cache of the verified nodes -----------------------
+ * What a target's layer does around the verification of drafted nodes (chains
+ * or token trees, in specdec_tree_verify's layout): turn and write the nodes'
+ * keys and values (append), attend to the context and to each node's ancestors
+ * (attention), and after the verification put the accepted branch where the
+ * next step expects it (commit); rows can be read back (read).
+ *
+ * A cache is two arrays [num_pages, num_kv_heads, page_size, head_dim] of 16-bit
+ * or e4m3 values, e4m3 with one positive float32 scale per row ([num_pages,
+ * num_kv_heads, page_size]): value = e4m3 * scale.  Slot s of request b is row
+ * s % page_size of page page_table[b][s / page_size].  head_dim is 64 or 128;
+ * num_pages * num_kv_heads * page_size < 2^31 rows, at any byte offset.  A page
+ * belongs to one request at a time where it is written. */
+typedef struct specdec_cache {
+  void* k;              /* 16-byte aligned */
+  void* v;
+  float* k_scale;       /* SPECDEC_E4M3 only, else NULL */
+  float* v_scale;
+  int dtype;            /* SPECDEC_BF16, SPECDEC_F16 or SPECDEC_E4M3 */
+  int num_kv_heads;
+  int head_dim;
+  int page_size;
+  int64_t num_pages;
+} specdec_cache_t;
+
+/* The nodes of a step.  Request b owns rows cu[b] .. cu[b+1]-1 (none is allowed)
+ * of the N rows that the call's arrays hold; node j of it stands at slot
+ * lengths[b] + j, and at position lengths[b] + depth(j).  parent holds indices
+ * within the request (node 0: -1, else an earlier node); NULL means chains. */
+typedef struct specdec_nodes {
+  const int32_t* page_table;   /* device [B] rows of max_pages page ids, table_stride apart */
+  int64_t table_stride;
+  int max_pages;
+  const int32_t* lengths;      /* device [B]: context slots already filled */
+  const int32_t* cu;           /* device [B+1] */
+  const int32_t* parent;       /* device [N] or NULL */
+  int B;
+  int64_t N;
+} specdec_nodes_t;
+
+#define SPECDEC_MAX_TREE_NODES 1024   /* nodes of a request with parents (attention) */
+
+/* Rules of all four: rows of `dtype` (SPECDEC_BF16 or SPECDEC_F16; a 16-bit
+ * cache's own type) with head_dim contiguous, 16-byte aligned, strides in
+ * elements and multiples of 8.  Host-checked problems return a negative status.
+ * A cu range that is malformed or passes N (SPECDEC_DEVERR_BAD_CU), a negative
+ * length, a slot or page outside the table or the cache, a position outside the
+ * rotary table (SPECDEC_DEVERR_BAD_CACHE) or a malformed tree
+ * (SPECDEC_DEVERR_BAD_TREE) set bits of the handle's error word; nothing outside
+ * the arrays is touched, and what such a node would have written is left alone
+ * unless stated below.  Rows behind the last request are left as they were.  The
+ * calls use none of the handle's workspace, so calls on one handle may overlap
+ * on several streams where their arrays allow it. */
+
+/* Writes the nodes' keys and values into their slots, and turns q and k by the
+ * nodes' positions on the way.
+ *   k, v       [N, num_kv_heads, head_dim]
+ *   q          [N, q_heads, head_dim] or NULL; out_q receives the turned rows,
+ *              contiguous (both or neither; a row whose position is outside the
+ *              table or whose tree is malformed becomes zeros)
+ *   rotary     device float32 [rotary_positions, 2, rotary_dim / 2], cos then sin
+ *              of each position, or NULL (q is then copied)
+ *   rotary_dim leading dimensions that turn: a multiple of 16 up to head_dim.
+ *              Pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved:
+ *              a' = a cos - b sin, b' = b cos + a sin, each product and the sum
+ *              rounded to 32 bits
+ * 16-bit caches round the 32-bit result once.  e4m3 caches store, for each row,
+ * scale = max(largest magnitude, 2^-40) times 1/448 (both in 32 bits) and the
+ * values / scale rounded to e4m3 (nearest, ties to even), of the 32-bit result; a
+ * NaN makes its row NaN. */
+int specdec_cache_append(specdec_handle_t h, const specdec_cache_t* cache,
+                         const specdec_nodes_t* nodes, int dtype, const void* k,
+                         int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                         int64_t v_row_stride, int64_t v_head_stride, const void* q,
+                         int64_t q_row_stride, int64_t q_head_stride, int q_heads, void* out_q,
+                         const float* rotary, int rotary_dim, int64_t rotary_positions,
+                         int interleaved, void* stream);
+
+/* Reads rows back: row r of request b (cu[b] <= r < cu[b+1]) is slot lengths[b] +
+ * r - cu[b]; out_k, out_v are contiguous [N, num_kv_heads, head_dim] of `dtype`,
+ * e4m3 values times their scale rounded once.  A slot that the cache does not
+ * hold reads as zeros.  parent is ignored. */
+int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
+                       const specdec_nodes_t* nodes, int dtype, void* out_k, void* out_v,
+                       void* stream);
+
+/* Attention of every node over its request's context (slots 0 .. lengths[b]-1)
+ * and its ancestors and itself (which append has written):
+ *   out[i, h] = sum_s softmax_s(softmax_scale q[i, h] . k[s, h / (q_heads /
+ *   num_kv_heads)]) v[s, same]
+ * q [N, q_heads, head_dim] strided, out contiguous [N, q_heads, head_dim].
+ * q_heads is a multiple of num_kv_heads.  Scores, maxima and sums are held in 32
+ * bits; weights meet the values rounded to 16 bits (to f16 over e4m3 caches).
+ * Keys in slots that the cache does not hold count as hidden (BAD_CACHE); a row
+ * that sees no key is zeros.  What a masked slot holds, infinities and NaN
+ * among it, reaches no row.  Requests whose cu, length or tree is out of range
+ * write nothing.
+ *   workspace  device memory of at least specdec_tree_attention_workspace()
+ *              bytes, 16-byte aligned, no initial contents; calls that may
+ *              overlap need one each */
+int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
+                           const specdec_nodes_t* nodes, int dtype, const void* q,
+                           int64_t q_row_stride, int64_t q_head_stride, int q_heads,
+                           float softmax_scale, void* out, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of specdec_tree_attention for any lengths, or a negative
+ * status. */
+int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache_t* cache,
+                                         int B, int64_t N, int q_heads);
+
+/* After the verification: moves the accepted nodes' rows (and scales) to the
+ * slots behind the root, lengths[b] + path[d] -> lengths[b] + 1 + d, and writes
+ * out_lengths[b] = lengths[b] + 1 + num_accepted[b] (lengths[b] for a request
+ * without nodes).
+ *   num_accepted  device [B]
+ *   path          device [N], the accepted nodes of request b in its first
+ *                 num_accepted[b] slots, rising (specdec_tree_verify's out_path);
+ *                 NULL for chains, whose rows stand where they belong
+ *   out_lengths   device [B]; may be nodes->lengths
+ * Slots behind the accepted ones keep their contents.  A count outside the
+ * request's nodes or a path that does not rise moves nothing and leaves the
+ * length (SPECDEC_DEVERR_BAD_TREE). */
+int specdec_cache_commit(specdec_handle_t h, const specdec_cache_t* cache,
+                         const specdec_nodes_t* nodes, const int32_t* num_accepted,
+                         const int32_t* path, int32_t* out_lengths, void* stream);
 
 /* Reads the handle's sticky device error word (SPECDEC_DEVERR_* bits) into
  * *device_error and clears it.  Queues the read on `stream` and waits for it, so

@@ -14,6 +14,8 @@ LIB_PATH = os.path.join(_PKG, "libspecdec.so")
 
 SPECDEC_F32 = 0
 SPECDEC_BF16 = 1
+SPECDEC_F16 = 2
+SPECDEC_E4M3 = 3
 
 SPECDEC_OK = 0
 SPECDEC_ERR_INVALID_ARG = -1
@@ -29,6 +31,9 @@ SPECDEC_DEVERR_BAD_CU = 2
 SPECDEC_DEVERR_CAPACITY = 4
 SPECDEC_DEVERR_TIMEOUT = 8
 SPECDEC_DEVERR_BAD_TREE = 16
+SPECDEC_DEVERR_BAD_CACHE = 32
+
+SPECDEC_MAX_TREE_NODES = 1024
 
 SPECDEC_FAULT_NONE = 0
 SPECDEC_FAULT_PAIR_STALL = 1
@@ -84,6 +89,29 @@ _rs_noalloc = _fn("specdec_rejection_sample_noalloc", _i32, _vp, _i32, _vp, _vp,
                   _f32, _u64, _i64, _vp, _vp, _vp, _vp, _vp)
 _tree = _fn("specdec_tree_verify", _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _f32,
             _u64, _u64, _vp, _vp, _vp, _vp)
+_rs_given = _fn("specdec_rejection_sample_given", _i32, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                _vp, _i32, _i32, _i64, _vp, _vp, _vp)
+
+
+class specdec_cache_t(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("dtype", _i32),
+                ("num_kv_heads", _i32), ("head_dim", _i32), ("page_size", _i32),
+                ("num_pages", _i64)]
+
+
+class specdec_nodes_t(ctypes.Structure):
+    _fields_ = [("page_table", _vp), ("table_stride", _i64), ("max_pages", _i32), ("lengths", _vp),
+                ("cu", _vp), ("parent", _vp), ("B", _i32), ("N", _i64)]
+
+
+_cp, _np = ctypes.POINTER(specdec_cache_t), ctypes.POINTER(specdec_nodes_t)
+_append = _fn("specdec_cache_append", _i32, _vp, _cp, _np, _i32, _vp, _i64, _i64, _vp, _i64, _i64,
+              _vp, _i64, _i64, _i32, _vp, _vp, _i32, _i64, _i32, _vp)
+_read = _fn("specdec_cache_read", _i32, _vp, _cp, _np, _i32, _vp, _vp, _vp)
+_attn_ws = _fn("specdec_tree_attention_workspace", _i64, _vp, _cp, _i32, _i64, _i32)
+_attn = _fn("specdec_tree_attention", _i32, _vp, _cp, _np, _i32, _vp, _i64, _i64, _i32, _f32, _vp,
+            _vp, _i64, _vp)
+_commit = _fn("specdec_cache_commit", _i32, _vp, _cp, _np, _vp, _vp, _vp, _vp)
 _status_string = _fn("specdec_status_string", ctypes.c_char_p, _i32)
 _destroy = _fn("specdec_destroy", _i32, _vp)
 
@@ -120,6 +148,41 @@ def specdec_rejection_sample_topk_topp(h, target_logits, dtype, draft_probs, dra
     return _rs_adj(h, target_logits, dtype, draft_probs, draft_ids, cu_num_draft_tokens, B, V, T,
                    top_k, top_p, seed & 0xFFFFFFFFFFFFFFFF, request_offset, out_tokens,
                    out_num_accepted, out_beta, out_target_prob, out_draft_prob, out_accept, stream)
+
+
+def specdec_rejection_sample_given(h, target_probs, target_row_stride, draft_probs,
+                                   draft_row_stride, draft_ids, cu_num_draft_tokens,
+                                   accept_uniforms, sample_uniforms, B, V, n_draft_positions,
+                                   out_tokens, out_num_accepted, stream) -> int:
+    return _rs_given(h, target_probs, target_row_stride, draft_probs, draft_row_stride, draft_ids,
+                     cu_num_draft_tokens, accept_uniforms, sample_uniforms, B, V,
+                     n_draft_positions, out_tokens, out_num_accepted, stream)
+
+
+def specdec_cache_append(h, cache, nodes, dtype, k, k_row_stride, k_head_stride, v, v_row_stride,
+                         v_head_stride, q, q_row_stride, q_head_stride, q_heads, out_q, rotary,
+                         rotary_dim, rotary_positions, interleaved, stream) -> int:
+    return _append(h, cache, nodes, dtype, k, k_row_stride, k_head_stride, v, v_row_stride,
+                   v_head_stride, q, q_row_stride, q_head_stride, q_heads, out_q, rotary,
+                   rotary_dim, rotary_positions, interleaved, stream)
+
+
+def specdec_cache_read(h, cache, nodes, dtype, out_k, out_v, stream) -> int:
+    return _read(h, cache, nodes, dtype, out_k, out_v, stream)
+
+
+def specdec_tree_attention_workspace(h, cache, B, N, q_heads) -> int:
+    return _attn_ws(h, cache, B, N, q_heads)
+
+
+def specdec_tree_attention(h, cache, nodes, dtype, q, q_row_stride, q_head_stride, q_heads,
+                           softmax_scale, out, workspace, workspace_bytes, stream) -> int:
+    return _attn(h, cache, nodes, dtype, q, q_row_stride, q_head_stride, q_heads, softmax_scale,
+                 out, workspace, workspace_bytes, stream)
+
+
+def specdec_cache_commit(h, cache, nodes, num_accepted, path, out_lengths, stream) -> int:
+    return _commit(h, cache, nodes, num_accepted, path, out_lengths, stream)
 
 
 def specdec_set_timing_events(h: int, before_rows, after_rows) -> int:
@@ -194,4 +257,6 @@ EXPORTED = ["specdec_create", "specdec_reserve", "specdec_rejection_sample",
             "specdec_set_fault_injection",
             "specdec_last_path", "specdec_uniform", "specdec_neg_log_uniform",
             "specdec_selection_mass", "specdec_rejection_sample_noalloc", "specdec_tree_verify",
+            "specdec_rejection_sample_given", "specdec_cache_append", "specdec_cache_read",
+            "specdec_tree_attention", "specdec_tree_attention_workspace", "specdec_cache_commit",
             "specdec_status_string", "specdec_destroy"]

@@ -1,0 +1,232 @@
+// Attention of drafted nodes over the paged cache: what its kernels share.
+//
+// Work is a flat list of units: for every request, kv head and row tile (an
+// item), one unit per tile of keys.  The units are split into as many equal
+// contiguous ranges as there are CTAs, so that ragged lengths leave no CTA
+// idle; an item that crosses a range leaves partial results (row maximum, sum
+// and weighted sum of values) that a second, dependent kernel joins.
+//
+// Rows of an item: r = node * group + head within the group, so one read of a
+// key serves every node and every query head that shares it.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/specdec.h"
+#include "cache.cuh"
+#include "device_common.cuh"
+
+namespace specdec {
+
+struct Request {
+  int64_t first;   // first node row
+  int64_t units;
+  int32_t n;       // nodes
+  int32_t len;     // context
+  int32_t rts;     // row tiles
+  int32_t tiles;   // key tiles
+};
+
+// The plan of request b for tiles of R rows and TK keys.  units = 0 for what
+// cannot be attended (no nodes, a cu or length out of range, a tree that is
+// too large); why gets the error bits.
+__host__ __device__ __forceinline__ Request attend_request(const CacheArgs& c, int group, int b, int R, int TK,
+                                                           uint32_t& why) {
+  Request q = {};
+  if (!node_range(c.cu, b, c.N, q.first, q.n)) {
+    why |= SPECDEC_DEVERR_BAD_CU;
+    return q;
+  }
+  q.len = c.lengths[b];
+  if (q.n == 0) return q;
+  if (q.len < 0 || (int64_t)q.len + q.n > (int64_t)c.geo.max_pages * c.geo.page_size) {
+    why |= SPECDEC_DEVERR_BAD_CACHE;
+    return q;
+  }
+  if (c.parent && q.n > kMaxTreeNodes) {
+    why |= SPECDEC_DEVERR_BAD_TREE;
+    return q;
+  }
+  q.rts = (int32_t)(((int64_t)q.n * group + R - 1) / R);
+  q.tiles = (int32_t)(((int64_t)q.len + q.n + TK - 1) / TK);
+  q.units = (int64_t)c.geo.kv_heads * q.rts * q.tiles;
+  return q;
+}
+
+#ifdef __CUDACC__
+
+struct ScanShared {
+  int64_t warp[32];
+  int64_t total;
+  int64_t before;
+  int32_t b;
+};
+
+// Units of all requests, and the request that holds unit `want(total)` with
+// the units before it.  Every thread of the block calls; NT threads.
+template <int NT, typename Want>
+__device__ __forceinline__ void find_unit(const CacheArgs& c, int group, int R, int TK, Want want,
+                                          ScanShared& sh, uint32_t& why) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (c.B + NT - 1) / NT;
+  const int b0 = min(c.B, tid * per), b1 = min(c.B, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += attend_request(c, group, b, R, TK, why).units;
+  int64_t scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if (lane >= o) scan += up;
+  }
+  if (lane == 31) sh.warp[warp] = scan;
+  if (tid == 0) sh.b = -1;
+  __syncthreads();
+  if (tid == 0) {
+    int64_t t = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+      const int64_t x = sh.warp[w];
+      sh.warp[w] = t;
+      t += x;
+    }
+    sh.total = t;
+  }
+  __syncthreads();
+  const int64_t u = want(sh.total);
+  int64_t at = sh.warp[warp] + scan - mine;
+  if (at <= u && u < at + mine) {   // one thread at most
+    for (int b = b0; b < b1; ++b) {
+      const int64_t x = attend_request(c, group, b, R, TK, why).units;
+      if (u < at + x) {
+        sh.b = b;
+        sh.before = at;
+        break;
+      }
+      at += x;
+    }
+  }
+  __syncthreads();
+}
+
+// Ancestors (with itself) of node j as bits of `words` words; a parent that is
+// no earlier node ends the walk (false).
+__device__ __forceinline__ bool ancestor_bits(const int32_t* parent, int j, int words, uint32_t* bits) {
+  for (int w = 0; w < words; ++w) bits[w] = 0;
+  while (true) {
+    bits[j >> 5] |= 1u << (j & 31);
+    if (j == 0) return true;
+    const int up = parent[j];
+    if (up < 0 || up >= j) return false;
+    j = up;
+  }
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
+}
+
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ void from_float(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_float(float x, __half& y) { y = __float2half_rn(x); }
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Workspace: two partial slots per range, each R rows of D sums, then (max, sum).
+template <int R, int D>
+struct Partials {
+  float* sums;
+  float2* stats;
+  __host__ __device__ Partials(void* ws, int G)
+      : sums(static_cast<float*>(ws)), stats(reinterpret_cast<float2*>(sums + (int64_t)2 * G * R * D)) {}
+  static constexpr int64_t bytes(int G) { return (int64_t)2 * G * R * (D * 4 + 8); }
+};
+
+// Joins the partial results of the items that several ranges share.  A block
+// takes 8 rows of every row tile of one request and kv head.
+template <typename T, int R, int TK, int D>
+__global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, const int G) {
+  __shared__ ScanShared sh;
+  const CacheArgs& c = a.c;
+  const int group = a.q_heads / c.geo.kv_heads;
+  const int b = blockIdx.x / c.geo.kv_heads, h = blockIdx.x % c.geo.kv_heads;
+  uint32_t why = 0;
+  const Request q = attend_request(c, group, b, R, TK, why);
+  // units before request b: a block-wide sum
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t mine = 0, all = 0;
+  for (int i = tid; i < c.B; i += 128) {
+    const int64_t x = attend_request(c, group, i, R, TK, why).units;
+    all += x;
+    if (i < b) mine += x;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+    all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+  }
+  if (lane == 0) {
+    sh.warp[warp] = mine;
+    sh.warp[warp + 4] = all;
+  }
+  __syncthreads();
+  int64_t before = 0, units = 0;
+  for (int w = 0; w < 4; ++w) {
+    before += sh.warp[w];
+    units += sh.warp[w + 4];
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (q.units == 0) return;
+  const int ranges = (int)min((int64_t)G, units);
+  const Partials<R, D> part(a.workspace, G);
+  const int rows = q.n * group;
+  for (int rt = 0; rt < q.rts; ++rt) {
+    const int64_t u0 = before + ((int64_t)h * q.rts + rt) * q.tiles, u1 = u0 + q.tiles;
+    const int g0 = range_of(units, ranges, u0), g1 = range_of(units, ranges, u1 - 1);
+    const int r0 = blockIdx.y * 8;
+    if (g0 == g1 || rt * R + r0 >= rows) continue;
+    for (int rr = warp; rr < 8; rr += 4) {
+      const int r = r0 + rr;
+      if (rt * R + r >= rows) break;
+      float m = -INFINITY;
+      // a range holds the item in its first slot if it begins inside the item
+      float l = 0.0f;
+      float acc[D / 32];
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) acc[k] = 0.0f;
+      for (int g = g0; g <= g1; ++g) {
+        const int64_t slot = 2 * (int64_t)g + (range_begin(units, ranges, g) >= u0 ? 0 : 1);
+        const float2 s = part.stats[slot * R + r];
+        const float mn = fmaxf(m, s.x);
+        const float ref = mn == -INFINITY ? 0.0f : mn;
+        const float wo = ex2(m - ref), wn = ex2(s.x - ref);
+        l = l * wo + s.y * wn;
+        const float* v = part.sums + (slot * R + r) * D + lane * (D / 32);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) acc[k] = acc[k] * wo + (wn > 0.0f ? v[k] * wn : 0.0f);
+        m = mn;
+      }
+      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+      const int row = rt * R + r;
+      T* out = static_cast<T*>(a.out) +
+               ((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + lane * (D / 32);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) from_float(acc[k] * inv, out[k]);
+    }
+  }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace specdec

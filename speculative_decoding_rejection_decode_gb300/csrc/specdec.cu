@@ -8,6 +8,7 @@
 #include <cstring>
 #include <new>
 
+#include "cache.cuh"
 #include "kernels.cuh"
 #include "tree.cuh"
 
@@ -355,6 +356,58 @@ int launch_greedy(specdec_ctx* h, Params& P, bool vec_ok, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
+// ---- host checks of the cache's operators ------------------------------------
+constexpr int kMaxRequests = 1 << 20;   // of one call of these operators
+constexpr int kMaxHeads = 1 << 12;
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+bool rows_ok(const void* p, int64_t row, int64_t head) {
+  return p && aligned16(p) && row % 8 == 0 && head % 8 == 0;
+}
+
+// Checks a cache and its nodes and fills the kernels' view of them (all but the
+// error word).  any_dtype: rows of no type are passed (commit).
+int cache_args(const specdec_cache_t* cache, const specdec_nodes_t* nodes, int dtype, CacheArgs& c,
+               bool any_dtype = false) {
+  if (!cache || !nodes) return SPECDEC_ERR_INVALID_ARG;
+  const bool fp8 = cache->dtype == SPECDEC_E4M3;
+  if (!fp8 && cache->dtype != SPECDEC_BF16 && cache->dtype != SPECDEC_F16) return SPECDEC_ERR_UNSUPPORTED_DTYPE;
+  if (!any_dtype && ((dtype != SPECDEC_BF16 && dtype != SPECDEC_F16) || (!fp8 && dtype != cache->dtype)))
+    return SPECDEC_ERR_UNSUPPORTED_DTYPE;
+  if (cache->head_dim != 64 && cache->head_dim != 128) return SPECDEC_ERR_INVALID_ARG;
+  if (cache->num_kv_heads <= 0 || cache->num_kv_heads > kMaxHeads || cache->page_size <= 0 || cache->num_pages <= 0)
+    return SPECDEC_ERR_INVALID_ARG;
+  // row numbers are held in 32 bits (their byte offsets are not)
+  const int64_t page_rows = (int64_t)cache->num_kv_heads * cache->page_size;
+  if (cache->num_pages > ((int64_t)1 << 31) / page_rows || cache->num_pages * page_rows >= ((int64_t)1 << 31))
+    return SPECDEC_ERR_CAPACITY;
+  if (!cache->k || !cache->v || !aligned16(cache->k) || !aligned16(cache->v)) return SPECDEC_ERR_INVALID_ARG;
+  if (fp8 && (!cache->k_scale || !cache->v_scale)) return SPECDEC_ERR_INVALID_ARG;
+  if (nodes->B <= 0 || nodes->B > kMaxRequests || nodes->N < 0 || nodes->N >= ((int64_t)1 << 31))
+    return SPECDEC_ERR_INVALID_ARG;
+  if ((int64_t)nodes->B * cache->num_kv_heads >= ((int64_t)1 << 31)) return SPECDEC_ERR_CAPACITY;  // grid
+  if (nodes->max_pages <= 0 || nodes->table_stride < nodes->max_pages) return SPECDEC_ERR_INVALID_ARG;
+  if (!nodes->page_table || !nodes->lengths || !nodes->cu) return SPECDEC_ERR_INVALID_ARG;
+  c.k = cache->k;
+  c.v = cache->v;
+  c.ks = fp8 ? cache->k_scale : nullptr;
+  c.vs = fp8 ? cache->v_scale : nullptr;
+  c.geo.num_pages = cache->num_pages;
+  c.geo.table_stride = nodes->table_stride;
+  c.geo.kv_heads = cache->num_kv_heads;
+  c.geo.page_size = cache->page_size;
+  c.geo.max_pages = nodes->max_pages;
+  c.head_dim = cache->head_dim;
+  c.table = nodes->page_table;
+  c.lengths = nodes->lengths;
+  c.cu = nodes->cu;
+  c.parent = nodes->parent;
+  c.B = nodes->B;
+  c.N = nodes->N;
+  return SPECDEC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -581,6 +634,154 @@ int specdec_tree_verify(specdec_handle_t h, const void* target_logits, int dtype
   const int rc = launch_tree(a, dtype, h->num_sms, st);
   if (h->ev_after) cudaEventRecord(h->ev_after, st);
   return rc;
+}
+
+int specdec_rejection_sample_given(specdec_handle_t h, const float* target_probs,
+                                   int64_t target_row_stride, const float* draft_probs,
+                                   int64_t draft_row_stride, const int32_t* draft_ids,
+                                   const int32_t* cu_num_draft_tokens,
+                                   const float* accept_uniforms, const float* sample_uniforms,
+                                   int B, int V, int64_t n_draft_positions, int32_t* out_tokens,
+                                   int32_t* out_num_accepted, void* stream) {
+  if (!h || B <= 0 || B > kMaxRequests || V <= 0 || V > (1 << 30) || n_draft_positions < 0)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (!target_probs || !cu_num_draft_tokens || !sample_uniforms || !out_tokens || !out_num_accepted)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (n_draft_positions > 0 && (!draft_ids || !accept_uniforms)) return SPECDEC_ERR_INVALID_ARG;
+  if (target_row_stride < V || (draft_probs && draft_row_stride < V)) return SPECDEC_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok()) return SPECDEC_ERR_CUDA;
+  GivenArgs a = {};
+  a.p = target_probs;
+  a.q = draft_probs;
+  a.p_row = target_row_stride;
+  a.q_row = draft_row_stride;
+  a.ids = draft_ids;
+  a.cu = cu_num_draft_tokens;
+  a.accept_u = accept_uniforms;
+  a.sample_u = sample_uniforms;
+  a.B = B;
+  a.V = V;
+  a.N_d = n_draft_positions;
+  a.out_tokens = out_tokens;
+  a.out_nacc = out_num_accepted;
+  a.err = h->small;
+  a.vec_ok = target_row_stride % 4 == 0 && reinterpret_cast<uintptr_t>(target_probs) % 16 == 0 &&
+             (!draft_probs ||
+              (draft_row_stride % 4 == 0 && reinterpret_cast<uintptr_t>(draft_probs) % 16 == 0));
+  return launch_given(a, h->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int specdec_cache_append(specdec_handle_t h, const specdec_cache_t* cache,
+                         const specdec_nodes_t* nodes, int dtype, const void* k,
+                         int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                         int64_t v_row_stride, int64_t v_head_stride, const void* q,
+                         int64_t q_row_stride, int64_t q_head_stride, int q_heads, void* out_q,
+                         const float* rotary, int rotary_dim, int64_t rotary_positions,
+                         int interleaved, void* stream) {
+  AppendArgs a = {};
+  int rc = cache_args(cache, nodes, dtype, a.c);
+  if (rc != SPECDEC_OK) return rc;
+  if (nodes->N > 0 && (!rows_ok(k, k_row_stride, k_head_stride) || !rows_ok(v, v_row_stride, v_head_stride)))
+    return SPECDEC_ERR_INVALID_ARG;
+  if ((q != nullptr) != (out_q != nullptr)) return SPECDEC_ERR_INVALID_ARG;
+  if (q && (q_heads <= 0 || q_heads > kMaxHeads || !rows_ok(q, q_row_stride, q_head_stride) || !aligned16(out_q)))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (rotary && (!aligned16(rotary) || rotary_dim <= 0 || rotary_dim % 16 != 0 ||
+                 rotary_dim > cache->head_dim || rotary_positions <= 0))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (!h) return SPECDEC_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok()) return SPECDEC_ERR_CUDA;
+  a.c.err = h->small;
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.k_row = k_row_stride;
+  a.k_head = k_head_stride;
+  a.v_row = v_row_stride;
+  a.v_head = v_head_stride;
+  a.q_row = q_row_stride;
+  a.q_head = q_head_stride;
+  a.q_heads = q_heads;
+  a.out_q = out_q;
+  a.rotary = rotary;
+  a.rotary_dim = rotary ? rotary_dim : 0;
+  a.positions = rotary_positions;
+  a.interleaved = interleaved ? 1 : 0;
+  return launch_append(a, cache->dtype, dtype, h->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
+                       const specdec_nodes_t* nodes, int dtype, void* out_k, void* out_v,
+                       void* stream) {
+  ReadArgs a = {};
+  int rc = cache_args(cache, nodes, dtype, a.c);
+  if (rc != SPECDEC_OK) return rc;
+  if (nodes->N > 0 && (!out_k || !out_v || !aligned16(out_k) || !aligned16(out_v)))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (!h) return SPECDEC_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok()) return SPECDEC_ERR_CUDA;
+  a.c.err = h->small;
+  a.out_k = out_k;
+  a.out_v = out_v;
+  return launch_read(a, cache->dtype, dtype, h->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache_t* cache,
+                                         int B, int64_t N, int q_heads) {
+  if (!h || !cache || B <= 0 || B > kMaxRequests || N < 0 || (cache->head_dim != 64 && cache->head_dim != 128) ||
+      cache->num_kv_heads <= 0 || q_heads <= 0 || q_heads > kMaxHeads || q_heads % cache->num_kv_heads != 0)
+    return SPECDEC_ERR_INVALID_ARG;
+  return attend_workspace_bytes(B, N, cache->num_kv_heads, q_heads, cache->head_dim, h->num_sms);
+}
+
+int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
+                           const specdec_nodes_t* nodes, int dtype, const void* q,
+                           int64_t q_row_stride, int64_t q_head_stride, int q_heads,
+                           float softmax_scale, void* out, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  AttendArgs a = {};
+  int rc = cache_args(cache, nodes, dtype, a.c);
+  if (rc != SPECDEC_OK) return rc;
+  if (q_heads <= 0 || q_heads > kMaxHeads || q_heads % cache->num_kv_heads != 0 || !std::isfinite(softmax_scale))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (nodes->N > 0 && (!rows_ok(q, q_row_stride, q_head_stride) || !out || !aligned16(out)))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (!h) return SPECDEC_ERR_INVALID_ARG;
+  const int64_t need =
+      attend_workspace_bytes(nodes->B, nodes->N, cache->num_kv_heads, q_heads, cache->head_dim, h->num_sms);
+  if (need > 0 && (!workspace || !aligned16(workspace))) return SPECDEC_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return SPECDEC_ERR_CAPACITY;
+  DeviceGuard guard(h->device);
+  if (!guard.ok()) return SPECDEC_ERR_CUDA;
+  a.c.err = h->small;
+  a.q = q;
+  a.q_row = q_row_stride;
+  a.q_head = q_head_stride;
+  a.q_heads = q_heads;
+  a.scale_log2 = softmax_scale * kLog2e;
+  a.out = out;
+  a.workspace = workspace;
+  return launch_attend(a, cache->dtype, dtype, h->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int specdec_cache_commit(specdec_handle_t h, const specdec_cache_t* cache,
+                         const specdec_nodes_t* nodes, const int32_t* num_accepted,
+                         const int32_t* path, int32_t* out_lengths, void* stream) {
+  CommitArgs a = {};
+  int rc = cache_args(cache, nodes, SPECDEC_BF16, a.c, true);
+  if (rc != SPECDEC_OK) return rc;
+  if (!num_accepted || !out_lengths) return SPECDEC_ERR_INVALID_ARG;
+  if (!h) return SPECDEC_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok()) return SPECDEC_ERR_CUDA;
+  a.c.err = h->small;
+  a.accepted = num_accepted;
+  a.path = path;
+  a.out_lengths = out_lengths;
+  return launch_commit(a, cache->dtype, h->num_sms, static_cast<cudaStream_t>(stream));
 }
 
 int specdec_get_error(specdec_handle_t h, int* device_error, void* stream) {

@@ -13,7 +13,8 @@ from ._lib import (SPECDEC_BF16, SPECDEC_F32, SPECDEC_PATH_AUTO, SPECDEC_PATH_DU
                    specdec_get_error, specdec_last_path, specdec_neg_log_uniform,
                    specdec_selection_mass,
                    specdec_rejection_sample, specdec_rejection_sample_ex,
-                   specdec_rejection_sample_noalloc, specdec_rejection_sample_topk_topp,
+                   specdec_rejection_sample_given, specdec_rejection_sample_noalloc,
+                   specdec_rejection_sample_topk_topp,
                    specdec_reserve, specdec_set_adjust_counters,
                    specdec_set_path, specdec_set_timing_events, specdec_status_string,
                    specdec_tree_verify, specdec_uniform)
@@ -124,6 +125,50 @@ class Verifier:
         node; node_parent holds indices within each request (node 0: -1)."""
         return _tree_call(self, target_logits, draft_probs, node_tokens, node_parent,
                           cu_num_nodes, T, seed, request_offset, with_path, out)
+
+    def sample_given(self, target_probs: torch.Tensor, draft_probs: torch.Tensor | None,
+                     draft_ids: torch.Tensor, cu_num_draft_tokens: torch.Tensor,
+                     accept_uniforms: torch.Tensor, sample_uniforms: torch.Tensor, *,
+                     out: VerifyOutput | None = None) -> VerifyOutput:
+        """Verifies drafted chains from probabilities (float32 rows, no logits) and
+        given random numbers on the current torch stream:
+        specdec_rejection_sample_given.  ``accept_uniforms`` [N_d] and
+        ``sample_uniforms`` [B] are float32 in [0, 1); probability rows may lie
+        further apart than V; ``draft_probs`` None is a one-hot drafter.  beta is
+        not computed (None)."""
+        dev = self.device
+        B, nd = cu_num_draft_tokens.numel() - 1, draft_ids.numel()
+        for t, dt, name in ((draft_ids, torch.int32, "draft_ids"),
+                            (cu_num_draft_tokens, torch.int32, "cu_num_draft_tokens"),
+                            (accept_uniforms, torch.float32, "accept_uniforms"),
+                            (sample_uniforms, torch.float32, "sample_uniforms")):
+            if t.device != dev or t.dtype != dt or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dt} tensor on the device")
+        if B < 1 or accept_uniforms.numel() != nd or sample_uniforms.numel() != B:
+            raise ValueError("need cu of B + 1 >= 2 entries, one accept uniform per draft and one "
+                             "sample uniform per request")
+        V = target_probs.shape[-1]
+        for t, rows, name in ((target_probs, nd + B, "target_probs"), (draft_probs, nd, "draft_probs")):
+            if t is not None and (t.device != dev or t.dtype != torch.float32 or t.dim() != 2
+                                  or t.shape[0] != rows or t.shape[1] != V
+                                  or (V > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < V)):
+                raise ValueError(f"{name} must be float32 rows [{rows}, V] on the device")
+        if out is None:
+            out = VerifyOutput(tokens=torch.empty(nd + B, dtype=torch.int32, device=dev),
+                               num_accepted=torch.empty(B, dtype=torch.int32, device=dev), beta=None)
+        else:
+            for t, n in ((out.tokens, nd + B), (out.num_accepted, B)):
+                if t.device != dev or t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+                    raise ValueError("out must hold contiguous int32 tokens [N_t] and num_accepted [B]")
+        # with no draft rows at all an empty tensor still means "rows given"
+        q = None if draft_probs is None else (_ptr(draft_probs) or self._empty.data_ptr())
+        rc = specdec_rejection_sample_given(
+            self._h, _ptr(target_probs), max(target_probs.stride(0), V), q,
+            V if draft_probs is None else max(draft_probs.stride(0), V), self._ids_ptr(draft_ids),
+            _ptr(cu_num_draft_tokens), _ptr(accept_uniforms) or None, _ptr(sample_uniforms), B, V,
+            nd, _ptr(out.tokens), _ptr(out.num_accepted), _stream_handle(dev))
+        _check(rc, "specdec_rejection_sample_given")
+        return out
 
     def __call__(self, target_logits: torch.Tensor, draft_probs: torch.Tensor | None,
                  draft_ids: torch.Tensor, cu_num_draft_tokens: torch.Tensor, T: float, seed: int,
