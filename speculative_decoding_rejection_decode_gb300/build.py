@@ -12,7 +12,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libspecdec.so")
-SOURCES = ["specdec.cu", "noalloc.cu", "tree.cu", "cache.cu", "attention.cu", "given.cu"]
+SOURCES = ["specdec.cu", "noalloc.cu", "tree.cu", "cache.cu", "attention.cu",
+           "attention_tile.cu", "given.cu"]
 HEADERS = ["device_common.cuh", "kernels.cuh", "tree.cuh", "paged_index.h", "cache.cuh", "attention.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

@@ -559,43 +559,33 @@ int launch_warp(const AttendArgs& a, int num_sms, cudaStream_t st) {
     return SPECDEC_ERR_CUDA;
   const int G = num_sms;
   kern<<<G, kThreads, L::BYTES, st>>>(a);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.c.B * a.c.geo.kv_heads, 2 * MT);
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attend_join_kernel<T, 16 * MT, TK, D>, a, G) != cudaSuccess) return SPECDEC_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+  return launch_join<T, 16 * MT, TK, D>(a, G, st);
 }
 
-template <typename T, bool FP8, int D>
-int launch_rows(const AttendArgs& a, int num_sms, cudaStream_t st) {
-  // rows of an average request decide the tile (the host does not see cu)
-  const int64_t rows = (a.c.N + a.c.B - 1) / a.c.B * (a.q_heads / a.c.geo.kv_heads);
-  return rows <= 16 ? launch_warp<T, FP8, D, 1>(a, num_sms, st) : launch_warp<T, FP8, D, 2>(a, num_sms, st);
+// Rows (nodes x heads that share a kv head) of an average request: what the
+// host knows of the rows of a tile.
+int64_t average_rows(int B, int64_t N, int kv_heads, int q_heads) {
+  return (N + B - 1) / B * (q_heads / kv_heads);
 }
+constexpr int kWarpRows = 16;   // up to these the warp kernel, above them the tile kernel
 
 template <typename T, bool FP8>
 int launch_dim(const AttendArgs& a, int num_sms, cudaStream_t st) {
-  return a.c.head_dim == 128 ? launch_rows<T, FP8, 128>(a, num_sms, st) : launch_rows<T, FP8, 64>(a, num_sms, st);
+  return a.c.head_dim == 128 ? launch_warp<T, FP8, 128, 1>(a, num_sms, st) : launch_warp<T, FP8, 64, 1>(a, num_sms, st);
 }
 
 }  // namespace
 
 int64_t attend_workspace_bytes(int B, int64_t N, int kv_heads, int q_heads, int head_dim, int num_sms) {
-  (void)B;
-  (void)N;
-  (void)kv_heads;
-  (void)q_heads;
-  return head_dim == 128 ? Partials<32, 128>::bytes(num_sms) : Partials<32, 64>::bytes(num_sms);
+  if (average_rows(B, N, kv_heads, q_heads) > kWarpRows) return attend_tile_workspace(head_dim, num_sms);
+  return head_dim == 128 ? Partials<16, 128>::bytes(num_sms) : Partials<16, 64>::bytes(num_sms);
 }
 
 int launch_attend(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st) {
   if (a.c.N == 0) return SPECDEC_OK;
+  if (average_rows(a.c.B, a.c.N, a.c.geo.kv_heads, a.q_heads) > kWarpRows)
+    return launch_attend_tile(a, cache_dtype, dtype, num_sms, st);
   const bool fp8 = cache_dtype == SPECDEC_E4M3;
   if (dtype == SPECDEC_BF16)
     return fp8 ? launch_dim<__nv_bfloat16, true>(a, num_sms, st) : launch_dim<__nv_bfloat16, false>(a, num_sms, st);

@@ -153,80 +153,90 @@ struct Partials {
   static constexpr int64_t bytes(int G) { return (int64_t)2 * G * R * (D * 4 + 8); }
 };
 
-// Joins the partial results of the items that several ranges share.  A block
-// takes 8 rows of every row tile of one request and kv head.
+// Joins the partial results of the items that several ranges share.  An item
+// that starts in range i - 1 and goes on into range i belongs to blocks (i, *);
+// block (i, y) takes 8 of its rows, a warp two of them.
 template <typename T, int R, int TK, int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, const int G) {
   __shared__ ScanShared sh;
   const CacheArgs& c = a.c;
   const int group = a.q_heads / c.geo.kv_heads;
-  const int b = blockIdx.x / c.geo.kv_heads, h = blockIdx.x % c.geo.kv_heads;
   uint32_t why = 0;
-  const Request q = attend_request(c, group, b, R, TK, why);
-  // units before request b: a block-wide sum
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t mine = 0, all = 0;
-  for (int i = tid; i < c.B; i += 128) {
-    const int64_t x = attend_request(c, group, i, R, TK, why).units;
-    all += x;
-    if (i < b) mine += x;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-    all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-  }
-  if (lane == 0) {
-    sh.warp[warp] = mine;
-    sh.warp[warp + 4] = all;
-  }
-  __syncthreads();
-  int64_t before = 0, units = 0;
-  for (int w = 0; w < 4; ++w) {
-    before += sh.warp[w];
-    units += sh.warp[w + 4];
-  }
+  int64_t u = 0;
+  int ranges = 0;
+  find_unit<128>(c, group, R, TK,
+                 [&](int64_t units) {
+                   ranges = (int)min((int64_t)G, units);
+                   u = (int)blockIdx.x + 1 < ranges ? range_begin(units, ranges, blockIdx.x + 1) : units;
+                   return u;
+                 },
+                 sh, why);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x + 1 >= ranges || sh.b < 0) return;
+  const int g0 = blockIdx.x;                     // the range before the boundary
+  const Request q = attend_request(c, group, sh.b, R, TK, why);
   if (q.units == 0) return;
-  const int ranges = (int)min((int64_t)G, units);
+  const int64_t item = (u - sh.before) / q.tiles;
+  const int64_t u0 = sh.before + item * q.tiles, u1 = u0 + q.tiles;
+  // not an item that begins at the boundary, nor one that range g0 also went on with
+  if (u0 == u || range_begin(sh.total, ranges, g0) > u0) return;
+  const int h = (int)(item / q.rts), rt = (int)(item % q.rts);
+  const int g1 = range_of(sh.total, ranges, u1 - 1);
   const Partials<R, D> part(a.workspace, G);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = q.n * group;
-  for (int rt = 0; rt < q.rts; ++rt) {
-    const int64_t u0 = before + ((int64_t)h * q.rts + rt) * q.tiles, u1 = u0 + q.tiles;
-    const int g0 = range_of(units, ranges, u0), g1 = range_of(units, ranges, u1 - 1);
-    const int r0 = blockIdx.y * 8;
-    if (g0 == g1 || rt * R + r0 >= rows) continue;
-    for (int rr = warp; rr < 8; rr += 4) {
-      const int r = r0 + rr;
-      if (rt * R + r >= rows) break;
-      float m = -INFINITY;
-      // a range holds the item in its first slot if it begins inside the item
-      float l = 0.0f;
-      float acc[D / 32];
+  constexpr int PER = D / 32;
+  for (int r = blockIdx.y * 8 + warp; r < (int)blockIdx.y * 8 + 8; r += 4) {
+    const int row = rt * R + r;
+    if (row >= rows) break;
+    // a range holds the item in its first slot if it begins inside the item
+    auto slot_of = [&](int g) { return 2 * (int64_t)g + (range_begin(sh.total, ranges, g) >= u0 ? 0 : 1); };
+    float m = -INFINITY;
+    for (int g = g0 + lane; g <= g1; g += 32) m = fmaxf(m, part.stats[slot_of(g) * R + r].x);
+    m = warp_max(m);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, acc[PER];
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) acc[k] = 0.0f;
-      for (int g = g0; g <= g1; ++g) {
-        const int64_t slot = 2 * (int64_t)g + (range_begin(units, ranges, g) >= u0 ? 0 : 1);
-        const float2 s = part.stats[slot * R + r];
-        const float mn = fmaxf(m, s.x);
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float wo = ex2(m - ref), wn = ex2(s.x - ref);
-        l = l * wo + s.y * wn;
-        const float* v = part.sums + (slot * R + r) * D + lane * (D / 32);
+    for (int k = 0; k < PER; ++k) acc[k] = 0.0f;
+#pragma unroll 4
+    for (int g = g0; g <= g1; ++g) {
+      const int64_t slot = slot_of(g);
+      const float2 s = part.stats[slot * R + r];
+      const float w = ex2(s.x - ref);
+      const float* v = part.sums + (slot * R + r) * D + lane * PER;
+      l += s.y * w;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) acc[k] = acc[k] * wo + (wn > 0.0f ? v[k] * wn : 0.0f);
-        m = mn;
-      }
-      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-      const int row = rt * R + r;
-      T* out = static_cast<T*>(a.out) +
-               ((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + lane * (D / 32);
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) from_float(acc[k] * inv, out[k]);
+      for (int k = 0; k < PER; ++k) acc[k] += s.x == -INFINITY ? 0.0f : v[k] * w;
     }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T* out = static_cast<T*>(a.out) +
+             ((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + lane * PER;
+#pragma unroll
+    for (int k = 0; k < PER; k += 2)
+      *reinterpret_cast<uint32_t*>(out + k) = pack2(acc[k] * inv, acc[k + 1] * inv, T());
   }
 }
 
+// Queues the join as a dependent of the attention kernel before it.
+template <typename T, int R, int TK, int D>
+int launch_join(const AttendArgs& a, int G, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)G, R / 8);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, R, TK, D>, a, G) == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
 #endif  // __CUDACC__
+
+// The tensor-core kernel (attention_tile.cu).
+int launch_attend_tile(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
+int64_t attend_tile_workspace(int head_dim, int num_sms);
+
 
 }  // namespace specdec

@@ -1,0 +1,842 @@
+// attend_tile_kernel: attention with many rows per request on the tensor cores
+// (tcgen05, accumulators and weights in tensor memory).  Contract in
+// include/specdec.h (specdec_tree_attention).
+//
+// A unit is 128 rows x 128 keys.  Per SM one CTA of 13 warps:
+//   producers (4 warps)  copy the keys' and values' rows of a tile, wherever their
+//                        pages lie, into the operand layout (128-byte swizzle);
+//                        8-bit rows land in a small ring first and are widened to
+//                        f16 on the way;
+//   products (1 thread)  S_w = Q K^T (both operands in shared memory) and
+//                        O_w += P_w V (P in tensor memory);
+//   softmax (2 groups    group w takes every second tile of a segment with a
+//   of 4 warps)          maximum, sum and O_w of its own, one row per thread, so
+//                        that one group's exponentials overlap the other's
+//                        products and nothing of a row crosses threads.
+// Tensor memory: S_0, S_1 (P_w lies over S_w), O_0, O_1: 4 x 128 columns.
+// The two groups' results are joined when a segment ends.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "attention.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kR = 128, kTK = 128;
+constexpr int kGroupWarps = 4;                       // softmax warps of a group
+constexpr int kSoftmaxThreads = 2 * kGroupWarps * 32;
+constexpr int kProducerWarps = 4;
+constexpr int kMmaWarp = 2 * kGroupWarps + kProducerWarps;
+constexpr int kTileThreads = (kMmaWarp + 1) * 32;
+constexpr int kFactorSlots = 4;                      // tiles whose key factors are held
+
+template <bool FP8, int D>
+struct TileLayout {
+  static constexpr int SLOT = kTK * D * 2;           // one operand tile
+  // 16-bit caches: three tiles of K and V in flight.  8-bit: two, and three raw
+  // tiles before them (a raw tile is half as large)
+  static constexpr int SLOTS = FP8 ? 4 : 6;
+  static constexpr int RAW = FP8 ? kTK * D : 0;
+  static constexpr int RAWS = FP8 ? 3 : 0;
+  static constexpr int Q = 0;
+  static constexpr int OPS = kR * D * 2;
+  static constexpr int RAW0 = OPS + SLOTS * SLOT;
+  static constexpr int FACT = RAW0 + RAWS * RAW;     // [slot][k factor, log2 vs, 1 / vs][key]
+  static constexpr int STATS = Q;                    // over the queries, once a segment's products are done
+  static constexpr int BYTES = FACT + (FP8 ? kFactorSlots * 3 * kTK * 4 : 0) + 1024;   // and room to align
+};
+
+struct TileShared {
+  uint64_t full[6], empty[6];
+  uint64_t fact[kFactorSlots];
+  uint64_t s_full[2], p_full[2];
+  uint64_t q_full, o_full;
+  uint32_t live[kFactorSlots][4];   // keys of a tile that the cache holds
+  float rowf[kR];
+  uint32_t tmem;
+  int poison;                       // some tile with nodes held a value that is not finite (stays set)
+  int dead;                         // a wait ran out
+};
+
+// ---- tcgen05 -------------------------------------------------------------------
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// d (+)= A B, both in shared memory
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"((uint32_t)add)
+      : "memory");
+}
+// d (+)= A B, A in tensor memory
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"((uint32_t)add)
+      : "memory");
+}
+
+// 32 neighbouring columns of this thread's lane; the wait stands in the same
+// statement so that no use of the values can move before it
+__device__ __forceinline__ void tc_ld32(uint32_t addr, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const float* x) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle, rows of 128 bytes in
+// groups of 8 (1024 bytes apart).  `lead`: bytes between 64-element chunks
+// where the contiguous dimension is not the one summed over (V).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
+  const uint32_t lo = ((addr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
+  const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// Instruction descriptor: f32 accumulators, 16-bit factors, 128 x n.
+template <typename E>
+__device__ __forceinline__ constexpr uint32_t product(int n, bool b_rows_summed) {
+  const uint32_t t = std::is_same<E, __half>::value ? 0u : 1u;
+  return (1u << 4) | (t << 7) | (t << 10) | (b_rows_summed ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kR >> 4) << 24);
+}
+
+// Byte offset of 16-byte chunk c (of the row's 16-bit values) of row r of an
+// operand tile: [64-value half][row][128 bytes], chunks spread by the row.
+__device__ __forceinline__ uint32_t op_chunk(int r, int c) {
+  return (uint32_t)((c >> 3) * (kTK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Takes the non-finite 16-bit values out of w; whether there were any.
+template <typename E>
+__device__ __forceinline__ bool clear_nonfinite(uint4& w) {
+  constexpr uint32_t X = std::is_same<E, __half>::value ? 0x7C00u : 0x7F80u;
+  uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((u[i] & X) == X) {
+      u[i] &= 0xFFFF0000u;
+      any = true;
+    }
+    if (((u[i] >> 16) & X) == X) {
+      u[i] &= 0x0000FFFFu;
+      any = true;
+    }
+  }
+  return any;
+}
+
+// A wait that gives up: the role goes on without waiting (its loops are finite
+// and its addresses do not depend on data), and the call reports the timeout.
+__device__ __forceinline__ void wait_or_give_up(TileShared& sh, uint32_t bar, uint32_t parity) {
+  if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
+  if (!mbar_wait(bar, parity)) *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+}
+
+// The segments of this CTA's range, the same for every role.
+struct Segments {
+  int64_t u, end, base;
+  Request q;
+  int b, h, rt, t0, t1, rows, node0;
+  bool whole, first;
+
+  __device__ __forceinline__ bool next(const CacheArgs& c, int group) {
+    if (u >= end) return false;
+    uint32_t ignored = 0;
+    while (u >= base + q.units) {
+      base += q.units;
+      if (++b >= c.B) return false;   // lengths that changed under the call
+      q = attend_request(c, group, b, kR, kTK, ignored);
+    }
+    const int64_t item = (u - base) / q.tiles;
+    t0 = (int)((u - base) % q.tiles);
+    t1 = (int)min((int64_t)q.tiles, t0 + (end - u));
+    h = (int)(item / q.rts);
+    rt = (int)(item % q.rts);
+    u += t1 - t0;
+    whole = t0 == 0 && t1 == q.tiles;
+    rows = min(kR, q.n * group - rt * kR);
+    node0 = rt * kR / group;
+    return true;
+  }
+};
+
+template <typename T, bool FP8, int D>
+__global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const AttendArgs a) {
+  using L = TileLayout<FP8, D>;
+  using E = typename std::conditional<FP8, __half, T>::type;
+  constexpr int CH = D / 8;                      // 16-byte chunks of an operand row
+  constexpr int KSTEPS = D / 16;
+  // the largest weight lies in [2^kHead, 2^(kHead + kLazy)]: f16 weights keep
+  // their bits far below the largest, and the maximum may lag by 2^kLazy
+  constexpr float kLazy = 8.0f;
+  constexpr float kHead = std::is_same<E, __half>::value ? 6.0f : 0.0f;
+  extern __shared__ char smem_raw[];
+  __shared__ ScanShared scan;
+  __shared__ __align__(8) TileShared sh;
+  char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base_s = smem_addr(smem);
+  const CacheArgs& c = a.c;
+  const int G = gridDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = a.q_heads / c.geo.kv_heads;
+  uint32_t why = 0;
+  int64_t u0 = 0;
+  find_unit<kTileThreads>(c, group, kR, kTK,
+                          [&](int64_t units) {
+                            const int ranges = (int)min((int64_t)G, units);
+                            u0 = (int)blockIdx.x < ranges ? range_begin(units, ranges, blockIdx.x) : units;
+                            return u0;
+                          },
+                          scan, why);
+  if (blockIdx.x == 0 && why) atomicOr(c.err, why);
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t units = scan.total;
+  const int ranges = (int)min((int64_t)G, units);
+  if ((int)blockIdx.x >= ranges || scan.b < 0) return;
+  if (tid == 0) {
+    for (int i = 0; i < L::SLOTS; ++i) {
+      mbar_init(smem_addr(&sh.full[i]), kProducerWarps);
+      mbar_init(smem_addr(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < kFactorSlots; ++i) mbar_init(smem_addr(&sh.fact[i]), kProducerWarps);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_addr(&sh.s_full[w]), 1);
+      mbar_init(smem_addr(&sh.p_full[w]), kGroupWarps);
+    }
+    mbar_init(smem_addr(&sh.q_full), 2 * kGroupWarps);
+    mbar_init(smem_addr(&sh.o_full), 2);   // the products' end, and the thread that issued them
+    sh.poison = 0;
+    sh.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "n"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = sh.tmem;
+  uint32_t ignored = 0;
+  Segments seg;
+  seg.u = u0;
+  seg.end = range_begin(units, ranges, blockIdx.x + 1);
+  seg.b = scan.b;
+  seg.base = scan.before;
+  seg.q = attend_request(c, group, seg.b, kR, kTK, ignored);
+  uint32_t bad = 0;
+
+  if (warp == kMmaWarp) {
+    // ---- products -------------------------------------------------------------
+    if (lane == 0) {
+      int seq = 0, tiles_of[2] = {0, 0};
+      uint32_t g = 0;
+      auto slot = [&](int n) { return base_s + L::OPS + (n % L::SLOTS) * L::SLOT; };
+      auto phase = [&](int n) { return (uint32_t)(n / L::SLOTS) & 1u; };
+      while (seg.next(c, group)) {
+        const int n = seg.t1 - seg.t0;
+        wait_or_give_up(sh, smem_addr(&sh.q_full), g & 1u);
+        for (int j = 0; j <= n; ++j) {
+          if (j < n) {
+            const int k = seq + 2 * j, w = j & 1;
+            // S_w and P_w are free once the product before last has read P_w
+            if (j >= 2) wait_or_give_up(sh, smem_addr(&sh.empty[(k - 3) % L::SLOTS]), phase(k - 3));
+            wait_or_give_up(sh, smem_addr(&sh.full[k % L::SLOTS]), phase(k));
+            tc_fence_after();
+            const uint64_t qd = operand(base_s + L::Q, 16), kd = operand(slot(k), 16);
+#pragma unroll
+            for (int s = 0; s < KSTEPS; ++s) {
+              const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
+              tc_mma_ss(tm + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0);
+            }
+            tc_commit(smem_addr(&sh.s_full[w]));
+            tc_commit(smem_addr(&sh.empty[k % L::SLOTS]));
+          }
+          if (j > 0) {
+            const int v = seq + 2 * (j - 1) + 1, w = (j - 1) & 1;
+            wait_or_give_up(sh, smem_addr(&sh.full[v % L::SLOTS]), phase(v));
+            wait_or_give_up(sh, smem_addr(&sh.p_full[w]), (uint32_t)tiles_of[w] & 1u);
+            ++tiles_of[w];
+            tc_fence_after();
+            const uint64_t vd = operand(slot(v), kTK * 128);
+#pragma unroll
+            for (int s = 0; s < kTK / 16; ++s)
+              tc_mma_ts(tm + 256 + w * 128, tm + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
+                        s > 0 || j > 2);
+            tc_commit(smem_addr(&sh.empty[v % L::SLOTS]));
+          }
+        }
+        tc_commit(smem_addr(&sh.o_full));
+        mbar_arrive(smem_addr(&sh.o_full));
+        seq += 2 * n;
+        ++g;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 2 * kGroupWarps) {
+    // ---- producers: each warp owns 32 keys of every tile -----------------------
+    const int pw = warp - 2 * kGroupWarps;
+    int tile = 0;                          // key tiles so far
+    // Operand tiles are handled in order K, V, K, V, ...; a lane keeps the cache
+    // row of its key.  `stage` starts an operand tile's copies, `publish` hands
+    // it to the products once they have landed.
+    struct Tile {
+      int row;          // cache row of this lane's key, -1: none
+      bool tail;        // the tile holds nodes
+    };
+    auto stage = [&](int n, const Tile& t, bool is_v) {
+      const char* src = static_cast<const char*>(is_v ? c.v : c.k);
+      if constexpr (FP8) {
+        const uint32_t dst = base_s + L::RAW0 + (n % L::RAWS) * L::RAW;
+        constexpr int RC = D / 16;       // 16-byte chunks of a raw row
+#pragma unroll
+        for (int i = 0; i < RC; ++i) {
+          const int x = i * 32 + lane, key = x / RC, ch = x % RC;
+          const int r = __shfl_sync(0xFFFFFFFFu, t.row, key);
+          copy16(dst + (pw * 32 * RC + x) * 16, src + (int64_t)max(r, 0) * D + ch * 16, r >= 0);
+        }
+      } else {
+        const uint32_t dst = base_s + L::OPS + (n % L::SLOTS) * L::SLOT;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int x = i * 32 + lane, key = x / CH, ch = x % CH;
+          const int r = __shfl_sync(0xFFFFFFFFu, t.row, key);
+          copy16(dst + op_chunk(pw * 32 + key, ch), src + (int64_t)max(r, 0) * (2 * D) + ch * 16, r >= 0);
+        }
+      }
+      copy_commit();
+    };
+    auto wait_slot = [&](int n) {
+      wait_or_give_up(sh, smem_addr(&sh.empty[n % L::SLOTS]), ((uint32_t)(n / L::SLOTS) & 1u) ^ 1u);
+    };
+    auto facts = [&](int tile_no, const Tile& t, float ks, float vs) {
+      const int f = tile_no % kFactorSlots;
+      const uint32_t live = __ballot_sync(0xFFFFFFFFu, t.row >= 0);
+      if (lane == 0) sh.live[f][pw] = live;
+      if constexpr (FP8) {
+        float* fp = reinterpret_cast<float*>(smem + L::FACT) + f * 3 * kTK + pw * 32 + lane;
+        const float vc = vs == vs ? fmaxf(vs, 8.673617379884035e-19f) : vs;   // 0: a row of zeros
+        fp[0] = t.row >= 0 ? ks : 0.0f;
+        fp[kTK] = t.row >= 0 ? __log2f(vc) : 0.0f;
+        const float iv = __frcp_rn(vc);   // finite: it meets weights of 0 (a NaN scale shows in log2 vs)
+        fp[2 * kTK] = t.row >= 0 && isfinite(iv) ? iv : 0.0f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
+    };
+    auto publish = [&](int n, bool tail_v) {
+      const uint32_t dst = base_s + L::OPS + (n % L::SLOTS) * L::SLOT;
+      bool hit = false;
+      if constexpr (FP8) {
+        const uint32_t raw = base_s + L::RAW0 + (n % L::RAWS) * L::RAW;
+        constexpr int RC = D / 16;
+#pragma unroll
+        for (int i = 0; i < RC; ++i) {
+          const int x = i * 32 + lane, key = x / RC, ch = x % RC;
+          uint4 w = lds128(raw + (pw * 32 * RC + x) * 16);
+          uint4 lo = make_uint4(e4m3x2_f16x2(w.x), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y), e4m3x2_f16x2(w.y >> 16));
+          uint4 hi = make_uint4(e4m3x2_f16x2(w.z), e4m3x2_f16x2(w.z >> 16), e4m3x2_f16x2(w.w), e4m3x2_f16x2(w.w >> 16));
+          if (tail_v) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
+          sts128(dst + op_chunk(pw * 32 + key, 2 * ch), lo);
+          sts128(dst + op_chunk(pw * 32 + key, 2 * ch + 1), hi);
+        }
+      } else if (tail_v) {
+        for (int i = 0; i < CH; ++i) {
+          const int x = i * 32 + lane, key = x / CH, ch = x % CH;
+          const uint32_t at = dst + op_chunk(pw * 32 + key, ch);
+          uint4 w = lds128(at);
+          if (clear_nonfinite<E>(w)) {
+            sts128(at, w);
+            hit = true;
+          }
+        }
+      }
+      if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.full[n % L::SLOTS]));
+    };
+    auto key_row = [&](const Segments& s, int t) -> Tile {
+      const int64_t at = (int64_t)t * kTK + pw * 32 + lane;
+      Tile x;
+      x.row = -1;
+      x.tail = (int64_t)t * kTK + kTK > s.q.len;
+      if (at < (int64_t)s.q.len + s.q.n) {
+        const int64_t r = cache_row(c.geo, c.table + s.b * c.geo.table_stride, at);
+        if (r < 0) bad |= SPECDEC_DEVERR_BAD_CACHE;
+        else x.row = (int)(r + (int64_t)s.h * c.geo.page_size);
+      }
+      return x;
+    };
+    // One pass over all tiles of all segments, looked one tile ahead.
+    bool more = seg.next(c, group);
+    int t = more ? seg.t0 : 0;
+    auto advance = [&](Tile& x) -> bool {     // the next tile in order
+      if (!more) return false;
+      x = key_row(seg, t);
+      if (++t == seg.t1) {
+        more = seg.next(c, group);
+        t = more ? seg.t0 : 0;
+      }
+      return true;
+    };
+    if constexpr (FP8) {
+      // raw copies run RAWS operand tiles ahead of the widening
+      constexpr int AHEAD = L::RAWS;
+      Tile cur = {-1, false};
+      const bool have = advance(cur);
+      // K and V of a tile share its rows: keep the rows of the tiles in flight
+      Tile q0 = cur, q1 = {-1, false}, q2 = {-1, false};
+      bool h0 = have, h1 = false, h2 = false;
+      float k0 = 0, v0 = 0, k1 = 0, v1 = 0, k2 = 0, v2 = 0;
+      auto scales = [&](const Tile& x, float& k, float& v) {
+        k = x.row >= 0 ? __ldg(c.ks + x.row) : 0.0f;
+        v = x.row >= 0 ? __ldg(c.vs + x.row) : 1.0f;
+      };
+      if (h0) {
+        scales(q0, k0, v0);
+        h1 = advance(q1);
+        if (h1) scales(q1, k1, v1);
+      }
+      // operand tiles 2i (K) and 2i + 1 (V) of the tile in q0; ahead of them the
+      // V of q0 and the K (and V) of q1
+      if (h0) stage(0, q0, false); else copy_commit();
+      if (h0) stage(1, q0, true); else copy_commit();
+      for (int n = 0; h0; n += 2) {
+        // K of q0: stage K of q1 behind it
+        if (h1) stage(n + 2, q1, false); else copy_commit();
+        h2 = h1 ? advance(q2) : false;
+        if (h2) scales(q2, k2, v2);
+        copy_wait<AHEAD - 1>();
+        wait_slot(n);
+        facts(tile, q0, k0, v0);
+        publish(n, false);
+        // V of q0: stage V of q1 behind it
+        __syncwarp();
+        if (h1) stage(n + 3, q1, true); else copy_commit();
+        copy_wait<AHEAD - 1>();
+        wait_slot(n + 1);
+        publish(n + 1, q0.tail);
+        __syncwarp();
+        ++tile;
+        q0 = q1; h0 = h1; k0 = k1; v0 = v1;
+        q1 = q2; h1 = h2; k1 = k2; v1 = v2;
+      }
+      copy_wait<0>();
+    } else {
+      // copies of operand tile n are published LAG operand tiles later; a slot is
+      // waited for only when everything its release depends on is published
+      // (LAG <= SLOTS - 2)
+      constexpr int LAG = L::SLOTS - 2;
+      uint32_t tails = 0;                // tail bits of the last tiles, newest in bit 0
+      Tile cur = {-1, false}, nxt = {-1, false};
+      bool have = advance(cur);
+      int n = 0;
+      while (have) {
+        const bool have_next = advance(nxt);
+        for (int half = 0; half < 2; ++half, ++n) {
+          wait_slot(n);
+          if (half == 0) {
+            facts(tile, cur, 0.0f, 0.0f);
+            tails = (tails << 1) | (cur.tail ? 1u : 0u);
+          }
+          stage(n, cur, half == 1);
+          if (n >= LAG) {
+            copy_wait<LAG>();
+            // operand tile n - LAG (LAG even): the same half, LAG / 2 tiles ago
+            publish(n - LAG, half == 1 && ((tails >> (LAG / 2)) & 1u));
+          }
+        }
+        ++tile;
+        cur = nxt;
+        have = have_next;
+      }
+      copy_wait<0>();
+      for (int m = n > LAG ? n - LAG : 0; m < n; ++m)
+        publish(m, (m & 1) && ((tails >> ((n - 1) / 2 - m / 2)) & 1u));
+    }
+  } else {
+    // ---- softmax ----------------------------------------------------------------
+    const int w = warp / kGroupWarps;            // group: tiles w, w + 2, ... of a segment
+    const int row = (warp % kGroupWarps) * 32 + lane;   // row of the tile = lane of tensor memory
+    const uint32_t lanes = (uint32_t)(warp % kGroupWarps) << 21;   // first lane, in bits 16..
+    const uint32_t ts = tm + lanes + w * 128, to = tm + lanes + 256 + w * 128;
+    const int sid = tid;                         // 0 .. 255
+    float2* stats = reinterpret_cast<float2*>(smem + L::STATS);
+    const Partials<kR, D> part(a.workspace, G);
+    int done = 0, tile0 = 0;                     // this group's tiles, all tiles before the segment
+    uint32_t g = 0;
+    bool first = true;
+    while (seg.next(c, group)) {
+      // queries
+      const float sgn = a.scale_log2 < 0.0f ? -1.0f : 1.0f;   // factors are positive: the sign goes to q
+      for (int x = sid; x < kR * CH; x += kSoftmaxThreads) {
+        const int r = x / CH, ch = x % CH;
+        const bool live = r < seg.rows;
+        const int gr = seg.rt * kR + (live ? r : 0);
+        const T* src = static_cast<const T*>(a.q) + (seg.q.first + gr / group) * a.q_row +
+                       (int64_t)(seg.h * group + gr % group) * a.q_head + ch * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live) v = __ldg(reinterpret_cast<const uint4*>(src));
+        float f = fabsf(a.scale_log2);
+        if constexpr (FP8) {
+          // f16 factors: the row is scaled by a power of two so that its largest
+          // value lies in [1, 2); the scores take the factor back
+          const T* e = reinterpret_cast<const T*>(&v);
+          float y[8], m = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y[i] = to_float(e[i]) * sgn;
+            m = fmaxf(m, fabsf(y[i]));
+          }
+#pragma unroll
+          for (int o = CH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          const int ex = min(max((int)(__float_as_uint(m) >> 23), 1), 253);
+          const float mul = __uint_as_float((uint32_t)(254 - ex) << 23);
+          f *= __uint_as_float((uint32_t)ex << 23);
+          v = make_uint4(pack2(y[0] * mul, y[1] * mul, E()), pack2(y[2] * mul, y[3] * mul, E()),
+                         pack2(y[4] * mul, y[5] * mul, E()), pack2(y[6] * mul, y[7] * mul, E()));
+        } else if (sgn < 0.0f) {
+          v.x ^= 0x80008000u;
+          v.y ^= 0x80008000u;
+          v.z ^= 0x80008000u;
+          v.w ^= 0x80008000u;
+        }
+        sts128(base_s + L::Q + op_chunk(r, ch), v);
+        if (ch == 0) sh.rowf[r] = f;
+      }
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.q_full));
+      named_bar_sync(1, kSoftmaxThreads);
+      const float rowf = sh.rowf[row];
+      const int n = seg.t1 - seg.t0;
+      const bool busy = (row & ~31) < seg.rows;    // the warp has rows of the tile
+      const int node = (seg.rt * kR + min(row, seg.rows - 1)) / group;
+      const int32_t* parent = c.parent ? c.parent + seg.q.first : nullptr;
+      float m = -INFINITY, l = 0.0f;               // reference maximum and sum of this group's tiles
+      // keys of tile t that the row sees, 128 bits
+      auto visible = [&](int t, uint32_t* bits) {
+        const int64_t j0 = (int64_t)t * kTK - seg.q.len;   // node index of the tile's first key
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // context: keys below -j0; a chain also sees nodes up to its own
+          const int64_t upto = (j0 < 0 ? -j0 : 0);
+          const int64_t lim = parent ? upto : max(upto, (int64_t)node + 1 - j0);
+          const int64_t k = lim - 32 * i;
+          bits[i] = k <= 0 ? 0u : (k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u);
+        }
+        if (parent) {
+          int x = node;
+          while (x >= j0) {
+            const int64_t k = x - j0;
+            if (k < kTK) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if ((int)(k >> 5) == i) bits[i] |= 1u << (k & 31);
+            }
+            if (x == 0) break;
+            const int up = __ldg(parent + x);
+            if (up < 0 || up >= x) {
+              bad |= SPECDEC_DEVERR_BAD_TREE;
+              break;
+            }
+            x = up;
+          }
+        }
+      };
+      for (int j = w; j < n; j += 2) {
+        const int t = seg.t0 + j, f = (tile0 + j) % kFactorSlots;
+        wait_or_give_up(sh, smem_addr(&sh.fact[f]), (uint32_t)((tile0 + j) / kFactorSlots) & 1u);
+        wait_or_give_up(sh, smem_addr(&sh.s_full[w]), (uint32_t)done & 1u);
+        ++done;
+        tc_fence_after();
+        if (busy) {
+          uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+          const bool tail = (int64_t)t * kTK + kTK > seg.q.len;
+          if (tail) visible(t, bits);
+          __syncwarp();
+          bool masked = tail;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t lv = sh.live[f][i];
+            masked |= lv != 0xFFFFFFFFu;
+            bits[i] &= lv;
+          }
+          const float* fk = reinterpret_cast<const float*>(smem + L::FACT) + f * 3 * kTK;
+          // scores of 32 keys, base 2 (8-bit caches: with the scale of V in the
+          // exponent, so that the weights that meet V are bounded)
+          auto scores = [&](int i, float* s) {
+            tc_ld32(ts + i * 32, s);
+            if constexpr (FP8) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                const float4 kf = *reinterpret_cast<const float4*>(fk + i * 32 + k);
+                const float4 lv = *reinterpret_cast<const float4*>(fk + kTK + i * 32 + k);
+                s[k] = fmaf(s[k] * kf.x, rowf, lv.x);
+                s[k + 1] = fmaf(s[k + 1] * kf.y, rowf, lv.y);
+                s[k + 2] = fmaf(s[k + 2] * kf.z, rowf, lv.z);
+                s[k + 3] = fmaf(s[k + 3] * kf.w, rowf, lv.w);
+              }
+            }
+            if (masked) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((bits[i] >> k) & 1u)) s[k] = -INFINITY;
+            }
+          };
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float s[32];
+            scores(i, s);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, s[k]);
+          }
+          if (!FP8) mx = mx == -INFINITY ? mx : mx * rowf;
+          // the reference follows the maximum only when it is left far behind
+          const bool move = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
+          const float mn = move ? mx : m;
+          if (j >= 2 && __any_sync(0xFFFFFFFFu, move)) {
+            const float fix = move ? ex2(m - mn) : 1.0f;
+            l *= fix;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              float o[32];
+              tc_ld32(to + i * 32, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= fix;
+              tc_st32(to + i * 32, o);
+            }
+          }
+          m = mn;
+          const float ref = (m == -INFINITY ? 0.0f : m) - kHead;
+          // weights, rounded to 16 bits for the product with V (half a step each
+          // at most) and summed unrounded
+          float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float s[32];
+            scores(i, s);
+            uint32_t p[16];
+            const float* iv = fk + 2 * kTK + i * 32;
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float e0, e1;
+              if constexpr (FP8) {
+                e0 = ex2(s[k] - ref);
+                e1 = ex2(s[k + 1] - ref);
+                const float2 v = *reinterpret_cast<const float2*>(iv + k);
+                sum0 = fmaf(e0, v.x, sum0);
+                sum1 = fmaf(e1, v.y, sum1);
+              } else {
+                e0 = ex2(fmaf(s[k], rowf, -ref));
+                e1 = ex2(fmaf(s[k + 1], rowf, -ref));
+                if (masked) {   // a factor of 0 would make NaN of -inf
+                  e0 = ((bits[i] >> k) & 1u) ? e0 : 0.0f;
+                  e1 = ((bits[i] >> (k + 1)) & 1u) ? e1 : 0.0f;
+                }
+                sum0 += e0;
+                sum1 += e1;
+              }
+              p[k / 2] = pack2(e0, e1, E());
+            }
+            tc_st16(ts + i * 16, p);
+          }
+          l += sum0 + sum1;
+          tc_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[w]));
+      }
+      // ---- the segment's end: both groups' results joined, half of the head each
+      wait_or_give_up(sh, smem_addr(&sh.o_full), g & 1u);
+      tc_fence_after();
+      stats[w * kR + row] = make_float2(m, l);
+      named_bar_sync(1, kSoftmaxThreads);
+      if (busy) {
+        const float2 s0 = stats[row], s1 = stats[kR + row];
+        const float mm = fmaxf(s0.x, s1.x), ref = mm == -INFINITY ? 0.0f : mm;
+        const float f0 = ex2(s0.x - ref), f1 = ex2(s1.x - ref);
+        const float lsum = s0.y * f0 + s1.y * f1;
+        const int gr = seg.rt * kR + row;
+        const bool live = row < seg.rows;
+        const float inv = seg.whole ? (lsum == 0.0f ? 0.0f : 1.0f / lsum) : 1.0f;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (first ? 0 : 1);
+        const bool poison = *reinterpret_cast<volatile int*>(&sh.poison) != 0;
+        const uint32_t o0 = tm + lanes + 256 + w * (D / 2), o1 = o0 + 128;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          float x[32];
+          __syncwarp();
+          tc_ld32(o0 + i * 32, x);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = s0.x == -INFINITY ? 0.0f : x[k] * f0;
+          if (n > 1) {
+            float y[32];
+            tc_ld32(o1 + i * 32, y);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] += s1.x == -INFINITY ? 0.0f : y[k] * f1;
+          }
+          const int d0 = w * (D / 2) + i * 32;
+          if (poison && live) {
+            // values that are not finite were taken out of the tiles that hold
+            // nodes: they belong to the rows that see their keys
+            for (int t = max(seg.t0, seg.q.len / kTK); t < seg.t1; ++t) {
+              uint32_t bits[4];
+              visible(t, bits);
+              for (int k = 0; k < kTK; ++k) {
+                const int64_t at = (int64_t)t * kTK + k;
+                if (!((bits[k >> 5] >> (k & 31)) & 1u) || at >= (int64_t)seg.q.len + seg.q.n) continue;
+                const int64_t r = cache_row(c.geo, c.table + seg.b * c.geo.table_stride, at);
+                if (r < 0) continue;
+                const int64_t e = (r + (int64_t)seg.h * c.geo.page_size) * D + d0;
+                for (int d = 0; d < 32; ++d) {
+                  float v;
+                  if constexpr (FP8) {
+                    const uint8_t raw = static_cast<const uint8_t*>(c.v)[e + d];
+                    v = (raw & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.0f;
+                  } else {
+                    v = to_float(static_cast<const T*>(c.v)[e + d]);
+                  }
+                  if (!isfinite(v)) {
+#pragma unroll
+                    for (int z = 0; z < 32; ++z)
+                      if (z == d) x[z] += v;
+                  }
+                }
+              }
+            }
+          }
+          if (live) {
+            if (seg.whole) {
+              T* out = static_cast<T*>(a.out) +
+                       ((seg.q.first + gr / group) * a.q_heads + seg.h * group + gr % group) * (int64_t)D + d0;
+#pragma unroll
+              for (int k = 0; k < 32; k += 8)
+                *reinterpret_cast<uint4*>(out + k) =
+                    make_uint4(pack2(x[k] * inv, x[k + 1] * inv, T()), pack2(x[k + 2] * inv, x[k + 3] * inv, T()),
+                               pack2(x[k + 4] * inv, x[k + 5] * inv, T()), pack2(x[k + 6] * inv, x[k + 7] * inv, T()));
+            } else {
+              float* out = part.sums + (slot * kR + row) * D + d0;
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<float4*>(out + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+            }
+          }
+        }
+        if (live && !seg.whole && w == 0) part.stats[slot * kR + row] = make_float2(mm, lsum);
+      }
+      tc_fence_before();
+      named_bar_sync(1, kSoftmaxThreads);   // the sums are read before queries lie over them
+      tile0 += n;
+      ++g;
+      first = false;
+    }
+  }
+  if (bad) atomicOr(c.err, bad);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && sh.dead) atomicOr(c.err, SPECDEC_DEVERR_TIMEOUT);
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(512));
+}
+
+template <typename T, bool FP8, int D>
+int launch_tile(const AttendArgs& a, int num_sms, cudaStream_t st) {
+  auto kern = attend_tile_kernel<T, FP8, D>;
+  constexpr int bytes = TileLayout<FP8, D>::BYTES;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return SPECDEC_ERR_CUDA;
+  kern<<<num_sms, kTileThreads, bytes, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+  return launch_join<T, kR, kTK, D>(a, num_sms, st);
+}
+
+template <typename T, bool FP8>
+int launch_tile_dim(const AttendArgs& a, int num_sms, cudaStream_t st) {
+  return a.c.head_dim == 128 ? launch_tile<T, FP8, 128>(a, num_sms, st) : launch_tile<T, FP8, 64>(a, num_sms, st);
+}
+
+}  // namespace
+
+int64_t attend_tile_workspace(int head_dim, int num_sms) {
+  return head_dim == 128 ? Partials<kR, 128>::bytes(num_sms) : Partials<kR, 64>::bytes(num_sms);
+}
+
+int launch_attend_tile(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st) {
+  const bool fp8 = cache_dtype == SPECDEC_E4M3;
+  if (dtype == SPECDEC_BF16)
+    return fp8 ? launch_tile_dim<__nv_bfloat16, true>(a, num_sms, st)
+               : launch_tile_dim<__nv_bfloat16, false>(a, num_sms, st);
+  return fp8 ? launch_tile_dim<__half, true>(a, num_sms, st) : launch_tile_dim<__half, false>(a, num_sms, st);
+}
+
+}  // namespace specdec
