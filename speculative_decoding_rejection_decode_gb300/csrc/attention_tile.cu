@@ -3,10 +3,12 @@
 // include/specdec.h (specdec_tree_attention).
 //
 // A unit is 128 rows x 128 keys.  Per SM one CTA of 13 warps:
-//   producers (4 warps)  copy the keys' and values' rows of a tile, wherever their
-//                        pages lie, into the operand layout (128-byte swizzle);
-//                        8-bit rows land in a small ring first and are widened to
-//                        f16 on the way;
+//   producers (4 warps)  bring the keys' and values' rows of a tile, wherever their
+//                        pages lie, into the operand layout (128-byte swizzle):
+//                        tiles that are all context by TMA boxes of up to 32 rows
+//                        of a page, tiles that hold nodes, bad pages or pages of
+//                        odd sizes by 16-byte copies; 8-bit rows land in a small
+//                        ring first and are widened to f16 on the way;
 //   products (1 thread)  S_w = Q K^T (both operands in shared memory) and
 //                        O_w += P_w V (P in tensor memory);
 //   softmax (2 groups    group w takes every second tile of a segment with a
@@ -15,6 +17,7 @@
 //                        products and nothing of a row crosses threads.
 // Tensor memory: S_0, S_1 (P_w lies over S_w), O_0, O_1: 4 x 128 columns.
 // The two groups' results are joined when a segment ends.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -54,6 +57,7 @@ struct TileLayout {
 
 struct TileShared {
   uint64_t full[6], empty[6];
+  uint64_t raw[3][kProducerWarps];  // a warp's part of a raw tile has landed
   uint64_t fact[kFactorSlots];
   uint64_t s_full[2], p_full[2];
   uint64_t q_full, o_full;
@@ -88,21 +92,22 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       : "memory");
 }
 
-// 32 neighbouring columns of this thread's lane; the wait stands in the same
-// statement so that no use of the values can move before it
+// 32 neighbouring columns of this thread's lane: issued, and waited for by a
+// statement that the values pass through, so that no use can move before it
+// (it waits for every load issued so far).
 __device__ __forceinline__ void tc_ld32(uint32_t addr, float* x) {
   uint32_t* r = reinterpret_cast<uint32_t*>(x);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr)
-      : "memory");
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tc_wait32(float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]),"+r"(r[1]),"+r"(r[2]),"+r"(r[3]),"+r"(r[4]),"+r"(r[5]),"+r"(r[6]),"+r"(r[7]),"+r"(r[8]),"+r"(r[9]),"+r"(r[10]),"+r"(r[11]),"+r"(r[12]),"+r"(r[13]),"+r"(r[14]),"+r"(r[15]),"+r"(r[16]),"+r"(r[17]),"+r"(r[18]),"+r"(r[19]),"+r"(r[20]),"+r"(r[21]),"+r"(r[22]),"+r"(r[23]),"+r"(r[24]),"+r"(r[25]),"+r"(r[26]),"+r"(r[27]),"+r"(r[28]),"+r"(r[29]),"+r"(r[30]),"+r"(r[31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tc_st32(uint32_t addr, const float* x) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
@@ -151,10 +156,51 @@ __device__ __forceinline__ uint32_t op_chunk(int r, int c) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+// Arrives on `bar` once every copy that this thread has issued has landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// A box of rows `row`, ... from column x of the map's array; completes on `bar`.
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(row)
+      : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Two 32-bit operations in one instruction, each rounded as alone.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -170,7 +216,10 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Takes the non-finite 16-bit values out of w; whether there were any.
+// Takes the non-finite 16-bit values out of w; whether there were any.  A row's
+// hidden nodes have weight 0, and 0 x inf would reach it through the product: in
+// tiles that hold nodes such values are left out, and the rows that do see their
+// keys get them when the segment ends.
 template <typename E>
 __device__ __forceinline__ bool clear_nonfinite(uint4& w) {
   constexpr uint32_t X = std::is_same<E, __half>::value ? 0x7C00u : 0x7F80u;
@@ -226,7 +275,9 @@ struct Segments {
 };
 
 template <typename T, bool FP8, int D>
-__global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kTileThreads, 1)
+    attend_tile_kernel(const AttendArgs a, const int box, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap) {
   using L = TileLayout<FP8, D>;
   using E = typename std::conditional<FP8, __half, T>::type;
   constexpr int CH = D / 8;                      // 16-byte chunks of an operand row
@@ -259,9 +310,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
   if ((int)blockIdx.x >= ranges || scan.b < 0) return;
   if (tid == 0) {
     for (int i = 0; i < L::SLOTS; ++i) {
-      mbar_init(smem_addr(&sh.full[i]), kProducerWarps);
+      mbar_init(smem_addr(&sh.full[i]), kProducerWarps * 32);
       mbar_init(smem_addr(&sh.empty[i]), 1);
     }
+    for (int i = 0; i < L::RAWS; ++i)
+      for (int w = 0; w < kProducerWarps; ++w) mbar_init(smem_addr(&sh.raw[i][w]), 32);
     for (int i = 0; i < kFactorSlots; ++i) mbar_init(smem_addr(&sh.fact[i]), kProducerWarps);
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_addr(&sh.s_full[w]), 1);
@@ -306,6 +359,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
             // S_w and P_w are free once the product before last has read P_w
             if (j >= 2) wait_or_give_up(sh, smem_addr(&sh.empty[(k - 3) % L::SLOTS]), phase(k - 3));
             wait_or_give_up(sh, smem_addr(&sh.full[k % L::SLOTS]), phase(k));
+            fence_async_proxy();   // rows that came by 16-byte copies
             tc_fence_after();
             const uint64_t qd = operand(base_s + L::Q, 16), kd = operand(slot(k), 16);
 #pragma unroll
@@ -321,6 +375,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
             wait_or_give_up(sh, smem_addr(&sh.full[v % L::SLOTS]), phase(v));
             wait_or_give_up(sh, smem_addr(&sh.p_full[w]), (uint32_t)tiles_of[w] & 1u);
             ++tiles_of[w];
+            fence_async_proxy();
             tc_fence_after();
             const uint64_t vd = operand(slot(v), kTK * 128);
 #pragma unroll
@@ -340,85 +395,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
   } else if (warp >= 2 * kGroupWarps) {
     // ---- producers: each warp owns 32 keys of every tile -----------------------
     const int pw = warp - 2 * kGroupWarps;
-    int tile = 0;                          // key tiles so far
-    // Operand tiles are handled in order K, V, K, V, ...; a lane keeps the cache
-    // row of its key.  `stage` starts an operand tile's copies, `publish` hands
-    // it to the products once they have landed.
     struct Tile {
       int row;          // cache row of this lane's key, -1: none
       bool tail;        // the tile holds nodes
-    };
-    auto stage = [&](int n, const Tile& t, bool is_v) {
-      const char* src = static_cast<const char*>(is_v ? c.v : c.k);
-      if constexpr (FP8) {
-        const uint32_t dst = base_s + L::RAW0 + (n % L::RAWS) * L::RAW;
-        constexpr int RC = D / 16;       // 16-byte chunks of a raw row
-#pragma unroll
-        for (int i = 0; i < RC; ++i) {
-          const int x = i * 32 + lane, key = x / RC, ch = x % RC;
-          const int r = __shfl_sync(0xFFFFFFFFu, t.row, key);
-          copy16(dst + (pw * 32 * RC + x) * 16, src + (int64_t)max(r, 0) * D + ch * 16, r >= 0);
-        }
-      } else {
-        const uint32_t dst = base_s + L::OPS + (n % L::SLOTS) * L::SLOT;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int x = i * 32 + lane, key = x / CH, ch = x % CH;
-          const int r = __shfl_sync(0xFFFFFFFFu, t.row, key);
-          copy16(dst + op_chunk(pw * 32 + key, ch), src + (int64_t)max(r, 0) * (2 * D) + ch * 16, r >= 0);
-        }
-      }
-      copy_commit();
-    };
-    auto wait_slot = [&](int n) {
-      wait_or_give_up(sh, smem_addr(&sh.empty[n % L::SLOTS]), ((uint32_t)(n / L::SLOTS) & 1u) ^ 1u);
-    };
-    auto facts = [&](int tile_no, const Tile& t, float ks, float vs) {
-      const int f = tile_no % kFactorSlots;
-      const uint32_t live = __ballot_sync(0xFFFFFFFFu, t.row >= 0);
-      if (lane == 0) sh.live[f][pw] = live;
-      if constexpr (FP8) {
-        float* fp = reinterpret_cast<float*>(smem + L::FACT) + f * 3 * kTK + pw * 32 + lane;
-        const float vc = vs == vs ? fmaxf(vs, 8.673617379884035e-19f) : vs;   // 0: a row of zeros
-        fp[0] = t.row >= 0 ? ks : 0.0f;
-        fp[kTK] = t.row >= 0 ? __log2f(vc) : 0.0f;
-        const float iv = __frcp_rn(vc);   // finite: it meets weights of 0 (a NaN scale shows in log2 vs)
-        fp[2 * kTK] = t.row >= 0 && isfinite(iv) ? iv : 0.0f;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
-    };
-    auto publish = [&](int n, bool tail_v) {
-      const uint32_t dst = base_s + L::OPS + (n % L::SLOTS) * L::SLOT;
-      bool hit = false;
-      if constexpr (FP8) {
-        const uint32_t raw = base_s + L::RAW0 + (n % L::RAWS) * L::RAW;
-        constexpr int RC = D / 16;
-#pragma unroll
-        for (int i = 0; i < RC; ++i) {
-          const int x = i * 32 + lane, key = x / RC, ch = x % RC;
-          uint4 w = lds128(raw + (pw * 32 * RC + x) * 16);
-          uint4 lo = make_uint4(e4m3x2_f16x2(w.x), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y), e4m3x2_f16x2(w.y >> 16));
-          uint4 hi = make_uint4(e4m3x2_f16x2(w.z), e4m3x2_f16x2(w.z >> 16), e4m3x2_f16x2(w.w), e4m3x2_f16x2(w.w >> 16));
-          if (tail_v) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
-          sts128(dst + op_chunk(pw * 32 + key, 2 * ch), lo);
-          sts128(dst + op_chunk(pw * 32 + key, 2 * ch + 1), hi);
-        }
-      } else if (tail_v) {
-        for (int i = 0; i < CH; ++i) {
-          const int x = i * 32 + lane, key = x / CH, ch = x % CH;
-          const uint32_t at = dst + op_chunk(pw * 32 + key, ch);
-          uint4 w = lds128(at);
-          if (clear_nonfinite<E>(w)) {
-            sts128(at, w);
-            hit = true;
-          }
-        }
-      }
-      if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
-      fence_async_proxy();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.full[n % L::SLOTS]));
+      bool boxes;       // this warp's 32 keys come by TMA
     };
     auto key_row = [&](const Segments& s, int t) -> Tile {
       const int64_t at = (int64_t)t * kTK + pw * 32 + lane;
@@ -430,12 +410,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
         if (r < 0) bad |= SPECDEC_DEVERR_BAD_CACHE;
         else x.row = (int)(r + (int64_t)s.h * c.geo.page_size);
       }
+      // (keys behind the last slot have to read as zeros: no boxes over them)
+      x.boxes = __all_sync(0xFFFFFFFFu, x.row >= 0) && box > 0 && !x.tail;
       return x;
     };
-    // One pass over all tiles of all segments, looked one tile ahead.
     bool more = seg.next(c, group);
     int t = more ? seg.t0 : 0;
-    auto advance = [&](Tile& x) -> bool {     // the next tile in order
+    auto advance = [&](Tile& x) -> bool {     // the next tile of the range, in order
       if (!more) return false;
       x = key_row(seg, t);
       if (++t == seg.t1) {
@@ -444,81 +425,161 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
       }
       return true;
     };
+    auto wait_slot = [&](int n) {
+      wait_or_give_up(sh, smem_addr(&sh.empty[n % L::SLOTS]), ((uint32_t)(n / L::SLOTS) & 1u) ^ 1u);
+    };
+    auto facts = [&](int tile_no, const Tile& x, float ks, float vs) {
+      const int f = tile_no % kFactorSlots;
+      const uint32_t live = __ballot_sync(0xFFFFFFFFu, x.row >= 0);
+      if (lane == 0) sh.live[f][pw] = live;
+      if constexpr (FP8) {
+        float* fp = reinterpret_cast<float*>(smem + L::FACT) + f * 3 * kTK + pw * 32 + lane;
+        const float vc = vs == vs ? fmaxf(vs, 8.673617379884035e-19f) : vs;   // 0: a row of zeros
+        const float iv = __frcp_rn(vc);   // finite: it meets weights of 0 (a NaN scale shows in log2 vs)
+        fp[0] = x.row >= 0 ? ks : 0.0f;
+        fp[kTK] = x.row >= 0 ? __log2f(vc) : 0.0f;
+        fp[2 * kTK] = x.row >= 0 && isfinite(iv) ? iv : 0.0f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
+    };
+    // This warp's 32 rows of the array that `map` describes by boxes of `box`
+    // rows and 128 (or D) bytes; every lane arrives on `bar`.
+    auto by_boxes = [&](uint32_t dst, int half_step, const CUtensorMap* map, const Tile& x, uint32_t bar) {
+      constexpr int HALVES = FP8 ? 1 : D / 64;
+      constexpr int LINE = FP8 ? D : 128;
+      if (lane == 0) mbar_arrive_expect_tx(bar, 32 * HALVES * LINE);
+      else mbar_arrive(bar);
+      __syncwarp();
+      const int r0 = (lane / HALVES) * box, half = lane % HALVES;
+      const int row = __shfl_sync(0xFFFFFFFFu, x.row, r0 & 31);
+      if (r0 < 32) box_load(dst + half * half_step + (pw * 32 + r0) * LINE, map, half * 64, row, bar);
+    };
+    bool more_tiles;
+    Tile cur = {-1, false, false}, nxt = {-1, false, false};
+    more_tiles = advance(cur);
     if constexpr (FP8) {
-      // raw copies run RAWS operand tiles ahead of the widening
-      constexpr int AHEAD = L::RAWS;
-      Tile cur = {-1, false};
-      const bool have = advance(cur);
-      // K and V of a tile share its rows: keep the rows of the tiles in flight
-      Tile q0 = cur, q1 = {-1, false}, q2 = {-1, false};
-      bool h0 = have, h1 = false, h2 = false;
-      float k0 = 0, v0 = 0, k1 = 0, v1 = 0, k2 = 0, v2 = 0;
-      auto scales = [&](const Tile& x, float& k, float& v) {
-        k = x.row >= 0 ? __ldg(c.ks + x.row) : 0.0f;
-        v = x.row >= 0 ? __ldg(c.vs + x.row) : 1.0f;
+      // Raw tiles are staged RAWS - 1 ahead of the one that is widened; a lane
+      // widens 16 bytes of 8 neighbouring rows' one chunk, which 8 lanes read and
+      // write without bank conflicts in both swizzles.
+      constexpr int RC = D / 16;             // 16-byte chunks of a raw row
+      auto raw_chunk = [&](int key, int ch) {
+        return D == 128 ? (uint32_t)(key * D + ((ch ^ (key & 7)) << 4)) : (uint32_t)(key * D + ((ch ^ ((key >> 1) & 3)) << 4));
       };
-      if (h0) {
-        scales(q0, k0, v0);
-        h1 = advance(q1);
-        if (h1) scales(q1, k1, v1);
-      }
-      // operand tiles 2i (K) and 2i + 1 (V) of the tile in q0; ahead of them the
-      // V of q0 and the K (and V) of q1
-      if (h0) stage(0, q0, false); else copy_commit();
-      if (h0) stage(1, q0, true); else copy_commit();
-      for (int n = 0; h0; n += 2) {
-        // K of q0: stage K of q1 behind it
-        if (h1) stage(n + 2, q1, false); else copy_commit();
-        h2 = h1 ? advance(q2) : false;
-        if (h2) scales(q2, k2, v2);
-        copy_wait<AHEAD - 1>();
-        wait_slot(n);
-        facts(tile, q0, k0, v0);
-        publish(n, false);
-        // V of q0: stage V of q1 behind it
-        __syncwarp();
-        if (h1) stage(n + 3, q1, true); else copy_commit();
-        copy_wait<AHEAD - 1>();
-        wait_slot(n + 1);
-        publish(n + 1, q0.tail);
-        __syncwarp();
-        ++tile;
-        q0 = q1; h0 = h1; k0 = k1; v0 = v1;
-        q1 = q2; h1 = h2; k1 = k2; v1 = v2;
-      }
-      copy_wait<0>();
-    } else {
-      // copies of operand tile n are published LAG operand tiles later; a slot is
-      // waited for only when everything its release depends on is published
-      // (LAG <= SLOTS - 2)
-      constexpr int LAG = L::SLOTS - 2;
-      uint32_t tails = 0;                // tail bits of the last tiles, newest in bit 0
-      Tile cur = {-1, false}, nxt = {-1, false};
-      bool have = advance(cur);
-      int n = 0;
-      while (have) {
-        const bool have_next = advance(nxt);
-        for (int half = 0; half < 2; ++half, ++n) {
-          wait_slot(n);
-          if (half == 0) {
-            facts(tile, cur, 0.0f, 0.0f);
-            tails = (tails << 1) | (cur.tail ? 1u : 0u);
+      auto stage = [&](int n, const Tile& x, bool is_v) {
+        const uint32_t dst = base_s + L::RAW0 + (n % L::RAWS) * L::RAW;
+        const uint32_t bar = smem_addr(&sh.raw[n % L::RAWS][pw]);
+        if (x.boxes) {
+          by_boxes(dst, 0, is_v ? &vmap : &kmap, x, bar);
+        } else {
+          const char* src = static_cast<const char*>(is_v ? c.v : c.k);
+#pragma unroll
+          for (int i = 0; i < RC; ++i) {
+            const int y = i * 32 + lane, key = y / RC, ch = y % RC;
+            const int r = __shfl_sync(0xFFFFFFFFu, x.row, key);
+            copy16(dst + raw_chunk(pw * 32 + key, ch), src + (int64_t)max(r, 0) * D + ch * 16, r >= 0);
           }
-          stage(n, cur, half == 1);
-          if (n >= LAG) {
-            copy_wait<LAG>();
-            // operand tile n - LAG (LAG even): the same half, LAG / 2 tiles ago
-            publish(n - LAG, half == 1 && ((tails >> (LAG / 2)) & 1u));
+          copy_arrive(bar);
+        }
+      };
+      auto widen = [&](int n, bool tail_v) {
+        wait_or_give_up(sh, smem_addr(&sh.raw[n % L::RAWS][pw]), (uint32_t)(n / L::RAWS) & 1u);
+        wait_slot(n);
+        const uint32_t raw = base_s + L::RAW0 + (n % L::RAWS) * L::RAW;
+        const uint32_t dst = base_s + L::OPS + (n % L::SLOTS) * L::SLOT;
+        bool hit = false;
+#pragma unroll
+        for (int i = 0; i < RC; ++i) {
+          const int key = pw * 32 + (lane & 7) + 8 * (RC == 8 ? i >> 1 : i);
+          const int ch = (lane >> 3) + (RC == 8 ? 4 * (i & 1) : 0);
+          const uint4 w = lds128(raw + raw_chunk(key, ch));
+          uint4 lo = make_uint4(e4m3x2_f16x2(w.x), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y), e4m3x2_f16x2(w.y >> 16));
+          uint4 hi = make_uint4(e4m3x2_f16x2(w.z), e4m3x2_f16x2(w.z >> 16), e4m3x2_f16x2(w.w), e4m3x2_f16x2(w.w >> 16));
+          if (tail_v) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
+          sts128(dst + op_chunk(key, 2 * ch), lo);
+          sts128(dst + op_chunk(key, 2 * ch + 1), hi);
+        }
+        if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
+        fence_async_proxy();
+        mbar_arrive(smem_addr(&sh.full[n % L::SLOTS]));
+        __syncwarp();   // the raw tile is read before it is filled again
+      };
+      auto scales = [&](const Tile& x, float& ks, float& vs) {
+        ks = x.row >= 0 ? __ldg(c.ks + x.row) : 0.0f;
+        vs = x.row >= 0 ? __ldg(c.vs + x.row) : 1.0f;
+      };
+      float k0 = 0.0f, v0 = 1.0f, k1 = 0.0f, v1 = 1.0f;
+      bool more_next = false;
+      if (more_tiles) {
+        scales(cur, k0, v0);
+        stage(0, cur, false);
+        stage(1, cur, true);
+        more_next = advance(nxt);
+      }
+      for (int n = 0, tile = 0; more_tiles; n += 2, ++tile) {
+        if (more_next) {
+          stage(n + 2, nxt, false);
+          scales(nxt, k1, v1);
+        }
+        facts(tile, cur, k0, v0);
+        widen(n, false);
+        if (more_next) stage(n + 3, nxt, true);
+        widen(n + 1, cur.tail);
+        cur = nxt;
+        more_tiles = more_next;
+        k0 = k1;
+        v0 = v1;
+        more_next = more_tiles && advance(nxt);
+      }
+    } else {
+      auto stage = [&](int n, const Tile& x, bool is_v) {
+        const uint32_t dst = base_s + L::OPS + (n % L::SLOTS) * L::SLOT;
+        const uint32_t bar = smem_addr(&sh.full[n % L::SLOTS]);
+        if (x.boxes) {
+          by_boxes(dst, kTK * 128, is_v ? &vmap : &kmap, x, bar);
+          return;
+        }
+        const char* src = static_cast<const char*>(is_v ? c.v : c.k);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int y = i * 32 + lane, key = y / CH, ch = y % CH;
+          const int r = __shfl_sync(0xFFFFFFFFu, x.row, key);
+          copy16(dst + op_chunk(pw * 32 + key, ch), src + (int64_t)max(r, 0) * (2 * D) + ch * 16, r >= 0);
+        }
+        if (!(is_v && x.tail)) {
+          copy_arrive(bar);
+          return;
+        }
+        // values of a tile that holds nodes: see clear_nonfinite
+        copy_commit();
+        copy_wait<0>();
+        bool hit = false;
+        for (int i = 0; i < CH; ++i) {
+          const int y = i * 32 + lane, key = y / CH, ch = y % CH;
+          const uint32_t at = dst + op_chunk(pw * 32 + key, ch);
+          uint4 w = lds128(at);
+          if (clear_nonfinite<E>(w)) {
+            sts128(at, w);
+            hit = true;
           }
         }
-        ++tile;
+        if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
+        fence_async_proxy();
+        mbar_arrive(bar);
+      };
+      for (int n = 0, tile = 0; more_tiles; n += 2, ++tile) {
+        const bool more_next = advance(nxt);
+        wait_slot(n);
+        facts(tile, cur, 0.0f, 0.0f);
+        stage(n, cur, false);
+        wait_slot(n + 1);
+        stage(n + 1, cur, true);
         cur = nxt;
-        have = have_next;
+        more_tiles = more_next;
       }
-      copy_wait<0>();
-      for (int m = n > LAG ? n - LAG : 0; m < n; ++m)
-        publish(m, (m & 1) && ((tails >> ((n - 1) / 2 - m / 2)) & 1u));
     }
+    copy_commit();
+    copy_wait<0>();
   } else {
     // ---- softmax ----------------------------------------------------------------
     const int w = warp / kGroupWarps;            // group: tiles w, w + 2, ... of a segment
@@ -628,35 +689,49 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
             bits[i] &= lv;
           }
           const float* fk = reinterpret_cast<const float*>(smem + L::FACT) + f * 3 * kTK;
-          // scores of 32 keys, base 2 (8-bit caches: with the scale of V in the
-          // exponent, so that the weights that meet V are bounded)
-          auto scores = [&](int i, float* s) {
-            tc_ld32(ts + i * 32, s);
+          // 8-bit caches: base-2 scores of 32 keys with the scale of V in the
+          // exponent, so that the weights that meet V are bounded
+          const uint64_t rowf2 = pair(rowf, rowf);
+          auto scaled = [&](int i, float* s) {
             if constexpr (FP8) {
 #pragma unroll
               for (int k = 0; k < 32; k += 4) {
-                const float4 kf = *reinterpret_cast<const float4*>(fk + i * 32 + k);
-                const float4 lv = *reinterpret_cast<const float4*>(fk + kTK + i * 32 + k);
-                s[k] = fmaf(s[k] * kf.x, rowf, lv.x);
-                s[k + 1] = fmaf(s[k + 1] * kf.y, rowf, lv.y);
-                s[k + 2] = fmaf(s[k + 2] * kf.z, rowf, lv.z);
-                s[k + 3] = fmaf(s[k + 3] * kf.w, rowf, lv.w);
+                const ulonglong2 kf = *reinterpret_cast<const ulonglong2*>(fk + i * 32 + k);
+                const ulonglong2 lv = *reinterpret_cast<const ulonglong2*>(fk + kTK + i * 32 + k);
+                unpair(fma2(mul2(pair(s[k], s[k + 1]), kf.x), rowf2, lv.x), s[k], s[k + 1]);
+                unpair(fma2(mul2(pair(s[k + 2], s[k + 3]), kf.y), rowf2, lv.y), s[k + 2], s[k + 3]);
               }
             }
+          };
+          auto hide = [&](int i, float* s) {
             if (masked) {
+              const uint32_t see = i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3];
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (!((bits[i] >> k) & 1u)) s[k] = -INFINITY;
+                if (!((see >> k) & 1u)) s[k] = -INFINITY;
             }
           };
-          float mx = -INFINITY;
+          float mx = -INFINITY, my = -INFINITY;
+          {
+            float s[2][32];
+            tc_ld32(ts, s[0]);
+#pragma unroll 1
+            for (int i = 0; i < 4; i += 2) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float s[32];
-            scores(i, s);
+              for (int z = 0; z < 2; ++z) {
+                tc_wait32(s[z]);
+                if (i + z < 3) tc_ld32(ts + (i + z + 1) * 32, s[z ^ 1]);
+                scaled(i + z, s[z]);
+                hide(i + z, s[z]);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, s[k]);
+                for (int k = 0; k < 32; k += 4) {
+                  mx = max3(mx, s[z][k], s[z][k + 1]);
+                  my = max3(my, s[z][k + 2], s[z][k + 3]);
+                }
+              }
+            }
           }
+          mx = fmaxf(mx, my);
           if (!FP8) mx = mx == -INFINITY ? mx : mx * rowf;
           // the reference follows the maximum only when it is left far behind
           const bool move = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
@@ -664,10 +739,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
           if (j >= 2 && __any_sync(0xFFFFFFFFu, move)) {
             const float fix = move ? ex2(m - mn) : 1.0f;
             l *= fix;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
               float o[32];
               tc_ld32(to + i * 32, o);
+              tc_wait32(o);
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] *= fix;
               tc_st32(to + i * 32, o);
@@ -675,38 +751,44 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
           }
           m = mn;
           const float ref = (m == -INFINITY ? 0.0f : m) - kHead;
+          const uint64_t ref2 = pair(-ref, -ref);
           // weights, rounded to 16 bits for the product with V (half a step each
           // at most) and summed unrounded
-          float sum0 = 0.0f, sum1 = 0.0f;
+          uint64_t sum = 0;   // (0, 0)
+          {
+            float s[2][32];
+            tc_ld32(ts, s[0]);
+#pragma unroll 1
+            for (int i = 0; i < 4; i += 2) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float s[32];
-            scores(i, s);
-            uint32_t p[16];
-            const float* iv = fk + 2 * kTK + i * 32;
+              for (int z = 0; z < 2; ++z) {
+                tc_wait32(s[z]);
+                if (i + z < 3) tc_ld32(ts + (i + z + 1) * 32, s[z ^ 1]);
+                scaled(i + z, s[z]);
+                uint32_t p[16];
+                const float* iv = fk + 2 * kTK + (i + z) * 32;
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float e0, e1;
-              if constexpr (FP8) {
-                e0 = ex2(s[k] - ref);
-                e1 = ex2(s[k + 1] - ref);
-                const float2 v = *reinterpret_cast<const float2*>(iv + k);
-                sum0 = fmaf(e0, v.x, sum0);
-                sum1 = fmaf(e1, v.y, sum1);
-              } else {
-                e0 = ex2(fmaf(s[k], rowf, -ref));
-                e1 = ex2(fmaf(s[k + 1], rowf, -ref));
-                if (masked) {   // a factor of 0 would make NaN of -inf
-                  e0 = ((bits[i] >> k) & 1u) ? e0 : 0.0f;
-                  e1 = ((bits[i] >> (k + 1)) & 1u) ? e1 : 0.0f;
+                for (int k = 0; k < 32; k += 2) {
+                  float e0, e1;
+                  unpair(FP8 ? add2(pair(s[z][k], s[z][k + 1]), ref2)
+                             : fma2(pair(s[z][k], s[z][k + 1]), rowf2, ref2), e0, e1);
+                  s[z][k] = e0;
+                  s[z][k + 1] = e1;
                 }
-                sum0 += e0;
-                sum1 += e1;
+                hide(i + z, s[z]);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                  const float e0 = ex2(s[z][k]), e1 = ex2(s[z][k + 1]);
+                  if constexpr (FP8) sum = fma2(pair(e0, e1), *reinterpret_cast<const uint64_t*>(iv + k), sum);
+                  else sum = add2(sum, pair(e0, e1));
+                  p[k / 2] = pack2(e0, e1, E());
+                }
+                tc_st16(ts + (i + z) * 16, p);
               }
-              p[k / 2] = pack2(e0, e1, E());
             }
-            tc_st16(ts + i * 16, p);
           }
+          float sum0, sum1;
+          unpair(sum, sum0, sum1);
           l += sum0 + sum1;
           tc_wait_st();
         }
@@ -730,16 +812,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
         const int64_t slot = 2 * (int64_t)blockIdx.x + (first ? 0 : 1);
         const bool poison = *reinterpret_cast<volatile int*>(&sh.poison) != 0;
         const uint32_t o0 = tm + lanes + 256 + w * (D / 2), o1 = o0 + 128;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < D / 64; ++i) {
           float x[32];
           __syncwarp();
           tc_ld32(o0 + i * 32, x);
+          tc_wait32(x);
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = s0.x == -INFINITY ? 0.0f : x[k] * f0;
           if (n > 1) {
             float y[32];
             tc_ld32(o1 + i * 32, y);
+            tc_wait32(y);
 #pragma unroll
             for (int k = 0; k < 32; ++k) x[k] += s1.x == -INFINITY ? 0.0f : y[k] * f1;
           }
@@ -809,13 +893,44 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const Atte
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(512));
 }
 
+// The array of cache rows as TMA sees it: [rows, D] with boxes of `box` rows and
+// 128 (8-bit: D) bytes, swizzled.  Encoded for every call: nothing is kept by an
+// address.
+bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int D, int box, bool fp8) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult got;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &got) != cudaSuccess ||
+        got != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(D * (fp8 ? 1 : 2))};
+  const cuuint32_t boxes[2] = {(cuuint32_t)(fp8 ? D : 64), (cuuint32_t)box}, steps[2] = {1, 1};
+  return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base),
+                dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                fp8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, bool FP8, int D>
 int launch_tile(const AttendArgs& a, int num_sms, cudaStream_t st) {
   auto kern = attend_tile_kernel<T, FP8, D>;
   constexpr int bytes = TileLayout<FP8, D>::BYTES;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return SPECDEC_ERR_CUDA;
-  kern<<<num_sms, kTileThreads, bytes, st>>>(a);
+  // rows of a box: within one page, whole groups of 8 rows of the swizzle
+  const int page = a.c.geo.page_size;
+  int box = page % 32 == 0 ? 32 : page % 16 == 0 ? 16 : page % 8 == 0 ? 8 : 0;
+  CUtensorMap kmap = {}, vmap = {};
+  const int64_t rows = a.c.geo.num_pages * a.c.geo.kv_heads * page;
+  if (box && (!encode_rows(&kmap, a.c.k, rows, D, box, FP8) || !encode_rows(&vmap, a.c.v, rows, D, box, FP8))) box = 0;
+  kern<<<num_sms, kTileThreads, bytes, st>>>(a, box, kmap, vmap);
   if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
   return launch_join<T, kR, kTK, D>(a, num_sms, st);
 }
