@@ -69,26 +69,32 @@ struct TileShared {
 };
 
 // ---- tcgen05 -------------------------------------------------------------------
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// Issued by one thread (`one`) of a warp that takes part as a whole: descriptors
+// then stay in uniform registers (issued from inside a divergent branch every
+// product paid for moving them there, about 110 clocks instead of 64).
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
+      : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // d (+)= A B, both in shared memory
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(add), "r"(one)
       : "memory");
 }
 // d (+)= A B, A in tensor memory
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(add), "r"(one)
       : "memory");
 }
 
@@ -345,53 +351,53 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp == kMmaWarp) {
     // ---- products -------------------------------------------------------------
-    if (lane == 0) {
-      int seq = 0, tiles_of[2] = {0, 0};
-      uint32_t g = 0;
-      auto slot = [&](int n) { return base_s + L::OPS + (n % L::SLOTS) * L::SLOT; };
-      auto phase = [&](int n) { return (uint32_t)(n / L::SLOTS) & 1u; };
-      while (seg.next(c, group)) {
-        const int n = seg.t1 - seg.t0;
-        wait_or_give_up(sh, smem_addr(&sh.q_full), g & 1u);
-        for (int j = 0; j <= n; ++j) {
-          if (j < n) {
-            const int k = seq + 2 * j, w = j & 1;
-            // S_w and P_w are free once the product before last has read P_w
-            if (j >= 2) wait_or_give_up(sh, smem_addr(&sh.empty[(k - 3) % L::SLOTS]), phase(k - 3));
-            wait_or_give_up(sh, smem_addr(&sh.full[k % L::SLOTS]), phase(k));
-            fence_async_proxy();   // rows that came by 16-byte copies
-            tc_fence_after();
-            const uint64_t qd = operand(base_s + L::Q, 16), kd = operand(slot(k), 16);
+    const uint32_t one = lane == 0 ? 1u : 0u;
+    int seq = 0;
+    uint32_t g = 0, tiles_of[2] = {0, 0};
+    const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0), ops = __shfl_sync(0xFFFFFFFFu, base_s, 0);
+    auto slot = [&](int n) { return ops + L::OPS + (n % L::SLOTS) * L::SLOT; };
+    auto phase = [&](int n) { return (uint32_t)(n / L::SLOTS) & 1u; };
+    while (seg.next(c, group)) {
+      const int n = seg.t1 - seg.t0;
+      wait_or_give_up(sh, smem_addr(&sh.q_full), g & 1u);
+      for (int j = 0; j <= n; ++j) {
+        if (j < n) {
+          const int k = seq + 2 * j, w = j & 1;
+          // S_w and P_w are free once the product before last has read P_w
+          if (j >= 2) wait_or_give_up(sh, smem_addr(&sh.empty[(k - 3) % L::SLOTS]), phase(k - 3));
+          wait_or_give_up(sh, smem_addr(&sh.full[k % L::SLOTS]), phase(k));
+          fence_async_proxy();   // rows that came by 16-byte copies
+          tc_fence_after();
+          const uint64_t qd = operand(ops + L::Q, 16), kd = operand(slot(k), 16);
 #pragma unroll
-            for (int s = 0; s < KSTEPS; ++s) {
-              const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
-              tc_mma_ss(tm + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0);
-            }
-            tc_commit(smem_addr(&sh.s_full[w]));
-            tc_commit(smem_addr(&sh.empty[k % L::SLOTS]));
+          for (int s = 0; s < KSTEPS; ++s) {
+            const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
+            tc_mma_ss(tmu + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0, one);
           }
-          if (j > 0) {
-            const int v = seq + 2 * (j - 1) + 1, w = (j - 1) & 1;
-            wait_or_give_up(sh, smem_addr(&sh.full[v % L::SLOTS]), phase(v));
-            wait_or_give_up(sh, smem_addr(&sh.p_full[w]), (uint32_t)tiles_of[w] & 1u);
-            ++tiles_of[w];
-            fence_async_proxy();
-            tc_fence_after();
-            const uint64_t vd = operand(slot(v), kTK * 128);
-#pragma unroll
-            for (int s = 0; s < kTK / 16; ++s)
-              tc_mma_ts(tm + 256 + w * 128, tm + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
-                        s > 0 || j > 2);
-            tc_commit(smem_addr(&sh.empty[v % L::SLOTS]));
-          }
+          tc_commit(smem_addr(&sh.s_full[w]), one);
+          tc_commit(smem_addr(&sh.empty[k % L::SLOTS]), one);
         }
-        tc_commit(smem_addr(&sh.o_full));
-        mbar_arrive(smem_addr(&sh.o_full));
-        seq += 2 * n;
-        ++g;
+        if (j > 0) {
+          const int v = seq + 2 * (j - 1) + 1, w = (j - 1) & 1;
+          wait_or_give_up(sh, smem_addr(&sh.full[v % L::SLOTS]), phase(v));
+          wait_or_give_up(sh, smem_addr(&sh.p_full[w]), (w ? tiles_of[1] : tiles_of[0]) & 1u);
+          if (w) ++tiles_of[1]; else ++tiles_of[0];
+          fence_async_proxy();
+          tc_fence_after();
+          const uint64_t vd = operand(slot(v), kTK * 128);
+#pragma unroll
+          for (int s = 0; s < kTK / 16; ++s)
+            tc_mma_ts(tmu + 256 + w * 128, tmu + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
+                      s > 0 || j > 2, one);
+          tc_commit(smem_addr(&sh.empty[v % L::SLOTS]), one);
+        }
       }
+      tc_commit(smem_addr(&sh.o_full), one);
+      if (lane == 0) mbar_arrive(smem_addr(&sh.o_full));
+      __syncwarp();
+      seq += 2 * n;
+      ++g;
     }
-    __syncwarp();
   } else if (warp >= 2 * kGroupWarps) {
     // ---- producers: each warp owns 32 keys of every tile -----------------------
     const int pw = warp - 2 * kGroupWarps;
