@@ -2,7 +2,7 @@
 // (tcgen05, accumulators and weights in tensor memory).  Contract in
 // include/specdec.h (specdec_tree_attention).
 //
-// A unit is 128 rows x 128 keys.  Per SM one CTA of 13 warps:
+// A unit is 128 rows x 128 keys.  Per SM one CTA:
 //   producers (4 warps)  bring the keys' and values' rows of a tile, wherever their
 //                        pages lie, into the operand layout (128-byte swizzle):
 //                        tiles that are all context by TMA boxes of up to 32 rows
@@ -36,7 +36,7 @@ constexpr int kGroupWarps = 4;                       // softmax warps of a group
 constexpr int kSoftmaxThreads = 2 * kGroupWarps * 32;
 constexpr int kProducerWarps = 4;
 constexpr int kMmaWarp = 2 * kGroupWarps + kProducerWarps;
-constexpr int kTileThreads = (kMmaWarp + 1) * 32;
+constexpr int kTileThreads = (kMmaWarp + 4) * 32;    // a whole warpgroup: registers move between those
 constexpr int kFactorSlots = 4;                      // tiles whose key factors are held
 
 template <bool FP8, int D>
@@ -50,9 +50,9 @@ struct TileLayout {
   static constexpr int Q = 0;
   static constexpr int OPS = kR * D * 2;
   static constexpr int RAW0 = OPS + SLOTS * SLOT;
-  static constexpr int FACT = RAW0 + RAWS * RAW;     // [slot][k factor, log2 vs, 1 / vs][key]
+  static constexpr int FACT = RAW0 + RAWS * RAW;     // [slot][key]: scale of the key's row
   static constexpr int STATS = Q;                    // over the queries, once a segment's products are done
-  static constexpr int BYTES = FACT + (FP8 ? kFactorSlots * 3 * kTK * 4 : 0) + 1024;   // and room to align
+  static constexpr int BYTES = FACT + (FP8 ? kFactorSlots * kTK * 4 : 0) + 1024;   // and room to align
 };
 
 struct TileShared {
@@ -62,6 +62,7 @@ struct TileShared {
   uint64_t s_full[2], p_full[2];
   uint64_t q_full, o_full;
   uint32_t live[kFactorSlots][4];   // keys of a tile that the cache holds
+  float vexp[kFactorSlots][4];      // 8-bit caches: 32 keys' values are held as v 2^-vexp
   float rowf[kR];
   uint32_t tmem;
   int poison;                       // some tile with nodes held a value that is not finite (stays set)
@@ -98,33 +99,24 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       : "memory");
 }
 
-// 32 neighbouring columns of this thread's lane: issued, and waited for by a
-// statement that the values pass through, so that no use can move before it
-// (it waits for every load issued so far).
+// Neighbouring columns of this thread's lane.  The wait stands in the same
+// statement, so that no use of the values can move before it.
+__device__ __forceinline__ void tc_ld64(uint32_t addr, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31]),"=r"(r[32]),"=r"(r[33]),"=r"(r[34]),"=r"(r[35]),"=r"(r[36]),"=r"(r[37]),"=r"(r[38]),"=r"(r[39]),"=r"(r[40]),"=r"(r[41]),"=r"(r[42]),"=r"(r[43]),"=r"(r[44]),"=r"(r[45]),"=r"(r[46]),"=r"(r[47]),"=r"(r[48]),"=r"(r[49]),"=r"(r[50]),"=r"(r[51]),"=r"(r[52]),"=r"(r[53]),"=r"(r[54]),"=r"(r[55]),"=r"(r[56]),"=r"(r[57]),"=r"(r[58]),"=r"(r[59]),"=r"(r[60]),"=r"(r[61]),"=r"(r[62]),"=r"(r[63])
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tc_ld32(uint32_t addr, float* x) {
   uint32_t* r = reinterpret_cast<uint32_t*>(x);
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void tc_wait32(float* x) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(x);
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]),"+r"(r[1]),"+r"(r[2]),"+r"(r[3]),"+r"(r[4]),"+r"(r[5]),"+r"(r[6]),"+r"(r[7]),"+r"(r[8]),"+r"(r[9]),"+r"(r[10]),"+r"(r[11]),"+r"(r[12]),"+r"(r[13]),"+r"(r[14]),"+r"(r[15]),"+r"(r[16]),"+r"(r[17]),"+r"(r[18]),"+r"(r[19]),"+r"(r[20]),"+r"(r[21]),"+r"(r[22]),"+r"(r[23]),"+r"(r[24]),"+r"(r[25]),"+r"(r[26]),"+r"(r[27]),"+r"(r[28]),"+r"(r[29]),"+r"(r[30]),"+r"(r[31])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tc_st32(uint32_t addr, const float* x) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31])
+      : "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
@@ -132,6 +124,15 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -222,6 +223,25 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 8 f16 values times a pair of equal factors.
+__device__ __forceinline__ uint4 times(uint4 w, uint32_t by) {
+  __half2* h = reinterpret_cast<__half2*>(&w);
+  const __half2 f = *reinterpret_cast<const __half2*>(&by);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __hmul2(h[i], f);
+  return w;
+}
+
+// Two 16-bit weights times 2^x (a power of two, exact where it does not underflow).
+__device__ __forceinline__ uint32_t shrink(uint32_t w, float by, __half) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(by));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t shrink(uint32_t w, float by, __nv_bfloat16) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(by));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Takes the non-finite 16-bit values out of w; whether there were any.  A row's
 // hidden nodes have weight 0, and 0 x inf would reach it through the product: in
 // tiles that hold nodes such values are left out, and the rows that do see their
@@ -248,6 +268,7 @@ __device__ __forceinline__ bool clear_nonfinite(uint4& w) {
 // A wait that gives up: the role goes on without waiting (its loops are finite
 // and its addresses do not depend on data), and the call reports the timeout.
 __device__ __forceinline__ void wait_or_give_up(TileShared& sh, uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return;
   if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
   if (!mbar_wait(bar, parity)) *reinterpret_cast<volatile int*>(&sh.dead) = 1;
 }
@@ -349,7 +370,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   seg.q = attend_request(c, group, seg.b, kR, kTK, ignored);
   uint32_t bad = 0;
 
-  if (warp == kMmaWarp) {
+  // Registers: 4 warpgroups are launched with 128 a thread.  The products' give 72,
+  // the producers' 16; the softmax groups take 40 each (168 + 168 + 112 + 56 <=
+  // 4 * 128).
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == kMmaWarp) {
     // ---- products -------------------------------------------------------------
     const uint32_t one = lane == 0 ? 1u : 0u;
     int seq = 0;
@@ -398,7 +424,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       seq += 2 * n;
       ++g;
     }
+    }
   } else if (warp >= 2 * kGroupWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
     // ---- producers: each warp owns 32 keys of every tile -----------------------
     const int pw = warp - 2 * kGroupWarps;
     struct Tile {
@@ -434,20 +462,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     auto wait_slot = [&](int n) {
       wait_or_give_up(sh, smem_addr(&sh.empty[n % L::SLOTS]), ((uint32_t)(n / L::SLOTS) & 1u) ^ 1u);
     };
-    auto facts = [&](int tile_no, const Tile& x, float ks, float vs) {
+    // What softmax needs to know of the tile's keys.  8-bit caches: the scale of
+    // K (applied to the scores, in 32 bits); the scale of V goes into the widened
+    // values, as a factor v 2^-vexp that f16 holds: the largest of the warp's 32
+    // keys lies in [2^5, 2^6), so products stay below 2^15 and keys down to 2^-20
+    // of the largest keep f16's full precision.  Returns that factor.
+    auto facts = [&](int tile_no, const Tile& x, float ks, float vs) -> float {
       const int f = tile_no % kFactorSlots;
       const uint32_t live = __ballot_sync(0xFFFFFFFFu, x.row >= 0);
       if (lane == 0) sh.live[f][pw] = live;
+      float factor = 0.0f;
       if constexpr (FP8) {
-        float* fp = reinterpret_cast<float*>(smem + L::FACT) + f * 3 * kTK + pw * 32 + lane;
-        const float vc = vs == vs ? fmaxf(vs, 8.673617379884035e-19f) : vs;   // 0: a row of zeros
-        const float iv = __frcp_rn(vc);   // finite: it meets weights of 0 (a NaN scale shows in log2 vs)
-        fp[0] = x.row >= 0 ? ks : 0.0f;
-        fp[kTK] = x.row >= 0 ? __log2f(vc) : 0.0f;
-        fp[2 * kTK] = x.row >= 0 && isfinite(iv) ? iv : 0.0f;
+        reinterpret_cast<float*>(smem + L::FACT)[f * kTK + pw * 32 + lane] = x.row >= 0 ? ks : 0.0f;
+        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, x.row >= 0 && vs > 0.0f && isfinite(vs) ? __float_as_uint(vs) : 0u);
+        const int b = most ? min(max((int)(most >> 23) - 127 - 5, -80), 80) : 0;
+        if (lane == 0) sh.vexp[f][pw] = (float)b;
+        if (x.row >= 0) factor = vs * __uint_as_float((uint32_t)(127 - b) << 23);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
+      return factor;
     };
     // This warp's 32 rows of the array that `map` describes by boxes of `box`
     // rows and 128 (or D) bytes; every lane arrives on `bar`.
@@ -488,7 +522,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           copy_arrive(bar);
         }
       };
-      auto widen = [&](int n, bool tail_v) {
+      auto widen = [&](int n, bool is_v, bool tail, float factor) {
+        const uint32_t own = pack2(factor, factor, __half());
         wait_or_give_up(sh, smem_addr(&sh.raw[n % L::RAWS][pw]), (uint32_t)(n / L::RAWS) & 1u);
         wait_slot(n);
         const uint32_t raw = base_s + L::RAW0 + (n % L::RAWS) * L::RAW;
@@ -501,7 +536,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint4 w = lds128(raw + raw_chunk(key, ch));
           uint4 lo = make_uint4(e4m3x2_f16x2(w.x), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y), e4m3x2_f16x2(w.y >> 16));
           uint4 hi = make_uint4(e4m3x2_f16x2(w.z), e4m3x2_f16x2(w.z >> 16), e4m3x2_f16x2(w.w), e4m3x2_f16x2(w.w >> 16));
-          if (tail_v) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
+          if (is_v) {
+            const uint32_t by = __shfl_sync(0xFFFFFFFFu, own, key & 31);
+            lo = times(lo, by);
+            hi = times(hi, by);
+            if (tail) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
+          }
           sts128(dst + op_chunk(key, 2 * ch), lo);
           sts128(dst + op_chunk(key, 2 * ch + 1), hi);
         }
@@ -527,10 +567,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           stage(n + 2, nxt, false);
           scales(nxt, k1, v1);
         }
-        facts(tile, cur, k0, v0);
-        widen(n, false);
+        const float factor = facts(tile, cur, k0, v0);
+        widen(n, false, false, 0.0f);
         if (more_next) stage(n + 3, nxt, true);
-        widen(n + 1, cur.tail);
+        widen(n + 1, true, cur.tail, factor);
         cur = nxt;
         more_tiles = more_next;
         k0 = k1;
@@ -588,6 +628,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     copy_wait<0>();
   } else {
     // ---- softmax ----------------------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int w = warp / kGroupWarps;            // group: tiles w, w + 2, ... of a segment
     const int row = (warp % kGroupWarps) * 32 + lane;   // row of the tile = lane of tensor memory
     const uint32_t lanes = (uint32_t)(warp % kGroupWarps) << 21;   // first lane, in bits 16..
@@ -609,7 +650,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                        (int64_t)(seg.h * group + gr % group) * a.q_head + ch * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (live) v = __ldg(reinterpret_cast<const uint4*>(src));
-        float f = fabsf(a.scale_log2);
+        float f = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);   // above 0: hidden keys are -inf times this
         if constexpr (FP8) {
           // f16 factors: the row is scaled by a power of two so that its largest
           // value lies in [1, 2); the scores take the factor back
@@ -694,108 +735,106 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             masked |= lv != 0xFFFFFFFFu;
             bits[i] &= lv;
           }
-          const float* fk = reinterpret_cast<const float*>(smem + L::FACT) + f * 3 * kTK;
-          // 8-bit caches: base-2 scores of 32 keys with the scale of V in the
-          // exponent, so that the weights that meet V are bounded
+          // One pass over the scores, 64 keys at a time.  Weights are 2^(e - m),
+          // m a whole number that follows the running maximum only when that is
+          // kLazy above it: what has been summed, the row's O_w and the tile's
+          // weights so far are then multiplied by a power of two, which is exact.
+          const float* fk = reinterpret_cast<const float*>(smem + L::FACT) + f * kTK;
           const uint64_t rowf2 = pair(rowf, rowf);
-          auto scaled = [&](int i, float* s) {
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            float s[64];
+            tc_ld64(ts + i * 64, s);
+            float shift[2] = {0.0f, 0.0f};   // 8-bit caches: the values' exponents
             if constexpr (FP8) {
+              shift[0] = sh.vexp[f][2 * i];
+              shift[1] = sh.vexp[f][2 * i + 1];
 #pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                const ulonglong2 kf = *reinterpret_cast<const ulonglong2*>(fk + i * 32 + k);
-                const ulonglong2 lv = *reinterpret_cast<const ulonglong2*>(fk + kTK + i * 32 + k);
-                unpair(fma2(mul2(pair(s[k], s[k + 1]), kf.x), rowf2, lv.x), s[k], s[k + 1]);
-                unpair(fma2(mul2(pair(s[k + 2], s[k + 3]), kf.y), rowf2, lv.y), s[k + 2], s[k + 3]);
+              for (int k = 0; k < 64; k += 4) {
+                const ulonglong2 kf = *reinterpret_cast<const ulonglong2*>(fk + i * 64 + k);
+                unpair(mul2(pair(s[k], s[k + 1]), kf.x), s[k], s[k + 1]);
+                unpair(mul2(pair(s[k + 2], s[k + 3]), kf.y), s[k + 2], s[k + 3]);
+                if (k % 16 == 12) asm volatile("" ::: "memory");   // not all factors at once in registers
               }
             }
-          };
-          auto hide = [&](int i, float* s) {
+            const uint32_t see[2] = {i ? bits[2] : bits[0], i ? bits[3] : bits[1]};
             if (masked) {
-              const uint32_t see = i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3];
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((see >> k) & 1u)) s[k] = -INFINITY;
+              for (int k = 0; k < 64; ++k)
+                if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = -INFINITY;
             }
-          };
-          float mx = -INFINITY, my = -INFINITY;
-          {
-            float s[2][32];
-            tc_ld32(ts, s[0]);
+            float mx[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float q[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) q[k] = fmaxf(s[32 * y + 2 * k], s[32 * y + 2 * k + 1]);
+#pragma unroll
+              for (int k = 8; k < 32; k += 8)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) q[x] = max3(q[x], s[32 * y + k + 2 * x], s[32 * y + k + 2 * x + 1]);
+              mx[y] = fmaxf(max3(q[0], q[1], q[2]), q[3]);
+              mx[y] = mx[y] == -INFINITY ? mx[y] : fmaf(mx[y], rowf, shift[y]);
+            }
+            const float most = fmaxf(mx[0], mx[1]);
+            const bool move = most > m + kLazy || (m == -INFINITY && most != -INFINITY);
+            if (__any_sync(0xFFFFFFFFu, move)) {
+              const float to_m = move ? ceilf(most) : m;
+              const float fix = move ? ex2(m - to_m) : 1.0f;
+              m = to_m;
+              if (j >= 2 || i > 0) {
+                tc_wait_st();   // what is read back here has been stored
+                l *= fix;
+                if (i > 0) {
 #pragma unroll 1
-            for (int i = 0; i < 4; i += 2) {
+                  for (int p = 0; p < 2; ++p) {
+                    uint32_t w16[16];
+                    tc_ld16(ts + p * 16, w16);
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                tc_wait32(s[z]);
-                if (i + z < 3) tc_ld32(ts + (i + z + 1) * 32, s[z ^ 1]);
-                scaled(i + z, s[z]);
-                hide(i + z, s[z]);
+                    for (int k = 0; k < 16; ++k) w16[k] = shrink(w16[k], fix, E());
+                    tc_st16(ts + p * 16, w16);
+                  }
+                }
+                if (j >= 2) {
+#pragma unroll 1
+                  for (int p = 0; p < D / 16; ++p) {
+                    uint32_t o[16];
+                    tc_ld16(to + p * 16, o);
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                  mx = max3(mx, s[z][k], s[z][k + 1]);
-                  my = max3(my, s[z][k + 2], s[z][k + 3]);
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
+                    tc_st16(to + p * 16, o);
+                  }
                 }
               }
             }
-          }
-          mx = fmaxf(mx, my);
-          if (!FP8) mx = mx == -INFINITY ? mx : mx * rowf;
-          // the reference follows the maximum only when it is left far behind
-          const bool move = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
-          const float mn = move ? mx : m;
-          if (j >= 2 && __any_sync(0xFFFFFFFFu, move)) {
-            const float fix = move ? ex2(m - mn) : 1.0f;
-            l *= fix;
-#pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
-              float o[32];
-              tc_ld32(to + i * 32, o);
-              tc_wait32(o);
+            // weights, rounded to 16 bits for the product with V (half a step
+            // each at most) and summed unrounded
+            const float ref = (m == -INFINITY ? 0.0f : m) - kHead;
+            uint64_t sum[2][2] = {{0, 0}, {0, 0}};
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= fix;
-              tc_st32(to + i * 32, o);
-            }
-          }
-          m = mn;
-          const float ref = (m == -INFINITY ? 0.0f : m) - kHead;
-          const uint64_t ref2 = pair(-ref, -ref);
-          // weights, rounded to 16 bits for the product with V (half a step each
-          // at most) and summed unrounded
-          uint64_t sum = 0;   // (0, 0)
-          {
-            float s[2][32];
-            tc_ld32(ts, s[0]);
-#pragma unroll 1
-            for (int i = 0; i < 4; i += 2) {
+            for (int y = 0; y < 2; ++y) {
+              const float add = shift[y] - ref;
+              const uint64_t add_2 = pair(add, add);
+              uint32_t p[16];
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                tc_wait32(s[z]);
-                if (i + z < 3) tc_ld32(ts + (i + z + 1) * 32, s[z ^ 1]);
-                scaled(i + z, s[z]);
-                uint32_t p[16];
-                const float* iv = fk + 2 * kTK + (i + z) * 32;
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                  float e0, e1;
-                  unpair(FP8 ? add2(pair(s[z][k], s[z][k + 1]), ref2)
-                             : fma2(pair(s[z][k], s[z][k + 1]), rowf2, ref2), e0, e1);
-                  s[z][k] = e0;
-                  s[z][k + 1] = e1;
-                }
-                hide(i + z, s[z]);
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                  const float e0 = ex2(s[z][k]), e1 = ex2(s[z][k + 1]);
-                  if constexpr (FP8) sum = fma2(pair(e0, e1), *reinterpret_cast<const uint64_t*>(iv + k), sum);
-                  else sum = add2(sum, pair(e0, e1));
-                  p[k / 2] = pack2(e0, e1, E());
-                }
-                tc_st16(ts + (i + z) * 16, p);
+              for (int k = 0; k < 32; k += 2) {
+                float e0, e1;
+                unpair(fma2(pair(s[32 * y + k], s[32 * y + k + 1]), rowf2, add_2), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum[y][(k >> 1) & 1] = add2(sum[y][(k >> 1) & 1], pair(e0, e1));
+                p[k / 2] = pack2(e0, e1, E());
               }
+              tc_st16(ts + i * 32 + y * 16, p);
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float s0, s1;
+              unpair(add2(sum[y][0], sum[y][1]), s0, s1);
+              if constexpr (FP8) l = fmaf(s0 + s1, __uint_as_float((uint32_t)(127 - (int)shift[y]) << 23), l);
+              else l += s0 + s1;
             }
           }
-          float sum0, sum1;
-          unpair(sum, sum0, sum1);
-          l += sum0 + sum1;
           tc_wait_st();
         }
         tc_fence_before();
@@ -823,13 +862,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           float x[32];
           __syncwarp();
           tc_ld32(o0 + i * 32, x);
-          tc_wait32(x);
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = s0.x == -INFINITY ? 0.0f : x[k] * f0;
           if (n > 1) {
             float y[32];
             tc_ld32(o1 + i * 32, y);
-            tc_wait32(y);
 #pragma unroll
             for (int k = 0; k < 32; ++k) x[k] += s1.x == -INFINITY ? 0.0f : y[k] * f1;
           }
@@ -849,8 +886,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int d = 0; d < 32; ++d) {
                   float v;
                   if constexpr (FP8) {
-                    const uint8_t raw = static_cast<const uint8_t*>(c.v)[e + d];
-                    v = (raw & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.0f;
+                    const __half_raw hr =
+                        __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(c.v)[e + d], __NV_E4M3);
+                    v = __half2float(*reinterpret_cast<const __half*>(&hr)) * c.vs[r + (int64_t)seg.h * c.geo.page_size];
                   } else {
                     v = to_float(static_cast<const T*>(c.v)[e + d]);
                   }
