@@ -136,9 +136,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
   const int G = gridDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.q_heads / c.geo.kv_heads;
+  const PlanArgs plan(c, group);
   uint32_t why = 0;
   int64_t u0 = 0;
-  find_unit<kThreads>(c, group, R, TK,
+  find_unit<kThreads>(plan, R, TK,
                       [&](int64_t units) {
                         const int ranges = (int)min((int64_t)G, units);
                         u0 = (int)blockIdx.x < ranges ? range_begin(units, ranges, blockIdx.x) : units;
@@ -164,12 +165,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
   bool first_segment = true;
 
   uint32_t ignored = 0;
-  Request q = attend_request(c, group, b, R, TK, ignored);
+  Request q = attend_request(plan, b, R, TK, ignored);
   for (int64_t u = u0; u < uend;) {
     while (u >= base + q.units) {
       base += q.units;
       if (++b >= c.B) return;   // lengths that changed under the call
-      q = attend_request(c, group, b, R, TK, ignored);
+      q = attend_request(plan, b, R, TK, ignored);
     }
     const int64_t item = (u - base) / q.tiles;
     const int t0 = (int)((u - base) % q.tiles);

@@ -30,11 +30,23 @@ struct Request {
   int32_t tiles;   // key tiles
 };
 
+// What the plan of a call depends on.
+struct PlanArgs {
+  const int32_t* cu;
+  const int32_t* lengths;
+  int64_t N, capacity;      // node rows; slots of a request
+  int32_t B, kv_heads, group;
+  bool tree;
+
+  __host__ __device__ __forceinline__ explicit PlanArgs(const CacheArgs& c, int g)
+      : cu(c.cu), lengths(c.lengths), N(c.N), capacity((int64_t)c.geo.max_pages * c.geo.page_size), B(c.B),
+        kv_heads(c.geo.kv_heads), group(g), tree(c.parent != nullptr) {}
+};
+
 // The plan of request b for tiles of R rows and TK keys.  units = 0 for what
 // cannot be attended (no nodes, a cu or length out of range, a tree that is
 // too large); why gets the error bits.
-__host__ __device__ __forceinline__ Request attend_request(const CacheArgs& c, int group, int b, int R, int TK,
-                                                           uint32_t& why) {
+__host__ __device__ __forceinline__ Request attend_request(const PlanArgs& c, int b, int R, int TK, uint32_t& why) {
   Request q = {};
   if (!node_range(c.cu, b, c.N, q.first, q.n)) {
     why |= SPECDEC_DEVERR_BAD_CU;
@@ -42,17 +54,21 @@ __host__ __device__ __forceinline__ Request attend_request(const CacheArgs& c, i
   }
   q.len = c.lengths[b];
   if (q.n == 0) return q;
-  if (q.len < 0 || (int64_t)q.len + q.n > (int64_t)c.geo.max_pages * c.geo.page_size) {
+  if (q.len < 0 || (int64_t)q.len + q.n > c.capacity) {
     why |= SPECDEC_DEVERR_BAD_CACHE;
     return q;
   }
-  if (c.parent && q.n > kMaxTreeNodes) {
+  if (c.tree && q.n > kMaxTreeNodes) {
     why |= SPECDEC_DEVERR_BAD_TREE;
     return q;
   }
-  q.rts = (int32_t)(((int64_t)q.n * group + R - 1) / R);
+  q.rts = (int32_t)(((int64_t)q.n * c.group + R - 1) / R);
   q.tiles = (int32_t)(((int64_t)q.len + q.n + TK - 1) / TK);
-  q.units = (int64_t)c.geo.kv_heads * q.rts * q.tiles;
+  q.units = (int64_t)c.kv_heads * q.rts * q.tiles;
+  if (q.units >= ((int64_t)1 << 31)) {   // units of a request are counted in 32 bits
+    q.units = 0;
+    why |= SPECDEC_DEVERR_BAD_CACHE;
+  }
   return q;
 }
 
@@ -68,13 +84,13 @@ struct ScanShared {
 // Units of all requests, and the request that holds unit `want(total)` with
 // the units before it.  Every thread of the block calls; NT threads.
 template <int NT, typename Want>
-__device__ __forceinline__ void find_unit(const CacheArgs& c, int group, int R, int TK, Want want,
+__device__ __forceinline__ void find_unit(const PlanArgs& c, int R, int TK, Want want,
                                           ScanShared& sh, uint32_t& why) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (c.B + NT - 1) / NT;
   const int b0 = min(c.B, tid * per), b1 = min(c.B, b0 + per);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += attend_request(c, group, b, R, TK, why).units;
+  for (int b = b0; b < b1; ++b) mine += attend_request(c, b, R, TK, why).units;
   int64_t scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -98,7 +114,7 @@ __device__ __forceinline__ void find_unit(const CacheArgs& c, int group, int R, 
   int64_t at = sh.warp[warp] + scan - mine;
   if (at <= u && u < at + mine) {   // one thread at most
     for (int b = b0; b < b1; ++b) {
-      const int64_t x = attend_request(c, group, b, R, TK, why).units;
+      const int64_t x = attend_request(c, b, R, TK, why).units;
       if (u < at + x) {
         sh.b = b;
         sh.before = at;
@@ -159,12 +175,12 @@ struct Partials {
 template <typename T, int R, int TK, int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, const int G) {
   __shared__ ScanShared sh;
-  const CacheArgs& c = a.c;
-  const int group = a.q_heads / c.geo.kv_heads;
+  const int group = a.q_heads / a.c.geo.kv_heads;
+  const PlanArgs plan(a.c, group);
   uint32_t why = 0;
   int64_t u = 0;
   int ranges = 0;
-  find_unit<128>(c, group, R, TK,
+  find_unit<128>(plan, R, TK,
                  [&](int64_t units) {
                    ranges = (int)min((int64_t)G, units);
                    u = (int)blockIdx.x + 1 < ranges ? range_begin(units, ranges, blockIdx.x + 1) : units;
@@ -174,7 +190,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, co
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if ((int)blockIdx.x + 1 >= ranges || sh.b < 0) return;
   const int g0 = blockIdx.x;                     // the range before the boundary
-  const Request q = attend_request(c, group, sh.b, R, TK, why);
+  const Request q = attend_request(plan, sh.b, R, TK, why);
   if (q.units == 0) return;
   const int64_t item = (u - sh.before) / q.tiles;
   const int64_t u0 = sh.before + item * q.tiles, u1 = u0 + q.tiles;

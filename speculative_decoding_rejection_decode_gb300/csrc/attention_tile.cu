@@ -3,12 +3,14 @@
 // include/specdec.h (specdec_tree_attention).
 //
 // A unit is 128 rows x 128 keys.  Per SM one CTA:
-//   producers (4 warps)  bring the keys' and values' rows of a tile, wherever their
-//                        pages lie, into the operand layout (128-byte swizzle):
-//                        tiles that are all context by TMA boxes of up to 32 rows
-//                        of a page, tiles that hold nodes, bad pages or pages of
-//                        odd sizes by 16-byte copies; 8-bit rows land in a small
-//                        ring first and are widened to f16 on the way;
+//   loaders (3 warps)    look up the pages and bring the rows of keys and values, every
+//                        third tile each, so that one's look-ups hide behind the others',
+//                        into the operand layout (swizzled rows of 128 bytes): by
+//                        TMA boxes of up to 32 rows of a page, or by 16-byte copies
+//                        where 32 keys hold nodes, end, miss a page or lie in pages
+//                        of odd sizes;
+//   wideners (4 warps)   8-bit caches: turn the values of a landed tile into f16
+//                        (the keys are multiplied as they are, see below);
 //   products (1 thread)  S_w = Q K^T (both operands in shared memory) and
 //                        O_w += P_w V (P in tensor memory);
 //   softmax (2 groups    group w takes every second tile of a segment with a
@@ -17,6 +19,13 @@
 //                        products and nothing of a row crosses threads.
 // Tensor memory: S_0, S_1 (P_w lies over S_w), O_0, O_1: 4 x 128 columns.
 // The two groups' results are joined when a segment ends.
+//
+// 8-bit keys meet the queries in e4m3 products: a query is the sum of two (f16:
+// three) e4m3 parts of 4 bits each, q = hi + lo (+ lo2), which hold bf16's 8 (f16's
+// 11) bits exactly down to 2^-9 (2^-6) of the row's largest value and to 2^-17 of it
+// below.  That keeps the keys as they lie in memory (widening keys as well as
+// values bound the kernel to 540 us where this form took 300: 32 requests of 29
+// nodes, 6000 to 16000 keys).  The keys' scales are applied to the scores.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -34,35 +43,42 @@ namespace {
 constexpr int kR = 128, kTK = 128;
 constexpr int kGroupWarps = 4;                       // softmax warps of a group
 constexpr int kSoftmaxThreads = 2 * kGroupWarps * 32;
-constexpr int kProducerWarps = 4;
-constexpr int kMmaWarp = 2 * kGroupWarps + kProducerWarps;
+constexpr int kWidenWarps = 4;
+constexpr int kMmaWarp = 2 * kGroupWarps + kWidenWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kLoaders = 3;                          // loader l takes tiles l, l + 3, ... of the range
 constexpr int kTileThreads = (kMmaWarp + 4) * 32;    // a whole warpgroup: registers move between those
-constexpr int kFactorSlots = 4;                      // tiles whose key factors are held
+constexpr int kFactSlots = 8;                        // tiles whose key facts are held (5 are needed)
 
-template <bool FP8, int D>
+template <typename T, bool FP8, int D>
 struct TileLayout {
-  static constexpr int SLOT = kTK * D * 2;           // one operand tile
-  // 16-bit caches: three tiles of K and V in flight.  8-bit: two, and three raw
-  // tiles before them (a raw tile is half as large)
-  static constexpr int SLOTS = FP8 ? 4 : 6;
-  static constexpr int RAW = FP8 ? kTK * D : 0;
-  static constexpr int RAWS = FP8 ? 3 : 0;
+  static constexpr int PARTS = FP8 ? (std::is_same<T, __half>::value ? 3 : 2) : 1;   // of a query
+  static constexpr int QB = kR * D * (FP8 ? PARTS : 2);
+  static constexpr int KB = kTK * D * (FP8 ? 1 : 2);   // a tile of keys
+  static constexpr int VB = kTK * D * 2;               // a tile of values as the product takes them
+  static constexpr int RB = FP8 ? kTK * D : 0;         // a tile of 8-bit values
+  static constexpr int KS = FP8 && PARTS == 2 ? 4 : 3; // tiles of each in flight
+  static constexpr int VS = FP8 ? 2 : 3;
+  static constexpr int RS = FP8 ? 3 : 0;
   static constexpr int Q = 0;
-  static constexpr int OPS = kR * D * 2;
-  static constexpr int RAW0 = OPS + SLOTS * SLOT;
-  static constexpr int FACT = RAW0 + RAWS * RAW;     // [slot][key]: scale of the key's row
-  static constexpr int STATS = Q;                    // over the queries, once a segment's products are done
-  static constexpr int BYTES = FACT + (FP8 ? kFactorSlots * kTK * 4 : 0) + 1024;   // and room to align
+  static constexpr int K = Q + QB;
+  static constexpr int V = K + KS * KB;
+  static constexpr int RAW = V + VS * VB;
+  static constexpr int KF = RAW + RS * RB;             // [slot][key] scale of the key
+  static constexpr int VF = KF + (FP8 ? kFactSlots * kTK * 4 : 0);   // [slot][key] factor of the values (f16 pair)
+  static constexpr int STATS = Q;                      // over the queries, once a segment's products are done
+  static constexpr int BYTES = VF + (FP8 ? kFactSlots * kTK * 4 : 0) + 1024;   // and room to align
 };
 
 struct TileShared {
-  uint64_t full[6], empty[6];
-  uint64_t raw[3][kProducerWarps];  // a warp's part of a raw tile has landed
-  uint64_t fact[kFactorSlots];
+  uint64_t k_full[4], k_empty[4];
+  uint64_t v_full[3], v_empty[3];
+  uint64_t raw_full[3], raw_empty[3];
+  uint64_t fact[kFactSlots];
   uint64_t s_full[2], p_full[2];
   uint64_t q_full, o_full;
-  uint32_t live[kFactorSlots][4];   // keys of a tile that the cache holds
-  float vexp[kFactorSlots][4];      // 8-bit caches: 32 keys' values are held as v 2^-vexp
+  uint32_t live[kFactSlots][4];     // keys of a tile that the cache holds
+  float vexp[kFactSlots][4];        // 8-bit caches: 32 keys' values are held as v 2^-vexp
+  int tail[kFactSlots];             // the tile holds nodes
   float rowf[kR];
   uint32_t tmem;
   int poison;                       // some tile with nodes held a value that is not finite (stays set)
@@ -87,6 +103,14 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, ui
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(add), "r"(one)
+      : "memory");
+}
+// the same for e4m3 factors, 32 of the summed dimension
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
       "r"(add), "r"(one)
       : "memory");
 }
@@ -137,27 +161,37 @@ __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t* r) {
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Shared-memory operand descriptor, 128-byte swizzle, rows of 128 bytes in
-// groups of 8 (1024 bytes apart).  `lead`: bytes between 64-element chunks
-// where the contiguous dimension is not the one summed over (V).
+// Shared-memory operand descriptor: swizzled rows of LINE = 128 (or 64) bytes in
+// groups of 8.  `lead`: bytes between 64-element chunks where the contiguous
+// dimension is not the one summed over (V).
+template <int LINE = 128>
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
   const uint32_t lo = ((addr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
-  const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  const uint32_t hi = (8u * LINE >> 4) | (1u << 14) | ((LINE == 128 ? 2u : 4u) << 29);
   return ((uint64_t)hi << 32) | lo;
 }
 
-// Instruction descriptor: f32 accumulators, 16-bit factors, 128 x n.
+// Instruction descriptors: f32 accumulators, 128 x n; 16-bit or e4m3 factors.
 template <typename E>
 __device__ __forceinline__ constexpr uint32_t product(int n, bool b_rows_summed) {
   const uint32_t t = std::is_same<E, __half>::value ? 0u : 1u;
   return (1u << 4) | (t << 7) | (t << 10) | (b_rows_summed ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kR >> 4) << 24);
 }
+__device__ __forceinline__ constexpr uint32_t product_e4m3(int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kR >> 4) << 24);
+}
 
 // Byte offset of 16-byte chunk c (of the row's 16-bit values) of row r of an
 // operand tile: [64-value half][row][128 bytes], chunks spread by the row.
 __device__ __forceinline__ uint32_t op_chunk(int r, int c) {
   return (uint32_t)((c >> 3) * (kTK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// The same for a tile of 8-bit rows of D bytes.
+template <int D>
+__device__ __forceinline__ uint32_t byte_chunk(int r, int c) {
+  return (uint32_t)(r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
@@ -218,6 +252,16 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
+  asm volatile("ld.shared.v2.u64 {%0,%1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -266,49 +310,120 @@ __device__ __forceinline__ bool clear_nonfinite(uint4& w) {
 }
 
 // A wait that gives up: the role goes on without waiting (its loops are finite
-// and its addresses do not depend on data), and the call reports the timeout.
+// and its addresses do not depend on data), and the call reports the timeout.  A
+// try sleeps up to a microsecond, so the wait ends within seconds at the most.
+// (Kept this small because it stands in many places: with a clock read in each,
+// the kernel's code passed the instruction cache.)
 __device__ __forceinline__ void wait_or_give_up(TileShared& sh, uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return;
-  if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
-  if (!mbar_wait(bar, parity)) *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+  for (int i = 0; i < (1 << 20); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return;
+    if ((i & 255) == 255 && *reinterpret_cast<volatile int*>(&sh.dead)) return;
+  }
+  *reinterpret_cast<volatile int*>(&sh.dead) = 1;
 }
 
-// The segments of this CTA's range, the same for every role.
+// The segments of this CTA's range; every role steps through them by itself, on a
+// copy in shared memory (registers are short).
 struct Segments {
-  int64_t u, end, base;
+  int64_t base;      // units before request b
+  int64_t end;
   Request q;
-  int b, h, rt, t0, t1, rows, node0;
-  bool whole, first;
-
-  __device__ __forceinline__ bool next(const CacheArgs& c, int group) {
-    if (u >= end) return false;
-    uint32_t ignored = 0;
-    while (u >= base + q.units) {
-      base += q.units;
-      if (++b >= c.B) return false;   // lengths that changed under the call
-      q = attend_request(c, group, b, kR, kTK, ignored);
-    }
-    const int64_t item = (u - base) / q.tiles;
-    t0 = (int)((u - base) % q.tiles);
-    t1 = (int)min((int64_t)q.tiles, t0 + (end - u));
-    h = (int)(item / q.rts);
-    rt = (int)(item % q.rts);
-    u += t1 - t0;
-    whole = t0 == 0 && t1 == q.tiles;
-    rows = min(kR, q.n * group - rt * kR);
-    node0 = rt * kR / group;
-    return true;
-  }
+  int b, h, rt, t0, t1, rows;
+  int u;             // next unit, from base
+  bool whole, more;
 };
+
+__device__ __forceinline__ void next_segment(Segments* s, const PlanArgs c) {
+  s->more = false;
+  if (s->base + s->u >= s->end) return;
+  uint32_t ignored = 0;
+  while (s->u >= (int)s->q.units) {
+    s->base += s->q.units;
+    s->u -= (int)s->q.units;
+    if (++s->b >= c.B) return;   // lengths that changed under the call
+    s->q = attend_request(c, s->b, kR, kTK, ignored);
+  }
+  const int tiles = s->q.tiles, rts = s->q.rts, u = s->u;
+  const int item = (int)((unsigned)u / (unsigned)tiles);
+  s->t0 = u - item * tiles;
+  s->t1 = (int)min((int64_t)tiles, s->t0 + (s->end - s->base - u));
+  s->h = (int)((unsigned)item / (unsigned)rts);
+  s->rt = item - s->h * rts;
+  s->u = u + s->t1 - s->t0;
+  s->whole = s->t0 == 0 && s->t1 == tiles;
+  s->rows = min(kR, s->q.n * c.group - s->rt * kR);
+  s->more = true;
+}
+
+// Keys of tile t that a node's rows see, 128 bits; false for a malformed tree.
+__device__ __forceinline__ bool visible(const Segments& s, const int32_t* all_parents, int node, int t, uint32_t* bits) {
+  const int32_t* parent = all_parents ? all_parents + s.q.first : nullptr;
+  const int64_t j0 = (int64_t)t * kTK - s.q.len;        // node index of the tile's first key
+  // context: keys below -j0; a chain also sees the nodes up to its own
+  const int64_t upto = j0 < 0 ? -j0 : 0;
+  const int64_t lim = parent ? upto : max(upto, (int64_t)node + 1 - j0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t k = lim - 32 * i;
+    bits[i] = k <= 0 ? 0u : (k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u);
+  }
+  if (!parent) return true;
+  for (int x = node; x >= j0;) {
+    const int64_t k = x - j0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k >= 32 * i && k < 32 * i + 32) bits[i] |= 1u << (k & 31);
+    if (x == 0) break;
+    const int up = __ldg(parent + x);
+    if (up < 0 || up >= x) return false;
+    x = up;
+  }
+  return true;
+}
+
+// Column d of what was left out of tiles t0 .. t1 - 1 (clear_nonfinite) for the
+// rows of `node`: the sum of the values that are not finite.
+template <typename T, bool FP8, int D>
+__device__ __noinline__ float left_out(const CacheArgs& c, const Segments& s, int node, int d) {
+  float sum = 0.0f;
+  const Request& q = s.q;
+  for (int t = max(s.t0, q.len / kTK); t < s.t1; ++t) {
+    uint32_t bits[4];
+    visible(s, c.parent, node, t, bits);
+    for (int k = 0; k < kTK; ++k) {
+      const int64_t at = (int64_t)t * kTK + k;
+      if (!((bits[k >> 5] >> (k & 31)) & 1u) || at >= (int64_t)q.len + q.n) continue;
+      const int64_t r0 = cache_row(c.geo, c.table + s.b * c.geo.table_stride, at);
+      if (r0 < 0) continue;
+      const int64_t r = r0 + (int64_t)s.h * c.geo.page_size;
+      float v;
+      if constexpr (FP8) {
+        const __half_raw e = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(c.v)[r * D + d], __NV_E4M3);
+        v = __half2float(*reinterpret_cast<const __half*>(&e)) * c.vs[r];
+      } else {
+        v = to_float(static_cast<const T*>(c.v)[r * D + d]);
+      }
+      if (!isfinite(v)) sum += v;
+    }
+  }
+  return sum;
+}
 
 template <typename T, bool FP8, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     attend_tile_kernel(const AttendArgs a, const int box, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
-  using L = TileLayout<FP8, D>;
+  using L = TileLayout<T, FP8, D>;
   using E = typename std::conditional<FP8, __half, T>::type;
   constexpr int CH = D / 8;                      // 16-byte chunks of an operand row
-  constexpr int KSTEPS = D / 16;
   // the largest weight lies in [2^kHead, 2^(kHead + kLazy)]: f16 weights keep
   // their bits far below the largest, and the maximum may lag by 2^kLazy
   constexpr float kLazy = 8.0f;
@@ -316,14 +431,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   extern __shared__ char smem_raw[];
   __shared__ ScanShared scan;
   __shared__ __align__(8) TileShared sh;
+  // segments of the softmax groups, the products and the loaders
+  __shared__ Segments segs[2 + kLoaders];
   char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t base_s = smem_addr(smem);
   const CacheArgs& c = a.c;
   const int G = gridDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.q_heads / c.geo.kv_heads;
+  const PlanArgs plan(c, group);
   uint32_t why = 0;
   int64_t u0 = 0;
-  find_unit<kTileThreads>(c, group, kR, kTK,
+  find_unit<kTileThreads>(plan, kR, kTK,
                           [&](int64_t units) {
                             const int ranges = (int)min((int64_t)G, units);
                             u0 = (int)blockIdx.x < ranges ? range_begin(units, ranges, blockIdx.x) : units;
@@ -336,13 +454,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int ranges = (int)min((int64_t)G, units);
   if ((int)blockIdx.x >= ranges || scan.b < 0) return;
   if (tid == 0) {
-    for (int i = 0; i < L::SLOTS; ++i) {
-      mbar_init(smem_addr(&sh.full[i]), kProducerWarps * 32);
-      mbar_init(smem_addr(&sh.empty[i]), 1);
+    for (int i = 0; i < L::KS; ++i) {
+      mbar_init(smem_addr(&sh.k_full[i]), 32);
+      mbar_init(smem_addr(&sh.k_empty[i]), 1);
     }
-    for (int i = 0; i < L::RAWS; ++i)
-      for (int w = 0; w < kProducerWarps; ++w) mbar_init(smem_addr(&sh.raw[i][w]), 32);
-    for (int i = 0; i < kFactorSlots; ++i) mbar_init(smem_addr(&sh.fact[i]), kProducerWarps);
+    for (int i = 0; i < L::VS; ++i) {
+      mbar_init(smem_addr(&sh.v_full[i]), FP8 ? kWidenWarps * 32 : 32);
+      mbar_init(smem_addr(&sh.v_empty[i]), 1);
+    }
+    for (int i = 0; i < L::RS; ++i) {
+      mbar_init(smem_addr(&sh.raw_full[i]), 32);
+      mbar_init(smem_addr(&sh.raw_empty[i]), kWidenWarps);
+    }
+    for (int i = 0; i < kFactSlots; ++i) mbar_init(smem_addr(&sh.fact[i]), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_addr(&sh.s_full[w]), 1);
       mbar_init(smem_addr(&sh.p_full[w]), kGroupWarps);
@@ -361,271 +485,291 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = sh.tmem;
-  uint32_t ignored = 0;
-  Segments seg;
-  seg.u = u0;
-  seg.end = range_begin(units, ranges, blockIdx.x + 1);
-  seg.b = scan.b;
-  seg.base = scan.before;
-  seg.q = attend_request(c, group, seg.b, kR, kTK, ignored);
+  const int64_t uend = range_begin(units, ranges, blockIdx.x + 1);
+  if (tid < 2 + kLoaders) {
+    uint32_t ignored = 0;
+    Segments& s = segs[tid];
+    s.end = uend;
+    s.b = scan.b;
+    s.base = scan.before;
+    s.u = (int)(u0 - scan.before);
+    s.q = attend_request(plan, scan.b, kR, kTK, ignored);
+    next_segment(&s, plan);
+  }
+  __syncthreads();
   uint32_t bad = 0;
 
-  // Registers: 4 warpgroups are launched with 128 a thread.  The products' give 72,
-  // the producers' 16; the softmax groups take 40 each (168 + 168 + 112 + 56 <=
-  // 4 * 128).
+  // Registers: 4 warpgroups are launched with 128 a thread.  The softmax groups take
+  // 40 more each from the two others (168 + 168 + 72 + 104 = 4 * 128).
+  auto wait_use = [&](uint64_t* bars, int slots, int n) {       // use n of a ring's slot is complete
+    wait_or_give_up(sh, smem_addr(&bars[n % slots]), (uint32_t)(n / slots) & 1u);
+  };
+  auto wait_free = [&](uint64_t* bars, int slots, int n) {      // the slot's use n - slots is complete
+    wait_or_give_up(sh, smem_addr(&bars[n % slots]), ((uint32_t)(n / slots) & 1u) ^ 1u);
+  };
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kMmaWarp) {
-    // ---- products -------------------------------------------------------------
-    const uint32_t one = lane == 0 ? 1u : 0u;
-    int seq = 0;
-    uint32_t g = 0, tiles_of[2] = {0, 0};
-    const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0), ops = __shfl_sync(0xFFFFFFFFu, base_s, 0);
-    auto slot = [&](int n) { return ops + L::OPS + (n % L::SLOTS) * L::SLOT; };
-    auto phase = [&](int n) { return (uint32_t)(n / L::SLOTS) & 1u; };
-    while (seg.next(c, group)) {
-      const int n = seg.t1 - seg.t0;
-      wait_or_give_up(sh, smem_addr(&sh.q_full), g & 1u);
-      for (int j = 0; j <= n; ++j) {
-        if (j < n) {
-          const int k = seq + 2 * j, w = j & 1;
-          // S_w and P_w are free once the product before last has read P_w
-          if (j >= 2) wait_or_give_up(sh, smem_addr(&sh.empty[(k - 3) % L::SLOTS]), phase(k - 3));
-          wait_or_give_up(sh, smem_addr(&sh.full[k % L::SLOTS]), phase(k));
-          fence_async_proxy();   // rows that came by 16-byte copies
-          tc_fence_after();
-          const uint64_t qd = operand(ops + L::Q, 16), kd = operand(slot(k), 16);
+      // ---- products -----------------------------------------------------------
+      const uint32_t one = lane == 0 ? 1u : 0u;
+      int seq = 0;                                // tiles before the segment
+      uint32_t g = 0, tiles_of[2] = {0, 0};
+      const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0), ops = __shfl_sync(0xFFFFFFFFu, base_s, 0);
+      Segments& seg = segs[1];
+      while (seg.more) {
+        const int n = seg.t1 - seg.t0;
+        wait_or_give_up(sh, smem_addr(&sh.q_full), g & 1u);
+#pragma unroll 1
+        for (int j = 0; j <= n; ++j) {
+          if (j < n) {
+            const int k = seq + j, w = j & 1;
+            // S_w and P_w are free once the product before last has read P_w
+            if (j >= 2) wait_use(sh.v_empty, L::VS, k - 2);
+            wait_use(sh.k_full, L::KS, k);
+            fence_async_proxy();   // rows that came by 16-byte copies
+            tc_fence_after();
+            const uint32_t kt = ops + L::K + (k % L::KS) * L::KB;
+            if constexpr (FP8) {
+              const uint64_t kd = operand<D>(kt, 16);
+#pragma unroll 1
+              for (int part = 0; part < L::PARTS; ++part) {
+                const uint64_t qd = operand<D>(ops + L::Q + part * kR * D, 16);
 #pragma unroll
-          for (int s = 0; s < KSTEPS; ++s) {
-            const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
-            tc_mma_ss(tmu + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0, one);
+                for (int s = 0; s < D / 32; ++s)
+                  tc_mma_e4m3(tmu + w * 128, qd + s * 2, kd + s * 2, product_e4m3(kTK), part + s > 0, one);
+              }
+            } else {
+              const uint64_t qd = operand(ops + L::Q, 16), kd = operand(kt, 16);
+#pragma unroll
+              for (int s = 0; s < D / 16; ++s) {
+                const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
+                tc_mma_ss(tmu + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0, one);
+              }
+            }
+            tc_commit(smem_addr(&sh.s_full[w]), one);
+            tc_commit(smem_addr(&sh.k_empty[k % L::KS]), one);
           }
-          tc_commit(smem_addr(&sh.s_full[w]), one);
-          tc_commit(smem_addr(&sh.empty[k % L::SLOTS]), one);
+          if (j > 0) {
+            const int v = seq + j - 1, w = (j - 1) & 1;
+            wait_use(sh.v_full, L::VS, v);
+            wait_or_give_up(sh, smem_addr(&sh.p_full[w]), (w ? tiles_of[1] : tiles_of[0]) & 1u);
+            if (w) ++tiles_of[1]; else ++tiles_of[0];
+            fence_async_proxy();
+            tc_fence_after();
+            const uint64_t vd = operand(ops + L::V + (v % L::VS) * L::VB, kTK * 128);
+#pragma unroll 2
+            for (int s = 0; s < kTK / 16; ++s)
+              tc_mma_ts(tmu + 256 + w * 128, tmu + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
+                        s > 0 || j > 2, one);
+            tc_commit(smem_addr(&sh.v_empty[v % L::VS]), one);
+          }
         }
-        if (j > 0) {
-          const int v = seq + 2 * (j - 1) + 1, w = (j - 1) & 1;
-          wait_or_give_up(sh, smem_addr(&sh.full[v % L::SLOTS]), phase(v));
-          wait_or_give_up(sh, smem_addr(&sh.p_full[w]), (w ? tiles_of[1] : tiles_of[0]) & 1u);
-          if (w) ++tiles_of[1]; else ++tiles_of[0];
-          fence_async_proxy();
-          tc_fence_after();
-          const uint64_t vd = operand(slot(v), kTK * 128);
-#pragma unroll
-          for (int s = 0; s < kTK / 16; ++s)
-            tc_mma_ts(tmu + 256 + w * 128, tmu + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
-                      s > 0 || j > 2, one);
-          tc_commit(smem_addr(&sh.empty[v % L::SLOTS]), one);
+        tc_commit(smem_addr(&sh.o_full), one);
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&sh.o_full));
+          next_segment(&seg, plan);
         }
+        __syncwarp();
+        seq += n;
+        ++g;
       }
-      tc_commit(smem_addr(&sh.o_full), one);
-      if (lane == 0) mbar_arrive(smem_addr(&sh.o_full));
-      __syncwarp();
-      seq += 2 * n;
-      ++g;
-    }
+    } else {
+      // ---- loaders: a lane looks after keys lane, lane + 32, ... of a tile ------
+      const int loader = warp - kLoadWarp;
+      struct Tile {
+        int row[4];       // cache row of the key, -1: none
+        uint32_t all;     // bit i: 32 keys from 32 i all have one
+        uint32_t clean;   // bit i: and none of them is a node
+        bool tail;        // the tile holds nodes
+      };
+      struct Look {       // page ids on their way
+        int id[4], off[4], h;
+        uint32_t context;
+        bool tail;
+      };
+      Segments& seg = segs[2 + loader];
+      int skip = loader, t = seg.t0;            // tiles of others before this loader's next
+      const uint32_t page_size = (uint32_t)c.geo.page_size;
+      auto look = [&](Look& x) -> bool {        // this loader's next tile
+        t += skip;
+        while (seg.more && t >= seg.t1) {
+          const int over = t - seg.t1;
+          __syncwarp();
+          if (lane == 0) next_segment(&seg, plan);
+          __syncwarp();
+          t = seg.t0 + over;
+        }
+        if (!seg.more) return false;
+        skip = kLoaders;
+        const int32_t* pages = c.table + seg.b * c.geo.table_stride;
+        const uint32_t len = (uint32_t)seg.q.len, end = len + (uint32_t)seg.q.n, first = (uint32_t)t * kTK;
+        x.tail = first + kTK > len;
+        x.h = seg.h;
+        x.context = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = first + i * 32 + lane, page = at / page_size;
+          x.off[i] = (int)(at - page * page_size);
+          x.id[i] = at < end ? __ldg(pages + page) : -2;    // end is within the table
+          if (first + i * 32 + 32 <= len) x.context |= 1u << i;
+        }
+        return true;
+      };
+      auto found = [&](const Look& l, Tile& x) {
+        x.tail = l.tail;
+        x.all = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = l.id[i] >= 0 && l.id[i] < c.geo.num_pages;
+          if (!in && l.id[i] != -2) bad |= SPECDEC_DEVERR_BAD_CACHE;
+          // fewer than 2^31 rows in all
+          x.row[i] = in ? (l.id[i] * c.geo.kv_heads + l.h) * (int)page_size + l.off[i] : -1;
+          if (__all_sync(0xFFFFFFFFu, in)) x.all |= 1u << i;
+        }
+        x.clean = x.all & l.context;
+      };
+      // The rows of a tile of the array `src` (16-bit, or 8-bit as it is) to `dst`:
+      // boxes for the groups of 32 keys in `boxes`, 16-byte copies for the others.
+      // Every lane arrives on `bar` when its copies have landed, unless `arrive`
+      // is false (then the copies have been waited for).
+      auto fetch = [&](uint32_t dst, const void* src, const CUtensorMap* map, const Tile& x, uint32_t boxes, uint32_t bar,
+                       bool arrive) {
+        constexpr int LINE = FP8 ? D : 128, HALVES = FP8 ? 1 : D / 64, RC = FP8 ? D / 16 : D / 8;
+        if (box == 0) boxes = 0;
+        if (boxes && lane == 0) mbar_expect_tx(bar, __popc(boxes) * 32 * HALVES * LINE);
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int mine = i == 0 ? x.row[0] : i == 1 ? x.row[1] : i == 2 ? x.row[2] : x.row[3];
+          if ((boxes >> i) & 1u) {
+            const int r0 = (lane / HALVES) * box, half = lane % HALVES;
+            const int row = __shfl_sync(0xFFFFFFFFu, mine, r0 & 31);
+            if (r0 < 32) box_load(dst + half * (kTK * 128) + (i * 32 + r0) * LINE, map, half * 64, row, bar);
+          } else {
+#pragma unroll 4
+            for (int z = 0; z < RC; ++z) {
+              const int y = z * 32 + lane, key = y / RC, ch = y % RC;
+              const int r = __shfl_sync(0xFFFFFFFFu, mine, key);
+              copy16(dst + (FP8 ? byte_chunk<D>(i * 32 + key, ch) : op_chunk(i * 32 + key, ch)),
+                     static_cast<const char*>(src) + (int64_t)max(r, 0) * (FP8 ? D : 2 * D) + ch * 16, r >= 0);
+            }
+          }
+        }
+        if (arrive) {
+          copy_arrive(bar);
+        } else {
+          copy_commit();
+          copy_wait<0>();
+        }
+      };
+      Look ahead;
+      bool have = look(ahead);
+      for (int n = loader; have; n += kLoaders) {
+        Tile now;
+        found(ahead, now);
+        have = look(ahead);
+        float ks[4], vs[4];
+        if constexpr (FP8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ks[i] = now.row[i] >= 0 ? __ldg(c.ks + now.row[i]) : 0.0f;
+            vs[i] = now.row[i] >= 0 ? __ldg(c.vs + now.row[i]) : 0.0f;
+          }
+        }
+        wait_free(sh.k_empty, L::KS, n);
+        fetch(base_s + L::K + (n % L::KS) * L::KB, c.k, &kmap, now, now.all, smem_addr(&sh.k_full[n % L::KS]), true);
+        if constexpr (FP8) {
+          wait_free(sh.raw_empty, L::RS, n);
+          fetch(base_s + L::RAW + (n % L::RS) * L::RB, c.v, &vmap, now, now.clean, smem_addr(&sh.raw_full[n % L::RS]), true);
+        } else {
+          const uint32_t bar = smem_addr(&sh.v_full[n % L::VS]), dst = base_s + L::V + (n % L::VS) * L::VB;
+          wait_free(sh.v_empty, L::VS, n);
+          fetch(dst, c.v, &vmap, now, now.clean, bar, !now.tail);
+          if (now.tail) {
+            // values of nodes: see clear_nonfinite
+            bool hit = false;
+            for (int i = 0; i < 4; ++i) {
+              if (box > 0 && ((now.clean >> i) & 1u)) continue;
+              for (int z = 0; z < CH; ++z) {
+                const int y = z * 32 + lane, key = y / CH, ch = y % CH;
+                const uint32_t at = dst + op_chunk(i * 32 + key, ch);
+                uint4 w = lds128(at);
+                if (clear_nonfinite<E>(w)) {
+                  sts128(at, w);
+                  hit = true;
+                }
+              }
+            }
+            if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
+            fence_async_proxy();
+            mbar_arrive(bar);
+          }
+        }
+        // What the other roles need to know of the tile's keys.  8-bit caches: the
+        // scale of K (applied to the scores, in 32 bits); the scale of V goes into
+        // the widened values, as a factor v 2^-vexp that f16 holds: the largest of
+        // 32 keys lies in [2^5, 2^6), so products stay below 2^15 and keys down to
+        // 2^-20 of the largest keep f16's full precision.
+        // (Slot n % 8 is free: the slot waits above imply that the products of tile
+        // n - 5 are done.)
+        const int f = n % kFactSlots;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t live = __ballot_sync(0xFFFFFFFFu, now.row[i] >= 0);
+          if (lane == 0) sh.live[f][i] = live;
+          if constexpr (FP8) {
+            const bool real = vs[i] > 0.0f && isfinite(vs[i]);
+            const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, real ? __float_as_uint(vs[i]) : 0u);
+            const int b = most ? min(max((int)(most >> 23) - 127 - 5, -80), 80) : 0;
+            if (lane == 0) sh.vexp[f][i] = (float)b;
+            const float factor = vs[i] * __uint_as_float((uint32_t)(127 - b) << 23);
+            reinterpret_cast<float*>(smem + L::KF)[f * kTK + i * 32 + lane] = ks[i];
+            reinterpret_cast<uint32_t*>(smem + L::VF)[f * kTK + i * 32 + lane] = pack2(factor, factor, __half());
+          }
+        }
+        if (lane == 0) sh.tail[f] = now.tail;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
+      }
+      copy_commit();
+      copy_wait<0>();
     }
   } else if (warp >= 2 * kGroupWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-    // ---- producers: each warp owns 32 keys of every tile -----------------------
-    const int pw = warp - 2 * kGroupWarps;
-    struct Tile {
-      int row;          // cache row of this lane's key, -1: none
-      bool tail;        // the tile holds nodes
-      bool boxes;       // this warp's 32 keys come by TMA
-    };
-    auto key_row = [&](const Segments& s, int t) -> Tile {
-      const int64_t at = (int64_t)t * kTK + pw * 32 + lane;
-      Tile x;
-      x.row = -1;
-      x.tail = (int64_t)t * kTK + kTK > s.q.len;
-      if (at < (int64_t)s.q.len + s.q.n) {
-        const int64_t r = cache_row(c.geo, c.table + s.b * c.geo.table_stride, at);
-        if (r < 0) bad |= SPECDEC_DEVERR_BAD_CACHE;
-        else x.row = (int)(r + (int64_t)s.h * c.geo.page_size);
-      }
-      // (keys behind the last slot have to read as zeros: no boxes over them)
-      x.boxes = __all_sync(0xFFFFFFFFu, x.row >= 0) && box > 0 && !x.tail;
-      return x;
-    };
-    bool more = seg.next(c, group);
-    int t = more ? seg.t0 : 0;
-    auto advance = [&](Tile& x) -> bool {     // the next tile of the range, in order
-      if (!more) return false;
-      x = key_row(seg, t);
-      if (++t == seg.t1) {
-        more = seg.next(c, group);
-        t = more ? seg.t0 : 0;
-      }
-      return true;
-    };
-    auto wait_slot = [&](int n) {
-      wait_or_give_up(sh, smem_addr(&sh.empty[n % L::SLOTS]), ((uint32_t)(n / L::SLOTS) & 1u) ^ 1u);
-    };
-    // What softmax needs to know of the tile's keys.  8-bit caches: the scale of
-    // K (applied to the scores, in 32 bits); the scale of V goes into the widened
-    // values, as a factor v 2^-vexp that f16 holds: the largest of the warp's 32
-    // keys lies in [2^5, 2^6), so products stay below 2^15 and keys down to 2^-20
-    // of the largest keep f16's full precision.  Returns that factor.
-    auto facts = [&](int tile_no, const Tile& x, float ks, float vs) -> float {
-      const int f = tile_no % kFactorSlots;
-      const uint32_t live = __ballot_sync(0xFFFFFFFFu, x.row >= 0);
-      if (lane == 0) sh.live[f][pw] = live;
-      float factor = 0.0f;
-      if constexpr (FP8) {
-        reinterpret_cast<float*>(smem + L::FACT)[f * kTK + pw * 32 + lane] = x.row >= 0 ? ks : 0.0f;
-        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, x.row >= 0 && vs > 0.0f && isfinite(vs) ? __float_as_uint(vs) : 0u);
-        const int b = most ? min(max((int)(most >> 23) - 127 - 5, -80), 80) : 0;
-        if (lane == 0) sh.vexp[f][pw] = (float)b;
-        if (x.row >= 0) factor = vs * __uint_as_float((uint32_t)(127 - b) << 23);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
-      return factor;
-    };
-    // This warp's 32 rows of the array that `map` describes by boxes of `box`
-    // rows and 128 (or D) bytes; every lane arrives on `bar`.
-    auto by_boxes = [&](uint32_t dst, int half_step, const CUtensorMap* map, const Tile& x, uint32_t bar) {
-      constexpr int HALVES = FP8 ? 1 : D / 64;
-      constexpr int LINE = FP8 ? D : 128;
-      if (lane == 0) mbar_arrive_expect_tx(bar, 32 * HALVES * LINE);
-      else mbar_arrive(bar);
-      __syncwarp();
-      const int r0 = (lane / HALVES) * box, half = lane % HALVES;
-      const int row = __shfl_sync(0xFFFFFFFFu, x.row, r0 & 31);
-      if (r0 < 32) box_load(dst + half * half_step + (pw * 32 + r0) * LINE, map, half * 64, row, bar);
-    };
-    bool more_tiles;
-    Tile cur = {-1, false, false}, nxt = {-1, false, false};
-    more_tiles = advance(cur);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if constexpr (FP8) {
-      // Raw tiles are staged RAWS - 1 ahead of the one that is widened; a lane
-      // widens 16 bytes of 8 neighbouring rows' one chunk, which 8 lanes read and
-      // write without bank conflicts in both swizzles.
-      constexpr int RC = D / 16;             // 16-byte chunks of a raw row
-      auto raw_chunk = [&](int key, int ch) {
-        return D == 128 ? (uint32_t)(key * D + ((ch ^ (key & 7)) << 4)) : (uint32_t)(key * D + ((ch ^ ((key >> 1) & 3)) << 4));
-      };
-      auto stage = [&](int n, const Tile& x, bool is_v) {
-        const uint32_t dst = base_s + L::RAW0 + (n % L::RAWS) * L::RAW;
-        const uint32_t bar = smem_addr(&sh.raw[n % L::RAWS][pw]);
-        if (x.boxes) {
-          by_boxes(dst, 0, is_v ? &vmap : &kmap, x, bar);
-        } else {
-          const char* src = static_cast<const char*>(is_v ? c.v : c.k);
-#pragma unroll
-          for (int i = 0; i < RC; ++i) {
-            const int y = i * 32 + lane, key = y / RC, ch = y % RC;
-            const int r = __shfl_sync(0xFFFFFFFFu, x.row, key);
-            copy16(dst + raw_chunk(pw * 32 + key, ch), src + (int64_t)max(r, 0) * D + ch * 16, r >= 0);
-          }
-          copy_arrive(bar);
-        }
-      };
-      auto widen = [&](int n, bool is_v, bool tail, float factor) {
-        const uint32_t own = pack2(factor, factor, __half());
-        wait_or_give_up(sh, smem_addr(&sh.raw[n % L::RAWS][pw]), (uint32_t)(n / L::RAWS) & 1u);
-        wait_slot(n);
-        const uint32_t raw = base_s + L::RAW0 + (n % L::RAWS) * L::RAW;
-        const uint32_t dst = base_s + L::OPS + (n % L::SLOTS) * L::SLOT;
+      // ---- wideners: 32 keys each; 8 lanes read and write one chunk of 8
+      // neighbouring rows, without bank conflicts in either swizzle -------------
+      const int pw = warp - 2 * kGroupWarps;
+      constexpr int RC = D / 16;             // 16-byte chunks of an 8-bit row
+      const int tiles = (int)(uend - u0);
+      for (int n = 0; n < tiles; ++n) {
+        const int f = n % kFactSlots;
+        wait_use(sh.fact, kFactSlots, n);
+        const bool tail = sh.tail[f] != 0;
+        const uint32_t own = reinterpret_cast<const uint32_t*>(smem + L::VF)[f * kTK + pw * 32 + lane];
+        wait_use(sh.raw_full, L::RS, n);
+        wait_free(sh.v_empty, L::VS, n);
+        const uint32_t raw = base_s + L::RAW + (n % L::RS) * L::RB, dst = base_s + L::V + (n % L::VS) * L::VB;
         bool hit = false;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < RC; ++i) {
-          const int key = pw * 32 + (lane & 7) + 8 * (RC == 8 ? i >> 1 : i);
+          const int in = (lane & 7) + 8 * (RC == 8 ? i >> 1 : i), key = pw * 32 + in;
           const int ch = (lane >> 3) + (RC == 8 ? 4 * (i & 1) : 0);
-          const uint4 w = lds128(raw + raw_chunk(key, ch));
-          uint4 lo = make_uint4(e4m3x2_f16x2(w.x), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y), e4m3x2_f16x2(w.y >> 16));
-          uint4 hi = make_uint4(e4m3x2_f16x2(w.z), e4m3x2_f16x2(w.z >> 16), e4m3x2_f16x2(w.w), e4m3x2_f16x2(w.w >> 16));
-          if (is_v) {
-            const uint32_t by = __shfl_sync(0xFFFFFFFFu, own, key & 31);
-            lo = times(lo, by);
-            hi = times(hi, by);
-            if (tail) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
-          }
+          const uint4 w = lds128(raw + byte_chunk<D>(key, ch));
+          const uint32_t by = __shfl_sync(0xFFFFFFFFu, own, in);
+          uint4 lo = times(make_uint4(e4m3x2_f16x2(w.x), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y), e4m3x2_f16x2(w.y >> 16)), by);
+          uint4 hi = times(make_uint4(e4m3x2_f16x2(w.z), e4m3x2_f16x2(w.z >> 16), e4m3x2_f16x2(w.w), e4m3x2_f16x2(w.w >> 16)), by);
+          if (tail) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
           sts128(dst + op_chunk(key, 2 * ch), lo);
           sts128(dst + op_chunk(key, 2 * ch + 1), hi);
         }
         if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
         fence_async_proxy();
-        mbar_arrive(smem_addr(&sh.full[n % L::SLOTS]));
-        __syncwarp();   // the raw tile is read before it is filled again
-      };
-      auto scales = [&](const Tile& x, float& ks, float& vs) {
-        ks = x.row >= 0 ? __ldg(c.ks + x.row) : 0.0f;
-        vs = x.row >= 0 ? __ldg(c.vs + x.row) : 1.0f;
-      };
-      float k0 = 0.0f, v0 = 1.0f, k1 = 0.0f, v1 = 1.0f;
-      bool more_next = false;
-      if (more_tiles) {
-        scales(cur, k0, v0);
-        stage(0, cur, false);
-        stage(1, cur, true);
-        more_next = advance(nxt);
-      }
-      for (int n = 0, tile = 0; more_tiles; n += 2, ++tile) {
-        if (more_next) {
-          stage(n + 2, nxt, false);
-          scales(nxt, k1, v1);
-        }
-        const float factor = facts(tile, cur, k0, v0);
-        widen(n, false, false, 0.0f);
-        if (more_next) stage(n + 3, nxt, true);
-        widen(n + 1, true, cur.tail, factor);
-        cur = nxt;
-        more_tiles = more_next;
-        k0 = k1;
-        v0 = v1;
-        more_next = more_tiles && advance(nxt);
-      }
-    } else {
-      auto stage = [&](int n, const Tile& x, bool is_v) {
-        const uint32_t dst = base_s + L::OPS + (n % L::SLOTS) * L::SLOT;
-        const uint32_t bar = smem_addr(&sh.full[n % L::SLOTS]);
-        if (x.boxes) {
-          by_boxes(dst, kTK * 128, is_v ? &vmap : &kmap, x, bar);
-          return;
-        }
-        const char* src = static_cast<const char*>(is_v ? c.v : c.k);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int y = i * 32 + lane, key = y / CH, ch = y % CH;
-          const int r = __shfl_sync(0xFFFFFFFFu, x.row, key);
-          copy16(dst + op_chunk(pw * 32 + key, ch), src + (int64_t)max(r, 0) * (2 * D) + ch * 16, r >= 0);
-        }
-        if (!(is_v && x.tail)) {
-          copy_arrive(bar);
-          return;
-        }
-        // values of a tile that holds nodes: see clear_nonfinite
-        copy_commit();
-        copy_wait<0>();
-        bool hit = false;
-        for (int i = 0; i < CH; ++i) {
-          const int y = i * 32 + lane, key = y / CH, ch = y % CH;
-          const uint32_t at = dst + op_chunk(pw * 32 + key, ch);
-          uint4 w = lds128(at);
-          if (clear_nonfinite<E>(w)) {
-            sts128(at, w);
-            hit = true;
-          }
-        }
-        if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
-        fence_async_proxy();
-        mbar_arrive(bar);
-      };
-      for (int n = 0, tile = 0; more_tiles; n += 2, ++tile) {
-        const bool more_next = advance(nxt);
-        wait_slot(n);
-        facts(tile, cur, 0.0f, 0.0f);
-        stage(n, cur, false);
-        wait_slot(n + 1);
-        stage(n + 1, cur, true);
-        cur = nxt;
-        more_tiles = more_next;
+        mbar_arrive(smem_addr(&sh.v_full[n % L::VS]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.raw_empty[n % L::RS]));
       }
     }
-    copy_commit();
-    copy_wait<0>();
   } else {
     // ---- softmax ----------------------------------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
@@ -639,7 +783,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int done = 0, tile0 = 0;                     // this group's tiles, all tiles before the segment
     uint32_t g = 0;
     bool first = true;
-    while (seg.next(c, group)) {
+    // The segment stands in shared memory: its fields would otherwise take the
+    // registers of the scores.
+    Segments& seg = segs[0];
+    while (seg.more) {
       // queries
       const float sgn = a.scale_log2 < 0.0f ? -1.0f : 1.0f;   // factors are positive: the sign goes to q
       for (int x = sid; x < kR * CH; x += kSoftmaxThreads) {
@@ -652,8 +799,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (live) v = __ldg(reinterpret_cast<const uint4*>(src));
         float f = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);   // above 0: hidden keys are -inf times this
         if constexpr (FP8) {
-          // f16 factors: the row is scaled by a power of two so that its largest
-          // value lies in [1, 2); the scores take the factor back
+          // the row is scaled by a power of two so that its largest value lies in
+          // [2^7, 2^8), below e4m3's 448; the scores take the factor back
           const T* e = reinterpret_cast<const T*>(&v);
           float y[8], m = 0.0f;
 #pragma unroll
@@ -663,18 +810,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
 #pragma unroll
           for (int o = CH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-          const int ex = min(max((int)(__float_as_uint(m) >> 23), 1), 253);
-          const float mul = __uint_as_float((uint32_t)(254 - ex) << 23);
-          f *= __uint_as_float((uint32_t)ex << 23);
-          v = make_uint4(pack2(y[0] * mul, y[1] * mul, E()), pack2(y[2] * mul, y[3] * mul, E()),
-                         pack2(y[4] * mul, y[5] * mul, E()), pack2(y[6] * mul, y[7] * mul, E()));
+          const int ex = min(max((int)(__float_as_uint(m) >> 23), 8), 253);
+          const float mul = __uint_as_float((uint32_t)(254 - ex + 7) << 23);
+          f *= __uint_as_float((uint32_t)(ex - 7) << 23);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = isfinite(y[i]) ? y[i] * mul : __uint_as_float(0x7FC00000u);
+#pragma unroll
+          for (int part = 0; part < L::PARTS; ++part) {
+            uint32_t w8[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(y[i], y[i + 1]), __NV_SATFINITE, __NV_E4M3);
+              w8[i >> 2] |= two << ((i & 2) * 8);
+              const uint32_t back = e4m3x2_f16x2(two);
+              const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&back));
+              y[i] -= got.x;
+              y[i + 1] -= got.y;
+            }
+            sts64(base_s + L::Q + part * kR * D + byte_chunk<D>(r, ch >> 1) + (ch & 1) * 8, w8[0], w8[1]);
+          }
         } else if (sgn < 0.0f) {
           v.x ^= 0x80008000u;
           v.y ^= 0x80008000u;
           v.z ^= 0x80008000u;
           v.w ^= 0x80008000u;
         }
-        sts128(base_s + L::Q + op_chunk(r, ch), v);
+        if constexpr (!FP8) sts128(base_s + L::Q + op_chunk(r, ch), v);
         if (ch == 0) sh.rowf[r] = f;
       }
       fence_async_proxy();
@@ -682,51 +843,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) mbar_arrive(smem_addr(&sh.q_full));
       named_bar_sync(1, kSoftmaxThreads);
       const float rowf = sh.rowf[row];
-      const int n = seg.t1 - seg.t0;
+      const int t0 = seg.t0, n = seg.t1 - t0, len = seg.q.len;
       const bool busy = (row & ~31) < seg.rows;    // the warp has rows of the tile
       const int node = (seg.rt * kR + min(row, seg.rows - 1)) / group;
-      const int32_t* parent = c.parent ? c.parent + seg.q.first : nullptr;
       float m = -INFINITY, l = 0.0f;               // reference maximum and sum of this group's tiles
-      // keys of tile t that the row sees, 128 bits
-      auto visible = [&](int t, uint32_t* bits) {
-        const int64_t j0 = (int64_t)t * kTK - seg.q.len;   // node index of the tile's first key
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // context: keys below -j0; a chain also sees nodes up to its own
-          const int64_t upto = (j0 < 0 ? -j0 : 0);
-          const int64_t lim = parent ? upto : max(upto, (int64_t)node + 1 - j0);
-          const int64_t k = lim - 32 * i;
-          bits[i] = k <= 0 ? 0u : (k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u);
-        }
-        if (parent) {
-          int x = node;
-          while (x >= j0) {
-            const int64_t k = x - j0;
-            if (k < kTK) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if ((int)(k >> 5) == i) bits[i] |= 1u << (k & 31);
-            }
-            if (x == 0) break;
-            const int up = __ldg(parent + x);
-            if (up < 0 || up >= x) {
-              bad |= SPECDEC_DEVERR_BAD_TREE;
-              break;
-            }
-            x = up;
-          }
-        }
-      };
       for (int j = w; j < n; j += 2) {
-        const int t = seg.t0 + j, f = (tile0 + j) % kFactorSlots;
-        wait_or_give_up(sh, smem_addr(&sh.fact[f]), (uint32_t)((tile0 + j) / kFactorSlots) & 1u);
+        const int t = t0 + j, f = (tile0 + j) % kFactSlots;
+        wait_use(sh.fact, kFactSlots, tile0 + j);
         wait_or_give_up(sh, smem_addr(&sh.s_full[w]), (uint32_t)done & 1u);
         ++done;
         tc_fence_after();
         if (busy) {
           uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-          const bool tail = (int64_t)t * kTK + kTK > seg.q.len;
-          if (tail) visible(t, bits);
+          const bool tail = (int64_t)t * kTK + kTK > len;
+          if (tail && !visible(seg, c.parent, node, t, bits)) bad |= SPECDEC_DEVERR_BAD_TREE;
           __syncwarp();
           bool masked = tail;
 #pragma unroll
@@ -739,7 +869,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           // m a whole number that follows the running maximum only when that is
           // kLazy above it: what has been summed, the row's O_w and the tile's
           // weights so far are then multiplied by a power of two, which is exact.
-          const float* fk = reinterpret_cast<const float*>(smem + L::FACT) + f * kTK;
+          const uint32_t fk_s = base_s + L::KF + f * kTK * 4;
           const uint64_t rowf2 = pair(rowf, rowf);
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
@@ -751,10 +881,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               shift[1] = sh.vexp[f][2 * i + 1];
 #pragma unroll
               for (int k = 0; k < 64; k += 4) {
-                const ulonglong2 kf = *reinterpret_cast<const ulonglong2*>(fk + i * 64 + k);
-                unpair(mul2(pair(s[k], s[k + 1]), kf.x), s[k], s[k + 1]);
-                unpair(mul2(pair(s[k + 2], s[k + 3]), kf.y), s[k + 2], s[k + 3]);
-                if (k % 16 == 12) asm volatile("" ::: "memory");   // not all factors at once in registers
+                uint64_t f0, f1;
+                lds_pairs(fk_s + (i * 64 + k) * 4, f0, f1);
+                unpair(mul2(pair(s[k], s[k + 1]), f0), s[k], s[k + 1]);
+                unpair(mul2(pair(s[k + 2], s[k + 3]), f1), s[k + 2], s[k + 3]);
               }
             }
             const uint32_t see[2] = {i ? bits[2] : bits[0], i ? bits[3] : bits[1]};
@@ -871,36 +1001,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int k = 0; k < 32; ++k) x[k] += s1.x == -INFINITY ? 0.0f : y[k] * f1;
           }
           const int d0 = w * (D / 2) + i * 32;
-          if (poison && live) {
-            // values that are not finite were taken out of the tiles that hold
-            // nodes: they belong to the rows that see their keys
-            for (int t = max(seg.t0, seg.q.len / kTK); t < seg.t1; ++t) {
-              uint32_t bits[4];
-              visible(t, bits);
-              for (int k = 0; k < kTK; ++k) {
-                const int64_t at = (int64_t)t * kTK + k;
-                if (!((bits[k >> 5] >> (k & 31)) & 1u) || at >= (int64_t)seg.q.len + seg.q.n) continue;
-                const int64_t r = cache_row(c.geo, c.table + seg.b * c.geo.table_stride, at);
-                if (r < 0) continue;
-                const int64_t e = (r + (int64_t)seg.h * c.geo.page_size) * D + d0;
-                for (int d = 0; d < 32; ++d) {
-                  float v;
-                  if constexpr (FP8) {
-                    const __half_raw hr =
-                        __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(c.v)[e + d], __NV_E4M3);
-                    v = __half2float(*reinterpret_cast<const __half*>(&hr)) * c.vs[r + (int64_t)seg.h * c.geo.page_size];
-                  } else {
-                    v = to_float(static_cast<const T*>(c.v)[e + d]);
-                  }
-                  if (!isfinite(v)) {
-#pragma unroll
-                    for (int z = 0; z < 32; ++z)
-                      if (z == d) x[z] += v;
-                  }
-                }
-              }
-            }
-          }
           if (live) {
             if (seg.whole) {
               T* out = static_cast<T*>(a.out) +
@@ -918,10 +1018,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
         }
+        // values that are not finite were left out of the tiles that hold nodes:
+        // the rows that see their keys get them now
+        if (poison && live) {
+#pragma unroll 1
+          for (int d = w * (D / 2); d < (w + 1) * (D / 2); ++d) {
+            const float v = left_out<T, FP8, D>(a.c, seg, (seg.rt * kR + row) / group, d);
+            if (v == 0.0f) continue;
+            if (seg.whole) {
+              T* out = static_cast<T*>(a.out) +
+                       ((seg.q.first + gr / group) * a.q_heads + seg.h * group + gr % group) * (int64_t)D + d;
+              from_float(to_float(*out) + v, *out);
+            } else {
+              part.sums[(slot * kR + row) * D + d] += v;
+            }
+          }
+        }
         if (live && !seg.whole && w == 0) part.stats[slot * kR + row] = make_float2(mm, lsum);
       }
       tc_fence_before();
       named_bar_sync(1, kSoftmaxThreads);   // the sums are read before queries lie over them
+      if (sid == 0) next_segment(&seg, plan);
+      named_bar_sync(1, kSoftmaxThreads);
       tile0 += n;
       ++g;
       first = false;
@@ -965,7 +1083,7 @@ bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int D, int bo
 template <typename T, bool FP8, int D>
 int launch_tile(const AttendArgs& a, int num_sms, cudaStream_t st) {
   auto kern = attend_tile_kernel<T, FP8, D>;
-  constexpr int bytes = TileLayout<FP8, D>::BYTES;
+  constexpr int bytes = TileLayout<T, FP8, D>::BYTES;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return SPECDEC_ERR_CUDA;
   // rows of a box: within one page, whole groups of 8 rows of the swizzle
