@@ -162,7 +162,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
   uint32_t* anc = reinterpret_cast<uint32_t*>(smem + L::ANC);
   const int quad = lane & 3, qrow = lane >> 2;
   uint32_t bad = 0;
-  bool first_segment = true;
 
   uint32_t ignored = 0;
   Request q = attend_request(plan, b, R, TK, ignored);
@@ -172,11 +171,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
       if (++b >= c.B) return;   // lengths that changed under the call
       q = attend_request(plan, b, R, TK, ignored);
     }
-    const int64_t item = (u - base) / q.tiles;
-    const int t0 = (int)((u - base) % q.tiles);
-    const int t1 = (int)min((int64_t)q.tiles, t0 + (uend - u));
+    const int64_t item = (u - base) / (q.tiles + kItemCost);
+    const int at = (int)((u - base) % (q.tiles + kItemCost));
+    const int t0 = max(at - kItemCost, 0);
+    const int t1 = (int)min((int64_t)q.tiles, at - kItemCost + (uend - u));
     const int h = (int)(item / q.rts), rt = (int)(item % q.rts);
-    u += t1 - t0;
+    u += q.tiles + kItemCost - at;
+    if (t1 <= t0) continue;
     const bool whole = t0 == 0 && t1 == q.tiles;
     const int rows = min(R, q.n * group - rt * R);            // rows of this tile
     const int node0 = rt * R / group;                          // its first node
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
           }
       }
     __syncthreads();
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 > 0 ? 0 : 1);
     for (int x = tid; x < R * D; x += kThreads) {
       const int r = x / D, d = x % D;
       float mm = -INFINITY;
@@ -546,7 +547,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
         if (d == 0) part.stats[slot * R + r] = make_float2(mm, sum);
       }
     }
-    first_segment = false;
   }
   if (bad) atomicOr(c.err, bad);
 }

@@ -6,6 +6,10 @@
 // idle; an item that crosses a range leaves partial results (row maximum, sum
 // and weighted sum of values) that a second, dependent kernel joins.
 //
+// An item also counts kItemCost units of its own: starting and ending it (queries,
+// an empty pipeline, results) takes about as long as that many tiles, and without
+// them the ranges that hold many short requests finished late.
+//
 // Rows of an item: r = node * group + head within the group, so one read of a
 // key serves every node and every query head that shares it.
 #pragma once
@@ -20,6 +24,8 @@
 #include "device_common.cuh"
 
 namespace specdec {
+
+constexpr int kItemCost = 2;
 
 struct Request {
   int64_t first;   // first node row
@@ -64,7 +70,7 @@ __host__ __device__ __forceinline__ Request attend_request(const PlanArgs& c, in
   }
   q.rts = (int32_t)(((int64_t)q.n * c.group + R - 1) / R);
   q.tiles = (int32_t)(((int64_t)q.len + q.n + TK - 1) / TK);
-  q.units = (int64_t)c.kv_heads * q.rts * q.tiles;
+  q.units = (int64_t)c.kv_heads * q.rts * (q.tiles + kItemCost);
   if (q.units >= ((int64_t)1 << 31)) {   // units of a request are counted in 32 bits
     q.units = 0;
     why |= SPECDEC_DEVERR_BAD_CACHE;
@@ -160,6 +166,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
 }
 
 // Workspace: two partial slots per range, each R rows of D sums, then (max, sum).
+// A range may go on with an item that began earlier (slot 0) and leave another to
+// the next range (slot 1).
 template <int R, int D>
 struct Partials {
   float* sums;
@@ -170,7 +178,7 @@ struct Partials {
 };
 
 // Joins the partial results of the items that several ranges share.  An item
-// that starts in range i - 1 and goes on into range i belongs to blocks (i, *);
+// whose first tile is in range i - 1 and that goes on into range i belongs to blocks (i, *);
 // block (i, y) takes 8 of its rows, a warp two of them.
 template <typename T, int R, int TK, int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, const int G) {
@@ -192,10 +200,10 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, co
   const int g0 = blockIdx.x;                     // the range before the boundary
   const Request q = attend_request(plan, sh.b, R, TK, why);
   if (q.units == 0) return;
-  const int64_t item = (u - sh.before) / q.tiles;
-  const int64_t u0 = sh.before + item * q.tiles, u1 = u0 + q.tiles;
+  const int64_t item = (u - sh.before) / (q.tiles + kItemCost);
+  const int64_t u0 = sh.before + item * (q.tiles + kItemCost) + kItemCost, u1 = u0 + q.tiles;   // its tiles
   // not an item that begins at the boundary, nor one that range g0 also went on with
-  if (u0 == u || range_begin(sh.total, ranges, g0) > u0) return;
+  if (u0 >= u || range_begin(sh.total, ranges, g0) > u0) return;
   const int h = (int)(item / q.rts), rt = (int)(item % q.rts);
   const int g1 = range_of(sh.total, ranges, u1 - 1);
   const Partials<R, D> part(a.workspace, G);
@@ -205,8 +213,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, co
   for (int r = blockIdx.y * 8 + warp; r < (int)blockIdx.y * 8 + 8; r += 4) {
     const int row = rt * R + r;
     if (row >= rows) break;
-    // a range holds the item in its first slot if it begins inside the item
-    auto slot_of = [&](int g) { return 2 * (int64_t)g + (range_begin(sh.total, ranges, g) >= u0 ? 0 : 1); };
+    auto slot_of = [&](int g) { return 2 * (int64_t)g + (range_begin(sh.total, ranges, g) > u0 ? 0 : 1); };
     float m = -INFINITY;
     for (int g = g0 + lane; g <= g1; g += 32) m = fmaxf(m, part.stats[slot_of(g) * R + r].x);
     m = warp_max(m);

@@ -6,11 +6,12 @@
 //   loaders (3 warps)    look up the pages and bring the rows of keys and values, every
 //                        third tile each, so that one's look-ups hide behind the others',
 //                        into the operand layout (swizzled rows of 128 bytes): by
-//                        TMA boxes of up to 32 rows of a page, or by 16-byte copies
-//                        where 32 keys hold nodes, end, miss a page or lie in pages
-//                        of odd sizes;
-//   wideners (4 warps)   8-bit caches: turn the values of a landed tile into f16
-//                        (the keys are multiplied as they are, see below);
+//                        TMA boxes of 8 to 128 rows of a page, or by 16-byte copies
+//                        where pages have odd sizes;
+//   finishers (4 warps)  take a tile of values when it has landed: 8-bit ones are
+//                        widened to f16 (the keys are multiplied as they are, see
+//                        below); in tiles that hold nodes or miss keys, what no row
+//                        may see is taken out;
 //   products (1 thread)  S_w = Q K^T (both operands in shared memory) and
 //                        O_w += P_w V (P in tensor memory);
 //   softmax (2 groups    group w takes every second tile of a segment with a
@@ -43,8 +44,8 @@ namespace {
 constexpr int kR = 128, kTK = 128;
 constexpr int kGroupWarps = 4;                       // softmax warps of a group
 constexpr int kSoftmaxThreads = 2 * kGroupWarps * 32;
-constexpr int kWidenWarps = 4;
-constexpr int kMmaWarp = 2 * kGroupWarps + kWidenWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kFinishWarps = 4;
+constexpr int kMmaWarp = 2 * kGroupWarps + kFinishWarps, kLoadWarp = kMmaWarp + 1;
 constexpr int kLoaders = 3;                          // loader l takes tiles l, l + 3, ... of the range
 constexpr int kTileThreads = (kMmaWarp + 4) * 32;    // a whole warpgroup: registers move between those
 constexpr int kFactSlots = 8;                        // tiles whose key facts are held (5 are needed)
@@ -58,12 +59,12 @@ struct TileLayout {
   static constexpr int RB = FP8 ? kTK * D : 0;         // a tile of 8-bit values
   static constexpr int KS = FP8 && PARTS == 2 ? 4 : 3; // tiles of each in flight
   static constexpr int VS = FP8 ? 2 : 3;
-  static constexpr int RS = FP8 ? 3 : 0;
+  static constexpr int RS = 3;                         // landed and not yet finished (16-bit: in place)
   static constexpr int Q = 0;
   static constexpr int K = Q + QB;
   static constexpr int V = K + KS * KB;
   static constexpr int RAW = V + VS * VB;
-  static constexpr int KF = RAW + RS * RB;             // [slot][key] scale of the key
+  static constexpr int KF = RAW + (FP8 ? RS * RB : 0);             // [slot][key] scale of the key
   static constexpr int VF = KF + (FP8 ? kFactSlots * kTK * 4 : 0);   // [slot][key] factor of the values (f16 pair)
   static constexpr int STATS = Q;                      // over the queries, once a segment's products are done
   static constexpr int BYTES = VF + (FP8 ? kFactSlots * kTK * 4 : 0) + 1024;   // and room to align
@@ -78,7 +79,7 @@ struct TileShared {
   uint64_t q_full, o_full;
   uint32_t live[kFactSlots][4];     // keys of a tile that the cache holds
   float vexp[kFactSlots][4];        // 8-bit caches: 32 keys' values are held as v 2^-vexp
-  int tail[kFactSlots];             // the tile holds nodes
+  int dirty[kFactSlots];            // the tile holds nodes, or misses keys
   float rowf[kR];
   uint32_t tmem;
   int poison;                       // some tile with nodes held a value that is not finite (stays set)
@@ -202,10 +203,11 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 // A box of rows `row`, ... from column x of the map's array; completes on `bar`.
-__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar, uint32_t one) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(row)
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(row), "r"(one)
       : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -287,9 +289,9 @@ __device__ __forceinline__ uint32_t shrink(uint32_t w, float by, __nv_bfloat16) 
 }
 
 // Takes the non-finite 16-bit values out of w; whether there were any.  A row's
-// hidden nodes have weight 0, and 0 x inf would reach it through the product: in
-// tiles that hold nodes such values are left out, and the rows that do see their
-// keys get them when the segment ends.
+// hidden nodes have weight 0, and 0 x inf would reach it through the product:
+// nodes' values of that kind are left out, and the rows that do see their keys get
+// them when the segment ends.
 template <typename E>
 __device__ __forceinline__ bool clear_nonfinite(uint4& w) {
   constexpr uint32_t X = std::is_same<E, __half>::value ? 0x7C00u : 0x7F80u;
@@ -343,21 +345,24 @@ struct Segments {
 
 __device__ __forceinline__ void next_segment(Segments* s, const PlanArgs c) {
   s->more = false;
-  if (s->base + s->u >= s->end) return;
-  uint32_t ignored = 0;
-  while (s->u >= (int)s->q.units) {
-    s->base += s->q.units;
-    s->u -= (int)s->q.units;
-    if (++s->b >= c.B) return;   // lengths that changed under the call
-    s->q = attend_request(c, s->b, kR, kTK, ignored);
-  }
-  const int tiles = s->q.tiles, rts = s->q.rts, u = s->u;
-  const int item = (int)((unsigned)u / (unsigned)tiles);
-  s->t0 = u - item * tiles;
-  s->t1 = (int)min((int64_t)tiles, s->t0 + (s->end - s->base - u));
-  s->h = (int)((unsigned)item / (unsigned)rts);
-  s->rt = item - s->h * rts;
-  s->u = u + s->t1 - s->t0;
+  do {
+    if (s->base + s->u >= s->end) return;
+    uint32_t ignored = 0;
+    while (s->u >= (int)s->q.units) {
+      s->base += s->q.units;
+      s->u -= (int)s->q.units;
+      if (++s->b >= c.B) return;   // lengths that changed under the call
+      s->q = attend_request(c, s->b, kR, kTK, ignored);
+    }
+    const int tiles = s->q.tiles, rts = s->q.rts, u = s->u;
+    const int item = (int)((unsigned)u / (unsigned)(tiles + kItemCost)), at = u - item * (tiles + kItemCost);
+    s->t0 = max(at - kItemCost, 0);
+    s->t1 = (int)min((int64_t)tiles, at - kItemCost + (s->end - s->base - u));
+    s->h = (int)((unsigned)item / (unsigned)rts);
+    s->rt = item - s->h * rts;
+    s->u = u + tiles + kItemCost - at;
+  } while (s->t1 <= s->t0);          // a range may end before an item's first tile
+  const int tiles = s->q.tiles;
   s->whole = s->t0 == 0 && s->t1 == tiles;
   s->rows = min(kR, s->q.n * c.group - s->rt * kR);
   s->more = true;
@@ -398,7 +403,7 @@ __device__ __noinline__ float left_out(const CacheArgs& c, const Segments& s, in
   for (int t = max(s.t0, q.len / kTK); t < s.t1; ++t) {
     uint32_t bits[4];
     visible(s, c.parent, node, t, bits);
-    for (int k = 0; k < kTK; ++k) {
+    for (int k = max(0, q.len - t * kTK); k < kTK; ++k) {   // nodes
       const int64_t at = (int64_t)t * kTK + k;
       if (!((bits[k >> 5] >> (k & 31)) & 1u) || at >= (int64_t)q.len + q.n) continue;
       const int64_t r0 = cache_row(c.geo, c.table + s.b * c.geo.table_stride, at);
@@ -431,8 +436,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   extern __shared__ char smem_raw[];
   __shared__ ScanShared scan;
   __shared__ __align__(8) TileShared sh;
-  // segments of the softmax groups, the products and the loaders
-  __shared__ Segments segs[2 + kLoaders];
+  // segments of the softmax groups, the products, the loaders and the wideners
+  __shared__ Segments segs[3 + kLoaders];
   char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t base_s = smem_addr(smem);
   const CacheArgs& c = a.c;
@@ -459,12 +464,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(smem_addr(&sh.k_empty[i]), 1);
     }
     for (int i = 0; i < L::VS; ++i) {
-      mbar_init(smem_addr(&sh.v_full[i]), FP8 ? kWidenWarps * 32 : 32);
+      mbar_init(smem_addr(&sh.v_full[i]), kFinishWarps * 32);
       mbar_init(smem_addr(&sh.v_empty[i]), 1);
     }
     for (int i = 0; i < L::RS; ++i) {
       mbar_init(smem_addr(&sh.raw_full[i]), 32);
-      mbar_init(smem_addr(&sh.raw_empty[i]), kWidenWarps);
+      mbar_init(smem_addr(&sh.raw_empty[i]), kFinishWarps);
     }
     for (int i = 0; i < kFactSlots; ++i) mbar_init(smem_addr(&sh.fact[i]), 1);
     for (int w = 0; w < 2; ++w) {
@@ -486,7 +491,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   const uint32_t tm = sh.tmem;
   const int64_t uend = range_begin(units, ranges, blockIdx.x + 1);
-  if (tid < 2 + kLoaders) {
+  if (tid < 3 + kLoaders) {
     uint32_t ignored = 0;
     Segments& s = segs[tid];
     s.end = uend;
@@ -578,14 +583,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int loader = warp - kLoadWarp;
       struct Tile {
         int row[4];       // cache row of the key, -1: none
-        uint32_t all;     // bit i: 32 keys from 32 i all have one
-        uint32_t clean;   // bit i: and none of them is a node
-        bool tail;        // the tile holds nodes
+        uint32_t live[4]; // which of the 128 keys have one
+        bool dirty;
       };
       struct Look {       // page ids on their way
         int id[4], off[4], h;
-        uint32_t context;
-        bool tail;
+        bool tail;        // the tile holds nodes
       };
       Segments& seg = segs[2 + loader];
       int skip = loader, t = seg.t0;            // tiles of others before this loader's next
@@ -605,47 +608,58 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t len = (uint32_t)seg.q.len, end = len + (uint32_t)seg.q.n, first = (uint32_t)t * kTK;
         x.tail = first + kTK > len;
         x.h = seg.h;
-        x.context = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t at = first + i * 32 + lane, page = at / page_size;
           x.off[i] = (int)(at - page * page_size);
           x.id[i] = at < end ? __ldg(pages + page) : -2;    // end is within the table
-          if (first + i * 32 + 32 <= len) x.context |= 1u << i;
         }
         return true;
       };
       auto found = [&](const Look& l, Tile& x) {
-        x.tail = l.tail;
-        x.all = 0;
+        uint32_t all = 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool in = l.id[i] >= 0 && l.id[i] < c.geo.num_pages;
           if (!in && l.id[i] != -2) bad |= SPECDEC_DEVERR_BAD_CACHE;
           // fewer than 2^31 rows in all
           x.row[i] = in ? (l.id[i] * c.geo.kv_heads + l.h) * (int)page_size + l.off[i] : -1;
-          if (__all_sync(0xFFFFFFFFu, in)) x.all |= 1u << i;
+          x.live[i] = __ballot_sync(0xFFFFFFFFu, in);
+          all &= x.live[i];
         }
-        x.clean = x.all & l.context;
+        x.dirty = l.tail || all != 0xFFFFFFFFu;
       };
-      // The rows of a tile of the array `src` (16-bit, or 8-bit as it is) to `dst`:
-      // boxes for the groups of 32 keys in `boxes`, 16-byte copies for the others.
-      // Every lane arrives on `bar` when its copies have landed, unless `arrive`
-      // is false (then the copies have been waited for).
-      auto fetch = [&](uint32_t dst, const void* src, const CUtensorMap* map, const Tile& x, uint32_t boxes, uint32_t bar,
-                       bool arrive) {
+      // The rows of a tile of the array `src` (16-bit, or 8-bit as it is) to `dst`;
+      // every lane arrives on `bar` when its copies have landed.  A box lies within
+      // one page: it is fetched if its first key lives, and what it brings of slots
+      // behind the last key is hidden (keys) or taken out (values).
+      auto fetch = [&](uint32_t dst, const void* src, const CUtensorMap* map, const Tile& x, uint32_t bar) {
         constexpr int LINE = FP8 ? D : 128, HALVES = FP8 ? 1 : D / 64, RC = FP8 ? D / 16 : D / 8;
-        if (box == 0) boxes = 0;
-        if (boxes && lane == 0) mbar_expect_tx(bar, __popc(boxes) * 32 * HALVES * LINE);
-        __syncwarp();
+        if (box > 0) {
+          const uint32_t one = lane == 0 ? 1u : 0u;
+          // first keys of boxes among each 32: one bit for boxes of 32, one in some
+          // groups for larger ones
+          const uint32_t firsts = box >= 32 ? 1u : box == 16 ? 0x00010001u : 0x01010101u;
+          int count = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (box <= 32 || (i * 32) % box == 0) count += __popc(x.live[i] & firsts);
+          if (one) mbar_expect_tx(bar, count * box * HALVES * LINE);
+          __syncwarp();
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const int mine = i == 0 ? x.row[0] : i == 1 ? x.row[1] : i == 2 ? x.row[2] : x.row[3];
-          if ((boxes >> i) & 1u) {
-            const int r0 = (lane / HALVES) * box, half = lane % HALVES;
+          for (int r0 = 0; r0 < kTK; r0 += box) {
+            const int i = r0 >> 5;
+            const int mine = i == 0 ? x.row[0] : i == 1 ? x.row[1] : i == 2 ? x.row[2] : x.row[3];
             const int row = __shfl_sync(0xFFFFFFFFu, mine, r0 & 31);
-            if (r0 < 32) box_load(dst + half * (kTK * 128) + (i * 32 + r0) * LINE, map, half * 64, row, bar);
-          } else {
+            if (row >= 0)
+#pragma unroll
+              for (int half = 0; half < HALVES; ++half)
+                box_load(dst + half * (kTK * 128) + r0 * LINE, map, half * 64, row, bar, one);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int mine = i == 0 ? x.row[0] : i == 1 ? x.row[1] : i == 2 ? x.row[2] : x.row[3];
 #pragma unroll 4
             for (int z = 0; z < RC; ++z) {
               const int y = z * 32 + lane, key = y / RC, ch = y % RC;
@@ -655,12 +669,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
         }
-        if (arrive) {
-          copy_arrive(bar);
-        } else {
-          copy_commit();
-          copy_wait<0>();
-        }
+        copy_arrive(bar);
       };
       Look ahead;
       bool have = look(ahead);
@@ -677,34 +686,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         wait_free(sh.k_empty, L::KS, n);
-        fetch(base_s + L::K + (n % L::KS) * L::KB, c.k, &kmap, now, now.all, smem_addr(&sh.k_full[n % L::KS]), true);
-        if constexpr (FP8) {
-          wait_free(sh.raw_empty, L::RS, n);
-          fetch(base_s + L::RAW + (n % L::RS) * L::RB, c.v, &vmap, now, now.clean, smem_addr(&sh.raw_full[n % L::RS]), true);
-        } else {
-          const uint32_t bar = smem_addr(&sh.v_full[n % L::VS]), dst = base_s + L::V + (n % L::VS) * L::VB;
-          wait_free(sh.v_empty, L::VS, n);
-          fetch(dst, c.v, &vmap, now, now.clean, bar, !now.tail);
-          if (now.tail) {
-            // values of nodes: see clear_nonfinite
-            bool hit = false;
-            for (int i = 0; i < 4; ++i) {
-              if (box > 0 && ((now.clean >> i) & 1u)) continue;
-              for (int z = 0; z < CH; ++z) {
-                const int y = z * 32 + lane, key = y / CH, ch = y % CH;
-                const uint32_t at = dst + op_chunk(i * 32 + key, ch);
-                uint4 w = lds128(at);
-                if (clear_nonfinite<E>(w)) {
-                  sts128(at, w);
-                  hit = true;
-                }
-              }
-            }
-            if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
-            fence_async_proxy();
-            mbar_arrive(bar);
-          }
-        }
+        fetch(base_s + L::K + (n % L::KS) * L::KB, c.k, &kmap, now, smem_addr(&sh.k_full[n % L::KS]));
+        wait_free(sh.raw_empty, L::RS, n);
+        if constexpr (!FP8) wait_free(sh.v_empty, L::VS, n);   // landing in place
+        fetch(base_s + (FP8 ? L::RAW + (n % L::RS) * L::RB : L::V + (n % L::VS) * L::VB), c.v, &vmap, now,
+              smem_addr(&sh.raw_full[n % L::RS]));
         // What the other roles need to know of the tile's keys.  8-bit caches: the
         // scale of K (applied to the scores, in 32 bits); the scale of V goes into
         // the widened values, as a factor v 2^-vexp that f16 holds: the largest of
@@ -715,8 +701,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int f = n % kFactSlots;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t live = __ballot_sync(0xFFFFFFFFu, now.row[i] >= 0);
-          if (lane == 0) sh.live[f][i] = live;
+          if (lane == 0) sh.live[f][i] = now.live[i];
           if constexpr (FP8) {
             const bool real = vs[i] > 0.0f && isfinite(vs[i]);
             const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, real ? __float_as_uint(vs[i]) : 0u);
@@ -727,7 +712,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             reinterpret_cast<uint32_t*>(smem + L::VF)[f * kTK + i * 32 + lane] = pack2(factor, factor, __half());
           }
         }
-        if (lane == 0) sh.tail[f] = now.tail;
+        if (lane == 0) sh.dirty[f] = now.dirty;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
       }
@@ -736,21 +721,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp >= 2 * kGroupWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if constexpr (FP8) {
-      // ---- wideners: 32 keys each; 8 lanes read and write one chunk of 8
-      // neighbouring rows, without bank conflicts in either swizzle -------------
-      const int pw = warp - 2 * kGroupWarps;
-      constexpr int RC = D / 16;             // 16-byte chunks of an 8-bit row
-      const int tiles = (int)(uend - u0);
-      for (int n = 0; n < tiles; ++n) {
-        const int f = n % kFactSlots;
-        wait_use(sh.fact, kFactSlots, n);
-        const bool tail = sh.tail[f] != 0;
-        const uint32_t own = reinterpret_cast<const uint32_t*>(smem + L::VF)[f * kTK + pw * 32 + lane];
-        wait_use(sh.raw_full, L::RS, n);
+    // ---- finishers: 32 keys each.  8 lanes read and write one chunk of 8
+    // neighbouring rows, without bank conflicts in any of the swizzles ------------
+    const int pw = warp - 2 * kGroupWarps;
+    Segments& seg = segs[2 + kLoaders];
+    for (int n = 0, t = seg.t0; seg.more; ++n) {
+      const int f = n % kFactSlots;
+      wait_use(sh.fact, kFactSlots, n);
+      const bool dirty = sh.dirty[f] != 0;
+      const uint32_t live = sh.live[f][pw];
+      const int nodes = seg.q.len - t * kTK - pw * 32;      // the warp's keys from here on are nodes
+      const uint32_t dst = base_s + L::V + (n % L::VS) * L::VB;
+      uint32_t own = 0;
+      if constexpr (FP8) own = reinterpret_cast<const uint32_t*>(smem + L::VF)[f * kTK + pw * 32 + lane];
+      wait_use(sh.raw_full, L::RS, n);
+      bool hit = false;
+      if constexpr (FP8) {
         wait_free(sh.v_empty, L::VS, n);
-        const uint32_t raw = base_s + L::RAW + (n % L::RS) * L::RB, dst = base_s + L::V + (n % L::VS) * L::VB;
-        bool hit = false;
+        const uint32_t raw = base_s + L::RAW + (n % L::RS) * L::RB;
+        constexpr int RC = D / 16;             // 16-byte chunks of an 8-bit row
 #pragma unroll 2
         for (int i = 0; i < RC; ++i) {
           const int in = (lane & 7) + 8 * (RC == 8 ? i >> 1 : i), key = pw * 32 + in;
@@ -759,15 +748,39 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint32_t by = __shfl_sync(0xFFFFFFFFu, own, in);
           uint4 lo = times(make_uint4(e4m3x2_f16x2(w.x), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y), e4m3x2_f16x2(w.y >> 16)), by);
           uint4 hi = times(make_uint4(e4m3x2_f16x2(w.z), e4m3x2_f16x2(w.z >> 16), e4m3x2_f16x2(w.w), e4m3x2_f16x2(w.w >> 16)), by);
-          if (tail) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
+          if (dirty) {
+            if (!((live >> in) & 1u)) lo = hi = make_uint4(0, 0, 0, 0);
+            else if (in >= nodes) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
+          }
           sts128(dst + op_chunk(key, 2 * ch), lo);
           sts128(dst + op_chunk(key, 2 * ch + 1), hi);
         }
-        if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
-        fence_async_proxy();
-        mbar_arrive(smem_addr(&sh.v_full[n % L::VS]));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.raw_empty[n % L::RS]));
+      } else if (dirty && (nodes < 32 || live != 0xFFFFFFFFu)) {
+#pragma unroll 1
+        for (int i = 0; i < CH; ++i) {
+          const int in = (lane & 7) + 8 * (i & 3), ch = (lane >> 3) + 4 * (i >> 2);
+          const uint32_t at = dst + op_chunk(pw * 32 + in, ch);
+          if (!((live >> in) & 1u)) {
+            sts128(at, make_uint4(0, 0, 0, 0));
+          } else if (in >= nodes) {
+            uint4 w = lds128(at);
+            if (clear_nonfinite<E>(w)) {
+              sts128(at, w);
+              hit = true;
+            }
+          }
+        }
+      }
+      if (hit) *reinterpret_cast<volatile int*>(&sh.poison) = 1;
+      fence_async_proxy();
+      mbar_arrive(smem_addr(&sh.v_full[n % L::VS]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.raw_empty[n % L::RS]));
+      if (++t == seg.t1) {
+        named_bar_sync(2, kFinishWarps * 32);
+        if (warp == 2 * kGroupWarps && lane == 0) next_segment(&seg, plan);
+        named_bar_sync(2, kFinishWarps * 32);
+        t = seg.t0;
       }
     }
   } else {
@@ -782,13 +795,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const Partials<kR, D> part(a.workspace, G);
     int done = 0, tile0 = 0;                     // this group's tiles, all tiles before the segment
     uint32_t g = 0;
-    bool first = true;
     // The segment stands in shared memory: its fields would otherwise take the
     // registers of the scores.
     Segments& seg = segs[0];
     while (seg.more) {
       // queries
       const float sgn = a.scale_log2 < 0.0f ? -1.0f : 1.0f;   // factors are positive: the sign goes to q
+      constexpr int kAhead = FP8 ? 2 : 4;   // loads in flight
+#pragma unroll kAhead
       for (int x = sid; x < kR * CH; x += kSoftmaxThreads) {
         const int r = x / CH, ch = x % CH;
         const bool live = r < seg.rows;
@@ -984,7 +998,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int gr = seg.rt * kR + row;
         const bool live = row < seg.rows;
         const float inv = seg.whole ? (lsum == 0.0f ? 0.0f : 1.0f / lsum) : 1.0f;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (first ? 0 : 1);
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (seg.t0 > 0 ? 0 : 1);
         const bool poison = *reinterpret_cast<volatile int*>(&sh.poison) != 0;
         const uint32_t o0 = tm + lanes + 256 + w * (D / 2), o1 = o0 + 128;
 #pragma unroll 1
@@ -1042,7 +1056,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       named_bar_sync(1, kSoftmaxThreads);
       tile0 += n;
       ++g;
-      first = false;
     }
   }
   if (bad) atomicOr(c.err, bad);
@@ -1088,7 +1101,9 @@ int launch_tile(const AttendArgs& a, int num_sms, cudaStream_t st) {
     return SPECDEC_ERR_CUDA;
   // rows of a box: within one page, whole groups of 8 rows of the swizzle
   const int page = a.c.geo.page_size;
-  int box = page % 32 == 0 ? 32 : page % 16 == 0 ? 16 : page % 8 == 0 ? 8 : 0;
+  int box = 128;
+  while (box > 4 && page % box) box >>= 1;
+  if (box < 8) box = 0;
   CUtensorMap kmap = {}, vmap = {};
   const int64_t rows = a.c.geo.num_pages * a.c.geo.kv_heads * page;
   if (box && (!encode_rows(&kmap, a.c.k, rows, D, box, FP8) || !encode_rows(&vmap, a.c.v, rows, D, box, FP8))) box = 0;
