@@ -3,8 +3,8 @@
 // include/specdec.h (specdec_tree_attention).
 //
 // A unit is 128 rows x 128 keys.  Per SM one CTA:
-//   loaders (3 warps)    look up the pages and bring the rows of keys and values, every
-//                        third tile each, so that one's look-ups hide behind the others',
+//   loaders (2 warps)    look up the pages and bring the rows of keys and values, every
+//                        second tile each, so that one's look-ups hide behind the other's,
 //                        into the operand layout (swizzled rows of 128 bytes): by
 //                        TMA boxes of 8 to 128 rows of a page, or by 16-byte copies
 //                        where pages have odd sizes;
@@ -12,8 +12,10 @@
 //                        widened to f16 (the keys are multiplied as they are, see
 //                        below); in tiles that hold nodes or miss keys, what no row
 //                        may see is taken out;
-//   products (1 thread)  S_w = Q K^T (both operands in shared memory) and
-//                        O_w += P_w V (P in tensor memory);
+//   products (2 warps)   S_w = Q K^T (both operands in shared memory) from one, O_w +=
+//                        P_w V (P in tensor memory) from the other: a warp stands
+//                        still while its products are taken up, and one warp's waits
+//                        for both left the tensor cores idle;
 //   softmax (2 groups    group w takes every second tile of a segment with a
 //   of 4 warps)          maximum, sum and O_w of its own, one row per thread, so
 //                        that one group's exponentials overlap the other's
@@ -45,9 +47,9 @@ constexpr int kR = 128, kTK = 128;
 constexpr int kGroupWarps = 4;                       // softmax warps of a group
 constexpr int kSoftmaxThreads = 2 * kGroupWarps * 32;
 constexpr int kFinishWarps = 4;
-constexpr int kMmaWarp = 2 * kGroupWarps + kFinishWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kLoaders = 3;                          // loader l takes tiles l, l + 3, ... of the range
-constexpr int kTileThreads = (kMmaWarp + 4) * 32;    // a whole warpgroup: registers move between those
+constexpr int kScoreWarp = 2 * kGroupWarps + kFinishWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kScoreWarp + 2;
+constexpr int kLoaders = 2;                          // loader l takes tiles l, l + 2, ... of the range
+constexpr int kTileThreads = (kScoreWarp + 4) * 32;    // a whole warpgroup: registers move between those
 constexpr int kFactSlots = 8;                        // tiles whose key facts are held (5 are needed)
 
 template <typename T, bool FP8, int D>
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ ScanShared scan;
   __shared__ __align__(8) TileShared sh;
   // segments of the softmax groups, the products, the loaders and the wideners
-  __shared__ Segments segs[3 + kLoaders];
+  __shared__ Segments segs[4 + kLoaders];
   char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t base_s = smem_addr(smem);
   const CacheArgs& c = a.c;
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     sh.dead = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "n"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   const uint32_t tm = sh.tmem;
   const int64_t uend = range_begin(units, ranges, blockIdx.x + 1);
-  if (tid < 3 + kLoaders) {
+  if (tid < 4 + kLoaders) {
     uint32_t ignored = 0;
     Segments& s = segs[tid];
     s.end = uend;
@@ -512,71 +514,79 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto wait_free = [&](uint64_t* bars, int slots, int n) {      // the slot's use n - slots is complete
     wait_or_give_up(sh, smem_addr(&bars[n % slots]), ((uint32_t)(n / slots) & 1u) ^ 1u);
   };
-  if (warp >= kMmaWarp) {
+  if (warp >= kScoreWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == kMmaWarp) {
-      // ---- products -----------------------------------------------------------
-      const uint32_t one = lane == 0 ? 1u : 0u;
-      int seq = 0;                                // tiles before the segment
-      uint32_t g = 0, tiles_of[2] = {0, 0};
-      const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0), ops = __shfl_sync(0xFFFFFFFFu, base_s, 0);
+    const uint32_t one = lane == 0 ? 1u : 0u;
+    if (warp == kScoreWarp) {
+      // ---- scores ---------------------------------------------------------------
       Segments& seg = segs[1];
-      while (seg.more) {
+      const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0), ops = __shfl_sync(0xFFFFFFFFu, base_s, 0);
+      int k = 0;                                  // tiles so far
+      for (uint32_t g = 0; seg.more; ++g) {
         const int n = seg.t1 - seg.t0;
         wait_or_give_up(sh, smem_addr(&sh.q_full), g & 1u);
 #pragma unroll 1
-        for (int j = 0; j <= n; ++j) {
-          if (j < n) {
-            const int k = seq + j, w = j & 1;
-            // S_w and P_w are free once the product before last has read P_w
-            if (j >= 2) wait_use(sh.v_empty, L::VS, k - 2);
-            wait_use(sh.k_full, L::KS, k);
-            fence_async_proxy();   // rows that came by 16-byte copies
-            tc_fence_after();
-            const uint32_t kt = ops + L::K + (k % L::KS) * L::KB;
-            if constexpr (FP8) {
-              const uint64_t kd = operand<D>(kt, 16);
+        for (int j = 0; j < n; ++j, ++k) {
+          const int w = j & 1;
+          // S_w and P_w are free once the product before last has read P_w
+          if (j >= 2) wait_use(sh.v_empty, L::VS, k - 2);
+          wait_use(sh.k_full, L::KS, k);
+          fence_async_proxy();   // rows that came by 16-byte copies
+          tc_fence_after();
+          const uint32_t kt = ops + L::K + (k % L::KS) * L::KB;
+          if constexpr (FP8) {
+            const uint64_t kd = operand<D>(kt, 16);
 #pragma unroll 1
-              for (int part = 0; part < L::PARTS; ++part) {
-                const uint64_t qd = operand<D>(ops + L::Q + part * kR * D, 16);
+            for (int part = 0; part < L::PARTS; ++part) {
+              const uint64_t qd = operand<D>(ops + L::Q + part * kR * D, 16);
 #pragma unroll
-                for (int s = 0; s < D / 32; ++s)
-                  tc_mma_e4m3(tmu + w * 128, qd + s * 2, kd + s * 2, product_e4m3(kTK), part + s > 0, one);
-              }
-            } else {
-              const uint64_t qd = operand(ops + L::Q, 16), kd = operand(kt, 16);
-#pragma unroll
-              for (int s = 0; s < D / 16; ++s) {
-                const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
-                tc_mma_ss(tmu + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0, one);
-              }
+              for (int s = 0; s < D / 32; ++s)
+                tc_mma_e4m3(tmu + w * 128, qd + s * 2, kd + s * 2, product_e4m3(kTK), part + s > 0, one);
             }
-            tc_commit(smem_addr(&sh.s_full[w]), one);
-            tc_commit(smem_addr(&sh.k_empty[k % L::KS]), one);
+          } else {
+            const uint64_t qd = operand(ops + L::Q, 16), kd = operand(kt, 16);
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+              const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
+              tc_mma_ss(tmu + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0, one);
+            }
           }
-          if (j > 0) {
-            const int v = seq + j - 1, w = (j - 1) & 1;
-            wait_use(sh.v_full, L::VS, v);
-            wait_or_give_up(sh, smem_addr(&sh.p_full[w]), (w ? tiles_of[1] : tiles_of[0]) & 1u);
-            if (w) ++tiles_of[1]; else ++tiles_of[0];
-            fence_async_proxy();
-            tc_fence_after();
-            const uint64_t vd = operand(ops + L::V + (v % L::VS) * L::VB, kTK * 128);
+          tc_commit(smem_addr(&sh.s_full[w]), one);
+          tc_commit(smem_addr(&sh.k_empty[k % L::KS]), one);
+        }
+        __syncwarp();
+        if (lane == 0) next_segment(&seg, plan);
+        __syncwarp();
+      }
+    } else if (warp == kValueWarp) {
+      // ---- weighted values --------------------------------------------------------
+      Segments& seg = segs[2];
+      const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0), ops = __shfl_sync(0xFFFFFFFFu, base_s, 0);
+      int v = 0;
+      uint32_t used[2] = {0, 0};                  // tiles of each group so far
+      while (seg.more) {
+        const int n = seg.t1 - seg.t0;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++v) {
+          const int w = j & 1;
+          wait_use(sh.v_full, L::VS, v);
+          wait_or_give_up(sh, smem_addr(&sh.p_full[w]), (w ? used[1] : used[0]) & 1u);
+          if (w) ++used[1]; else ++used[0];
+          tc_fence_after();
+          const uint64_t vd = operand(ops + L::V + (v % L::VS) * L::VB, kTK * 128);
 #pragma unroll 2
-            for (int s = 0; s < kTK / 16; ++s)
-              tc_mma_ts(tmu + 256 + w * 128, tmu + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
-                        s > 0 || j > 2, one);
-            tc_commit(smem_addr(&sh.v_empty[v % L::VS]), one);
-          }
+          for (int s = 0; s < kTK / 16; ++s)
+            tc_mma_ts(tmu + 256 + w * 128, tmu + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
+                      s > 0 || j >= 2, one);
+          tc_commit(smem_addr(&sh.v_empty[v % L::VS]), one);
         }
         tc_commit(smem_addr(&sh.o_full), one);
+        __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_addr(&sh.o_full));
           next_segment(&seg, plan);
         }
         __syncwarp();
-        seq += n;
-        ++g;
       }
     } else {
       // ---- loaders: a lane looks after keys lane, lane + 32, ... of a tile ------
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int id[4], off[4], h;
         bool tail;        // the tile holds nodes
       };
-      Segments& seg = segs[2 + loader];
+      Segments& seg = segs[3 + loader];
       int skip = loader, t = seg.t0;            // tiles of others before this loader's next
       const uint32_t page_size = (uint32_t)c.geo.page_size;
       auto look = [&](Look& x) -> bool {        // this loader's next tile
@@ -724,7 +734,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---- finishers: 32 keys each.  8 lanes read and write one chunk of 8
     // neighbouring rows, without bank conflicts in any of the swizzles ------------
     const int pw = warp - 2 * kGroupWarps;
-    Segments& seg = segs[2 + kLoaders];
+    Segments& seg = segs[3 + kLoaders];
     for (int n = 0, t = seg.t0; seg.more; ++n) {
       const int f = n % kFactSlots;
       wait_use(sh.fact, kFactSlots, n);
@@ -1064,7 +1074,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (tid == 0 && sh.dead) atomicOr(c.err, SPECDEC_DEVERR_TIMEOUT);
-  if (warp == kMmaWarp)
+  if (warp == kScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(512));
 }
 
