@@ -114,52 +114,70 @@ __device__ __forceinline__ void load8(const float* p, float* x) {
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 
-// One block per row of a tile: threads are (head slot, chunk of 8 values); a
-// thread keeps its cos and sin for every head it turns.  Products and their
-// sum are rounded one by one (no fused multiply-add), as the formula
+constexpr int kRows = 16;   // rows of a block at most
+
+// Where the rows of a block lie: found by one thread each, all at once, before
+// any value is moved.
+struct RowPlace {
+  int64_t row;        // cache row of head 0, -1: none
+  int64_t turn;       // offset of the position's cos in the rotary table, -1: none
+  int32_t owned;      // the row belongs to a request
+};
+
+__device__ __forceinline__ RowPlace place_of(const CacheArgs& c, int64_t r, bool rotary, int rotary_dim, int64_t positions) {
+  RowPlace p = {-1, -1, 0};
+  uint32_t bad = 0;
+  const int b = request_of_row(c.cu, c.B, r);
+  if (b < 0) {  // rows behind the last request are not touched
+    if (r < (int64_t)c.cu[c.B]) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
+    return p;
+  }
+  p.owned = 1;
+  const int64_t first = c.cu[b], len = c.lengths[b];
+  const int j = (int)(r - first);
+  p.row = len < 0 ? -1 : cache_row(c.geo, c.table + b * c.geo.table_stride, len + j);
+  if (p.row < 0) bad |= SPECDEC_DEVERR_BAD_CACHE;
+  if (rotary) {
+    const int depth = node_depth(c.parent ? c.parent + first : nullptr, j);
+    if (depth < 0) bad |= SPECDEC_DEVERR_BAD_TREE;
+    else if (len < 0 || len + depth >= positions) bad |= SPECDEC_DEVERR_BAD_CACHE;
+    else p.turn = (len + depth) * rotary_dim;
+    if (p.turn < 0) p.row = -1;
+  }
+  if (bad) atomicOr(c.err, bad);
+  return p;
+}
+
+// Threads are (head slot, chunk of 8 values); a thread keeps its cos and sin for
+// every head it turns.  Products and their sum are rounded one by one (no fused
+// multiply-add), as the formula
 //   a' = a cos - b sin, b' = b cos + a sin
 // reads in 32 bits, so that what is quantised does not depend on contraction.
 template <typename T, bool FP8, int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, const int rows) {
   constexpr int LANES = D / 8;                 // lanes of a row
   constexpr int SLOTS = kThreads / LANES;      // heads in flight
+  __shared__ RowPlace places[kRows];
   const int chunk = threadIdx.x % LANES, slot0 = threadIdx.x / LANES;
   const CacheArgs& c = a.c;
   const int half = a.rotary_dim / 2;
   const int d0 = chunk * 8;
-  for (int64_t r = (int64_t)blockIdx.x * rows; r < min((int64_t)(blockIdx.x + 1) * rows, c.N); ++r) {
-    const int b = request_of_row(c.cu, c.B, r);
-    if (b < 0) {  // rows behind the last request are not touched
-      if (threadIdx.x == 0 && r < (int64_t)c.cu[c.B]) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
-      continue;
-    }
-    const int64_t first = c.cu[b];
-    const int j = (int)(r - first);
-    const int64_t len = c.lengths[b];
-    const int64_t row0 = len < 0 ? -1 : cache_row(c.geo, c.table + b * c.geo.table_stride, len + j);
-    bool live = row0 >= 0;
-    uint32_t bad = live ? 0u : SPECDEC_DEVERR_BAD_CACHE;
-    const float *cosp = nullptr, *sinp = nullptr;
-    if (a.rotary) {
-      const int depth = node_depth(c.parent ? c.parent + first : nullptr, j);
-      const int64_t pos = len + depth;
-      if (depth < 0) {
-        bad |= SPECDEC_DEVERR_BAD_TREE;
-        live = false;
-      } else if (len < 0 || pos >= a.positions) {
-        bad |= SPECDEC_DEVERR_BAD_CACHE;
-        live = false;
-      } else {
-        cosp = a.rotary + pos * 2 * half;
-        sinp = cosp + half;
-      }
-    }
-    if (bad && threadIdx.x == 0) atomicOr(c.err, bad);
-    const bool turned = cosp && d0 < a.rotary_dim;
+  const int64_t r0 = (int64_t)blockIdx.x * rows;
+  const int here = (int)min((int64_t)rows, c.N - r0);
+  if ((int)threadIdx.x < here) places[threadIdx.x] = place_of(c, r0 + threadIdx.x, a.rotary != nullptr, a.rotary_dim, a.positions);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (int64_t)c.cu[c.B] > c.N) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
+  __syncthreads();
+  const int kv = c.geo.kv_heads, total = 2 * kv + (a.q ? a.q_heads : 0);
+  for (int i = 0; i < here; ++i) {
+    const RowPlace p = places[i];
+    if (!p.owned) continue;
+    const int64_t r = r0 + i;
+    const bool turned = p.turn >= 0 && d0 < a.rotary_dim;
     float cs[8], sn[8];
-    int64_t partner = 0;
+    int partner = 0;
     float sign = 1.0f;
     if (turned) {
+      const float *cosp = a.rotary + p.turn, *sinp = cosp + half;
       if (a.interleaved) {
         const float4 x = __ldg(reinterpret_cast<const float4*>(cosp + d0 / 2));
         const float4 y = __ldg(reinterpret_cast<const float4*>(sinp + d0 / 2));
@@ -173,106 +191,128 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
         sign = low ? -1.0f : 1.0f;
       }
     }
-    const int turns = a.q ? a.q_heads : 0;
-    // heads in order: k, v, then q, SLOTS at a time; every lane of a warp takes
-    // part in each step, with its own source row
-    const int total = 2 * c.geo.kv_heads + turns;
-    for (int h0 = 0; h0 < total; h0 += SLOTS) {
-      const int hh = h0 + slot0;
-      const bool isk = hh < c.geo.kv_heads;
-      const bool isv = !isk && hh < 2 * c.geo.kv_heads;
-      const bool any = hh < total;
-      const int h = isk ? hh : (isv ? hh - c.geo.kv_heads : hh - 2 * c.geo.kv_heads);
-      const T* src = nullptr;
-      if (any)
-        src = isk ? static_cast<const T*>(a.k) + r * a.k_row + h * a.k_head
-                  : isv ? static_cast<const T*>(a.v) + r * a.v_row + h * a.v_head
-                        : static_cast<const T*>(a.q) + r * a.q_row + h * a.q_head;
-      Vec8 x = {};
-      if (any) {
-        x = widen<T>(__ldg(reinterpret_cast<const uint4*>(src + d0)));
-        if (turned && !isv) {
-          Vec8 y;
-          if (a.interleaved) {
+    // heads in order: k, v, then q, SLOTS at a time; U steps' loads are under way
+    // together, and every lane of a warp takes part in each step (row_amax)
+    constexpr int U = 3;
+    for (int h0 = 0; h0 < total; h0 += U * SLOTS) {
+      uint4 w[U], o[U];
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              y.x[i] = __fsub_rn(__fmul_rn(x.x[i], cs[i]), __fmul_rn(x.x[i + 1], sn[i]));
-              y.x[i + 1] = __fadd_rn(__fmul_rn(x.x[i + 1], cs[i]), __fmul_rn(x.x[i], sn[i]));
-            }
-          } else {
-            const Vec8 o = widen<T>(__ldg(reinterpret_cast<const uint4*>(src + d0 + partner)));
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              y.x[i] = __fadd_rn(__fmul_rn(x.x[i], cs[i]), sign * __fmul_rn(o.x[i], sn[i]));
-          }
-          x = y;
+      for (int u = 0; u < U; ++u) {
+        const int hh = h0 + u * SLOTS + slot0;
+        if (hh < total) {
+          const bool isk = hh < kv, isv = !isk && hh < 2 * kv;
+          const T* src = isk ? static_cast<const T*>(a.k) + r * a.k_row + hh * a.k_head
+                         : isv ? static_cast<const T*>(a.v) + r * a.v_row + (hh - kv) * a.v_head
+                               : static_cast<const T*>(a.q) + r * a.q_row + (hh - 2 * kv) * a.q_head;
+          w[u] = __ldg(reinterpret_cast<const uint4*>(src + d0));
+          if (turned && !isv && !a.interleaved) o[u] = __ldg(reinterpret_cast<const uint4*>(src + d0 + partner));
         }
       }
-      // stored rows and turned q rows part here; row_amax needs whole warps, so
-      // the 8-bit store runs for every lane and q lanes drop its result
-      if (FP8 && h0 < 2 * c.geo.kv_heads) {
-        void* base = isk ? c.k : c.v;
-        store_row<T, FP8, D>(base, isk ? c.ks : c.vs, row0 + (int64_t)h * c.geo.page_size, chunk, x,
-                             any && live && (isk || isv));
-      } else if (!FP8 && any && (isk || isv)) {
-        store_row<T, FP8, D>(isk ? c.k : c.v, nullptr, row0 + (int64_t)h * c.geo.page_size, chunk, x, live);
-      }
-      if (any && !isk && !isv) {
-        if (a.rotary && !cosp) x = Vec8{};  // no position: a defined row
-        reinterpret_cast<uint4*>(static_cast<T*>(a.out_q) + (r * a.q_heads + h) * D)[chunk] = narrow<T>(x);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (h0 + u * SLOTS >= total) break;
+        const int hh = h0 + u * SLOTS + slot0;
+        const bool any = hh < total, isk = hh < kv, isv = !isk && hh < 2 * kv;
+        Vec8 x = {};
+        if (any) {
+          x = widen<T>(w[u]);
+          if (turned && !isv) {
+            Vec8 y;
+            if (a.interleaved) {
+#pragma unroll
+              for (int k = 0; k < 8; k += 2) {
+                y.x[k] = __fsub_rn(__fmul_rn(x.x[k], cs[k]), __fmul_rn(x.x[k + 1], sn[k]));
+                y.x[k + 1] = __fadd_rn(__fmul_rn(x.x[k + 1], cs[k]), __fmul_rn(x.x[k], sn[k]));
+              }
+            } else {
+              const Vec8 z = widen<T>(o[u]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                y.x[k] = __fadd_rn(__fmul_rn(x.x[k], cs[k]), sign * __fmul_rn(z.x[k], sn[k]));
+            }
+            x = y;
+          }
+        }
+        // stored rows and turned q rows part here; row_amax needs whole warps, so
+        // the 8-bit store runs for every lane and q lanes drop its result
+        if (h0 + u * SLOTS < 2 * kv) {
+          const int64_t row = p.row + (int64_t)(isk ? hh : hh - kv) * c.geo.page_size;
+          store_row<T, FP8, D>(isk ? c.k : c.v, isk ? c.ks : c.vs, row, chunk, x, any && p.row >= 0 && (isk || isv));
+        }
+        if (any && !isk && !isv) {
+          if (a.rotary && p.turn < 0) x = Vec8{};  // no position: a defined row
+          reinterpret_cast<uint4*>(static_cast<T*>(a.out_q) + (r * a.q_heads + hh - 2 * kv) * D)[chunk] = narrow<T>(x);
+        }
       }
     }
   }
 }
 
+// A thread takes 16 bytes of a cache row (16 or 8 values) at a time, four under
+// way together.
 template <typename T, bool FP8, int D>
-__global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a, const int rows) {
-  constexpr int LANES = D / 8;
-  constexpr int SLOTS = kThreads / LANES;
-  const int chunk = threadIdx.x % LANES, slot0 = threadIdx.x / LANES;
+__global__ void __launch_bounds__(256) read_kernel(const ReadArgs a, const int rows) {
+  constexpr int CH = FP8 ? D / 16 : D / 8;     // 16-byte chunks of a cache row
+  constexpr int U = 4;
+  __shared__ RowPlace places[kRows];
   const CacheArgs& c = a.c;
-  for (int64_t r = (int64_t)blockIdx.x * rows; r < min((int64_t)(blockIdx.x + 1) * rows, c.N); ++r) {
-    const int b = request_of_row(c.cu, c.B, r);
-    if (b < 0) {
-      if (threadIdx.x == 0 && r < (int64_t)c.cu[c.B]) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
-      continue;
+  const int64_t r0 = (int64_t)blockIdx.x * rows;
+  const int here = (int)min((int64_t)rows, c.N - r0);
+  if ((int)threadIdx.x < here) places[threadIdx.x] = place_of(c, r0 + threadIdx.x, false, 0, 0);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (int64_t)c.cu[c.B] > c.N) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
+  __syncthreads();
+  const int kv = c.geo.kv_heads, per = 2 * kv * CH, items = here * per;
+  for (int i0 = threadIdx.x; i0 < items; i0 += U * 256) {
+    uint4 w[U];
+    float s[U];
+    T* out[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 256;
+      out[u] = nullptr;
+      w[u] = make_uint4(0, 0, 0, 0);
+      s[u] = 0.0f;
+      if (i >= items) continue;
+      const int in = i / per, at = i - in * per, hh = at / CH, ch = at % CH;
+      const RowPlace p = places[in];
+      if (!p.owned) continue;
+      const bool isk = hh < kv;
+      const int h = isk ? hh : hh - kv;
+      out[u] = static_cast<T*>(isk ? a.out_k : a.out_v) + ((r0 + in) * kv + h) * D + ch * (FP8 ? 16 : 8);
+      if (p.row < 0) continue;                 // a slot that the cache does not hold: zeros
+      const int64_t row = p.row + (int64_t)h * c.geo.page_size;
+      w[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(isk ? c.k : c.v) + row * (CH * 16)) + ch);
+      if constexpr (FP8) s[u] = __ldg((isk ? c.ks : c.vs) + row);
     }
-    const int64_t len = c.lengths[b];
-    const int64_t row0 =
-        len < 0 ? -1 : cache_row(c.geo, c.table + b * c.geo.table_stride, len + (r - c.cu[b]));
-    if (row0 < 0 && threadIdx.x == 0) atomicOr(c.err, SPECDEC_DEVERR_BAD_CACHE);
-    for (int hh = slot0; hh < 2 * c.geo.kv_heads; hh += SLOTS) {
-      const bool isk = hh < c.geo.kv_heads;
-      const int h = isk ? hh : hh - c.geo.kv_heads;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (row0 >= 0) {
-        const int64_t row = row0 + (int64_t)h * c.geo.page_size;
-        if constexpr (FP8) {
-          const uint2 e = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(isk ? c.k : c.v) + row * D) + chunk);
-          const float s = __ldg((isk ? c.ks : c.vs) + row);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!out[u]) continue;
+      if constexpr (FP8) {
+        const uint32_t e[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
           Vec8 x;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t half = (i < 2 ? e.x : e.y) >> ((i & 1) * 16);
-            const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(half & 0xFFFFu), __NV_E4M3);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t two = e[2 * z + (k >> 1)] >> ((k & 1) * 16);
+            const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3);
             const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&f));
-            x.x[2 * i] = g.x * s;
-            x.x[2 * i + 1] = g.y * s;
+            x.x[2 * k] = g.x * s[u];
+            x.x[2 * k + 1] = g.y * s[u];
           }
-          w = narrow<T>(x);
-        } else {
-          w = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(isk ? c.k : c.v) + row * D) + chunk);
+          reinterpret_cast<uint4*>(out[u])[z] = narrow<T>(x);
         }
+      } else {
+        *reinterpret_cast<uint4*>(out[u]) = w[u];
       }
-      T* out = static_cast<T*>(isk ? a.out_k : a.out_v) + (r * c.geo.kv_heads + h) * D;
-      reinterpret_cast<uint4*>(out)[chunk] = w;
     }
   }
 }
 
 // One block per request.  A thread owns 16 bytes of a head's row (or a scale)
-// and moves them for d = 0, 1, ... in order.  Paths rise (path[d] > path[d-1],
-// so path[d] >= d + 1): no row that is still to be read has been written.
+// and moves them for d = 0, 1, ... in order, four under way together.  Paths rise
+// (path[d] > path[d-1], so path[d] >= d + 1): no row that is still to be read has
+// been written.
 __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a, const int row_bytes) {
   const CacheArgs& c = a.c;
   const int b = blockIdx.x;
@@ -315,20 +355,42 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a, const i
   if (threadIdx.x == 0) a.out_lengths[b] = (int32_t)(len + (n ? 1 + acc : 0));
   if (!a.path) return;
   const int vecs = row_bytes / 16, per = 2 * vecs + (c.ks ? 2 : 0);
-  for (int t = threadIdx.x; t < c.geo.kv_heads * per; t += blockDim.x) {
-    const int h = t / per, w = t % per;
-    for (int d = 0; d < acc; ++d) {
+  constexpr int kMoves = 64;
+  __shared__ int64_t from[kMoves], to[kMoves];   // cache rows of head 0
+  for (int d0 = 0; d0 < acc; d0 += kMoves) {
+    const int moves = min(kMoves, acc - d0);
+    __syncthreads();
+    if ((int)threadIdx.x < moves) {
+      const int d = d0 + threadIdx.x;
       const int32_t at = a.path[first + d];
-      if (at == d + 1) continue;
-      const int64_t src = cache_row(c.geo, pages, len + at) + (int64_t)h * c.geo.page_size;
-      const int64_t dst = cache_row(c.geo, pages, len + d + 1) + (int64_t)h * c.geo.page_size;
-      if (w < 2 * vecs) {
-        uint4* base = static_cast<uint4*>(w < vecs ? c.k : c.v);
-        const int at16 = w < vecs ? w : w - vecs;
-        base[dst * vecs + at16] = base[src * vecs + at16];
-      } else {
-        float* s = w == 2 * vecs ? c.ks : c.vs;
-        s[dst] = s[src];
+      from[threadIdx.x] = cache_row(c.geo, pages, len + at);
+      to[threadIdx.x] = cache_row(c.geo, pages, len + d + 1);
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < c.geo.kv_heads * per; t += blockDim.x) {
+      const int h = t / per, w = t % per;
+      const int64_t head = (int64_t)h * c.geo.page_size;
+      constexpr int U = 4;
+      for (int m0 = 0; m0 < moves; m0 += U) {
+        if (w < 2 * vecs) {
+          uint4* base = static_cast<uint4*>(w < vecs ? c.k : c.v) + (w < vecs ? w : w - vecs);
+          uint4 x[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (m0 + u < moves) x[u] = base[(from[m0 + u] + head) * vecs];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (m0 + u < moves) base[(to[m0 + u] + head) * vecs] = x[u];
+        } else {
+          float* s = w == 2 * vecs ? c.ks : c.vs;
+          float x[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (m0 + u < moves) x[u] = s[from[m0 + u] + head];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (m0 + u < moves) s[to[m0 + u] + head] = x[u];
+        }
       }
     }
   }
@@ -350,10 +412,10 @@ int append_of(const AppendArgs& a, int num_sms, cudaStream_t st) {
 
 template <typename T, bool FP8>
 int read_of(const ReadArgs& a, int num_sms, cudaStream_t st) {
-  const int rows = rows_per_block(a.c.N, num_sms, 16);
+  const int rows = rows_per_block(a.c.N, num_sms, kRows);
   const int64_t grid = (a.c.N + rows - 1) / rows;
-  if (a.c.head_dim == 128) read_kernel<T, FP8, 128><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
-  else read_kernel<T, FP8, 64><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
+  if (a.c.head_dim == 128) read_kernel<T, FP8, 128><<<(unsigned)grid, 256, 0, st>>>(a, rows);
+  else read_kernel<T, FP8, 64><<<(unsigned)grid, 256, 0, st>>>(a, rows);
   return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 

@@ -11,8 +11,8 @@
 //
 // A request is a cluster of C CTAs.  Each warp of the cluster sums a contiguous
 // piece of the row; the piece sums meet in distributed shared memory (no
-// workspace, no atomics, a fixed order), and the warp whose piece holds the
-// crossing reads its piece again, from L2, to find the entry.
+// workspace, no atomics, a fixed order); the CTA whose piece holds the crossing
+// reads it again, from L2, first by warps and then entry by entry.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -160,7 +160,7 @@ __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
 }
 
 __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a) {
-  __shared__ double sums[2][kGivenWarps];
+  __shared__ double sums[2][kGivenWarps], parts[kGivenWarps];
   const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   const int b = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
     R.q = nullptr;
     R.drop = -1;
   }
+  cluster_sync_all();  // no CTA leaves while another may read its sums
   // ---- the crossing: one piece, the same choice in every warp --------------
   if (ok) {
     const double t = (double)__ldg(a.sample_u + b) * total;
@@ -252,14 +253,43 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
       if (some) heavy = c * 32 + 31 - __clz(some);
     }
     if (winner < 0) winner = heavy;   // s >= 1, or a sum that is not finite
-    if (total > 0.0 && winner == mine) {
+    if (total > 0.0 && winner >= 0 && winner / kGivenWarps == rank) {
+      // the CTA that owns it splits the piece over its warps once more, so that
+      // the last look through single entries is short
 #pragma unroll
       for (int c = 0; c < kMaxPieces / 32; ++c) {
-        const double e = __shfl_sync(0xFFFFFFFFu, end[c], (mine - 1) & 31);
-        if (mine > 0 && (mine - 1) / 32 == c) before = e;
+        const double e = __shfl_sync(0xFFFFFFFFu, end[c], (winner - 1) & 31);
+        if (winner > 0 && (winner - 1) / 32 == c) before = e;
       }
-      const int token = piece_find(R, v0, v1, before, t, lane);
-      if (lane == 0) a.out_tokens[d0 + b + n] = token;
+      const int p0 = min(a.V, winner * len), p1 = min(a.V, p0 + len);
+      const int len2 = ((len + kGivenWarps - 1) / kGivenWarps + 3) & ~3;
+      const int q0 = min(p1, p0 + warp * len2), q1 = min(p1, q0 + len2);
+      const double part = piece_sum(R, q0, q1, lane);
+      if (lane == 0) parts[warp] = part;
+      __syncthreads();
+      int pick = -1, some = -1;
+      double at = before, pick_at = before, some_at = before;
+#pragma unroll
+      for (int w = 0; w < kGivenWarps; ++w) {
+        const double y = parts[w];
+        if (y > 0.0) {
+          some = w;
+          some_at = at;
+          if (pick < 0 && t < at + y) {
+            pick = w;
+            pick_at = at;
+          }
+        }
+        at += y;
+      }
+      if (pick < 0) {   // rounding at the piece's very end
+        pick = some;
+        pick_at = some_at;
+      }
+      if (pick == warp) {
+        const int token = piece_find(R, q0, q1, pick_at, t, lane);
+        if (lane == 0) a.out_tokens[d0 + b + n] = token;
+      }
     }
     if (rank == 0) {
       if (tid == 0) {
@@ -269,7 +299,6 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
       for (int i = n + 1 + tid; i <= gamma; i += kGivenThreads) a.out_tokens[d0 + b + i] = -1;
     }
   }
-  cluster_sync_all();  // no CTA leaves while another may read its sums
 }
 
 }  // namespace

@@ -48,12 +48,12 @@ SPECDEC_HD int request_of_row(const int32_t* cu, int B, int64_t r) {
 // `pages`; head h lies h * page_size rows further.  -1 for a slot or a page
 // id outside the table or the cache: the caller skips the access.
 SPECDEC_HD int64_t cache_row(const PagedGeo& g, const int32_t* pages, int64_t slot) {
-  if (slot < 0) return -1;
-  const int64_t at = slot / g.page_size;
-  if (at >= g.max_pages) return -1;
+  if (slot < 0 || slot > 0xFFFFFFFFll) return -1;  // lengths and nodes are 32-bit
+  const uint32_t at = (uint32_t)slot / (uint32_t)g.page_size;
+  if (at >= (uint32_t)g.max_pages) return -1;
   const int64_t page = pages[at];
   if (page < 0 || page >= g.num_pages) return -1;
-  return page * g.kv_heads * g.page_size + (slot - at * g.page_size);
+  return page * g.kv_heads * g.page_size + ((uint32_t)slot - at * (uint32_t)g.page_size);
 }
 
 // Depth of node j below its request's node 0, from parents within the request
