@@ -213,23 +213,43 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, co
   for (int r = blockIdx.y * 8 + warp; r < (int)blockIdx.y * 8 + 8; r += 4) {
     const int row = rt * R + r;
     if (row >= rows) break;
-    auto slot_of = [&](int g) { return 2 * (int64_t)g + (range_begin(sh.total, ranges, g) > u0 ? 0 : 1); };
+    // range g0 left the item in its second slot, the others began inside it
+    const int64_t at0 = (2 * (int64_t)g0 + 1) * R + r;
+    auto at_of = [&](int g) { return g == g0 ? at0 : 2 * (int64_t)g * R + r; };
     float m = -INFINITY;
-    for (int g = g0 + lane; g <= g1; g += 32) m = fmaxf(m, part.stats[slot_of(g) * R + r].x);
+    for (int g = g0 + lane; g <= g1; g += 32) m = fmaxf(m, part.stats[at_of(g)].x);
     m = warp_max(m);
     const float ref = m == -INFINITY ? 0.0f : m;
     float l = 0.0f, acc[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = 0.0f;
-#pragma unroll 4
-    for (int g = g0; g <= g1; ++g) {
-      const int64_t slot = slot_of(g);
-      const float2 s = part.stats[slot * R + r];
-      const float w = ex2(s.x - ref);
-      const float* v = part.sums + (slot * R + r) * D + lane * PER;
-      l += s.y * w;
+    constexpr int U = 4;
+    for (int g = g0; g <= g1; g += U) {      // four partials' loads under way together
+      float2 s[U];
+      float v[U][PER];
 #pragma unroll
-      for (int k = 0; k < PER; ++k) acc[k] += s.x == -INFINITY ? 0.0f : v[k] * w;
+      for (int u = 0; u < U; ++u) {
+        s[u] = make_float2(-INFINITY, 0.0f);
+        if (g + u <= g1) {
+          const int64_t at = at_of(g + u);
+          s[u] = part.stats[at];
+          const float* p = part.sums + at * D + lane * PER;
+          if constexpr (PER == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p);
+            v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(p);
+            v[u][0] = x.x; v[u][1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float w = ex2(s[u].x - ref);
+        l += s[u].y * w;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) acc[k] += s[u].x == -INFINITY ? 0.0f : v[u][k] * w;
+      }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     T* out = static_cast<T*>(a.out) +

@@ -124,10 +124,38 @@ struct RowPlace {
   int32_t owned;      // the row belongs to a request
 };
 
-__device__ __forceinline__ RowPlace place_of(const CacheArgs& c, int64_t r, bool rotary, int rotary_dim, int64_t positions) {
+// Request of a block's first row, by a warp: 32 places of cu at a time (a thread's
+// bisection of 512 requests waits for 9 loads in a row).  -1: none.
+__device__ __forceinline__ int warp_request_of_row(const int32_t* cu, int B, int64_t r) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = B;          // cu[lo] <= r is looked for with the largest lo < hi
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const bool below = at < hi && (int64_t)__ldg(cu + at) <= r;
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, below);
+    const int last = who ? 31 - __clz(who) : 0;
+    hi = min(hi, lo + (last + 1) * step);
+    lo = lo + last * step;
+  }
+  return (int64_t)__ldg(cu + lo) <= r ? lo : -1;
+}
+
+// The request of row r, from that of an earlier row: the next few, or a bisection.
+__device__ __forceinline__ int request_from(const int32_t* cu, int B, int b, int64_t r) {
+  if (b >= 0) {
+    for (int i = 0; i < 8 && b < B; ++i, ++b) {
+      if ((int64_t)cu[b] > r) break;
+      if (r < (int64_t)cu[b + 1]) return b;
+    }
+  }
+  return request_of_row(cu, B, r);
+}
+
+__device__ __forceinline__ RowPlace place_of(const CacheArgs& c, int from, int64_t r, bool rotary, int rotary_dim,
+                                             int64_t positions) {
   RowPlace p = {-1, -1, 0};
   uint32_t bad = 0;
-  const int b = request_of_row(c.cu, c.B, r);
+  const int b = request_from(c.cu, c.B, from, r);
   if (b < 0) {  // rows behind the last request are not touched
     if (r < (int64_t)c.cu[c.B]) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
     return p;
@@ -164,7 +192,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
   const int d0 = chunk * 8;
   const int64_t r0 = (int64_t)blockIdx.x * rows;
   const int here = (int)min((int64_t)rows, c.N - r0);
-  if ((int)threadIdx.x < here) places[threadIdx.x] = place_of(c, r0 + threadIdx.x, a.rotary != nullptr, a.rotary_dim, a.positions);
+  if (threadIdx.x < 32) {
+    const int from = warp_request_of_row(c.cu, c.B, r0);
+    if ((int)threadIdx.x < here)
+      places[threadIdx.x] = place_of(c, from, r0 + threadIdx.x, a.rotary != nullptr, a.rotary_dim, a.positions);
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0 && (int64_t)c.cu[c.B] > c.N) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
   __syncthreads();
   const int kv = c.geo.kv_heads, total = 2 * kv + (a.q ? a.q_heads : 0);
@@ -172,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
     const RowPlace p = places[i];
     if (!p.owned) continue;
     const int64_t r = r0 + i;
-    const bool turned = p.turn >= 0 && d0 < a.rotary_dim;
+    const bool turned = p.turn >= 0 && d0 < a.rotary_dim, half_layout = p.turn >= 0 && !a.interleaved;
     float cs[8], sn[8];
     int partner = 0;
     float sign = 1.0f;
@@ -187,15 +219,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
         const bool low = d0 < half;
         load8(cosp + (low ? d0 : d0 - half), cs);
         load8(sinp + (low ? d0 : d0 - half), sn);
-        partner = low ? half : -half;
+        partner = (low ? half : -half) / 8;
         sign = low ? -1.0f : 1.0f;
       }
     }
     // heads in order: k, v, then q, SLOTS at a time; U steps' loads are under way
     // together, and every lane of a warp takes part in each step (row_amax)
-    constexpr int U = 3;
+    constexpr int U = 6;
+    const int other = (int)(threadIdx.x & 31 & ~(LANES - 1)) | (chunk + partner);   // lane of the pairs' other halves
     for (int h0 = 0; h0 < total; h0 += U * SLOTS) {
-      uint4 w[U], o[U];
+      uint4 w[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int hh = h0 + u * SLOTS + slot0;
@@ -205,7 +238,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
                          : isv ? static_cast<const T*>(a.v) + r * a.v_row + (hh - kv) * a.v_head
                                : static_cast<const T*>(a.q) + r * a.q_row + (hh - 2 * kv) * a.q_head;
           w[u] = __ldg(reinterpret_cast<const uint4*>(src + d0));
-          if (turned && !isv && !a.interleaved) o[u] = __ldg(reinterpret_cast<const uint4*>(src + d0 + partner));
+        } else {
+          w[u] = make_uint4(0, 0, 0, 0);
         }
       }
 #pragma unroll
@@ -213,9 +247,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
         if (h0 + u * SLOTS >= total) break;
         const int hh = h0 + u * SLOTS + slot0;
         const bool any = hh < total, isk = hh < kv, isv = !isk && hh < 2 * kv;
-        Vec8 x = {};
+        Vec8 x = widen<T>(w[u]);
+        uint4 o = w[u];
+        if (half_layout) {   // the same in the whole block
+          o.x = __shfl_sync(0xFFFFFFFFu, w[u].x, other);
+          o.y = __shfl_sync(0xFFFFFFFFu, w[u].y, other);
+          o.z = __shfl_sync(0xFFFFFFFFu, w[u].z, other);
+          o.w = __shfl_sync(0xFFFFFFFFu, w[u].w, other);
+        }
         if (any) {
-          x = widen<T>(w[u]);
           if (turned && !isv) {
             Vec8 y;
             if (a.interleaved) {
@@ -225,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
                 y.x[k + 1] = __fadd_rn(__fmul_rn(x.x[k + 1], cs[k]), __fmul_rn(x.x[k], sn[k]));
               }
             } else {
-              const Vec8 z = widen<T>(o[u]);
+              const Vec8 z = widen<T>(o);
 #pragma unroll
               for (int k = 0; k < 8; ++k)
                 y.x[k] = __fadd_rn(__fmul_rn(x.x[k], cs[k]), sign * __fmul_rn(z.x[k], sn[k]));
@@ -258,7 +298,10 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadArgs a, const int r
   const CacheArgs& c = a.c;
   const int64_t r0 = (int64_t)blockIdx.x * rows;
   const int here = (int)min((int64_t)rows, c.N - r0);
-  if ((int)threadIdx.x < here) places[threadIdx.x] = place_of(c, r0 + threadIdx.x, false, 0, 0);
+  if (threadIdx.x < 32) {
+    const int from = warp_request_of_row(c.cu, c.B, r0);
+    if ((int)threadIdx.x < here) places[threadIdx.x] = place_of(c, from, r0 + threadIdx.x, false, 0, 0);
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0 && (int64_t)c.cu[c.B] > c.N) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
   __syncthreads();
   const int kv = c.geo.kv_heads, per = 2 * kv * CH, items = here * per;
@@ -396,14 +439,16 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a, const i
   }
 }
 
-inline int rows_per_block(int64_t N, int num_sms, int most) {
-  const int64_t r = N / ((int64_t)num_sms * 16);
-  return (int)(r < 1 ? 1 : (r > most ? most : r));
+// Rows of a block: one wave of resident blocks where N allows (a block's look-ups
+// are a few dependent loads, whatever its rows).
+inline int rows_per_block(int64_t N, int num_sms, int resident) {
+  const int64_t r = (N + (int64_t)num_sms * resident - 1) / ((int64_t)num_sms * resident);
+  return (int)(r < 1 ? 1 : (r > kRows ? kRows : r));
 }
 
 template <typename T, bool FP8>
 int append_of(const AppendArgs& a, int num_sms, cudaStream_t st) {
-  const int rows = rows_per_block(a.c.N, num_sms, 4);
+  const int rows = rows_per_block(a.c.N, num_sms, 6);
   const int64_t grid = (a.c.N + rows - 1) / rows;
   if (a.c.head_dim == 128) append_kernel<T, FP8, 128><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
   else append_kernel<T, FP8, 64><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
@@ -412,7 +457,7 @@ int append_of(const AppendArgs& a, int num_sms, cudaStream_t st) {
 
 template <typename T, bool FP8>
 int read_of(const ReadArgs& a, int num_sms, cudaStream_t st) {
-  const int rows = rows_per_block(a.c.N, num_sms, kRows);
+  const int rows = rows_per_block(a.c.N, num_sms, 5);
   const int64_t grid = (a.c.N + rows - 1) / rows;
   if (a.c.head_dim == 128) read_kernel<T, FP8, 128><<<(unsigned)grid, 256, 0, st>>>(a, rows);
   else read_kernel<T, FP8, 64><<<(unsigned)grid, 256, 0, st>>>(a, rows);
