@@ -99,7 +99,7 @@ class KVCache:
         if k.shape[3] not in (64, 128):
             raise ValueError("head_dim must be 64 or 128")
         self.verifier, self.k, self.v, self.k_scale, self.v_scale = verifier, k, v, k_scale, v_scale
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.dtype, self._at = k.device, k.dtype, k.get_device()
         self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = k.shape
         self._c = specdec_cache_t(_ptr(k), _ptr(v), _ptr(k_scale) or None, _ptr(v_scale) or None,
                                   _DTYPE[k.dtype], self.num_kv_heads, self.head_dim,
@@ -119,35 +119,38 @@ class KVCache:
                    *(torch.ones(shape[:3], dtype=torch.float32, device=dev) for _ in range(2)))
 
     def _nodes(self, page_table, lengths, cu, parent, N):
-        dev, B = self.device, cu.numel() - 1
+        i32, at, B = torch.int32, self._at, cu.numel() - 1
         if B < 1 or lengths.numel() != B:
             raise ValueError("need cu of B + 1 >= 2 entries and B lengths")
-        for t, name in ((page_table, "page_table"), (lengths, "lengths"), (cu, "cu"),
-                        (parent, "node_parent")):
-            if t is not None and (t.dtype != torch.int32 or t.device != dev):
-                raise ValueError(f"{name} must be an int32 tensor on the device")
-        if not lengths.is_contiguous() or not cu.is_contiguous() \
-                or (parent is not None and (not parent.is_contiguous() or parent.numel() != N)):
-            raise ValueError("lengths, cu and node_parent (one entry per row) must be contiguous")
-        if page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1 \
-                or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        if page_table.dtype is not i32 or lengths.dtype is not i32 or cu.dtype is not i32 \
+                or page_table.get_device() != at or lengths.get_device() != at or cu.get_device() != at:
+            raise ValueError("page_table, lengths and cu must be int32 tensors on the device")
+        if not lengths.is_contiguous() or not cu.is_contiguous():
+            raise ValueError("lengths and cu must be contiguous")
+        if parent is not None and (parent.dtype is not i32 or parent.get_device() != at
+                                   or parent.numel() != N or not parent.is_contiguous()):
+            raise ValueError("node_parent must be a contiguous int32 tensor on the device, one entry per row")
+        if page_table.dim() != 2 or page_table.shape[0] != B:
+            raise ValueError("page_table must be [B, max_pages]")
+        most, (row, one) = page_table.shape[1], page_table.stride()
+        if most < 1 or (most > 1 and one != 1):
             raise ValueError("page_table must be [B, max_pages] with contiguous rows")
-        n = specdec_nodes_t(page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]),
-                            page_table.shape[1], lengths.data_ptr(), cu.data_ptr(),
-                            _ptr(parent) or None, B, N)
-        return ctypes.byref(n)
+        return ctypes.byref(specdec_nodes_t(page_table.data_ptr(), max(row, most), most, lengths.data_ptr(),
+                                            cu.data_ptr(), None if parent is None else parent.data_ptr() or None,
+                                            B, N))
 
     def _rows(self, t, N, heads, dtype, name):
         """Data pointer and strides of rows [N, heads, head_dim]."""
-        if t.dim() != 3 or t.shape[0] != N or t.shape[1] != heads or t.shape[2] != self.head_dim:
+        if t.shape != (N, heads, self.head_dim):
             raise ValueError(f"{name} must be [{N}, {heads}, {self.head_dim}]")
-        if t.dtype != dtype or t.device != self.device:
+        if t.dtype is not dtype or t.get_device() != self._at:
             raise ValueError(f"{name} must be {dtype} on the device")
         row, head, one = t.stride()
-        if one != 1 or row % 8 or head % 8 or t.data_ptr() % 16:
+        at = t.data_ptr()
+        if one != 1 or row % 8 or head % 8 or at % 16:
             raise ValueError(f"{name} needs contiguous values, 16-byte aligned rows and strides of "
                              "multiples of 8")
-        return t.data_ptr(), row, head
+        return at, row, head
 
     def _row_dtype(self, t):
         if t.dtype not in (torch.bfloat16, torch.float16) or (self.dtype != torch.float8_e4m3fn

@@ -556,8 +556,8 @@ int launch_warp(const AttendArgs& a, int num_sms, cudaStream_t st) {
   using L = WarpLayout<FP8, D, 16 * MT>;
   constexpr int TK = WarpTile<FP8, D>::TK;
   auto kern = attend_warp_kernel<T, FP8, D, MT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) != cudaSuccess)
-    return SPECDEC_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_shared(kern, L::BYTES, done)) return SPECDEC_ERR_CUDA;
   const int G = num_sms;
   kern<<<G, kThreads, L::BYTES, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;

@@ -19,6 +19,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/specdec.h"
 #include "cache.cuh"
 #include "device_common.cuh"
@@ -258,6 +260,19 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, co
     for (int k = 0; k < PER; k += 2)
       *reinterpret_cast<uint32_t*>(out + k) = pack2(acc[k] * inv, acc[k + 1] * inv, T());
   }
+}
+
+// Allows `kern` its dynamic shared memory on the current device, once for each
+// device (`done`: one word of device bits for each kernel).
+template <typename K>
+bool allow_shared(K kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_release);
+  return true;
 }
 
 // Queues the join as a dependent of the attention kernel before it.

@@ -1107,8 +1107,8 @@ template <typename T, bool FP8, int D>
 int launch_tile(const AttendArgs& a, int num_sms, cudaStream_t st) {
   auto kern = attend_tile_kernel<T, FP8, D>;
   constexpr int bytes = TileLayout<T, FP8, D>::BYTES;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return SPECDEC_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_shared(kern, bytes, done)) return SPECDEC_ERR_CUDA;
   // rows of a box: within one page, whole groups of 8 rows of the swizzle
   const int page = a.c.geo.page_size;
   int box = 128;

@@ -45,7 +45,12 @@ def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of the call below
+
+
 def _stream_handle(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -136,29 +141,25 @@ class Verifier:
         ``sample_uniforms`` [B] are float32 in [0, 1); probability rows may lie
         further apart than V; ``draft_probs`` None is a one-hot drafter.  beta is
         not computed (None)."""
-        dev = self.device
+        dev, i32, f32 = self.device, torch.int32, torch.float32
         B, nd = cu_num_draft_tokens.numel() - 1, draft_ids.numel()
-        for t, dt, name in ((draft_ids, torch.int32, "draft_ids"),
-                            (cu_num_draft_tokens, torch.int32, "cu_num_draft_tokens"),
-                            (accept_uniforms, torch.float32, "accept_uniforms"),
-                            (sample_uniforms, torch.float32, "sample_uniforms")):
-            if t.device != dev or t.dtype != dt or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {dt} tensor on the device")
-        if B < 1 or accept_uniforms.numel() != nd or sample_uniforms.numel() != B:
-            raise ValueError("need cu of B + 1 >= 2 entries, one accept uniform per draft and one "
-                             "sample uniform per request")
+        for t, dt, n, name in ((draft_ids, i32, nd, "draft_ids"),
+                               (cu_num_draft_tokens, i32, max(B, 1) + 1, "cu_num_draft_tokens"),
+                               (accept_uniforms, f32, nd, "accept_uniforms"),
+                               (sample_uniforms, f32, B, "sample_uniforms")):
+            if t.dtype is not dt or t.device != dev or t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of {n} entries on the device")
         V = target_probs.shape[-1]
         for t, rows, name in ((target_probs, nd + B, "target_probs"), (draft_probs, nd, "draft_probs")):
-            if t is not None and (t.device != dev or t.dtype != torch.float32 or t.dim() != 2
-                                  or t.shape[0] != rows or t.shape[1] != V
+            if t is not None and (t.dtype is not f32 or t.device != dev or t.shape != (rows, V)
                                   or (V > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < V)):
-                raise ValueError(f"{name} must be float32 rows [{rows}, V] on the device")
+                raise ValueError(f"{name} must be float32 rows [{rows}, {V}] on the device")
         if out is None:
-            out = VerifyOutput(tokens=torch.empty(nd + B, dtype=torch.int32, device=dev),
-                               num_accepted=torch.empty(B, dtype=torch.int32, device=dev), beta=None)
+            out = VerifyOutput(torch.empty(nd + B, dtype=i32, device=dev),
+                               torch.empty(B, dtype=i32, device=dev), None)
         else:
             for t, n in ((out.tokens, nd + B), (out.num_accepted, B)):
-                if t.device != dev or t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+                if t.device != dev or t.dtype is not i32 or t.numel() != n or not t.is_contiguous():
                     raise ValueError("out must hold contiguous int32 tokens [N_t] and num_accepted [B]")
         # with no draft rows at all an empty tensor still means "rows given"
         q = None if draft_probs is None else (_ptr(draft_probs) or self._empty.data_ptr())
