@@ -4,10 +4,10 @@
 // Only one target row (and, after a rejection, one draft row) of a request is
 // read in full: the accept tests need single entries.  The extra token is the
 // inverse of the cumulative weights, t = first v with C(v) > s C(V - 1), so the
-// sums decide a whole number and are held to about 2^-48: every lane keeps a
-// pair of floats (Knuth's two-sum gives each rounding error exactly), pairs
-// meet in double precision.  A double addition per entry instead would be
-// bound by the FP64 pipe, not by memory.
+// sums decide a whole number and are held to about 2^-44, as pairs of floats with
+// error-free additions (Knuth, Dekker).  Double precision would be bound by the
+// FP64 pipe (two lanes a clock here): even the scans over 64 piece sums and the
+// look through the last entries took longer in it than reading the rows.
 //
 // A request is a cluster of C CTAs.  Each warp of the cluster sums a contiguous
 // piece of the row; the piece sums meet in distributed shared memory (no
@@ -29,24 +29,74 @@ constexpr int kMaxCtas = 8;   // CTAs of a request (the portable cluster size)
 constexpr int kMaxPieces = kMaxCtas * kGivenWarps;
 constexpr int kStep = 128;   // entries a warp reads at once: 4 per lane
 
-struct Pair {  // hi + lo, |lo| at most a few roundings of hi
-  float hi, lo;
-};
-
-__device__ __forceinline__ void two_sum(Pair& s, float x) {
-  const float t = __fadd_rn(s.hi, x);
-  const float b = __fsub_rn(t, s.hi);
-  const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, b)), __fsub_rn(x, b));
-  s.hi = t;
-  s.lo = __fadd_rn(s.lo, e);
+// Two 32-bit operations in one instruction, each rounded as alone.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {   // a - b: a product with -1 is exact
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(0xBF800000BF800000ull), "l"(a));
+  return r;
 }
 
-// max(0, p - q) with the rounding error of the difference (0 where p <= q).
-// Entries that are not above 0 (NaN among them) weigh nothing.
+// Two running sums, each hi + lo with |lo| a few roundings of hi (Knuth's two-sum
+// gives the error of each addition exactly).
+struct Sums {
+  uint64_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add(uint64_t w) {
+    const uint64_t t = add2(hi, w), b = sub2(t, hi);
+    lo = add2(lo, add2(sub2(hi, sub2(t, b)), sub2(w, b)));
+    hi = t;
+  }
+};
+
+// A sum held as hi + lo, |lo| at most half a step of hi.
+struct Exact {
+  float hi, lo;
+};
+__device__ __forceinline__ Exact renormed(float s, float e) {   // |s| >= |e|
+  const float h = __fadd_rn(s, e);
+  return Exact{h, __fsub_rn(e, __fsub_rn(h, s))};
+}
+__device__ __forceinline__ Exact plus(Exact a, Exact b) {
+  const float s = __fadd_rn(a.hi, b.hi), z = __fsub_rn(s, a.hi);
+  float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, z)), __fsub_rn(b.hi, z));
+  e = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
+  return renormed(s, e);
+}
+__device__ __forceinline__ Exact scaled(Exact a, float s) {
+  const float p = __fmul_rn(a.hi, s);
+  return renormed(p, __fmaf_rn(a.lo, s, __fmaf_rn(a.hi, s, -p)));
+}
+__device__ __forceinline__ bool above(Exact a, Exact b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+__device__ __forceinline__ Exact shuffled(Exact a, int from) {
+  return Exact{__shfl_sync(0xFFFFFFFFu, a.hi, from), __shfl_sync(0xFFFFFFFFu, a.lo, from)};
+}
+__device__ __forceinline__ Exact scan_lanes(Exact x, int lane) {   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Exact up = shuffled(x, (lane - o) & 31);
+    if (lane >= o) x = plus(up, x);
+  }
+  return x;
+}
+
+// max(0, p - q) with the rounding error of the difference (0 where p <= q).  Where
+// p > q >= 0 the error is (p - d) - q, exactly (Dekker).  Entries that are not
+// above 0 (NaN among them) weigh nothing.
 __device__ __forceinline__ void weigh(float p, float q, float& w, float& e) {
   const float d = __fsub_rn(p, q);
-  const float b = __fsub_rn(d, p);
-  const float r = __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(q, b));
+  const float r = __fsub_rn(__fsub_rn(p, d), q);
   const bool on = d > 0.0f;
   w = on ? d : 0.0f;
   e = on ? r : 0.0f;
@@ -70,97 +120,146 @@ __device__ __forceinline__ void load4(const float* row, int v, int V, bool vec, 
   }
 }
 
-__device__ __forceinline__ void weights4(const Rows& R, int v, const float* p, const float* q,
-                                         float* w, float* e) {
+// One entry's weight and error.
+__device__ __forceinline__ void weight(const Rows& R, int v, float p, float q, float& w, float& e) {
+  weigh(p, R.q ? q : (v == R.drop ? 1.0f : 0.0f), w, e);
+}
+
+// Adds the weights of 4 entries of each of U steps.
+template <bool Q, bool WHOLE, int U>
+__device__ __forceinline__ void add_steps(const Rows& R, int base, int v1, int lane, Sums& s) {
+  float p[U][4], q[U][4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float qq = R.q ? q[k] : (v + k == R.drop ? 1.0f : 0.0f);
-    weigh(p[k], qq, w[k], e[k]);
+  for (int u = 0; u < U; ++u) {
+    const int v = base + u * kStep + lane * 4;
+    if constexpr (WHOLE) {
+      const float4 f = __ldcs(reinterpret_cast<const float4*>(R.p + v));
+      p[u][0] = f.x; p[u][1] = f.y; p[u][2] = f.z; p[u][3] = f.w;
+      if constexpr (Q) {
+        const float4 g = __ldcs(reinterpret_cast<const float4*>(R.q + v));
+        q[u][0] = g.x; q[u][1] = g.y; q[u][2] = g.z; q[u][3] = g.w;
+      }
+    } else if (v < v1) {
+      load4(R.p, v, v1, R.vec, p[u]);
+      if constexpr (Q) load4(R.q, v, v1, R.vec, q[u]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[u][k] = q[u][k] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if constexpr (!Q) {   // a one-hot drafter's entry: max(0, p - 1) in p's place
+      const int off = R.drop - (base + u * kStep + lane * 4);
+      if ((unsigned)off < 4u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k == off) p[u][k] = __fsub_rn(p[u][k], 1.0f);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      float w0, w1;
+      if constexpr (Q) {
+        const uint64_t p2 = pair(p[u][k], p[u][k + 1]), q2 = pair(q[u][k], q[u][k + 1]);
+        const uint64_t d2 = sub2(p2, q2);
+        float e0, e1;
+        unpair(d2, w0, w1);
+        unpair(sub2(sub2(p2, d2), q2), e0, e1);
+        e0 = w0 > 0.0f ? e0 : 0.0f;
+        e1 = w1 > 0.0f ? e1 : 0.0f;
+        s.lo = add2(s.lo, pair(e0, e1));
+      } else {
+        w0 = p[u][k];
+        w1 = p[u][k + 1];
+      }
+      s.add(pair(fmaxf(w0, 0.0f), fmaxf(w1, 0.0f)));   // fmaxf drops NaN
+    }
   }
 }
 
 // Sum of the weights of [v0, v1) (v0 a multiple of 4) over the warp.
-__device__ __forceinline__ double piece_sum(const Rows& R, int v0, int v1, int lane) {
-  Pair s = {0.0f, 0.0f};
+__device__ __forceinline__ Exact piece_sum(const Rows& R, int v0, int v1, int lane) {
+  Sums s;
   constexpr int U = 4;
-  for (int base = v0; base < v1; base += U * kStep) {
-    float p[U][4], q[U][4];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = base + u * kStep + lane * 4;
-      if (v < v1) {
-        load4(R.p, v, v1, R.vec, p[u]);
-        if (R.q) load4(R.q, v, v1, R.vec, q[u]);
-      } else {
-        p[u][0] = p[u][1] = p[u][2] = p[u][3] = 0.0f;
-        q[u][0] = q[u][1] = q[u][2] = q[u][3] = 0.0f;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float w[4], e[4];
-      weights4(R, base + u * kStep + lane * 4, p[u], q[u], w, e);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        two_sum(s, w[k]);
-        s.lo = __fadd_rn(s.lo, e[k]);
-      }
+  int base = v0;
+  if (R.vec) {   // whole steps: plain 16-byte loads, all under way before the first is used
+    if (R.q) {
+      for (; base + U * kStep <= v1; base += U * kStep) add_steps<true, true, U>(R, base, v1, lane, s);
+    } else {
+      for (; base + U * kStep <= v1; base += U * kStep) add_steps<false, true, U>(R, base, v1, lane, s);
     }
   }
-  double d = (double)s.hi + (double)s.lo;
+  if (R.q) {
+    for (; base < v1; base += U * kStep) add_steps<true, false, U>(R, base, v1, lane, s);
+  } else {
+    for (; base < v1; base += U * kStep) add_steps<false, false, U>(R, base, v1, lane, s);
+  }
+  float a, b, c, d;
+  unpair(s.hi, a, b);
+  unpair(s.lo, c, d);
+  Exact x = plus(renormed(a, c), renormed(b, d));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-  return d;
+  for (int o = 16; o > 0; o >>= 1) x = plus(x, shuffled(x, lane ^ o));
+  return x;
 }
 
 // First v of [v0, v1) whose cumulative weight (after `before`) is above t;
 // the last entry that weighs anything where rounding hides it.
-__device__ __forceinline__ int piece_find(const Rows& R, int v0, int v1, double before, double t, int lane) {
+__device__ __forceinline__ int piece_find(const Rows& R, int v0, int v1, Exact before, Exact t, int lane) {
   int last = v0;
-  for (int base = v0; base < v1; base += kStep) {
-    const int v = base + lane * 4;
-    float p[4] = {}, q[4] = {}, w[4], e[4];
-    if (v < v1) {
-      load4(R.p, v, v1, R.vec, p);
-      if (R.q) load4(R.q, v, v1, R.vec, q);
-    }
-    weights4(R, v, p, q, w, e);
-    double c[4], sum = 0.0;
-    int mine = -1;
+  constexpr int U = 4;
+  for (int base0 = v0; base0 < v1; base0 += U * kStep) {
+    float p[U][4], q[U][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      sum += (double)w[k] + (double)e[k];
-      c[k] = sum;
-      if (w[k] > 0.0f) mine = v + k;
-    }
-    double scan = sum;
+    for (int u = 0; u < U; ++u) {
+      const int v = base0 + u * kStep + lane * 4;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double up = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-      if (lane >= o) scan += up;
+      for (int k = 0; k < 4; ++k) p[u][k] = q[u][k] = 0.0f;
+      if (v < v1) {
+        load4(R.p, v, v1, R.vec, p[u]);
+        if (R.q) load4(R.q, v, v1, R.vec, q[u]);
+      }
     }
-    const double at = before + (scan - sum);
-    int hit = -1;
 #pragma unroll
-    for (int k = 3; k >= 0; --k)
-      if (w[k] > 0.0f && at + c[k] > t) hit = v + k;
-    const unsigned who = __ballot_sync(0xFFFFFFFFu, hit >= 0);
-    if (who) return __shfl_sync(0xFFFFFFFFu, hit, __ffs(who) - 1);
-    const unsigned some = __ballot_sync(0xFFFFFFFFu, mine >= 0);
-    if (some) last = __shfl_sync(0xFFFFFFFFu, mine, 31 - __clz(some));
-    before += __shfl_sync(0xFFFFFFFFu, scan, 31);
+    for (int u = 0; u < U; ++u) {
+      const int v = base0 + u * kStep + lane * 4;
+      if (base0 + u * kStep >= v1) break;
+      Exact c[4], sum = {0.0f, 0.0f};
+      float w[4], e[4];
+      int mine = -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        weight(R, v + k, p[u][k], q[u][k], w[k], e[k]);
+        sum = plus(sum, Exact{w[k], e[k]});
+        c[k] = sum;
+        if (w[k] > 0.0f) mine = v + k;
+      }
+      const Exact scan = scan_lanes(sum, lane);
+      Exact at = shuffled(scan, (lane - 1) & 31);
+      at = lane ? plus(before, at) : before;
+      int hit = -1;
+#pragma unroll
+      for (int k = 3; k >= 0; --k)
+        if (w[k] > 0.0f && above(plus(at, c[k]), t)) hit = v + k;
+      const unsigned who = __ballot_sync(0xFFFFFFFFu, hit >= 0);
+      if (who) return __shfl_sync(0xFFFFFFFFu, hit, __ffs(who) - 1);
+      const unsigned some = __ballot_sync(0xFFFFFFFFu, mine >= 0);
+      if (some) last = __shfl_sync(0xFFFFFFFFu, mine, 31 - __clz(some));
+      before = plus(before, shuffled(scan, 31));
+    }
   }
   return last;
 }
 
-__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
-  double d;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(d) : "r"(addr) : "memory");
-  return d;
+__device__ __forceinline__ Exact ld_cluster_sum(uint32_t addr) {
+  Exact x;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.hi), "=f"(x.lo) : "r"(addr) : "memory");
+  return x;
 }
 
 __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a) {
-  __shared__ double sums[2][kGivenWarps], parts[kGivenWarps];
+  __shared__ __align__(8) Exact sums[2][kGivenWarps], parts[kGivenWarps];
   const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   const int b = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -213,74 +312,75 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
   const int len = ((a.V + pieces - 1) / pieces + 3) & ~3;
   const int mine = rank * kGivenWarps + warp;
   const int v0 = min(a.V, mine * len), v1 = min(a.V, v0 + len);
-  double total = 0.0, x[kMaxPieces / 32], end[kMaxPieces / 32];
+  Exact total = {0.0f, 0.0f}, end[kMaxPieces / 32];
+  bool heavy_piece[kMaxPieces / 32];
   for (int round = 0; round < 2; ++round) {
-    const double own_sum = ok ? piece_sum(R, v0, v1, lane) : 0.0;
+    Exact own_sum = {0.0f, 0.0f};
+    if (ok) own_sum = piece_sum(R, v0, v1, lane);
     if (lane == 0) sums[round][warp] = own_sum;
     cluster_sync_all();
     // the same order in every warp: lane l holds pieces l and l + 32
-    total = 0.0;
+    total = Exact{0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < kMaxPieces / 32; ++c) {
+      end[c] = total;
+      heavy_piece[c] = false;
+      if (c * 32 >= pieces) continue;
       const int k = c * 32 + lane;
-      x[c] = 0.0;
+      Exact x = {0.0f, 0.0f};
       if (k < pieces)
-        x[c] = ld_cluster_f64(mapa(smem_addr(&sums[round][k % kGivenWarps]), k / kGivenWarps));
-      double scan = x[c];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-        if (lane >= o) scan += up;
-      }
-      end[c] = total + scan;
-      total += __shfl_sync(0xFFFFFFFFu, scan, 31);
+        x = ld_cluster_sum(mapa(smem_addr(&sums[round][k % kGivenWarps]), k / kGivenWarps));
+      heavy_piece[c] = x.hi > 0.0f;
+      const Exact scan = scan_lanes(x, lane);
+      end[c] = plus(total, scan);
+      total = shuffled(end[c], 31);
     }
-    if (total > 0.0 || !(R.q || R.drop >= 0)) break;   // the same in the whole cluster
+    if (total.hi > 0.0f || !(R.q || R.drop >= 0)) break;   // the same in the whole cluster
     R.q = nullptr;
     R.drop = -1;
   }
   cluster_sync_all();  // no CTA leaves while another may read its sums
   // ---- the crossing: one piece, the same choice in every warp --------------
   if (ok) {
-    const double t = (double)__ldg(a.sample_u + b) * total;
+    const Exact t = scaled(total, __ldg(a.sample_u + b));
     int winner = -1, heavy = -1;   // first piece that passes t; last one that weighs anything
-    double before = 0.0;
 #pragma unroll
     for (int c = 0; c < kMaxPieces / 32; ++c) {
-      const unsigned pass = __ballot_sync(0xFFFFFFFFu, x[c] > 0.0 && t < end[c]);
-      const unsigned some = __ballot_sync(0xFFFFFFFFu, x[c] > 0.0);
+      const unsigned pass = __ballot_sync(0xFFFFFFFFu, heavy_piece[c] && above(end[c], t));
+      const unsigned some = __ballot_sync(0xFFFFFFFFu, heavy_piece[c]);
       if (winner < 0 && pass) winner = c * 32 + __ffs(pass) - 1;
       if (some) heavy = c * 32 + 31 - __clz(some);
     }
     if (winner < 0) winner = heavy;   // s >= 1, or a sum that is not finite
-    if (total > 0.0 && winner >= 0 && winner / kGivenWarps == rank) {
+    if (total.hi > 0.0f && winner >= 0 && winner / kGivenWarps == rank) {
       // the CTA that owns it splits the piece over its warps once more, so that
       // the last look through single entries is short
+      Exact before = {0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < kMaxPieces / 32; ++c) {
-        const double e = __shfl_sync(0xFFFFFFFFu, end[c], (winner - 1) & 31);
+        const Exact e = shuffled(end[c], (winner - 1) & 31);
         if (winner > 0 && (winner - 1) / 32 == c) before = e;
       }
       const int p0 = min(a.V, winner * len), p1 = min(a.V, p0 + len);
       const int len2 = ((len + kGivenWarps - 1) / kGivenWarps + 3) & ~3;
       const int q0 = min(p1, p0 + warp * len2), q1 = min(p1, q0 + len2);
-      const double part = piece_sum(R, q0, q1, lane);
+      const Exact part = piece_sum(R, q0, q1, lane);
       if (lane == 0) parts[warp] = part;
       __syncthreads();
       int pick = -1, some = -1;
-      double at = before, pick_at = before, some_at = before;
+      Exact at = before, pick_at = before, some_at = before;
 #pragma unroll
       for (int w = 0; w < kGivenWarps; ++w) {
-        const double y = parts[w];
-        if (y > 0.0) {
+        const Exact y = parts[w], next = plus(at, y);
+        if (y.hi > 0.0f) {
           some = w;
           some_at = at;
-          if (pick < 0 && t < at + y) {
+          if (pick < 0 && above(next, t)) {
             pick = w;
             pick_at = at;
           }
         }
-        at += y;
+        at = next;
       }
       if (pick < 0) {   // rounding at the piece's very end
         pick = some;
@@ -294,7 +394,7 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
     if (rank == 0) {
       if (tid == 0) {
         a.out_nacc[b] = n;
-        if (!(total > 0.0)) a.out_tokens[d0 + b + n] = 0;   // a row without weight
+        if (!(total.hi > 0.0f)) a.out_tokens[d0 + b + n] = 0;   // a row without weight
       }
       for (int i = n + 1 + tid; i <= gamma; i += kGivenThreads) a.out_tokens[d0 + b + i] = -1;
     }
