@@ -256,8 +256,14 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
-  asm volatile("ld.shared.v2.u64 {%0,%1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+// 16 neighbouring floats in pairs, their loads under way together.
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t* f) {
+  asm volatile(
+      "ld.shared.v2.u64 {%0,%1}, [%8];\n\tld.shared.v2.u64 {%2,%3}, [%8+16];\n\t"
+      "ld.shared.v2.u64 {%4,%5}, [%8+32];\n\tld.shared.v2.u64 {%6,%7}, [%8+48];"
+      : "=l"(f[0]), "=l"(f[1]), "=l"(f[2]), "=l"(f[3]), "=l"(f[4]), "=l"(f[5]), "=l"(f[6]), "=l"(f[7])
+      : "r"(addr)
+      : "memory");
 }
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
@@ -603,6 +609,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       Segments& seg = segs[3 + loader];
       int skip = loader, t = seg.t0;            // tiles of others before this loader's next
       const uint32_t page_size = (uint32_t)c.geo.page_size;
+      const int page_bits = (page_size & (page_size - 1)) == 0 ? 31 - __clz((int)page_size) : -1;
       auto look = [&](Look& x) -> bool {        // this loader's next tile
         t += skip;
         while (seg.more && t >= seg.t1) {
@@ -620,7 +627,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         x.h = seg.h;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t at = first + i * 32 + lane, page = at / page_size;
+          const uint32_t at = first + i * 32 + lane;
+          const uint32_t page = page_bits >= 0 ? at >> page_bits : at / page_size;
           x.off[i] = (int)(at - page * page_size);
           x.id[i] = at < end ? __ldg(pages + page) : -2;    // end is within the table
         }
@@ -758,14 +766,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint32_t by = __shfl_sync(0xFFFFFFFFu, own, in);
           uint4 lo = times(make_uint4(e4m3x2_f16x2(w.x), e4m3x2_f16x2(w.x >> 16), e4m3x2_f16x2(w.y), e4m3x2_f16x2(w.y >> 16)), by);
           uint4 hi = times(make_uint4(e4m3x2_f16x2(w.z), e4m3x2_f16x2(w.z >> 16), e4m3x2_f16x2(w.w), e4m3x2_f16x2(w.w >> 16)), by);
-          if (dirty) {
-            if (!((live >> in) & 1u)) lo = hi = make_uint4(0, 0, 0, 0);
-            else if (in >= nodes) hit |= clear_nonfinite<E>(lo) | clear_nonfinite<E>(hi);
-          }
           sts128(dst + op_chunk(key, 2 * ch), lo);
           sts128(dst + op_chunk(key, 2 * ch + 1), hi);
         }
-      } else if (dirty && (nodes < 32 || live != 0xFFFFFFFFu)) {
+        __syncwarp();
+      }
+      if (dirty && (nodes < 32 || live != 0xFFFFFFFFu)) {
 #pragma unroll 1
         for (int i = 0; i < CH; ++i) {
           const int in = (lane & 7) + 8 * (i & 3), ch = (lane >> 3) + 4 * (i >> 2);
@@ -898,17 +904,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
             float s[64];
-            tc_ld64(ts + i * 64, s);
             float shift[2] = {0.0f, 0.0f};   // 8-bit caches: the values' exponents
             if constexpr (FP8) {
               shift[0] = sh.vexp[f][2 * i];
               shift[1] = sh.vexp[f][2 * i + 1];
+            }
+            tc_ld64(ts + i * 64, s);
+            if constexpr (FP8) {
 #pragma unroll
-              for (int k = 0; k < 64; k += 4) {
-                uint64_t f0, f1;
-                lds_pairs(fk_s + (i * 64 + k) * 4, f0, f1);
-                unpair(mul2(pair(s[k], s[k + 1]), f0), s[k], s[k + 1]);
-                unpair(mul2(pair(s[k + 2], s[k + 3]), f1), s[k + 2], s[k + 3]);
+              for (int k = 0; k < 64; k += 16) {
+                uint64_t f[8];
+                lds_pairs(fk_s + (i * 64 + k) * 4, f);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) unpair(mul2(pair(s[k + 2 * z], s[k + 2 * z + 1]), f[z]), s[k + 2 * z], s[k + 2 * z + 1]);
               }
             }
             const uint32_t see[2] = {i ? bits[2] : bits[0], i ? bits[3] : bits[1]};
