@@ -432,7 +432,7 @@ __device__ __noinline__ float left_out(const CacheArgs& c, const Segments& s, in
 
 template <typename T, bool FP8, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    attend_tile_kernel(const AttendArgs a, const int box, const __grid_constant__ CUtensorMap kmap,
+    attend_tile_kernel(const AttendArgs a, const int box, const bool grouped, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
   using L = TileLayout<T, FP8, D>;
   using E = typename std::conditional<FP8, __half, T>::type;
@@ -595,22 +595,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
       }
     } else {
-      // ---- loaders: a lane looks after keys lane, lane + 32, ... of a tile ------
+      // ---- loaders ----------------------------------------------------------------
+      // Pages that are a multiple of 32 slots (`grouped`): 32 keys from a multiple of
+      // 32 lie in one page, so lanes 0 .. 3 look up one page each and hold the cache
+      // row and the live keys of their 32; else a lane looks after keys lane, lane +
+      // 32, ...  (The common way is kept short: straight code that runs once a tile
+      // comes from beyond the instruction cache each time.)
       const int loader = warp - kLoadWarp;
-      struct Tile {
-        int row[4];       // cache row of the key, -1: none
-        uint32_t live[4]; // which of the 128 keys have one
-        bool dirty;
-      };
-      struct Look {       // page ids on their way
-        int id[4], off[4], h;
-        bool tail;        // the tile holds nodes
+      const uint32_t one = lane == 0 ? 1u : 0u;
+      const uint32_t page_size = (uint32_t)c.geo.page_size;
+      struct Place {
+        const int32_t* pages;
+        uint32_t first, len, end;
+        int h, id;
       };
       Segments& seg = segs[3 + loader];
       int skip = loader, t = seg.t0;            // tiles of others before this loader's next
-      const uint32_t page_size = (uint32_t)c.geo.page_size;
-      const int page_bits = (page_size & (page_size - 1)) == 0 ? 31 - __clz((int)page_size) : -1;
-      auto look = [&](Look& x) -> bool {        // this loader's next tile
+      auto go = [&](Place& x) -> bool {         // this loader's next tile
         t += skip;
         while (seg.more && t >= seg.t1) {
           const int over = t - seg.t1;
@@ -621,63 +622,60 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (!seg.more) return false;
         skip = kLoaders;
-        const int32_t* pages = c.table + seg.b * c.geo.table_stride;
-        const uint32_t len = (uint32_t)seg.q.len, end = len + (uint32_t)seg.q.n, first = (uint32_t)t * kTK;
-        x.tail = first + kTK > len;
+        x.pages = c.table + seg.b * c.geo.table_stride;
+        x.len = (uint32_t)seg.q.len;
+        x.end = x.len + (uint32_t)seg.q.n;      // within the table
+        x.first = (uint32_t)t * kTK;
         x.h = seg.h;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t at = first + i * 32 + lane;
-          const uint32_t page = page_bits >= 0 ? at >> page_bits : at / page_size;
-          x.off[i] = (int)(at - page * page_size);
-          x.id[i] = at < end ? __ldg(pages + page) : -2;    // end is within the table
-        }
+        x.id = -2;
+        const uint32_t at = x.first + lane * 32;
+        if (grouped && lane < 4 && at < x.end) x.id = __ldg(x.pages + at / page_size);
         return true;
       };
-      auto found = [&](const Look& l, Tile& x) {
-        uint32_t all = 0xFFFFFFFFu;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = l.id[i] >= 0 && l.id[i] < c.geo.num_pages;
-          if (!in && l.id[i] != -2) bad |= SPECDEC_DEVERR_BAD_CACHE;
-          // fewer than 2^31 rows in all
-          x.row[i] = in ? (l.id[i] * c.geo.kv_heads + l.h) * (int)page_size + l.off[i] : -1;
-          x.live[i] = __ballot_sync(0xFFFFFFFFu, in);
-          all &= x.live[i];
-        }
-        x.dirty = l.tail || all != 0xFFFFFFFFu;
+      // fewer than 2^31 rows in all; -1: the cache does not hold the slot
+      auto row_at = [&](const Place& x, int id, uint32_t at) -> int {
+        if (id >= 0 && id < c.geo.num_pages) return (id * c.geo.kv_heads + x.h) * (int)page_size + (int)(at % page_size);
+        if (id != -2) bad |= SPECDEC_DEVERR_BAD_CACHE;
+        return -1;
       };
       // The rows of a tile of the array `src` (16-bit, or 8-bit as it is) to `dst`;
       // every lane arrives on `bar` when its copies have landed.  A box lies within
       // one page: it is fetched if its first key lives, and what it brings of slots
       // behind the last key is hidden (keys) or taken out (values).
-      auto fetch = [&](uint32_t dst, const void* src, const CUtensorMap* map, const Tile& x, uint32_t bar) {
-        constexpr int LINE = FP8 ? D : 128, HALVES = FP8 ? 1 : D / 64, RC = FP8 ? D / 16 : D / 8;
-        if (box > 0) {
-          const uint32_t one = lane == 0 ? 1u : 0u;
-          // first keys of boxes among each 32: one bit for boxes of 32, one in some
-          // groups for larger ones
-          const uint32_t firsts = box >= 32 ? 1u : box == 16 ? 0x00010001u : 0x01010101u;
-          int count = 0;
+      constexpr int LINE = FP8 ? D : 128, HALVES = FP8 ? 1 : D / 64, RC = FP8 ? D / 16 : D / 8;
+      auto load_box = [&](uint32_t dst, const CUtensorMap* map, int r0, int row, uint32_t bar) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (box <= 32 || (i * 32) % box == 0) count += __popc(x.live[i] & firsts);
-          if (one) mbar_expect_tx(bar, count * box * HALVES * LINE);
-          __syncwarp();
+        for (int half = 0; half < HALVES; ++half)
+          box_load(dst + half * (kTK * 128) + r0 * LINE, map, half * 64, row, bar, one);
+      };
+      auto fetch_grouped = [&](uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+        const unsigned firsts = __ballot_sync(0xFFFFFFFFu, lane < 4 && (lane * 32) % box == 0 && row >= 0);
+        if (one) mbar_expect_tx(bar, __popc(firsts) * box * HALVES * LINE);
+        __syncwarp();
 #pragma unroll 1
-          for (int r0 = 0; r0 < kTK; r0 += box) {
-            const int i = r0 >> 5;
-            const int mine = i == 0 ? x.row[0] : i == 1 ? x.row[1] : i == 2 ? x.row[2] : x.row[3];
-            const int row = __shfl_sync(0xFFFFFFFFu, mine, r0 & 31);
-            if (row >= 0)
+        for (int i = 0; i < 4; ++i) {
+          const int r = __shfl_sync(0xFFFFFFFFu, row, i);
+          if ((firsts >> i) & 1u) load_box(dst, map, i * 32, r, bar);
+        }
+        mbar_arrive(bar);
+      };
+      auto fetch_any = [&](uint32_t dst, const void* src, const CUtensorMap* map, const int* row, uint32_t bar) {
+        const uint32_t firsts = box == 16 ? 0x00010001u : 0x01010101u;   // first keys of boxes among 32
+        int count = 0;
 #pragma unroll
-              for (int half = 0; half < HALVES; ++half)
-                box_load(dst + half * (kTK * 128) + r0 * LINE, map, half * 64, row, bar, one);
-          }
-        } else {
+        for (int i = 0; i < 4; ++i) count += __popc(__ballot_sync(0xFFFFFFFFu, row[i] >= 0) & firsts);
+        if (one && box > 0) mbar_expect_tx(bar, count * box * HALVES * LINE);
+        __syncwarp();
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int mine = i == 0 ? x.row[0] : i == 1 ? x.row[1] : i == 2 ? x.row[2] : x.row[3];
+        for (int i = 0; i < 4; ++i) {
+          const int mine = i == 0 ? row[0] : i == 1 ? row[1] : i == 2 ? row[2] : row[3];
+          if (box > 0) {
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += box) {
+              const int r = __shfl_sync(0xFFFFFFFFu, mine, r0);
+              if (r >= 0) load_box(dst, map, i * 32 + r0, r, bar);
+            }
+          } else {
 #pragma unroll 4
             for (int z = 0; z < RC; ++z) {
               const int y = z * 32 + lane, key = y / RC, ch = y % RC;
@@ -689,26 +687,66 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         copy_arrive(bar);
       };
-      Look ahead;
-      bool have = look(ahead);
+      Place ahead;
+      bool have = go(ahead);
       for (int n = loader; have; n += kLoaders) {
-        Tile now;
-        found(ahead, now);
-        have = look(ahead);
-        float ks[4], vs[4];
-        if constexpr (FP8) {
+        const Place now = ahead;
+        const bool tail = now.first + kTK > now.len;
+        int row = -1, rows[4] = {-1, -1, -1, -1};
+        uint32_t live = 0;                       // lanes 0 .. 3: of their 32 keys
+        if (grouped) {
+          const uint32_t at = now.first + lane * 32;
+          if (lane < 4) {
+            row = row_at(now, now.id, at);
+            if (row >= 0) live = now.end - at >= 32 ? 0xFFFFFFFFu : (1u << (now.end - at)) - 1u;
+          }
+        } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            ks[i] = now.row[i] >= 0 ? __ldg(c.ks + now.row[i]) : 0.0f;
-            vs[i] = now.row[i] >= 0 ? __ldg(c.vs + now.row[i]) : 0.0f;
+            const uint32_t at = now.first + i * 32 + lane;
+            rows[i] = row_at(now, at < now.end ? __ldg(now.pages + at / page_size) : -2, at);
+            const uint32_t l = __ballot_sync(0xFFFFFFFFu, rows[i] >= 0);
+            if (lane == i) live = l;
           }
         }
+        const bool dirty = tail || __any_sync(0xFFFFFFFFu, lane < 4 && live != 0xFFFFFFFFu);
+        // scales, 4 neighbouring keys a lane
+        float4 ks = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vs = ks;
+        uint32_t seen = 0;                       // which of the 4 live
+        if constexpr (FP8) {
+          const int sub = (lane & 7) * 4;
+          seen = __shfl_sync(0xFFFFFFFFu, live, lane >> 3) >> sub;
+          if (grouped) {
+            const int r = __shfl_sync(0xFFFFFFFFu, row, lane >> 3);
+            if (r >= 0) {
+              ks = __ldg(reinterpret_cast<const float4*>(c.ks + r + sub));
+              vs = __ldg(reinterpret_cast<const float4*>(c.vs + r + sub));
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              int r = -1;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int x = __shfl_sync(0xFFFFFFFFu, rows[i], sub + k);
+                if ((lane >> 3) == i) r = x;
+              }
+              (&ks.x)[k] = r >= 0 ? __ldg(c.ks + r) : 0.0f;
+              (&vs.x)[k] = r >= 0 ? __ldg(c.vs + r) : 0.0f;
+            }
+          }
+        }
+        have = go(ahead);
+        const uint32_t kdst = base_s + L::K + (n % L::KS) * L::KB, kbar = smem_addr(&sh.k_full[n % L::KS]);
+        const uint32_t vdst = base_s + (FP8 ? L::RAW + (n % L::RS) * L::RB : L::V + (n % L::VS) * L::VB);
+        const uint32_t vbar = smem_addr(&sh.raw_full[n % L::RS]);
         wait_free(sh.k_empty, L::KS, n);
-        fetch(base_s + L::K + (n % L::KS) * L::KB, c.k, &kmap, now, smem_addr(&sh.k_full[n % L::KS]));
+        if (grouped) fetch_grouped(kdst, &kmap, row, kbar);
+        else fetch_any(kdst, c.k, &kmap, rows, kbar);
         wait_free(sh.raw_empty, L::RS, n);
         if constexpr (!FP8) wait_free(sh.v_empty, L::VS, n);   // landing in place
-        fetch(base_s + (FP8 ? L::RAW + (n % L::RS) * L::RB : L::V + (n % L::VS) * L::VB), c.v, &vmap, now,
-              smem_addr(&sh.raw_full[n % L::RS]));
+        if (grouped) fetch_grouped(vdst, &vmap, row, vbar);
+        else fetch_any(vdst, c.v, &vmap, rows, vbar);
         // What the other roles need to know of the tile's keys.  8-bit caches: the
         // scale of K (applied to the scores, in 32 bits); the scale of V goes into
         // the widened values, as a factor v 2^-vexp that f16 holds: the largest of
@@ -717,20 +755,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // (Slot n % 8 is free: the slot waits above imply that the products of tile
         // n - 5 are done.)
         const int f = n % kFactSlots;
+        if (lane < 4) sh.live[f][lane] = live;
+        if (lane == 0) sh.dirty[f] = dirty;
+        if constexpr (FP8) {
+          float* kk = &ks.x;
+          float* vv = &vs.x;
+          uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (lane == 0) sh.live[f][i] = now.live[i];
-          if constexpr (FP8) {
-            const bool real = vs[i] > 0.0f && isfinite(vs[i]);
-            const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, real ? __float_as_uint(vs[i]) : 0u);
-            const int b = most ? min(max((int)(most >> 23) - 127 - 5, -80), 80) : 0;
-            if (lane == 0) sh.vexp[f][i] = (float)b;
-            const float factor = vs[i] * __uint_as_float((uint32_t)(127 - b) << 23);
-            reinterpret_cast<float*>(smem + L::KF)[f * kTK + i * 32 + lane] = ks[i];
-            reinterpret_cast<uint32_t*>(smem + L::VF)[f * kTK + i * 32 + lane] = pack2(factor, factor, __half());
+          for (int k = 0; k < 4; ++k) {
+            const bool in = (seen >> k) & 1u;
+            if (!in) kk[k] = vv[k] = 0.0f;
+            if (vv[k] > 0.0f && isfinite(vv[k])) most = max(most, __float_as_uint(vv[k]));
           }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+          const int b = most ? min(max((int)(most >> 23) - 127 - 5, -80), 80) : 0;
+          const float by = __uint_as_float((uint32_t)(127 - b) << 23);
+          if ((lane & 7) == 0) sh.vexp[f][lane >> 3] = (float)b;
+          reinterpret_cast<float4*>(smem + L::KF)[f * (kTK / 4) + lane] = ks;
+          reinterpret_cast<uint4*>(smem + L::VF)[f * (kTK / 4) + lane] =
+              make_uint4(pack2(vv[0] * by, vv[0] * by, __half()), pack2(vv[1] * by, vv[1] * by, __half()),
+                         pack2(vv[2] * by, vv[2] * by, __half()), pack2(vv[3] * by, vv[3] * by, __half()));
         }
-        if (lane == 0) sh.dirty[f] = now.dirty;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
       }
@@ -1122,10 +1168,13 @@ int launch_tile(const AttendArgs& a, int num_sms, cudaStream_t st) {
   int box = 128;
   while (box > 4 && page % box) box >>= 1;
   if (box < 8) box = 0;
+  // scales of 4 keys are read at once
+  const bool grouped = box >= 32 && (!FP8 || (reinterpret_cast<uintptr_t>(a.c.ks) % 16 == 0 && reinterpret_cast<uintptr_t>(a.c.vs) % 16 == 0));
+  if (!grouped && box > 16) box = 16;
   CUtensorMap kmap = {}, vmap = {};
   const int64_t rows = a.c.geo.num_pages * a.c.geo.kv_heads * page;
   if (box && (!encode_rows(&kmap, a.c.k, rows, D, box, FP8) || !encode_rows(&vmap, a.c.v, rows, D, box, FP8))) box = 0;
-  kern<<<num_sms, kTileThreads, bytes, st>>>(a, box, kmap, vmap);
+  kern<<<num_sms, kTileThreads, bytes, st>>>(a, box, grouped && box > 0, kmap, vmap);
   if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
   return launch_join<T, kR, kTK, D>(a, num_sms, st);
 }
