@@ -50,6 +50,7 @@ constexpr int kFinishWarps = 4;
 constexpr int kScoreWarp = 2 * kGroupWarps + kFinishWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kScoreWarp + 2;
 constexpr int kLoaders = 2;                          // loader l takes tiles l, l + 2, ... of the range
 constexpr int kTileThreads = (kScoreWarp + 4) * 32;    // a whole warpgroup: registers move between those
+constexpr int kW = 32;                               // scores of a row that a thread holds at once (64 took 4 % longer)
 constexpr int kFactSlots = 8;                        // tiles whose key facts are held (5 are needed)
 
 template <typename T, bool FP8, int D>
@@ -128,15 +129,6 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
 
 // Neighbouring columns of this thread's lane.  The wait stands in the same
 // statement, so that no use of the values can move before it.
-__device__ __forceinline__ void tc_ld64(uint32_t addr, float* x) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(x);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31]),"=r"(r[32]),"=r"(r[33]),"=r"(r[34]),"=r"(r[35]),"=r"(r[36]),"=r"(r[37]),"=r"(r[38]),"=r"(r[39]),"=r"(r[40]),"=r"(r[41]),"=r"(r[42]),"=r"(r[43]),"=r"(r[44]),"=r"(r[45]),"=r"(r[46]),"=r"(r[47]),"=r"(r[48]),"=r"(r[49]),"=r"(r[50]),"=r"(r[51]),"=r"(r[52]),"=r"(r[53]),"=r"(r[54]),"=r"(r[55]),"=r"(r[56]),"=r"(r[57]),"=r"(r[58]),"=r"(r[59]),"=r"(r[60]),"=r"(r[61]),"=r"(r[62]),"=r"(r[63])
-      : "r"(addr)
-      : "memory");
-}
 __device__ __forceinline__ void tc_ld32(uint32_t addr, float* x) {
   uint32_t* r = reinterpret_cast<uint32_t*>(x);
   asm volatile(
@@ -941,50 +933,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             masked |= lv != 0xFFFFFFFFu;
             bits[i] &= lv;
           }
-          // One pass over the scores, 64 keys at a time.  Weights are 2^(e - m),
+          // One pass over the scores, kW keys at a time.  Weights are 2^(e - m),
           // m a whole number that follows the running maximum only when that is
           // kLazy above it: what has been summed, the row's O_w and the tile's
           // weights so far are then multiplied by a power of two, which is exact.
           const uint32_t fk_s = base_s + L::KF + f * kTK * 4;
           const uint64_t rowf2 = pair(rowf, rowf);
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            float s[64];
-            float shift[2] = {0.0f, 0.0f};   // 8-bit caches: the values' exponents
-            if constexpr (FP8) {
-              shift[0] = sh.vexp[f][2 * i];
-              shift[1] = sh.vexp[f][2 * i + 1];
-            }
-            tc_ld64(ts + i * 64, s);
+          for (int i = 0; i < kTK / kW; ++i) {
+            float s[kW], shift = 0.0f;
+            if constexpr (FP8) shift = sh.vexp[f][i];   // 8-bit caches: the values' exponent
+            tc_ld32(ts + i * kW, s);
             if constexpr (FP8) {
 #pragma unroll
-              for (int k = 0; k < 64; k += 16) {
+              for (int k = 0; k < kW; k += 16) {
                 uint64_t f[8];
-                lds_pairs(fk_s + (i * 64 + k) * 4, f);
+                lds_pairs(fk_s + (i * kW + k) * 4, f);
 #pragma unroll
                 for (int z = 0; z < 8; ++z) unpair(mul2(pair(s[k + 2 * z], s[k + 2 * z + 1]), f[z]), s[k + 2 * z], s[k + 2 * z + 1]);
               }
             }
-            const uint32_t see[2] = {i ? bits[2] : bits[0], i ? bits[3] : bits[1]};
             if (masked) {
+              const uint32_t see = i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3];
 #pragma unroll
-              for (int k = 0; k < 64; ++k)
-                if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = -INFINITY;
+              for (int k = 0; k < kW; ++k)
+                if (!((see >> k) & 1u)) s[k] = -INFINITY;
             }
-            float mx[2];
+            float q[4];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float q[4];
+            for (int k = 0; k < 4; ++k) q[k] = fmaxf(s[2 * k], s[2 * k + 1]);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) q[k] = fmaxf(s[32 * y + 2 * k], s[32 * y + 2 * k + 1]);
+            for (int k = 8; k < kW; k += 8)
 #pragma unroll
-              for (int k = 8; k < 32; k += 8)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) q[x] = max3(q[x], s[32 * y + k + 2 * x], s[32 * y + k + 2 * x + 1]);
-              mx[y] = fmaxf(max3(q[0], q[1], q[2]), q[3]);
-              mx[y] = mx[y] == -INFINITY ? mx[y] : fmaf(mx[y], rowf, shift[y]);
-            }
-            const float most = fmaxf(mx[0], mx[1]);
+              for (int x = 0; x < 4; ++x) q[x] = max3(q[x], s[k + 2 * x], s[k + 2 * x + 1]);
+            const float mx = fmaxf(max3(q[0], q[1], q[2]), q[3]);
+            const float most = mx == -INFINITY ? mx : fmaf(mx, rowf, shift);
             const bool move = most > m + kLazy || (m == -INFINITY && most != -INFINITY);
             if (__any_sync(0xFFFFFFFFu, move)) {
               const float to_m = move ? ceilf(most) : m;
@@ -995,7 +978,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 l *= fix;
                 if (i > 0) {
 #pragma unroll 1
-                  for (int p = 0; p < 2; ++p) {
+                  for (int p = 0; p < i; ++p) {
                     uint32_t w16[16];
                     tc_ld16(ts + p * 16, w16);
 #pragma unroll
@@ -1018,30 +1001,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // weights, rounded to 16 bits for the product with V (half a step
             // each at most) and summed unrounded
             const float ref = (m == -INFINITY ? 0.0f : m) - kHead;
-            uint64_t sum[2][2] = {{0, 0}, {0, 0}};
+            const float add = shift - ref;
+            const uint64_t add_2 = pair(add, add);
+            uint64_t sum[2] = {0, 0};
+            uint32_t p[kW / 2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float add = shift[y] - ref;
-              const uint64_t add_2 = pair(add, add);
-              uint32_t p[16];
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                float e0, e1;
-                unpair(fma2(pair(s[32 * y + k], s[32 * y + k + 1]), rowf2, add_2), e0, e1);
-                e0 = ex2(e0);
-                e1 = ex2(e1);
-                sum[y][(k >> 1) & 1] = add2(sum[y][(k >> 1) & 1], pair(e0, e1));
-                p[k / 2] = pack2(e0, e1, E());
-              }
-              tc_st16(ts + i * 32 + y * 16, p);
+            for (int k = 0; k < kW; k += 2) {
+              float e0, e1;
+              unpair(fma2(pair(s[k], s[k + 1]), rowf2, add_2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(e0, e1));
+              p[k / 2] = pack2(e0, e1, E());
             }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float s0, s1;
-              unpair(add2(sum[y][0], sum[y][1]), s0, s1);
-              if constexpr (FP8) l = fmaf(s0 + s1, __uint_as_float((uint32_t)(127 - (int)shift[y]) << 23), l);
-              else l += s0 + s1;
-            }
+            tc_st16(ts + i * (kW / 2), p);
+            float s0, s1;
+            unpair(add2(sum[0], sum[1]), s0, s1);
+            if constexpr (FP8) l = fmaf(s0 + s1, __uint_as_float((uint32_t)(127 - (int)shift) << 23), l);
+            else l += s0 + s1;
           }
           tc_wait_st();
         }
