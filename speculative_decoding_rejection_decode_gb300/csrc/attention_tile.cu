@@ -69,8 +69,13 @@ struct TileLayout {
   static constexpr int RAW = V + VS * VB;
   static constexpr int KF = RAW + (FP8 ? RS * RB : 0);             // [slot][key] scale of the key
   static constexpr int VF = KF + (FP8 ? kFactSlots * kTK * 4 : 0);   // [slot][key] factor of the values (f16 pair)
+  // f16 rows over 8-bit caches: values are widened exactly (by a power of two) and
+  // the rest of their scale, in [1, 2), is applied to the weights in 32 bits; a
+  // rounded factor and product would add two errors of f16's own size to the result
+  static constexpr bool EXACT = FP8 && std::is_same<T, __half>::value;
+  static constexpr int MF = VF + (FP8 ? kFactSlots * kTK * 4 : 0);   // [slot][key] that rest
   static constexpr int STATS = Q;                      // over the queries, once a segment's products are done
-  static constexpr int BYTES = VF + (FP8 ? kFactSlots * kTK * 4 : 0) + 1024;   // and room to align
+  static constexpr int BYTES = MF + (EXACT ? kFactSlots * kTK * 4 : 0) + 1024;   // and room to align
 };
 
 struct TileShared {
@@ -743,7 +748,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // scale of K (applied to the scores, in 32 bits); the scale of V goes into
         // the widened values, as a factor v 2^-vexp that f16 holds: the largest of
         // 32 keys lies in [2^5, 2^6), so products stay below 2^15 and keys down to
-        // 2^-20 of the largest keep f16's full precision.
+        // 2^-20 of the largest keep f16's full precision (bf16 rows: the factor and
+        // its products with the values are rounded to f16, an eighth of what the
+        // result's own rounding is).
         // (Slot n % 8 is free: the slot waits above imply that the products of tile
         // n - 5 are done.)
         const int f = n % kFactSlots;
@@ -765,6 +772,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const float by = __uint_as_float((uint32_t)(127 - b) << 23);
           if ((lane & 7) == 0) sh.vexp[f][lane >> 3] = (float)b;
           reinterpret_cast<float4*>(smem + L::KF)[f * (kTK / 4) + lane] = ks;
+          if constexpr (L::EXACT) {
+            float rest[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t e = __float_as_uint(vv[k]) & 0x7F800000u;   // 2^exponent
+              const bool split = e != 0 && e != 0x7F800000u;
+              rest[k] = split ? vv[k] / __uint_as_float(e) : 1.0f;       // exact
+              if (split) vv[k] = __uint_as_float(e);
+            }
+            reinterpret_cast<float4*>(smem + L::MF)[f * (kTK / 4) + lane] = make_float4(rest[0], rest[1], rest[2], rest[3]);
+          }
           reinterpret_cast<uint4*>(smem + L::VF)[f * (kTK / 4) + lane] =
               make_uint4(pack2(vv[0] * by, vv[0] * by, __half()), pack2(vv[1] * by, vv[1] * by, __half()),
                          pack2(vv[2] * by, vv[2] * by, __half()), pack2(vv[3] * by, vv[3] * by, __half()));
@@ -1005,6 +1023,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const uint64_t add_2 = pair(add, add);
             uint64_t sum[2] = {0, 0};
             uint32_t p[kW / 2];
+            uint64_t rest[L::EXACT ? kW / 2 : 1];   // of the values' scales
+            if constexpr (L::EXACT) {
+              lds_pairs(base_s + L::MF + (f * kTK + i * kW) * 4, rest);
+              lds_pairs(base_s + L::MF + (f * kTK + i * kW) * 4 + 64, rest + 8);
+            }
 #pragma unroll
             for (int k = 0; k < kW; k += 2) {
               float e0, e1;
@@ -1012,6 +1035,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               e0 = ex2(e0);
               e1 = ex2(e1);
               sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(e0, e1));
+              if constexpr (L::EXACT) unpair(mul2(pair(e0, e1), rest[k / 2]), e0, e1);
               p[k / 2] = pack2(e0, e1, E());
             }
             tc_st16(ts + i * (kW / 2), p);

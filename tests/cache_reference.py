@@ -136,8 +136,12 @@ def attend_tolerance(step, want, big):
     head_dim 2^-24 sum |q k| scale <= 128 * 2^-24 * 30 = 2.3e-4 for these inputs
     (|q| < 7, |k| < 7 and sum |q k| / sqrt(head_dim) < 30), with the exponential's
     own error of 2^-21 far below; the sums over up to 2^11 keys in float32 add
-    2^-13 V at most.  The result is rounded to its type."""
+    2^-13 V at most.  bf16 rows over 8-bit caches may scale the values in f16, the
+    factor and each product rounded: half a step of f16 each.  The result is rounded
+    to its type."""
     weight = HALF_STEP[torch.float16 if step.ks is not None else step.dtype]
+    if step.ks is not None and step.dtype == torch.bfloat16:
+        weight += 2 * HALF_STEP[torch.float16]
     return (weight + 2 * 2.3e-4 + 2.0 ** -13) * big[..., None] + HALF_STEP[step.dtype] * want.abs() + 1e-30
 
 
