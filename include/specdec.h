@@ -328,7 +328,8 @@ typedef struct specdec_nodes {
  * A cu range that is malformed or passes N (SPECDEC_DEVERR_BAD_CU), a negative
  * length, a slot or page outside the table or the cache, a position outside the
  * rotary table (SPECDEC_DEVERR_BAD_CACHE) or a malformed tree
- * (SPECDEC_DEVERR_BAD_TREE) set bits of the handle's error word; nothing outside
+ * (SPECDEC_DEVERR_BAD_TREE, where the tree matters: rotary positions, attention,
+ * commit) set bits of the handle's error word; nothing outside
  * the arrays is touched, and what such a node would have written is left alone
  * unless stated below.  Rows behind the last request are left as they were.  The
  * calls use none of the handle's workspace, so calls on one handle may overlap
@@ -338,7 +339,7 @@ typedef struct specdec_nodes {
  * nodes' positions on the way.
  *   k, v       [N, num_kv_heads, head_dim]
  *   q          [N, q_heads, head_dim] or NULL; out_q receives the turned rows,
- *              contiguous (both or neither; a row whose position is outside the
+ *              contiguous, and may be q itself (both or neither; a row whose position is outside the
  *              table or whose tree is malformed becomes zeros)
  *   rotary     device float32 [rotary_positions, 2, rotary_dim / 2], cos then sin
  *              of each position, or NULL (q is then copied)
@@ -370,13 +371,16 @@ int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
  * and its ancestors and itself (which append has written):
  *   out[i, h] = sum_s softmax_s(softmax_scale q[i, h] . k[s, h / (q_heads /
  *   num_kv_heads)]) v[s, same]
- * q [N, q_heads, head_dim] strided, out contiguous [N, q_heads, head_dim].
+ * q [N, q_heads, head_dim] strided, out contiguous [N, q_heads, head_dim], which
+ * must not overlap q.
  * q_heads is a multiple of num_kv_heads.  Scores, maxima and sums are held in 32
  * bits; weights meet the values rounded to 16 bits (to f16 over e4m3 caches).
  * Keys in slots that the cache does not hold count as hidden (BAD_CACHE); a row
  * that sees no key is zeros.  What a masked slot holds, infinities and NaN
  * among it, reaches no row.  Requests whose cu, length or tree is out of range
- * write nothing.
+ * write nothing, and neither do those of 2^31 or more tiles of 128 rows x 128 keys
+ * (SPECDEC_DEVERR_BAD_CACHE).  Waits inside the kernel are bounded: one that runs out
+ * sets SPECDEC_DEVERR_TIMEOUT, and the call's outputs are then undefined.
  *   workspace  device memory of at least specdec_tree_attention_workspace()
  *              bytes, 16-byte aligned, no initial contents; calls that may
  *              overlap need one each */

@@ -65,6 +65,15 @@ def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0,
     return out
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the spans of memory of two tensors meet."""
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
 class KVCache:
     """Keys and values of one layer in pages, over a Verifier's handle.
 
@@ -167,7 +176,8 @@ class KVCache:
         and head strides) behind the context: node j of request b into slot
         lengths[b] + j.  With ``rotary`` (``rotary_table``) k and q are turned to
         position lengths[b] + depth(j) first, in pairs (i, i + rotary_dim / 2) or,
-        interleaved, (2i, 2i + 1).  Returns the turned q (contiguous), or None."""
+        interleaved, (2i, 2i + 1).  Returns the turned q (contiguous; ``out_q`` may be
+        q itself), or None."""
         N = k.shape[0]
         dt = self._row_dtype(k)
         kp = self._rows(k, N, self.num_kv_heads, k.dtype, "k")
@@ -244,6 +254,9 @@ class KVCache:
         elif out.shape != q.shape or out.dtype != q.dtype or out.device != self.device \
                 or not out.is_contiguous():
             raise ValueError("out must be contiguous and like q")
+        elif N and out.untyped_storage().data_ptr() == q.untyped_storage().data_ptr() \
+                and _overlap(out, q):
+            raise ValueError("out must not overlap q")
         if N:
             h = self.verifier.handle
             need = specdec_tree_attention_workspace(h, self._ref, cu_num_nodes.numel() - 1, N, heads)

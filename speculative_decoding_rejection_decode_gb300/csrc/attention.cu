@@ -1,7 +1,7 @@
 // Attention of drafted nodes (chains and token trees) over the paged cache.
 // Contract in include/specdec.h (specdec_tree_attention).
 //
-// attend_warp_kernel: few rows per request (up to 32 a tile).  The pass is
+// attend_warp_kernel: few rows per request (16 a tile).  The pass is
 // bound by reading the cache once; each warp streams its own 16 or 32 keys of
 // a tile through a ring in shared memory (asynchronous 16-byte copies, three
 // blocks deep, no block-wide barrier), keeps the running maximum, sum and
@@ -569,7 +569,12 @@ int launch_warp(const AttendArgs& a, int num_sms, cudaStream_t st) {
 int64_t average_rows(int B, int64_t N, int kv_heads, int q_heads) {
   return (N + B - 1) / B * (q_heads / kv_heads);
 }
-constexpr int kWarpRows = 16;   // up to these the warp kernel, above them the tile kernel
+// Up to these the warp kernel, above them the tile kernel.  4 rows, contexts of 500
+// / 64 up to 8191 / 4 of 30000, 8 kv heads of 128, us a call, warp and tile kernel:
+// bf16 12.7 and 15.1 / 220 and 222 / 89 and 92, e4m3 13.8 and 15.8 / 208 and 249 /
+// 81 and 90; 16 rows: bf16 14.8 and 15.8 / 241 and 228 / 93 and 94, e4m3 15.4 and
+// 16.6 / 220 and 259 / 84 and 94.
+constexpr int kWarpRows = 16;
 
 template <typename T, bool FP8>
 int launch_dim(const AttendArgs& a, int num_sms, cudaStream_t st) {

@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                        (int64_t)(seg.h * group + gr % group) * a.q_head + ch * 8;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (live) v = __ldg(reinterpret_cast<const uint4*>(src));
-        float f = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);   // above 0: hidden keys are -inf times this
+        float f = fabsf(a.scale_log2);
         if constexpr (FP8) {
           // the row is scaled by a power of two so that its largest value lies in
           // [2^7, 2^8), below e4m3's 448; the scores take the factor back
@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           v.w ^= 0x80008000u;
         }
         if constexpr (!FP8) sts128(base_s + L::Q + op_chunk(r, ch), v);
-        if (ch == 0) sh.rowf[r] = f;
+        if (ch == 0) sh.rowf[r] = fmaxf(f, 1.17549435e-38f);   // above 0: hidden keys are -inf times this
       }
       fence_async_proxy();
       __syncwarp();

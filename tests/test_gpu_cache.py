@@ -317,7 +317,8 @@ ATTEND = [
 
 
 @pytest.mark.parametrize("case", range(len(ATTEND)))
-@pytest.mark.parametrize("dtype,cache,head_dim", [(BF, BF, 128), (HF, HF, 64), (BF, E4, 128), (HF, E4, 64), (HF, HF, 128), (BF, BF, 64)])
+@pytest.mark.parametrize("dtype,cache,head_dim", [(BF, BF, 128), (HF, HF, 64), (BF, E4, 128), (HF, E4, 64), (HF, HF, 128), (BF, BF, 64),
+                                                  (HF, E4, 128), (BF, E4, 64)])
 def test_attend(V, case, dtype, cache, head_dim):
     s = Step(**ATTEND[case], dtype=dtype, cache=cache, head_dim=head_dim, seed=case, extra_rows=1)
     out = torch.full((s.N, s.heads, head_dim), 7.0, dtype=dtype, device="cuda")
@@ -340,6 +341,83 @@ def test_attend_scale_strides_and_repeat(V):
     assert ((got.double() - want).abs() <= attend_tolerance(s, want, big)).all()
     for _ in range(3):      # the same bits every time
         assert torch.equal(got, s.cache(V).attend(s.q, table[:, :40], s.lengths, s.cu, s.parent, scale=0.05))
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+@pytest.mark.parametrize("nodes", [2, 9])
+@pytest.mark.parametrize("scale", [0.0, -0.07, 1e-30])
+def test_attend_odd_scales(V, cache, nodes, scale):
+    s = Step(ctx=[300, 40], nodes=[nodes, nodes], tree="star", cache=cache, seed=4)
+    got = s.cache(V).attend(s.q, *args(s), scale=scale)
+    want, big = s.attend(scale=scale)
+    assert V.get_error() == 0
+    assert ((got.double() - want).abs() <= attend_tolerance(s, want, big)).all()
+
+
+@pytest.mark.parametrize("nodes", [2, 9])
+@pytest.mark.parametrize("power", [-120, 100])
+def test_attend_queries_of_any_size(V, nodes, power):
+    # 8-bit caches: the kernels scale a query row by a power of two
+    s = Step(ctx=[300, 40], nodes=[nodes, nodes], cache=E4, seed=5)
+    s.q *= 2.0 ** power
+    got = s.cache(V).attend(s.q, *args(s), scale=2.0 ** (-3.5 - power) if power > 0 else None)
+    want, big = s.attend(scale=2.0 ** (-3.5 - power) if power > 0 else None)
+    assert ((got.double() - want).abs() <= attend_tolerance(s, want, big)).all()
+
+
+@pytest.mark.parametrize("nodes", [1, 12])
+@pytest.mark.parametrize("page", [64, 40])
+def test_attend_scales_off_16_bytes(V, nodes, page):
+    s = Step(ctx=[700, 90], nodes=[nodes, nodes], cache=E4, page=page, seed=6)
+    want = s.cache(V).attend(s.q, *args(s))
+    for name in ("ks", "vs"):
+        flat = torch.empty(getattr(s, name).numel() + 1, device="cuda")[1:]
+        flat.copy_(getattr(s, name).reshape(-1))
+        setattr(s, name, flat.view(s.ks.shape) if name == "ks" else flat.view(s.k.shape[:3]))
+    assert torch.equal(s.cache(V).attend(s.q, *args(s)), want)
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+@pytest.mark.parametrize("nodes", [1, 7])
+def test_attend_many_requests(V, cache, nodes):
+    # more requests than CTAs, some without nodes or context
+    rng = np.random.default_rng(2)
+    ctx = [int(x) for x in rng.integers(0, 400, 400)]
+    ctx[5] = ctx[399] = 0
+    n = [0 if i % 17 == 3 else nodes for i in range(400)]
+    s = Step(ctx=ctx, nodes=n, kv_heads=2, group=4, head_dim=64, page=32, cache=cache, seed=7)
+    got = s.cache(V).attend(s.q, *args(s))
+    want, big = s.attend()
+    assert V.get_error() == 0
+    assert ((got.double() - want).abs() <= attend_tolerance(s, want, big)).all()
+
+
+def test_attend_far_contexts(V):
+    # one request over 70000 keys: every range of the work holds a part of it
+    s = Step(ctx=[70000], nodes=[6], kv_heads=1, group=8, page=64, seed=8)
+    got = s.cache(V).attend(s.q, *args(s))
+    want, big = s.attend()
+    # float32 sums over 2^17 keys instead of the bound's 2^11: 2^6 times its 2^-13
+    tol = attend_tolerance(s, want, big) + (2.0 ** -7 - 2.0 ** -13) * big[..., None]
+    assert ((got.double() - want).abs() <= tol).all()
+    # and on average far below: weights rounded at random
+    assert float((got.double() - want).norm() / want.norm()) < 2 * 2.0 ** -8
+
+
+def test_outputs_in_place_and_overlapping(V):
+    from speculative_decoding_rejection_decode_gb300 import rotary_table
+    table = rotary_table(600, 128)
+    for inter in (False, True):
+        s = Step(ctx=[500, 3], nodes=[9, 30], tree="random", seed=9)
+        want = s.cache(V).append(s.new_k, s.new_v, *args(s), q=s.q, rotary=table, interleaved=inter)
+        got = s.cache(V).append(s.new_k, s.new_v, *args(s), q=s.q, rotary=table, interleaved=inter, out_q=s.q)
+        assert got is s.q and torch.equal(got, want)
+    with pytest.raises(ValueError):
+        s.cache(V).attend(s.q, *args(s), out=s.q)
+    wide = torch.zeros(2 * s.N, s.heads, 128, dtype=BF, device="cuda")
+    with pytest.raises(ValueError):
+        s.cache(V).attend(wide[1:s.N + 1], *args(s), out=wide[:s.N])
+    s.cache(V).attend(wide[:s.N], *args(s), out=wide[s.N:])      # side by side is fine
 
 
 @pytest.mark.parametrize("cache", [BF, E4])
