@@ -390,10 +390,10 @@ int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
                            float softmax_scale, void* out, void* workspace,
                            int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of specdec_tree_attention for any lengths, or a negative
- * status. */
+/* Workspace bytes of specdec_tree_attention for any lengths that max_pages hold
+ * (0 for small calls, whose workspace may be NULL), or a negative status. */
 int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache_t* cache,
-                                         int B, int64_t N, int q_heads);
+                                         int B, int64_t N, int q_heads, int max_pages);
 
 /* After the verification: moves the accepted nodes' rows (and scales) to the
  * slots behind the root, lengths[b] + path[d] -> lengths[b] + 1 + d, and writes

@@ -108,7 +108,7 @@ _cp, _np = ctypes.POINTER(specdec_cache_t), ctypes.POINTER(specdec_nodes_t)
 _append = _fn("specdec_cache_append", _i32, _vp, _cp, _np, _i32, _vp, _i64, _i64, _vp, _i64, _i64,
               _vp, _i64, _i64, _i32, _vp, _vp, _i32, _i64, _i32, _vp)
 _read = _fn("specdec_cache_read", _i32, _vp, _cp, _np, _i32, _vp, _vp, _vp)
-_attn_ws = _fn("specdec_tree_attention_workspace", _i64, _vp, _cp, _i32, _i64, _i32)
+_attn_ws = _fn("specdec_tree_attention_workspace", _i64, _vp, _cp, _i32, _i64, _i32, _i32)
 _attn = _fn("specdec_tree_attention", _i32, _vp, _cp, _np, _i32, _vp, _i64, _i64, _i32, _f32, _vp,
             _vp, _i64, _vp)
 _commit = _fn("specdec_cache_commit", _i32, _vp, _cp, _np, _vp, _vp, _vp, _vp)
@@ -171,8 +171,8 @@ def specdec_cache_read(h, cache, nodes, dtype, out_k, out_v, stream) -> int:
     return _read(h, cache, nodes, dtype, out_k, out_v, stream)
 
 
-def specdec_tree_attention_workspace(h, cache, B, N, q_heads) -> int:
-    return _attn_ws(h, cache, B, N, q_heads)
+def specdec_tree_attention_workspace(h, cache, B, N, q_heads, max_pages) -> int:
+    return _attn_ws(h, cache, B, N, q_heads, max_pages)
 
 
 def specdec_tree_attention(h, cache, nodes, dtype, q, q_row_stride, q_head_stride, q_heads,

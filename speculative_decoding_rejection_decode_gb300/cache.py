@@ -259,13 +259,14 @@ class KVCache:
             raise ValueError("out must not overlap q")
         if N:
             h = self.verifier.handle
-            need = specdec_tree_attention_workspace(h, self._ref, cu_num_nodes.numel() - 1, N, heads)
+            need = specdec_tree_attention_workspace(h, self._ref, cu_num_nodes.numel() - 1, N, heads,
+                                                    page_table.shape[1])
             if need < 0:
                 _check(need, "specdec_tree_attention_workspace")
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
             _check(specdec_tree_attention(h, self._ref, nodes, dt, *qp, heads,
                                           self.head_dim ** -0.5 if scale is None else float(scale),
-                                          out.data_ptr(), ws.data_ptr(), need,
+                                          out.data_ptr(), _ptr(ws) or None, need,
                                           _stream_handle(self.device)), "specdec_tree_attention")
         return out
 

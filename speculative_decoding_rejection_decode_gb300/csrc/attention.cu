@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
   const int G = gridDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.q_heads / c.geo.kv_heads;
-  const PlanArgs plan(c, group);
+  const PlanArgs plan(a);
   uint32_t why = 0;
   int64_t u0 = 0;
   find_unit<kThreads>(plan, R, TK,
@@ -171,13 +171,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
       if (++b >= c.B) return;   // lengths that changed under the call
       q = attend_request(plan, b, R, TK, ignored);
     }
-    const int64_t item = (u - base) / (q.tiles + kItemCost);
-    const int at = (int)((u - base) % (q.tiles + kItemCost));
+    const int cost = (a.whole ? 1 : q.tiles) + kItemCost;
+    const int64_t item = (u - base) / cost;
+    const int at = (int)((u - base) % cost);
     const int t0 = max(at - kItemCost, 0);
-    const int t1 = (int)min((int64_t)q.tiles, at - kItemCost + (uend - u));
+    int t1 = (int)min((int64_t)(cost - kItemCost), at - kItemCost + (uend - u));
     const int h = (int)(item / q.rts), rt = (int)(item % q.rts);
-    u += q.tiles + kItemCost - at;
+    u += cost - at;
     if (t1 <= t0) continue;
+    if (a.whole) t1 = q.tiles;
     const bool whole = t0 == 0 && t1 == q.tiles;
     const int rows = min(R, q.n * group - rt * R);            // rows of this tile
     const int node0 = rt * R / group;                          // its first node
@@ -185,8 +187,47 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
     const int32_t* parent = c.parent ? c.parent + q.first : nullptr;
     const int words = (q.n + 31) >> 5;
 
-    // ---- queries: shared memory, as the products want them ------------------
     __syncthreads();   // the last segment's readers are done
+    // ---- the warp's blocks: tile t, keys [t TK + warp KB, + KB) --------------
+    const int64_t all_keys = (int64_t)q.len + q.n;
+    auto row_of = [&](int t) -> int {   // cache row of this lane's key of block t, -1: none
+      const int64_t s = (int64_t)t * TK + warp * KB + lane;
+      if (t >= t1 || lane >= KB || s >= all_keys) return -1;
+      const int64_t r = cache_row(c.geo, pages, s);
+      if (r < 0) {
+        bad |= SPECDEC_DEVERR_BAD_CACHE;
+        return -1;
+      }
+      return (int)(r + (int64_t)h * c.geo.page_size);
+    };
+    auto issue = [&](int t, int row) {
+      const uint32_t st = ring_s + ((t - t0) % kStages) * W::STAGE;
+      if (t < t1) {
+#pragma unroll
+        for (int i = 0; i < KB * CH / 32; ++i) {
+          const int x = i * 32 + lane, key = x / CH, ch = x % CH;
+          const int r = __shfl_sync(0xFFFFFFFFu, row, key);
+          const int64_t off = (int64_t)max(r, 0) * W::ROW + ch * 16;
+          const uint32_t dst = st + spread<CH>(key, ch) * 16;
+          copy16(dst, static_cast<const char*>(c.k) + off, r >= 0);
+          copy16(dst + KB * W::ROW, static_cast<const char*>(c.v) + off, r >= 0);
+        }
+        if constexpr (FP8) {
+          copy4(st + 2 * KB * W::ROW + lane * 4, c.ks + max(row, 0), row >= 0);
+          copy4(st + 2 * KB * W::ROW + KB * 4 + lane * 4, c.vs + max(row, 0), row >= 0);
+        }
+      }
+      copy_commit();
+    };
+    int rows_now[kStages];            // cache rows of the blocks in flight (which keys are live)
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      rows_now[i] = row_of(t0 + i);
+      issue(t0 + i, rows_now[i]);
+    }
+    int ahead = row_of(t0 + kStages - 1);
+    // ---- queries: shared memory, as the products want them (the first blocks are
+    // on their way meanwhile) ---------------------------------------------------
     for (int r = warp; r < R; r += kWarps) {
       constexpr int PER = D / 32;
       float x[PER];
@@ -250,44 +291,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
       rf[mt][0] = rowf[mt * 16 + qrow];
       rf[mt][1] = rowf[mt * 16 + qrow + 8];
     }
-    // ---- the warp's blocks: tile t, keys [t TK + warp KB, + KB) --------------
-    const int64_t all_keys = (int64_t)q.len + q.n;
-    auto row_of = [&](int t) -> int {   // cache row of this lane's key of block t, -1: none
-      const int64_t s = (int64_t)t * TK + warp * KB + lane;
-      if (t >= t1 || lane >= KB || s >= all_keys) return -1;
-      const int64_t r = cache_row(c.geo, pages, s);
-      if (r < 0) {
-        bad |= SPECDEC_DEVERR_BAD_CACHE;
-        return -1;
-      }
-      return (int)(r + (int64_t)h * c.geo.page_size);
-    };
-    auto issue = [&](int t, int row) {
-      const uint32_t st = ring_s + ((t - t0) % kStages) * W::STAGE;
-      if (t < t1) {
-#pragma unroll
-        for (int i = 0; i < KB * CH / 32; ++i) {
-          const int x = i * 32 + lane, key = x / CH, ch = x % CH;
-          const int r = __shfl_sync(0xFFFFFFFFu, row, key);
-          const int64_t off = (int64_t)max(r, 0) * W::ROW + ch * 16;
-          const uint32_t dst = st + spread<CH>(key, ch) * 16;
-          copy16(dst, static_cast<const char*>(c.k) + off, r >= 0);
-          copy16(dst + KB * W::ROW, static_cast<const char*>(c.v) + off, r >= 0);
-        }
-        if constexpr (FP8) {
-          copy4(st + 2 * KB * W::ROW + lane * 4, c.ks + max(row, 0), row >= 0);
-          copy4(st + 2 * KB * W::ROW + KB * 4 + lane * 4, c.vs + max(row, 0), row >= 0);
-        }
-      }
-      copy_commit();
-    };
-    int rows_now[kStages];            // cache rows of the blocks in flight (which keys are live)
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      rows_now[i] = row_of(t0 + i);
-      issue(t0 + i, rows_now[i]);
-    }
-    int ahead = row_of(t0 + kStages - 1);
     for (int t = t0; t < t1; ++t) {
       issue(t + kStages - 1, ahead);
       const int now = rows_now[0];
@@ -510,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
         v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
         v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
         const int r = mt * 16 + qrow + 8 * y;
+        if (r >= rows) continue;
         if (quad == 0) stats[warp * R + r] = make_float2(m[mt][y], v);
 #pragma unroll
         for (int nt = 0; nt < D / 8; ++nt)
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
       }
     __syncthreads();
     const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 > 0 ? 0 : 1);
-    for (int x = tid; x < R * D; x += kThreads) {
+    for (int x = tid; x < rows * D; x += kThreads) {
       const int r = x / D, d = x % D;
       float mm = -INFINITY;
 #pragma unroll
@@ -536,12 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
         acc += s.x == -INFINITY ? 0.0f : merge[(w * R + r) * D + d] * f;
       }
       if (whole) {
-        if (r < rows) {
-          const int row = rt * R + r;
-          T y;
-          from_float(sum == 0.0f ? 0.0f : acc / sum, y);
-          static_cast<T*>(a.out)[((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + d] = y;
-        }
+        const int row = rt * R + r;
+        T y;
+        from_float(sum == 0.0f ? 0.0f : acc / sum, y);
+        static_cast<T*>(a.out)[((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + d] = y;
       } else {
         part.sums[(slot * R + r) * D + d] = acc;
         if (d == 0) part.stats[slot * R + r] = make_float2(mm, sum);
@@ -561,7 +563,7 @@ int launch_warp(const AttendArgs& a, int num_sms, cudaStream_t st) {
   const int G = num_sms;
   kern<<<G, kThreads, L::BYTES, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  return launch_join<T, 16 * MT, TK, D>(a, G, st);
+  return a.whole ? SPECDEC_OK : launch_join<T, 16 * MT, TK, D>(a, G, st);
 }
 
 // Rows (nodes x heads that share a kv head) of an average request: what the
@@ -583,15 +585,20 @@ int launch_dim(const AttendArgs& a, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-int64_t attend_workspace_bytes(int B, int64_t N, int kv_heads, int q_heads, int head_dim, int num_sms) {
-  if (average_rows(B, N, kv_heads, q_heads) > kWarpRows) return attend_tile_workspace(head_dim, num_sms);
+int64_t attend_workspace_bytes(int B, int64_t N, int kv_heads, int q_heads, int head_dim, int64_t capacity, int num_sms) {
+  const bool tile = average_rows(B, N, kv_heads, q_heads) > kWarpRows;
+  if (whole_items(B, N, kv_heads, q_heads, capacity, tile ? 128 : 16, num_sms)) return 0;
+  if (tile) return attend_tile_workspace(head_dim, num_sms);
   return head_dim == 128 ? Partials<16, 128>::bytes(num_sms) : Partials<16, 64>::bytes(num_sms);
 }
 
-int launch_attend(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st) {
-  if (a.c.N == 0) return SPECDEC_OK;
-  if (average_rows(a.c.B, a.c.N, a.c.geo.kv_heads, a.q_heads) > kWarpRows)
-    return launch_attend_tile(a, cache_dtype, dtype, num_sms, st);
+int launch_attend(const AttendArgs& args, int cache_dtype, int dtype, int num_sms, cudaStream_t st) {
+  if (args.c.N == 0) return SPECDEC_OK;
+  AttendArgs a = args;
+  const CacheArgs& c = a.c;
+  const bool tile = average_rows(c.B, c.N, c.geo.kv_heads, a.q_heads) > kWarpRows;
+  a.whole = whole_items(c.B, c.N, c.geo.kv_heads, a.q_heads, (int64_t)c.geo.max_pages * c.geo.page_size, tile ? 128 : 16, num_sms);
+  if (tile) return launch_attend_tile(a, cache_dtype, dtype, num_sms, st);
   const bool fp8 = cache_dtype == SPECDEC_E4M3;
   if (dtype == SPECDEC_BF16)
     return fp8 ? launch_dim<__nv_bfloat16, true>(a, num_sms, st) : launch_dim<__nv_bfloat16, false>(a, num_sms, st);

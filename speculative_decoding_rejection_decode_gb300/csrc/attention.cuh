@@ -44,12 +44,21 @@ struct PlanArgs {
   const int32_t* lengths;
   int64_t N, capacity;      // node rows; slots of a request
   int32_t B, kv_heads, group;
-  bool tree;
+  bool tree, whole;         // whole: items are not split
 
-  __host__ __device__ __forceinline__ explicit PlanArgs(const CacheArgs& c, int g)
-      : cu(c.cu), lengths(c.lengths), N(c.N), capacity((int64_t)c.geo.max_pages * c.geo.page_size), B(c.B),
-        kv_heads(c.geo.kv_heads), group(g), tree(c.parent != nullptr) {}
+  __host__ __device__ __forceinline__ explicit PlanArgs(const AttendArgs& a)
+      : cu(a.c.cu), lengths(a.c.lengths), N(a.c.N), capacity((int64_t)a.c.geo.max_pages * a.c.geo.page_size), B(a.c.B),
+        kv_heads(a.c.geo.kv_heads), group(a.q_heads / a.c.geo.kv_heads), tree(a.c.parent != nullptr), whole(a.whole) {}
 };
+
+// Whether a call leaves items whole: contexts of at most 4 tiles by the page
+// table's width, and no more items than two for each CTA.  One launch and no
+// workspace then; splitting such items only pays where they are many and ragged.
+// (One token over 500 keys, 8 kv heads: see the kernels' figures.)
+inline bool whole_items(int B, int64_t N, int kv_heads, int q_heads, int64_t capacity, int rows, int num_sms) {
+  const int64_t avg = (N + B - 1) / B * (q_heads / kv_heads);
+  return capacity <= 512 && (int64_t)B * kv_heads * ((avg + rows - 1) / rows) <= 2 * (int64_t)num_sms;
+}
 
 // The plan of request b for tiles of R rows and TK keys.  units = 0 for what
 // cannot be attended (no nodes, a cu or length out of range, a tree that is
@@ -72,7 +81,7 @@ __host__ __device__ __forceinline__ Request attend_request(const PlanArgs& c, in
   }
   q.rts = (int32_t)(((int64_t)q.n * c.group + R - 1) / R);
   q.tiles = (int32_t)(((int64_t)q.len + q.n + TK - 1) / TK);
-  q.units = (int64_t)c.kv_heads * q.rts * (q.tiles + kItemCost);
+  q.units = (int64_t)c.kv_heads * q.rts * ((c.whole ? 1 : q.tiles) + kItemCost);
   if (q.units >= ((int64_t)1 << 31)) {   // units of a request are counted in 32 bits
     q.units = 0;
     why |= SPECDEC_DEVERR_BAD_CACHE;
@@ -186,7 +195,7 @@ template <typename T, int R, int TK, int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, const int G) {
   __shared__ ScanShared sh;
   const int group = a.q_heads / a.c.geo.kv_heads;
-  const PlanArgs plan(a.c, group);
+  const PlanArgs plan(a);
   uint32_t why = 0;
   int64_t u = 0;
   int ranges = 0;

@@ -359,7 +359,7 @@ __device__ __forceinline__ void next_segment(Segments* s, const PlanArgs c) {
       if (++s->b >= c.B) return;   // lengths that changed under the call
       s->q = attend_request(c, s->b, kR, kTK, ignored);
     }
-    const int tiles = s->q.tiles, rts = s->q.rts, u = s->u;
+    const int tiles = c.whole ? 1 : s->q.tiles, rts = s->q.rts, u = s->u;
     const int item = (int)((unsigned)u / (unsigned)(tiles + kItemCost)), at = u - item * (tiles + kItemCost);
     s->t0 = max(at - kItemCost, 0);
     s->t1 = (int)min((int64_t)tiles, at - kItemCost + (s->end - s->base - u));
@@ -367,8 +367,8 @@ __device__ __forceinline__ void next_segment(Segments* s, const PlanArgs c) {
     s->rt = item - s->h * rts;
     s->u = u + tiles + kItemCost - at;
   } while (s->t1 <= s->t0);          // a range may end before an item's first tile
-  const int tiles = s->q.tiles;
-  s->whole = s->t0 == 0 && s->t1 == tiles;
+  if (c.whole) s->t1 = s->q.tiles;
+  s->whole = s->t0 == 0 && s->t1 == s->q.tiles;
   s->rows = min(kR, s->q.n * c.group - s->rt * kR);
   s->more = true;
 }
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const CacheArgs& c = a.c;
   const int G = gridDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.q_heads / c.geo.kv_heads;
-  const PlanArgs plan(c, group);
+  const PlanArgs plan(a);
   uint32_t why = 0;
   int64_t u0 = 0;
   find_unit<kTileThreads>(plan, kR, kTK,
@@ -1177,7 +1177,7 @@ int launch_tile(const AttendArgs& a, int num_sms, cudaStream_t st) {
   if (box && (!encode_rows(&kmap, a.c.k, rows, D, box, FP8) || !encode_rows(&vmap, a.c.v, rows, D, box, FP8))) box = 0;
   kern<<<num_sms, kTileThreads, bytes, st>>>(a, box, grouped && box > 0, kmap, vmap);
   if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  return launch_join<T, kR, kTK, D>(a, num_sms, st);
+  return a.whole ? SPECDEC_OK : launch_join<T, kR, kTK, D>(a, num_sms, st);
 }
 
 template <typename T, bool FP8>

@@ -65,6 +65,7 @@ struct AttendArgs {
   float scale_log2;     // softmax scale * log2(e)
   void* out;            // [N, q_heads, head_dim] contiguous
   void* workspace;
+  bool whole;           // items are not split: no workspace, no join (set by launch_attend)
 };
 
 struct GivenArgs {
@@ -89,7 +90,7 @@ int launch_append(const AppendArgs& a, int cache_dtype, int dtype, int num_sms, 
 int launch_read(const ReadArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
 int launch_commit(const CommitArgs& a, int cache_dtype, int num_sms, cudaStream_t st);
 int launch_attend(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
-int64_t attend_workspace_bytes(int B, int64_t N, int kv_heads, int q_heads, int head_dim, int num_sms);
+int64_t attend_workspace_bytes(int B, int64_t N, int kv_heads, int q_heads, int head_dim, int64_t capacity, int num_sms);
 int launch_given(const GivenArgs& a, int num_sms, cudaStream_t st);
 
 }  // namespace specdec

@@ -730,11 +730,12 @@ int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
 }
 
 int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache_t* cache,
-                                         int B, int64_t N, int q_heads) {
-  if (!h || !cache || B <= 0 || B > kMaxRequests || N < 0 || (cache->head_dim != 64 && cache->head_dim != 128) ||
+                                         int B, int64_t N, int q_heads, int max_pages) {
+  if (!h || !cache || max_pages <= 0 || cache->page_size <= 0 || B <= 0 || B > kMaxRequests || N < 0 || (cache->head_dim != 64 && cache->head_dim != 128) ||
       cache->num_kv_heads <= 0 || q_heads <= 0 || q_heads > kMaxHeads || q_heads % cache->num_kv_heads != 0)
     return SPECDEC_ERR_INVALID_ARG;
-  return attend_workspace_bytes(B, N, cache->num_kv_heads, q_heads, cache->head_dim, h->num_sms);
+  return attend_workspace_bytes(B, N, cache->num_kv_heads, q_heads, cache->head_dim,
+                                (int64_t)max_pages * cache->page_size, h->num_sms);
 }
 
 int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
@@ -751,7 +752,8 @@ int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
     return SPECDEC_ERR_INVALID_ARG;
   if (!h) return SPECDEC_ERR_INVALID_ARG;
   const int64_t need =
-      attend_workspace_bytes(nodes->B, nodes->N, cache->num_kv_heads, q_heads, cache->head_dim, h->num_sms);
+      attend_workspace_bytes(nodes->B, nodes->N, cache->num_kv_heads, q_heads, cache->head_dim,
+                             (int64_t)nodes->max_pages * cache->page_size, h->num_sms);
   if (need > 0 && (!workspace || !aligned16(workspace))) return SPECDEC_ERR_INVALID_ARG;
   if (workspace_bytes < need) return SPECDEC_ERR_CAPACITY;
   DeviceGuard guard(h->device);

@@ -80,7 +80,7 @@ def test_rows_are_checked_before_any_device_work(lib):
         assert attend(**bad) == INVALID
     assert lib.specdec_cache_read(None, c, n, lib.SPECDEC_BF16, None, 16, None) == INVALID
     assert lib.specdec_cache_commit(None, c, n, None, 16, 16, None) == INVALID
-    assert lib.specdec_tree_attention_workspace(None, c, 1, 1, 8) == INVALID
+    assert lib.specdec_tree_attention_workspace(None, c, 1, 1, 8, 4) == INVALID
     # good arguments and no handle
     assert append() == INVALID and attend() == INVALID
 
