@@ -142,8 +142,8 @@ class KVCache:
         if page_table.dim() != 2 or page_table.shape[0] != B:
             raise ValueError("page_table must be [B, max_pages]")
         most, (row, one) = page_table.shape[1], page_table.stride()
-        if most < 1 or (most > 1 and one != 1):
-            raise ValueError("page_table must be [B, max_pages] with contiguous rows")
+        if most < 1 or (most > 1 and one != 1) or (B > 1 and row < most):
+            raise ValueError("page_table must be [B, max_pages] with contiguous rows of their own")
         return ctypes.byref(specdec_nodes_t(page_table.data_ptr(), max(row, most), most, lengths.data_ptr(),
                                             cu.data_ptr(), None if parent is None else parent.data_ptr() or None,
                                             B, N))
@@ -191,6 +191,9 @@ class KVCache:
             elif out_q.shape != q.shape or out_q.dtype != k.dtype or out_q.device != self.device \
                     or not out_q.is_contiguous():
                 raise ValueError("out_q must be contiguous and like q")
+            elif N and ((_overlap(out_q, q) and not (out_q.data_ptr() == q.data_ptr() and q.is_contiguous()))
+                        or _overlap(out_q, k) or _overlap(out_q, v)):
+                raise ValueError("out_q must be q itself or overlap none of q, k and v")
         elif out_q is not None:
             raise ValueError("out_q without q")
         dim = positions = 0

@@ -160,8 +160,14 @@ __device__ __forceinline__ RowPlace place_of(const CacheArgs& c, int from, int64
     if (r < (int64_t)c.cu[c.B]) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
     return p;
   }
+  int64_t first;
+  int32_t nodes;
+  if (!node_range(c.cu, b, c.N, first, nodes)) {
+    atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
+    return p;
+  }
   p.owned = 1;
-  const int64_t first = c.cu[b], len = c.lengths[b];
+  const int64_t len = c.lengths[b];
   const int j = (int)(r - first);
   p.row = len < 0 ? -1 : cache_row(c.geo, c.table + b * c.geo.table_stride, len + j);
   if (p.row < 0) bad |= SPECDEC_DEVERR_BAD_CACHE;

@@ -168,6 +168,23 @@ def test_calls_refuse_what_does_not_fit(lib):
                out=(k, torch.zeros(4, 2, 64, dtype=torch.bfloat16)))
 
 
+def test_table_rows_and_turned_queries_that_overlap_are_refused(lib):
+    c = small_cache(lib)
+    n = nodes_of()
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    one = torch.zeros(1, 2, dtype=torch.int32).expand(2, 2)              # every request the same row
+    with pytest.raises(ValueError, match="page_table"):
+        c.append(k, k, **dict(n, page_table=one))
+    wide = torch.zeros(4, 8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="out_q"):
+        c.append(k, k, **n, q=wide[1:], out_q=wide[:3])                  # one row further
+    rows = torch.zeros(3, 12, 64, dtype=torch.bfloat16)
+    flat = rows.view(-1)[:3 * 8 * 64].view(3, 8, 64)                     # over the rows' own values
+    for q, x in ((rows[:, :8], k), (torch.zeros(3, 8, 64, dtype=torch.bfloat16), rows[:, 8:10])):
+        with pytest.raises(ValueError, match="out_q"):
+            c.append(x, x, **n, q=q, out_q=flat)
+
+
 def test_sample_given_refuses_what_does_not_fit(lib):
     from speculative_decoding_rejection_decode_gb300 import Verifier
     v = Verifier.__new__(Verifier)

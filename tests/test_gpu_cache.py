@@ -188,6 +188,32 @@ def test_append_bad_pages_positions_and_trees(V):
     V.get_error()
 
 
+@pytest.mark.parametrize("parents", [False, True])
+def test_append_and_read_of_malformed_ranges(V, parents):
+    from speculative_decoding_rejection_decode_gb300 import rotary_table
+    table = rotary_table(64, 128)
+    for at, value, hit in ((0, -3, 0), (3, 100, 2)):      # starts below 0; passes the rows given
+        s = Step(ctx=[3, 20, 9], nodes=[4, 4, 4], tree="random" if parents else "chain", page=8, seed=3, poison=False)
+        if parents:
+            s.parent[:4] = torch.tensor([-1, 0, 1, 1], dtype=torch.int32, device="cuda")
+        k0 = s.k.clone()
+        cu = s.cu.clone()
+        cu[at] = value
+        out_q = torch.full_like(s.q, 7.0)
+        s.cache(V).append(s.new_k, s.new_v, s.table, s.lengths, cu, s.parent, q=s.q, rotary=table, out_q=out_q)
+        assert V.get_error() == BAD_CU
+        out = (torch.full_like(s.new_k, 7.0), torch.full_like(s.new_k, 7.0))
+        s.cache(V).read(s.table, s.lengths, cu, out=out)
+        assert V.get_error() == BAD_CU
+        for b in range(3):
+            for j in range(4):
+                page, off = s.row(b, s.ctx[b] + j)
+                r = s.firsts[b] + j
+                assert torch.equal(s.k[page, :, off], k0[page, :, off]) == (b == hit)
+                assert bool((out_q[r] == 7.0).all()) == (b == hit)
+                assert torch.equal(out[0][r], torch.full_like(out[0][r], 7.0) if b == hit else s.k[page, :, off])
+
+
 # ---- read --------------------------------------------------------------------------
 
 @pytest.mark.parametrize("cache,dtype,head_dim,page", [(E4, BF, 128, 16), (E4, HF, 64, 48), (BF, BF, 128, 7), (HF, HF, 64, 64)])
