@@ -27,8 +27,7 @@
 // three) e4m3 parts of 4 bits each, q = hi + lo (+ lo2), which hold bf16's 8 (f16's
 // 11) bits exactly down to 2^-9 (2^-6) of the row's largest value and to 2^-17 of it
 // below.  That keeps the keys as they lie in memory (widening keys as well as
-// values bound the kernel to 540 us where this form took 300: 32 requests of 29
-// nodes, 6000 to 16000 keys).  The keys' scales are applied to the scores.
+// values took 1.8 times as long: 32 requests of 29 nodes, 6000 to 16000 keys).  The keys' scales are applied to the scores.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -399,32 +398,38 @@ __device__ __forceinline__ bool visible(const Segments& s, const int32_t* all_pa
   return true;
 }
 
-// Column d of what was left out of tiles t0 .. t1 - 1 (clear_nonfinite) for the
-// rows of `node`: the sum of the values that are not finite.
+// What was left out of tiles t0 .. t1 - 1 (clear_nonfinite) for the rows of `node`:
+// the values of columns d0 .. d0 + D / 2 - 1 that are not finite are added to out (or,
+// where that is null, to sums).
 template <typename T, bool FP8, int D>
-__device__ __noinline__ float left_out(const CacheArgs& c, const Segments& s, int node, int d) {
-  float sum = 0.0f;
+__device__ __noinline__ void left_out(const CacheArgs& c, const Segments& s, int node, int d0, T* out, float* sums) {
   const Request& q = s.q;
   for (int t = max(s.t0, q.len / kTK); t < s.t1; ++t) {
     uint32_t bits[4];
     visible(s, c.parent, node, t, bits);
     for (int k = max(0, q.len - t * kTK); k < kTK; ++k) {   // nodes
       const int64_t at = (int64_t)t * kTK + k;
-      if (!((bits[k >> 5] >> (k & 31)) & 1u) || at >= (int64_t)q.len + q.n) continue;
+      if (at >= (int64_t)q.len + q.n) break;
+      const uint32_t of = k < 32 ? bits[0] : k < 64 ? bits[1] : k < 96 ? bits[2] : bits[3];
+      if (!((of >> (k & 31)) & 1u)) continue;
       const int64_t r0 = cache_row(c.geo, c.table + s.b * c.geo.table_stride, at);
       if (r0 < 0) continue;
       const int64_t r = r0 + (int64_t)s.h * c.geo.page_size;
-      float v;
-      if constexpr (FP8) {
-        const __half_raw e = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(c.v)[r * D + d], __NV_E4M3);
-        v = __half2float(*reinterpret_cast<const __half*>(&e)) * c.vs[r];
-      } else {
-        v = to_float(static_cast<const T*>(c.v)[r * D + d]);
+#pragma unroll 4
+      for (int d = d0; d < d0 + D / 2; ++d) {
+        float v;
+        if constexpr (FP8) {
+          const __half_raw e = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(c.v)[r * D + d], __NV_E4M3);
+          v = __half2float(*reinterpret_cast<const __half*>(&e)) * c.vs[r];
+        } else {
+          v = to_float(static_cast<const T*>(c.v)[r * D + d]);
+        }
+        if (isfinite(v)) continue;
+        if (out) from_float(to_float(out[d]) + v, out[d]);
+        else sums[d] += v;
       }
-      if (!isfinite(v)) sum += v;
     }
   }
-  return sum;
 }
 
 template <typename T, bool FP8, int D>
@@ -768,7 +773,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-          const int b = most ? min(max((int)(most >> 23) - 127 - 5, -80), 80) : 0;
+          const int b = most ? max((int)(most >> 23) - 127 - 5, -80) : 0;   // 122 at most
           const float by = __uint_as_float((uint32_t)(127 - b) << 23);
           if ((lane & 7) == 0) sh.vexp[f][lane >> 3] = (float)b;
           reinterpret_cast<float4*>(smem + L::KF)[f * (kTK / 4) + lane] = ks;
@@ -1100,18 +1105,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // values that are not finite were left out of the tiles that hold nodes:
         // the rows that see their keys get them now
         if (poison && live) {
-#pragma unroll 1
-          for (int d = w * (D / 2); d < (w + 1) * (D / 2); ++d) {
-            const float v = left_out<T, FP8, D>(a.c, seg, (seg.rt * kR + row) / group, d);
-            if (v == 0.0f) continue;
-            if (seg.whole) {
-              T* out = static_cast<T*>(a.out) +
-                       ((seg.q.first + gr / group) * a.q_heads + seg.h * group + gr % group) * (int64_t)D + d;
-              from_float(to_float(*out) + v, *out);
-            } else {
-              part.sums[(slot * kR + row) * D + d] += v;
-            }
-          }
+          T* out = nullptr;
+          if (seg.whole)
+            out = static_cast<T*>(a.out) + ((seg.q.first + gr / group) * a.q_heads + seg.h * group + gr % group) * (int64_t)D;
+          left_out<T, FP8, D>(a.c, seg, gr / group, w * (D / 2), out, part.sums + (slot * kR + row) * D);
         }
         if (live && !seg.whole && w == 0) part.stats[slot * kR + row] = make_float2(mm, lsum);
       }
@@ -1128,7 +1125,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 0 && sh.dead) atomicOr(c.err, SPECDEC_DEVERR_TIMEOUT);
+  if (sh.dead) {   // copies and products that no role has waited for end before their memory goes
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    if (tid == 0) atomicOr(c.err, SPECDEC_DEVERR_TIMEOUT);
+    __syncthreads();
+  }
   if (warp == kScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(512));
 }

@@ -570,6 +570,49 @@ def test_pages_past_32_bit_offsets(V):
     assert got.tolist() == [202] and torch.equal(k[1], s.new_k[2]) and V.get_error() == 0
 
 
+def test_tiles_of_pages_past_32_bit_offsets(V):
+    from speculative_decoding_rejection_decode_gb300 import KVCache
+    for page in (128, 24):                       # fetched as boxes of 128 rows, and of 8
+        pages, kv = 70000 * 128 // page, 2
+        c = KVCache.empty(V, pages, page, kv, 128, BF)
+        s = Step(ctx=[200], nodes=[9], kv_heads=kv, page=page, tree="random", seed=13, poison=False)
+        far = [pages - 1 - i if i % 2 else i for i in range(1, len(s.pages[0]) + 1)]
+        for here, there in zip(s.pages[0], far):
+            c.k[there], c.v[there] = s.k[here], s.v[here]
+        table = torch.tensor([far], dtype=torch.int32, device="cuda")
+        want = s.cache(V).attend(s.q, *args(s))
+        assert torch.equal(c.attend(s.q, table, s.lengths, s.cu, s.parent), want)
+        del c
+
+
+@pytest.mark.parametrize("nodes", [3, 40])
+def test_values_near_the_largest(V, nodes):
+    # scales of 8-bit values far above and below one: what bf16 rows may hold
+    for power in (-40, 100, 116):
+        s = Step(ctx=[300], nodes=[nodes], cache=E4, seed=15)
+        s.vs *= 2.0 ** power
+        out = s.cache(V).attend(s.q, *args(s))
+        want, big = s.attend()
+        assert ((out.double() - want).abs() <= attend_tolerance(s, want, big)).all()
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+def test_infinite_value_in_a_deep_tree(V, cache):
+    s = Step(ctx=[50], nodes=[1000], kv_heads=1, group=1, head_dim=64, tree="random", cache=cache, seed=16)
+    s.parent[:] = torch.arange(1000, device="cuda", dtype=torch.int32) - 1   # one branch
+    clean = s.cache(V).attend(s.q, *args(s))
+    page, off = s.row(0, 52)
+    if cache == E4:
+        s.v.view(torch.uint8)[page, 0, off, 5] = 0x7F
+    else:
+        s.v[page, 0, off, 5] = math.inf
+    out = s.cache(V).attend(s.q, *args(s))
+    assert V.get_error() == 0
+    assert torch.equal(out[:2], clean[:2]) and not out[2:, :, 5].isfinite().any()
+    out[:, :, 5] = clean[:, :, 5]
+    assert torch.equal(out, clean)
+
+
 # ---- graphs and streams -------------------------------------------------------------
 
 def test_two_graphs_of_one_handle_on_two_streams(V):
