@@ -2,10 +2,14 @@
 // quantisation on the way), reading rows back, and moving an accepted branch
 // into place.  Contract in include/specdec.h.
 //
-// All three are bound by memory traffic (latency for one request): a thread
-// moves 8 values (16 bytes of a 16-bit row) and a row of head_dim values is
+// A thread moves 8 values (16 bytes of a 16-bit row) and a row of head_dim values is
 // held by head_dim / 8 neighbouring lanes, so that a row's absolute maximum is
-// a few shuffles and nothing passes through shared memory.
+// a few shuffles and nothing passes through shared memory.  Bounds: the read-back by
+// memory traffic (64 contexts of up to 8191 e4m3 rows of 8 heads of 128: 1.70 GB in
+// 258 us, 6.6 TB/s); the append, whose rows are quantised with IEEE divisions, by its
+// instructions and by the look-ups before its first row (15k tree nodes of 48 heads,
+// with their read-back: 435 MB in 94 us); the commit, and every call for one request,
+// by latency (29 nodes of 48 heads written and read back: 4.5 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -187,8 +191,11 @@ __device__ __forceinline__ RowPlace place_of(const CacheArgs& c, int from, int64
 // multiply-add), as the formula
 //   a' = a cos - b sin, b' = b cos + a sin
 // reads in 32 bits, so that what is quantised does not depend on contraction.
+// k and v, which may be quantised, and q have loops of their own, the first with one
+// copy of its body: one loop for all heads, unrolled, was 8 % slower for one tree and
+// held 6 blocks of an SM where this form holds 7.
 template <typename T, bool FP8, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, const int rows) {
+__global__ void __launch_bounds__(kThreads, 7) append_kernel(const AppendArgs a, const int rows) {
   constexpr int LANES = D / 8;                 // lanes of a row
   constexpr int SLOTS = kThreads / LANES;      // heads in flight
   __shared__ RowPlace places[kRows];
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && (int64_t)c.cu[c.B] > c.N) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
   __syncthreads();
-  const int kv = c.geo.kv_heads, total = 2 * kv + (a.q ? a.q_heads : 0);
+  const int kv = c.geo.kv_heads, heads = a.q ? a.q_heads : 0;
   for (int i = 0; i < here; ++i) {
     const RowPlace p = places[i];
     if (!p.owned) continue;
@@ -229,66 +236,72 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
         sign = low ? -1.0f : 1.0f;
       }
     }
-    // heads in order: k, v, then q, SLOTS at a time; U steps' loads are under way
-    // together, and every lane of a warp takes part in each step (row_amax)
-    constexpr int U = 6;
     const int other = (int)(threadIdx.x & 31 & ~(LANES - 1)) | (chunk + partner);   // lane of the pairs' other halves
-    for (int h0 = 0; h0 < total; h0 += U * SLOTS) {
-      uint4 w[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int hh = h0 + u * SLOTS + slot0;
-        if (hh < total) {
-          const bool isk = hh < kv, isv = !isk && hh < 2 * kv;
-          const T* src = isk ? static_cast<const T*>(a.k) + r * a.k_row + hh * a.k_head
-                         : isv ? static_cast<const T*>(a.v) + r * a.v_row + (hh - kv) * a.v_head
-                               : static_cast<const T*>(a.q) + r * a.q_row + (hh - 2 * kv) * a.q_head;
-          w[u] = __ldg(reinterpret_cast<const uint4*>(src + d0));
-        } else {
-          w[u] = make_uint4(0, 0, 0, 0);
-        }
+    auto turn = [&](uint4 w, bool keys) -> Vec8 {   // the whole warp calls
+      Vec8 x = widen<T>(w);
+      uint4 o = w;
+      if (half_layout) {   // the same in the whole block
+        o.x = __shfl_sync(0xFFFFFFFFu, w.x, other);
+        o.y = __shfl_sync(0xFFFFFFFFu, w.y, other);
+        o.z = __shfl_sync(0xFFFFFFFFu, w.z, other);
+        o.w = __shfl_sync(0xFFFFFFFFu, w.w, other);
       }
+      if (!turned || !keys) return x;
+      Vec8 y;
+      if (a.interleaved) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (h0 + u * SLOTS >= total) break;
+        for (int k = 0; k < 8; k += 2) {
+          y.x[k] = __fsub_rn(__fmul_rn(x.x[k], cs[k]), __fmul_rn(x.x[k + 1], sn[k]));
+          y.x[k + 1] = __fadd_rn(__fmul_rn(x.x[k + 1], cs[k]), __fmul_rn(x.x[k], sn[k]));
+        }
+      } else {
+        const Vec8 z = widen<T>(o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          y.x[k] = __fadd_rn(__fmul_rn(x.x[k], cs[k]), sign * __fmul_rn(z.x[k], sn[k]));
+      }
+      return y;
+    };
+    // k and v heads two steps of SLOTS at a time, q heads four; the first of both are
+    // under way together
+    constexpr int UK = 2, UQ = 4;
+    const T* q0 = static_cast<const T*>(a.q) + r * a.q_row + d0;
+    uint4 wq[UQ];
+    auto load_q = [&](int h0) {
+#pragma unroll
+      for (int u = 0; u < UQ; ++u) {
+        const int h = h0 + u * SLOTS + slot0;
+        wq[u] = h < heads ? __ldg(reinterpret_cast<const uint4*>(q0 + h * a.q_head)) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    for (int h0 = 0; h0 < 2 * kv; h0 += UK * SLOTS) {
+      uint4 w[UK];
+#pragma unroll
+      for (int u = 0; u < UK; ++u) {
         const int hh = h0 + u * SLOTS + slot0;
-        const bool any = hh < total, isk = hh < kv, isv = !isk && hh < 2 * kv;
-        Vec8 x = widen<T>(w[u]);
-        uint4 o = w[u];
-        if (half_layout) {   // the same in the whole block
-          o.x = __shfl_sync(0xFFFFFFFFu, w[u].x, other);
-          o.y = __shfl_sync(0xFFFFFFFFu, w[u].y, other);
-          o.z = __shfl_sync(0xFFFFFFFFu, w[u].z, other);
-          o.w = __shfl_sync(0xFFFFFFFFu, w[u].w, other);
-        }
-        if (any) {
-          if (turned && !isv) {
-            Vec8 y;
-            if (a.interleaved) {
+        const T* src = hh < kv ? static_cast<const T*>(a.k) + r * a.k_row + hh * a.k_head
+                               : static_cast<const T*>(a.v) + r * a.v_row + (hh - kv) * a.v_head;
+        w[u] = hh < 2 * kv ? __ldg(reinterpret_cast<const uint4*>(src + d0)) : make_uint4(0, 0, 0, 0);
+      }
+      if (h0 == 0) load_q(0);
+#pragma unroll 1
+      for (int u = 0; u < UK; ++u) {
+        const int hh = h0 + u * SLOTS + slot0;
+        const bool isk = hh < kv;
+        const Vec8 x = turn(u ? w[1] : w[0], isk);
+        const int64_t row = p.row + (int64_t)(isk ? hh : hh - kv) * c.geo.page_size;
+        store_row<T, FP8, D>(isk ? c.k : c.v, isk ? c.ks : c.vs, row, chunk, x, hh < 2 * kv && p.row >= 0);
+      }
+    }
+    const bool lost = a.rotary && p.turn < 0;   // no position: defined rows
+    T* out0 = static_cast<T*>(a.out_q) + r * heads * D + d0;
+    for (int h0 = 0; h0 < heads; h0 += UQ * SLOTS) {
+      if (h0) load_q(h0);
 #pragma unroll
-              for (int k = 0; k < 8; k += 2) {
-                y.x[k] = __fsub_rn(__fmul_rn(x.x[k], cs[k]), __fmul_rn(x.x[k + 1], sn[k]));
-                y.x[k + 1] = __fadd_rn(__fmul_rn(x.x[k + 1], cs[k]), __fmul_rn(x.x[k], sn[k]));
-              }
-            } else {
-              const Vec8 z = widen<T>(o);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                y.x[k] = __fadd_rn(__fmul_rn(x.x[k], cs[k]), sign * __fmul_rn(z.x[k], sn[k]));
-            }
-            x = y;
-          }
-        }
-        // stored rows and turned q rows part here; row_amax needs whole warps, so
-        // the 8-bit store runs for every lane and q lanes drop its result
-        if (h0 + u * SLOTS < 2 * kv) {
-          const int64_t row = p.row + (int64_t)(isk ? hh : hh - kv) * c.geo.page_size;
-          store_row<T, FP8, D>(isk ? c.k : c.v, isk ? c.ks : c.vs, row, chunk, x, any && p.row >= 0 && (isk || isv));
-        }
-        if (any && !isk && !isv) {
-          if (a.rotary && p.turn < 0) x = Vec8{};  // no position: a defined row
-          reinterpret_cast<uint4*>(static_cast<T*>(a.out_q) + (r * a.q_heads + hh - 2 * kv) * D)[chunk] = narrow<T>(x);
-        }
+      for (int u = 0; u < UQ; ++u) {
+        const int h = h0 + u * SLOTS + slot0;
+        const Vec8 x = turn(wq[u], true);
+        if (h < heads) *reinterpret_cast<uint4*>(out0 + h * D) = lost ? make_uint4(0, 0, 0, 0) : narrow<T>(x);
       }
     }
   }
@@ -446,9 +459,8 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a, const i
 }
 
 // Rows of a block, whose places are looked up together (a few dependent loads).
-// Reads take one wave of resident blocks where N allows.  Appends go row by row
-// within a block: 6 rows of 48 heads and 14848 rows in all took 109 us with their
-// read-back, 1 row 132 us, 8 rows 121 us.
+// Both take one wave of resident blocks where N allows.  Appends of 48 heads and
+// 15k rows in all took 94 us with their read-back, two waves 97, three 104.
 inline int rows_per_block(int64_t N, int64_t blocks, int most) {
   const int64_t r = (N + blocks - 1) / blocks;
   return (int)(r < 1 ? 1 : (r > most ? most : r));
@@ -456,7 +468,7 @@ inline int rows_per_block(int64_t N, int64_t blocks, int most) {
 
 template <typename T, bool FP8>
 int append_of(const AppendArgs& a, int num_sms, cudaStream_t st) {
-  const int rows = rows_per_block(a.c.N, (int64_t)num_sms * 16, 6);
+  const int rows = rows_per_block(a.c.N, (int64_t)num_sms * 7, 16);
   const int64_t grid = (a.c.N + rows - 1) / rows;
   if (a.c.head_dim == 128) append_kernel<T, FP8, 128><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
   else append_kernel<T, FP8, 64><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
