@@ -6,6 +6,9 @@
 // a tile through a ring in shared memory (asynchronous 16-byte copies, three
 // blocks deep, no block-wide barrier), keeps the running maximum, sum and
 // weighted sum of its keys in registers, and the warps meet once per segment.
+// Measured (32 query and 8 kv heads of 128, bf16): one node over 500 keys 12 us, all
+// of it latency; 64 nodes over up to 4000 keys 593 MB in 111 us, 5.4 TB/s, the copies
+// of a CTA not deep enough at its first and last blocks (70 % of DRAM's cycles).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -171,11 +174,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
       if (++b >= c.B) return;   // lengths that changed under the call
       q = attend_request(plan, b, R, TK, ignored);
     }
-    const int cost = (a.whole ? 1 : q.tiles) + kItemCost;
+    const int cost = (a.whole ? 1 : q.tiles) + plan.item_cost;
     const int64_t item = (u - base) / cost;
     const int at = (int)((u - base) % cost);
-    const int t0 = max(at - kItemCost, 0);
-    int t1 = (int)min((int64_t)(cost - kItemCost), at - kItemCost + (uend - u));
+    const int t0 = max(at - plan.item_cost, 0);
+    int t1 = (int)min((int64_t)(cost - plan.item_cost), at - plan.item_cost + (uend - u));
     const int h = (int)(item / q.rts), rt = (int)(item % q.rts);
     u += cost - at;
     if (t1 <= t0) continue;
@@ -598,8 +601,9 @@ int launch_attend(const AttendArgs& args, int cache_dtype, int dtype, int num_sm
   const CacheArgs& c = a.c;
   const bool tile = average_rows(c.B, c.N, c.geo.kv_heads, a.q_heads) > kWarpRows;
   a.whole = whole_items(c.B, c.N, c.geo.kv_heads, a.q_heads, (int64_t)c.geo.max_pages * c.geo.page_size, tile ? 128 : 16, num_sms);
-  if (tile) return launch_attend_tile(a, cache_dtype, dtype, num_sms, st);
   const bool fp8 = cache_dtype == SPECDEC_E4M3;
+  a.item_cost = fp8 && !tile ? kItemCostWarp8 : kItemCost;
+  if (tile) return launch_attend_tile(a, cache_dtype, dtype, num_sms, st);
   if (dtype == SPECDEC_BF16)
     return fp8 ? launch_dim<__nv_bfloat16, true>(a, num_sms, st) : launch_dim<__nv_bfloat16, false>(a, num_sms, st);
   return fp8 ? launch_dim<__half, true>(a, num_sms, st) : launch_dim<__half, false>(a, num_sms, st);

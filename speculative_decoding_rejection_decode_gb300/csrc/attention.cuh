@@ -6,9 +6,14 @@
 // idle; an item that crosses a range leaves partial results (row maximum, sum
 // and weighted sum of values) that a second, dependent kernel joins.
 //
-// An item also counts kItemCost units of its own: starting and ending it (queries,
+// An item also counts item_cost units of its own: starting and ending it (queries,
 // an empty pipeline, results) takes about as long as that many tiles, and without
-// them the ranges that hold many short requests finished late.
+// them the ranges that hold many short requests finished late.  us at a cost of 2, 4,
+// 5, 6 (32 query and 8 kv heads of 128): tile kernel, 64 requests of 2 to 9 nodes over up
+// to 8191 keys, bf16 237, 221, 219, 216; 32 of 29 over 6000 to 16000, e4m3 303, 298, 296,
+// 296; warp kernel, 64 of 1 over up to 8191, bf16 183, 172, 172, 172 and e4m3 180, 183,
+// 187, 187; 200 of 1 to 4 over up to 1500, bf16 201, 174, 171, 170 and e4m3 190, 194,
+// 195, 202 (its tiles are of 256 keys and take longer).
 //
 // Rows of an item: r = node * group + head within the group, so one read of a
 // key serves every node and every query head that shares it.
@@ -27,7 +32,8 @@
 
 namespace specdec {
 
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 5;       // units of an item's own
+constexpr int kItemCostWarp8 = 2;  // the same in the warp kernel over 8-bit caches
 
 struct Request {
   int64_t first;   // first node row
@@ -43,12 +49,12 @@ struct PlanArgs {
   const int32_t* cu;
   const int32_t* lengths;
   int64_t N, capacity;      // node rows; slots of a request
-  int32_t B, kv_heads, group;
+  int32_t B, kv_heads, group, item_cost;
   bool tree, whole;         // whole: items are not split
 
   __host__ __device__ __forceinline__ explicit PlanArgs(const AttendArgs& a)
       : cu(a.c.cu), lengths(a.c.lengths), N(a.c.N), capacity((int64_t)a.c.geo.max_pages * a.c.geo.page_size), B(a.c.B),
-        kv_heads(a.c.geo.kv_heads), group(a.q_heads / a.c.geo.kv_heads), tree(a.c.parent != nullptr), whole(a.whole) {}
+        kv_heads(a.c.geo.kv_heads), group(a.q_heads / a.c.geo.kv_heads), item_cost(a.item_cost), tree(a.c.parent != nullptr), whole(a.whole) {}
 };
 
 // Whether a call leaves items whole: contexts of at most 4 tiles by the page
@@ -84,7 +90,7 @@ __host__ __device__ __forceinline__ Request attend_request(const PlanArgs& c, in
   }
   q.rts = (int32_t)(((int64_t)q.n * c.group + R - 1) / R);
   q.tiles = (int32_t)(((int64_t)q.len + q.n + TK - 1) / TK);
-  q.units = (int64_t)c.kv_heads * q.rts * ((c.whole ? 1 : q.tiles) + kItemCost);
+  q.units = (int64_t)c.kv_heads * q.rts * ((c.whole ? 1 : q.tiles) + c.item_cost);
   if (q.units >= ((int64_t)1 << 31)) {   // units of a request are counted in 32 bits
     q.units = 0;
     why |= SPECDEC_DEVERR_BAD_CACHE;
@@ -214,8 +220,8 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, co
   const int g0 = blockIdx.x;                     // the range before the boundary
   const Request q = attend_request(plan, sh.b, R, TK, why);
   if (q.units == 0) return;
-  const int64_t item = (u - sh.before) / (q.tiles + kItemCost);
-  const int64_t u0 = sh.before + item * (q.tiles + kItemCost) + kItemCost, u1 = u0 + q.tiles;   // its tiles
+  const int64_t item = (u - sh.before) / (q.tiles + plan.item_cost);
+  const int64_t u0 = sh.before + item * (q.tiles + plan.item_cost) + plan.item_cost, u1 = u0 + q.tiles;   // its tiles
   // not an item that begins at the boundary, nor one that range g0 also went on with
   if (u0 >= u || range_begin(sh.total, ranges, g0) > u0) return;
   const int h = (int)(item / q.rts), rt = (int)(item % q.rts);

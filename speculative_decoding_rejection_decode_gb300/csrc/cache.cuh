@@ -65,6 +65,7 @@ struct AttendArgs {
   float scale_log2;     // softmax scale * log2(e)
   void* out;            // [N, q_heads, head_dim] contiguous
   void* workspace;
+  int item_cost;        // units of an item's own (attention.cuh; set by launch_attend)
   bool whole;           // items are not split: no workspace, no join (set by launch_attend)
 };
 

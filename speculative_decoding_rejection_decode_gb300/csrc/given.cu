@@ -13,6 +13,10 @@
 // piece of the row; the piece sums meet in distributed shared memory (no
 // workspace, no atomics, a fixed order); the CTA whose piece holds the crossing
 // reads it again, from L2, first by warps and then entry by entry.
+//
+// Measured: 256 requests of 1 to 8 drafts and 151936 entries, 261 MB in 59 us = 4.4
+// TB/s (the accept tests' few dependent loads and the final look stand before and
+// after the rows' stream); 8 requests of 32000 entries 7.6 us, latency.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -405,8 +409,9 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
 
 int launch_given(const GivenArgs& a, int num_sms, cudaStream_t st) {
   // CTAs of a request: as many as give every warp a step of its row and as one wave
-  // holds (4 CTAs of an SM are resident).  256 requests of 151936 entries: 2 CTAs
-  // each took 81 us, 1 112, 4 85, 8 94; 8 requests of 32000: 8 CTAs 11 us, 4 12, 1 21.
+  // holds (4 CTAs of an SM are resident).  With sums in double precision, which cost
+  // each form alike, 256 requests of 151936 entries: 2 CTAs each took 81 us, 1 112,
+  // 4 85, 8 94; 8 requests of 32000: 8 CTAs 11 us, 4 12, 1 21.
   int C = kMaxCtas;
   while (C > 1 && (a.V < C * kGivenWarps * kStep || (int64_t)a.B * C > (int64_t)num_sms * 4)) C >>= 1;
   cudaLaunchConfig_t cfg = {};
