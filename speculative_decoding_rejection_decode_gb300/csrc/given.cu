@@ -409,9 +409,9 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
 
 int launch_given(const GivenArgs& a, int num_sms, cudaStream_t st) {
   // CTAs of a request: as many as give every warp a step of its row and as one wave
-  // holds (4 CTAs of an SM are resident).  With sums in double precision, which cost
-  // each form alike, 256 requests of 151936 entries: 2 CTAs each took 81 us, 1 112,
-  // 4 85, 8 94; 8 requests of 32000: 8 CTAs 11 us, 4 12, 1 21.
+  // holds (4 CTAs of an SM are resident).  us with half, with these and with twice as many: 256
+  // requests of 151936 entries 74, 59, 59 (1, 2, 4 CTAs); 128 40, 34, 35; 512 of 128000 -, 95,
+  // 91 (1, 2); 400 of 32000 -, 24, 27; 8 of 32000 12, 11 (4, 8, in an earlier form).
   int C = kMaxCtas;
   while (C > 1 && (a.V < C * kGivenWarps * kStep || (int64_t)a.B * C > (int64_t)num_sms * 4)) C >>= 1;
   cudaLaunchConfig_t cfg = {};
