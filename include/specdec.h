@@ -376,9 +376,11 @@ int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
  * q_heads is a multiple of num_kv_heads.  Scores, maxima and sums are held in 32
  * bits; weights meet the values rounded to 16 bits (to f16 over e4m3 caches).
  * Keys in slots that the cache does not hold count as hidden (BAD_CACHE); a row
- * that sees no key is zeros.  What a masked slot holds, infinities and NaN
- * among it, reaches no row.  Requests whose cu, length or tree is out of range
- * write nothing, and neither do those of 2^31 or more tiles of 128 rows x 128 keys
+ * that sees no key is zeros, and so are the rows of a node whose own parent or an
+ * ancestor's is no earlier node (BAD_TREE; the request's other nodes are not
+ * touched by it).  What a masked slot holds, infinities and NaN
+ * among it, reaches no row.  Requests whose cu or length is out of range, or whose
+ * tree is larger than SPECDEC_MAX_TREE_NODES, write nothing, and neither do those of 2^31 or more tiles of 128 rows x 128 keys
  * (SPECDEC_DEVERR_BAD_CACHE).  Waits inside the kernel are bounded: one that runs out
  * sets SPECDEC_DEVERR_TIMEOUT, and the call's outputs are then undefined.  Of an
  * e4m3 cache's values, rows whose scale is below 2^-20 of the largest among 32

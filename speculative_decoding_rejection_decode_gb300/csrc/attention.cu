@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
   constexpr int QCH = D / 8;
   extern __shared__ __align__(128) char smem[];
   __shared__ ScanShared scan;
+  __shared__ int lost[R];           // nodes of the tile whose parents do not lead to node 0
   const CacheArgs& c = a.c;
   const int G = gridDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -272,8 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
     const bool tail = (int64_t)t1 * TK > q.len;                // the segment sees nodes
     if (tail && parent) {
       const int nodes = (rt * R + rows - 1) / group - node0 + 1;
-      for (int i = tid; i < nodes; i += kThreads)
-        if (!ancestor_bits(parent, node0 + i, words, anc + i * words)) bad |= SPECDEC_DEVERR_BAD_TREE;
+      for (int i = tid; i < nodes; i += kThreads) {
+        lost[i] = !ancestor_bits(parent, node0 + i, words, anc + i * words);
+        if (lost[i]) bad |= SPECDEC_DEVERR_BAD_TREE;
+      }
     }
     __syncthreads();
 
@@ -542,14 +545,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
         sum += s.y * f;
         acc += s.x == -INFINITY ? 0.0f : merge[(w * R + r) * D + d] * f;
       }
+      const bool gone = tail && parent && lost[(rt * R + r) / group - node0];   // a row of zeros
       if (whole) {
         const int row = rt * R + r;
         T y;
-        from_float(sum == 0.0f ? 0.0f : acc / sum, y);
+        from_float(gone || sum == 0.0f ? 0.0f : acc / sum, y);
         static_cast<T*>(a.out)[((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + d] = y;
       } else {
         part.sums[(slot * R + r) * D + d] = acc;
-        if (d == 0) part.stats[slot * R + r] = make_float2(mm, sum);
+        if (d == 0) part.stats[slot * R + r] = make_float2(mm, gone ? kLostRow : sum);
       }
     }
   }

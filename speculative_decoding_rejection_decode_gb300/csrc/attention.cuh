@@ -185,6 +185,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// The sum that marks a row whose node's parents do not lead to node 0 (sums are at
+// least 0, or NaN): any part of an item that meets the break gives it, and the row
+// becomes zeros.
+constexpr float kLostRow = -INFINITY;
+
 // Workspace: two partial slots per range, each R rows of D sums, then (max, sum).
 // A range may go on with an item that began earlier (slot 0) and leave another to
 // the next range (slot 1).
@@ -237,8 +242,14 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, co
     const int64_t at0 = (2 * (int64_t)g0 + 1) * R + r;
     auto at_of = [&](int g) { return g == g0 ? at0 : 2 * (int64_t)g * R + r; };
     float m = -INFINITY;
-    for (int g = g0 + lane; g <= g1; g += 32) m = fmaxf(m, part.stats[at_of(g)].x);
+    bool gone = false;
+    for (int g = g0 + lane; g <= g1; g += 32) {
+      const float2 s = part.stats[at_of(g)];
+      m = fmaxf(m, s.x);
+      gone |= s.y == kLostRow;
+    }
     m = warp_max(m);
+    gone = __any_sync(0xFFFFFFFFu, gone);
     const float ref = m == -INFINITY ? 0.0f : m;
     float l = 0.0f, acc[PER];
 #pragma unroll
@@ -276,7 +287,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, co
              ((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + lane * PER;
 #pragma unroll
     for (int k = 0; k < PER; k += 2)
-      *reinterpret_cast<uint32_t*>(out + k) = pack2(acc[k] * inv, acc[k + 1] * inv, T());
+      *reinterpret_cast<uint32_t*>(out + k) = gone ? 0u : pack2(acc[k] * inv, acc[k + 1] * inv, T());
   }
 }
 

@@ -945,6 +945,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const bool busy = (row & ~31) < seg.rows;    // the warp has rows of the tile
       const int node = (seg.rt * kR + min(row, seg.rows - 1)) / group;
       float m = -INFINITY, l = 0.0f;               // reference maximum and sum of this group's tiles
+      bool lost = false;                           // the row's node has no walk to node 0
       for (int j = w; j < n; j += 2) {
         const int t = t0 + j, f = (tile0 + j) % kFactSlots;
         wait_use(sh.fact, kFactSlots, tile0 + j);
@@ -954,7 +955,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (busy) {
           uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
           const bool tail = (int64_t)t * kTK + kTK > len;
-          if (tail && !visible(seg, c.parent, node, t, bits)) bad |= SPECDEC_DEVERR_BAD_TREE;
+          if (tail && !visible(seg, c.parent, node, t, bits)) lost = true;
           __syncwarp();
           bool masked = tail;
 #pragma unroll
@@ -1065,10 +1066,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // ---- the segment's end: both groups' results joined, half of the head each
       wait_or_give_up(sh, smem_addr(&sh.o_full), g & 1u);
       tc_fence_after();
-      stats[w * kR + row] = make_float2(m, l);
+      if (lost) bad |= SPECDEC_DEVERR_BAD_TREE;
+      stats[w * kR + row] = make_float2(m, lost ? kLostRow : l);
       named_bar_sync(1, kSoftmaxThreads);
       if (busy) {
-        const float2 s0 = stats[row], s1 = stats[kR + row];
+        float2 s0 = stats[row], s1 = stats[kR + row];
+        const bool gone = s0.y == kLostRow || s1.y == kLostRow;
+        if (gone) s0 = s1 = make_float2(-INFINITY, 0.0f);   // a row of zeros
         const float mm = fmaxf(s0.x, s1.x), ref = mm == -INFINITY ? 0.0f : mm;
         const float f0 = ex2(s0.x - ref), f1 = ex2(s1.x - ref);
         const float lsum = s0.y * f0 + s1.y * f1;
@@ -1111,13 +1115,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         // values that are not finite were left out of the tiles that hold nodes:
         // the rows that see their keys get them now
-        if (poison && live) {
+        if (poison && live && !gone) {
           T* out = nullptr;
           if (seg.whole)
             out = static_cast<T*>(a.out) + ((seg.q.first + gr / group) * a.q_heads + seg.h * group + gr % group) * (int64_t)D;
           left_out<T, FP8, D>(a.c, seg, gr / group, w * (D / 2), out, part.sums + (slot * kR + row) * D);
         }
-        if (live && !seg.whole && w == 0) part.stats[slot * kR + row] = make_float2(mm, lsum);
+        if (live && !seg.whole && w == 0) part.stats[slot * kR + row] = make_float2(mm, gone ? kLostRow : lsum);
       }
       tc_fence_before();
       named_bar_sync(1, kSoftmaxThreads);   // the sums are read before queries lie over them
