@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a, const i
   int64_t first;
   int32_t n;
   const int64_t len = c.lengths[b];
-  __shared__ int bad;
+  __shared__ uint32_t bad;
   if (threadIdx.x == 0) bad = 0;
   __syncthreads();  // every thread has read the length that thread 0 may replace
   if (!node_range(c.cu, b, c.N, first, n) || len < 0) {
@@ -393,21 +393,27 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a, const i
   }
   const int32_t acc = a.accepted[b];
   const int32_t* pages = c.table + b * c.geo.table_stride;
-  bool ok = acc >= 0 && (acc < n || (acc == 0 && n == 0));
-  uint32_t why = SPECDEC_DEVERR_BAD_TREE;
-  if (ok && a.path) {
-    for (int d = threadIdx.x; d < acc; d += blockDim.x) {
-      const int32_t at = a.path[first + d], before = d ? a.path[first + d - 1] : 0;
-      if (at <= before || at >= n) bad = 1;
-      else if (cache_row(c.geo, pages, len + at) < 0 || cache_row(c.geo, pages, len + d + 1) < 0) bad = 2;
+  uint32_t why = acc >= 0 && (acc < n || (acc == 0 && n == 0)) ? 0u : (uint32_t)SPECDEC_DEVERR_BAD_TREE;
+  if (!why && n) {
+    // the slots that the new length takes in, len .. len + acc, are the cache's own,
+    // for chains too: an append may have left their rows out
+    if (len + acc >= min((int64_t)c.geo.max_pages * c.geo.page_size, (int64_t)INT32_MAX)) {
+      why = SPECDEC_DEVERR_BAD_CACHE;
+    } else {
+      for (int d = threadIdx.x; d <= acc; d += blockDim.x) {
+        uint32_t found = cache_row(c.geo, pages, len + d) < 0 ? SPECDEC_DEVERR_BAD_CACHE : 0u;
+        if (a.path && d < acc) {
+          const int32_t at = a.path[first + d], before = d ? a.path[first + d - 1] : 0;
+          if (at <= before || at >= n) found |= SPECDEC_DEVERR_BAD_TREE;
+          else if (cache_row(c.geo, pages, len + at) < 0) found |= SPECDEC_DEVERR_BAD_CACHE;
+        }
+        if (found) atomicOr(&bad, found);
+      }
     }
   }
   __syncthreads();
-  if (bad) {
-    ok = false;
-    if (bad == 2) why = SPECDEC_DEVERR_BAD_CACHE;
-  }
-  if (!ok) {
+  why |= bad;
+  if (why) {
     if (threadIdx.x == 0) {
       atomicOr(c.err, why);
       a.out_lengths[b] = (int32_t)len;

@@ -53,3 +53,33 @@ def test_rows_of_malformed_trees_are_zeros(V, cache, nodes, ctx, up):
         else:
             assert torch.equal(out[j], good[j]), j
     assert torch.equal(out[nodes:], good[nodes:])
+
+
+# ---- commits over slots that are not there -------------------------------------------
+
+@pytest.mark.parametrize("path", [False, True])
+@pytest.mark.parametrize("what", ["table", "page", "last page", "root page", "length"])
+def test_commit_keeps_the_length_where_slots_are_missing(V, path, what):
+    # request 1's accepted rows stood (partly) in slots that no page holds: append
+    # left them out, and the length must not take them in
+    s = Step(ctx=[5, 14, 3], nodes=[4, 6, 5], cache=E4, page=4, seed=8, poison=False)
+    table, lengths = s.table.clone(), s.lengths.clone()
+    if what == "table":
+        lengths[1] = table.shape[1] * 4 - 4                 # slots 16 .. 19 of the table's 20, of 5 to take in
+    elif what == "length":
+        lengths[1] = 2 ** 31 - 3
+    else:
+        table[1, {"page": 4, "last page": 4, "root page": 3}[what]] = {"page": s.num_pages, "last page": -1, "root page": 1 << 30}[what]
+    c = s.cache(V)
+    c.append(s.new_k, s.new_v, table, lengths, s.cu)
+    assert V.get_error() == BAD_CACHE
+    before = [t.clone() for t in (s.k.view(torch.uint8), s.v.view(torch.uint8), s.ks, s.vs)]
+    got = c.commit(table, lengths, s.cu, i32([2, 4, 0]), i32([1, 2, -1, -1] + [1, 2, 3, 4, -1, -1] + [-1] * 5) if path else None)
+    assert V.get_error() == BAD_CACHE and V.get_error() == 0
+    assert got.tolist() == [8, int(lengths[1]), 4]
+    for now, was in zip((s.k.view(torch.uint8), s.v.view(torch.uint8), s.ks, s.vs), before):
+        assert torch.equal(now, was)                         # rows 1, 2, ... stand where they belong
+    # the last slot of the last page is a slot like any other
+    lengths[1] = s.table.shape[1] * 4 - 5
+    assert c.commit(s.table, lengths, s.cu, i32([2, 4, 0])).tolist() == [8, s.table.shape[1] * 4, 4]
+    assert V.get_error() == 0
