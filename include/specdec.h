@@ -383,9 +383,10 @@ int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
  * tree is larger than SPECDEC_MAX_TREE_NODES, write nothing, and neither do those of 2^31 or more tiles of 128 rows x 128 keys
  * (SPECDEC_DEVERR_BAD_CACHE).  Waits inside the kernel are bounded: one that runs out
  * sets SPECDEC_DEVERR_TIMEOUT, and the call's outputs are then undefined.  Of an
- * e4m3 cache's values, rows whose scale is below 2^-20 of the largest among 32
- * neighbouring slots lose bits, and scales below 2^-60 (append writes none) count as
- * about 2^-60.
+ * e4m3 cache's values in the context, rows whose scale is below 2^-20 of the largest
+ * among 32 neighbouring slots may lose bits (in the nodes' slots, which not every row
+ * sees, and in those within 127 of them they do not), and scales below 2^-60 (append
+ * writes none) count as about 2^-60.
  *   workspace  device memory of at least specdec_tree_attention_workspace()
  *              bytes, 16-byte aligned, no initial contents; calls that may
  *              overlap need one each */

@@ -57,6 +57,7 @@ constexpr int kScoreWarp = 2 * kGroupWarps + kFinishWarps, kValueWarp = kScoreWa
 constexpr int kLoaders = 2;                          // loader l takes tiles l, l + 2, ... of the range
 constexpr int kTileThreads = (kScoreWarp + 4) * 32;    // a whole warpgroup: registers move between those
 constexpr int kW = 32;                               // scores of a row that a thread holds at once (64 took 4 % longer)
+constexpr float kLeastScale = 8.673617379884035e-19f;   // 2^-60: smaller scales of values count as this
 constexpr int kFactSlots = 8;                        // tiles whose key facts are held (5 are needed)
 
 template <typename T, bool FP8, int D>
@@ -74,15 +75,21 @@ struct TileLayout {
   static constexpr int V = K + KS * KB;
   static constexpr int RAW = V + VS * VB;
   static constexpr int KF = RAW + (FP8 ? RS * RB : 0);             // [slot][key] scale of the key
-  static constexpr int VF = KF + (FP8 ? kFactSlots * kTK * 4 : 0);   // [slot][key] factor of the values (f16 pair)
+  // [slot][key] factor of the values (f16 pair); kWide tiles: log2 of their scale
+  static constexpr int VF = KF + (FP8 ? kFactSlots * kTK * 4 : 0);
   // f16 rows over 8-bit caches: values are widened exactly (by a power of two) and
   // the rest of their scale, in [1, 2), is applied to the weights in 32 bits; a
   // rounded factor and product would add two errors of f16's own size to the result
   static constexpr bool EXACT = FP8 && std::is_same<T, __half>::value;
-  static constexpr int MF = VF + (FP8 ? kFactSlots * kTK * 4 : 0);   // [slot][key] that rest
+  // [slot][key] that rest; kWide tiles: 1 / scale
+  static constexpr int MF = VF + (FP8 ? kFactSlots * kTK * 4 : 0);
   static constexpr int STATS = Q;                      // over the queries, once a segment's products are done
-  static constexpr int BYTES = MF + (EXACT ? kFactSlots * kTK * 4 : 0) + 1024;   // and room to align
+  static constexpr int BYTES = MF + (FP8 ? kFactSlots * kTK * 4 : 0) + 1024;   // and room to align
 };
+
+// What a tile's keys ask for besides the products.
+constexpr int kClean = 0, kDirty = 1;
+constexpr int kWide = 2;   // dirty, and the scales of its values differ too much for one factor
 
 struct TileShared {
   uint64_t k_full[4], k_empty[4];
@@ -93,7 +100,7 @@ struct TileShared {
   uint64_t q_full, o_full;
   uint32_t live[kFactSlots][4];     // keys of a tile that the cache holds
   float vexp[kFactSlots][4];        // 8-bit caches: 32 keys' values are held as v 2^-vexp
-  int dirty[kFactSlots];            // the tile holds nodes, or misses keys
+  int dirty[kFactSlots];            // kDirty: the tile holds nodes, or misses keys; kWide as well
   float rowf[kR];
   uint32_t tmem;
   int poison;                       // some tile with nodes held a value that is not finite (stays set)
@@ -439,6 +446,157 @@ __device__ __noinline__ void left_out(const CacheArgs& c, const Segments& s, int
   }
 }
 
+// One tile's scores of this thread's row become weights: one pass, kW keys at a time.
+// Weights are 2^(e - m), m a whole number that follows the running maximum only when
+// that is kLazy above it: what has been summed, the row's O_w (`summed`: there is
+// one) and the tile's weights so far are then multiplied by a power of two, which is
+// exact.  The largest weight lies in [2^kHead, 2^(kHead + kLazy)]: f16 weights keep
+// their bits far below the largest, and the maximum may lag by 2^kLazy.
+template <typename T, bool FP8, int D, bool WIDE>
+__device__ __forceinline__ void tile_scores(uint32_t ts, uint32_t to, uint32_t base_s, int f, const float* vexp,
+                                            const uint32_t* bits, bool masked, float rowf, bool summed, float& m, float& l) {
+  using L = TileLayout<T, FP8, D>;
+  using E = typename std::conditional<FP8, __half, T>::type;
+  constexpr float kLazy = 8.0f;
+  constexpr float kHead = std::is_same<E, __half>::value ? 6.0f : 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < kTK / kW; ++i) {
+    const float of = WIDE ? 1.0f : rowf;   // kWide: in the scores already
+    const uint64_t rowf2 = pair(of, of);
+    float s[kW], shift = 0.0f;
+    if constexpr (FP8 && !WIDE) shift = vexp[i];   // 8-bit caches: the values' exponent
+    tc_ld32(ts + i * kW, s);
+    if constexpr (FP8) {
+#pragma unroll
+      for (int k = 0; k < kW; k += 16) {
+        uint64_t kf[8];
+        lds_pairs(base_s + L::KF + (f * kTK + i * kW + k) * 4, kf);
+#pragma unroll
+        for (int z = 0; z < 8; ++z) unpair(mul2(pair(s[k + 2 * z], s[k + 2 * z + 1]), kf[z]), s[k + 2 * z], s[k + 2 * z + 1]);
+      }
+    }
+    if (masked) {
+      const uint32_t see = i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3];
+      if constexpr (WIDE) {
+        const uint64_t row2 = pair(rowf, rowf);
+#pragma unroll
+        for (int k = 0; k < kW; k += 16) {
+          uint64_t lv[8];
+          lds_pairs(base_s + L::VF + (f * kTK + i * kW + k) * 4, lv);
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            unpair(fma2(pair(s[k + 2 * z], s[k + 2 * z + 1]), row2, lv[z]), s[k + 2 * z], s[k + 2 * z + 1]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kW; ++k)
+        if (!((see >> k) & 1u)) s[k] = -INFINITY;
+    }
+    float q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q[k] = fmaxf(s[2 * k], s[2 * k + 1]);
+#pragma unroll
+    for (int k = 8; k < kW; k += 8)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) q[x] = max3(q[x], s[k + 2 * x], s[k + 2 * x + 1]);
+    const float mx = fmaxf(max3(q[0], q[1], q[2]), q[3]);
+    const float most = mx == -INFINITY ? mx : fmaf(mx, of, shift);
+    const bool move = most > m + kLazy || (m == -INFINITY && most != -INFINITY);
+    if (__any_sync(0xFFFFFFFFu, move)) {
+      const float to_m = move ? ceilf(most) : m;
+      const float fix = move ? ex2(m - to_m) : 1.0f;
+      m = to_m;
+      if (summed || i > 0) {
+        tc_wait_st();   // what is read back here has been stored
+        l *= fix;
+        if (i > 0) {
+#pragma unroll 1
+          for (int p = 0; p < i; ++p) {
+            uint32_t w16[16];
+            tc_ld16(ts + p * 16, w16);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w16[k] = shrink(w16[k], fix, E());
+            tc_st16(ts + p * 16, w16);
+          }
+        }
+        if (summed) {
+#pragma unroll 1
+          for (int p = 0; p < D / 16; ++p) {
+            uint32_t o[16];
+            tc_ld16(to + p * 16, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
+            tc_st16(to + p * 16, o);
+          }
+        }
+      }
+    }
+    // weights, rounded to 16 bits for the product with V (half a step
+    // each at most) and summed unrounded
+    const float ref = (m == -INFINITY ? 0.0f : m) - kHead;
+    const float add = shift - ref;
+    const uint64_t add_2 = pair(add, add);
+    uint64_t sum[2] = {0, 0};
+    uint32_t p[kW / 2];
+    constexpr bool REST = L::EXACT || WIDE;
+    [[maybe_unused]] uint64_t rest[REST ? kW / 2 : 1];   // of the values' scales
+    if constexpr (REST) {
+      lds_pairs(base_s + L::MF + (f * kTK + i * kW) * 4, rest);
+      lds_pairs(base_s + L::MF + (f * kTK + i * kW) * 4 + 64, rest + 8);
+    }
+#pragma unroll
+    for (int k = 0; k < kW; k += 2) {
+      float e0, e1;
+      unpair(fma2(pair(s[k], s[k + 1]), rowf2, add_2), e0, e1);
+      e0 = ex2(e0);
+      e1 = ex2(e1);
+      if constexpr (WIDE) sum[(k >> 1) & 1] = fma2(pair(e0, e1), rest[k / 2], sum[(k >> 1) & 1]);
+      else sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(e0, e1));
+      if constexpr (L::EXACT && !WIDE) unpair(mul2(pair(e0, e1), rest[k / 2]), e0, e1);
+      p[k / 2] = pack2(e0, e1, E());
+    }
+    tc_st16(ts + i * (kW / 2), p);
+    float s0, s1;
+    unpair(add2(sum[0], sum[1]), s0, s1);
+    if constexpr (FP8) l = fmaf(s0 + s1, WIDE ? 1.0f : __uint_as_float((uint32_t)(127 - (int)shift) << 23), l);
+    else l += s0 + s1;
+  }
+}
+
+// The same for kWide tiles, out of line: they are rare, and their code among the
+// others' cost all tiles 4 to 8 % (299 us -> 312 to 325).
+template <typename T, bool FP8, int D>
+__device__ __noinline__ float2 wide_scores(uint32_t ts, uint32_t to, uint32_t base_s, int f, uint4 see, float rowf,
+                                           bool summed, float m, float l) {
+  const uint32_t bits[4] = {see.x, see.y, see.z, see.w};
+  tile_scores<T, FP8, D, true>(ts, to, base_s, f, nullptr, bits, true, rowf, summed, m, l);
+  return make_float2(m, l);
+}
+
+// Whether a tile with nodes is a kWide one, by the scales of its values (4 a lane;
+// `most`: the largest of 32 keys, as bits); what the other roles need is then written
+// here, out of line for the same reason.
+template <typename T, int D>
+__device__ __noinline__ bool wide_facts(char* smem, int f, float4 vs, uint32_t most) {
+  using L = TileLayout<T, true, D>;
+  const int lane = threadIdx.x & 31;
+  const float* vv = &vs.x;
+  uint32_t least = most;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (vv[k] > 0.0f) least = min(least, __float_as_uint(vv[k]));
+  if (!__any_sync(0xFFFFFFFFu, (most >> 23) > (least >> 23) + 20)) return false;
+  float lv[4], inv[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    lv[k] = vv[k] == vv[k] ? __log2f(fmaxf(vv[k], kLeastScale)) : vv[k];
+    inv[k] = lv[k] == lv[k] ? ex2(-lv[k]) : 1.0f;   // hidden keys' weights of 0 stay 0
+  }
+  reinterpret_cast<float4*>(smem + L::VF)[f * (kTK / 4) + lane] = make_float4(lv[0], lv[1], lv[2], lv[3]);
+  reinterpret_cast<float4*>(smem + L::MF)[f * (kTK / 4) + lane] = make_float4(inv[0], inv[1], inv[2], inv[3]);
+  return true;
+}
+
 template <typename T, bool FP8, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
     attend_tile_kernel(const AttendArgs a, const int box, const bool grouped, const __grid_constant__ CUtensorMap kmap,
@@ -446,10 +604,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using L = TileLayout<T, FP8, D>;
   using E = typename std::conditional<FP8, __half, T>::type;
   constexpr int CH = D / 8;                      // 16-byte chunks of an operand row
-  // the largest weight lies in [2^kHead, 2^(kHead + kLazy)]: f16 weights keep
-  // their bits far below the largest, and the maximum may lag by 2^kLazy
-  constexpr float kLazy = 8.0f;
-  constexpr float kHead = std::is_same<E, __half>::value ? 6.0f : 0.0f;
   extern __shared__ char smem_raw[];
   __shared__ ScanShared scan;
   __shared__ __align__(8) TileShared sh;
@@ -763,11 +917,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // 2^-20 of the largest keep f16's full precision (bf16 rows: the factor and
         // its products with the values are rounded to f16, an eighth of what the
         // result's own rounding is).
+        // That serves keys which every row sees.  In a tile with nodes a row must not
+        // lose bits to the scale of a key that is hidden from it.  Where such a tile's
+        // scales are more than 2^20 apart (kWide) the values are widened as they are,
+        // log2 of the scale is added to the scores, so that each row's weights carry the
+        // scales of the keys that it sees, and the weights' sum takes them out again.
+        // (All tiles with nodes that way: 64 requests of 9 nodes 281 us instead of 257.)
         // (Slot n % 8 is free: the slot waits above imply that the products of tile
         // n - 5 are done.)
         const int f = n % kFactSlots;
         if (lane < 4) sh.live[f][lane] = live;
-        if (lane == 0) sh.dirty[f] = dirty;
+        int kind = dirty ? kDirty : kClean;
         if constexpr (FP8) {
           float* kk = &ks.x;
           float* vv = &vs.x;
@@ -780,25 +940,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+          if (dirty && wide_facts<T, D>(smem, f, vs, most)) kind = kWide;
           const int b = most ? max((int)(most >> 23) - 127 - 5, -80) : 0;   // 122 at most
           const float by = __uint_as_float((uint32_t)(127 - b) << 23);
           if ((lane & 7) == 0) sh.vexp[f][lane >> 3] = (float)b;
           reinterpret_cast<float4*>(smem + L::KF)[f * (kTK / 4) + lane] = ks;
-          if constexpr (L::EXACT) {
-            float rest[4];
+          if (kind != kWide) {
+            if constexpr (L::EXACT) {
+              float rest[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t e = __float_as_uint(vv[k]) & 0x7F800000u;   // 2^exponent
-              const bool split = e != 0 && e != 0x7F800000u;
-              rest[k] = split ? vv[k] / __uint_as_float(e) : 1.0f;       // exact
-              if (split) vv[k] = __uint_as_float(e);
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t e = __float_as_uint(vv[k]) & 0x7F800000u;   // 2^exponent
+                const bool split = e != 0 && e != 0x7F800000u;
+                rest[k] = split ? vv[k] / __uint_as_float(e) : 1.0f;       // exact
+                if (split) vv[k] = __uint_as_float(e);
+              }
+              reinterpret_cast<float4*>(smem + L::MF)[f * (kTK / 4) + lane] = make_float4(rest[0], rest[1], rest[2], rest[3]);
             }
-            reinterpret_cast<float4*>(smem + L::MF)[f * (kTK / 4) + lane] = make_float4(rest[0], rest[1], rest[2], rest[3]);
+            reinterpret_cast<uint4*>(smem + L::VF)[f * (kTK / 4) + lane] =
+                make_uint4(pack2(vv[0] * by, vv[0] * by, __half()), pack2(vv[1] * by, vv[1] * by, __half()),
+                           pack2(vv[2] * by, vv[2] * by, __half()), pack2(vv[3] * by, vv[3] * by, __half()));
           }
-          reinterpret_cast<uint4*>(smem + L::VF)[f * (kTK / 4) + lane] =
-              make_uint4(pack2(vv[0] * by, vv[0] * by, __half()), pack2(vv[1] * by, vv[1] * by, __half()),
-                         pack2(vv[2] * by, vv[2] * by, __half()), pack2(vv[3] * by, vv[3] * by, __half()));
         }
+        if (lane == 0) sh.dirty[f] = kind;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
       }
@@ -814,12 +978,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int n = 0, t = seg.t0; seg.more; ++n) {
       const int f = n % kFactSlots;
       wait_use(sh.fact, kFactSlots, n);
-      const bool dirty = sh.dirty[f] != 0;
+      const bool dirty = sh.dirty[f] != kClean;
       const uint32_t live = sh.live[f][pw];
       const int nodes = seg.q.len - t * kTK - pw * 32;      // the warp's keys from here on are nodes
       const uint32_t dst = base_s + L::V + (n % L::VS) * L::VB;
       uint32_t own = 0;
-      if constexpr (FP8) own = reinterpret_cast<const uint32_t*>(smem + L::VF)[f * kTK + pw * 32 + lane];
+      if constexpr (FP8) {
+        own = reinterpret_cast<const uint32_t*>(smem + L::VF)[f * kTK + pw * 32 + lane];
+        if (sh.dirty[f] == kWide) own = 0x3C003C00u;   // 1: the scales are in the weights
+      }
       wait_use(sh.raw_full, L::RS, n);
       bool hit = false;
       if constexpr (FP8) {
@@ -964,98 +1131,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             masked |= lv != 0xFFFFFFFFu;
             bits[i] &= lv;
           }
-          // One pass over the scores, kW keys at a time.  Weights are 2^(e - m),
-          // m a whole number that follows the running maximum only when that is
-          // kLazy above it: what has been summed, the row's O_w and the tile's
-          // weights so far are then multiplied by a power of two, which is exact.
-          const uint32_t fk_s = base_s + L::KF + f * kTK * 4;
-          const uint64_t rowf2 = pair(rowf, rowf);
-#pragma unroll 1
-          for (int i = 0; i < kTK / kW; ++i) {
-            float s[kW], shift = 0.0f;
-            if constexpr (FP8) shift = sh.vexp[f][i];   // 8-bit caches: the values' exponent
-            tc_ld32(ts + i * kW, s);
-            if constexpr (FP8) {
-#pragma unroll
-              for (int k = 0; k < kW; k += 16) {
-                uint64_t f[8];
-                lds_pairs(fk_s + (i * kW + k) * 4, f);
-#pragma unroll
-                for (int z = 0; z < 8; ++z) unpair(mul2(pair(s[k + 2 * z], s[k + 2 * z + 1]), f[z]), s[k + 2 * z], s[k + 2 * z + 1]);
-              }
-            }
-            if (masked) {
-              const uint32_t see = i == 0 ? bits[0] : i == 1 ? bits[1] : i == 2 ? bits[2] : bits[3];
-#pragma unroll
-              for (int k = 0; k < kW; ++k)
-                if (!((see >> k) & 1u)) s[k] = -INFINITY;
-            }
-            float q[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) q[k] = fmaxf(s[2 * k], s[2 * k + 1]);
-#pragma unroll
-            for (int k = 8; k < kW; k += 8)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) q[x] = max3(q[x], s[k + 2 * x], s[k + 2 * x + 1]);
-            const float mx = fmaxf(max3(q[0], q[1], q[2]), q[3]);
-            const float most = mx == -INFINITY ? mx : fmaf(mx, rowf, shift);
-            const bool move = most > m + kLazy || (m == -INFINITY && most != -INFINITY);
-            if (__any_sync(0xFFFFFFFFu, move)) {
-              const float to_m = move ? ceilf(most) : m;
-              const float fix = move ? ex2(m - to_m) : 1.0f;
-              m = to_m;
-              if (j >= 2 || i > 0) {
-                tc_wait_st();   // what is read back here has been stored
-                l *= fix;
-                if (i > 0) {
-#pragma unroll 1
-                  for (int p = 0; p < i; ++p) {
-                    uint32_t w16[16];
-                    tc_ld16(ts + p * 16, w16);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) w16[k] = shrink(w16[k], fix, E());
-                    tc_st16(ts + p * 16, w16);
-                  }
-                }
-                if (j >= 2) {
-#pragma unroll 1
-                  for (int p = 0; p < D / 16; ++p) {
-                    uint32_t o[16];
-                    tc_ld16(to + p * 16, o);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
-                    tc_st16(to + p * 16, o);
-                  }
-                }
-              }
-            }
-            // weights, rounded to 16 bits for the product with V (half a step
-            // each at most) and summed unrounded
-            const float ref = (m == -INFINITY ? 0.0f : m) - kHead;
-            const float add = shift - ref;
-            const uint64_t add_2 = pair(add, add);
-            uint64_t sum[2] = {0, 0};
-            uint32_t p[kW / 2];
-            uint64_t rest[L::EXACT ? kW / 2 : 1];   // of the values' scales
-            if constexpr (L::EXACT) {
-              lds_pairs(base_s + L::MF + (f * kTK + i * kW) * 4, rest);
-              lds_pairs(base_s + L::MF + (f * kTK + i * kW) * 4 + 64, rest + 8);
-            }
-#pragma unroll
-            for (int k = 0; k < kW; k += 2) {
-              float e0, e1;
-              unpair(fma2(pair(s[k], s[k + 1]), rowf2, add_2), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(e0, e1));
-              if constexpr (L::EXACT) unpair(mul2(pair(e0, e1), rest[k / 2]), e0, e1);
-              p[k / 2] = pack2(e0, e1, E());
-            }
-            tc_st16(ts + i * (kW / 2), p);
-            float s0, s1;
-            unpair(add2(sum[0], sum[1]), s0, s1);
-            if constexpr (FP8) l = fmaf(s0 + s1, __uint_as_float((uint32_t)(127 - (int)shift) << 23), l);
-            else l += s0 + s1;
+          if (FP8 && masked && sh.dirty[f] == kWide) {
+            const float2 ml = wide_scores<T, FP8, D>(ts, to, base_s, f, make_uint4(bits[0], bits[1], bits[2], bits[3]), rowf, j >= 2, m, l);
+            m = ml.x;
+            l = ml.y;
+          } else {
+            tile_scores<T, FP8, D, false>(ts, to, base_s, f, sh.vexp[f], bits, masked, rowf, j >= 2, m, l);
           }
           tc_wait_st();
         }

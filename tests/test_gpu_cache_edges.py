@@ -83,3 +83,28 @@ def test_commit_keeps_the_length_where_slots_are_missing(V, path, what):
     lengths[1] = s.table.shape[1] * 4 - 5
     assert c.commit(s.table, lengths, s.cu, i32([2, 4, 0])).tolist() == [8, s.table.shape[1] * 4, 4]
     assert V.get_error() == 0
+
+
+# ---- hidden rows of any size -----------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,head_dim", [(BF, 128), (HF, 128), (BF, 64), (HF, 64)])
+@pytest.mark.parametrize("nodes,ctx", [(4, 50), (40, 50), (40, 900), (200, 0)])
+@pytest.mark.parametrize("scale", [1e30, 1e4, 1e-30, math.inf, math.nan])
+def test_scales_of_hidden_nodes_reach_no_row(V, dtype, head_dim, nodes, ctx, scale):
+    # one node's values are larger (or smaller) than all others' by far: its siblings
+    # do not see it, and keep every bit of theirs
+    s = Step(ctx=[ctx, 11], nodes=[nodes, 40], tree="star", dtype=dtype, cache=E4, head_dim=head_dim, seed=9)
+    page, off = s.row(0, ctx + 2)
+    s.vs[page, :, off] = scale
+    page, off = s.row(0, ctx + 1)
+    s.vs[page, 0, off] = 0.0                                # a row of zeros among them
+    out = s.cache(V).attend(s.q, *args(s))
+    want, big = s.attend()
+    assert V.get_error() == 0
+    if not math.isfinite(scale):                            # (0 x inf is NaN: no value of that row is finite)
+        assert not out[2].isfinite().any()
+        out[2], want[2], big[2] = 0, 0, 0
+    ok = (out.double() - want).abs() <= attend_tolerance(s, want, big)
+    # its own row may lie beyond f16, whose values from 65520 on round to infinity
+    ok |= out.isinf() & (want.abs() >= 65504) if dtype == HF else False
+    assert ok.all(), [r for r in range(s.N) if not ok[r].all()]
