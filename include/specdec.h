@@ -266,8 +266,9 @@ int specdec_tree_verify(specdec_handle_t h, const void* target_logits, int dtype
  * inverse of the cumulative weights in index order: the first v with
  * sum_{j <= v} w(j) > s_b sum_j w(j), w = max(0, p_n - q_n) after a rejection
  * (p_n where that is 0 everywhere) and w = p_gamma for the bonus, in sums held
- * to about 2^-44 of the total.  Entries that are not above 0 (NaN among them)
- * weigh nothing; a row without weight gives token 0.  Rows are not normalised.
+ * to about 2^-44 of the total (2^-36 where every rounding errs alike, for any V).
+ * Entries that are not above 0 (NaN among them) weigh nothing, and none may be
+ * infinite; a row without weight gives token 0.  Rows are not normalised.
  * out_tokens [N_t] and out_num_accepted [B] as in specdec_rejection_sample;
  * a request whose cu range is malformed or passes N_d writes nothing
  * (SPECDEC_DEVERR_BAD_CU).  One launch, no workspace: calls on one handle may

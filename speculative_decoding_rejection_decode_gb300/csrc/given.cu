@@ -7,7 +7,10 @@
 // sums decide a whole number and are held to about 2^-44, as pairs of floats with
 // error-free additions (Knuth, Dekker).  Double precision would be bound by the
 // FP64 pipe (two lanes a clock here): even the scans over 64 piece sums and the
-// look through the last entries took longer in it than reading the rows.
+// look through the last entries took longer in it than reading the rows.  The errors
+// of K additions are themselves summed in 32 bits, which costs (K 2^-24)^2 of the sum
+// at the worst, so a lane hands its pair over to a double every 64 additions: 2^-36
+// then, whatever V is (additions that all err alike; usual rows come to 2^-44).
 //
 // A request is a cluster of C CTAs.  Each warp of the cluster sums a contiguous
 // piece of the row; the piece sums meet in distributed shared memory (no
@@ -32,6 +35,8 @@ constexpr int kGivenWarps = kGivenThreads / 32;
 constexpr int kMaxCtas = 8;   // CTAs of a request (the portable cluster size)
 constexpr int kMaxPieces = kMaxCtas * kGivenWarps;
 constexpr int kStep = 128;   // entries a warp reads at once: 4 per lane
+constexpr int kChunk = 4096; // entries that a warp sums in pairs of floats (64 additions a lane)
+constexpr int kLook = 16384; // entries that a warp looks through one by one
 
 // Two 32-bit operations in one instruction, each rounded as alone.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -54,7 +59,7 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {   // a - b: a
 }
 
 // Two running sums, each hi + lo with |lo| a few roundings of hi (Knuth's two-sum
-// gives the error of each addition exactly).
+// gives the error of each addition exactly; lo is not folded into hi on the way).
 struct Sums {
   uint64_t hi = 0, lo = 0;
   __device__ __forceinline__ void add(uint64_t w) {
@@ -184,25 +189,35 @@ __device__ __forceinline__ void add_steps(const Rows& R, int base, int v1, int l
 
 // Sum of the weights of [v0, v1) (v0 a multiple of 4) over the warp.
 __device__ __forceinline__ Exact piece_sum(const Rows& R, int v0, int v1, int lane) {
-  Sums s;
   constexpr int U = 4;
-  int base = v0;
-  if (R.vec) {   // whole steps: plain 16-byte loads, all under way before the first is used
-    if (R.q) {
-      for (; base + U * kStep <= v1; base += U * kStep) add_steps<true, true, U>(R, base, v1, lane, s);
-    } else {
-      for (; base + U * kStep <= v1; base += U * kStep) add_steps<false, true, U>(R, base, v1, lane, s);
+  double total = 0.0;
+  Exact x = {0.0f, 0.0f};
+  for (int base = v0; base < v1;) {
+    const int end = min(v1, base + kChunk);
+    Sums s;
+    if (R.vec) {   // whole steps: plain 16-byte loads, all under way before the first is used
+      if (R.q) {
+        for (; base + U * kStep <= end; base += U * kStep) add_steps<true, true, U>(R, base, v1, lane, s);
+      } else {
+        for (; base + U * kStep <= end; base += U * kStep) add_steps<false, true, U>(R, base, v1, lane, s);
+      }
     }
+    if (R.q) {
+      for (; base < end; base += U * kStep) add_steps<true, false, U>(R, base, v1, lane, s);
+    } else {
+      for (; base < end; base += U * kStep) add_steps<false, false, U>(R, base, v1, lane, s);
+    }
+    float a, b, c, d;
+    unpair(s.hi, a, b);
+    unpair(s.lo, c, d);
+    x = plus(renormed(a, c), renormed(b, d));
+    if (v1 - v0 <= kChunk) break;   // short pieces stay away from the FP64 pipe
+    total += (double)x.hi + (double)x.lo;
   }
-  if (R.q) {
-    for (; base < v1; base += U * kStep) add_steps<true, false, U>(R, base, v1, lane, s);
-  } else {
-    for (; base < v1; base += U * kStep) add_steps<false, false, U>(R, base, v1, lane, s);
+  if (v1 - v0 > kChunk) {
+    x.hi = (float)total;
+    x.lo = (float)(total - (double)x.hi);
   }
-  float a, b, c, d;
-  unpair(s.hi, a, b);
-  unpair(s.lo, c, d);
-  Exact x = plus(renormed(a, c), renormed(b, d));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = plus(x, shuffled(x, lane ^ o));
   return x;
@@ -365,30 +380,42 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
         const Exact e = shuffled(end[c], (winner - 1) & 31);
         if (winner > 0 && (winner - 1) / 32 == c) before = e;
       }
-      const int p0 = min(a.V, winner * len), p1 = min(a.V, p0 + len);
-      const int len2 = ((len + kGivenWarps - 1) / kGivenWarps + 3) & ~3;
-      const int q0 = min(p1, p0 + warp * len2), q1 = min(p1, q0 + len2);
-      const Exact part = piece_sum(R, q0, q1, lane);
-      if (lane == 0) parts[warp] = part;
-      __syncthreads();
-      int pick = -1, some = -1;
-      Exact at = before, pick_at = before, some_at = before;
+      int p0 = min(a.V, winner * len), p1 = min(a.V, p0 + len), part_len = len;
+      int pick, q0, q1;
+      Exact pick_at;
+      while (true) {
+        part_len = ((part_len + kGivenWarps - 1) / kGivenWarps + 3) & ~3;
+        q0 = min(p1, p0 + warp * part_len);
+        q1 = min(p1, q0 + part_len);
+        const Exact part = piece_sum(R, q0, q1, lane);
+        if (lane == 0) parts[warp] = part;
+        __syncthreads();
+        pick = -1;
+        int some = -1;
+        Exact at = before, some_at = before;
+        pick_at = before;
 #pragma unroll
-      for (int w = 0; w < kGivenWarps; ++w) {
-        const Exact y = parts[w], next = plus(at, y);
-        if (y.hi > 0.0f) {
-          some = w;
-          some_at = at;
-          if (pick < 0 && above(next, t)) {
-            pick = w;
-            pick_at = at;
+        for (int w = 0; w < kGivenWarps; ++w) {
+          const Exact y = parts[w], next = plus(at, y);
+          if (y.hi > 0.0f) {
+            some = w;
+            some_at = at;
+            if (pick < 0 && above(next, t)) {
+              pick = w;
+              pick_at = at;
+            }
           }
+          at = next;
         }
-        at = next;
-      }
-      if (pick < 0) {   // rounding at the piece's very end
-        pick = some;
-        pick_at = some_at;
+        if (pick < 0) {   // rounding at the piece's very end
+          pick = some;
+          pick_at = some_at;
+        }
+        if (part_len <= kLook || pick < 0) break;   // the same in every warp
+        p0 = min(p1, p0 + pick * part_len);
+        p1 = min(p1, p0 + part_len);
+        before = pick_at;
+        __syncthreads();   // parts are read before the next round's
       }
       if (pick == warp) {
         const int token = piece_find(R, q0, q1, pick_at, t, lane);
