@@ -340,8 +340,9 @@ typedef struct specdec_nodes {
  * nodes' positions on the way.
  *   k, v       [N, num_kv_heads, head_dim]
  *   q          [N, q_heads, head_dim] or NULL; out_q receives the turned rows,
- *              contiguous, and may be q itself (both or neither; a row whose position is outside the
- *              table or whose tree is malformed becomes zeros)
+ *              contiguous, and may be q itself where q is contiguous, but must not
+ *              overlap q, k or v in any other way (both or neither; a row whose
+ *              position is outside the table or whose tree is malformed becomes zeros)
  *   rotary     device float32 [rotary_positions, 2, rotary_dim / 2], cos then sin
  *              of each position, or NULL (q is then copied)
  *   rotary_dim leading dimensions that turn: a multiple of 16 up to head_dim.
@@ -410,7 +411,8 @@ int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache
  *   path          device [N], the accepted nodes of request b in its first
  *                 num_accepted[b] slots, rising (specdec_tree_verify's out_path);
  *                 NULL for chains, whose rows stand where they belong
- *   out_lengths   device [B]; may be nodes->lengths
+ *   out_lengths   device [B]; may be nodes->lengths itself, and overlaps no input
+ *                 otherwise
  * Slots behind the accepted ones keep their contents.  A count outside the
  * request's nodes or a path that does not rise moves nothing and leaves the
  * length (SPECDEC_DEVERR_BAD_TREE), and so does a new length that takes in a slot

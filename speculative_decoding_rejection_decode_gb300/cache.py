@@ -231,6 +231,8 @@ class KVCache:
             if t.shape != (N, self.num_kv_heads, self.head_dim) or t.dtype != out[0].dtype \
                     or t.device != self.device or not t.is_contiguous():
                 raise ValueError("out must be two contiguous [n_rows, num_kv_heads, head_dim] tensors")
+        if N and _overlap(*out):
+            raise ValueError("out must be two tensors of their own")
         dt = self._row_dtype(out[0])
         nodes = self._nodes(page_table, starts, cu_rows, None, N)
         if N:
@@ -281,13 +283,18 @@ class KVCache:
         new lengths, lengths + 1 + num_accepted (``out_lengths`` may be
         ``lengths`` itself)."""
         B, dev = cu_num_nodes.numel() - 1, self.device
-        if out_lengths is None:
+        given = out_lengths is not None
+        if not given:
             out_lengths = torch.empty(B, dtype=torch.int32, device=dev)
         for t, n, name in ((num_accepted, B, "num_accepted"), (out_lengths, B, "out_lengths"),
                            (path, None, "path")):
             if t is not None and (t.dtype != torch.int32 or t.device != dev or not t.is_contiguous()
                                   or (n is not None and t.numel() != n)):
                 raise ValueError(f"{name} must be a contiguous int32 tensor on the device")
+        if given and out_lengths.data_ptr() != lengths.data_ptr() and any(
+                t is not None and t.numel() and _overlap(out_lengths, t)
+                for t in (lengths, num_accepted, cu_num_nodes, path, page_table)):
+            raise ValueError("out_lengths must be lengths itself or overlap none of the inputs")
         # without a path nothing but the lengths changes; any N bounds cu then
         N = (1 << 31) - 1 if path is None else path.numel()
         nodes = self._nodes(page_table, lengths, cu_num_nodes, None, N)

@@ -366,6 +366,19 @@ bool rows_ok(const void* p, int64_t row, int64_t head) {
   return p && aligned16(p) && row % 8 == 0 && head % 8 == 0;
 }
 
+// Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte.
+bool meet(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes > 0 && b_bytes > 0 && (x < y ? y - x < (uintptr_t)a_bytes : x - y < (uintptr_t)b_bytes);
+}
+
+// The same for contiguous bytes and the span of strided 16-bit rows [N, heads, dim].
+bool meet_rows(const void* out, int64_t out_bytes, const void* p, int64_t row, int64_t head, int64_t N, int heads, int dim) {
+  const int64_t r = (N - 1) * row, h = (heads - 1) * head;
+  const int64_t first = (r < 0 ? r : 0) + (h < 0 ? h : 0), last = (r > 0 ? r : 0) + (h > 0 ? h : 0) + dim;
+  return N > 0 && meet(out, out_bytes, static_cast<const char*>(p) + 2 * first, 2 * (last - first));
+}
+
 // Checks a cache and its nodes and fills the kernels' view of them (all but the
 // error word).  any_dtype: rows of no type are passed (commit).
 int cache_args(const specdec_cache_t* cache, const specdec_nodes_t* nodes, int dtype, CacheArgs& c,
@@ -687,6 +700,15 @@ int specdec_cache_append(specdec_handle_t h, const specdec_cache_t* cache,
   if ((q != nullptr) != (out_q != nullptr)) return SPECDEC_ERR_INVALID_ARG;
   if (q && (q_heads <= 0 || q_heads > kMaxHeads || !rows_ok(q, q_row_stride, q_head_stride) || !aligned16(out_q)))
     return SPECDEC_ERR_INVALID_ARG;
+  if (q && nodes->N > 0) {   // rows are written while others are still to be read
+    const int64_t N = nodes->N, out_bytes = 2 * N * q_heads * cache->head_dim;
+    const int kv = cache->num_kv_heads, D = cache->head_dim;
+    const bool itself = out_q == q && (q_heads == 1 || q_head_stride == D) && (N == 1 || q_row_stride == (int64_t)q_heads * D);
+    if ((!itself && meet_rows(out_q, out_bytes, q, q_row_stride, q_head_stride, N, q_heads, D)) ||
+        meet_rows(out_q, out_bytes, k, k_row_stride, k_head_stride, N, kv, D) ||
+        meet_rows(out_q, out_bytes, v, v_row_stride, v_head_stride, N, kv, D))
+      return SPECDEC_ERR_INVALID_ARG;
+  }
   if (rotary && (!aligned16(rotary) || rotary_dim <= 0 || rotary_dim % 16 != 0 ||
                  rotary_dim > cache->head_dim || rotary_positions <= 0))
     return SPECDEC_ERR_INVALID_ARG;
@@ -720,6 +742,8 @@ int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
   if (rc != SPECDEC_OK) return rc;
   if (nodes->N > 0 && (!out_k || !out_v || !aligned16(out_k) || !aligned16(out_v)))
     return SPECDEC_ERR_INVALID_ARG;
+  const int64_t out_bytes = 2 * nodes->N * cache->num_kv_heads * cache->head_dim;
+  if (meet(out_k, out_bytes, out_v, out_bytes)) return SPECDEC_ERR_INVALID_ARG;
   if (!h) return SPECDEC_ERR_INVALID_ARG;
   DeviceGuard guard(h->device);
   if (!guard.ok()) return SPECDEC_ERR_CUDA;
@@ -750,6 +774,8 @@ int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
     return SPECDEC_ERR_INVALID_ARG;
   if (nodes->N > 0 && (!rows_ok(q, q_row_stride, q_head_stride) || !out || !aligned16(out)))
     return SPECDEC_ERR_INVALID_ARG;
+  if (meet_rows(out, 2 * nodes->N * q_heads * cache->head_dim, q, q_row_stride, q_head_stride, nodes->N, q_heads, cache->head_dim))
+    return SPECDEC_ERR_INVALID_ARG;
   if (!h) return SPECDEC_ERR_INVALID_ARG;
   const int64_t need =
       attend_workspace_bytes(nodes->B, nodes->N, cache->num_kv_heads, q_heads, cache->head_dim,
@@ -776,6 +802,13 @@ int specdec_cache_commit(specdec_handle_t h, const specdec_cache_t* cache,
   int rc = cache_args(cache, nodes, SPECDEC_BF16, a.c, true);
   if (rc != SPECDEC_OK) return rc;
   if (!num_accepted || !out_lengths) return SPECDEC_ERR_INVALID_ARG;
+  // a request's length is written while others' inputs are still to be read
+  const int64_t bytes = 4 * (int64_t)nodes->B;
+  if ((out_lengths != nodes->lengths && meet(out_lengths, bytes, nodes->lengths, bytes)) ||
+      meet(out_lengths, bytes, num_accepted, bytes) || meet(out_lengths, bytes, nodes->cu, bytes + 4) ||
+      (path && meet(out_lengths, bytes, path, 4 * nodes->N)) ||
+      meet(out_lengths, bytes, nodes->page_table, 4 * ((nodes->B - 1) * nodes->table_stride + nodes->max_pages)))
+    return SPECDEC_ERR_INVALID_ARG;
   if (!h) return SPECDEC_ERR_INVALID_ARG;
   DeviceGuard guard(h->device);
   if (!guard.ok()) return SPECDEC_ERR_CUDA;

@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from cache_reference import HALF_STEP, Step, ancestors, attend_tolerance
+from cache_reference import Step, ancestors, attend_tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,48 @@ def test_scales_of_hidden_nodes_reach_no_row(V, dtype, head_dim, nodes, ctx, sca
     # its own row may lie beyond f16, whose values from 65520 on round to infinity
     ok |= out.isinf() & (want.abs() >= 65504) if dtype == HF else False
     assert ok.all(), [r for r in range(s.N) if not ok[r].all()]
+
+
+# ---- outputs over inputs, at the C entries ---------------------------------------------------
+
+def test_outputs_over_inputs_are_refused_by_the_library(V):
+    import ctypes
+    from speculative_decoding_rejection_decode_gb300 import _lib
+    s = Step(ctx=[9, 2], nodes=[3, 4], kv_heads=2, group=2, seed=8, poison=False)
+    c, N, D = s.cache(V), s.N, 128
+    before = s.k.clone()
+    buf = torch.zeros(4, N * 8 * D, dtype=BF, device="cuda")
+    at, st = buf.data_ptr(), torch.cuda.current_stream().cuda_stream
+    i = torch.zeros(64, dtype=torch.int32, device="cuda")
+    i[32:34] = s.lengths
+    nodes = lambda **kw: ctypes.byref(_lib.specdec_nodes_t(**{**dict(
+        page_table=s.table.data_ptr(), table_stride=s.table.shape[1], max_pages=s.table.shape[1], lengths=s.lengths.data_ptr(),
+        cu=s.cu.data_ptr(), parent=None, B=2, N=N), **kw}))
+    wide = 8 * D     # rows of q, k and v side by side
+
+    def append(q=at, q_row=wide, out=at + 2 * N * wide, heads=4):
+        return _lib.specdec_cache_append(V.handle, c._ref, nodes(), _lib.SPECDEC_BF16, at + 8 * D, wide, D, at + 12 * D, wide, D,
+                                         q, q_row, D, heads, out, None, 0, 0, 0, st)
+
+    def attend(q, out, q_row=4 * D):
+        return _lib.specdec_tree_attention(V.handle, c._ref, nodes(), _lib.SPECDEC_BF16, q, q_row, D, 4, 1.0, out, None, 0, st)
+
+    invalid = _lib.SPECDEC_ERR_INVALID_ARG
+    for bad in (dict(out=at), dict(out=at + 16), dict(out=at + 2 * N * wide - 16), dict(q=at + 2 * N * wide, q_row=4 * D, out=at + 2 * N * wide + 16),
+                dict(q=at + 4 * N * wide, q_row=4 * D, out=at + 8 * D)):
+        assert append(**bad) == invalid, bad
+    for q, out in ((at, at), (at, at + 2 * (N - 1) * 4 * D), (at + 16, at)):
+        assert attend(q, out) == invalid
+    for out_k, out_v in ((at, at), (at, at + 2 * N * 2 * D - 16)):
+        assert _lib.specdec_cache_read(V.handle, c._ref, nodes(), _lib.SPECDEC_BF16, out_k, out_v, st) == invalid
+    p = i.data_ptr()
+    for acc, path, out, kw in ((p, None, p, {}), (p, p + 32, p + 32 + 4 * (N - 1), {}), (p, None, p + 132, dict(lengths=p + 128)),
+                               (p, None, p + 40, dict(cu=p + 32)), (p, None, s.table.data_ptr() + 4, {})):
+        assert _lib.specdec_cache_commit(V.handle, c._ref, nodes(**kw), acc, path, out, st) == invalid
+    torch.cuda.synchronize()
+    assert torch.equal(s.k, before) and V.get_error() == 0
+    # side by side, q itself and lengths themselves are fine
+    assert append() == 0 and append(q=at + 2 * N * wide, q_row=4 * D, out=at + 2 * N * wide) == 0
+    assert attend(at, at + 2 * N * 4 * D) == 0
+    assert _lib.specdec_cache_commit(V.handle, c._ref, nodes(lengths=p + 128), p, None, p + 128, st) == 0
+    assert i[32:34].tolist() == [10, 3] and V.get_error() == 0
