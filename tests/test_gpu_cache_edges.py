@@ -153,3 +153,102 @@ def test_outputs_over_inputs_are_refused_by_the_library(V):
     assert attend(at, at + 2 * N * 4 * D) == 0
     assert _lib.specdec_cache_commit(V.handle, c._ref, nodes(lengths=p + 128), p, None, p + 128, st) == 0
     assert i[32:34].tolist() == [10, 3] and V.get_error() == 0
+
+
+# ---- scores of any size ------------------------------------------------------------------
+
+def score_tolerance(s, want, big):
+    """attend_tolerance with the scores' errors taken from the scores.  A key's score
+    (base e) is off by at most D_s = head_dim 2^-24 scale sum |q k| (a float32 sum of
+    products) + 2^-22 |z| (the scale, to base 2, and the last addition, each rounded
+    to 32 bits) + 2^-20 (the exponential), and over 8-bit caches 2^-17 max |q|
+    scale sum |k| (the tile kernel's queries).  With weights w' ~ w e^d, |d_s| <= D_s,
+    the result moves by sum w (e^d - 1)(v - o) / sum w e^d, at most
+    sum w (e^D - 1) |v - o| / sum w e^-D."""
+    scale = s.head_dim ** -0.5
+    K, W = s.values("k"), s.values("v")
+    tol = attend_tolerance(s, want, big)
+    for b in range(s.B):
+        for i in range(s.nodes[b]):
+            r = s.firsts[b] + i
+            at = list(range(s.ctx[b])) + sorted(s.ctx[b] + j for j in ancestors(s.parents[b], i))
+            at = torch.tensor(at, device=K.device)
+            pages = torch.tensor(s.pages[b], device=K.device)[at // s.page]
+            k, v = K[pages, :, at % s.page], W[pages, :, at % s.page]
+            q = s.q[r].double().view(s.kv_heads, s.group, -1)
+            z = torch.einsum("hgd,shd->hgs", q, k) * scale
+            d = s.head_dim * 2.0 ** -24 * scale * torch.einsum("hgd,shd->hgs", q.abs(), k.abs()) + 2.0 ** -22 * z.abs() + 2.0 ** -20
+            if s.ks is not None:
+                d = d + 2.0 ** -17 * scale * q.abs().amax(-1, keepdim=True) * k.abs().sum(-1).t()[:, None]
+            w = torch.softmax(z, -1)
+            o = want[r].view(s.kv_heads, s.group, -1)
+            off = (v.transpose(0, 1)[:, None] - o[:, :, None]).abs()
+            # (weights of 1e-200 and less stay nothing whatever their error)
+            up = torch.where(w > 1e-200, w * torch.expm1(d.clamp(max=300.0)), 0.0)
+            moved = torch.einsum("hgs,hgsd->hgd", up, off) / (w * (-d).exp()).sum(-1, keepdim=True)
+            tol[r] += moved.reshape(s.heads, -1)
+    return tol
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (BF, E4), (HF, E4)])
+@pytest.mark.parametrize("nodes", [3, 40])                       # both kernels
+def test_every_row_of_extreme_scores(V, dtype, cache, nodes):
+    s = Step(ctx=[700], nodes=[nodes], dtype=dtype, cache=cache, seed=10)
+    s.q[0] *= 200.0                                             # one key takes all the weight
+    s.q[1] = 0.0                                                # all weights equal
+    for slot, by in ((3, 300.0), (300, -100.0), (690, 30.0)):    # far above and below the rest, early and late
+        page, off = s.row(0, slot)
+        if cache == E4:
+            s.ks[page, :, off] *= abs(by)
+        else:
+            s.k[page, :, off] = (s.k[page, :, off].float() * by).to(cache)
+    out = s.cache(V).attend(s.q, *args(s))
+    want, big = s.attend()
+    tol = score_tolerance(s, want, big)
+    assert V.get_error() == 0
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), [r for r in range(s.N) if not (err[r] <= tol[r]).all()]
+    assert float((tol <= 0.1 * big[..., None]).double().mean()) > 0.9   # the bound says something
+
+
+# ---- batches of unequal requests, long chains ------------------------------------------------
+
+@pytest.mark.parametrize("cache", [BF, E4])
+def test_one_large_request_among_many_small_ones(V, cache):
+    # 16 rows for the average request: the large one has 75 row tiles in the kernel
+    # for few rows, split over the ranges
+    s = Step(ctx=[(37 * i) % 301 for i in range(64)] + [3000] + [(53 * i) % 200 for i in range(64)], nodes=[1] * 64 + [300] + [1] * 64,
+             kv_heads=2, group=4, page=64, cache=cache, seed=3)
+    out = s.cache(V).attend(s.q, *args(s))
+    want, big = s.attend()
+    assert V.get_error() == 0
+    # float32 sums over up to 2^12 keys instead of the bound's 2^11
+    tol = attend_tolerance(s, want, big) + 2.0 ** -13 * big[..., None]
+    assert ((out.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+@pytest.mark.parametrize("ctx", [0, 77, 261])
+def test_long_chains(V, cache, ctx):
+    # a prompt: contexts that end inside a tile, chains past the largest tree
+    s = Step(ctx=[ctx, 5], nodes=[1100, 2], kv_heads=1, group=2, page=48, cache=cache, seed=4)
+    out = s.cache(V).attend(s.q, *args(s))
+    want, big = s.attend()
+    assert V.get_error() == 0
+    assert ((out.double() - want).abs() <= attend_tolerance(s, want, big)).all()
+
+
+# ---- a range that passes the rows --------------------------------------------------------------
+
+@pytest.mark.parametrize("tree", ["chain", "random"])
+def test_append_of_a_range_that_passes_the_rows(V, tree):
+    s = Step(ctx=[3, 20, 9], nodes=[4, 4, 4], tree=tree, page=8, seed=3, poison=False)
+    k0, v0 = s.k.clone(), s.v.clone()
+    s.cu[2] = 100                                               # of request 1, and request 2 starts there
+    s.cache(V).append(s.new_k, s.new_v, *args(s))
+    assert V.get_error() == BAD_CU and V.get_error() == 0
+    for now, was, new in ((s.k, k0, s.new_k), (s.v, v0, s.new_v)):
+        for j in range(4):
+            page, off = s.row(0, 3 + j)
+            assert torch.equal(now[page, :, off], new[j])
+        assert torch.equal(now[s.pages[1] + s.pages[2]], was[s.pages[1] + s.pages[2]])
