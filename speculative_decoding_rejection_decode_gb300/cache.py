@@ -28,10 +28,11 @@ def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0,
       "linear"   every angle divided by factor
       "base"     base * factor^(rotary_dim / (rotary_dim - 2)): the slowest pair
                  is stretched by factor, the fastest not at all
-      "by_parts" pairs that turn at least ``fast_turns`` times over
-                 trained_positions keep their angle, pairs that turn at most
-                 ``slow_turns`` times are divided by factor, with a linear ramp
-                 over the pair index between; cos and sin are multiplied by
+      "by_parts" the YaRN method (Peng et al. 2023): pairs that turn at least
+                 ``fast_turns`` times over trained_positions keep their angle,
+                 pairs that turn at most ``slow_turns`` times are divided by
+                 factor, with a linear ramp over the pair index between (its ends
+                 on whole pairs, rounded outward); cos and sin are multiplied by
                  1 + 0.1 ln(factor), which sharpens the softmax"""
     if positions < 1 or rotary_dim < 2 or rotary_dim % 2 or not factor >= 1.0 or not base > 1.0:
         raise ValueError("need positions >= 1, an even rotary_dim, factor >= 1 and base > 1")
@@ -51,9 +52,10 @@ def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0,
         def pair_of(turns):    # pair index whose angle passes `turns` circles
             return rotary_dim * math.log(trained_positions / (turns * 2 * math.pi)) / (2 * math.log(base))
 
-        lo = max(math.floor(pair_of(fast_turns)), 0)
-        hi = min(math.ceil(pair_of(slow_turns)), rotary_dim - 1)
-        kept = 1.0 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        # more turns lie at a smaller pair index, so lo < hi; either may lie beyond the
+        # pairs there are, which then all stand on the ramp or beside it
+        lo, hi = math.floor(pair_of(fast_turns)), math.ceil(pair_of(slow_turns))
+        kept = 1.0 - ((i - lo) / (hi - lo)).clamp(0.0, 1.0)
         freq = freq * kept + freq / factor * (1.0 - kept)
         gain = 1.0 + 0.1 * math.log(factor)
     elif scaling not in (None, "base"):
