@@ -25,6 +25,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
+constexpr int kRowsTile = 16;   // rows of an item's tile: one mma.sync
 
 template <bool FP8, int D>
 struct WarpTile {
@@ -126,11 +127,11 @@ __device__ __forceinline__ uint32_t nonfinite(uint4 w) {
   return got;
 }
 
-template <typename T, bool FP8, int D, int MT>
+template <typename T, bool FP8, int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendArgs a) {
   using W = WarpTile<FP8, D>;
   using E = typename std::conditional<FP8, __half, T>::type;   // type of the products' factors
-  constexpr int R = 16 * MT, KB = W::KB, TK = W::TK, CH = W::CH;
+  constexpr int R = kRowsTile, KB = W::KB, TK = W::TK, CH = W::CH;
   using L = WarpLayout<FP8, D, R>;
   constexpr int QCH = D / 8;
   extern __shared__ __align__(128) char smem[];
@@ -280,23 +281,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
     }
     __syncthreads();
 
-    float o[MT][D / 8][4];
-    float m[MT][2], l[MT][2];
+    float o[D / 8][4];
+    float m[2], l[2];
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.0f;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.0f;
+    for (int nt = 0; nt < D / 8; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < D / 8; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[mt][nt][k] = 0.0f;
-    }
-    float rf[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      rf[mt][0] = rowf[mt * 16 + qrow];
-      rf[mt][1] = rowf[mt * 16 + qrow + 8];
-    }
+      for (int k = 0; k < 4; ++k) o[nt][k] = 0.0f;
+    float rf[2];
+    rf[0] = rowf[qrow];
+    rf[1] = rowf[qrow + 8];
     for (int t = t0; t < t1; ++t) {
       issue(t + kStages - 1, ahead);
       const int now = rows_now[0];
@@ -310,22 +305,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
       if (live) {
         const uint32_t k_s = ring_s + ((t - t0) % kStages) * W::STAGE, v_s = k_s + KB * W::ROW;
         char* kv = ring + ((t - t0) % kStages) * W::STAGE;
-        float s[MT][KB / 8][4];
+        float s[KB / 8][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < KB / 8; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < KB / 8; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[mt][nt][k] = 0.0f;
+          for (int k = 0; k < 4; ++k) s[nt][k] = 0.0f;
         // scores: rows x keys, 16 of the head dimension at a time
 #pragma unroll
         for (int kk = 0; kk < D / 16; kk += (FP8 ? 2 : 1)) {
-          uint32_t qa[FP8 ? 2 : 1][MT][4];
+          uint32_t qa[FP8 ? 2 : 1][4];
 #pragma unroll
           for (int z = 0; z < (FP8 ? 2 : 1); ++z)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              ldm4(q_s + spread<QCH>(mt * 16 + (lane & 15), (kk + z) * 2 + (lane >> 4)) * 16, qa[z][mt]);
+            ldm4(q_s + spread<QCH>(lane & 15, (kk + z) * 2 + (lane >> 4)) * 16, qa[z]);
 #pragma unroll
           for (int np = 0; np < KB / 16; ++np) {
             uint32_t w[4];
@@ -338,15 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {  // 16 of the head dimension
                   const uint32_t b0 = e4m3x2_f16x2(w[2 * i + z]), b1 = e4m3x2_f16x2(w[2 * i + z] >> 16);
-#pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][2 * np + i], qa[z][mt], b0, b1, E());
+                  mma16816(s[2 * np + i], qa[z], b0, b1, E());
                 }
             } else {
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816(s[mt][2 * np], qa[0][mt], w[0], w[1], E());
-                mma16816(s[mt][2 * np + 1], qa[0][mt], w[2], w[3], E());
-              }
+              mma16816(s[2 * np], qa[0], w[0], w[1], E());
+              mma16816(s[2 * np + 1], qa[0], w[2], w[3], E());
             }
           }
         }
@@ -356,9 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
         const int64_t key0 = (int64_t)t * TK + warp * KB;
         const bool masked = live != (KB == 32 ? 0xFFFFFFFFu : (1u << (KB & 31)) - 1u) || key0 + KB > q.len;
         float iv[FP8 ? KB / 8 : 1][2];   // 1 / vs
-        float mx[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) mx[mt][0] = mx[mt][1] = -INFINITY;
+        float mx[2];
+        mx[0] = mx[1] = -INFINITY;
         auto sees = [&](int r, int key) -> bool {
           if (!((live >> key) & 1u)) return false;
           const int64_t j = key0 + key - q.len;
@@ -382,65 +368,56 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
               iv[nt][x] = __frcp_rn(vc);
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                float& e = s[mt][nt][2 * y + x];
-                e = FP8 ? fmaf(e * kf, rf[mt][y], lv) : e * rf[mt][y];
-                if (masked && !sees(mt * 16 + qrow + 8 * y, key)) e = -INFINITY;
-                mx[mt][y] = fmaxf(mx[mt][y], e);
-              }
+            for (int y = 0; y < 2; ++y) {
+              float& e = s[nt][2 * y + x];
+              e = FP8 ? fmaf(e * kf, rf[y], lv) : e * rf[y];
+              if (masked && !sees(qrow + 8 * y, key)) e = -INFINITY;
+              mx[y] = fmaxf(mx[y], e);
+            }
           }
         bool moved = false;
-        float ref[MT][2], fix[MT][2];   // weights are 2^(e - ref)
+        float ref[2], fix[2];   // weights are 2^(e - ref)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float v = mx[mt][y];
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-            const float mn = fmaxf(m[mt][y], v);
-            moved |= mn != m[mt][y];
-            const float at = mn == -INFINITY ? 0.0f : mn;
-            fix[mt][y] = ex2(m[mt][y] - at);
-            ref[mt][y] = at - kHeadroom<E>;
-            m[mt][y] = mn;
-          }
+        for (int y = 0; y < 2; ++y) {
+          float v = mx[y];
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+          const float mn = fmaxf(m[y], v);
+          moved |= mn != m[y];
+          const float at = mn == -INFINITY ? 0.0f : mn;
+          fix[y] = ex2(m[y] - at);
+          ref[y] = at - kHeadroom<E>;
+          m[y] = mn;
+        }
         if (__any_sync(0xFFFFFFFFu, moved)) {
+          l[0] *= fix[0];
+          l[1] *= fix[1];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            l[mt][0] *= fix[mt][0];
-            l[mt][1] *= fix[mt][1];
-#pragma unroll
-            for (int nt = 0; nt < D / 8; ++nt) {
-              o[mt][nt][0] *= fix[mt][0];
-              o[mt][nt][1] *= fix[mt][0];
-              o[mt][nt][2] *= fix[mt][1];
-              o[mt][nt][3] *= fix[mt][1];
-            }
+          for (int nt = 0; nt < D / 8; ++nt) {
+            o[nt][0] *= fix[0];
+            o[nt][1] *= fix[0];
+            o[nt][2] *= fix[1];
+            o[nt][3] *= fix[1];
           }
         }
         // weights; rounded to 16 bits for the product with V (at most half a
         // step of a factor in [0, 1] each), summed unrounded
-        uint32_t p[MT][KB / 16][4];
+        uint32_t p[KB / 16][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < KB / 8; ++nt) {
+          float w[4];
 #pragma unroll
-          for (int nt = 0; nt < KB / 8; ++nt) {
-            float w[4];
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const float e = ex2(s[mt][nt][2 * y + x] - ref[mt][y]);
-                w[2 * y + x] = e;
-                if constexpr (FP8) l[mt][y] += s[mt][nt][2 * y + x] == -INFINITY ? 0.0f : e * iv[nt][x];
-                else l[mt][y] += e;
-              }
-            p[mt][nt / 2][(nt & 1) * 2] = pack2(w[0], w[1], E());
-            p[mt][nt / 2][(nt & 1) * 2 + 1] = pack2(w[2], w[3], E());
-          }
+            for (int x = 0; x < 2; ++x) {
+              const float e = ex2(s[nt][2 * y + x] - ref[y]);
+              w[2 * y + x] = e;
+              if constexpr (FP8) l[y] += s[nt][2 * y + x] == -INFINITY ? 0.0f : e * iv[nt][x];
+              else l[y] += e;
+            }
+          p[nt / 2][(nt & 1) * 2] = pack2(w[0], w[1], E());
+          p[nt / 2][(nt & 1) * 2 + 1] = pack2(w[2], w[3], E());
+        }
         // A value that is not finite belongs to the rows that see its key and
         // to no other (0 x inf would reach them through the product): it is
         // added to those and taken out of the block.  Only blocks that some
@@ -452,15 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
           if (__any_sync(0xFFFFFFFFu, any)) {
             for (int key = 0; key < KB; ++key)
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
+              for (int nt = 0; nt < D / 8; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < D / 8; ++nt)
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const int d = FP8 ? (nt >> 1) * 16 + quad * 4 + (k & 1) * 2 + (nt & 1) : nt * 8 + quad * 2 + (k & 1);
-                    const float v = v_element<T, FP8, CH>(vb, key, d);
-                    if (!isfinite(v) && sees(mt * 16 + qrow + 8 * (k >> 1), key)) o[mt][nt][k] += v;
-                  }
+                for (int k = 0; k < 4; ++k) {
+                  const int d = FP8 ? (nt >> 1) * 16 + quad * 4 + (k & 1) * 2 + (nt & 1) : nt * 8 + quad * 2 + (k & 1);
+                  const float v = v_element<T, FP8, CH>(vb, key, d);
+                  if (!isfinite(v) && sees(qrow + 8 * (k >> 1), key)) o[nt][k] += v;
+                }
             __syncwarp();
             for (int x = lane; x < KB * CH; x += 32) {
               const uint32_t got = nonfinite<T, FP8>(*reinterpret_cast<uint4*>(vb + x * 16));
@@ -489,18 +464,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
                 const uint32_t x = __byte_perm(w[2 * i], 0, 0x3120), y = __byte_perm(w[2 * i + 1], 0, 0x3120);
                 const uint32_t x0 = e4m3x2_f16x2(x), x1 = e4m3x2_f16x2(x >> 16);
                 const uint32_t y0 = e4m3x2_f16x2(y), y1 = e4m3x2_f16x2(y >> 16);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  mma16816(o[mt][dt + 2 * i], p[mt][kk], x0, y0, E());
-                  mma16816(o[mt][dt + 2 * i + 1], p[mt][kk], x1, y1, E());
-                }
+                mma16816(o[dt + 2 * i], p[kk], x0, y0, E());
+                mma16816(o[dt + 2 * i + 1], p[kk], x1, y1, E());
               }
             } else {
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816(o[mt][dt], p[mt][kk], w[0], w[1], E());
-                mma16816(o[mt][dt + 1], p[mt][kk], w[2], w[3], E());
-              }
+              mma16816(o[dt], p[kk], w[0], w[1], E());
+              mma16816(o[dt + 1], p[kk], w[2], w[3], E());
             }
           }
       }
@@ -512,23 +481,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
     float* merge = reinterpret_cast<float*>(smem);                       // [warps][R][D]
     float2* stats = reinterpret_cast<float2*>(smem + kWarps * R * D * 4);  // [warps][R]
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int y = 0; y < 2; ++y) {
+      float v = l[y];
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+      const int r = qrow + 8 * y;
+      if (r >= rows) continue;
+      if (quad == 0) stats[warp * R + r] = make_float2(m[y], v);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float v = l[mt][y];
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-        const int r = mt * 16 + qrow + 8 * y;
-        if (r >= rows) continue;
-        if (quad == 0) stats[warp * R + r] = make_float2(m[mt][y], v);
+      for (int nt = 0; nt < D / 8; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < D / 8; ++nt)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int d = FP8 ? (nt >> 1) * 16 + quad * 4 + x * 2 + (nt & 1) : nt * 8 + quad * 2 + x;
-            merge[(warp * R + r) * D + d] = o[mt][nt][2 * y + x];
-          }
-      }
+        for (int x = 0; x < 2; ++x) {
+          const int d = FP8 ? (nt >> 1) * 16 + quad * 4 + x * 2 + (nt & 1) : nt * 8 + quad * 2 + x;
+          merge[(warp * R + r) * D + d] = o[nt][2 * y + x];
+        }
+    }
     __syncthreads();
     const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 > 0 ? 0 : 1);
     for (int x = tid; x < rows * D; x += kThreads) {
@@ -560,17 +527,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
   if (bad) atomicOr(c.err, bad);
 }
 
-template <typename T, bool FP8, int D, int MT>
+template <typename T, bool FP8, int D>
 int launch_warp(const AttendArgs& a, int num_sms, cudaStream_t st) {
-  using L = WarpLayout<FP8, D, 16 * MT>;
+  using L = WarpLayout<FP8, D, kRowsTile>;
   constexpr int TK = WarpTile<FP8, D>::TK;
-  auto kern = attend_warp_kernel<T, FP8, D, MT>;
+  auto kern = attend_warp_kernel<T, FP8, D>;
   static std::atomic<uint64_t> done{0};
   if (!allow_shared(kern, L::BYTES, done)) return SPECDEC_ERR_CUDA;
   const int G = num_sms;
   kern<<<G, kThreads, L::BYTES, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  return a.whole ? SPECDEC_OK : launch_join<T, 16 * MT, TK, D>(a, G, st);
+  return a.whole ? SPECDEC_OK : launch_join<T, kRowsTile, TK, D>(a, G, st);
 }
 
 // Rows (nodes x heads that share a kv head) of an average request: what the
@@ -587,16 +554,16 @@ constexpr int kWarpRows = 16;
 
 template <typename T, bool FP8>
 int launch_dim(const AttendArgs& a, int num_sms, cudaStream_t st) {
-  return a.c.head_dim == 128 ? launch_warp<T, FP8, 128, 1>(a, num_sms, st) : launch_warp<T, FP8, 64, 1>(a, num_sms, st);
+  return a.c.head_dim == 128 ? launch_warp<T, FP8, 128>(a, num_sms, st) : launch_warp<T, FP8, 64>(a, num_sms, st);
 }
 
 }  // namespace
 
 int64_t attend_workspace_bytes(int B, int64_t N, int kv_heads, int q_heads, int head_dim, int64_t capacity, int num_sms) {
   const bool tile = average_rows(B, N, kv_heads, q_heads) > kWarpRows;
-  if (whole_items(B, N, kv_heads, q_heads, capacity, tile ? 128 : 16, num_sms)) return 0;
+  if (whole_items(B, N, kv_heads, q_heads, capacity, tile ? 128 : kRowsTile, num_sms)) return 0;
   if (tile) return attend_tile_workspace(head_dim, num_sms);
-  return head_dim == 128 ? Partials<16, 128>::bytes(num_sms) : Partials<16, 64>::bytes(num_sms);
+  return head_dim == 128 ? Partials<kRowsTile, 128>::bytes(num_sms) : Partials<kRowsTile, 64>::bytes(num_sms);
 }
 
 int launch_attend(const AttendArgs& args, int cache_dtype, int dtype, int num_sms, cudaStream_t st) {
@@ -604,7 +571,7 @@ int launch_attend(const AttendArgs& args, int cache_dtype, int dtype, int num_sm
   AttendArgs a = args;
   const CacheArgs& c = a.c;
   const bool tile = average_rows(c.B, c.N, c.geo.kv_heads, a.q_heads) > kWarpRows;
-  a.whole = whole_items(c.B, c.N, c.geo.kv_heads, a.q_heads, (int64_t)c.geo.max_pages * c.geo.page_size, tile ? 128 : 16, num_sms);
+  a.whole = whole_items(c.B, c.N, c.geo.kv_heads, a.q_heads, (int64_t)c.geo.max_pages * c.geo.page_size, tile ? 128 : kRowsTile, num_sms);
   const bool fp8 = cache_dtype == SPECDEC_E4M3;
   a.item_cost = fp8 && !tile ? kItemCostWarp8 : kItemCost;
   if (tile) return launch_attend_tile(a, cache_dtype, dtype, num_sms, st);

@@ -508,8 +508,7 @@ int launch_read(const ReadArgs& a, int cache_dtype, int dtype, int num_sms, cuda
   return fp8 ? read_of<__half, true>(a, num_sms, st) : read_of<__half, false>(a, num_sms, st);
 }
 
-int launch_commit(const CommitArgs& a, int cache_dtype, int num_sms, cudaStream_t st) {
-  (void)num_sms;
+int launch_commit(const CommitArgs& a, int cache_dtype, cudaStream_t st) {
   const int row_bytes = a.c.head_dim * (cache_dtype == SPECDEC_E4M3 ? 1 : 2);
   commit_kernel<<<a.c.B, 256, 0, st>>>(a, row_bytes);
   return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;

@@ -89,7 +89,7 @@ struct GivenArgs {
 // cache_dtype, dtype: SPECDEC_BF16, SPECDEC_F16 or (cache_dtype) SPECDEC_E4M3.
 int launch_append(const AppendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
 int launch_read(const ReadArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
-int launch_commit(const CommitArgs& a, int cache_dtype, int num_sms, cudaStream_t st);
+int launch_commit(const CommitArgs& a, int cache_dtype, cudaStream_t st);
 int launch_attend(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
 int64_t attend_workspace_bytes(int B, int64_t N, int kv_heads, int q_heads, int head_dim, int64_t capacity, int num_sms);
 int launch_given(const GivenArgs& a, int num_sms, cudaStream_t st);

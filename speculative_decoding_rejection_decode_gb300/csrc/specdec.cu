@@ -816,7 +816,7 @@ int specdec_cache_commit(specdec_handle_t h, const specdec_cache_t* cache,
   a.accepted = num_accepted;
   a.path = path;
   a.out_lengths = out_lengths;
-  return launch_commit(a, cache->dtype, h->num_sms, static_cast<cudaStream_t>(stream));
+  return launch_commit(a, cache->dtype, static_cast<cudaStream_t>(stream));
 }
 
 int specdec_get_error(specdec_handle_t h, int* device_error, void* stream) {
