@@ -545,11 +545,15 @@ int launch_warp(const AttendArgs& a, int num_sms, cudaStream_t st) {
 int64_t average_rows(int B, int64_t N, int kv_heads, int q_heads) {
   return (N + B - 1) / B * (q_heads / kv_heads);
 }
-// Up to these the warp kernel, above them the tile kernel.  4 rows, contexts of 500
-// / 64 up to 8191 / 4 of 30000, 8 kv heads of 128, us a call, warp and tile kernel:
-// bf16 12.7 and 15.1 / 220 and 222 / 89 and 92, e4m3 13.8 and 15.8 / 208 and 249 /
-// 81 and 90; 16 rows: bf16 14.8 and 15.8 / 241 and 228 / 93 and 94, e4m3 15.4 and
-// 16.6 / 220 and 259 / 84 and 94.
+// Up to these (a tile of the warp kernel) the warp kernel, above them the tile kernel.
+// One context of 500 / 64 up to 8191 / 4 of 30000 / 200 up to 1500, 8 kv heads of 128,
+// device us, warp and tile kernel:
+//   4 rows  bf16 11.7 13.7 / 204 211 / 85 89 / 138 177, e4m3 12.7 15.1 / 204 234 / 80 89 / 155 216
+//   12      bf16 14.0 13.7 / 213 214 / 89 91 / 165 178, e4m3 14.7 15.4 / 217 241 / 84 91 / 186 219
+//   16      bf16 14.8 13.7 / 221 214 / 90 91 / 177 178, e4m3 15.4 15.7 / 224 242 / 85 92 / 195 221
+//   20      bf16 15.1 13.7 / 394 217 / 157 92 / 298 179, e4m3 15.7 15.7 / 403 247 / 146 94 / 330 220
+// The average decides: in a batch of one large request among many small ones, the
+// large one takes a tile of 16 rows at a time.
 constexpr int kWarpRows = 16;
 
 template <typename T, bool FP8>

@@ -60,10 +60,11 @@ struct PlanArgs {
 // Whether a call leaves items whole: contexts of at most 4 tiles by the page
 // table's width, and no more items than two for each CTA.  One launch and no
 // workspace then; splitting such items only pays where they are many and ragged.
-// us a call, whole and split, 32 query and 8 kv heads of 128: 1 request of 1 node over
-// 60 / 250 / 480 keys 7.6 and 8.6 / 9.7 and 11.0 / 12.0 and 10.9, of 29 nodes 14.0 and
-// 17.4 / 18.1 and 22.2 / 19.8 and 22.8; 32 requests of 1 node 12.3 and 13.8 / 17.8 and
-// 22.1 / 24.2 and 29.4, of 29 nodes 23.2 and 28.0 / 32.1 and 48.2 / 37.3 and 54.8.
+// Device us, whole and split, 32 query and 8 kv heads of 128, bf16: 1 request of 1 node
+// over 60 / 250 / 480 keys 7.5 and 8.9 / 9.3 and 10.9 / 11.6 and 11.0 (the second launch
+// and the workspace take the host more than these 0.6), of 29 nodes 12.3 and 15.6 /
+// 14.0 and 20.0 / 15.7 and 20.8; 32 requests of 1 node 12.3 and 13.8 / 15.8 and 19.8 /
+// 23.0 and 27.3, of 29 nodes 21.2 and 26.0 / 31.1 and 40.0 / 36.4 and 46.2.
 inline bool whole_items(int B, int64_t N, int kv_heads, int q_heads, int64_t capacity, int rows, int num_sms) {
   const int64_t avg = (N + B - 1) / B * (q_heads / kv_heads);
   return capacity <= 512 && (int64_t)B * kv_heads * ((avg + rows - 1) / rows) <= 2 * (int64_t)num_sms;

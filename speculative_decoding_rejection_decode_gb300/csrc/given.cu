@@ -436,9 +436,11 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
 
 int launch_given(const GivenArgs& a, int num_sms, cudaStream_t st) {
   // CTAs of a request: as many as give every warp a step of its row and as one wave
-  // holds (4 CTAs of an SM are resident).  us with half, with these and with twice as many: 256
-  // requests of 151936 entries 74, 59, 59 (1, 2, 4 CTAs); 128 40, 34, 35; 512 of 128000 -, 95,
-  // 91 (1, 2); 400 of 32000 -, 24, 27; 8 of 32000 12, 11 (4, 8, in an earlier form).
+  // holds (4 CTAs of an SM are resident).  us with half, with these and with twice as many:
+  // 64 requests of 151936 entries 24, 21, - (4, 8 CTAs); 128 40, 34, 35; 160 60, 44, 46; 256
+  // 72, 59, 60; 304 of 128000 66, 55, 59.  Of more requests than a wave of single CTAs
+  // takes, short rows lose by two of them (400 of 32000 24 and 26) and long ones would
+  // gain (512 of 128000 95 and 91, 480 of 151936 108 and 102): one serves both.
   int C = kMaxCtas;
   while (C > 1 && (a.V < C * kGivenWarps * kStep || (int64_t)a.B * C > (int64_t)num_sms * 4)) C >>= 1;
   cudaLaunchConfig_t cfg = {};
