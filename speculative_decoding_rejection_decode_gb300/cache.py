@@ -228,13 +228,13 @@ class KVCache:
             shape = (N, self.num_kv_heads, self.head_dim)
             out = (torch.empty(shape, dtype=dtype, device=self.device),
                    torch.empty(shape, dtype=dtype, device=self.device))
+        elif out[0].numel() and _overlap(*out):
+            raise ValueError("out must be two tensors of their own")
         N = out[0].shape[0]
         for t in out:
             if t.shape != (N, self.num_kv_heads, self.head_dim) or t.dtype != out[0].dtype \
                     or t.device != self.device or not t.is_contiguous():
                 raise ValueError("out must be two contiguous [n_rows, num_kv_heads, head_dim] tensors")
-        if N and _overlap(*out):
-            raise ValueError("out must be two tensors of their own")
         dt = self._row_dtype(out[0])
         nodes = self._nodes(page_table, starts, cu_rows, None, N)
         if N:

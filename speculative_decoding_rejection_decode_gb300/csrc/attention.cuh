@@ -61,8 +61,8 @@ struct PlanArgs {
 // table's width, and no more items than two for each CTA.  One launch and no
 // workspace then; splitting such items only pays where they are many and ragged.
 // Device us, whole and split, 32 query and 8 kv heads of 128, bf16: 1 request of 1 node
-// over 60 / 250 / 480 keys 7.5 and 8.9 / 9.3 and 10.9 / 11.6 and 11.0 (the second launch
-// and the workspace take the host more than these 0.6), of 29 nodes 12.3 and 15.6 /
+// over 60 / 250 / 480 keys 7.5 and 8.9 / 9.3 and 10.9 / 11.6 and 11.0 (a call,
+// host included: 17.0 and 23.2, for the second launch and the workspace), of 29 nodes 12.3 and 15.6 /
 // 14.0 and 20.0 / 15.7 and 20.8; 32 requests of 1 node 12.3 and 13.8 / 15.8 and 19.8 /
 // 23.0 and 27.3, of 29 nodes 21.2 and 26.0 / 31.1 and 40.0 / 36.4 and 46.2.
 inline bool whole_items(int B, int64_t N, int kv_heads, int q_heads, int64_t capacity, int rows, int num_sms) {
