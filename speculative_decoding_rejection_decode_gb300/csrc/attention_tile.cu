@@ -24,10 +24,10 @@
 // The two groups' results are joined when a segment ends.
 //
 // Measured (32 or 64 query and 8 kv heads of 128): bf16, 2 to 9 nodes over up to 8191
-// keys, 64 requests, 1.30 GB in 219 us = 5.9 TB/s; 8 nodes over 100k and 131k keys 947
-// MB in 160 us = 5.9 TB/s: bound by memory.  e4m3, 29 nodes over 6000 to 16000 keys, 32
-// requests: 805 MB and 177 GFLOP in 298 us, bound by the chain of roles that a tile
-// passes (its scores, exponentials, weights and values widened: no unit above 36 % of
+// keys, 64 requests, 1.30 GB in 217 us = 6.0 TB/s; 8 nodes over 100k and 131k keys 947
+// MB in 158 us = 6.0 TB/s: bound by memory.  e4m3, 29 nodes over 6000 to 16000 keys, 32
+// requests: 805 MB and 177 GFLOP in 300 us, bound by the chain of roles that a tile
+// passes (its scores, exponentials, weights and values widened: no unit above 37 % of
 // its rate, the softmax's and finishers' instructions the largest part).
 //
 // 8-bit keys meet the queries in e4m3 products: a query is the sum of two (f16:
