@@ -417,7 +417,8 @@ int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache
  * request's nodes or a path that does not rise moves nothing and leaves the
  * length (SPECDEC_DEVERR_BAD_TREE), and so does a new length that takes in a slot
  * which the page table or the cache does not hold (SPECDEC_DEVERR_BAD_CACHE; for
- * chains too). */
+ * chains too).  Rows that append left out for their position or tree alone are
+ * seen in the error word only. */
 int specdec_cache_commit(specdec_handle_t h, const specdec_cache_t* cache,
                          const specdec_nodes_t* nodes, const int32_t* num_accepted,
                          const int32_t* path, int32_t* out_lengths, void* stream);
