@@ -388,7 +388,8 @@ int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
  * e4m3 cache's values in the context, rows whose scale is below 2^-20 of the largest
  * among 32 neighbouring slots may lose bits (in the nodes' slots, which not every row
  * sees, and in those within 127 of them they do not), and scales below 2^-60 (append
- * writes none) count as about 2^-60.
+ * writes none) count as about 2^-60.  Scales of values that a row sees together may lie
+ * 2^100 apart; beyond that a key with the smaller may lose its weight.
  *   workspace  device memory of at least specdec_tree_attention_workspace()
  *              bytes, 16-byte aligned, no initial contents; calls that may
  *              overlap need one each */

@@ -81,10 +81,9 @@ struct TileLayout {
   // the rest of their scale, in [1, 2), is applied to the weights in 32 bits; a
   // rounded factor and product would add two errors of f16's own size to the result
   static constexpr bool EXACT = FP8 && std::is_same<T, __half>::value;
-  // [slot][key] that rest; kWide tiles: 1 / scale
-  static constexpr int MF = VF + (FP8 ? kFactSlots * kTK * 4 : 0);
+  static constexpr int MF = VF + (FP8 ? kFactSlots * kTK * 4 : 0);   // [slot][key] that rest
   static constexpr int STATS = Q;                      // over the queries, once a segment's products are done
-  static constexpr int BYTES = MF + (FP8 ? kFactSlots * kTK * 4 : 0) + 1024;   // and room to align
+  static constexpr int BYTES = MF + (EXACT ? kFactSlots * kTK * 4 : 0) + 1024;   // and room to align
 };
 
 // What a tile's keys ask for besides the products.
@@ -537,8 +536,22 @@ __device__ __forceinline__ void tile_scores(uint32_t ts, uint32_t to, uint32_t b
     const float add = shift - ref;
     const uint64_t add_2 = pair(add, add);
     uint64_t sum[2] = {0, 0};
+    if constexpr (WIDE) {   // exponentials of their own: the weights may underflow where these do not
+#pragma unroll
+      for (int k = 0; k < kW; k += 16) {
+        uint64_t lv[8];
+        lds_pairs(base_s + L::VF + (f * kTK + i * kW + k) * 4, lv);
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const float s0 = s[k + 2 * z], s1 = s[k + 2 * z + 1];
+          float a0, a1;
+          unpair(lv[z], a0, a1);
+          sum[z & 1] = add2(sum[z & 1], pair(s0 == -INFINITY ? 0.0f : ex2(s0 + add - a0), s1 == -INFINITY ? 0.0f : ex2(s1 + add - a1)));
+        }
+      }
+    }
     uint32_t p[kW / 2];
-    constexpr bool REST = L::EXACT || WIDE;
+    constexpr bool REST = L::EXACT && !WIDE;
     [[maybe_unused]] uint64_t rest[REST ? kW / 2 : 1];   // of the values' scales
     if constexpr (REST) {
       lds_pairs(base_s + L::MF + (f * kTK + i * kW) * 4, rest);
@@ -550,9 +563,8 @@ __device__ __forceinline__ void tile_scores(uint32_t ts, uint32_t to, uint32_t b
       unpair(fma2(pair(s[k], s[k + 1]), rowf2, add_2), e0, e1);
       e0 = ex2(e0);
       e1 = ex2(e1);
-      if constexpr (WIDE) sum[(k >> 1) & 1] = fma2(pair(e0, e1), rest[k / 2], sum[(k >> 1) & 1]);
-      else sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(e0, e1));
-      if constexpr (L::EXACT && !WIDE) unpair(mul2(pair(e0, e1), rest[k / 2]), e0, e1);
+      if constexpr (!WIDE) sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(e0, e1));
+      if constexpr (REST) unpair(mul2(pair(e0, e1), rest[k / 2]), e0, e1);
       p[k / 2] = pack2(e0, e1, E());
     }
     tc_st16(ts + i * (kW / 2), p);
@@ -586,14 +598,10 @@ __device__ __noinline__ bool wide_facts(char* smem, int f, float4 vs, uint32_t m
   for (int k = 0; k < 4; ++k)
     if (vv[k] > 0.0f) least = min(least, __float_as_uint(vv[k]));
   if (!__any_sync(0xFFFFFFFFu, (most >> 23) > (least >> 23) + 20)) return false;
-  float lv[4], inv[4];
+  float lv[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    lv[k] = vv[k] == vv[k] ? __log2f(fmaxf(vv[k], kLeastScale)) : vv[k];
-    inv[k] = lv[k] == lv[k] ? ex2(-lv[k]) : 1.0f;   // hidden keys' weights of 0 stay 0
-  }
+  for (int k = 0; k < 4; ++k) lv[k] = vv[k] == vv[k] ? __log2f(fmaxf(vv[k], kLeastScale)) : vv[k];
   reinterpret_cast<float4*>(smem + L::VF)[f * (kTK / 4) + lane] = make_float4(lv[0], lv[1], lv[2], lv[3]);
-  reinterpret_cast<float4*>(smem + L::MF)[f * (kTK / 4) + lane] = make_float4(inv[0], inv[1], inv[2], inv[3]);
   return true;
 }
 
@@ -921,7 +929,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // lose bits to the scale of a key that is hidden from it.  Where such a tile's
         // scales are more than 2^20 apart (kWide) the values are widened as they are,
         // log2 of the scale is added to the scores, so that each row's weights carry the
-        // scales of the keys that it sees, and the weights' sum takes them out again.
+        // scales of the keys that it sees; their sum is of the weights without them.
         // (All tiles with nodes that way: 64 requests of 9 nodes 281 us instead of 257.)
         // (Slot n % 8 is free: the slot waits above imply that the products of tile
         // n - 5 are done.)

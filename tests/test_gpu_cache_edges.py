@@ -252,3 +252,20 @@ def test_append_of_a_range_that_passes_the_rows(V, tree):
             page, off = s.row(0, 3 + j)
             assert torch.equal(now[page, :, off], new[j])
         assert torch.equal(now[s.pages[1] + s.pages[2]], was[s.pages[1] + s.pages[2]])
+
+
+@pytest.mark.parametrize("scale,other", [(1e30, 0.01), (1e30, 0.0), (1e18, 2.0 ** -49)])
+@pytest.mark.parametrize("ctx", [0, 40])
+def test_rows_that_see_a_large_scale_keep_the_others_weights(V, scale, other, ctx):
+    # the values of the small ones are nothing beside the large one, their softmax
+    # weights are not (a chain: nodes from 2 on see both)
+    s = Step(ctx=[ctx], nodes=[30], cache=E4, seed=5)
+    s.vs[...] = 0.01
+    for slot, by in ((ctx + 1, scale), (ctx, other)):
+        page, off = s.row(0, slot)
+        s.vs[page, :, off] = by
+    out = s.cache(V).attend(s.q, *args(s))
+    want, big = s.attend()
+    # a scale of 0 counts as 2^-60
+    tol = attend_tolerance(s, want, big) + 448 * 2.0 ** -60
+    assert ((out.double() - want).abs() <= tol).all()
