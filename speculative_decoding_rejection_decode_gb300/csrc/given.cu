@@ -20,7 +20,7 @@
 // Measured: 256 requests of 1 to 8 drafts and 151936 entries, of which 226 reject one
 // (two rows each), 293 MB in 59 us = 5.0 TB/s (the accept tests' few dependent loads
 // and the final look stand before and after the rows' stream); 8 requests of 32000
-// entries 7.9 us, latency.
+// entries 7.6 us, latency.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -188,13 +188,15 @@ __device__ __forceinline__ void add_steps(const Rows& R, int base, int v1, int l
   }
 }
 
-// Sum of the weights of [v0, v1) (v0 a multiple of 4) over the warp.
+// Sum of the weights of [v0, v1) (v0 a multiple of 4) over the warp; LONG: it may pass
+// kChunk entries.
+template <bool LONG>
 __device__ __forceinline__ Exact piece_sum(const Rows& R, int v0, int v1, int lane) {
   constexpr int U = 4;
   double total = 0.0;
   Exact x = {0.0f, 0.0f};
   for (int base = v0; base < v1;) {
-    const int end = min(v1, base + kChunk);
+    const int end = LONG ? min(v1, base + kChunk) : v1;
     Sums s;
     if (R.vec) {   // whole steps: plain 16-byte loads, all under way before the first is used
       if (R.q) {
@@ -212,10 +214,10 @@ __device__ __forceinline__ Exact piece_sum(const Rows& R, int v0, int v1, int la
     unpair(s.hi, a, b);
     unpair(s.lo, c, d);
     x = plus(renormed(a, c), renormed(b, d));
-    if (v1 - v0 <= kChunk) break;   // short pieces stay away from the FP64 pipe
+    if (!LONG || v1 - v0 <= kChunk) break;   // short pieces stay away from the FP64 pipe
     total += (double)x.hi + (double)x.lo;
   }
-  if (v1 - v0 > kChunk) {
+  if (LONG && v1 - v0 > kChunk) {
     x.hi = (float)total;
     x.lo = (float)(total - (double)x.hi);
   }
@@ -278,6 +280,9 @@ __device__ __forceinline__ Exact ld_cluster_sum(uint32_t addr) {
   return x;
 }
 
+// LONG: a warp's piece of the row passes kChunk entries.  (One kernel for both cost 8
+// requests of 32000 entries 0.4 us of 7.9.)
+template <bool LONG>
 __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a) {
   __shared__ __align__(8) Exact sums[2][kGivenWarps], parts[kGivenWarps];
   const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
   bool heavy_piece[kMaxPieces / 32];
   for (int round = 0; round < 2; ++round) {
     Exact own_sum = {0.0f, 0.0f};
-    if (ok) own_sum = piece_sum(R, v0, v1, lane);
+    if (ok) own_sum = piece_sum<LONG>(R, v0, v1, lane);
     if (lane == 0) sums[round][warp] = own_sum;
     cluster_sync_all();
     // the same order in every warp: lane l holds pieces l and l + 32
@@ -388,7 +393,7 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
         part_len = ((part_len + kGivenWarps - 1) / kGivenWarps + 3) & ~3;
         q0 = min(p1, p0 + warp * part_len);
         q1 = min(p1, q0 + part_len);
-        const Exact part = piece_sum(R, q0, q1, lane);
+        const Exact part = piece_sum<LONG>(R, q0, q1, lane);
         if (lane == 0) parts[warp] = part;
         __syncthreads();
         pick = -1;
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(const GivenArgs a)
           pick = some;
           pick_at = some_at;
         }
-        if (part_len <= kLook || pick < 0) break;   // the same in every warp
+        if (!LONG || part_len <= kLook || pick < 0) break;   // the same in every warp
         p0 = min(p1, p0 + pick * part_len);
         p1 = min(p1, p0 + part_len);
         before = pick_at;
@@ -455,7 +460,8 @@ int launch_given(const GivenArgs& a, int num_sms, cudaStream_t st) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, given_kernel, a) == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+  const bool is_long = a.V > C * kGivenWarps * kChunk;
+  return cudaLaunchKernelEx(&cfg, is_long ? given_kernel<true> : given_kernel<false>, a) == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
 }  // namespace specdec
