@@ -281,6 +281,60 @@ int specdec_rejection_sample_given(specdec_handle_t h, const float* target_probs
                                    int B, int V, int64_t n_draft_positions, int32_t* out_tokens,
                                    int32_t* out_num_accepted, void* stream);
 
+/* ---- log probabilities of given tokens --------------------------------------
+ * What a step answers beside its tokens, and what a drafter learns from: with
+ * p = softmax(row / T), for every token t of n_tokens
+ *   out_logprob[t]  = ln p(ids[t])
+ *   out_entropy[t]  = -sum_v p(v) ln p(v)
+ *   out_top_ids[t], out_top_logprobs[t]: the `top` entries with the largest logits
+ *                     (equal ones by rising index) and their ln p; slots past V
+ *                     are -1 and -inf
+ *   out_stats[t]    = (rho, log2 sum_v 2^((x_v - rho) c)), c = log2(e) / T, rho a logit:
+ *                     what specdec_logprobs_grad needs of the row
+ *   logits      device rows of V entries of `dtype` (SPECDEC_F32, _BF16 or _F16),
+ *               row_stride elements apart (>= V), num_rows of them, of any alignment
+ *   T           temperature, 2^-60 or above and finite
+ *   ids         device [n_tokens], or NULL: no given tokens (then out_logprob is
+ *               NULL).  A token whose id is below 0 is skipped: its row is not read,
+ *               its numbers are 0 and its alternatives -1 (specdec_rejection_sample
+ *               and specdec_tree_verify fill unused slots with -1, so their
+ *               out_tokens can be given as they are)
+ *   rows        device [n_tokens], each token's row, the same one for several if so
+ *               wanted; NULL: token t has row t (num_rows >= n_tokens)
+ *   top         0 .. SPECDEC_MAX_TOP
+ * Each output may be NULL (the two of the alternatives when top is 0), but not all;
+ * they overlap neither the inputs nor each other.  Sums are held in 32 bits with a
+ * reference that follows the maximum; entries of -inf have no weight, and may be
+ * alternatives with ln p = -inf.  A row that has no distribution (NaN or +inf among
+ * its entries, or nothing above -inf) gives NaN, and -1 for its alternatives.  An id
+ * of V or more (SPECDEC_DEVERR_BAD_DRAFT_ID) or a row outside [0, num_rows)
+ * (SPECDEC_DEVERR_BAD_CU) is skipped like an id below 0.  One launch, no workspace:
+ * calls on one handle may overlap on several streams. */
+#define SPECDEC_MAX_TOP 32
+int specdec_logprobs(specdec_handle_t h, const void* logits, int dtype, int64_t row_stride,
+                     int64_t num_rows, int V, float T, const int32_t* ids, const int32_t* rows,
+                     int64_t n_tokens, int top, float* out_logprob, float* out_entropy,
+                     int32_t* out_top_ids, float* out_top_logprobs, float* out_stats,
+                     void* stream);
+
+/* The gradient of the logits, from those of specdec_logprobs' outputs, for tokens that
+ * have a row each (row t; the call's `rows` was NULL):
+ *   out[t, v] = (1 / T) (g [v = ids[t]] + sum_j g_j [v = top_ids[t, j]]
+ *               - p(v) (g + sum_j g_j + h (ln p(v) + entropy[t])))
+ * with g = grad_logprob[t], h = grad_entropy[t], g_j = grad_top[t, j]; each gradient
+ * may be NULL (0).  logits, ids, T and top are those of the forward call, and
+ * logprob, entropy, top_ids, top_logprobs and stats what it gave; those that no
+ * given gradient needs may be NULL (never stats).  out has rows of V entries of
+ * `dtype`, out_row_stride apart, all of them written (a skipped token's with zeros, a
+ * row's without distribution with NaN), rounded once; it may be the logits themselves
+ * (same address and stride) and overlaps no input otherwise. */
+int specdec_logprobs_grad(specdec_handle_t h, const void* logits, int dtype, int64_t row_stride,
+                          int V, float T, const int32_t* ids, int64_t n_tokens, int top,
+                          const float* logprob, const float* entropy, const int32_t* top_ids,
+                          const float* top_logprobs, const float* stats,
+                          const float* grad_logprob, const float* grad_entropy,
+                          const float* grad_top, void* out, int64_t out_row_stride, void* stream);
+
 /* ---- the paged key/value cache of the verified nodes -----------------------
  * What a target's layer does around the verification of drafted nodes (chains
  * or token trees, in specdec_tree_verify's layout): turn and write the nodes'
@@ -361,6 +415,46 @@ int specdec_cache_append(specdec_handle_t h, const specdec_cache_t* cache,
                          const float* rotary, int rotary_dim, int64_t rotary_positions,
                          int interleaved, void* stream);
 
+/* specdec_cache_append for nodes whose positions are not slot numbers (targets that read
+ * images and videos: time, height and width), rotary not NULL:
+ *   positions  device [num_axes, N], axes position_stride elements apart, or NULL: row
+ *              r turns by position positions[a][r] on axis a, whatever its depth (the
+ *              tree is not read)
+ *   axes       HOST array of rotary_dim / 2 entries below num_axes, the axis of each
+ *              pair (pair i takes its cos and sin from entry i of the table's row at
+ *              the position on its axis), or NULL: all of axis 0
+ *   num_axes   1 .. SPECDEC_MAX_AXES (ignored without positions)
+ *   offsets    device [B] or NULL, instead of positions: request b's nodes stand at
+ *              lengths[b] + depth + offsets[b] on every axis (a prompt's images take
+ *              more slots than positions)
+ * A row one of whose positions, on any of the axes, lies outside the table is left out
+ * as by specdec_cache_append (SPECDEC_DEVERR_BAD_CACHE). */
+#define SPECDEC_MAX_AXES 4
+int specdec_cache_append_positions(specdec_handle_t h, const specdec_cache_t* cache,
+                         const specdec_nodes_t* nodes, int dtype, const void* k,
+                         int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                         int64_t v_row_stride, int64_t v_head_stride, const void* q,
+                         int64_t q_row_stride, int64_t q_head_stride, int q_heads, void* out_q,
+                         const float* rotary, int rotary_dim, int64_t rotary_positions,
+                         int interleaved, const int32_t* positions, int64_t position_stride,
+                         int num_axes, const uint8_t* axes, const int32_t* offsets, void* stream);
+
+/* Turns dense rows x [N, heads, head_dim] (an encoder's queries and keys, a projection's
+ * rows before they are split) by positions on several axes; positions, axes, rotary
+ * and the arithmetic as in specdec_cache_append_positions, head_dim a multiple of 8 up to
+ * 1024, rotary_dim a multiple of 16 up to head_dim and 128.
+ *   inverse   not 0: turned back (sin negated), which is also the gradient of a turn
+ *   out       the same shape, rows and heads that do not overlap one another; x itself
+ *             (same address and strides), or no byte of x
+ * A row one of whose positions lies outside the table becomes zeros
+ * (SPECDEC_DEVERR_BAD_CACHE).  One launch, no workspace. */
+int specdec_rotate(specdec_handle_t h, int dtype, const void* x, int64_t x_row_stride,
+                   int64_t x_head_stride, int64_t N, int heads, int head_dim,
+                   const int32_t* positions, int64_t position_stride, int num_axes,
+                   const uint8_t* axes, const float* rotary, int rotary_dim,
+                   int64_t rotary_positions, int interleaved, int inverse, void* out,
+                   int64_t out_row_stride, int64_t out_head_stride, void* stream);
+
 /* Reads rows back: row r of request b (cu[b] <= r < cu[b+1]) is slot lengths[b] +
  * r - cu[b]; out_k, out_v are contiguous [N, num_kv_heads, head_dim] of `dtype`,
  * e4m3 values times their scale rounded once.  A slot that the cache does not
@@ -403,6 +497,28 @@ int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
  * (0 for small calls, whose workspace may be NULL), or a negative status. */
 int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache_t* cache,
                                          int B, int64_t N, int q_heads, int max_pages);
+
+/* Attention of every row over its request's slots 0 .. lengths[b]-1 and no others: of a
+ * target's rows over an encoder's states, which specdec_cache_append has written once
+ * (lengths 0, one chain of states for each request, usually no rotary), or which lie in
+ * memory as [B, num_kv_heads, most, head_dim] (a cache of B pages of `most` slots whose
+ * page table is 0 .. B-1).  Any number of rows against any number of states; every row
+ * of a request sees the same ones.  nodes->parent is ignored.
+ *   mask  device [B] rows of mask_slots bytes, mask_stride apart (>= mask_slots), or
+ *         NULL: a slot whose byte is 0, or that lies at mask_slots or beyond, is hidden
+ *         from the request's rows, whatever it holds
+ * Everything else as for specdec_tree_attention: a row that sees no state (length 0, all
+ * masked) is zeros. */
+int specdec_cross_attention(specdec_handle_t h, const specdec_cache_t* cache,
+                            const specdec_nodes_t* nodes, int dtype, const void* q,
+                            int64_t q_row_stride, int64_t q_head_stride, int q_heads,
+                            const uint8_t* mask, int64_t mask_stride, int64_t mask_slots,
+                            float softmax_scale, void* out, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of specdec_cross_attention, as specdec_tree_attention_workspace. */
+int64_t specdec_cross_attention_workspace(specdec_handle_t h, const specdec_cache_t* cache,
+                                          int B, int64_t N, int q_heads, int max_pages);
 
 /* After the verification: moves the accepted nodes' rows (and scales) to the
  * slots behind the root, lengths[b] + path[d] -> lengths[b] + 1 + d, and writes

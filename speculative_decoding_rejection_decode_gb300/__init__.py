@@ -30,7 +30,8 @@ _LAZY = {"Verifier", "VerifyOutput", "SpecdecError", "uniform", "neg_log_uniform
          "specdec_neg_log_uniform", "specdec_selection_mass", "selection_mass",
          "specdec_status_string", "specdec_destroy",
          "specdec_rejection_sample_noalloc", "specdec_tree_verify", "TreeOutput",
-         "specdec_rejection_sample_given",
+         "specdec_rejection_sample_given", "specdec_logprobs", "specdec_logprobs_grad", "LogprobOutput",
+         "specdec_rotate", "rotary_axes", "tree_rows", "SPECDEC_MAX_TOP", "SPECDEC_MAX_AXES",
          "SPECDEC_F32", "SPECDEC_BF16",
          "SPECDEC_PATH_AUTO", "SPECDEC_PATH_FUSED", "SPECDEC_PATH_TWO_PASS", "SPECDEC_PATH_SWEEP",
          "SPECDEC_PATH_STREAM", "SPECDEC_PATH_PAIR", "SPECDEC_PATH_DUAL", "SPECDEC_PATH_GREEDY"}
@@ -38,7 +39,8 @@ _LAZY = {"Verifier", "VerifyOutput", "SpecdecError", "uniform", "neg_log_uniform
 
 _LAZY_CACHE = {"KVCache", "rotary_table", "specdec_cache_append", "specdec_cache_read",
                "specdec_tree_attention", "specdec_tree_attention_workspace",
-               "specdec_cache_commit", "SPECDEC_F16", "SPECDEC_E4M3"}
+               "specdec_cache_append_positions", "specdec_cross_attention",
+               "specdec_cross_attention_workspace", "specdec_cache_commit", "SPECDEC_F16", "SPECDEC_E4M3"}
 
 
 def __getattr__(name):

@@ -34,6 +34,8 @@ SPECDEC_DEVERR_BAD_TREE = 16
 SPECDEC_DEVERR_BAD_CACHE = 32
 
 SPECDEC_MAX_TREE_NODES = 1024
+SPECDEC_MAX_TOP = 32
+SPECDEC_MAX_AXES = 4
 
 SPECDEC_FAULT_NONE = 0
 SPECDEC_FAULT_PAIR_STALL = 1
@@ -112,6 +114,17 @@ _attn_ws = _fn("specdec_tree_attention_workspace", _i64, _vp, _cp, _i32, _i64, _
 _attn = _fn("specdec_tree_attention", _i32, _vp, _cp, _np, _i32, _vp, _i64, _i64, _i32, _f32, _vp,
             _vp, _i64, _vp)
 _commit = _fn("specdec_cache_commit", _i32, _vp, _cp, _np, _vp, _vp, _vp, _vp)
+_append_pos = _fn("specdec_cache_append_positions", _i32, _vp, _cp, _np, _i32, _vp, _i64, _i64, _vp, _i64,
+                  _i64, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _vp)
+_rotate = _fn("specdec_rotate", _i32, _vp, _i32, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _i32, _vp,
+              _vp, _i32, _i64, _i32, _i32, _vp, _i64, _i64, _vp)
+_cross_ws = _fn("specdec_cross_attention_workspace", _i64, _vp, _cp, _i32, _i64, _i32, _i32)
+_cross = _fn("specdec_cross_attention", _i32, _vp, _cp, _np, _i32, _vp, _i64, _i64, _i32, _vp, _i64, _i64,
+             _f32, _vp, _vp, _i64, _vp)
+_logprobs = _fn("specdec_logprobs", _i32, _vp, _vp, _i32, _i64, _i64, _i32, _f32, _vp, _vp, _i64, _i32,
+                _vp, _vp, _vp, _vp, _vp, _vp)
+_logprobs_grad = _fn("specdec_logprobs_grad", _i32, _vp, _vp, _i32, _i64, _i32, _f32, _vp, _i64, _i32,
+                     _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp)
 _status_string = _fn("specdec_status_string", ctypes.c_char_p, _i32)
 _destroy = _fn("specdec_destroy", _i32, _vp)
 
@@ -183,6 +196,51 @@ def specdec_tree_attention(h, cache, nodes, dtype, q, q_row_stride, q_head_strid
 
 def specdec_cache_commit(h, cache, nodes, num_accepted, path, out_lengths, stream) -> int:
     return _commit(h, cache, nodes, num_accepted, path, out_lengths, stream)
+
+
+def specdec_cache_append_positions(h, cache, nodes, dtype, k, k_row_stride, k_head_stride, v,
+                                   v_row_stride, v_head_stride, q, q_row_stride, q_head_stride,
+                                   q_heads, out_q, rotary, rotary_dim, rotary_positions,
+                                   interleaved, positions, position_stride, num_axes, axes,
+                                   offsets, stream) -> int:
+    return _append_pos(h, cache, nodes, dtype, k, k_row_stride, k_head_stride, v, v_row_stride,
+                       v_head_stride, q, q_row_stride, q_head_stride, q_heads, out_q, rotary,
+                       rotary_dim, rotary_positions, interleaved, positions, position_stride,
+                       num_axes, axes, offsets, stream)
+
+
+def specdec_rotate(h, dtype, x, x_row_stride, x_head_stride, N, heads, head_dim, positions,
+                   position_stride, num_axes, axes, rotary, rotary_dim, rotary_positions,
+                   interleaved, inverse, out, out_row_stride, out_head_stride, stream) -> int:
+    return _rotate(h, dtype, x, x_row_stride, x_head_stride, N, heads, head_dim, positions,
+                   position_stride, num_axes, axes, rotary, rotary_dim, rotary_positions,
+                   interleaved, inverse, out, out_row_stride, out_head_stride, stream)
+
+
+def specdec_cross_attention_workspace(h, cache, B, N, q_heads, max_pages) -> int:
+    return _cross_ws(h, cache, B, N, q_heads, max_pages)
+
+
+def specdec_cross_attention(h, cache, nodes, dtype, q, q_row_stride, q_head_stride, q_heads, mask,
+                            mask_stride, mask_slots, softmax_scale, out, workspace,
+                            workspace_bytes, stream) -> int:
+    return _cross(h, cache, nodes, dtype, q, q_row_stride, q_head_stride, q_heads, mask,
+                  mask_stride, mask_slots, softmax_scale, out, workspace, workspace_bytes, stream)
+
+
+def specdec_logprobs(h, logits, dtype, row_stride, num_rows, V, T, ids, rows, n_tokens, top,
+                     out_logprob, out_entropy, out_top_ids, out_top_logprobs, out_stats,
+                     stream) -> int:
+    return _logprobs(h, logits, dtype, row_stride, num_rows, V, T, ids, rows, n_tokens, top,
+                     out_logprob, out_entropy, out_top_ids, out_top_logprobs, out_stats, stream)
+
+
+def specdec_logprobs_grad(h, logits, dtype, row_stride, V, T, ids, n_tokens, top, logprob, entropy,
+                          top_ids, top_logprobs, stats, grad_logprob, grad_entropy, grad_top, out,
+                          out_row_stride, stream) -> int:
+    return _logprobs_grad(h, logits, dtype, row_stride, V, T, ids, n_tokens, top, logprob, entropy,
+                          top_ids, top_logprobs, stats, grad_logprob, grad_entropy, grad_top, out,
+                          out_row_stride, stream)
 
 
 def specdec_set_timing_events(h: int, before_rows, after_rows) -> int:
@@ -259,4 +317,6 @@ EXPORTED = ["specdec_create", "specdec_reserve", "specdec_rejection_sample",
             "specdec_selection_mass", "specdec_rejection_sample_noalloc", "specdec_tree_verify",
             "specdec_rejection_sample_given", "specdec_cache_append", "specdec_cache_read",
             "specdec_tree_attention", "specdec_tree_attention_workspace", "specdec_cache_commit",
+            "specdec_cache_append_positions", "specdec_rotate", "specdec_cross_attention",
+            "specdec_cross_attention_workspace", "specdec_logprobs", "specdec_logprobs_grad",
             "specdec_status_string", "specdec_destroy"]

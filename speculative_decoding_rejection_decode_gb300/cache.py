@@ -9,9 +9,10 @@ import math
 import torch
 
 from ._lib import (SPECDEC_BF16, SPECDEC_E4M3, SPECDEC_F16, specdec_cache_append,  # noqa: F401
-                   specdec_cache_commit, specdec_cache_read, specdec_cache_t, specdec_nodes_t,
-                   specdec_tree_attention, specdec_tree_attention_workspace)
-from .verifier import Verifier, _check, _ptr, _stream_handle
+                   specdec_cache_append_positions, specdec_cache_commit, specdec_cache_read,
+                   specdec_cache_t, specdec_cross_attention, specdec_cross_attention_workspace,
+                   specdec_nodes_t, specdec_tree_attention, specdec_tree_attention_workspace)
+from .verifier import Verifier, _check, _ptr, _overlap, _stream_handle, position_args, rotary_axes  # noqa: F401
 
 _DTYPE = {torch.bfloat16: SPECDEC_BF16, torch.float16: SPECDEC_F16,
           torch.float8_e4m3fn: SPECDEC_E4M3}
@@ -65,15 +66,6 @@ def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0,
     out[:, 0] = a.cos() * gain
     out[:, 1] = a.sin() * gain
     return out
-
-
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether the spans of memory of two tensors meet."""
-    def span(t):
-        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
 
 
 class KVCache:
@@ -173,13 +165,18 @@ class KVCache:
                lengths: torch.Tensor, cu_num_nodes: torch.Tensor,
                node_parent: torch.Tensor | None = None, *, q: torch.Tensor | None = None,
                rotary: torch.Tensor | None = None, interleaved: bool = False,
+               positions: torch.Tensor | None = None, axes=None,
+               position_offsets: torch.Tensor | None = None,
                out_q: torch.Tensor | None = None) -> torch.Tensor | None:
         """Writes the nodes' keys and values ([N, num_kv_heads, head_dim], any row
         and head strides) behind the context: node j of request b into slot
         lengths[b] + j.  With ``rotary`` (``rotary_table``) k and q are turned to
         position lengths[b] + depth(j) first, in pairs (i, i + rotary_dim / 2) or,
-        interleaved, (2i, 2i + 1).  Returns the turned q (contiguous; ``out_q`` may be
-        q itself), or None."""
+        interleaved, (2i, 2i + 1).  Where positions are not slot numbers (images, videos),
+        ``positions`` gives the rows' own (int32 [N], or [axes, N] with ``axes``, the
+        axis of each pair: ``rotary_axes``), or ``position_offsets`` (int32 [B]) what
+        each request adds to lengths[b] + depth(j).  Returns the turned q (contiguous;
+        ``out_q`` may be q itself), or None."""
         N = k.shape[0]
         dt = self._row_dtype(k)
         kp = self._rows(k, N, self.num_kv_heads, k.dtype, "k")
@@ -198,20 +195,43 @@ class KVCache:
                 raise ValueError("out_q must be q itself or overlap none of q, k and v")
         elif out_q is not None:
             raise ValueError("out_q without q")
-        dim = positions = 0
+        dim = positions_held = 0
         if rotary is not None:
             if rotary.dim() != 3 or rotary.shape[1] != 2 or rotary.dtype != torch.float32 \
                     or rotary.device != self.device or not rotary.is_contiguous():
                 raise ValueError("rotary must be contiguous float32 [positions, 2, rotary_dim / 2] "
                                  "on the device")
-            positions, dim = rotary.shape[0], 2 * rotary.shape[2]
+            positions_held, dim = rotary.shape[0], 2 * rotary.shape[2]
             if dim % 16 or not 0 < dim <= self.head_dim:
                 raise ValueError("rotary_dim must be a multiple of 16 up to head_dim")
+        elif positions is not None or position_offsets is not None:
+            raise ValueError("positions without rotary")
+        if axes is not None and positions is None:
+            raise ValueError("axes without positions")
         nodes = self._nodes(page_table, lengths, cu_num_nodes, node_parent, N)
+        if positions is not None or position_offsets is not None:
+            if positions is not None and position_offsets is not None:
+                raise ValueError("positions and position_offsets exclude each other")
+            if positions is not None:
+                where = (*position_args(positions, axes, N, dim // 2, self._at), None)
+                if N and q is not None and _overlap(out_q, positions):
+                    raise ValueError("out_q must not overlap positions")
+            else:
+                t = position_offsets
+                if t.dtype is not torch.int32 or t.get_device() != self._at or t.numel() != lengths.numel() \
+                        or not t.is_contiguous():
+                    raise ValueError("position_offsets must be a contiguous int32 tensor on the device, one entry per request")
+                where = (None, 0, 1, None, t.data_ptr())
+            if N:
+                _check(specdec_cache_append_positions(
+                    self.verifier.handle, self._ref, nodes, dt, *kp, *vp, *qp, heads,
+                    None if q is None else out_q.data_ptr(), rotary.data_ptr(), dim, positions_held,
+                    int(interleaved), *where, _stream_handle(self.device)), "specdec_cache_append_positions")
+            return out_q
         if N:
             _check(specdec_cache_append(self.verifier.handle, self._ref, nodes, dt, *kp, *vp, *qp, heads,
                                         None if q is None else out_q.data_ptr(), _ptr(rotary) or None,
-                                        dim, positions, int(interleaved), _stream_handle(self.device)),
+                                        dim, positions_held, int(interleaved), _stream_handle(self.device)),
                    "specdec_cache_append")
         return out_q
 
@@ -243,19 +263,13 @@ class KVCache:
                    "specdec_cache_read")
         return out
 
-    def attend(self, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
-               cu_num_nodes: torch.Tensor, node_parent: torch.Tensor | None = None, *,
-               scale: float | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
-        """Attention of the nodes' queries ([N, q_heads, head_dim], q_heads a
-        multiple of num_kv_heads) over their request's context and their own
-        ancestors, which ``append`` has written: specdec_tree_attention.  ``scale``
-        defaults to 1 / sqrt(head_dim).  Returns [N, q_heads, head_dim]."""
+    def _attention(self, q, page_table, lengths, cu, parent, mask, scale, out, ask, call, name):
         N, heads = q.shape[0], q.shape[1] if q.dim() == 3 else 0
         dt = self._row_dtype(q)
         qp = self._rows(q, N, heads, q.dtype, "q")
         if heads < 1 or heads % self.num_kv_heads:
             raise ValueError("q_heads must be a multiple of num_kv_heads")
-        nodes = self._nodes(page_table, lengths, cu_num_nodes, node_parent, N)
+        nodes = self._nodes(page_table, lengths, cu, parent, N)
         if out is None:
             out = torch.empty(N, heads, self.head_dim, dtype=q.dtype, device=self.device)
         elif out.shape != q.shape or out.dtype != q.dtype or out.device != self.device \
@@ -266,16 +280,49 @@ class KVCache:
             raise ValueError("out must not overlap q")
         if N:
             h = self.verifier.handle
-            need = specdec_tree_attention_workspace(h, self._ref, cu_num_nodes.numel() - 1, N, heads,
-                                                    page_table.shape[1])
+            need = ask(h, self._ref, cu.numel() - 1, N, heads, page_table.shape[1])
             if need < 0:
-                _check(need, "specdec_tree_attention_workspace")
+                _check(need, name + "_workspace")
             ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-            _check(specdec_tree_attention(h, self._ref, nodes, dt, *qp, heads,
-                                          self.head_dim ** -0.5 if scale is None else float(scale),
-                                          out.data_ptr(), _ptr(ws) or None, need,
-                                          _stream_handle(self.device)), "specdec_tree_attention")
+            _check(call(h, self._ref, nodes, dt, *qp, heads, *mask,
+                        self.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
+                        _ptr(ws) or None, need, _stream_handle(self.device)), name)
         return out
+
+    def attend(self, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+               cu_num_nodes: torch.Tensor, node_parent: torch.Tensor | None = None, *,
+               scale: float | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+        """Attention of the nodes' queries ([N, q_heads, head_dim], q_heads a
+        multiple of num_kv_heads) over their request's context and their own
+        ancestors, which ``append`` has written: specdec_tree_attention.  ``scale``
+        defaults to 1 / sqrt(head_dim).  Returns [N, q_heads, head_dim]."""
+        return self._attention(q, page_table, lengths, cu_num_nodes, node_parent, (), scale, out,
+                               specdec_tree_attention_workspace, specdec_tree_attention,
+                               "specdec_tree_attention")
+
+    def cross_attend(self, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+                     cu_rows: torch.Tensor, *, mask: torch.Tensor | None = None,
+                     scale: float | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+        """Cross attention: every row of q ([N, q_heads, head_dim], request b's rows
+        cu_rows[b] .. cu_rows[b + 1] - 1) over its request's slots 0 .. lengths[b] - 1,
+        an encoder's states that ``append`` has written once, and no others:
+        specdec_cross_attention.  States held as [B, num_kv_heads, most, head_dim] are a
+        cache of B pages with the page table arange(B)[:, None].  ``mask`` (bool or uint8
+        [B, slots]): slots where it is 0, or behind its columns, are hidden.  A row
+        that sees no state is zeros."""
+        m = (None, 0, 0)
+        if mask is not None:
+            if mask.dtype not in (torch.bool, torch.uint8) or mask.get_device() != self._at or mask.dim() != 2 \
+                    or mask.shape[0] != lengths.numel() or (mask.shape[1] > 1 and mask.stride(1) != 1) \
+                    or (mask.shape[0] > 1 and mask.stride(0) < mask.shape[1]):
+                raise ValueError("mask must be bool or uint8 [B, slots] on the device with contiguous rows of their own")
+            # a mask without columns hides everything; it still needs an address
+            m = (mask.data_ptr() or self.verifier._empty.data_ptr(), max(mask.stride(0), mask.shape[1]), mask.shape[1])
+            if out is not None and _overlap(out, mask):
+                raise ValueError("out must not overlap mask")
+        return self._attention(q, page_table, lengths, cu_rows, None, m, scale, out,
+                               specdec_cross_attention_workspace, specdec_cross_attention,
+                               "specdec_cross_attention")
 
     def commit(self, page_table: torch.Tensor, lengths: torch.Tensor, cu_num_nodes: torch.Tensor,
                num_accepted: torch.Tensor, path: torch.Tensor | None = None, *,

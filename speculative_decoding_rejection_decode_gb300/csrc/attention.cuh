@@ -50,11 +50,11 @@ struct PlanArgs {
   const int32_t* lengths;
   int64_t N, capacity;      // node rows; slots of a request
   int32_t B, kv_heads, group, item_cost;
-  bool tree, whole;         // whole: items are not split
+  bool tree, whole, cross;  // whole: items are not split; cross: the keys are the context alone
 
   __host__ __device__ __forceinline__ explicit PlanArgs(const AttendArgs& a)
       : cu(a.c.cu), lengths(a.c.lengths), N(a.c.N), capacity((int64_t)a.c.geo.max_pages * a.c.geo.page_size), B(a.c.B),
-        kv_heads(a.c.geo.kv_heads), group(a.q_heads / a.c.geo.kv_heads), item_cost(a.item_cost), tree(a.c.parent != nullptr), whole(a.whole) {}
+        kv_heads(a.c.geo.kv_heads), group(a.q_heads / a.c.geo.kv_heads), item_cost(a.item_cost), tree(a.c.parent != nullptr), whole(a.whole), cross(a.cross) {}
 };
 
 // Whether a call leaves items whole: contexts of at most 4 tiles by the page
@@ -81,7 +81,8 @@ __host__ __device__ __forceinline__ Request attend_request(const PlanArgs& c, in
   }
   q.len = c.lengths[b];
   if (q.n == 0) return q;
-  if (q.len < 0 || (int64_t)q.len + q.n > c.capacity) {
+  const int64_t keys = (int64_t)q.len + (c.cross ? 0 : q.n);
+  if (q.len < 0 || keys > c.capacity) {
     why |= SPECDEC_DEVERR_BAD_CACHE;
     return q;
   }
@@ -90,7 +91,8 @@ __host__ __device__ __forceinline__ Request attend_request(const PlanArgs& c, in
     return q;
   }
   q.rts = (int32_t)(((int64_t)q.n * c.group + R - 1) / R);
-  q.tiles = (int32_t)(((int64_t)q.len + q.n + TK - 1) / TK);
+  q.tiles = (int32_t)((keys + TK - 1) / TK);
+  if (q.tiles == 0) q.tiles = 1;   // no key at all: rows of zeros are still to be written
   q.units = (int64_t)c.kv_heads * q.rts * ((c.whole ? 1 : q.tiles) + c.item_cost);
   if (q.units >= ((int64_t)1 << 31)) {   // units of a request are counted in 32 bits
     q.units = 0;
@@ -324,6 +326,9 @@ int launch_join(const AttendArgs& a, int G, cudaStream_t st) {
 
 // The tensor-core kernel (attention_tile.cu).
 int launch_attend_tile(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
+// Both kernels over an encoder's states (cross_tile.cu, cross.cu).
+int launch_cross_tile(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
+int launch_cross_warp(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
 int64_t attend_tile_workspace(int head_dim, int num_sms);
 
 

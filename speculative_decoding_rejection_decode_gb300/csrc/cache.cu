@@ -19,49 +19,12 @@
 
 #include "../../include/specdec.h"
 #include "cache.cuh"
+#include "row_values.cuh"
 
 namespace specdec {
 namespace {
 
 constexpr int kThreads = 128;
-
-struct Vec8 {
-  float x[8];
-};
-
-__device__ __forceinline__ float2 unpack(uint32_t w, __nv_bfloat16) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-__device__ __forceinline__ float2 unpack(uint32_t w, __half) {
-  return __half22float2(*reinterpret_cast<__half2*>(&w));
-}
-__device__ __forceinline__ uint32_t pack(float a, float b, __nv_bfloat16) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack(float a, float b, __half) {
-  __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-template <typename T>
-__device__ __forceinline__ Vec8 widen(uint4 w) {
-  Vec8 v;
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack(u[i], T());
-    v.x[2 * i] = f.x;
-    v.x[2 * i + 1] = f.y;
-  }
-  return v;
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 narrow(const Vec8& v) {
-  return make_uint4(pack(v.x[0], v.x[1], T()), pack(v.x[2], v.x[3], T()),
-                    pack(v.x[4], v.x[5], T()), pack(v.x[6], v.x[7], T()));
-}
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float r;
@@ -111,10 +74,15 @@ __device__ __forceinline__ void store_row(void* base, float* scales, int64_t row
   }
 }
 
-// 8 neighbouring cos (or sin) of the table, or 4 of them each used twice.
+// 4 neighbouring cos (or sin), of the table or (SHARED) of the block's own copy, or 8.
+template <bool SHARED>
+__device__ __forceinline__ float4 load4(const float* p) {
+  if constexpr (SHARED) return *reinterpret_cast<const float4*>(p);
+  else return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <bool SHARED>
 __device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = load4<SHARED>(p), b = load4<SHARED>(p + 4);
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
@@ -157,7 +125,7 @@ __device__ __forceinline__ int request_from(const int32_t* cu, int B, int b, int
 }
 
 __device__ __forceinline__ RowPlace place_of(const CacheArgs& c, int from, int64_t r, bool rotary, int rotary_dim,
-                                             int64_t positions) {
+                                             int64_t positions, const int32_t* offsets = nullptr) {
   RowPlace p = {-1, -1, 0};
   uint32_t bad = 0;
   const int b = request_from(c.cu, c.B, from, r);
@@ -179,8 +147,11 @@ __device__ __forceinline__ RowPlace place_of(const CacheArgs& c, int from, int64
   if (rotary) {
     const int depth = node_depth(c.parent ? c.parent + first : nullptr, j);
     if (depth < 0) bad |= SPECDEC_DEVERR_BAD_TREE;
-    else if (len < 0 || len + depth >= positions) bad |= SPECDEC_DEVERR_BAD_CACHE;
-    else p.turn = (len + depth) * rotary_dim;
+    else {
+      const int64_t at = len + depth + (offsets ? offsets[b] : 0);
+      if (len < 0 || at < 0 || at >= positions) bad |= SPECDEC_DEVERR_BAD_CACHE;
+      else p.turn = at * rotary_dim;
+    }
     if (p.turn < 0) p.row = -1;
   }
   if (bad) atomicOr(c.err, bad);
@@ -195,11 +166,15 @@ __device__ __forceinline__ RowPlace place_of(const CacheArgs& c, int from, int64
 // k and v, which may be quantised, and q have loops of their own, the first with one
 // copy of its body: one loop for all heads, unrolled, was 8 % slower for one tree and
 // held 6 blocks of an SM where this form holds 7.
-template <typename T, bool FP8, int D>
+// AXES: the rows bring positions on several axes, and each pair turns by its own; the
+// block then takes the cos and sin of its rows' pairs to shared memory, all at once.
+template <typename T, bool FP8, int D, bool AXES>
 __global__ void __launch_bounds__(kThreads, 7) append_kernel(const AppendArgs a, const int rows) {
   constexpr int LANES = D / 8;                 // lanes of a row
   constexpr int SLOTS = kThreads / LANES;      // heads in flight
   __shared__ RowPlace places[kRows];
+  __shared__ __align__(16) float turns[AXES ? kRows : 1][2][AXES ? D / 2 : 4];   // cos, sin of a row's pairs
+  __shared__ int64_t at_axis[AXES ? kRows : 1][kMaxAxes];                      // their positions in the table
   const int chunk = threadIdx.x % LANES, slot0 = threadIdx.x / LANES;
   const CacheArgs& c = a.c;
   const int half = a.rotary_dim / 2;
@@ -208,11 +183,34 @@ __global__ void __launch_bounds__(kThreads, 7) append_kernel(const AppendArgs a,
   const int here = (int)min((int64_t)rows, c.N - r0);
   if (threadIdx.x < 32) {
     const int from = warp_request_of_row(c.cu, c.B, r0);
-    if ((int)threadIdx.x < here)
-      places[threadIdx.x] = place_of(c, from, r0 + threadIdx.x, a.rotary != nullptr, a.rotary_dim, a.positions);
+    if ((int)threadIdx.x < here) {
+      RowPlace p = place_of(c, from, r0 + threadIdx.x, !AXES && a.rotary != nullptr, a.rotary_dim, a.positions, a.offsets);
+      if constexpr (AXES) {
+        if (p.owned) {
+          p.turn = 0;
+          for (int i = 0; i < a.num_axes; ++i) {
+            const int64_t at = a.pos[i * a.pos_stride + r0 + threadIdx.x];
+            if (at < 0 || at >= a.positions) p.row = p.turn = -1;
+            at_axis[threadIdx.x][i] = at * a.rotary_dim;
+          }
+          if (p.turn < 0) atomicOr(c.err, SPECDEC_DEVERR_BAD_CACHE);
+        }
+      }
+      places[threadIdx.x] = p;
+    }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && (int64_t)c.cu[c.B] > c.N) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
   __syncthreads();
+  if constexpr (AXES) {
+    for (int x = threadIdx.x; x < here * half; x += kThreads) {
+      const int i = x / half, j = x - i * half;
+      if (places[i].turn < 0) continue;
+      const float* from = a.rotary + at_axis[i][axis_of(a.axes, j)] + j;
+      turns[i][0][j] = __ldg(from);
+      turns[i][1][j] = __ldg(from + half);
+    }
+    __syncthreads();
+  }
   const int kv = c.geo.kv_heads, heads = a.q ? a.q_heads : 0;
   for (int i = 0; i < here; ++i) {
     const RowPlace p = places[i];
@@ -223,16 +221,16 @@ __global__ void __launch_bounds__(kThreads, 7) append_kernel(const AppendArgs a,
     int partner = 0;
     float sign = 1.0f;
     if (turned) {
-      const float *cosp = a.rotary + p.turn, *sinp = cosp + half;
+      const float *cosp = AXES ? turns[AXES ? i : 0][0] : a.rotary + p.turn, *sinp = AXES ? turns[AXES ? i : 0][1] : cosp + half;
       if (a.interleaved) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(cosp + d0 / 2));
-        const float4 y = __ldg(reinterpret_cast<const float4*>(sinp + d0 / 2));
+        const float4 x = load4<AXES>(cosp + d0 / 2);
+        const float4 y = load4<AXES>(sinp + d0 / 2);
         cs[0] = cs[1] = x.x; cs[2] = cs[3] = x.y; cs[4] = cs[5] = x.z; cs[6] = cs[7] = x.w;
         sn[0] = sn[1] = y.x; sn[2] = sn[3] = y.y; sn[4] = sn[5] = y.z; sn[6] = sn[7] = y.w;
       } else {
         const bool low = d0 < half;
-        load8(cosp + (low ? d0 : d0 - half), cs);
-        load8(sinp + (low ? d0 : d0 - half), sn);
+        load8<AXES>(cosp + (low ? d0 : d0 - half), cs);
+        load8<AXES>(sinp + (low ? d0 : d0 - half), sn);
         partner = (low ? half : -half) / 8;
         sign = low ? -1.0f : 1.0f;
       }
@@ -477,8 +475,13 @@ template <typename T, bool FP8>
 int append_of(const AppendArgs& a, int num_sms, cudaStream_t st) {
   const int rows = rows_per_block(a.c.N, (int64_t)num_sms * 7, 16);
   const int64_t grid = (a.c.N + rows - 1) / rows;
-  if (a.c.head_dim == 128) append_kernel<T, FP8, 128><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
-  else append_kernel<T, FP8, 64><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
+  if (a.pos) {
+    if (a.c.head_dim == 128) append_kernel<T, FP8, 128, true><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
+    else append_kernel<T, FP8, 64, true><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
+  } else {
+    if (a.c.head_dim == 128) append_kernel<T, FP8, 128, false><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
+    else append_kernel<T, FP8, 64, false><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
+  }
   return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 

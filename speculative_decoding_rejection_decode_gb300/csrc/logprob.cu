@@ -1,0 +1,599 @@
+// Log probabilities of given tokens, with the entropy and the top alternatives of
+// their rows, and the gradient of the logits.  Contract in include/specdec.h
+// (specdec_logprobs, specdec_logprobs_grad).
+//
+// One pass over a row.  With c = log2(e) / T, a reference rho near the row's largest
+// logit and y_v = (x_v - rho) c,
+//   S = sum 2^y_v,  W = sum 2^y_v y_v,
+//   ln p(v) = ln 2 (y_v - log2 S),  H = ln 2 (log2 S - W / S).
+// The difference is taken first: it is exact for neighbouring logits, however large.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/specdec.h"
+#include "device_common.cuh"
+#include "logprob.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kNT = 512, kNW = kNT / 32;   // threads of a row's block
+constexpr int kU = 4;                      // 16-byte loads of a thread under way together
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kFloor = -1000.0f;         // y of entries without weight, where they meet a product
+constexpr float kLazy = 8.0f;              // log2 of how far the reference may lag behind the largest entry
+constexpr int kCap = 96;                   // candidates of a warp at most
+constexpr int kSlack = 32;                 // candidates beyond n that a step may leave
+
+template <typename T>
+struct Row;   // what differs between the types of logits
+
+template <>
+struct Row<float> {
+  static constexpr int E = 4;
+  static constexpr uint32_t kNone = 0xFF800000u;   // -inf
+  using Max = float;
+  static __device__ __forceinline__ float2 two(const uint4& w, int i) {
+    const uint32_t* u = &w.x;
+    return make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+  }
+  static __device__ __forceinline__ float most(const uint4& w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+};
+template <>
+struct Row<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static constexpr uint32_t kNone = 0xFF80FF80u;
+  static __device__ __forceinline__ float2 two(const uint4& w, int i) {
+    const uint32_t u = (&w.x)[i];
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ float most(const uint4& w) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+    return fmaxf(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
+};
+template <>
+struct Row<__half> {
+  static constexpr int E = 8;
+  static constexpr uint32_t kNone = 0xFC00FC00u;
+  static __device__ __forceinline__ float2 two(const uint4& w, int i) {
+    return __half22float2(reinterpret_cast<const __half2*>(&w)[i]);
+  }
+  static __device__ __forceinline__ float most(const uint4& w) {
+    const __half2* h = reinterpret_cast<const __half2*>(&w);
+    const float2 f = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+    return fmaxf(f.x, f.y);
+  }
+};
+
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ void as_type(float x, float& y) { y = x; }
+__device__ __forceinline__ void as_type(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void as_type(float x, __half& y) { y = __float2half_rn(x); }
+
+// Two 32-bit operations in one instruction, each rounded as alone.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Rows are read once: they shall not displace what others keep in the caches.
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// ---- sums of a part of a row ---------------------------------------------------
+
+struct Sums {
+  float rho, s, w;
+};
+
+// Brings the sums to another reference (at least their own, or any for empty sums).
+__device__ __forceinline__ void move_to(Sums& a, float rho, float c) {
+  if (a.rho == rho) return;
+  if (a.rho == -INFINITY) {
+    a.s = a.w = 0.0f;
+  } else {
+    const float d = (a.rho - rho) * c, f = ex2(d);
+    a.w = f * fmaf(d < kFloor ? kFloor : d, a.s, a.w);
+    a.s *= f;
+  }
+  a.rho = rho;
+}
+__device__ __forceinline__ void join(Sums& a, Sums b, float c) {
+  const float rho = a.rho != a.rho || b.rho != b.rho ? __uint_as_float(0x7FC00000u) : fmaxf(a.rho, b.rho);
+  move_to(a, rho, c);
+  move_to(b, rho, c);
+  a.s += b.s;
+  a.w += b.w;
+}
+
+// ---- the largest entries of a row -----------------------------------------------
+// Entries are ordered by key: the value, then the lower index.  A warp looks at
+// entries of rising index, so of the value of its list's n-th none can follow; and what
+// lies below a value that n entries of the block's part are known to reach is left out
+// (which is known when differs from run to run, what is found does not).
+
+__device__ __forceinline__ uint32_t order_of(float x) {   // -0 counts as 0
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t index) { return (uint64_t)order_of(x) << 32 | (uint32_t)~index; }
+
+__device__ __forceinline__ uint64_t warp_most(uint64_t k) {
+  const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(k >> 32));
+  const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// The n largest of cnt <= kCap keys in buf, sorted, to buf; how many there are.
+__device__ __forceinline__ int keep_most(uint64_t* buf, int cnt, int n) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  uint64_t k[kCap / 32];
+#pragma unroll
+  for (int i = 0; i < kCap / 32; ++i) k[i] = i * 32 + lane < cnt ? buf[i * 32 + lane] : 0;
+  __syncwarp();
+  const int m = min(cnt, n);
+  for (int r = 0; r < m; ++r) {
+    uint64_t mine = k[0];
+#pragma unroll
+    for (int i = 1; i < kCap / 32; ++i) mine = mine > k[i] ? mine : k[i];
+    const uint64_t best = warp_most(mine);
+#pragma unroll
+    for (int i = 0; i < kCap / 32; ++i)
+      if (k[i] == best) k[i] = 0;
+    if (lane == 0) buf[r] = best;
+  }
+  __syncwarp();
+  return m;
+}
+
+// The least value that may still be among the n largest.
+__device__ __forceinline__ float bound_of(uint32_t own, const volatile uint32_t* known) {
+  const uint32_t k = *known;
+  return value_of(own > k ? own : k);
+}
+
+struct Listed {
+  int cnt;        // entries of the warp's list
+  uint32_t own;   // order of the least value that its own entries leave room for
+};
+
+// Offers the first m of the neighbouring entries in w, the first one's index given.
+// Out of line: a row's first steps come here often, the others hardly ever.
+template <typename T>
+__device__ __noinline__ Listed offer(uint64_t* buf, Listed s, int n, uint4 w, int m, uint32_t index, uint32_t* known) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < Row<T>::E; ++i) {
+    const float2 f = Row<T>::two(w, i >> 1);
+    const float x = i & 1 ? f.y : f.x;
+    const bool in = i < m && x >= bound_of(s.own, known);
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
+    if (!who) continue;
+    if (s.cnt + 32 > kCap) {
+      // entries of this step may still equal the last one's value with a lower index
+      s.cnt = keep_most(buf, s.cnt, n);
+      if (lane == 0) atomicMax(known, (uint32_t)(buf[n - 1] >> 32));
+      __syncwarp();
+    }
+    if (in) buf[s.cnt + __popc(who & ((1u << lane) - 1u))] = key_of(x, index + i);
+    s.cnt += __popc(who);
+  }
+  if (s.cnt > n + kSlack) {
+    s.cnt = keep_most(buf, s.cnt, n);
+    const uint32_t last = (uint32_t)(buf[n - 1] >> 32);
+    s.own = last + 1u;
+    if (lane == 0) atomicMax(known, last);
+  }
+  __syncwarp();
+  return s;
+}
+
+struct LogprobShared {
+  Sums part[kNW];
+  Sums ranks[8];                        // of the cluster's blocks (rank 0)
+  uint32_t known;                       // order of a value that n entries are known to reach
+  int count[kNW];
+  uint64_t best[kMaxTop];
+  uint64_t bests[8][kMaxTop];           // of the cluster's blocks (rank 0)
+  uint64_t list[kNW][kCap];
+};
+
+// The n largest of sorted lists, lane i < lists holding list i, to out (0: none).
+template <typename At>
+__device__ __forceinline__ void merge_sorted(int lists, int n, At at, uint64_t* out) {
+  const int lane = threadIdx.x & 31;
+  int pos = 0;
+  uint64_t head = lane < lists ? at(lane, 0) : 0;
+  for (int r = 0; r < n; ++r) {
+    const uint64_t best = warp_most(head);
+    if (best && head == best) {
+      ++pos;
+      head = pos < n ? at(lane, pos) : 0;
+    }
+    if (lane == 0) out[r] = best;
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void put_remote(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void put_remote(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ Sums warp_join(Sums a, float c) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Sums b = {__shfl_xor_sync(0xFFFFFFFFu, a.rho, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
+                    __shfl_xor_sync(0xFFFFFFFFu, a.w, o)};
+    join(a, b, c);
+  }
+  return a;
+}
+
+// A token's row, by a cluster of 1, 2, 4 or 8 blocks that take a part of it each; rank
+// 0 joins the parts and writes.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kNT, 2) logprob_kernel(const LogprobArgs a) {
+  using R = Row<T>;
+  constexpr int E = R::E;
+  __shared__ LogprobShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ranks = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
+  const int64_t t = blockIdx.x / (unsigned)ranks;
+  const int n = a.top;
+  const int32_t id = a.ids ? a.ids[t] : 0;
+  const int64_t row = a.rows ? (int64_t)a.rows[t] : t;
+  if (id < 0 || id >= a.V || row < 0 || row >= a.R) {   // no row is read; the whole cluster leaves
+    if (rank == 0) {
+      if (tid == 0) {
+        if (id >= a.V) atomicOr(a.err, SPECDEC_DEVERR_BAD_DRAFT_ID);
+        else if (id >= 0) atomicOr(a.err, SPECDEC_DEVERR_BAD_CU);
+        if (a.logprob) a.logprob[t] = 0.0f;
+        if (a.entropy) a.entropy[t] = 0.0f;
+        if (a.stats) a.stats[t] = make_float2(0.0f, 0.0f);
+      }
+      if (TOP && tid < n) {
+        a.top_ids[t * n + tid] = -1;
+        a.top_logprobs[t * n + tid] = 0.0f;
+      }
+    }
+    return;
+  }
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this block runs
+  const T* x = static_cast<const T*>(a.x) + row * a.row_stride;
+  const int lead = min(a.V, (int)((16u - ((uint32_t)reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / (int)sizeof(T));
+  const int vecs = (a.V - lead) / E, done = lead + vecs * E;
+  const int v0 = (int)((int64_t)vecs * rank / ranks), v1 = (int)((int64_t)vecs * (rank + 1) / ranks);
+  const uint4* xv = reinterpret_cast<const uint4*>(x + lead);
+  const float given = a.logprob && rank == 0 && tid == 0 ? as_float(x[id]) : 0.0f;
+  if constexpr (TOP) {
+    if (tid == 0) sh.known = order_of(-INFINITY);
+    __syncthreads();
+  }
+  Sums mine = {-INFINITY, 0.0f, 0.0f};
+  uint64_t s2[2] = {0, 0}, w2[2] = {0, 0};
+  const uint64_t c2 = pair(a.c, a.c);
+  const float lag = kLazy / a.c;
+  [[maybe_unused]] Listed lst = {0, 0u};
+  auto gather = [&] {
+    float p, q;
+    unpair(add2(s2[0], s2[1]), p, q);
+    mine.s = p + q;
+    unpair(add2(w2[0], w2[1]), p, q);
+    mine.w = p + q;
+  };
+  // U x 16 bytes of a thread, of which the first m entries of each count
+  auto take = [&](const uint4* w, auto count, int m, uint32_t index) {
+    constexpr int U = decltype(count)::value;
+    float most = R::most(w[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) most = fmaxf(most, R::most(w[u]));
+    if (!(most <= mine.rho + lag)) {          // first entries, larger ones, NaN
+      gather();
+      move_to(mine, most, a.c);
+      s2[0] = pair(mine.s, 0.0f);
+      w2[0] = pair(mine.w, 0.0f);
+      s2[1] = w2[1] = 0;
+    }
+    const float ref = mine.rho == -INFINITY ? 0.0f : -mine.rho;
+    const uint64_t r2 = pair(ref, ref);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const float2 f = R::two(w[u], i);
+        float y0, y1;
+        unpair(mul2(add2(pair(f.x, f.y), r2), c2), y0, y1);
+        const uint64_t e2 = pair(ex2(y0), ex2(y1));
+        s2[i & 1] = add2(s2[i & 1], e2);
+        // 2^y is 0 there, and 0 x -inf would not be
+        w2[i & 1] = fma2(e2, pair(fmaxf(y0, kFloor), fmaxf(y1, kFloor)), w2[i & 1]);
+      }
+    if constexpr (TOP) {
+      if (__any_sync(0xFFFFFFFFu, most >= bound_of(lst.own, &sh.known))) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (__any_sync(0xFFFFFFFFu, R::most(w[u]) >= bound_of(lst.own, &sh.known)))
+            lst = offer<T>(sh.list[warp], lst, n, w[u], m, index + u * (kNT * E), &sh.known);
+      }
+    }
+  };
+  // A first value that n entries reach: the n-th of the lanes' largest.
+  auto first_bound = [&](float most) {
+    uint64_t k = key_of(most, lane), best = 0;
+    for (int r = 0; r < n; ++r) {
+      best = warp_most(k);
+      if (k == best) k = 0;
+    }
+    if (lane == 0 && value_of((uint32_t)(best >> 32)) == value_of((uint32_t)(best >> 32)))
+      atomicMax(&sh.known, (uint32_t)(best >> 32));
+    __syncthreads();
+  };
+  using Many = std::integral_constant<int, kU>;
+  using One = std::integral_constant<int, 1>;
+  const uint4 none = make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
+  if (rank == 0 && lead > 0 && warp == 0) {   // up to the first 16-byte boundary
+    uint4 w = none;
+    if (lane < lead) *reinterpret_cast<T*>(&w) = x[lane];
+    take(&w, One(), lane < lead ? 1 : 0, (uint32_t)lane);
+  }
+  int v = v0;
+  for (; v + kU * kNT <= v1; v += kU * kNT) {
+    uint4 w[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) w[u] = load_once(xv + v + u * kNT + tid);
+    if (TOP && v == v0) {
+      float most = R::most(w[0]);
+#pragma unroll
+      for (int u = 1; u < kU; ++u) most = fmaxf(most, R::most(w[u]));
+      first_bound(most);
+    }
+    take(w, Many(), E, (uint32_t)(lead + (v + tid) * E));
+  }
+  for (; v < v1; v += kNT) {
+    const bool in = v + tid < v1;
+    uint4 w = none;
+    if (in) w = load_once(xv + v + tid);
+    if (TOP && v == v0) first_bound(R::most(w));
+    take(&w, One(), in ? E : 0, (uint32_t)(lead + (v + tid) * E));
+  }
+  if (rank == ranks - 1 && done < a.V && warp == 0) {   // behind the last one
+    const bool in = lane < a.V - done;
+    uint4 w = none;
+    if (in) *reinterpret_cast<T*>(&w) = x[done + lane];
+    take(&w, One(), in ? 1 : 0, (uint32_t)(done + lane));
+  }
+  gather();
+  mine = warp_join(mine, a.c);
+  if (lane == 0) sh.part[warp] = mine;
+  if constexpr (TOP) {
+    const int kept = keep_most(sh.list[warp], lst.cnt, n);
+    if (lane == 0) sh.count[warp] = kept;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const Sums empty = {-INFINITY, 0.0f, 0.0f};
+    mine = warp_join(lane < kNW ? sh.part[lane] : empty, a.c);
+    if constexpr (TOP)
+      merge_sorted(kNW, n, [&](int l, int p) { return p < sh.count[l] ? sh.list[l][p] : 0; }, sh.best);
+  }
+  if (ranks > 1) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every block runs
+    if (warp == 0) {
+      if (lane == 0) {
+        const uint32_t at = mapa(smem_addr(&sh.ranks[rank]), 0);
+        put_remote(at, mine.rho);
+        put_remote(at + 4, mine.s);
+        put_remote(at + 8, mine.w);
+      }
+      if (TOP && lane < n) put_remote(mapa(smem_addr(&sh.bests[rank][lane]), 0), sh.best[lane]);
+    }
+    cluster_sync_all();
+    if (rank) return;
+    if (warp == 0) {
+      const Sums empty = {-INFINITY, 0.0f, 0.0f};
+      mine = warp_join(lane < ranks ? sh.ranks[lane] : empty, a.c);
+      if constexpr (TOP) {
+        merge_sorted(ranks, n, [&](int l, int p) { return sh.bests[l][p]; }, sh.best);
+      }
+    }
+  }
+  if (warp) return;
+  const bool fine = mine.s > 0.0f && mine.s < INFINITY;   // not: no distribution
+  const float none_f = __uint_as_float(0x7FC00000u);
+  const float lg = log2f(mine.s);
+  if (lane == 0) {
+    if (a.logprob) a.logprob[t] = fine ? kLn2 * ((given - mine.rho) * a.c - lg) : none_f;
+    if (a.entropy) a.entropy[t] = fine ? kLn2 * (lg - mine.w / mine.s) : none_f;
+    if (a.stats) a.stats[t] = fine ? make_float2(mine.rho, lg) : make_float2(none_f, none_f);
+  }
+  if (TOP && lane < n) {
+    const uint64_t k = sh.best[lane];
+    const float y = (value_of((uint32_t)(k >> 32)) - mine.rho) * a.c - lg;
+    a.top_ids[t * n + lane] = fine && k ? (int32_t)~(uint32_t)k : -1;
+    a.top_logprobs[t * n + lane] = !fine ? none_f : k ? kLn2 * y : -INFINITY;
+  }
+}
+
+// ---- the gradient of the logits ---------------------------------------------------
+// With z = log2 p(v) and the gradients g of ln p(id), h of H and g_j of the
+// alternatives' ln p:
+//   d x_v = (1 / T) (g [v = id] + sum_j g_j [v = id_j] - p (g + sum_j g_j + h (ln p + H)))
+// One pass, a 16-byte load and a store of a thread at a time; the few entries with a
+// term of their own are written again, whole, behind the block's.
+constexpr int kGT = 256, kGU = 4;
+constexpr int kGVecs = 4096;   // 16-byte pieces of a row that a block takes, about
+
+template <typename T>
+__global__ void __launch_bounds__(kGT) logprob_grad_kernel(const LogprobGradArgs a, const int parts) {
+  using R = Row<T>;
+  constexpr int E = R::E;
+  const int tid = threadIdx.x, n = a.top;
+  const int64_t t = blockIdx.x / (unsigned)parts;
+  const int part = (int)(blockIdx.x - (unsigned)t * (unsigned)parts);
+  const T* x = static_cast<const T*>(a.x) + t * a.row_stride;
+  T* out = static_cast<T*>(a.out) + t * a.out_stride;
+  const int32_t id = a.ids ? a.ids[t] : -1;
+  const bool live = a.ids ? id >= 0 && id < a.V : true;
+  const int lead = min(a.V, (int)((16u - ((uint32_t)reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / (int)sizeof(T));
+  const int vecs = (a.V - lead) / E;
+  const int v0 = (int)((int64_t)vecs * part / parts), v1 = (int)((int64_t)vecs * (part + 1) / parts);
+  // this block's entries
+  const int e0 = part ? lead + v0 * E : 0, e1 = part == parts - 1 ? a.V : lead + v1 * E;
+  uint4* ov = reinterpret_cast<uint4*>(out + lead);
+  if (!live) {
+    for (int v = v0 + tid; v < v1; v += kGT) ov[v] = make_uint4(0, 0, 0, 0);
+    T zero;
+    as_type(0.0f, zero);
+    if (part == 0 && tid < lead) out[tid] = zero;
+    for (int i = lead + v1 * E + tid; i < e1; i += kGT) out[i] = zero;
+    return;
+  }
+  const float2 st = a.stats[t];
+  const float g = a.g_logprob && a.ids ? a.g_logprob[t] : 0.0f, h = a.g_entropy ? a.g_entropy[t] : 0.0f;
+  float all = g;
+  if (a.g_top)
+    for (int j = 0; j < n; ++j) {
+      const int32_t at = a.top_ids[t * n + j];
+      if (at >= 0 && at < a.V) all += a.g_top[t * n + j];
+    }
+  const float k0 = -(all + (h != 0.0f ? h * a.entropy[t] : 0.0f)) * a.inv_t, k1 = -h * kLn2 * a.inv_t;
+  auto slope = [&](float z) { return ex2(z) * fmaf(k1, fmaxf(z, kFloor), k0); };
+  auto one = [&](T v) -> T {
+    T y;
+    as_type(slope(fmaf(as_float(v) - st.x, a.c, -st.y)), y);
+    return y;
+  };
+  if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
+    const uint4* xv = reinterpret_cast<const uint4*>(x + lead);
+    const uint64_t c2 = pair(a.c, a.c), r2 = pair(-st.x, -st.x), l2 = pair(-st.y, -st.y), k1_2 = pair(k1, k1), k0_2 = pair(k0, k0);
+    auto turn = [&](uint4 w) -> uint4 {
+      uint4 y;
+      T* to = reinterpret_cast<T*>(&y);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const float2 f = R::two(w, i);
+        float z0, z1, b0, b1;
+        unpair(fma2(add2(pair(f.x, f.y), r2), c2, l2), z0, z1);
+        unpair(fma2(k1_2, pair(fmaxf(z0, kFloor), fmaxf(z1, kFloor)), k0_2), b0, b1);
+        as_type(ex2(z0) * b0, to[2 * i]);
+        as_type(ex2(z1) * b1, to[2 * i + 1]);
+      }
+      return y;
+    };
+    int v = v0;
+    for (; v + kGU * kGT <= v1; v += kGU * kGT) {
+      uint4 w[kGU];
+#pragma unroll
+      for (int u = 0; u < kGU; ++u) w[u] = __ldcs(xv + v + u * kGT + tid);
+#pragma unroll
+      for (int u = 0; u < kGU; ++u) __stcs(ov + v + u * kGT + tid, turn(w[u]));
+    }
+    for (; v + tid < v1; v += kGT) ov[v + tid] = turn(xv[v + tid]);
+    if (part == 0 && tid < lead) out[tid] = one(x[tid]);
+    const int i = lead + v1 * E + tid;
+    if (i < e1) out[i] = one(x[i]);
+  } else {
+    for (int i = e0 + tid; i < e1; i += kGT) out[i] = one(x[i]);
+  }
+  if (!(a.g_logprob && a.ids) && !a.g_top) return;
+  __syncthreads();
+  if (tid <= n) {
+    const bool own = tid == n;
+    const int32_t at = own ? (a.g_logprob ? id : -1) : a.g_top ? a.top_ids[t * n + tid] : -1;
+    if (at >= e0 && at < e1) {
+      float add = a.g_logprob && at == id ? g : 0.0f;
+      if (a.g_top)
+        for (int j = 0; j < n; ++j)
+          if (a.top_ids[t * n + j] == at) add += a.g_top[t * n + j];
+      const float z = (own ? a.logprob[t] : a.top_logprobs[t * n + tid]) * 1.44269504088896341f;
+      as_type(fmaf(add, a.inv_t, slope(z)), out[at]);
+    }
+  }
+}
+
+template <typename T>
+int forward_of(const LogprobArgs& a, int num_sms, cudaStream_t st) {
+  // Blocks of a row: enough that every SM has two, of at least one load a thread.
+  const int vecs = a.V / Row<T>::E;
+  int ranks = 1;
+  while (ranks < 8 && a.M * ranks < 2 * num_sms && vecs / (2 * ranks) >= kNT) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.M * ranks));
+  cfg.blockDim = dim3(kNT);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)ranks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = a.top ? cudaLaunchKernelEx(&cfg, logprob_kernel<T, true>, a) : cudaLaunchKernelEx(&cfg, logprob_kernel<T, false>, a);
+  return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+template <typename T>
+int gradient_of(const LogprobGradArgs& a, cudaStream_t st) {
+  const int64_t vecs = a.V / Row<T>::E;
+  int64_t parts = (vecs + kGVecs - 1) / kGVecs;
+  if (parts < 1) parts = 1;
+  while (parts > 1 && a.M * parts > INT32_MAX) --parts;
+  logprob_grad_kernel<T><<<(unsigned)(a.M * parts), kGT, 0, st>>>(a, (int)parts);
+  return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_logprob(const LogprobArgs& a, int dtype, int num_sms, cudaStream_t st) {
+  if (a.M == 0) return SPECDEC_OK;
+  if (dtype == SPECDEC_F32) return forward_of<float>(a, num_sms, st);
+  return dtype == SPECDEC_BF16 ? forward_of<__nv_bfloat16>(a, num_sms, st) : forward_of<__half>(a, num_sms, st);
+}
+
+int launch_logprob_grad(const LogprobGradArgs& a, int dtype, int num_sms, cudaStream_t st) {
+  if (a.M == 0) return SPECDEC_OK;
+  if (dtype == SPECDEC_F32) return gradient_of<float>(a, st);
+  return dtype == SPECDEC_BF16 ? gradient_of<__nv_bfloat16>(a, st) : gradient_of<__half>(a, st);
+}
+
+}  // namespace specdec

@@ -10,6 +10,7 @@
 
 #include "cache.cuh"
 #include "kernels.cuh"
+#include "logprob.cuh"
 #include "tree.cuh"
 
 using namespace specdec;
@@ -359,6 +360,7 @@ int launch_greedy(specdec_ctx* h, Params& P, bool vec_ok, cudaStream_t st) {
 // ---- host checks of the cache's operators ------------------------------------
 constexpr int kMaxRequests = 1 << 20;   // of one call of these operators
 constexpr int kMaxHeads = 1 << 12;
+constexpr int kMaxRotateDim = 1 << 10;   // head_dim of dense rows
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -377,6 +379,23 @@ bool meet_rows(const void* out, int64_t out_bytes, const void* p, int64_t row, i
   const int64_t r = (N - 1) * row, h = (heads - 1) * head;
   const int64_t first = (r < 0 ? r : 0) + (h < 0 ? h : 0), last = (r > 0 ? r : 0) + (h > 0 ? h : 0) + dim;
   return N > 0 && meet(out, out_bytes, static_cast<const char*>(p) + 2 * first, 2 * (last - first));
+}
+
+// Sizes of the calls on rows of logits.  T below 2^-60 would leave the exponent's range.
+bool logit_sizes_ok(int64_t row_stride, int64_t num_rows, int V, float T, int64_t n_tokens, int top) {
+  return V > 0 && V <= (1 << 30) && row_stride >= V && num_rows >= 0 && num_rows < ((int64_t)1 << 31) && n_tokens >= 0 &&
+         n_tokens < ((int64_t)1 << 31) && top >= 0 && top <= kMaxTop && T >= 8.673617379884035e-19f && std::isfinite(T);
+}
+
+// The kernels' view of the axes of rotary pairs (each below num_axes; null: all 0).
+bool pairs_of(const uint8_t* axes, int num_axes, int rotary_dim, RotaryAxes& out) {
+  if (num_axes < 1 || num_axes > kMaxAxes || rotary_dim / 2 > kMaxPairs) return false;
+  out = {};
+  for (int i = 0; axes && i < rotary_dim / 2; ++i) {
+    if (axes[i] >= num_axes) return false;
+    out.word[i >> 4] |= (uint32_t)axes[i] << ((i & 15) * 2);
+  }
+  return true;
 }
 
 // Checks a cache and its nodes and fills the kernels' view of them (all but the
@@ -685,13 +704,14 @@ int specdec_rejection_sample_given(specdec_handle_t h, const float* target_probs
   return launch_given(a, h->num_sms, static_cast<cudaStream_t>(stream));
 }
 
-int specdec_cache_append(specdec_handle_t h, const specdec_cache_t* cache,
-                         const specdec_nodes_t* nodes, int dtype, const void* k,
-                         int64_t k_row_stride, int64_t k_head_stride, const void* v,
-                         int64_t v_row_stride, int64_t v_head_stride, const void* q,
-                         int64_t q_row_stride, int64_t q_head_stride, int q_heads, void* out_q,
-                         const float* rotary, int rotary_dim, int64_t rotary_positions,
-                         int interleaved, void* stream) {
+// Both appends.
+static int append_rows(specdec_handle_t h, const specdec_cache_t* cache, const specdec_nodes_t* nodes, int dtype,
+                       const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                       int64_t v_row_stride, int64_t v_head_stride, const void* q, int64_t q_row_stride,
+                       int64_t q_head_stride, int q_heads, void* out_q, const float* rotary, int rotary_dim,
+                       int64_t rotary_positions, int interleaved, const int32_t* positions,
+                       int64_t position_stride, int num_axes, const uint8_t* axes, const int32_t* offsets,
+                       void* stream) {
   AppendArgs a = {};
   int rc = cache_args(cache, nodes, dtype, a.c);
   if (rc != SPECDEC_OK) return rc;
@@ -712,6 +732,13 @@ int specdec_cache_append(specdec_handle_t h, const specdec_cache_t* cache,
   if (rotary && (!aligned16(rotary) || rotary_dim <= 0 || rotary_dim % 16 != 0 ||
                  rotary_dim > cache->head_dim || rotary_positions <= 0))
     return SPECDEC_ERR_INVALID_ARG;
+  if (positions && offsets) return SPECDEC_ERR_INVALID_ARG;
+  if ((positions || offsets) && !rotary) return SPECDEC_ERR_INVALID_ARG;
+  if (positions) {
+    if (!pairs_of(axes, num_axes, rotary_dim, a.axes) || (num_axes > 1 && position_stride < nodes->N)) return SPECDEC_ERR_INVALID_ARG;
+    const int64_t bytes = 4 * ((num_axes - 1) * position_stride + nodes->N);
+    if (q && nodes->N > 0 && meet(out_q, 2 * nodes->N * q_heads * cache->head_dim, positions, bytes)) return SPECDEC_ERR_INVALID_ARG;
+  }
   if (!h) return SPECDEC_ERR_INVALID_ARG;
   DeviceGuard guard(h->device);
   if (!guard.ok()) return SPECDEC_ERR_CUDA;
@@ -731,7 +758,36 @@ int specdec_cache_append(specdec_handle_t h, const specdec_cache_t* cache,
   a.rotary_dim = rotary ? rotary_dim : 0;
   a.positions = rotary_positions;
   a.interleaved = interleaved ? 1 : 0;
+  a.pos = positions;
+  a.pos_stride = position_stride;
+  a.num_axes = num_axes;
+  a.offsets = offsets;
   return launch_append(a, cache->dtype, dtype, h->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int specdec_cache_append(specdec_handle_t h, const specdec_cache_t* cache,
+                         const specdec_nodes_t* nodes, int dtype, const void* k,
+                         int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                         int64_t v_row_stride, int64_t v_head_stride, const void* q,
+                         int64_t q_row_stride, int64_t q_head_stride, int q_heads, void* out_q,
+                         const float* rotary, int rotary_dim, int64_t rotary_positions,
+                         int interleaved, void* stream) {
+  return append_rows(h, cache, nodes, dtype, k, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride, q,
+                     q_row_stride, q_head_stride, q_heads, out_q, rotary, rotary_dim, rotary_positions, interleaved,
+                     nullptr, 0, 0, nullptr, nullptr, stream);
+}
+
+int specdec_cache_append_positions(specdec_handle_t h, const specdec_cache_t* cache,
+                         const specdec_nodes_t* nodes, int dtype, const void* k,
+                         int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                         int64_t v_row_stride, int64_t v_head_stride, const void* q,
+                         int64_t q_row_stride, int64_t q_head_stride, int q_heads, void* out_q,
+                         const float* rotary, int rotary_dim, int64_t rotary_positions,
+                         int interleaved, const int32_t* positions, int64_t position_stride,
+                         int num_axes, const uint8_t* axes, const int32_t* offsets, void* stream) {
+  return append_rows(h, cache, nodes, dtype, k, k_row_stride, k_head_stride, v, v_row_stride, v_head_stride, q,
+                     q_row_stride, q_head_stride, q_heads, out_q, rotary, rotary_dim, rotary_positions, interleaved,
+                     positions, position_stride, num_axes, axes, offsets, stream);
 }
 
 int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
@@ -753,20 +809,31 @@ int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
   return launch_read(a, cache->dtype, dtype, h->num_sms, static_cast<cudaStream_t>(stream));
 }
 
-int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache_t* cache,
-                                         int B, int64_t N, int q_heads, int max_pages) {
+// Both workspaces.
+static int64_t attention_workspace(bool cross, specdec_handle_t h, const specdec_cache_t* cache, int B, int64_t N,
+                                   int q_heads, int max_pages) {
   if (!h || !cache || max_pages <= 0 || cache->page_size <= 0 || B <= 0 || B > kMaxRequests || N < 0 || (cache->head_dim != 64 && cache->head_dim != 128) ||
       cache->num_kv_heads <= 0 || q_heads <= 0 || q_heads > kMaxHeads || q_heads % cache->num_kv_heads != 0)
     return SPECDEC_ERR_INVALID_ARG;
-  return attend_workspace_bytes(B, N, cache->num_kv_heads, q_heads, cache->head_dim,
+  return attend_workspace_bytes(cross, B, N, cache->num_kv_heads, q_heads, cache->head_dim,
                                 (int64_t)max_pages * cache->page_size, h->num_sms);
 }
 
-int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
-                           const specdec_nodes_t* nodes, int dtype, const void* q,
-                           int64_t q_row_stride, int64_t q_head_stride, int q_heads,
-                           float softmax_scale, void* out, void* workspace,
-                           int64_t workspace_bytes, void* stream) {
+int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache_t* cache,
+                                         int B, int64_t N, int q_heads, int max_pages) {
+  return attention_workspace(false, h, cache, B, N, q_heads, max_pages);
+}
+
+int64_t specdec_cross_attention_workspace(specdec_handle_t h, const specdec_cache_t* cache,
+                                          int B, int64_t N, int q_heads, int max_pages) {
+  return attention_workspace(true, h, cache, B, N, q_heads, max_pages);
+}
+
+// Both attentions.
+static int attention(bool cross, specdec_handle_t h, const specdec_cache_t* cache, const specdec_nodes_t* nodes,
+                     int dtype, const void* q, int64_t q_row_stride, int64_t q_head_stride, int q_heads,
+                     const uint8_t* mask, int64_t mask_stride, int64_t mask_slots, float softmax_scale, void* out,
+                     void* workspace, int64_t workspace_bytes, void* stream) {
   AttendArgs a = {};
   int rc = cache_args(cache, nodes, dtype, a.c);
   if (rc != SPECDEC_OK) return rc;
@@ -776,9 +843,12 @@ int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
     return SPECDEC_ERR_INVALID_ARG;
   if (meet_rows(out, 2 * nodes->N * q_heads * cache->head_dim, q, q_row_stride, q_head_stride, nodes->N, q_heads, cache->head_dim))
     return SPECDEC_ERR_INVALID_ARG;
+  if (cross && mask && (mask_slots < 0 || mask_stride < mask_slots)) return SPECDEC_ERR_INVALID_ARG;
+  if (cross && mask && meet(out, 2 * nodes->N * q_heads * cache->head_dim, mask, (nodes->B - 1) * mask_stride + mask_slots))
+    return SPECDEC_ERR_INVALID_ARG;
   if (!h) return SPECDEC_ERR_INVALID_ARG;
   const int64_t need =
-      attend_workspace_bytes(nodes->B, nodes->N, cache->num_kv_heads, q_heads, cache->head_dim,
+      attend_workspace_bytes(cross, nodes->B, nodes->N, cache->num_kv_heads, q_heads, cache->head_dim,
                              (int64_t)nodes->max_pages * cache->page_size, h->num_sms);
   if (need > 0 && (!workspace || !aligned16(workspace))) return SPECDEC_ERR_INVALID_ARG;
   if (workspace_bytes < need) return SPECDEC_ERR_CAPACITY;
@@ -792,7 +862,177 @@ int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
   a.scale_log2 = softmax_scale * kLog2e;
   a.out = out;
   a.workspace = workspace;
+  a.cross = cross;
+  a.mask = mask;
+  a.mask_stride = mask_stride;
+  a.mask_slots = mask_slots;
+  if (cross) a.c.parent = nullptr;
   return launch_attend(a, cache->dtype, dtype, h->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int specdec_tree_attention(specdec_handle_t h, const specdec_cache_t* cache,
+                           const specdec_nodes_t* nodes, int dtype, const void* q,
+                           int64_t q_row_stride, int64_t q_head_stride, int q_heads,
+                           float softmax_scale, void* out, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  return attention(false, h, cache, nodes, dtype, q, q_row_stride, q_head_stride, q_heads, nullptr, 0, 0, softmax_scale,
+                   out, workspace, workspace_bytes, stream);
+}
+
+int specdec_cross_attention(specdec_handle_t h, const specdec_cache_t* cache,
+                            const specdec_nodes_t* nodes, int dtype, const void* q,
+                            int64_t q_row_stride, int64_t q_head_stride, int q_heads,
+                            const uint8_t* mask, int64_t mask_stride, int64_t mask_slots,
+                            float softmax_scale, void* out, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+  return attention(true, h, cache, nodes, dtype, q, q_row_stride, q_head_stride, q_heads, mask, mask_stride, mask_slots,
+                   softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+int specdec_rotate(specdec_handle_t h, int dtype, const void* x, int64_t x_row_stride,
+                   int64_t x_head_stride, int64_t N, int heads, int head_dim,
+                   const int32_t* positions, int64_t position_stride, int num_axes,
+                   const uint8_t* axes, const float* rotary, int rotary_dim,
+                   int64_t rotary_positions, int interleaved, int inverse, void* out,
+                   int64_t out_row_stride, int64_t out_head_stride, void* stream) {
+  RotateArgs a = {};
+  if (dtype != SPECDEC_BF16 && dtype != SPECDEC_F16) return SPECDEC_ERR_UNSUPPORTED_DTYPE;
+  if (N < 0 || N >= ((int64_t)1 << 31) || heads <= 0 || heads > kMaxHeads || head_dim <= 0 || head_dim % 8 != 0 || head_dim > kMaxRotateDim)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (!rotary || !aligned16(rotary) || rotary_dim <= 0 || rotary_dim % 16 != 0 || rotary_dim > head_dim || rotary_positions <= 0)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (!pairs_of(axes, num_axes, rotary_dim, a.axes) || (num_axes > 1 && position_stride < N)) return SPECDEC_ERR_INVALID_ARG;
+  if (N > 0 && (!positions || !rows_ok(x, x_row_stride, x_head_stride) || !rows_ok(out, out_row_stride, out_head_stride)))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (N > 0) {
+    // rows of the output of their own, over no input but the same values
+    if ((heads > 1 && (out_head_stride < head_dim)) || (N > 1 && out_row_stride < (heads - 1) * out_head_stride + head_dim))
+      return SPECDEC_ERR_INVALID_ARG;
+    const int64_t bytes = 2 * ((N - 1) * out_row_stride + (heads - 1) * out_head_stride + head_dim);
+    const bool itself = out == x && (heads == 1 || x_head_stride == out_head_stride) && (N == 1 || x_row_stride == out_row_stride);
+    if ((!itself && meet_rows(out, bytes, x, x_row_stride, x_head_stride, N, heads, head_dim)) ||
+        meet(out, bytes, positions, 4 * ((num_axes - 1) * position_stride + N)) ||
+        meet(out, bytes, rotary, 4 * rotary_positions * rotary_dim))
+      return SPECDEC_ERR_INVALID_ARG;
+  }
+  if (!h) return SPECDEC_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok()) return SPECDEC_ERR_CUDA;
+  a.x = x;
+  a.out = out;
+  a.x_row = x_row_stride;
+  a.x_head = x_head_stride;
+  a.out_row = out_row_stride;
+  a.out_head = out_head_stride;
+  a.N = N;
+  a.heads = heads;
+  a.head_dim = head_dim;
+  a.pos = positions;
+  a.pos_stride = position_stride;
+  a.num_axes = num_axes;
+  a.rotary = rotary;
+  a.rotary_dim = rotary_dim;
+  a.positions = rotary_positions;
+  a.interleaved = interleaved ? 1 : 0;
+  a.inverse = inverse ? 1 : 0;
+  a.err = h->small;
+  return launch_rotate(a, dtype, h->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int specdec_logprobs(specdec_handle_t h, const void* logits, int dtype, int64_t row_stride,
+                     int64_t num_rows, int V, float T, const int32_t* ids, const int32_t* rows,
+                     int64_t n_tokens, int top, float* out_logprob, float* out_entropy,
+                     int32_t* out_top_ids, float* out_top_logprobs, float* out_stats, void* stream) {
+  if (dtype != SPECDEC_F32 && dtype != SPECDEC_BF16 && dtype != SPECDEC_F16) return SPECDEC_ERR_UNSUPPORTED_DTYPE;
+  if (!logit_sizes_ok(row_stride, num_rows, V, T, n_tokens, top)) return SPECDEC_ERR_INVALID_ARG;
+  if (n_tokens > 0) {
+    if (!logits || num_rows < 1 || (!rows && num_rows < n_tokens)) return SPECDEC_ERR_INVALID_ARG;
+    if ((out_logprob && !ids) || (!out_logprob && !out_entropy && !top && !out_stats)) return SPECDEC_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == SPECDEC_F32 ? 4 : 2) != 0 || reinterpret_cast<uintptr_t>(out_stats) % 8 != 0)
+      return SPECDEC_ERR_INVALID_ARG;
+    if (top && (!out_top_ids || !out_top_logprobs)) return SPECDEC_ERR_INVALID_ARG;
+    // a token's results are written while others' rows and ids are still to be read
+    const int64_t row_bytes = ((num_rows - 1) * row_stride + V) * (dtype == SPECDEC_F32 ? 4 : 2);
+    const struct { const void* p; int64_t bytes; } outs[] = {
+        {out_logprob, 4 * n_tokens}, {out_entropy, 4 * n_tokens}, {out_stats, 8 * n_tokens},
+        {top ? out_top_ids : nullptr, 4 * n_tokens * top}, {top ? out_top_logprobs : nullptr, 4 * n_tokens * top}};
+    for (int i = 0; i < 5; ++i) {
+      if (!outs[i].p) continue;
+      if (meet(outs[i].p, outs[i].bytes, logits, row_bytes) || (ids && meet(outs[i].p, outs[i].bytes, ids, 4 * n_tokens)) ||
+          (rows && meet(outs[i].p, outs[i].bytes, rows, 4 * n_tokens)))
+        return SPECDEC_ERR_INVALID_ARG;
+      for (int j = 0; j < i; ++j)
+        if (outs[j].p && meet(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return SPECDEC_ERR_INVALID_ARG;
+    }
+  }
+  if (!h) return SPECDEC_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok()) return SPECDEC_ERR_CUDA;
+  LogprobArgs a = {};
+  a.x = logits;
+  a.row_stride = row_stride;
+  a.R = num_rows;
+  a.V = V;
+  a.c = kLog2e / T;
+  a.ids = ids;
+  a.rows = rows;
+  a.M = n_tokens;
+  a.top = top;
+  a.logprob = out_logprob;
+  a.entropy = out_entropy;
+  a.top_ids = out_top_ids;
+  a.top_logprobs = out_top_logprobs;
+  a.stats = reinterpret_cast<float2*>(out_stats);
+  a.err = h->small;
+  return launch_logprob(a, dtype, h->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int specdec_logprobs_grad(specdec_handle_t h, const void* logits, int dtype, int64_t row_stride,
+                          int V, float T, const int32_t* ids, int64_t n_tokens, int top,
+                          const float* logprob, const float* entropy, const int32_t* top_ids,
+                          const float* top_logprobs, const float* stats, const float* grad_logprob,
+                          const float* grad_entropy, const float* grad_top, void* out,
+                          int64_t out_row_stride, void* stream) {
+  if (dtype != SPECDEC_F32 && dtype != SPECDEC_BF16 && dtype != SPECDEC_F16) return SPECDEC_ERR_UNSUPPORTED_DTYPE;
+  if (!logit_sizes_ok(row_stride, n_tokens, V, T, n_tokens, top) || out_row_stride < V) return SPECDEC_ERR_INVALID_ARG;
+  if (n_tokens > 0) {
+    const int size = dtype == SPECDEC_F32 ? 4 : 2;
+    if (!logits || !out || !stats || reinterpret_cast<uintptr_t>(logits) % size != 0 ||
+        reinterpret_cast<uintptr_t>(out) % size != 0 || reinterpret_cast<uintptr_t>(stats) % 8 != 0)
+      return SPECDEC_ERR_INVALID_ARG;
+    if ((grad_logprob && (!ids || !logprob)) || (grad_entropy && !entropy) || (grad_top && (!top || !top_ids || !top_logprobs)))
+      return SPECDEC_ERR_INVALID_ARG;
+    const int64_t bytes = ((n_tokens - 1) * row_stride + V) * size, out_bytes = ((n_tokens - 1) * out_row_stride + V) * size;
+    if (!(out == logits && row_stride == out_row_stride) && meet(out, out_bytes, logits, bytes)) return SPECDEC_ERR_INVALID_ARG;
+    const struct { const void* p; int64_t bytes; } ins[] = {
+        {ids, 4 * n_tokens}, {logprob, 4 * n_tokens}, {entropy, 4 * n_tokens}, {stats, 8 * n_tokens}, {grad_logprob, 4 * n_tokens},
+        {grad_entropy, 4 * n_tokens}, {top_ids, 4 * n_tokens * top}, {top_logprobs, 4 * n_tokens * top}, {grad_top, 4 * n_tokens * top}};
+    for (const auto& in : ins)
+      if (in.p && meet(out, out_bytes, in.p, in.bytes)) return SPECDEC_ERR_INVALID_ARG;
+  }
+  if (!h) return SPECDEC_ERR_INVALID_ARG;
+  DeviceGuard guard(h->device);
+  if (!guard.ok()) return SPECDEC_ERR_CUDA;
+  LogprobGradArgs a = {};
+  a.x = logits;
+  a.row_stride = row_stride;
+  a.M = n_tokens;
+  a.V = V;
+  a.c = kLog2e / T;
+  a.inv_t = 1.0f / T;
+  a.ids = ids;
+  a.top = grad_top ? top : 0;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.stats = reinterpret_cast<const float2*>(stats);
+  a.g_logprob = grad_logprob;
+  a.g_entropy = grad_entropy;
+  a.g_top = grad_top;
+  a.out = out;
+  a.out_stride = out_row_stride;
+  return launch_logprob_grad(a, dtype, h->num_sms, static_cast<cudaStream_t>(stream));
 }
 
 int specdec_cache_commit(specdec_handle_t h, const specdec_cache_t* cache,

@@ -7,10 +7,11 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (SPECDEC_BF16, SPECDEC_F32, SPECDEC_PATH_AUTO, SPECDEC_PATH_DUAL,  # noqa: F401
+from ._lib import (SPECDEC_BF16, SPECDEC_F16, SPECDEC_F32, SPECDEC_MAX_AXES, SPECDEC_MAX_TOP, SPECDEC_PATH_AUTO, SPECDEC_PATH_DUAL,  # noqa: F401
                    SPECDEC_PATH_FUSED, SPECDEC_PATH_GREEDY, SPECDEC_PATH_PAIR, SPECDEC_PATH_STREAM, SPECDEC_PATH_SWEEP,
                    SPECDEC_PATH_TWO_PASS, specdec_create, specdec_destroy,
-                   specdec_get_error, specdec_last_path, specdec_neg_log_uniform,
+                   specdec_get_error, specdec_last_path, specdec_logprobs,
+                   specdec_logprobs_grad, specdec_neg_log_uniform, specdec_rotate,
                    specdec_selection_mass,
                    specdec_rejection_sample, specdec_rejection_sample_ex,
                    specdec_rejection_sample_given, specdec_rejection_sample_noalloc,
@@ -41,6 +42,29 @@ class VerifyOutput:
     accept: torch.Tensor | None = None        # int32 [N_d]
 
 
+@dataclass
+class LogprobOutput:
+    logprob: torch.Tensor | None        # float32 [M] ln p(id); None without ids
+    entropy: torch.Tensor               # float32 [M]
+    top_ids: torch.Tensor | None        # int32 [M, top]; None where top is 0
+    top_logprobs: torch.Tensor | None   # float32 [M, top]
+    stats: torch.Tensor                 # float32 [M, 2] what the gradient needs of the rows
+
+
+_LOGITS = {torch.float32: SPECDEC_F32, torch.bfloat16: SPECDEC_BF16, torch.float16: SPECDEC_F16}
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the spans of memory of two tensors meet."""
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    if not a.numel() or not b.numel():
+        return False
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
@@ -65,6 +89,7 @@ class Verifier:
         idx = dev.index if dev.index is not None else torch.cuda.current_device()
         rc, self._h = specdec_create(idx)
         _check(rc, "specdec_create")
+        self._at = idx
         # a valid device address for required arrays that are empty (draft_ids
         # when every request has gamma = 0): the C ABI wants a pointer even then
         self._empty = torch.zeros(4, dtype=torch.int32, device=dev)
@@ -171,6 +196,136 @@ class Verifier:
         _check(rc, "specdec_rejection_sample_given")
         return out
 
+    def _logit_rows(self, t, name):
+        """Data pointer, type and row stride of rows of logits [R, V]."""
+        if t.dim() != 2 or t.dtype not in _LOGITS or t.get_device() != self._at \
+                or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name} must be float32, bfloat16 or float16 rows [R, V] on the device")
+        return t.data_ptr(), _LOGITS[t.dtype], max(t.stride(0), t.shape[1])
+
+    def _flat(self, t, dtype, shape, name):
+        if t.dtype is not dtype or t.get_device() != self._at or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on the device")
+
+    def logprobs(self, logits: torch.Tensor, ids: torch.Tensor | None = None, *,
+                 rows: torch.Tensor | None = None, T: float = 1.0, top: int = 0,
+                 out: "LogprobOutput | None" = None) -> "LogprobOutput":
+        """Log probabilities of given tokens under softmax(row / T), with the entropy of
+        their rows and the ``top`` largest entries (equal logits by rising id), on the
+        current torch stream: specdec_logprobs.  ``logits``: [R, V] float32, bfloat16 or
+        float16, rows of any stride; ``ids`` (int32 [M], None: no given tokens), ids
+        below 0 are skipped (zeros, alternatives -1), so the ``tokens`` of a
+        verification can be given as they are; ``rows`` (int32 [M]) the row of each
+        token (``tree_rows`` for the tokens of ``tree``), None: its own."""
+        f32, i32 = torch.float32, torch.int32
+        x, dt, stride = self._logit_rows(logits, "logits")
+        R, V = logits.shape
+        M = rows.numel() if rows is not None else ids.numel() if ids is not None else R
+        for t, name in ((ids, "ids"), (rows, "rows")):
+            if t is not None:
+                self._flat(t, i32, (M,), name)
+        if M > R and rows is None:
+            raise ValueError("more ids than rows")
+        if not 0 <= top <= SPECDEC_MAX_TOP:
+            raise ValueError(f"top must be 0 .. {SPECDEC_MAX_TOP}")
+        if out is None:
+            e = lambda *s, dtype=f32: torch.empty(s, dtype=dtype, device=self.device)
+            out = LogprobOutput(e(M) if ids is not None else None, e(M), e(M, top, dtype=i32) if top else None,
+                                e(M, top) if top else None, e(M, 2))
+        else:
+            want = {"logprob": ((M,), f32) if ids is not None else None, "entropy": ((M,), f32),
+                    "top_ids": ((M, top), i32) if top else None, "top_logprobs": ((M, top), f32) if top else None,
+                    "stats": ((M, 2), f32)}
+            for name, w in want.items():
+                t = getattr(out, name)
+                if (t is None) != (w is None):
+                    raise ValueError(f"out.{name} does not go with ids and top")
+                if w:
+                    self._flat(t, w[1], w[0], f"out.{name}")
+        if M:
+            if R == 0:
+                raise ValueError("logits has no rows")
+            _check(specdec_logprobs(self._h, x, dt, stride, R, V, float(T), _ptr(ids) or None, _ptr(rows) or None,
+                                    M, top, _ptr(out.logprob) or None, out.entropy.data_ptr(),
+                                    _ptr(out.top_ids) or None, _ptr(out.top_logprobs) or None,
+                                    out.stats.data_ptr(), _stream_handle(self.device)), "specdec_logprobs")
+        return out
+
+    def logprobs_grad(self, logits: torch.Tensor, ids: torch.Tensor | None, forward: "LogprobOutput", *,
+                      grad_logprob: torch.Tensor | None = None, grad_entropy: torch.Tensor | None = None,
+                      grad_top: torch.Tensor | None = None, T: float = 1.0,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+        """The gradient of the logits from those of what ``logprobs`` gave (``forward``,
+        with the same logits, ids and T and without ``rows``), float32 [M], [M] and [M,
+        top]: specdec_logprobs_grad.  Returns [M, V] of the logits' type; ``out`` may be
+        the logits themselves."""
+        f32 = torch.float32
+        x, dt, stride = self._logit_rows(logits, "logits")
+        (R, V), M = logits.shape, forward.stats.shape[0]
+        if M != R:
+            raise ValueError("the gradient needs a token for every row of the logits")
+        if ids is not None:
+            self._flat(ids, torch.int32, (M,), "ids")
+        if (ids is None) != (forward.logprob is None):
+            raise ValueError("ids are not those of the forward call")
+        top = 0 if forward.top_ids is None else forward.top_ids.shape[1]
+        self._flat(forward.stats, f32, (M, 2), "forward.stats")
+        self._flat(forward.entropy, f32, (M,), "forward.entropy")
+        if ids is not None:
+            self._flat(forward.logprob, f32, (M,), "forward.logprob")
+        if top:
+            self._flat(forward.top_ids, torch.int32, (M, top), "forward.top_ids")
+            self._flat(forward.top_logprobs, f32, (M, top), "forward.top_logprobs")
+        for t, shape, name in ((grad_logprob, (M,), "grad_logprob"), (grad_entropy, (M,), "grad_entropy"),
+                               (grad_top, (M, top), "grad_top")):
+            if t is not None:
+                self._flat(t, f32, shape, name)
+        if grad_logprob is not None and ids is None:
+            raise ValueError("grad_logprob without ids")
+        if grad_top is not None and not top:
+            raise ValueError("grad_top without alternatives")
+        if out is None:
+            out = torch.empty(M, V, dtype=logits.dtype, device=self.device)
+        o, odt, ostride = self._logit_rows(out, "out")
+        if out.shape != logits.shape or odt != dt:
+            raise ValueError("out must be like the logits")
+        if M:
+            _check(specdec_logprobs_grad(
+                self._h, x, dt, stride, V, float(T), _ptr(ids) or None, M, top, _ptr(forward.logprob) or None,
+                forward.entropy.data_ptr(), _ptr(forward.top_ids) or None, _ptr(forward.top_logprobs) or None,
+                forward.stats.data_ptr(), _ptr(grad_logprob) or None, _ptr(grad_entropy) or None,
+                _ptr(grad_top) or None, o, ostride, _stream_handle(self.device)), "specdec_logprobs_grad")
+        return out
+
+    def rotate(self, x: torch.Tensor, positions: torch.Tensor, rotary: torch.Tensor, *, axes=None,
+               interleaved: bool = False, inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+        """Dense rows x [N, heads, head_dim] (bfloat16 or float16, any row and head
+        strides) turned by positions (int32 [N], or [axes, N] with ``axes``, the axis of
+        each pair: ``rotary_axes``) of the table ``rotary`` (``rotary_table``), pairs as
+        in ``KVCache.append``: specdec_rotate.  ``inverse`` turns back, which is also
+        the gradient.  Returns contiguous rows, or ``out``: x itself or rows of their own."""
+        if x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float16) or x.get_device() != self._at:
+            raise ValueError("x must be bfloat16 or float16 [N, heads, head_dim] on the device")
+        N, heads, D = x.shape
+        if out is None:
+            out = torch.empty(N, heads, D, dtype=x.dtype, device=self.device)
+        elif out.shape != x.shape or out.dtype != x.dtype or out.get_device() != self._at:
+            raise ValueError("out must be like x")
+        for t, name in ((x, "x"), (out, "out")):
+            row, head, one = t.stride()
+            if N and (one != 1 or row % 8 or head % 8 or t.data_ptr() % 16):
+                raise ValueError(f"{name} needs contiguous values, 16-byte aligned rows and strides of multiples of 8")
+        if D % 8 or not heads:
+            raise ValueError("x needs heads, of a multiple of 8 values")
+        table, count, dim = rotary_args(rotary, self._at, D)
+        pos, stride, n, which = position_args(positions, axes, N, dim // 2, self._at)
+        if N:
+            _check(specdec_rotate(self._h, _LOGITS[x.dtype], x.data_ptr(), x.stride(0), x.stride(1), N, heads, D,
+                                  pos, stride, n, which, table, dim, count, int(interleaved), int(inverse),
+                                  out.data_ptr(), out.stride(0), out.stride(1), _stream_handle(self.device)),
+                   "specdec_rotate")
+        return out
+
     def __call__(self, target_logits: torch.Tensor, draft_probs: torch.Tensor | None,
                  draft_ids: torch.Tensor, cu_num_draft_tokens: torch.Tensor, T: float, seed: int,
                  *, with_beta: bool = True, extended: bool = False,
@@ -235,6 +390,69 @@ class Verifier:
                 _ptr(out.num_accepted), _ptr(out.beta), stream)
         _check(rc, "specdec_rejection_sample")
         return out
+
+
+def rotary_args(rotary: torch.Tensor, at: int, head_dim: int) -> tuple[int, int, int]:
+    """Data pointer, positions and turning dimensions of a table of cos and sin."""
+    if rotary.dim() != 3 or rotary.shape[1] != 2 or rotary.dtype is not torch.float32 \
+            or rotary.get_device() != at or not rotary.is_contiguous():
+        raise ValueError("rotary must be contiguous float32 [positions, 2, rotary_dim / 2] on the device")
+    count, dim = rotary.shape[0], 2 * rotary.shape[2]
+    if dim % 16 or not 0 < dim <= min(head_dim, 128) or not count:
+        raise ValueError("rotary_dim must be a multiple of 16 up to head_dim and 128")
+    return rotary.data_ptr(), count, dim
+
+
+def position_args(positions: torch.Tensor, axes, N: int, pairs: int, at: int):
+    """Data pointer and stride of positions, the number of axes and each pair's own."""
+    if positions.dtype is not torch.int32 or positions.get_device() != at or positions.dim() not in (1, 2) \
+            or positions.shape[-1] != N or (N > 1 and positions.stride(-1) != 1):
+        raise ValueError("positions must be int32 [N] or [axes, N] on the device, the rows' neighbours")
+    n = 1 if positions.dim() == 1 else positions.shape[0]
+    if not 1 <= n <= SPECDEC_MAX_AXES:
+        raise ValueError(f"positions must have 1 .. {SPECDEC_MAX_AXES} axes")
+    if n > 1 and axes is None:
+        raise ValueError("positions on several axes need the axis of each pair")
+    stride = positions.stride(0) if n > 1 else N
+    if stride < N:
+        raise ValueError("positions must have rows of their own")
+    if axes is None:
+        return positions.data_ptr(), stride, n, None
+    which = tuple(axes)
+    if len(which) != pairs or min(which) < 0 or max(which) >= n:
+        raise ValueError(f"axes must be {pairs} entries, one for each pair, below {n}")
+    return positions.data_ptr(), stride, n, bytes(which)
+
+
+def rotary_axes(sections, *, spread: bool = False) -> tuple[int, ...]:
+    """The axis of each rotary pair for ``sections``, the number of pairs of each axis
+    (of time, height and width, say): one block of pairs after the other, or with
+    ``spread`` dealt in turn, 0, 1, 2, 0, 1, 2, ..., an axis that has its share passed
+    over."""
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0 or not sum(left):
+        raise ValueError("sections must be the number of pairs of each axis")
+    if not spread:
+        return tuple(a for a, n in enumerate(left) for _ in range(n))
+    got = []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                left[a] -= 1
+                got.append(a)
+    return tuple(got)
+
+
+def tree_rows(path: torch.Tensor, cu_num_nodes: torch.Tensor) -> torch.Tensor:
+    """The target row (int32 [N]) that each slot of ``Verifier.tree``'s tokens comes
+    from: node 0's for a request's first token, then those of the accepted nodes; -1
+    where no token stands."""
+    first = cu_num_nodes[:-1].long()
+    slots = torch.arange(path.numel(), device=path.device)
+    req = torch.searchsorted(cu_num_nodes[1:].contiguous(), slots.to(torch.int32), right=True).clamp(max=first.numel() - 1)
+    before = torch.cat([path.new_zeros(1), path[:-1]])
+    node = torch.where(slots == first[req], 0, before)
+    return torch.where(node >= 0, first[req] + node, -1).to(torch.int32)
 
 
 @dataclass
