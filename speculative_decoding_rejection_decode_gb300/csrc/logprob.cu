@@ -2,7 +2,11 @@
 // their rows, and the gradient of the logits.  Contract in include/specdec.h
 // (specdec_logprobs, specdec_logprobs_grad).
 //
-// One pass over a row.  With c = log2(e) / T, a reference rho near the row's largest
+// One pass over a row, bound by memory where rows are many: 2048 rows of 128256 bf16 90 us,
+// 5.8 TB/s (with 20 alternatives 114); 640 of 151936 36 us, 5.4 TB/s (48; all rows in one
+// wave of blocks).  Two batches of loads take turns, so that one is always under way; 6
+// blocks of an SM instead of 5 took 98 and 40 us, 256 threads in 3 blocks 93 and 43.
+//  With c = log2(e) / T, a reference rho near the row's largest
 // logit and y_v = (x_v - rho) c,
 //   S = sum 2^y_v,  W = sum 2^y_v y_v,
 //   ln p(v) = ln 2 (y_v - log2 S),  H = ln 2 (log2 S - W / S).
@@ -21,22 +25,40 @@
 namespace specdec {
 namespace {
 
-constexpr int kNT = 512, kNW = kNT / 32;   // threads of a row's block
+constexpr int kNT = 128, kNW = kNT / 32;   // threads of a row's block
+constexpr int kBlocks = 5;                 // of them on an SM
 constexpr int kU = 4;                      // 16-byte loads of a thread under way together
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kFloor = -1000.0f;         // y of entries without weight, where they meet a product
 constexpr float kLazy = 8.0f;              // log2 of how far the reference may lag behind the largest entry
-constexpr int kCap = 96;                   // candidates of a warp at most
-constexpr int kSlack = 32;                 // candidates beyond n that a step may leave
+constexpr int kGroups = 64, kGroup = kNT / kGroups;   // groups of threads, whose largest entries set the bound
+constexpr int kRoom = 1024;                // 16-byte pieces that a block puts aside at most, and candidates
+constexpr int kCap = 96;                   // of a warp's list, where those were too many
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 template <typename T>
-struct Row;   // what differs between the types of logits
+struct Row;   // what differs between the types of logits (raised, lifted: to at least low, or NaN)
 
 template <>
 struct Row<float> {
   static constexpr int E = 4;
   static constexpr uint32_t kNone = 0xFF800000u;   // -inf
-  using Max = float;
+  using Low = float;
+  static __device__ __forceinline__ Low below(float x) { return x; }
+  static __device__ __forceinline__ uint4 raised(const uint4& w, Low low) {
+    uint4 v;
+    const float* f = reinterpret_cast<const float*>(&w);
+    float* g = reinterpret_cast<float*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = max_nan(f[i], low);
+    return v;
+  }
+  static __device__ __forceinline__ float2 lifted(float2 f, Low) { return f; }
   static __device__ __forceinline__ float2 two(const uint4& w, int i) {
     const uint32_t* u = &w.x;
     return make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
@@ -49,6 +71,19 @@ template <>
 struct Row<__nv_bfloat16> {
   static constexpr int E = 8;
   static constexpr uint32_t kNone = 0xFF80FF80u;
+  using Low = __nv_bfloat162;
+  static __device__ __forceinline__ Low below(float x) {
+    const __nv_bfloat16 b = __float2bfloat16_rd(x);
+    return __nv_bfloat162(b, b);
+  }
+  static __device__ __forceinline__ uint4 raised(const uint4& w, Low low) {
+    uint4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<__nv_bfloat162*>(&v)[i] = __hmax2_nan(reinterpret_cast<const __nv_bfloat162*>(&w)[i], low);
+    return v;
+  }
+  static __device__ __forceinline__ float2 lifted(float2 f, Low) { return f; }
   static __device__ __forceinline__ float2 two(const uint4& w, int i) {
     const uint32_t u = (&w.x)[i];
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
@@ -64,6 +99,10 @@ template <>
 struct Row<__half> {
   static constexpr int E = 8;
   static constexpr uint32_t kNone = 0xFC00FC00u;
+  using Low = float;   // f16 does not reach far enough below its values
+  static __device__ __forceinline__ Low below(float x) { return x; }
+  static __device__ __forceinline__ uint4 raised(const uint4& w, Low) { return w; }
+  static __device__ __forceinline__ float2 lifted(float2 f, Low low) { return make_float2(max_nan(f.x, low), max_nan(f.y, low)); }
   static __device__ __forceinline__ float2 two(const uint4& w, int i) {
     return __half22float2(reinterpret_cast<const __half2*>(&w)[i]);
   }
@@ -132,19 +171,36 @@ __device__ __forceinline__ void move_to(Sums& a, float rho, float c) {
   }
   a.rho = rho;
 }
-__device__ __forceinline__ void join(Sums& a, Sums b, float c) {
-  const float rho = a.rho != a.rho || b.rho != b.rho ? __uint_as_float(0x7FC00000u) : fmaxf(a.rho, b.rho);
+
+// All lanes' sums, in every lane.
+__device__ __forceinline__ Sums warp_join(Sums a, float c) {
+  float rho = a.rho;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float b = __shfl_xor_sync(0xFFFFFFFFu, rho, o);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(rho) : "f"(b));
+  }
   move_to(a, rho, c);
-  move_to(b, rho, c);
-  a.s += b.s;
-  a.w += b.w;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, o);
+    a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, o);
+  }
+  return a;
 }
 
 // ---- the largest entries of a row -----------------------------------------------
-// Entries are ordered by key: the value, then the lower index.  A warp looks at
-// entries of rising index, so of the value of its list's n-th none can follow; and what
-// lies below a value that n entries of the block's part are known to reach is left out
-// (which is known when differs from run to run, what is found does not).
+// Entries are ordered by key: the value, then the lower index.  A block takes a bound, a
+// value that n of its entries reach, from the largest entries of its 64 groups of threads
+// (the n-th largest of 64: a little below the n-th of all that they have seen), and takes
+// a new one whenever three times as many batches have gone by.  What reaches the bound
+// is put aside as the 16 bytes that hold it, about 10 n of them for a row in no order, and
+// looked at by all threads together when the row is through (entries looked at and keys
+// made by the thread that meets them, and one bound for the row: 238 us where this form
+// took 63, 640 rows of 151936 and n = 20).  Rows of many equal
+// entries, of a rising order or with fewer than n entries above -inf leave too many
+// candidates or too few: the block then goes over its part again with a list for each warp
+// (offer).
 
 __device__ __forceinline__ uint32_t order_of(float x) {   // -0 counts as 0
   const uint32_t u = __float_as_uint(x + 0.0f);
@@ -184,7 +240,10 @@ __device__ __forceinline__ int keep_most(uint64_t* buf, int cnt, int n) {
   return m;
 }
 
-// The least value that may still be among the n largest.
+// The least value that may still be among the n largest: a warp looks at entries of
+// rising index, so of the value of its list's n-th none can follow, and `known` is the
+// order of a value that n entries of the block's part are known to reach (when depends
+// on the run, what is found does not).
 __device__ __forceinline__ float bound_of(uint32_t own, const volatile uint32_t* known) {
   const uint32_t k = *known;
   return value_of(own > k ? own : k);
@@ -196,7 +255,6 @@ struct Listed {
 };
 
 // Offers the first m of the neighbouring entries in w, the first one's index given.
-// Out of line: a row's first steps come here often, the others hardly ever.
 template <typename T>
 __device__ __noinline__ Listed offer(uint64_t* buf, Listed s, int n, uint4 w, int m, uint32_t index, uint32_t* known) {
   const int lane = threadIdx.x & 31;
@@ -216,7 +274,7 @@ __device__ __noinline__ Listed offer(uint64_t* buf, Listed s, int n, uint4 w, in
     if (in) buf[s.cnt + __popc(who & ((1u << lane) - 1u))] = key_of(x, index + i);
     s.cnt += __popc(who);
   }
-  if (s.cnt > n + kSlack) {
+  if (s.cnt > n + 32) {
     s.cnt = keep_most(buf, s.cnt, n);
     const uint32_t last = (uint32_t)(buf[n - 1] >> 32);
     s.own = last + 1u;
@@ -227,14 +285,35 @@ __device__ __noinline__ Listed offer(uint64_t* buf, Listed s, int n, uint4 w, in
 }
 
 struct LogprobShared {
+  alignas(16) uint4 aside[kRoom];       // pieces with an entry that reached the bound,
+  uint32_t index[kRoom];                // and their first entries
+  alignas(16) float groups[kGroups];    // read 16 bytes at a time
   Sums part[kNW];
   Sums ranks[8];                        // of the cluster's blocks (rank 0)
-  uint32_t known;                       // order of a value that n entries are known to reach
+  uint32_t known;
+  int pieces, found;                    // put aside, and candidates: also those beyond the room
+  float bound;
   int count[kNW];
   uint64_t best[kMaxTop];
   uint64_t bests[8][kMaxTop];           // of the cluster's blocks (rank 0)
+  uint64_t cand[kRoom];
   uint64_t list[kNW][kCap];
 };
+
+// A warp's cnt <= 64 keys in order, the n largest to list.
+__device__ __forceinline__ int sort_most(const uint64_t* keys, int cnt, int n, uint64_t* list) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t k0 = lane < cnt ? keys[lane] : 0, k1 = lane + 32 < cnt ? keys[lane + 32] : 0;
+  int r0 = 0, r1 = 0;
+  for (int i = 0; i < cnt; ++i) {
+    const uint64_t k = keys[i];
+    r0 += k > k0;
+    r1 += k > k1;
+  }
+  if (k0 && r0 < n) list[r0] = k0;
+  if (k1 && r1 < n) list[r1] = k1;
+  return min(cnt, n);
+}
 
 // The n largest of sorted lists, lane i < lists holding list i, to out (0: none).
 template <typename At>
@@ -260,20 +339,10 @@ __device__ __forceinline__ void put_remote(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ Sums warp_join(Sums a, float c) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Sums b = {__shfl_xor_sync(0xFFFFFFFFu, a.rho, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
-                    __shfl_xor_sync(0xFFFFFFFFu, a.w, o)};
-    join(a, b, c);
-  }
-  return a;
-}
-
 // A token's row, by a cluster of 1, 2, 4 or 8 blocks that take a part of it each; rank
 // 0 joins the parts and writes.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kNT, 2) logprob_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kNT, kBlocks) logprob_kernel(const LogprobArgs a) {
   using R = Row<T>;
   constexpr int E = R::E;
   __shared__ LogprobShared sh;
@@ -305,16 +374,20 @@ __global__ void __launch_bounds__(kNT, 2) logprob_kernel(const LogprobArgs a) {
   const int vecs = (a.V - lead) / E, done = lead + vecs * E;
   const int v0 = (int)((int64_t)vecs * rank / ranks), v1 = (int)((int64_t)vecs * (rank + 1) / ranks);
   const uint4* xv = reinterpret_cast<const uint4*>(x + lead);
+  // entries before the first 16-byte boundary and behind the last: the first and last rank's
+  const int before = rank == 0 ? lead : 0, behind = rank == ranks - 1 ? a.V - done : 0;
   const float given = a.logprob && rank == 0 && tid == 0 ? as_float(x[id]) : 0.0f;
-  if constexpr (TOP) {
-    if (tid == 0) sh.known = order_of(-INFINITY);
-    __syncthreads();
+  if (TOP && tid == 0) {   // (the first bound's barrier follows)
+    sh.pieces = sh.found = 0;
+    sh.bound = -INFINITY;
   }
   Sums mine = {-INFINITY, 0.0f, 0.0f};
   uint64_t s2[2] = {0, 0}, w2[2] = {0, 0};
   const uint64_t c2 = pair(a.c, a.c);
   const float lag = kLazy / a.c;
-  [[maybe_unused]] Listed lst = {0, 0u};
+  float ref = 0.0f;
+  typename R::Low low = R::below(kFloor / a.c);   // entries of -inf count as this: 0 x -inf would be NaN
+  [[maybe_unused]] float bound = -INFINITY;
   auto gather = [&] {
     float p, q;
     unpair(add2(s2[0], s2[1]), p, q);
@@ -322,95 +395,177 @@ __global__ void __launch_bounds__(kNT, 2) logprob_kernel(const LogprobArgs a) {
     unpair(add2(w2[0], w2[1]), p, q);
     mine.w = p + q;
   };
-  // U x 16 bytes of a thread, of which the first m entries of each count
-  auto take = [&](const uint4* w, auto count, int m, uint32_t index) {
-    constexpr int U = decltype(count)::value;
+  auto most_of = [&](const uint4* w, auto count) {
     float most = R::most(w[0]);
 #pragma unroll
-    for (int u = 1; u < U; ++u) most = fmaxf(most, R::most(w[u]));
+    for (int u = 1; u < decltype(count)::value; ++u) most = fmaxf(most, R::most(w[u]));
+    return most;
+  };
+  // U x 16 bytes of a thread; the first one's first index, and how far the others' lie apart
+  auto take = [&](const uint4* w, auto count, float most, uint32_t index, uint32_t apart) {
+    constexpr int U = decltype(count)::value;
     if (!(most <= mine.rho + lag)) {          // first entries, larger ones, NaN
       gather();
       move_to(mine, most, a.c);
       s2[0] = pair(mine.s, 0.0f);
       w2[0] = pair(mine.w, 0.0f);
       s2[1] = w2[1] = 0;
+      ref = -mine.rho;
+      // far enough below that 2^y is 0, however rho is rounded
+      low = R::below(mine.rho - fmaxf(-kFloor / a.c, fabsf(mine.rho) * 0.03125f));
     }
-    const float ref = mine.rho == -INFINITY ? 0.0f : -mine.rho;
     const uint64_t r2 = pair(ref, ref);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const uint4 v = R::raised(w[u], low);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
-        const float2 f = R::two(w[u], i);
+        const float2 f = R::lifted(R::two(v, i), low);
         float y0, y1;
-        unpair(mul2(add2(pair(f.x, f.y), r2), c2), y0, y1);
+        const uint64_t y2 = mul2(add2(pair(f.x, f.y), r2), c2);
+        unpair(y2, y0, y1);
         const uint64_t e2 = pair(ex2(y0), ex2(y1));
         s2[i & 1] = add2(s2[i & 1], e2);
-        // 2^y is 0 there, and 0 x -inf would not be
-        w2[i & 1] = fma2(e2, pair(fmaxf(y0, kFloor), fmaxf(y1, kFloor)), w2[i & 1]);
+        w2[i & 1] = fma2(e2, y2, w2[i & 1]);
       }
-    if constexpr (TOP) {
-      if (__any_sync(0xFFFFFFFFu, most >= bound_of(lst.own, &sh.known))) {
+    }
+    if (TOP && most >= bound) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (__any_sync(0xFFFFFFFFu, R::most(w[u]) >= bound_of(lst.own, &sh.known)))
-            lst = offer<T>(sh.list[warp], lst, n, w[u], m, index + u * (kNT * E), &sh.known);
-      }
+      for (int u = 0; u < U; ++u)
+        if (R::most(w[u]) >= bound) {
+          const int at = atomicAdd(&sh.pieces, 1);
+          if (at < kRoom) {
+            sh.aside[at] = w[u];
+            sh.index[at] = index + u * apart;
+          }
+        }
     }
   };
-  // A first value that n entries reach: the n-th of the lanes' largest.
-  auto first_bound = [&](float most) {
-    uint64_t k = key_of(most, lane), best = 0;
-    for (int r = 0; r < n; ++r) {
-      best = warp_most(k);
-      if (k == best) k = 0;
-    }
-    if (lane == 0 && value_of((uint32_t)(best >> 32)) == value_of((uint32_t)(best >> 32)))
-      atomicMax(&sh.known, (uint32_t)(best >> 32));
+  // A bound from what the threads have seen: a group's threads find the place of their
+  // largest entry among the others'.
+  auto new_bound = [&](float seen) {
+#pragma unroll
+    for (int o = 1; o < kGroup; o <<= 1) seen = fmaxf(seen, __shfl_xor_sync(0xFFFFFFFFu, seen, o));
+    if (tid % kGroup == 0) sh.groups[tid / kGroup] = seen;
     __syncthreads();
+    int above = 0, reach = 0;
+#pragma unroll
+    for (int i = 0; i < kGroups / kGroup; i += 4) {
+      const float4 k = *reinterpret_cast<const float4*>(&sh.groups[tid % kGroup * (kGroups / kGroup) + i]);
+      above += (k.x > seen) + (k.y > seen) + (k.z > seen) + (k.w > seen);
+      reach += (k.x >= seen) + (k.y >= seen) + (k.z >= seen) + (k.w >= seen);
+    }
+    int both = above | reach << 16;
+#pragma unroll
+    for (int o = 1; o < kGroup; o <<= 1) both += __shfl_xor_sync(0xFFFFFFFFu, both, o);
+    if ((both & 0xFFFF) < n && both >> 16 >= n) sh.bound = seen;   // the n-th largest
+    __syncthreads();
+    bound = sh.bound;
   };
   using Many = std::integral_constant<int, kU>;
   using One = std::integral_constant<int, 1>;
   const uint4 none = make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
-  if (rank == 0 && lead > 0 && warp == 0) {   // up to the first 16-byte boundary
-    uint4 w = none;
-    if (lane < lead) *reinterpret_cast<T*>(&w) = x[lane];
-    take(&w, One(), lane < lead ? 1 : 0, (uint32_t)lane);
-  }
-  int v = v0;
-  for (; v + kU * kNT <= v1; v += kU * kNT) {
-    uint4 w[kU];
+  // A thread's loads lie a kU-th of the part apart: the first ones, which set the bound,
+  // then come from all over it.
+  const int steps = (v1 - v0) / (kU * kNT);
+  [[maybe_unused]] float seen = -INFINITY;
+  int next = 0;                        // the batch behind which the bound is taken anew
+  auto load = [&](uint4* w, int s) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) w[u] = load_once(xv + v + u * kNT + tid);
-    if (TOP && v == v0) {
-      float most = R::most(w[0]);
-#pragma unroll
-      for (int u = 1; u < kU; ++u) most = fmaxf(most, R::most(w[u]));
-      first_bound(most);
+    for (int u = 0; u < kU; ++u) w[u] = load_once(xv + v0 + (u * steps + s) * kNT + tid);
+  };
+  auto batch = [&](const uint4* w, int s) {
+    const float most = most_of(w, Many());
+    if constexpr (TOP) {
+      seen = fmaxf(seen, most);
+      if (s == next) {
+        new_bound(seen);
+        next = 3 * next + 2;
+      }
     }
-    take(w, Many(), E, (uint32_t)(lead + (v + tid) * E));
+    take(w, Many(), most, (uint32_t)(lead + (v0 + s * kNT + tid) * E), (uint32_t)(steps * kNT * E));
+  };
+  uint4 wa[kU], wb[kU];                // one batch is under way while the other is taken in
+  if (steps > 0) load(wa, 0);
+  for (int s = 0; s < steps; s += 2) {
+    if (s + 1 < steps) load(wb, s + 1);
+    batch(wa, s);
+    if (s + 1 < steps) {
+      if (s + 2 < steps) load(wa, s + 2);
+      batch(wb, s + 1);
+    }
   }
-  for (; v < v1; v += kNT) {
-    const bool in = v + tid < v1;
+  for (int v = v0 + steps * kU * kNT; v < v1; v += kNT) {
     uint4 w = none;
-    if (in) w = load_once(xv + v + tid);
-    if (TOP && v == v0) first_bound(R::most(w));
-    take(&w, One(), in ? E : 0, (uint32_t)(lead + (v + tid) * E));
+    if (v + tid < v1) w = load_once(xv + v + tid);
+    const float most = R::most(w);
+    if (TOP && v == v0) new_bound(most);
+    take(&w, One(), most, (uint32_t)(lead + (v + tid) * E), 0u);
   }
-  if (rank == ranks - 1 && done < a.V && warp == 0) {   // behind the last one
-    const bool in = lane < a.V - done;
+  if (TOP && v0 == v1) __syncthreads();       // pieces is set
+  if (before + behind > 0 && warp == 0) {     // fewer than 16 entries, a piece each
+    const int at = lane < before ? lane : done + lane - before;
     uint4 w = none;
-    if (in) *reinterpret_cast<T*>(&w) = x[done + lane];
-    take(&w, One(), in ? 1 : 0, (uint32_t)(done + lane));
+    if (lane < before + behind) *reinterpret_cast<T*>(&w) = x[at];
+    take(&w, One(), R::most(w), (uint32_t)at, 0u);
   }
   gather();
   mine = warp_join(mine, a.c);
   if (lane == 0) sh.part[warp] = mine;
-  if constexpr (TOP) {
-    const int kept = keep_most(sh.list[warp], lst.cnt, n);
-    if (lane == 0) sh.count[warp] = kept;
-  }
   __syncthreads();
+  if constexpr (TOP) {
+    const int pieces = sh.pieces, entries = (v1 - v0) * E + before + behind;
+    for (int i = tid; pieces <= kRoom && i < pieces; i += kNT) {
+      const uint4 w = sh.aside[i];
+      const uint32_t index = sh.index[i];
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const float2 f = R::two(w, k >> 1);
+        const float e = k & 1 ? f.y : f.x;
+        if (e >= bound && e != -INFINITY) {
+          const int at = atomicAdd(&sh.found, 1);
+          if (at < kRoom) sh.cand[at] = key_of(e, index + k);
+        }
+      }
+    }
+    __syncthreads();
+    const int found = sh.found;
+    if (pieces <= kRoom && found <= kRoom && found >= min(n, entries)) {
+      const int per = (found + kNW - 1) / kNW, at = min(found, warp * per);
+      const int cnt = min(per, found - at);
+      int kept = 0;
+      for (int i = 0; i < cnt; i += 64) {     // once, as a rule
+        kept += sort_most(sh.cand + at + i, min(64, cnt - i), n, sh.list[warp] + kept);
+        if (i > 0) kept = keep_most(sh.list[warp], kept, n);
+      }
+      if (lane == 0) sh.count[warp] = kept;
+    } else {
+      // lists for each warp, of rising indices
+      if (tid == 0) sh.known = order_of(-INFINITY);
+      __syncthreads();
+      Listed lst = {0, 0u};
+      if (before > 0 && warp == 0) {
+        uint4 w = none;
+        if (lane < before) *reinterpret_cast<T*>(&w) = x[lane];
+        lst = offer<T>(sh.list[warp], lst, n, w, lane < before ? 1 : 0, (uint32_t)lane, &sh.known);
+      }
+      for (int v = v0; v < v1; v += kNT) {
+        const bool in = v + tid < v1;
+        uint4 w = none;
+        if (in) w = __ldg(xv + v + tid);
+        if (__any_sync(0xFFFFFFFFu, in && R::most(w) >= bound_of(lst.own, &sh.known)))
+          lst = offer<T>(sh.list[warp], lst, n, w, in ? E : 0, (uint32_t)(lead + (v + tid) * E), &sh.known);
+      }
+      if (behind > 0 && warp == 0) {
+        uint4 w = none;
+        if (lane < behind) *reinterpret_cast<T*>(&w) = x[done + lane];
+        lst = offer<T>(sh.list[warp], lst, n, w, lane < behind ? 1 : 0, (uint32_t)(done + lane), &sh.known);
+      }
+      const int kept = keep_most(sh.list[warp], lst.cnt, n);
+      if (lane == 0) sh.count[warp] = kept;
+    }
+    __syncthreads();
+  }
   if (warp == 0) {
     const Sums empty = {-INFINITY, 0.0f, 0.0f};
     mine = warp_join(lane < kNW ? sh.part[lane] : empty, a.c);
@@ -433,9 +588,7 @@ __global__ void __launch_bounds__(kNT, 2) logprob_kernel(const LogprobArgs a) {
     if (warp == 0) {
       const Sums empty = {-INFINITY, 0.0f, 0.0f};
       mine = warp_join(lane < ranks ? sh.ranks[lane] : empty, a.c);
-      if constexpr (TOP) {
-        merge_sorted(ranks, n, [&](int l, int p) { return sh.bests[l][p]; }, sh.best);
-      }
+      if constexpr (TOP) merge_sorted(ranks, n, [&](int l, int p) { return sh.bests[l][p]; }, sh.best);
     }
   }
   if (warp) return;
@@ -554,10 +707,12 @@ __global__ void __launch_bounds__(kGT) logprob_grad_kernel(const LogprobGradArgs
 
 template <typename T>
 int forward_of(const LogprobArgs& a, int num_sms, cudaStream_t st) {
-  // Blocks of a row: enough that every SM has two, of at least one load a thread.
+  // Blocks of a row: as many as the SMs hold at once, of at least two loads a thread.
+  // us of 1, 2, 4, 8 blocks a row (256 threads each): 48 rows of 32000 f32 7.3, 6.3, 5.3,
+  // 5.2; 152 of 128256 bf16 15.5, 12.4, 14.5, 16.4; 640 of 151936 46, 44, 48, 60.
   const int vecs = a.V / Row<T>::E;
   int ranks = 1;
-  while (ranks < 8 && a.M * ranks < 2 * num_sms && vecs / (2 * ranks) >= kNT) ranks *= 2;
+  while (ranks < 8 && 2 * a.M * ranks <= kBlocks * num_sms && vecs / (2 * ranks) >= 2 * kNT) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.M * ranks));
   cfg.blockDim = dim3(kNT);

@@ -381,10 +381,10 @@ bool meet_rows(const void* out, int64_t out_bytes, const void* p, int64_t row, i
   return N > 0 && meet(out, out_bytes, static_cast<const char*>(p) + 2 * first, 2 * (last - first));
 }
 
-// Sizes of the calls on rows of logits.  T below 2^-60 would leave the exponent's range.
+// Sizes of the calls on rows of logits.  Beyond T = 2^-60 .. 2^60 log2(e) / T leaves no room in the exponent.
 bool logit_sizes_ok(int64_t row_stride, int64_t num_rows, int V, float T, int64_t n_tokens, int top) {
   return V > 0 && V <= (1 << 30) && row_stride >= V && num_rows >= 0 && num_rows < ((int64_t)1 << 31) && n_tokens >= 0 &&
-         n_tokens < ((int64_t)1 << 31) && top >= 0 && top <= kMaxTop && T >= 8.673617379884035e-19f && std::isfinite(T);
+         n_tokens < ((int64_t)1 << 31) && top >= 0 && top <= kMaxTop && T >= 8.673617379884035e-19f && T <= 1.152921504606847e18f;
 }
 
 // The kernels' view of the axes of rotary pairs (each below num_axes; null: all 0).

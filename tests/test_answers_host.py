@@ -22,7 +22,7 @@ def test_log_probabilities_are_checked_before_any_device_work(lib):  # noqa: F81
 
     assert call(dtype=lib.SPECDEC_E4M3) == DTYPE
     for bad in (dict(logits=None), dict(logits=(1 << 30) + 1), dict(row_stride=99), dict(num_rows=3), dict(num_rows=0), dict(V=0),
-                dict(V=(1 << 30) + 1), dict(T=0.0), dict(T=-1.0), dict(T=math.inf), dict(T=math.nan), dict(T=1e-30), dict(ids=None),
+                dict(V=(1 << 30) + 1), dict(T=0.0), dict(T=-1.0), dict(T=math.inf), dict(T=math.nan), dict(T=1e-30), dict(T=2e18), dict(ids=None),
                 dict(n_tokens=-1), dict(n_tokens=1 << 31), dict(top=-1), dict(top=33), dict(out_top_ids=None),
                 dict(out_top_logprobs=None), dict(out_stats=(1 << 25) + 4),
                 dict(out_logprob=None, out_entropy=None, top=0, out_stats=None),
