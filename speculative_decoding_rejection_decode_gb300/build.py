@@ -13,9 +13,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libspecdec.so")
 SOURCES = ["specdec.cu", "noalloc.cu", "tree.cu", "cache.cu", "attention.cu",
-           "attention_tile.cu", "given.cu", "cross.cu", "cross_tile.cu", "rotary.cu", "logprob.cu"]
+           "attention_tile.cu", "given.cu", "cross.cu", "cross_tile.cu", "cross_wide.cu", "rotary.cu", "logprob.cu"]
 HEADERS = ["device_common.cuh", "kernels.cuh", "tree.cuh", "paged_index.h", "cache.cuh", "attention.cuh",
-           "attention_warp.cuh", "attention_tile.cuh", "row_values.cuh", "logprob.cuh"]
+           "attention_warp.cuh", "attention_tile.cuh", "attention_tc.cuh", "row_values.cuh", "logprob.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

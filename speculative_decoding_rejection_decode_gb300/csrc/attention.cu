@@ -21,12 +21,26 @@ int64_t average_rows(int B, int64_t N, int kv_heads, int q_heads) {
 // large one takes a tile of 16 rows at a time.
 constexpr int kWarpRows = 16;
 
+// Which kernel serves a call.
+enum class Kernel { kWarp, kTile, kWide };
+
+constexpr int kTileRows = 128;   // rows of a tile of the tile kernel
+
+Kernel kernel_of(bool cross, int cache_dtype, int page_size, int64_t avg) {
+  if (avg <= kWarpRows) return Kernel::kWarp;
+  return cross && cache_dtype != SPECDEC_E4M3 && page_size % 8 == 0 && avg > kTileRows ? Kernel::kWide : Kernel::kTile;
+}
+
+int rows_of(Kernel k) { return k == Kernel::kWarp ? kRowsTile : k == Kernel::kTile ? kTileRows : kWideRows; }
+
 }  // namespace
 
-int64_t attend_workspace_bytes(bool cross, int B, int64_t N, int kv_heads, int q_heads, int head_dim, int64_t capacity, int num_sms) {
-  const bool tile = average_rows(B, N, kv_heads, q_heads) > kWarpRows;
-  if (whole_items(B, N, kv_heads, q_heads, capacity, tile ? 128 : kRowsTile, num_sms)) return 0;
-  if (tile) return attend_tile_workspace(head_dim, num_sms);
+int64_t attend_workspace_bytes(bool cross, int cache_dtype, int page_size, int B, int64_t N, int kv_heads, int q_heads,
+                               int head_dim, int64_t capacity, int num_sms) {
+  const Kernel k = kernel_of(cross, cache_dtype, page_size, average_rows(B, N, kv_heads, q_heads));
+  if (whole_items(B, N, kv_heads, q_heads, capacity, rows_of(k), num_sms)) return 0;
+  if (k == Kernel::kWide) return cross_wide_workspace(head_dim, num_sms);
+  if (k == Kernel::kTile) return attend_tile_workspace(head_dim, num_sms);
   return head_dim == 128 ? Partials<kRowsTile, 128>::bytes(num_sms) : Partials<kRowsTile, 64>::bytes(num_sms);
 }
 
@@ -34,13 +48,12 @@ int launch_attend(const AttendArgs& args, int cache_dtype, int dtype, int num_sm
   if (args.c.N == 0) return SPECDEC_OK;
   AttendArgs a = args;
   const CacheArgs& c = a.c;
-  const bool tile = average_rows(c.B, c.N, c.geo.kv_heads, a.q_heads) > kWarpRows;
-  a.whole = whole_items(c.B, c.N, c.geo.kv_heads, a.q_heads, (int64_t)c.geo.max_pages * c.geo.page_size, tile ? 128 : kRowsTile, num_sms);
-  a.item_cost = cache_dtype == SPECDEC_E4M3 && !tile ? kItemCostWarp8 : kItemCost;
-  if (a.cross) {
-    return tile ? launch_cross_tile(a, cache_dtype, dtype, num_sms, st) : launch_cross_warp(a, cache_dtype, dtype, num_sms, st);
-  }
-  return tile ? launch_attend_tile(a, cache_dtype, dtype, num_sms, st) : launch_warp_types<false>(a, cache_dtype, dtype, num_sms, st);
+  const Kernel k = kernel_of(a.cross, cache_dtype, c.geo.page_size, average_rows(c.B, c.N, c.geo.kv_heads, a.q_heads));
+  a.whole = whole_items(c.B, c.N, c.geo.kv_heads, a.q_heads, (int64_t)c.geo.max_pages * c.geo.page_size, rows_of(k), num_sms);
+  a.item_cost = cache_dtype == SPECDEC_E4M3 && k == Kernel::kWarp ? kItemCostWarp8 : kItemCost;
+  if (k == Kernel::kWide) return launch_cross_wide(a, dtype, num_sms, st);
+  if (k == Kernel::kTile) return a.cross ? launch_cross_tile(a, cache_dtype, dtype, num_sms, st) : launch_attend_tile(a, cache_dtype, dtype, num_sms, st);
+  return a.cross ? launch_cross_warp(a, cache_dtype, dtype, num_sms, st) : launch_warp_types<false>(a, cache_dtype, dtype, num_sms, st);
 }
 
 }  // namespace specdec

@@ -329,6 +329,10 @@ int launch_attend_tile(const AttendArgs& a, int cache_dtype, int dtype, int num_
 // Both kernels over an encoder's states (cross_tile.cu, cross.cu).
 int launch_cross_tile(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
 int launch_cross_warp(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
+// Many rows per request over 16-bit states in pages of a multiple of 8 slots (cross_wide.cu).
+constexpr int kWideRows = 256;   // of an item's tile
+int launch_cross_wide(const AttendArgs& a, int dtype, int num_sms, cudaStream_t st);
+int64_t cross_wide_workspace(int head_dim, int num_sms);
 int64_t attend_tile_workspace(int head_dim, int num_sms);
 
 

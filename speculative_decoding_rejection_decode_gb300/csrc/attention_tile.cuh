@@ -47,12 +47,11 @@
 
 #include <type_traits>
 
-#include "attention.cuh"
+#include "attention_tc.cuh"
 
 namespace specdec {
 namespace {
 
-constexpr int kR = 128, kTK = 128;
 constexpr int kGroupWarps = 4;                       // softmax warps of a group
 constexpr int kSoftmaxThreads = 2 * kGroupWarps * 32;
 constexpr int kFinishWarps = 4;
@@ -109,186 +108,6 @@ struct TileShared {
   int dead;                         // a wait ran out
 };
 
-// ---- tcgen05 -------------------------------------------------------------------
-// Issued by one thread (`one`) of a warp that takes part as a whole: descriptors
-// then stay in uniform registers (issued from inside a divergent branch every
-// product paid for moving them there, about 110 clocks instead of 64).
-__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// d (+)= A B, both in shared memory
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(add), "r"(one)
-      : "memory");
-}
-// the same for e4m3 factors, 32 of the summed dimension
-__device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(add), "r"(one)
-      : "memory");
-}
-// d (+)= A B, A in tensor memory
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(add), "r"(one)
-      : "memory");
-}
-
-// Neighbouring columns of this thread's lane.  The wait stands in the same
-// statement, so that no use of the values can move before it.
-__device__ __forceinline__ void tc_ld32(uint32_t addr, float* x) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(x);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]),"=r"(r[1]),"=r"(r[2]),"=r"(r[3]),"=r"(r[4]),"=r"(r[5]),"=r"(r[6]),"=r"(r[7]),"=r"(r[8]),"=r"(r[9]),"=r"(r[10]),"=r"(r[11]),"=r"(r[12]),"=r"(r[13]),"=r"(r[14]),"=r"(r[15]),"=r"(r[16]),"=r"(r[17]),"=r"(r[18]),"=r"(r[19]),"=r"(r[20]),"=r"(r[21]),"=r"(r[22]),"=r"(r[23]),"=r"(r[24]),"=r"(r[25]),"=r"(r[26]),"=r"(r[27]),"=r"(r[28]),"=r"(r[29]),"=r"(r[30]),"=r"(r[31])
-      : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Shared-memory operand descriptor: swizzled rows of LINE = 128 (or 64) bytes in
-// groups of 8.  `lead`: bytes between 64-element chunks where the contiguous
-// dimension is not the one summed over (V).
-template <int LINE = 128>
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-  const uint32_t lo = ((addr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
-  const uint32_t hi = (8u * LINE >> 4) | (1u << 14) | ((LINE == 128 ? 2u : 4u) << 29);
-  return ((uint64_t)hi << 32) | lo;
-}
-
-// Instruction descriptors: f32 accumulators, 128 x n; 16-bit or e4m3 factors.
-template <typename E>
-__device__ __forceinline__ constexpr uint32_t product(int n, bool b_rows_summed) {
-  const uint32_t t = std::is_same<E, __half>::value ? 0u : 1u;
-  return (1u << 4) | (t << 7) | (t << 10) | (b_rows_summed ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
-         ((uint32_t)(kR >> 4) << 24);
-}
-__device__ __forceinline__ constexpr uint32_t product_e4m3(int n) {
-  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kR >> 4) << 24);
-}
-
-// Byte offset of 16-byte chunk c (of the row's 16-bit values) of row r of an
-// operand tile: [64-value half][row][128 bytes], chunks spread by the row.
-__device__ __forceinline__ uint32_t op_chunk(int r, int c) {
-  return (uint32_t)((c >> 3) * (kTK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
-// The same for a tile of 8-bit rows of D bytes.
-template <int D>
-__device__ __forceinline__ uint32_t byte_chunk(int r, int c) {
-  return (uint32_t)(r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
-}
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-// Arrives on `bar` once every copy that this thread has issued has landed.
-__device__ __forceinline__ void copy_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-// A box of rows `row`, ... from column x of the map's array; completes on `bar`.
-__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(row), "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Two 32-bit operations in one instruction, each rounded as alone.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-// 16 neighbouring floats in pairs, their loads under way together.
-__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t* f) {
-  asm volatile(
-      "ld.shared.v2.u64 {%0,%1}, [%8];\n\tld.shared.v2.u64 {%2,%3}, [%8+16];\n\t"
-      "ld.shared.v2.u64 {%4,%5}, [%8+32];\n\tld.shared.v2.u64 {%6,%7}, [%8+48];"
-      : "=l"(f[0]), "=l"(f[1]), "=l"(f[2]), "=l"(f[3]), "=l"(f[4]), "=l"(f[5]), "=l"(f[6]), "=l"(f[7])
-      : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // 8 f16 values times a pair of equal factors.
 __device__ __forceinline__ uint4 times(uint4 w, uint32_t by) {
   __half2* h = reinterpret_cast<__half2*>(&w);
@@ -329,63 +148,6 @@ __device__ __forceinline__ bool clear_nonfinite(uint4& w) {
     }
   }
   return any;
-}
-
-// A wait that gives up: the role goes on without waiting (its loops are finite
-// and its addresses do not depend on data), and the call reports the timeout.  A
-// try sleeps up to a microsecond, so the wait ends within seconds at the most.
-// (Kept this small because it stands in many places: with a clock read in each,
-// the kernel's code passed the instruction cache.)
-__device__ __forceinline__ void wait_or_give_up(TileShared& sh, uint32_t bar, uint32_t parity) {
-  for (int i = 0; i < (1 << 20); ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return;
-    if ((i & 255) == 255 && *reinterpret_cast<volatile int*>(&sh.dead)) return;
-  }
-  *reinterpret_cast<volatile int*>(&sh.dead) = 1;
-}
-
-// The segments of this CTA's range; every role steps through them by itself, on a
-// copy in shared memory (registers are short).
-struct Segments {
-  int64_t base;      // units before request b
-  int64_t end;
-  Request q;
-  int b, h, rt, t0, t1, rows;
-  int u;             // next unit, from base
-  bool whole, more;
-};
-
-__device__ __forceinline__ void next_segment(Segments* s, const PlanArgs c) {
-  s->more = false;
-  do {
-    if (s->base + s->u >= s->end) return;
-    uint32_t ignored = 0;
-    while (s->u >= (int)s->q.units) {
-      s->base += s->q.units;
-      s->u -= (int)s->q.units;
-      if (++s->b >= c.B) return;   // lengths that changed under the call
-      s->q = attend_request(c, s->b, kR, kTK, ignored);
-    }
-    const int tiles = c.whole ? 1 : s->q.tiles, rts = s->q.rts, u = s->u;
-    const int item = (int)((unsigned)u / (unsigned)(tiles + c.item_cost)), at = u - item * (tiles + c.item_cost);
-    s->t0 = max(at - c.item_cost, 0);
-    s->t1 = (int)min((int64_t)tiles, at - c.item_cost + (s->end - s->base - u));
-    s->h = (int)((unsigned)item / (unsigned)rts);
-    s->rt = item - s->h * rts;
-    s->u = u + tiles + c.item_cost - at;
-  } while (s->t1 <= s->t0);          // a range may end before an item's first tile
-  if (c.whole) s->t1 = s->q.tiles;
-  s->whole = s->t0 == 0 && s->t1 == s->q.tiles;
-  s->rows = min(kR, s->q.n * c.group - s->rt * kR);
-  s->more = true;
 }
 
 // Keys of tile t that a node's rows see, 128 bits; false for a malformed tree.
@@ -681,7 +443,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     s.base = scan.before;
     s.u = (int)(u0 - scan.before);
     s.q = attend_request(plan, scan.b, kR, kTK, ignored);
-    next_segment(&s, plan);
+    next_segment<kR>(&s, plan);
   }
   __syncthreads();
   uint32_t bad = 0;
@@ -689,14 +451,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // Registers: 4 warpgroups are launched with 128 a thread.  The softmax groups take
   // 40 more each from the two others (168 + 168 + 72 + 104 = 4 * 128).
   auto wait_use = [&](uint64_t* bars, int slots, int n) {       // use n of a ring's slot is complete
-    wait_or_give_up(sh, smem_addr(&bars[n % slots]), (uint32_t)(n / slots) & 1u);
+    wait_or_give_up(sh.dead, smem_addr(&bars[n % slots]), (uint32_t)(n / slots) & 1u);
   };
   auto wait_free = [&](uint64_t* bars, int slots, int n) {      // the slot's use n - slots is complete
-    wait_or_give_up(sh, smem_addr(&bars[n % slots]), ((uint32_t)(n / slots) & 1u) ^ 1u);
+    wait_or_give_up(sh.dead, smem_addr(&bars[n % slots]), ((uint32_t)(n / slots) & 1u) ^ 1u);
   };
   if (warp >= kScoreWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    const uint32_t one = lane == 0 ? 1u : 0u;
     if (warp == kScoreWarp) {
       // ---- scores ---------------------------------------------------------------
       Segments& seg = segs[1];
@@ -704,7 +465,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int k = 0;                                  // tiles so far
       for (uint32_t g = 0; seg.more; ++g) {
         const int n = seg.t1 - seg.t0;
-        wait_or_give_up(sh, smem_addr(&sh.q_full), g & 1u);
+        wait_or_give_up(sh.dead, smem_addr(&sh.q_full), g & 1u);
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++k) {
           const int w = j & 1;
@@ -713,29 +474,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           wait_use(sh.k_full, L::KS, k);
           fence_async_proxy();   // rows that came by 16-byte copies
           tc_fence_after();
-          const uint32_t kt = ops + L::K + (k % L::KS) * L::KB;
-          if constexpr (FP8) {
-            const uint64_t kd = operand<D>(kt, 16);
-#pragma unroll 1
-            for (int part = 0; part < L::PARTS; ++part) {
-              const uint64_t qd = operand<D>(ops + L::Q + part * kR * D, 16);
+          if (tc_elect()) {
+            const uint32_t kt = ops + L::K + (k % L::KS) * L::KB;
+            if constexpr (FP8) {
+              const uint64_t kd = operand<D>(kt, 16);
 #pragma unroll
-              for (int s = 0; s < D / 32; ++s)
-                tc_mma_e4m3(tmu + w * 128, qd + s * 2, kd + s * 2, product_e4m3(kTK), part + s > 0, one);
-            }
-          } else {
-            const uint64_t qd = operand(ops + L::Q, 16), kd = operand(kt, 16);
+              for (int part = 0; part < L::PARTS; ++part) {
+                const uint64_t qd = operand<D>(ops + L::Q + part * kR * D, 16);
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-              const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
-              tc_mma_ss(tmu + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0, one);
+                for (int s = 0; s < D / 32; ++s)
+                  tc_mma_e4m3(tmu + w * 128, qd + s * 2, kd + s * 2, product_e4m3(kTK), part + s > 0);
+              }
+            } else {
+              const uint64_t qd = operand(ops + L::Q, 16), kd = operand(kt, 16);
+#pragma unroll
+              for (int s = 0; s < D / 16; ++s) {
+                const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
+                tc_mma_ss(tmu + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0);
+              }
             }
+            tc_commit(smem_addr(&sh.s_full[w]));
+            tc_commit(smem_addr(&sh.k_empty[k % L::KS]));
           }
-          tc_commit(smem_addr(&sh.s_full[w]), one);
-          tc_commit(smem_addr(&sh.k_empty[k % L::KS]), one);
+          __syncwarp();
         }
         __syncwarp();
-        if (lane == 0) next_segment(&seg, plan);
+        if (lane == 0) next_segment<kR>(&seg, plan);
         __syncwarp();
       }
     } else if (warp == kValueWarp) {
@@ -750,21 +514,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int j = 0; j < n; ++j, ++v) {
           const int w = j & 1;
           wait_use(sh.v_full, L::VS, v);
-          wait_or_give_up(sh, smem_addr(&sh.p_full[w]), (w ? used[1] : used[0]) & 1u);
+          wait_or_give_up(sh.dead, smem_addr(&sh.p_full[w]), (w ? used[1] : used[0]) & 1u);
           if (w) ++used[1]; else ++used[0];
           tc_fence_after();
-          const uint64_t vd = operand(ops + L::V + (v % L::VS) * L::VB, kTK * 128);
-#pragma unroll 2
-          for (int s = 0; s < kTK / 16; ++s)
-            tc_mma_ts(tmu + 256 + w * 128, tmu + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
-                      s > 0 || j >= 2, one);
-          tc_commit(smem_addr(&sh.v_empty[v % L::VS]), one);
+          if (tc_elect()) {
+            const uint64_t vd = operand(ops + L::V + (v % L::VS) * L::VB, kTK * 128);
+#pragma unroll
+            for (int s = 0; s < kTK / 16; ++s)
+              tc_mma_ts(tmu + 256 + w * 128, tmu + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
+                        s > 0 || j >= 2);
+            tc_commit(smem_addr(&sh.v_empty[v % L::VS]));
+            if (j + 1 == n) tc_commit(smem_addr(&sh.o_full));
+          }
+          __syncwarp();
         }
-        tc_commit(smem_addr(&sh.o_full), one);
-        __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_addr(&sh.o_full));
-          next_segment(&seg, plan);
+          next_segment<kR>(&seg, plan);
         }
         __syncwarp();
       }
@@ -791,7 +557,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         while (seg.more && t >= seg.t1) {
           const int over = t - seg.t1;
           __syncwarp();
-          if (lane == 0) next_segment(&seg, plan);
+          if (lane == 0) next_segment<kR>(&seg, plan);
           __syncwarp();
           t = seg.t0 + over;
         }
@@ -1061,7 +827,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) mbar_arrive(smem_addr(&sh.raw_empty[n % L::RS]));
       if (++t == seg.t1) {
         named_bar_sync(2, kFinishWarps * 32);
-        if (warp == 2 * kGroupWarps && lane == 0) next_segment(&seg, plan);
+        if (warp == 2 * kGroupWarps && lane == 0) next_segment<kR>(&seg, plan);
         named_bar_sync(2, kFinishWarps * 32);
         t = seg.t0;
       }
@@ -1148,7 +914,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int j = w; j < n; j += 2) {
         const int t = t0 + j, f = (tile0 + j) % kFactSlots;
         wait_use(sh.fact, kFactSlots, tile0 + j);
-        wait_or_give_up(sh, smem_addr(&sh.s_full[w]), (uint32_t)done & 1u);
+        wait_or_give_up(sh.dead, smem_addr(&sh.s_full[w]), (uint32_t)done & 1u);
         ++done;
         tc_fence_after();
         if (busy) {
@@ -1177,7 +943,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[w]));
       }
       // ---- the segment's end: both groups' results joined, half of the head each
-      wait_or_give_up(sh, smem_addr(&sh.o_full), g & 1u);
+      wait_or_give_up(sh.dead, smem_addr(&sh.o_full), g & 1u);
       tc_fence_after();
       if (lost) bad |= SPECDEC_DEVERR_BAD_TREE;
       stats[w * kR + row] = make_float2(m, lost ? kLostRow : l);
@@ -1238,7 +1004,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       tc_fence_before();
       named_bar_sync(1, kSoftmaxThreads);   // the sums are read before queries lie over them
-      if (sid == 0) next_segment(&seg, plan);
+      if (sid == 0) next_segment<kR>(&seg, plan);
       named_bar_sync(1, kSoftmaxThreads);
       tile0 += n;
       ++g;
@@ -1256,31 +1022,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   if (warp == kScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(512));
-}
-
-// The array of cache rows as TMA sees it: [rows, D] with boxes of `box` rows and
-// 128 (8-bit: D) bytes, swizzled.  Encoded for every call: nothing is kept by an
-// address.
-bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int D, int box, bool fp8) {
-  using Encode = decltype(&cuTensorMapEncodeTiled);
-  static const Encode encode = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult got;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &got) != cudaSuccess ||
-        got != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      f = nullptr;
-    }
-    return reinterpret_cast<Encode>(f);
-  }();
-  if (!encode) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(D * (fp8 ? 1 : 2))};
-  const cuuint32_t boxes[2] = {(cuuint32_t)(fp8 ? D : 64), (cuuint32_t)box}, steps[2] = {1, 1};
-  return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base),
-                dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                fp8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool CROSS, typename T, bool FP8, int D>

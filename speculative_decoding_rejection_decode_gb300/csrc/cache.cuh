@@ -128,7 +128,7 @@ int launch_rotate(const RotateArgs& a, int dtype, int num_sms, cudaStream_t st);
 int launch_read(const ReadArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
 int launch_commit(const CommitArgs& a, int cache_dtype, cudaStream_t st);
 int launch_attend(const AttendArgs& a, int cache_dtype, int dtype, int num_sms, cudaStream_t st);
-int64_t attend_workspace_bytes(bool cross, int B, int64_t N, int kv_heads, int q_heads, int head_dim, int64_t capacity, int num_sms);
+int64_t attend_workspace_bytes(bool cross, int cache_dtype, int page_size, int B, int64_t N, int kv_heads, int q_heads, int head_dim, int64_t capacity, int num_sms);
 int launch_given(const GivenArgs& a, int num_sms, cudaStream_t st);
 
 }  // namespace specdec

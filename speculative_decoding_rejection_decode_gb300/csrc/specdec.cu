@@ -815,7 +815,7 @@ static int64_t attention_workspace(bool cross, specdec_handle_t h, const specdec
   if (!h || !cache || max_pages <= 0 || cache->page_size <= 0 || B <= 0 || B > kMaxRequests || N < 0 || (cache->head_dim != 64 && cache->head_dim != 128) ||
       cache->num_kv_heads <= 0 || q_heads <= 0 || q_heads > kMaxHeads || q_heads % cache->num_kv_heads != 0)
     return SPECDEC_ERR_INVALID_ARG;
-  return attend_workspace_bytes(cross, B, N, cache->num_kv_heads, q_heads, cache->head_dim,
+  return attend_workspace_bytes(cross, cache->dtype, cache->page_size, B, N, cache->num_kv_heads, q_heads, cache->head_dim,
                                 (int64_t)max_pages * cache->page_size, h->num_sms);
 }
 
@@ -848,7 +848,7 @@ static int attention(bool cross, specdec_handle_t h, const specdec_cache_t* cach
     return SPECDEC_ERR_INVALID_ARG;
   if (!h) return SPECDEC_ERR_INVALID_ARG;
   const int64_t need =
-      attend_workspace_bytes(cross, nodes->B, nodes->N, cache->num_kv_heads, q_heads, cache->head_dim,
+      attend_workspace_bytes(cross, cache->dtype, cache->page_size, nodes->B, nodes->N, cache->num_kv_heads, q_heads, cache->head_dim,
                              (int64_t)nodes->max_pages * cache->page_size, h->num_sms);
   if (need > 0 && (!workspace || !aligned16(workspace))) return SPECDEC_ERR_INVALID_ARG;
   if (workspace_bytes < need) return SPECDEC_ERR_CAPACITY;

@@ -191,19 +191,24 @@ def test_bad_pages_and_lengths(V, rows):
     s.mask[1, 32:64] = False
     want, big = reference(s)
     assert ((got.double() - want).abs() <= attend_tolerance(s, want, big)).all()
-    # lengths outside the table, a malformed cu: nothing of those requests is written
+    # lengths outside the table, a malformed cu: nothing of those requests is written.  The
+    # others' keys may be split in other places then, whose partial sums are added in
+    # another order in 32 bits (2^-13 of attend_tolerance): the formula is the measure
+    s.mask = None
+    want, big = reference(s)
+    near = lambda x, at: ((x[at].double() - want[at]).abs() <= attend_tolerance(s, want, big)[at]).all()
     out = torch.full_like(good, 7.0)
     lengths = s.lengths.clone()
     lengths[0], lengths[2] = -1, s.table.shape[1] * 32 + 1
     c.cross_attend(s.q, s.table, lengths, s.cu, out=out)
     assert V.get_error() == BAD_CACHE
-    assert (out[:rows] == 7).all() and (out[2 * rows:] == 7).all() and torch.equal(out[rows:2 * rows], good[rows:2 * rows])
+    assert (out[:rows] == 7).all() and (out[2 * rows:] == 7).all() and near(out, slice(rows, 2 * rows))
     cu = s.cu.clone()
     cu[3] = s.N + 1
     out.fill_(7.0)
     c.cross_attend(s.q, s.table, s.lengths, cu, out=out)
     assert V.get_error() == BAD_CU
-    assert torch.equal(out[:2 * rows], good[:2 * rows]) and (out[2 * rows:] == 7).all()
+    assert near(out, slice(0, 2 * rows)) and (out[2 * rows:] == 7).all()
 
 
 @pytest.mark.parametrize("nodes", [3, 300])
