@@ -176,12 +176,18 @@ __device__ __forceinline__ void tile_weights(uint32_t ts, uint32_t to, uint4 liv
 }
 
 // A box of whole nodes' heads from (x, head, node) of the queries; completes on `bar`.
-__device__ __forceinline__ void box3_load(uint32_t dst, const CUtensorMap* map, int x, int head, int node, uint32_t bar, uint32_t one) {
+__device__ __forceinline__ void box3_load(uint32_t dst, const CUtensorMap* map, int x, int head, int node, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %6, 0;\n\t"
-      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(head), "r"(node), "r"(one)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(head), "r"(node)
       : "memory");
+}
+
+// 32 bytes in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 template <typename T, int D>
@@ -342,87 +348,82 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
   } else if (warp == kLoad) {
     // ---- loader -----------------------------------------------------------------
-    // Lane i looks after box i of a tile (keys i box, ...), which lies in one page: it is
-    // fetched if its first key lives, and what it brings of slots behind the last key, or
-    // of masked ones, is hidden (keys) or taken out (values).
+    // A box lies in one page: it is fetched if its first key lives, and what it brings of
+    // slots behind the last key, or of masked ones, is hidden (keys) or taken out (values).
+    // A lane looks up one box; 32 of them serve `batch` tiles.  (One tile's look-ups at a
+    // time, and its boxes one after the other from one lane, took longer than the products:
+    // 4700 clocks a unit.)
     Segments& seg = segs[1];
-    const uint32_t one = lane == 0 ? 1u : 0u, page_size = (uint32_t)c.geo.page_size;
-    const int boxes = kTK / box;
-    int t = seg.t0, id = -2;
-    uint32_t see = 0;
-    auto look = [&] {                            // page of this lane's box, mask of keys 32 i + lane
-      const uint32_t first = (uint32_t)t * kTK, at = first + lane * box, len = (uint32_t)seg.q.len;
-      id = -2;
-      if (lane < boxes && at < len) id = __ldg(c.table + seg.b * c.geo.table_stride + at / page_size);
-      see = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t s = first + i * 32 + lane;
-        if (s < len && (!a.mask || (s < a.mask_slots && __ldg(a.mask + seg.b * a.mask_stride + s)))) see |= 1u << i;
-      }
-    };
-    if (seg.more) look();
+    constexpr int HALVES = D / 64;               // boxes of 64 values of a row
+    const uint32_t page_size = (uint32_t)c.geo.page_size;
+    const int shift = __ffs(box) - 1, boxes = kTK >> shift, batch = 32 / boxes;
     uint32_t begun = 0;                          // segments so far
-    for (int n = 0; seg.more; ++n) {
-      // queries that come by boxes of whole nodes (the group divides 128), read behind the last row too
-      int64_t qnode = -1;
-      int qtiles = 0, qhead = 0;
-      if (qbox && t == seg.t0) {
-        qnode = seg.q.first + (int64_t)seg.rt * (kWideR / group);
-        qtiles = seg.rows > kR ? 2 : 1;
-        qhead = seg.h * group;
-      }
-      int row = -1;                              // cache row of the box's first key
-      if (id >= 0 && id < c.geo.num_pages)
-        row = (id * c.geo.kv_heads + seg.h) * (int)page_size + (int)(((uint32_t)t * kTK + lane * box) % page_size);
-      else if (id != -2)
-        bad |= SPECDEC_DEVERR_BAD_CACHE;
-      const unsigned held = __ballot_sync(0xFFFFFFFFu, row >= 0);   // boxes that are fetched
-      const int f = n % kFacts;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool in = ((see >> i) & 1u) && ((held >> ((i * 32 + lane) / box)) & 1u);
-        const uint32_t live = __ballot_sync(0xFFFFFFFFu, in);
+    int n = 0;                                   // tiles so far
+    while (seg.more) {
+      const int t0 = seg.t0, t1 = seg.t1, h = seg.h;
+      const uint32_t len = (uint32_t)seg.q.len;
+      const int32_t* pages = c.table + seg.b * c.geo.table_stride;
+      const uint8_t* mask = a.mask ? a.mask + seg.b * a.mask_stride : nullptr;
+      int row = -1;                              // cache row of the first key of this lane's box
+      for (int t = t0, p = batch; t < t1; ++t, ++n) {
+        if (p == batch) {
+          p = 0;
+          const uint32_t key = (uint32_t)t * kTK + ((uint32_t)lane << shift), page = key / page_size;
+          row = -1;
+          if (key < len && t + lane / boxes < t1) {
+            const int id = __ldg(pages + page);
+            if (id >= 0 && id < c.geo.num_pages) row = (id * c.geo.kv_heads + h) * (int)page_size + (int)(key - page * page_size);
+            else bad |= SPECDEC_DEVERR_BAD_CACHE;
+          }
+        }
+        const unsigned every = boxes == 32 ? 0xFFFFFFFFu : (1u << boxes) - 1u;
+        const unsigned held = (__ballot_sync(0xFFFFFFFFu, row >= 0) >> (p * boxes)) & every;   // of this tile
+        const uint32_t first = (uint32_t)t * kTK;
+        const int f = n % kFacts;
         // (slot n % 8 is free: the waits for tile n - 5's slots below have passed)
-        if (lane == 0) sh.live[f][i] = live;
+        if (held == every && first + kTK <= len && !mask) {
+          if (lane < 4) sh.live[f][lane] = 0xFFFFFFFFu;
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t in = i * 32 + lane, s = first + in;
+            const bool see = s < len && ((held >> (in >> shift)) & 1u) && (!mask || (s < a.mask_slots && __ldg(mask + s)));
+            const uint32_t live = __ballot_sync(0xFFFFFFFFu, see);
+            if (lane == 0) sh.live[f][i] = live;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
+        const int mine = __shfl_sync(0xFFFFFFFFu, row, (p * boxes + lane / HALVES) & 31);
+        const bool fetches = lane < boxes * HALVES && mine >= 0;
+        const uint32_t to = (uint32_t)(lane % HALVES) * (kTK * 128) + ((uint32_t)(lane / HALVES) << shift) * 128;
+        auto fetch = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar) {
+          if (lane == 0) mbar_arrive_expect_tx(bar, (__popc(held) << shift) * D * 2);
+          __syncwarp();
+          if (fetches) box_load(dst + to, map, lane % HALVES * 64, mine, bar, 1u);
+        };
+        wait_free(sh.k_empty, L::KS, n);
+        fetch(base_s + L::K + (n % L::KS) * L::TB, &kmap, smem_addr(&sh.k_full[n % L::KS]));
+        // queries that come by boxes of whole nodes (the group divides 128), read behind the last row too
+        if (qbox && t == t0) {
+          if (begun) wait_or_give_up(sh.dead, smem_addr(&sh.q_empty), (begun - 1) & 1u);
+          ++begun;
+          const int tiles = seg.rows > kR ? 2 : 1, node = (int)(seg.q.first + (int64_t)seg.rt * (kWideR / group));
+          if (lane < tiles) mbar_arrive_expect_tx(smem_addr(&sh.q_full[lane]), L::TB);
+          __syncwarp();
+          if (lane < tiles * HALVES) {
+            const int w = lane / HALVES, half = lane % HALVES;
+            box3_load(base_s + L::Q + w * L::TB + half * (kR * 128), &qmap, half * 64, h * group, node + w * (kR / group),
+                      smem_addr(&sh.q_full[w]));
+          }
+        }
+        wait_free(sh.v_empty, L::VS, n);
+        fetch(base_s + L::V + (n % L::VS) * L::TB, &vmap, smem_addr(&sh.v_raw[n % L::VS]));
+        ++p;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.fact[f]));
-      // the next tile's look-ups are on their way while this one's slots come free
-      if (++t == seg.t1) {
-        __syncwarp();
-        if (lane == 0) next_segment<kWideR>(&seg, plan);
-        __syncwarp();
-        t = seg.t0;
-      }
-      if (seg.more) look();
-      auto fetch = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar) {
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(held) * box * D * 2);
-        __syncwarp();
-#pragma unroll 1
-        for (int i = 0; i < boxes; ++i) {
-          const int r = __shfl_sync(0xFFFFFFFFu, row, i);
-          if (r < 0) continue;
-#pragma unroll
-          for (int half = 0; half < D / 64; ++half)
-            box_load(dst + half * (kTK * 128) + i * box * 128, map, half * 64, r, bar, one);
-        }
-      };
-      wait_free(sh.k_empty, L::KS, n);
-      fetch(base_s + L::K + (n % L::KS) * L::TB, &kmap, smem_addr(&sh.k_full[n % L::KS]));
-      if (qnode >= 0) {
-        if (begun) wait_or_give_up(sh.dead, smem_addr(&sh.q_empty), (begun - 1) & 1u);
-        ++begun;
-        for (int w = 0; w < qtiles; ++w) {
-          const uint32_t bar = smem_addr(&sh.q_full[w]);
-          if (lane == 0) mbar_arrive_expect_tx(bar, L::TB);
-          __syncwarp();
-          for (int half = 0; half < D / 64; ++half)
-            box3_load(base_s + L::Q + w * L::TB + half * (kR * 128), &qmap, half * 64, qhead, (int)(qnode + w * (kR / group)), bar, one);
-        }
-      }
-      wait_free(sh.v_empty, L::VS, n);
-      fetch(base_s + L::V + (n % L::VS) * L::TB, &vmap, smem_addr(&sh.v_raw[n % L::VS]));
+      if (lane == 0) next_segment<kWideR>(&seg, plan);
+      __syncwarp();
     }
   } else if (warp == kFinish) {
     // ---- finisher -------------------------------------------------------------------
@@ -532,6 +533,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const bool live = of < seg.rows;
         const float inv = seg.whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (seg.t0 > 0 ? 0 : 1);
+        const bool aligned = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         const int64_t at = (seg.q.first + gr / group) * a.q_heads + seg.h * group + gr % group;
 #pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
@@ -541,7 +543,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (!live) continue;
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = m == -INFINITY ? 0.0f : x[k] * inv;
-          if (seg.whole) {
+          // (a row's own lines: 32 bytes a store, half as many stores as of 16)
+          if (seg.whole && aligned) {
+            T* out = static_cast<T*>(a.out) + at * D + i * 32;
+            uint32_t y[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) y[k] = pack2(x[2 * k], x[2 * k + 1], T());
+            store32(out, y);
+            store32(out + 16, y + 8);
+          } else if (seg.whole) {
             T* out = static_cast<T*>(a.out) + at * D + i * 32;
 #pragma unroll
             for (int k = 0; k < 32; k += 8)
