@@ -603,12 +603,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       auto fetch_grouped = [&](uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
         const unsigned firsts = __ballot_sync(0xFFFFFFFFu, lane < 4 && (lane * 32) % box == 0 && row >= 0);
         if (one) mbar_expect_tx(bar, __popc(firsts) * box * HALVES * LINE);
-        __syncwarp();
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const int r = __shfl_sync(0xFFFFFFFFu, row, i);
-          if ((firsts >> i) & 1u) load_box(dst, map, i * 32, r, bar);
-        }
+        // a lane for each box
+        const int i = lane / HALVES, half = lane % HALVES, r = __shfl_sync(0xFFFFFFFFu, row, i);
+        if (i < 4 && ((firsts >> i) & 1u)) box_load(dst + half * (kTK * 128) + i * 32 * LINE, map, half * 64, r, bar, 1u);
         mbar_arrive(bar);
       };
       auto fetch_any = [&](uint32_t dst, const void* src, const CUtensorMap* map, const int* row, uint32_t bar) {

@@ -44,7 +44,7 @@ struct alignas(16) WideShared {   // live is read 16 bytes at a time
   uint64_t k_full[4], k_empty[4];
   uint64_t v_raw[4], v_full[4], v_empty[4];   // landed; what no row may see taken out; read
   uint64_t fact[kFacts];
-  uint64_t s_full[2], p_most[2], p_rest[2];   // scores; weights of the first 96 keys, of all
+  uint64_t s_full[2], p_full[2];              // scores; weights
   uint64_t q_full[2], q_empty, o_full[2];
   alignas(16) uint32_t live[kFacts][4];       // keys of a tile that rows see
   uint32_t tmem;
@@ -101,10 +101,10 @@ __device__ __noinline__ void rescale(uint32_t ts, uint32_t to, int parts, bool s
 // product with V (half a step each at most) and summed unrounded, 32 at a time; the
 // maximum of the next 32 is found beside the exponentials of these.  The reference m, a
 // whole number, follows the maximum only where that has passed it by kLazy: what has been
-// summed is then multiplied by a power of two, exactly.  Nothing moves any more once the
-// maximum of the last 32 is known: the products may then take the first 96 keys' weights.
+// summed is then multiplied by a power of two, exactly.  (Handing on the first 96 keys'
+// weights before the last 32 gained nothing.)
 template <typename T, int D, bool MASKED>
-__device__ __forceinline__ void tile_weights(uint32_t ts, uint32_t to, uint4 live, float rowf, bool summed, uint64_t* p_most,
+__device__ __forceinline__ void tile_weights(uint32_t ts, uint32_t to, uint4 live, float rowf, bool summed,
                                              float& m, float& l, uint64_t* sum) {
   constexpr float kLazy = 8.0f;
   constexpr float kHead = std::is_same<T, __half>::value ? 6.0f : 0.0f;   // f16 weights keep their bits
@@ -166,12 +166,6 @@ __device__ __forceinline__ void tile_weights(uint32_t ts, uint32_t to, uint4 liv
     if (i < 2) tc_fetch32(ts + (i + 2) * 32, x);
     tc_st16(ts + i * 16, p);
     if (i < 3) refer(mx, i + 1);
-    if (i == 2) {
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(p_most));
-    }
   }
 }
 
@@ -234,8 +228,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int i = 0; i < kFacts; ++i) mbar_init(smem_addr(&sh.fact[i]), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_addr(&sh.s_full[w]), 1);
-      mbar_init(smem_addr(&sh.p_most[w]), 4);
-      mbar_init(smem_addr(&sh.p_rest[w]), 4);
+      mbar_init(smem_addr(&sh.p_full[w]), 4);
       mbar_init(smem_addr(&sh.q_full[w]), qbox ? 1 : 4);
       mbar_init(smem_addr(&sh.o_full[w]), 1);
     }
@@ -314,20 +307,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const uint32_t phase = (used >> w) & 1u;
           used ^= 1u << w;
           const uint64_t vd = operand(base_s + L::V + vs * L::TB, kTK * 128);
-          wait_or_give_up(sh.dead, smem_addr(&sh.p_most[w]), phase);
+          wait_or_give_up(sh.dead, smem_addr(&sh.p_full[w]), phase);
           tc_fence_after();
           if (tc_elect()) {
 #pragma unroll
-            for (int s = 0; s < 6; ++s)
+            for (int s = 0; s < 8; ++s)
               tc_mma_ts(tm + 256 + w * 128, tm + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<T>(D, true), s > 0 || j > 0);
-          }
-          __syncwarp();
-          wait_or_give_up(sh.dead, smem_addr(&sh.p_rest[w]), phase);
-          tc_fence_after();
-          if (tc_elect()) {
-#pragma unroll
-            for (int s = 6; s < 8; ++s)
-              tc_mma_ts(tm + 256 + w * 128, tm + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<T>(D, true), 1);
             if (j + 1 < n) scores(w, ks);
             else tc_commit(smem_addr(&sh.o_full[w]));
             if (w + 1 == tiles) {
@@ -509,12 +494,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           tc_fence_after();
           const uint4 live = *reinterpret_cast<const uint4*>(sh.live[f]);
           uint64_t sum[2] = {0, 0};
-          if ((live.x & live.y & live.z & live.w) == 0xFFFFFFFFu) tile_weights<T, D, false>(ts, to, live, rowf, j > 0, &sh.p_most[w], m, l, sum);
-          else tile_weights<T, D, true>(ts, to, live, rowf, j > 0, &sh.p_most[w], m, l, sum);
+          if ((live.x & live.y & live.z & live.w) == 0xFFFFFFFFu) tile_weights<T, D, false>(ts, to, live, rowf, j > 0, m, l, sum);
+          else tile_weights<T, D, true>(ts, to, live, rowf, j > 0, m, l, sum);
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&sh.p_rest[w]));
+          if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[w]));
           float s0, s1;
           unpair(add2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
