@@ -348,12 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
         // scale in the exponent: the weights that meet V are
         // 2^(u + log2 vs - m), whose largest 16 bits hold whatever the scales are
         const int64_t key0 = (int64_t)t * TK + warp * KB;
-        const bool masked = live != (KB == 32 ? 0xFFFFFFFFu : (1u << (KB & 31)) - 1u) || key0 + KB > q.len;
+        const bool masked = live != (KB == 32 ? 0xFFFFFFFFu : (1u << (KB & 31)) - 1u) || (!CROSS && key0 + KB > q.len);
         float iv[FP8 ? KB / 8 : 1][2];   // 1 / vs
         float mx[2];
         mx[0] = mx[1] = -INFINITY;
         auto sees = [&](int r, int key) -> bool {
           if (!((live >> key) & 1u)) return false;
+          if constexpr (CROSS) return true;
           const int64_t j = key0 + key - q.len;
           if (j < 0) return true;
           if (r >= rows) return false;
@@ -428,8 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
         // A value that is not finite belongs to the rows that see its key and
         // to no other (0 x inf would reach them through the product): it is
         // added to those and taken out of the block.  Only blocks that some
-        // row does not see in full need the look.
-        if (masked) {
+        // row does not see in full need the look (an encoder's states that live are
+        // seen by every row).
+        if (!CROSS && masked) {
           char* vb = kv + KB * W::ROW;
           uint32_t any = 0;
           for (int x = lane; x < KB * CH; x += 32) any |= nonfinite<T, FP8>(*reinterpret_cast<uint4*>(vb + x * 16));
