@@ -13,10 +13,8 @@
 //                        widened to f16 (the keys are multiplied as they are, see
 //                        below); in tiles that hold nodes or miss keys, what no row
 //                        may see is taken out;
-//   products (2 warps)   S_w = Q K^T (both operands in shared memory) from one, O_w +=
-//                        P_w V (P in tensor memory) from the other: a warp stands
-//                        still while its products are taken up, and one warp's waits
-//                        for both left the tensor cores idle;
+//   products (1 warp)    S_w = Q K^T (both operands in shared memory), O_w += P_w V (P in
+//                        tensor memory);
 //   softmax (2 groups    group w takes every second tile of a segment with a
 //   of 4 warps)          maximum, sum and O_w of its own, one row per thread, so
 //                        that one group's exponentials overlap the other's
@@ -55,9 +53,9 @@ namespace {
 constexpr int kGroupWarps = 4;                       // softmax warps of a group
 constexpr int kSoftmaxThreads = 2 * kGroupWarps * 32;
 constexpr int kFinishWarps = 4;
-constexpr int kScoreWarp = 2 * kGroupWarps + kFinishWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kScoreWarp + 2;
+constexpr int kProductWarp = 2 * kGroupWarps + kFinishWarps, kLoadWarp = kProductWarp + 2;   // (one between is idle)
 constexpr int kLoaders = 2;                          // loader l takes tiles l, l + 2, ... of the range
-constexpr int kTileThreads = (kScoreWarp + 4) * 32;    // a whole warpgroup: registers move between those
+constexpr int kTileThreads = (kProductWarp + 4) * 32;    // a whole warpgroup: registers move between those
 constexpr int kW = 32;                               // scores of a row that a thread holds at once (64 took 4 % longer)
 constexpr float kLeastScale = 8.673617379884035e-19f;   // 2^-60: smaller scales of values count as this
 constexpr int kFactSlots = 8;                        // tiles whose key facts are held (5 are needed)
@@ -426,7 +424,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     sh.dead = 0;
     fence_mbar_init();
   }
-  if (warp == kScoreWarp) {
+  if (warp == kProductWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "n"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
@@ -456,74 +454,70 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto wait_free = [&](uint64_t* bars, int slots, int n) {      // the slot's use n - slots is complete
     wait_or_give_up(sh.dead, smem_addr(&bars[n % slots]), ((uint32_t)(n / slots) & 1u) ^ 1u);
   };
-  if (warp >= kScoreWarp) {
+  if (warp >= kProductWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == kScoreWarp) {
-      // ---- scores ---------------------------------------------------------------
+    if (warp == kProductWarp) {
+      // ---- products ---------------------------------------------------------------
+      // One warp for all of them, in the order ... P_w V of a tile, S_w of the tile after next
+      // ...: the tensor cores take products up in order, so that S_w may follow P_w V at once
+      // although it lies over P_w (with a warp each for scores and weighted values, scores
+      // waited for the other's products to end and be seen).
       Segments& seg = segs[1];
       const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0), ops = __shfl_sync(0xFFFFFFFFu, base_s, 0);
+      auto scores = [&](int w, int n) {            // of tile n; the elected thread's
+        const uint32_t kt = ops + L::K + (n % L::KS) * L::KB;
+        if constexpr (FP8) {
+          const uint64_t kd = operand<D>(kt, 16);
+#pragma unroll
+          for (int part = 0; part < L::PARTS; ++part) {
+            const uint64_t qd = operand<D>(ops + L::Q + part * kR * D, 16);
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s)
+              tc_mma_e4m3(tmu + w * 128, qd + s * 2, kd + s * 2, product_e4m3(kTK), part + s > 0);
+          }
+        } else {
+          const uint64_t qd = operand(ops + L::Q, 16), kd = operand(kt, 16);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
+            tc_mma_ss(tmu + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0);
+          }
+        }
+        tc_commit(smem_addr(&sh.s_full[w]));
+        tc_commit(smem_addr(&sh.k_empty[n % L::KS]));
+      };
+      auto keys = [&](int n) {
+        wait_use(sh.k_full, L::KS, n);
+        fence_async_proxy();   // rows that came by 16-byte copies
+        tc_fence_after();
+      };
       int k = 0;                                  // tiles so far
+      uint32_t used = 0;                          // bit w: phase of group w's weights
       for (uint32_t g = 0; seg.more; ++g) {
         const int n = seg.t1 - seg.t0;
         wait_or_give_up(sh.dead, smem_addr(&sh.q_full), g & 1u);
 #pragma unroll 1
-        for (int j = 0; j < n; ++j, ++k) {
-          const int w = j & 1;
-          // S_w and P_w are free once the product before last has read P_w
-          if (j >= 2) wait_use(sh.v_empty, L::VS, k - 2);
-          wait_use(sh.k_full, L::KS, k);
-          fence_async_proxy();   // rows that came by 16-byte copies
-          tc_fence_after();
-          if (tc_elect()) {
-            const uint32_t kt = ops + L::K + (k % L::KS) * L::KB;
-            if constexpr (FP8) {
-              const uint64_t kd = operand<D>(kt, 16);
-#pragma unroll
-              for (int part = 0; part < L::PARTS; ++part) {
-                const uint64_t qd = operand<D>(ops + L::Q + part * kR * D, 16);
-#pragma unroll
-                for (int s = 0; s < D / 32; ++s)
-                  tc_mma_e4m3(tmu + w * 128, qd + s * 2, kd + s * 2, product_e4m3(kTK), part + s > 0);
-              }
-            } else {
-              const uint64_t qd = operand(ops + L::Q, 16), kd = operand(kt, 16);
-#pragma unroll
-              for (int s = 0; s < D / 16; ++s) {
-                const uint32_t off = (uint32_t)((s >> 2) * (kTK * 128) + (s & 3) * 32) >> 4;
-                tc_mma_ss(tmu + w * 128, qd + off, kd + off, product<E>(kTK, false), s > 0);
-              }
-            }
-            tc_commit(smem_addr(&sh.s_full[w]));
-            tc_commit(smem_addr(&sh.k_empty[k % L::KS]));
-          }
+        for (int j = 0; j < 2 && j < n; ++j) {
+          keys(k + j);
+          if (tc_elect()) scores(j, k + j);
           __syncwarp();
         }
-        __syncwarp();
-        if (lane == 0) next_segment<kR>(&seg, plan);
-        __syncwarp();
-      }
-    } else if (warp == kValueWarp) {
-      // ---- weighted values --------------------------------------------------------
-      Segments& seg = segs[2];
-      const uint32_t tmu = __shfl_sync(0xFFFFFFFFu, tm, 0), ops = __shfl_sync(0xFFFFFFFFu, base_s, 0);
-      int v = 0;
-      uint32_t used[2] = {0, 0};                  // tiles of each group so far
-      while (seg.more) {
-        const int n = seg.t1 - seg.t0;
 #pragma unroll 1
-        for (int j = 0; j < n; ++j, ++v) {
+        for (int j = 0; j < n; ++j, ++k) {
           const int w = j & 1;
-          wait_use(sh.v_full, L::VS, v);
-          wait_or_give_up(sh.dead, smem_addr(&sh.p_full[w]), (w ? used[1] : used[0]) & 1u);
-          if (w) ++used[1]; else ++used[0];
+          wait_use(sh.v_full, L::VS, k);
+          if (j + 2 < n) keys(k + 2);
+          wait_or_give_up(sh.dead, smem_addr(&sh.p_full[w]), (used >> w) & 1u);
+          used ^= 1u << w;
           tc_fence_after();
           if (tc_elect()) {
-            const uint64_t vd = operand(ops + L::V + (v % L::VS) * L::VB, kTK * 128);
+            const uint64_t vd = operand(ops + L::V + (k % L::VS) * L::VB, kTK * 128);
 #pragma unroll
             for (int s = 0; s < kTK / 16; ++s)
               tc_mma_ts(tmu + 256 + w * 128, tmu + w * 128 + s * 8, vd + (uint32_t)(s * 2048 >> 4), product<E>(D, true),
                         s > 0 || j >= 2);
-            tc_commit(smem_addr(&sh.v_empty[v % L::VS]));
+            tc_commit(smem_addr(&sh.v_empty[k % L::VS]));
+            if (j + 2 < n) scores(w, k + 2);
             if (j + 1 == n) tc_commit(smem_addr(&sh.o_full));
           }
           __syncwarp();
@@ -534,7 +528,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         __syncwarp();
       }
-    } else {
+    } else if (warp >= kLoadWarp) {
       // ---- loaders ----------------------------------------------------------------
       // Pages that are a multiple of 32 slots (`grouped`): 32 keys from a multiple of
       // 32 lie in one page, so lanes 0 .. 3 look up one page each and hold the cache
@@ -1017,7 +1011,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (tid == 0) atomicOr(c.err, SPECDEC_DEVERR_TIMEOUT);
     __syncthreads();
   }
-  if (warp == kScoreWarp)
+  if (warp == kProductWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(512));
 }
 
