@@ -200,9 +200,10 @@ template <int R, int D>
 struct Partials {
   float* sums;
   float2* stats;
-  __host__ __device__ Partials(void* ws, int G)
-      : sums(static_cast<float*>(ws)), stats(reinterpret_cast<float2*>(sums + (int64_t)2 * G * R * D)) {}
-  static constexpr int64_t bytes(int G) { return (int64_t)2 * G * R * (D * 4 + 8); }
+  __host__ __device__ Partials(void* ws, int G)   // from a multiple of 32 bytes: rows are stored 32 at a time
+      : sums(reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~(uintptr_t)31)),
+        stats(reinterpret_cast<float2*>(sums + (int64_t)2 * G * R * D)) {}
+  static constexpr int64_t bytes(int G) { return (int64_t)2 * G * R * (D * 4 + 8) + 32; }
 };
 
 // Joins the partial results of the items that several ranges share.  An item

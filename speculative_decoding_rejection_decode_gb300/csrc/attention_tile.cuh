@@ -978,8 +978,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             } else {
               float* out = part.sums + (slot * kR + row) * D + d0;
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4*>(out + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+              for (int k = 0; k < 32; k += 8) store32(out + k, reinterpret_cast<const uint32_t*>(x + k));
             }
           }
         }

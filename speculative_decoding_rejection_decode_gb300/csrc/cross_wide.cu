@@ -177,13 +177,6 @@ __device__ __forceinline__ void box3_load(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// 32 bytes in one store.
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kWideThreads, 1)
     cross_wide_kernel(const AttendArgs a, const int box, const bool qbox, const __grid_constant__ CUtensorMap kmap,
@@ -545,7 +538,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           } else {
             float* out = part.sums + (slot * kWideR + of) * D + i * 32;
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(out + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+            for (int k = 0; k < 32; k += 8) store32(out + k, reinterpret_cast<const uint32_t*>(x + k));
           }
         }
         if (live && !seg.whole) part.stats[slot * kWideR + of] = make_float2(m, l);
