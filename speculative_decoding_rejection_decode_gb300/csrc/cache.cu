@@ -2,15 +2,10 @@
 // quantisation on the way), reading rows back, and moving an accepted branch
 // into place.  Contract in include/specdec.h.
 //
-// A thread moves 8 values (16 bytes of a 16-bit row) and a row of head_dim values is
-// held by head_dim / 8 neighbouring lanes, so that a row's absolute maximum is
-// a few shuffles and nothing passes through shared memory.  Bounds: the read-back by
-// memory traffic (64 contexts of up to 8191 e4m3 rows of 8 heads of 128: 1.70 GB in
-// 258 us, 6.6 TB/s); the append by no single unit (65 % of the issue slots, 62 % of the
-// copy rate: a block's rows follow one another, each waiting for its own loads, after
-// the look-ups before the first; 15k tree nodes of 48 heads, with their read-back: 435
-// MB in 95 us); the commit, and every call for one request,
-// by latency (29 nodes of 48 heads written: 4.5 us).
+// Bounds: the read-back and the append by memory traffic (64 contexts of up to 8191 e4m3
+// rows of 8 heads of 128 read: 1.70 GB in 258 us, 6.6 TB/s; 40619 rows of 48 heads turned
+// and quantised: 918 MB in 160 us, 5.7 TB/s); the commit, and every call for one request, by
+// latency (29 nodes of 48 heads written: 5 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -25,6 +20,7 @@ namespace specdec {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kAppendBlocks = 5;   // of an append on an SM
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float r;
@@ -32,62 +28,35 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   return r;
 }
 
-// Absolute maximum of a row held by LANES neighbouring lanes.
-template <int LANES>
-__device__ __forceinline__ float row_amax(const Vec8& v) {
-  float m = 0.0f;
+// 16 values / scale rounded to e4m3 (to nearest, ties to even), 8 bytes for each half.  The
+// quotients are those of an IEEE division, so that the stored byte and scale are a function
+// of the row alone, whatever computes them: q + (x - q scale) r is the quotient rounded to
+// nearest where r is the reciprocal so rounded and q = x r (Markstein, 1990; that the bytes
+// are a division's has been counted over every scale's mantissa beside every border between
+// two bytes).  Taken as q - (q scale - x) r, a zero keeps its sign.  |x / scale| passes 448
+// by rounding at most, which rounds back to 448.
+__device__ __forceinline__ void quantise(float* x, float scale, uint2* to) {
+  uint32_t w[8];
+  float d = scale;
+  if (!(scale < 1e30f)) {                    // out of the reciprocal's range: both by 2^-40
+    d = scale == INFINITY ? 0.0f : scale * 9.094947017729282e-13f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(v.x[i]));
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  return m;
-}
-
-// x / scale rounded to e4m3 (to nearest, ties to even).  An IEEE division: the
-// stored byte and scale are a function of the row alone, whatever computes
-// them.  |x / scale| passes 448 by rounding at most, which rounds back to 448.
-__device__ __forceinline__ uint2 quantise(const Vec8& v, float scale) {
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = make_float2(__fdiv_rn(v.x[2 * i], scale), __fdiv_rn(v.x[2 * i + 1], scale));
-    const uint32_t two = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-    w[i >> 1] |= two << ((i & 1) * 16);
+    for (int i = 0; i < 16; ++i) x[i] *= 9.094947017729282e-13f;
   }
-  return make_uint2(w[0], w[1]);
-}
-
-// Writes one lane's 8 values of a cache row.  All lanes of the warp call.
-template <typename T, bool FP8, int D>
-__device__ __forceinline__ void store_row(void* base, float* scales, int64_t row, int chunk,
-                                          const Vec8& v, bool live) {
-  if constexpr (FP8) {
-    const float m = row_amax<D / 8>(v);
-    const float scale = __fmul_rn(max_nan(m, kScaleFloor), 1.0f / kE4M3Max);
-    const uint2 w = quantise(v, scale);
-    if (live) {
-      reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + row * D)[chunk] = w;
-      if (chunk == 0) scales[row] = scale;
-    }
-  } else {
-    if (live) reinterpret_cast<uint4*>(static_cast<T*>(base) + row * D)[chunk] = narrow<T>(v);
+  const float r = scale == INFINITY ? 0.0f : __frcp_rn(d);   // finite / inf is 0, inf / inf NaN
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float2 f = make_float2(__fmul_rn(x[2 * i], r), __fmul_rn(x[2 * i + 1], r));
+    f.x = __fmaf_rn(-__fmaf_rn(f.x, d, -x[2 * i]), r, f.x);
+    f.y = __fmaf_rn(-__fmaf_rn(f.y, d, -x[2 * i + 1]), r, f.y);
+    w[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
   }
+  to[0] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  to[1] = make_uint2(w[4] | w[5] << 16, w[6] | w[7] << 16);
 }
 
-// 4 neighbouring cos (or sin), of the table or (SHARED) of the block's own copy, or 8.
-template <bool SHARED>
-__device__ __forceinline__ float4 load4(const float* p) {
-  if constexpr (SHARED) return *reinterpret_cast<const float4*>(p);
-  else return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <bool SHARED>
-__device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = load4<SHARED>(p), b = load4<SHARED>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
-constexpr int kRows = 16;   // rows of a block at most
+constexpr int kRows = 24;   // rows of an append's block at most (a lane finds the place of one)
+constexpr int kReadRows = 16;   // of a read's
 
 // Where the rows of a block lie: found by one thread each, all at once, before
 // any value is moved.
@@ -158,149 +127,207 @@ __device__ __forceinline__ RowPlace place_of(const CacheArgs& c, int from, int64
   return p;
 }
 
-// Threads are (head slot, chunk of 8 values); a thread keeps its cos and sin for
-// every head it turns.  Products and their sum are rounded one by one (no fused
-// multiply-add), as the formula
+// A thread has two chunks of 8 values of a row, both halves of the same pairs in the halves
+// layout, so that a turn crosses no lanes; D / 16 lanes hold a row.  cos and sin of the
+// block's rows, each pair's from the row of the table at the position on its own axis,
+// come to shared memory all at once.  Products and their sum are rounded one by one (no
+// fused multiply-add), as the formula
 //   a' = a cos - b sin, b' = b cos + a sin
 // reads in 32 bits, so that what is quantised does not depend on contraction.
-// k and v, which may be quantised, and q have loops of their own, the first with one
-// copy of its body: one loop for all heads, unrolled, was 8 % slower for one tree and
-// held 6 blocks of an SM where this form holds 7.
-// AXES: the rows bring positions on several axes, and each pair turns by its own; the
-// block then takes the cos and sin of its rows' pairs to shared memory, all at once.
-template <typename T, bool FP8, int D, bool AXES>
-__global__ void __launch_bounds__(kThreads, 7) append_kernel(const AppendArgs a, const int rows) {
-  constexpr int LANES = D / 8;                 // lanes of a row
+template <typename T, bool FP8, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, kAppendBlocks) append_kernel(const AppendArgs a, const int rows) {
+  constexpr int LANES = D / 16;                // lanes of a row
   constexpr int SLOTS = kThreads / LANES;      // heads in flight
   __shared__ RowPlace places[kRows];
-  __shared__ __align__(16) float turns[AXES ? kRows : 1][2][AXES ? D / 2 : 4];   // cos, sin of a row's pairs
-  __shared__ int64_t at_axis[AXES ? kRows : 1][kMaxAxes];                      // their positions in the table
-  const int chunk = threadIdx.x % LANES, slot0 = threadIdx.x / LANES;
+  __shared__ __align__(16) float turns[kRows][2][D / 2];   // cos, sin of a row's pairs
+  __shared__ int64_t at_axis[kRows][kMaxAxes];             // their positions in the table
+  const int l = threadIdx.x % LANES, slot0 = threadIdx.x / LANES;
   const CacheArgs& c = a.c;
   const int half = a.rotary_dim / 2;
-  const int d0 = chunk * 8;
   const int64_t r0 = (int64_t)blockIdx.x * rows;
   const int here = (int)min((int64_t)rows, c.N - r0);
   if (threadIdx.x < 32) {
     const int from = warp_request_of_row(c.cu, c.B, r0);
     if ((int)threadIdx.x < here) {
-      RowPlace p = place_of(c, from, r0 + threadIdx.x, !AXES && a.rotary != nullptr, a.rotary_dim, a.positions, a.offsets);
-      if constexpr (AXES) {
-        if (p.owned) {
-          p.turn = 0;
-          for (int i = 0; i < a.num_axes; ++i) {
-            const int64_t at = a.pos[i * a.pos_stride + r0 + threadIdx.x];
-            if (at < 0 || at >= a.positions) p.row = p.turn = -1;
-            at_axis[threadIdx.x][i] = at * a.rotary_dim;
-          }
-          if (p.turn < 0) atomicOr(c.err, SPECDEC_DEVERR_BAD_CACHE);
+      const bool given = a.pos != nullptr;
+      RowPlace p = place_of(c, from, r0 + threadIdx.x, !given && a.rotary != nullptr, a.rotary_dim, a.positions, a.offsets);
+      if (given && p.owned) {
+        p.turn = 0;
+        for (int i = 0; i < a.num_axes; ++i) {
+          const int64_t at = a.pos[i * a.pos_stride + r0 + threadIdx.x];
+          if (at < 0 || at >= a.positions) p.row = p.turn = -1;
+          at_axis[threadIdx.x][i] = at * a.rotary_dim;
         }
+        if (p.turn < 0) atomicOr(c.err, SPECDEC_DEVERR_BAD_CACHE);
+      } else {
+        at_axis[threadIdx.x][0] = p.turn;      // (axes are all 0 here)
       }
       places[threadIdx.x] = p;
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && (int64_t)c.cu[c.B] > c.N) atomicOr(c.err, SPECDEC_DEVERR_BAD_CU);
   __syncthreads();
-  if constexpr (AXES) {
-    for (int x = threadIdx.x; x < here * half; x += kThreads) {
-      const int i = x / half, j = x - i * half;
-      if (places[i].turn < 0) continue;
-      const float* from = a.rotary + at_axis[i][axis_of(a.axes, j)] + j;
-      turns[i][0][j] = __ldg(from);
-      turns[i][1][j] = __ldg(from + half);
-    }
-    __syncthreads();
-  }
+  // this thread's chunks: their first values, and where they turn the first of their pairs
+  const int pairs = INTERLEAVED ? 0 : half / 8;   // lanes that hold both halves of 8 pairs
+  const bool both = l < pairs;
+  const int da = both ? l * 8 : INTERLEAVED ? l * 8 : a.rotary_dim + (l - pairs) * 16;
+  const int db = both ? half + l * 8 : INTERLEAVED ? (l + LANES) * 8 : da + 8;
   const int kv = c.geo.kv_heads, heads = a.q ? a.q_heads : 0;
+  // A step is SLOTS heads: of k and v, one sequence of 2 kv, or of q.  The first steps' places
+  // are kept from row to row, and their loads for the next row are under way while this
+  // one's values are turned and stored.
+  struct Values {
+    uint4 a, b;
+  };
+  struct Lane {
+    const T* from;        // this row's chunk a
+    int64_t stride;
+    bool on;
+  };
+  auto kv_lane = [&](int step) -> Lane {
+    const int hh = step * SLOTS + slot0;
+    if (hh < kv) return {static_cast<const T*>(a.k) + r0 * a.k_row + hh * a.k_head + da, a.k_row, true};
+    return {static_cast<const T*>(a.v) + r0 * a.v_row + (hh - kv) * a.v_head + da, a.v_row, hh < 2 * kv};
+  };
+  auto q_lane = [&](int step) -> Lane {
+    const int h = step * SLOTS + slot0;
+    return {static_cast<const T*>(a.q) + r0 * a.q_row + h * a.q_head + da, a.q_row, h < heads};
+  };
+  const int apart = db - da;
+  auto load = [&](const Lane& x, int i) -> Values {
+    Values v = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (x.on && i < here && places[i].owned) {
+      const T* from = x.from + i * x.stride;
+      v.a = __ldg(reinterpret_cast<const uint4*>(from));
+      v.b = __ldg(reinterpret_cast<const uint4*>(from + apart));
+    }
+    return v;
+  };
+  float cs[8], sn[8];
+  bool ta = false, tb = false;                 // whether the chunks turn
+  auto turned = [&](const Values& w, bool turns_too, float* x) {
+    const Vec8 va = widen<T>(w.a), vb = widen<T>(w.b);
+    if constexpr (INTERLEAVED) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const Vec8& v = z ? vb : va;
+        const bool turn = turns_too && (z ? tb : ta);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float u = v.x[2 * k], y = v.x[2 * k + 1], cc = cs[4 * z + k], ss = sn[4 * z + k];
+          x[8 * z + 2 * k] = turn ? __fsub_rn(__fmul_rn(u, cc), __fmul_rn(y, ss)) : u;
+          x[8 * z + 2 * k + 1] = turn ? __fadd_rn(__fmul_rn(y, cc), __fmul_rn(u, ss)) : y;
+        }
+      }
+    } else if (turns_too && ta) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k] = __fsub_rn(__fmul_rn(va.x[k], cs[k]), __fmul_rn(vb.x[k], sn[k]));
+        x[8 + k] = __fadd_rn(__fmul_rn(vb.x[k], cs[k]), __fmul_rn(va.x[k], sn[k]));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k] = va.x[k];
+        x[8 + k] = vb.x[k];
+      }
+    }
+  };
+  auto store16 = [&](T* to, const float* x) {
+    *reinterpret_cast<uint4*>(to + da) = make_uint4(pack(x[0], x[1], T()), pack(x[2], x[3], T()), pack(x[4], x[5], T()), pack(x[6], x[7], T()));
+    *reinterpret_cast<uint4*>(to + db) = make_uint4(pack(x[8], x[9], T()), pack(x[10], x[11], T()), pack(x[12], x[13], T()), pack(x[14], x[15], T()));
+  };
+  auto store_kv = [&](const Values& w, int step, const RowPlace& p) {   // the whole block calls
+    const int hh = step * SLOTS + slot0;
+    const bool isv = hh >= kv;
+    float x[16];
+    turned(w, !isv, x);
+    const bool live = hh < 2 * kv && p.row >= 0;
+    const int64_t row = p.row + (int64_t)((isv ? hh - kv : hh) * c.geo.page_size);
+    if constexpr (FP8) {
+      float m = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) m = max_nan(m, fabsf(x[k]));
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      if (!live) return;
+      const float scale = __fmul_rn(max_nan(m, kScaleFloor), 1.0f / kE4M3Max);
+      uint8_t* to = static_cast<uint8_t*>(isv ? c.v : c.k) + row * D;
+      uint2 bytes[2];
+      quantise(x, scale, bytes);
+      *reinterpret_cast<uint2*>(to + da) = bytes[0];
+      *reinterpret_cast<uint2*>(to + db) = bytes[1];
+      if (l == 0) (isv ? c.vs : c.ks)[row] = scale;
+    } else if (live) {
+      store16(static_cast<T*>(isv ? c.v : c.k) + row * D, x);
+    }
+  };
+  auto store_q = [&](const Values& w, int step, int64_t r, bool lost) {
+    const int h = step * SLOTS + slot0;
+    if (h >= heads) return;
+    float x[16];
+    turned(w, true, x);
+    if (lost) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = 0.0f;
+    }
+    store16(static_cast<T*>(a.out_q) + (r * heads + h) * D, x);
+  };
+  const int kv_steps = (2 * kv + SLOTS - 1) / SLOTS, q_steps = (heads + SLOTS - 1) / SLOTS;
+  const Lane lkv = kv_lane(0), lq0 = q_lane(0), lq1 = q_lane(1);
+  Values wkv = load(lkv, 0), wq0 = load(lq0, 0), wq1 = load(lq1, 0);
+  for (int x = threadIdx.x; x < here * half; x += kThreads) {
+    const int i = x / half, j = x - i * half;
+    if (places[i].turn < 0) continue;
+    const float* from = a.rotary + at_axis[i][axis_of(a.axes, j)] + j;
+    turns[i][0][j] = __ldg(from);
+    turns[i][1][j] = __ldg(from + half);
+  }
+  __syncthreads();
   for (int i = 0; i < here; ++i) {
     const RowPlace p = places[i];
-    if (!p.owned) continue;
     const int64_t r = r0 + i;
-    const bool turned = p.turn >= 0 && d0 < a.rotary_dim, half_layout = p.turn >= 0 && !a.interleaved;
-    float cs[8], sn[8];
-    int partner = 0;
-    float sign = 1.0f;
-    if (turned) {
-      const float *cosp = AXES ? turns[AXES ? i : 0][0] : a.rotary + p.turn, *sinp = AXES ? turns[AXES ? i : 0][1] : cosp + half;
-      if (a.interleaved) {
-        const float4 x = load4<AXES>(cosp + d0 / 2);
-        const float4 y = load4<AXES>(sinp + d0 / 2);
-        cs[0] = cs[1] = x.x; cs[2] = cs[3] = x.y; cs[4] = cs[5] = x.z; cs[6] = cs[7] = x.w;
-        sn[0] = sn[1] = y.x; sn[2] = sn[3] = y.y; sn[4] = sn[5] = y.z; sn[6] = sn[7] = y.w;
-      } else {
-        const bool low = d0 < half;
-        load8<AXES>(cosp + (low ? d0 : d0 - half), cs);
-        load8<AXES>(sinp + (low ? d0 : d0 - half), sn);
-        partner = (low ? half : -half) / 8;
-        sign = low ? -1.0f : 1.0f;
-      }
-    }
-    const int other = (int)(threadIdx.x & 31 & ~(LANES - 1)) | (chunk + partner);   // lane of the pairs' other halves
-    auto turn = [&](uint4 w, bool keys) -> Vec8 {   // the whole warp calls
-      Vec8 x = widen<T>(w);
-      uint4 o = w;
-      if (half_layout) {   // the same in the whole block
-        o.x = __shfl_sync(0xFFFFFFFFu, w.x, other);
-        o.y = __shfl_sync(0xFFFFFFFFu, w.y, other);
-        o.z = __shfl_sync(0xFFFFFFFFu, w.z, other);
-        o.w = __shfl_sync(0xFFFFFFFFu, w.w, other);
-      }
-      if (!turned || !keys) return x;
-      Vec8 y;
-      if (a.interleaved) {
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          y.x[k] = __fsub_rn(__fmul_rn(x.x[k], cs[k]), __fmul_rn(x.x[k + 1], sn[k]));
-          y.x[k + 1] = __fadd_rn(__fmul_rn(x.x[k + 1], cs[k]), __fmul_rn(x.x[k], sn[k]));
+    ta = tb = false;
+    if (p.turn >= 0) {
+      const float *cosp = turns[i][0], *sinp = turns[i][1];
+      if constexpr (INTERLEAVED) {
+        ta = da < a.rotary_dim;
+        tb = db < a.rotary_dim;
+        if (ta) {
+          *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(cosp + da / 2);
+          *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(sinp + da / 2);
         }
-      } else {
-        const Vec8 z = widen<T>(o);
+        if (tb) {
+          *reinterpret_cast<float4*>(cs + 4) = *reinterpret_cast<const float4*>(cosp + db / 2);
+          *reinterpret_cast<float4*>(sn + 4) = *reinterpret_cast<const float4*>(sinp + db / 2);
+        }
+      } else if (both) {
+        ta = true;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          y.x[k] = __fadd_rn(__fmul_rn(x.x[k], cs[k]), sign * __fmul_rn(z.x[k], sn[k]));
-      }
-      return y;
-    };
-    // k and v heads two steps of SLOTS at a time, q heads four; the first of both are
-    // under way together
-    constexpr int UK = 2, UQ = 4;
-    const T* q0 = static_cast<const T*>(a.q) + r * a.q_row + d0;
-    uint4 wq[UQ];
-    auto load_q = [&](int h0) {
-#pragma unroll
-      for (int u = 0; u < UQ; ++u) {
-        const int h = h0 + u * SLOTS + slot0;
-        wq[u] = h < heads ? __ldg(reinterpret_cast<const uint4*>(q0 + h * a.q_head)) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    for (int h0 = 0; h0 < 2 * kv; h0 += UK * SLOTS) {
-      uint4 w[UK];
-#pragma unroll
-      for (int u = 0; u < UK; ++u) {
-        const int hh = h0 + u * SLOTS + slot0;
-        const T* src = hh < kv ? static_cast<const T*>(a.k) + r * a.k_row + hh * a.k_head
-                               : static_cast<const T*>(a.v) + r * a.v_row + (hh - kv) * a.v_head;
-        w[u] = hh < 2 * kv ? __ldg(reinterpret_cast<const uint4*>(src + d0)) : make_uint4(0, 0, 0, 0);
-      }
-      if (h0 == 0) load_q(0);
-#pragma unroll 1
-      for (int u = 0; u < UK; ++u) {
-        const int hh = h0 + u * SLOTS + slot0;
-        const bool isk = hh < kv;
-        const Vec8 x = turn(u ? w[1] : w[0], isk);
-        const int64_t row = p.row + (int64_t)(isk ? hh : hh - kv) * c.geo.page_size;
-        store_row<T, FP8, D>(isk ? c.k : c.v, isk ? c.ks : c.vs, row, chunk, x, hh < 2 * kv && p.row >= 0);
+        for (int k = 0; k < 8; k += 4) {
+          *reinterpret_cast<float4*>(cs + k) = *reinterpret_cast<const float4*>(cosp + da + k);
+          *reinterpret_cast<float4*>(sn + k) = *reinterpret_cast<const float4*>(sinp + da + k);
+        }
       }
     }
     const bool lost = a.rotary && p.turn < 0;   // no position: defined rows
-    T* out0 = static_cast<T*>(a.out_q) + r * heads * D + d0;
-    for (int h0 = 0; h0 < heads; h0 += UQ * SLOTS) {
-      if (h0) load_q(h0);
-#pragma unroll
-      for (int u = 0; u < UQ; ++u) {
-        const int h = h0 + u * SLOTS + slot0;
-        const Vec8 x = turn(wq[u], true);
-        if (h < heads) *reinterpret_cast<uint4*>(out0 + h * D) = lost ? make_uint4(0, 0, 0, 0) : narrow<T>(x);
+    const Values now = wkv;
+    wkv = load(lkv, i + 1);
+    if (p.owned) {
+      store_kv(now, 0, p);
+#pragma unroll 1
+      for (int s = 1; s < kv_steps; ++s) store_kv(load(kv_lane(s), i), s, p);
+    }
+    if (heads) {
+      const Values now0 = wq0;
+      wq0 = load(lq0, i + 1);
+      if (p.owned) store_q(now0, 0, r, lost);
+      const Values now1 = wq1;
+      wq1 = load(lq1, i + 1);
+      if (p.owned) {
+        store_q(now1, 1, r, lost);
+#pragma unroll 1
+        for (int s = 2; s < q_steps; ++s) store_q(load(q_lane(s), i), s, r, lost);
       }
     }
   }
@@ -312,7 +339,7 @@ template <typename T, bool FP8, int D>
 __global__ void __launch_bounds__(256) read_kernel(const ReadArgs a, const int rows) {
   constexpr int CH = FP8 ? D / 16 : D / 8;     // 16-byte chunks of a cache row
   constexpr int U = 4;
-  __shared__ RowPlace places[kRows];
+  __shared__ RowPlace places[kReadRows];
   const CacheArgs& c = a.c;
   const int64_t r0 = (int64_t)blockIdx.x * rows;
   const int here = (int)min((int64_t)rows, c.N - r0);
@@ -463,31 +490,33 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a, const i
   }
 }
 
-// Rows of a block, whose places are looked up together (a few dependent loads).
-// Both take one wave of resident blocks where N allows.  Appends of 48 heads and
-// 15k rows in all took 94 us with their read-back, two waves 97, three 104.
-inline int rows_per_block(int64_t N, int64_t blocks, int most) {
-  const int64_t r = (N + blocks - 1) / blocks;
-  return (int)(r < 1 ? 1 : (r > most ? most : r));
+// Rows of an append's block, whose places are looked up together (a few dependent loads):
+// as many that the blocks fill whole waves of the resident ones.  40619 rows of 48 heads
+// into e4m3, 16, 24, 32 rows at most: 162, 160, 159 us, 15k (read back) 90, 88, 88; one
+// wave, or 16 rows whatever is left for the last wave, 167 and 104.
+inline int rows_per_block(int64_t N, int64_t blocks) {
+  const int64_t waves = (N + blocks * kRows - 1) / (blocks * kRows), r = (N + blocks * waves - 1) / (blocks * waves);
+  return (int)(r < 1 ? 1 : r);
 }
 
-template <typename T, bool FP8>
-int append_of(const AppendArgs& a, int num_sms, cudaStream_t st) {
-  const int rows = rows_per_block(a.c.N, (int64_t)num_sms * 7, 16);
-  const int64_t grid = (a.c.N + rows - 1) / rows;
-  if (a.pos) {
-    if (a.c.head_dim == 128) append_kernel<T, FP8, 128, true><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
-    else append_kernel<T, FP8, 64, true><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
-  } else {
-    if (a.c.head_dim == 128) append_kernel<T, FP8, 128, false><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
-    else append_kernel<T, FP8, 64, false><<<(unsigned)grid, kThreads, 0, st>>>(a, rows);
-  }
+template <typename T, bool FP8, int D>
+int append_dim(const AppendArgs& a, int num_sms, cudaStream_t st) {
+  const int rows = rows_per_block(a.c.N, (int64_t)num_sms * kAppendBlocks);
+  const unsigned grid = (unsigned)((a.c.N + rows - 1) / rows);
+  if (a.interleaved) append_kernel<T, FP8, D, true><<<grid, kThreads, 0, st>>>(a, rows);
+  else append_kernel<T, FP8, D, false><<<grid, kThreads, 0, st>>>(a, rows);
   return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
 template <typename T, bool FP8>
+int append_of(const AppendArgs& a, int num_sms, cudaStream_t st) {
+  return a.c.head_dim == 128 ? append_dim<T, FP8, 128>(a, num_sms, st) : append_dim<T, FP8, 64>(a, num_sms, st);
+}
+
+template <typename T, bool FP8>
 int read_of(const ReadArgs& a, int num_sms, cudaStream_t st) {
-  const int rows = rows_per_block(a.c.N, (int64_t)num_sms * 5, kRows);
+  const int64_t even = (a.c.N + (int64_t)num_sms * 5 - 1) / ((int64_t)num_sms * 5);   // one wave, where that is
+  const int rows = (int)(even > kReadRows ? kReadRows : even);
   const int64_t grid = (a.c.N + rows - 1) / rows;
   if (a.c.head_dim == 128) read_kernel<T, FP8, 128><<<(unsigned)grid, 256, 0, st>>>(a, rows);
   else read_kernel<T, FP8, 64><<<(unsigned)grid, 256, 0, st>>>(a, rows);

@@ -222,3 +222,53 @@ def test_rows_with_bad_positions_are_left_out(V):
     assert V.get_error() == 0
     s.cache(V).append(s.new_k, s.new_v, *args(s), parent, rotary=table, position_offsets=off * 0)
     assert V.get_error() == BAD_TREE
+
+
+def test_extreme_rows_quantise_as_a_division_does(V):
+    # infinite, NaN, huge and tiny values: the bytes and scales of elementary torch operations
+    s = Step(ctx=[0], nodes=[40], cache=E4, seed=31, poison=False)
+    x = s.new_v
+    x[0, 0, 3], x[1, 0, 3], x[2, 1, 100] = math.inf, -math.inf, math.nan
+    x[3] = 3.38e38
+    x[4] *= 1e37
+    x[5] *= 1e33                          # scales around the largest that a reciprocal serves
+    x[6] *= 1e32
+    x[7] *= 1e-38
+    x[8] = 0
+    x[9] *= 1e-30
+    x[10, :, 1:] *= 1e-36
+    x[11, 0, 0], x[11, 0, 1:] = 3e38, -1e-38
+    s.cache(V).append(s.new_k, s.new_v, *args(s))
+    f = x.float()
+    scale = f.abs().amax(-1).clamp(min=2.0 ** -40) * (1.0 / 448.0)
+    want = (f / scale[..., None]).to(E4).view(torch.uint8)
+    for j in range(40):
+        page, off = s.row(0, j)
+        got = s.v.view(torch.uint8)[page, :, off]
+        nan = (want[j] & 0x7F) == 0x7F
+        assert torch.equal(got[~nan], want[j][~nan]) and ((got[nan] & 0x7F) == 0x7F).all(), j
+        a, b = s.vs[page, :, off], scale[j]
+        assert torch.equal(a.nan_to_num(-1.0), b.nan_to_num(-1.0))
+    assert V.get_error() == 0
+
+
+def test_quotients_beside_the_borders(V):
+    # rows whose largest value is any 16-bit one, and beside it values next to every border
+    # between two bytes: what is stored is what the division gives
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    mids = torch.cat([(1 + (2 * torch.arange(8) + 1) / 16) * 2.0 ** e for e in (-6, -3, 0, 5, 8)] + [(2 * torch.arange(8) + 1) * 2.0 ** -10]).cuda()
+    for dtype in (BF, HF):
+        top = torch.arange(1 << 10, device="cuda") / (1 << 10) + 1          # every mantissa of either type
+        s = Step(ctx=[0], nodes=[1 << 10], kv_heads=1, cache=E4, dtype=dtype, seed=32, poison=False)
+        scale = top.to(dtype).float() * (1.0 / 448.0)
+        x = (mids[None, :48] * scale[:, None] * (1 + (torch.rand(1 << 10, 48, generator=g, device="cuda") - 0.5) * 2.0 ** -7)).to(dtype)
+        x = torch.cat([top.to(dtype)[:, None], x, -x, torch.zeros(1 << 10, 31, dtype=dtype, device="cuda")], 1)[:, None]
+        x = torch.minimum(torch.maximum(x, -top.to(dtype)[:, None, None]), top.to(dtype)[:, None, None])
+        s.cache(V).append(x, x, *args(s))
+        f = x.float()
+        sc = f.abs().amax(-1).clamp(min=2.0 ** -40) * (1.0 / 448.0)
+        want = (f / sc[..., None]).to(E4).view(torch.uint8)
+        slots = torch.arange(1 << 10, device="cuda")
+        pages = torch.tensor(s.pages[0], device="cuda")[slots // s.page]
+        assert torch.equal(s.k.view(torch.uint8)[pages, :, slots % s.page], want)
