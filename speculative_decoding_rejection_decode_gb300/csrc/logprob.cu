@@ -2,15 +2,18 @@
 // their rows, and the gradient of the logits.  Contract in include/specdec.h
 // (specdec_logprobs, specdec_logprobs_grad).
 //
-// One pass over a row, bound by memory where rows are many: 2048 rows of 128256 bf16 90 us,
-// 5.8 TB/s (with 20 alternatives 114); 640 of 151936 36 us, 5.4 TB/s (48; all rows in one
-// wave of blocks).  Two batches of loads take turns, so that one is always under way; 6
-// blocks of an SM instead of 5 took 98 and 40 us, 256 threads in 3 blocks 93 and 43.
-//  With c = log2(e) / T, a reference rho near the row's largest
-// logit and y_v = (x_v - rho) c,
+// With c = log2(e) / T, a reference rho near the row's largest logit and y_v = (x_v - rho) c,
 //   S = sum 2^y_v,  W = sum 2^y_v y_v,
 //   ln p(v) = ln 2 (y_v - log2 S),  H = ln 2 (log2 S - W / S).
 // The difference is taken first: it is exact for neighbouring logits, however large.
+//
+// One pass over a row, bound by memory where rows are many: 2048 rows of 128256 bf16 90 us,
+// 5.8 TB/s (with 20 alternatives 104); 640 of 151936 36 us, 5.4 TB/s (45; all rows in one
+// wave of blocks).  Two batches of loads take turns, so that one is always under way; 6
+// blocks of an SM instead of 5 took 98 and 40 us, 256 threads in 3 blocks 93 and 43.  Blocks
+// that stay and take tokens in turns, finding those with an id by a count, took 93 and 128
+// with alternatives; a call of 6400 tokens with 640 ids is no faster that way either (its
+// blocks without an id cost 8 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,9 +33,11 @@ constexpr int kBlocks = 5;                 // of them on an SM
 constexpr int kU = 4;                      // 16-byte loads of a thread under way together
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kFloor = -1000.0f;         // y of entries without weight, where they meet a product
+constexpr float kLeast = -3.402823466e38f;   // the lowest finite number
 constexpr float kLazy = 8.0f;              // log2 of how far the reference may lag behind the largest entry
 constexpr int kGroups = 64, kGroup = kNT / kGroups;   // groups of threads, whose largest entries set the bound
-constexpr int kRoom = 1024;                // 16-byte pieces that a block puts aside at most, and candidates
+constexpr int kRoom = 1024;                // 16-byte pieces that a block puts aside at most
+constexpr int kCand = 2 * kNT;             // candidates at most
 constexpr int kCap = 96;                   // of a warp's list, where those were too many
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
@@ -293,43 +298,31 @@ struct LogprobShared {
   uint32_t known;
   int pieces, found;                    // put aside, and candidates: also those beyond the room
   float bound;
-  int count[kNW];
   uint64_t best[kMaxTop];
-  uint64_t bests[8][kMaxTop];           // of the cluster's blocks (rank 0)
-  uint64_t cand[kRoom];
+  uint64_t bests[8 * kMaxTop];          // of the cluster's blocks (rank 0)
+  uint64_t cand[kCand];
   uint64_t list[kNW][kCap];
 };
 
-// A warp's cnt <= 64 keys in order, the n largest to list.
-__device__ __forceinline__ int sort_most(const uint64_t* keys, int cnt, int n, uint64_t* list) {
-  const int lane = threadIdx.x & 31;
-  const uint64_t k0 = lane < cnt ? keys[lane] : 0, k1 = lane + 32 < cnt ? keys[lane + 32] : 0;
+// The n largest of cnt keys, in order, to out, by all threads: a thread counts the keys
+// above its own.  (Not for cnt > kNT x 2; keys are distinct.)
+__device__ __forceinline__ void place_most(const uint64_t* keys, int cnt, int n, uint64_t* out) {
+  const int i0 = threadIdx.x, i1 = threadIdx.x + kNT;
+  const uint64_t k0 = i0 < cnt ? keys[i0] : 0, k1 = i1 < cnt ? keys[i1] : 0;
   int r0 = 0, r1 = 0;
-  for (int i = 0; i < cnt; ++i) {
-    const uint64_t k = keys[i];
-    r0 += k > k0;
-    r1 += k > k1;
-  }
-  if (k0 && r0 < n) list[r0] = k0;
-  if (k1 && r1 < n) list[r1] = k1;
-  return min(cnt, n);
-}
-
-// The n largest of sorted lists, lane i < lists holding list i, to out (0: none).
-template <typename At>
-__device__ __forceinline__ void merge_sorted(int lists, int n, At at, uint64_t* out) {
-  const int lane = threadIdx.x & 31;
-  int pos = 0;
-  uint64_t head = lane < lists ? at(lane, 0) : 0;
-  for (int r = 0; r < n; ++r) {
-    const uint64_t best = warp_most(head);
-    if (best && head == best) {
-      ++pos;
-      head = pos < n ? at(lane, pos) : 0;
+  if (cnt <= kNT) {
+#pragma unroll 4
+    for (int i = 0; i < cnt; ++i) r0 += keys[i] > k0;
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < cnt; ++i) {
+      const uint64_t k = keys[i];
+      r0 += k > k0;
+      r1 += k > k1;
     }
-    if (lane == 0) out[r] = best;
   }
-  __syncwarp();
+  if (k0 && r0 < n) out[r0] = k0;
+  if (k1 && r1 < n) out[r1] = k1;
 }
 
 __device__ __forceinline__ void put_remote(uint32_t addr, uint64_t v) {
@@ -379,15 +372,16 @@ __global__ void __launch_bounds__(kNT, kBlocks) logprob_kernel(const LogprobArgs
   const float given = a.logprob && rank == 0 && tid == 0 ? as_float(x[id]) : 0.0f;
   if (TOP && tid == 0) {   // (the first bound's barrier follows)
     sh.pieces = sh.found = 0;
-    sh.bound = -INFINITY;
+    sh.bound = kLeast;
   }
+  if (TOP && tid < kMaxTop) sh.best[tid] = 0;
   Sums mine = {-INFINITY, 0.0f, 0.0f};
   uint64_t s2[2] = {0, 0}, w2[2] = {0, 0};
   const uint64_t c2 = pair(a.c, a.c);
   const float lag = kLazy / a.c;
   float ref = 0.0f;
   typename R::Low low = R::below(kFloor / a.c);   // entries of -inf count as this: 0 x -inf would be NaN
-  [[maybe_unused]] float bound = -INFINITY;
+  [[maybe_unused]] float bound = kLeast;   // always above -inf, which is never put aside
   auto gather = [&] {
     float p, q;
     unpair(add2(s2[0], s2[1]), p, q);
@@ -458,7 +452,7 @@ __global__ void __launch_bounds__(kNT, kBlocks) logprob_kernel(const LogprobArgs
     int both = above | reach << 16;
 #pragma unroll
     for (int o = 1; o < kGroup; o <<= 1) both += __shfl_xor_sync(0xFFFFFFFFu, both, o);
-    if ((both & 0xFFFF) < n && both >> 16 >= n) sh.bound = seen;   // the n-th largest
+    if ((both & 0xFFFF) < n && both >> 16 >= n) sh.bound = fmaxf(seen, kLeast);   // the n-th largest
     __syncthreads();
     bound = sh.bound;
   };
@@ -522,23 +516,16 @@ __global__ void __launch_bounds__(kNT, kBlocks) logprob_kernel(const LogprobArgs
       for (int k = 0; k < E; ++k) {
         const float2 f = R::two(w, k >> 1);
         const float e = k & 1 ? f.y : f.x;
-        if (e >= bound && e != -INFINITY) {
+        if (e >= bound) {
           const int at = atomicAdd(&sh.found, 1);
-          if (at < kRoom) sh.cand[at] = key_of(e, index + k);
+          if (at < kCand) sh.cand[at] = key_of(e, index + k);
         }
       }
     }
     __syncthreads();
     const int found = sh.found;
-    if (pieces <= kRoom && found <= kRoom && found >= min(n, entries)) {
-      const int per = (found + kNW - 1) / kNW, at = min(found, warp * per);
-      const int cnt = min(per, found - at);
-      int kept = 0;
-      for (int i = 0; i < cnt; i += 64) {     // once, as a rule
-        kept += sort_most(sh.cand + at + i, min(64, cnt - i), n, sh.list[warp] + kept);
-        if (i > 0) kept = keep_most(sh.list[warp], kept, n);
-      }
-      if (lane == 0) sh.count[warp] = kept;
+    if (pieces <= kRoom && found <= kCand && found >= min(n, entries)) {
+      place_most(sh.cand, found, n, sh.best);
     } else {
       // lists for each warp, of rising indices
       if (tid == 0) sh.known = order_of(-INFINITY);
@@ -562,16 +549,16 @@ __global__ void __launch_bounds__(kNT, kBlocks) logprob_kernel(const LogprobArgs
         lst = offer<T>(sh.list[warp], lst, n, w, lane < behind ? 1 : 0, (uint32_t)(done + lane), &sh.known);
       }
       const int kept = keep_most(sh.list[warp], lst.cnt, n);
-      if (lane == 0) sh.count[warp] = kept;
+      if (lane < n) sh.cand[warp * n + lane] = lane < kept ? sh.list[warp][lane] : 0;
+      __syncthreads();
+      place_most(sh.cand, kNW * n, n, sh.best);
     }
-    __syncthreads();
   }
   if (warp == 0) {
     const Sums empty = {-INFINITY, 0.0f, 0.0f};
     mine = warp_join(lane < kNW ? sh.part[lane] : empty, a.c);
-    if constexpr (TOP)
-      merge_sorted(kNW, n, [&](int l, int p) { return p < sh.count[l] ? sh.list[l][p] : 0; }, sh.best);
   }
+  if (TOP) __syncthreads();
   if (ranks > 1) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every block runs
     if (warp == 0) {
@@ -581,14 +568,17 @@ __global__ void __launch_bounds__(kNT, kBlocks) logprob_kernel(const LogprobArgs
         put_remote(at + 4, mine.s);
         put_remote(at + 8, mine.w);
       }
-      if (TOP && lane < n) put_remote(mapa(smem_addr(&sh.bests[rank][lane]), 0), sh.best[lane]);
+      if (TOP && lane < n) put_remote(mapa(smem_addr(&sh.bests[rank * n + lane]), 0), sh.best[lane]);
     }
     cluster_sync_all();
     if (rank) return;
     if (warp == 0) {
       const Sums empty = {-INFINITY, 0.0f, 0.0f};
       mine = warp_join(lane < ranks ? sh.ranks[lane] : empty, a.c);
-      if constexpr (TOP) merge_sorted(ranks, n, [&](int l, int p) { return sh.bests[l][p]; }, sh.best);
+    }
+    if constexpr (TOP) {
+      place_most(sh.bests, ranks * n, n, sh.best);
+      __syncthreads();
     }
   }
   if (warp) return;
@@ -612,9 +602,11 @@ __global__ void __launch_bounds__(kNT, kBlocks) logprob_kernel(const LogprobArgs
 // With z = log2 p(v) and the gradients g of ln p(id), h of H and g_j of the
 // alternatives' ln p:
 //   d x_v = (1 / T) (g [v = id] + sum_j g_j [v = id_j] - p (g + sum_j g_j + h (ln p + H)))
-// One pass, a 16-byte load and a store of a thread at a time; the few entries with a
-// term of their own are written again, whole, behind the block's.
-constexpr int kGT = 256, kGU = 4;
+// One pass, bound by memory: 921 of 1973 rows of 128257 bf16 (the others are zeros) 117 us,
+// 6.3 TB/s; four loads of a thread at a time instead of two 119, eight 132, past the caches
+// 123, half or twice the pieces of a block 133 and 131.  The few entries with a term of
+// their own are written again, whole, behind the block's.
+constexpr int kGT = 256, kGU = 2;
 constexpr int kGVecs = 4096;   // 16-byte pieces of a row that a block takes, about
 
 template <typename T>
@@ -678,9 +670,9 @@ __global__ void __launch_bounds__(kGT) logprob_grad_kernel(const LogprobGradArgs
     for (; v + kGU * kGT <= v1; v += kGU * kGT) {
       uint4 w[kGU];
 #pragma unroll
-      for (int u = 0; u < kGU; ++u) w[u] = __ldcs(xv + v + u * kGT + tid);
+      for (int u = 0; u < kGU; ++u) w[u] = __ldg(xv + v + u * kGT + tid);
 #pragma unroll
-      for (int u = 0; u < kGU; ++u) __stcs(ov + v + u * kGT + tid, turn(w[u]));
+      for (int u = 0; u < kGU; ++u) ov[v + u * kGT + tid] = turn(w[u]);
     }
     for (; v + tid < v1; v += kGT) ov[v + tid] = turn(xv[v + tid]);
     if (part == 0 && tid < lead) out[tid] = one(x[tid]);
@@ -707,12 +699,16 @@ __global__ void __launch_bounds__(kGT) logprob_grad_kernel(const LogprobGradArgs
 
 template <typename T>
 int forward_of(const LogprobArgs& a, int num_sms, cudaStream_t st) {
-  // Blocks of a row: as many as the SMs hold at once, of at least two loads a thread.
-  // us of 1, 2, 4, 8 blocks a row (256 threads each): 48 rows of 32000 f32 7.3, 6.3, 5.3,
-  // 5.2; 152 of 128256 bf16 15.5, 12.4, 14.5, 16.4; 640 of 151936 46, 44, 48, 60.
+  // Blocks of a row: 2 or 4 where the SMs hold them all at once, of at least two loads a
+  // thread, and 8 where they fill two thirds of the SMs at most.  us of 1, 2, 4, 8 blocks a
+  // row, none and 20 alternatives: rows of 128256 bf16
+  //   48   - - 8.3 7.3, - - 13.7 13.4      152  19.6 13.4 12.4 14.5, 23.6 18.6 19.6 27.2
+  //   64   - - 8.3 7.3, - - 14.5 15.5      380  25.7 20.6 30.9 37.1, 30.0 27.7 43.9 60.4
+  //   95   15.5 10.1 8.6 11.4, 20.6 17.3 15.5 20.8      1000  55 53 66 87, 62 70 95 142
   const int vecs = a.V / Row<T>::E;
+  const int64_t slots = (int64_t)kBlocks * num_sms;
   int ranks = 1;
-  while (ranks < 8 && 2 * a.M * ranks <= kBlocks * num_sms && vecs / (2 * ranks) >= 2 * kNT) ranks *= 2;
+  while (ranks < 8 && (ranks < 4 ? 2 * a.M * ranks <= slots : 12 * a.M <= slots) && vecs / (2 * ranks) >= 2 * kNT) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.M * ranks));
   cfg.blockDim = dim3(kNT);
