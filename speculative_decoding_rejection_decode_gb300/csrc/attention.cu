@@ -26,9 +26,20 @@ enum class Kernel { kWarp, kTile, kWide };
 
 constexpr int kTileRows = 128;   // rows of a tile of the tile kernel
 
-Kernel kernel_of(bool cross, int cache_dtype, int page_size, int64_t avg) {
+// The wide kernel (cross_wide.cu) reads a key for 256 rows, and is bound by the products; the
+// tile kernel divides a call's rows among more CTAs.  Tile and wide kernel, device us, 32
+// query and 8 kv heads of 128, bf16 states (rows of a request and kv head):
+//   1 request, 2816 states    128  29 29    160  27 31    256  29 36    512  31 37
+//   8 of 2816                 128  46 50    160  53 54    384  70 74    512  84 79
+//   64 of 1500                128 115 116   144 171 127   256 193 136   512 349 221
+// The wide one takes over where the rows pass a tile and the tiles are more than one and a
+// half for each SM.
+Kernel kernel_of(bool cross, int cache_dtype, int page_size, int B, int64_t N, int kv_heads, int q_heads, int num_sms) {
+  const int64_t avg = average_rows(B, N, kv_heads, q_heads);
   if (avg <= kWarpRows) return Kernel::kWarp;
-  return cross && cache_dtype != SPECDEC_E4M3 && page_size % 8 == 0 && avg > kTileRows ? Kernel::kWide : Kernel::kTile;
+  const int64_t tiles = (int64_t)B * kv_heads * ((avg + kTileRows - 1) / kTileRows);
+  return cross && cache_dtype != SPECDEC_E4M3 && page_size % 8 == 0 && avg > kTileRows && 2 * tiles > 3 * (int64_t)num_sms
+             ? Kernel::kWide : Kernel::kTile;
 }
 
 int rows_of(Kernel k) { return k == Kernel::kWarp ? kRowsTile : k == Kernel::kTile ? kTileRows : kWideRows; }
@@ -37,7 +48,7 @@ int rows_of(Kernel k) { return k == Kernel::kWarp ? kRowsTile : k == Kernel::kTi
 
 int64_t attend_workspace_bytes(bool cross, int cache_dtype, int page_size, int B, int64_t N, int kv_heads, int q_heads,
                                int head_dim, int64_t capacity, int num_sms) {
-  const Kernel k = kernel_of(cross, cache_dtype, page_size, average_rows(B, N, kv_heads, q_heads));
+  const Kernel k = kernel_of(cross, cache_dtype, page_size, B, N, kv_heads, q_heads, num_sms);
   if (whole_items(B, N, kv_heads, q_heads, capacity, rows_of(k), num_sms)) return 0;
   if (k == Kernel::kWide) return cross_wide_workspace(head_dim, num_sms);
   if (k == Kernel::kTile) return attend_tile_workspace(head_dim, num_sms);
@@ -48,7 +59,7 @@ int launch_attend(const AttendArgs& args, int cache_dtype, int dtype, int num_sm
   if (args.c.N == 0) return SPECDEC_OK;
   AttendArgs a = args;
   const CacheArgs& c = a.c;
-  const Kernel k = kernel_of(a.cross, cache_dtype, c.geo.page_size, average_rows(c.B, c.N, c.geo.kv_heads, a.q_heads));
+  const Kernel k = kernel_of(a.cross, cache_dtype, c.geo.page_size, c.B, c.N, c.geo.kv_heads, a.q_heads, num_sms);
   a.whole = whole_items(c.B, c.N, c.geo.kv_heads, a.q_heads, (int64_t)c.geo.max_pages * c.geo.page_size, rows_of(k), num_sms);
   a.item_cost = cache_dtype == SPECDEC_E4M3 && k == Kernel::kWarp ? kItemCostWarp8 : kItemCost;
   if (k == Kernel::kWide) return launch_cross_wide(a, dtype, num_sms, st);
