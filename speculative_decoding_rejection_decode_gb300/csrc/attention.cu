@@ -13,10 +13,10 @@ int64_t average_rows(int B, int64_t N, int kv_heads, int q_heads) {
 // Up to these (a tile of the warp kernel) the warp kernel, above them the tile kernel.
 // One context of 500 / 64 up to 8191 / 4 of 30000 / 200 up to 1500, 8 kv heads of 128,
 // device us, warp and tile kernel:
-//   4 rows  bf16 11.7 13.7 / 204 211 / 85 89 / 138 177, e4m3 12.7 15.1 / 204 234 / 80 89 / 155 216
-//   12      bf16 14.0 13.7 / 213 214 / 89 91 / 165 178, e4m3 14.7 15.4 / 217 241 / 84 91 / 186 219
-//   16      bf16 14.8 13.7 / 221 214 / 90 91 / 177 178, e4m3 15.4 15.7 / 224 242 / 85 92 / 195 221
-//   20      bf16 15.1 13.7 / 394 217 / 157 92 / 298 179, e4m3 15.7 15.7 / 403 247 / 146 94 / 330 220
+//   4 rows  bf16 14.9 18.1 / 179 184 / 87 90 / 127 150, e4m3 14.8 18.9 / 179 208 / 81 81 / 152 197
+//   12      bf16 16.8 18.8 / 183 185 / 92 92 / 144 151, e4m3 16.8 19.1 / 188 206 / 85 82 / 172 199
+//   16      bf16 17.3 18.8 / 182 185 / 93 92 / 148 151, e4m3 16.9 19.4 / 192 207 / 86 82 / 177 199
+//   20      bf16 17.0 18.9 / 340 189 / 165 94 / 255 153, e4m3 18.4 19.0 / 345 210 / 146 82 / 306 198
 // The average decides: in a batch of one large request among many small ones, the
 // large one takes a tile of 16 rows at a time.
 constexpr int kWarpRows = 16;

@@ -11,9 +11,11 @@
 // them the ranges that hold many short requests finished late.  us at a cost of 2, 4,
 // 5, 6 (32 query and 8 kv heads of 128): tile kernel, 64 requests of 2 to 9 nodes over up
 // to 8191 keys, bf16 237, 221, 219, 216; 32 of 29 over 6000 to 16000, e4m3 303, 298, 296,
-// 296; warp kernel, 64 of 1 over up to 8191, bf16 183, 172, 172, 172 and e4m3 180, 183,
-// 187, 187; 200 of 1 to 4 over up to 1500, bf16 201, 174, 171, 170 and e4m3 190, 194,
-// 195, 202 (its tiles are of 256 keys and take longer).
+// 296; warp kernel at a cost of 1, 2, 3, 5, 64 of 1 over up to 8191, bf16 193, 183, 180,
+// 180; 200 of 1 to 4 over up to 1500, bf16 182, 170, 157, 151; 64 of 2 to 9 over up to
+// 2047, 32 kv heads, bf16 300, 256, 236, 216 (at 7 and more it rises again); e4m3 at 2, 3,
+// 4, 6: 178, 183, 185, 191; 173, 179, 183, 191; 258, 259, 269, 286 (its tiles are of 256
+// keys and take longer).
 //
 // Rows of an item: r = node * group + head within the group, so one read of a
 // key serves every node and every query head that shares it.

@@ -44,9 +44,10 @@ struct WarpTile {
 template <bool FP8, int D, int R>
 struct WarpLayout {
   using W = WarpTile<FP8, D>;
-  static constexpr int MERGE = kWarps * R * (D * 4 + 8);       // reuses the ring
-  static constexpr int Q = W::RING > MERGE ? W::RING : MERGE;  // R rows of D 16-bit values
-  static constexpr int ROWF = Q + R * D * 2;                   // per-row factor of the scores
+  static_assert(R * D * 4 <= W::STAGE, "a warp's sums lie in a stage of its ring");
+  static constexpr int Q = W::RING;                            // R rows of D 16-bit values
+  static constexpr int STATS = Q + R * D * 2;                  // maximum and sum of each warp's rows
+  static constexpr int ROWF = STATS + kWarps * R * 8;          // per-row factor of the scores
   static constexpr int ANC = ROWF + R * 4;                     // ancestors of the tile's nodes
   static constexpr int BYTES = ANC + R * (kMaxTreeNodes / 8);
 };
@@ -162,8 +163,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
   if ((int)blockIdx.x >= ranges || scan.b < 0) return;
   const int64_t uend = range_begin(units, ranges, blockIdx.x + 1);
   const Partials<R, D> part(a.workspace, G);
-  int b = scan.b;
-  int64_t base = scan.before;       // units before request b
   char* ring = smem + warp * (kStages * W::STAGE);
   const uint32_t ring_s = smem_addr(ring);
   const uint32_t q_s = smem_addr(smem + L::Q);
@@ -172,72 +171,120 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
   const int quad = lane & 3, qrow = lane >> 2;
   uint32_t bad = 0;
 
-  uint32_t ignored = 0;
-  Request q = attend_request(plan, b, R, TK, ignored);
-  for (int64_t u = u0; u < uend;) {
-    while (u >= base + q.units) {
-      base += q.units;
-      if (++b >= c.B) return;   // lengths that changed under the call
-      q = attend_request(plan, b, R, TK, ignored);
+  // A place in the CTA's range: the tiles t0 .. t1 of an item.
+  struct Walk {
+    int64_t u, base;   // units up to the item's end, and before request b
+    int b, h, rt, t0, t1;
+    Request q;
+  };
+  auto next_segment = [&](Walk& w) -> bool {
+    while (w.u < uend) {
+      uint32_t ignored = 0;
+      while (w.u >= w.base + w.q.units) {
+        w.base += w.q.units;
+        if (++w.b >= c.B) {   // lengths that changed under the call
+          w.u = uend;
+          return false;
+        }
+        w.q = attend_request(plan, w.b, R, TK, ignored);
+      }
+      const int cost = (a.whole ? 1 : w.q.tiles) + plan.item_cost;
+      const int64_t item = (w.u - w.base) / cost;
+      const int at = (int)((w.u - w.base) % cost);
+      w.t0 = max(at - plan.item_cost, 0);
+      w.t1 = (int)min((int64_t)(cost - plan.item_cost), at - plan.item_cost + (uend - w.u));
+      w.h = (int)(item / w.q.rts);
+      w.rt = (int)(item % w.q.rts);
+      w.u += cost - at;
+      if (w.t1 <= w.t0) continue;
+      if (a.whole) w.t1 = w.q.tiles;
+      return true;
     }
-    const int cost = (a.whole ? 1 : q.tiles) + plan.item_cost;
-    const int64_t item = (u - base) / cost;
-    const int at = (int)((u - base) % cost);
-    const int t0 = max(at - plan.item_cost, 0);
-    int t1 = (int)min((int64_t)(cost - plan.item_cost), at - plan.item_cost + (uend - u));
-    const int h = (int)(item / q.rts), rt = (int)(item % q.rts);
-    u += cost - at;
-    if (t1 <= t0) continue;
-    if (a.whole) t1 = q.tiles;
+    return false;
+  };
+
+  // ---- the warp's blocks: tile t, keys [t TK + warp KB, + KB).  They are asked for two
+  // ahead of the one that is worked on, across the items of the range: a new item's first
+  // blocks are on their way while the last one's rows are joined (64 requests of 2 to 9
+  // rows, 32 heads of their own, up to 2047 states: WARP_FIGURES) -------------------------
+  uint32_t ignored = 0;
+  Walk far = {u0, scan.before, scan.b, 0, 0, 0, 0, attend_request(plan, scan.b, R, TK, ignored)};
+  bool more = next_segment(far);   // far.t0: the next tile to be looked up
+  Walk now = far;
+  // What leads to the cache row of this lane's key of that block is loaded while the block
+  // before is worked on, and looked at behind it: a warp that met the mask and then the page
+  // table stood still for both (WARP_LOOK).
+  struct Look {
+    int page;        // as the table has it
+    int row;         // the rest of the row
+    bool in;         // a key of the request
+    uint8_t seen;    // as the mask has it
+  };
+  auto look = [&]() -> Look {
+    Look l = {0, 0, false, 1};
+    const int64_t s = (int64_t)far.t0 * TK + warp * KB + lane;
+    if (more && lane < KB && s < (int64_t)far.q.len + (CROSS ? 0 : far.q.n)) {
+      const uint32_t p = (uint32_t)s / (uint32_t)c.geo.page_size;
+      l.in = true;
+      l.page = __ldg(c.table + far.b * c.geo.table_stride + p);
+      l.row = far.h * c.geo.page_size + (int)((uint32_t)s - p * (uint32_t)c.geo.page_size);
+      if constexpr (CROSS) {
+        if (a.mask) {
+          l.seen = 0;
+          if (s < a.mask_slots) l.seen = __ldg(a.mask + far.b * a.mask_stride + s);
+        }
+      }
+    }
+    return l;
+  };
+  auto row_of = [&](const Look& l) -> int {   // -1: no key that may be seen
+    if (!l.in || !l.seen) return -1;
+    if (l.page < 0 || l.page >= c.geo.num_pages) {
+      bad |= SPECDEC_DEVERR_BAD_CACHE;
+      return -1;
+    }
+    return (int)((int64_t)l.page * c.geo.kv_heads * c.geo.page_size + l.row);
+  };
+  int to = 0;                         // the stage that the next block goes to
+  auto issue = [&](int row) {         // and on to the tile behind it
+    const uint32_t st = ring_s + to * W::STAGE;
+    to = to + 1 == kStages ? 0 : to + 1;
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < KB * CH / 32; ++i) {
+        const int x = i * 32 + lane, key = x / CH, ch = x % CH;
+        const int r = __shfl_sync(0xFFFFFFFFu, row, key);
+        const int64_t off = (int64_t)max(r, 0) * W::ROW + ch * 16;
+        const uint32_t dst = st + spread<CH>(key, ch) * 16;
+        copy16(dst, static_cast<const char*>(c.k) + off, r >= 0);
+        copy16(dst + KB * W::ROW, static_cast<const char*>(c.v) + off, r >= 0);
+      }
+      if constexpr (FP8) {
+        copy4(st + 2 * KB * W::ROW + lane * 4, c.ks + max(row, 0), row >= 0);
+        copy4(st + 2 * KB * W::ROW + KB * 4 + lane * 4, c.vs + max(row, 0), row >= 0);
+      }
+      if (++far.t0 >= far.t1) more = next_segment(far);
+    }
+    copy_commit();
+  };
+  int rows_now[kStages];            // cache rows of the blocks in flight (which keys are live)
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    rows_now[i] = row_of(look());
+    issue(rows_now[i]);
+  }
+  Look next = look();
+  int stage = 0;                    // of the block that is worked on
+  for (bool any = now.t1 > now.t0; any; any = next_segment(now)) {
+    const Request& q = now.q;
+    const int h = now.h, rt = now.rt, t0 = now.t0, t1 = now.t1;
     const bool whole = t0 == 0 && t1 == q.tiles;
     const int rows = min(R, q.n * group - rt * R);            // rows of this tile
     const int node0 = rt * R / group;                          // its first node
-    const int32_t* pages = c.table + b * c.geo.table_stride;
     const int32_t* parent = c.parent ? c.parent + q.first : nullptr;
     const int words = (q.n + 31) >> 5;
 
     __syncthreads();   // the last segment's readers are done
-    // ---- the warp's blocks: tile t, keys [t TK + warp KB, + KB) --------------
-    const int64_t all_keys = (int64_t)q.len + (CROSS ? 0 : q.n);
-    auto row_of = [&](int t) -> int {   // cache row of this lane's key of block t, -1: none
-      const int64_t s = (int64_t)t * TK + warp * KB + lane;
-      if (t >= t1 || lane >= KB || s >= all_keys) return -1;
-      if constexpr (CROSS) {
-        if (a.mask && (s >= a.mask_slots || !__ldg(a.mask + b * a.mask_stride + s))) return -1;
-      }
-      const int64_t r = cache_row(c.geo, pages, s);
-      if (r < 0) {
-        bad |= SPECDEC_DEVERR_BAD_CACHE;
-        return -1;
-      }
-      return (int)(r + (int64_t)h * c.geo.page_size);
-    };
-    auto issue = [&](int t, int row) {
-      const uint32_t st = ring_s + ((t - t0) % kStages) * W::STAGE;
-      if (t < t1) {
-#pragma unroll
-        for (int i = 0; i < KB * CH / 32; ++i) {
-          const int x = i * 32 + lane, key = x / CH, ch = x % CH;
-          const int r = __shfl_sync(0xFFFFFFFFu, row, key);
-          const int64_t off = (int64_t)max(r, 0) * W::ROW + ch * 16;
-          const uint32_t dst = st + spread<CH>(key, ch) * 16;
-          copy16(dst, static_cast<const char*>(c.k) + off, r >= 0);
-          copy16(dst + KB * W::ROW, static_cast<const char*>(c.v) + off, r >= 0);
-        }
-        if constexpr (FP8) {
-          copy4(st + 2 * KB * W::ROW + lane * 4, c.ks + max(row, 0), row >= 0);
-          copy4(st + 2 * KB * W::ROW + KB * 4 + lane * 4, c.vs + max(row, 0), row >= 0);
-        }
-      }
-      copy_commit();
-    };
-    int rows_now[kStages];            // cache rows of the blocks in flight (which keys are live)
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      rows_now[i] = row_of(t0 + i);
-      issue(t0 + i, rows_now[i]);
-    }
-    int ahead = row_of(t0 + kStages - 1);
     // ---- queries: shared memory, as the products want them (the first blocks are
     // on their way meanwhile) ---------------------------------------------------
     for (int r = warp; r < R; r += kWarps) {
@@ -299,19 +346,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
     float rf[2];
     rf[0] = rowf[qrow];
     rf[1] = rowf[qrow + 8];
+    int last = 0;                     // the stage of the segment's last block
     for (int t = t0; t < t1; ++t) {
-      issue(t + kStages - 1, ahead);
-      const int now = rows_now[0];
+      const int row = rows_now[0];
+      const int ahead = row_of(next);
+      issue(ahead);
 #pragma unroll
       for (int i = 0; i + 1 < kStages - 1; ++i) rows_now[i] = rows_now[i + 1];
       rows_now[kStages - 2] = ahead;
-      ahead = row_of(t + kStages);
+      next = look();
       copy_wait<kStages - 1>();
       __syncwarp();
-      const uint32_t live = __ballot_sync(0xFFFFFFFFu, now >= 0);
+      const uint32_t live = __ballot_sync(0xFFFFFFFFu, row >= 0);
       if (live) {
-        const uint32_t k_s = ring_s + ((t - t0) % kStages) * W::STAGE, v_s = k_s + KB * W::ROW;
-        char* kv = ring + ((t - t0) % kStages) * W::STAGE;
+        const uint32_t k_s = ring_s + stage * W::STAGE, v_s = k_s + KB * W::ROW;
+        char* kv = ring + stage * W::STAGE;
         float s[KB / 8][4];
 #pragma unroll
         for (int nt = 0; nt < KB / 8; ++nt)
@@ -483,12 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
           }
       }
       __syncwarp();   // the block is read before its stage is filled again
+      last = stage;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    copy_wait<0>();
-    // ---- the warps meet -------------------------------------------------------
-    __syncthreads();
-    float* merge = reinterpret_cast<float*>(smem);                       // [warps][R][D]
-    float2* stats = reinterpret_cast<float2*>(smem + kWarps * R * D * 4);  // [warps][R]
+    // ---- the warps meet: each leaves its sums in the stage that it has read last -----
+    float2* stats = reinterpret_cast<float2*>(smem + L::STATS);  // [warps][R]
+    // pairs of a row's sums as a lane holds them, rows turned so that 4 of them lie in
+    // different banks
+    auto pair_of = [&](int w, int r, int i) {
+      return reinterpret_cast<float2*>(smem + w * (kStages * W::STAGE) + last * W::STAGE) + r * (D / 2) + (i ^ ((r & 7) << 2));
+    };
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       float v = l[y];
@@ -498,41 +551,46 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
       if (r >= rows) continue;
       if (quad == 0) stats[warp * R + r] = make_float2(m[y], v);
 #pragma unroll
-      for (int nt = 0; nt < D / 8; ++nt)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int d = FP8 ? (nt >> 1) * 16 + quad * 4 + x * 2 + (nt & 1) : nt * 8 + quad * 2 + x;
-          merge[(warp * R + r) * D + d] = o[nt][2 * y + x];
-        }
+      for (int nt = 0; nt < D / 8; ++nt) *pair_of(warp, r, nt * 4 + quad) = make_float2(o[nt][2 * y], o[nt][2 * y + 1]);
     }
     __syncthreads();
     const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 > 0 ? 0 : 1);
-    for (int x = tid; x < rows * D; x += kThreads) {
-      const int r = x / D, d = x % D;
+    for (int x = tid; x < rows * (D / 2); x += kThreads) {
+      const int r = x / (D / 2), i = x % (D / 2), nt = i / 4;
+      const int d = FP8 ? (nt >> 1) * 16 + i % 4 * 4 + (nt & 1) : 2 * i;
+      constexpr int NEXT = FP8 ? 2 : 1;     // the pair's second element is d + NEXT
       float mm = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stats[w * R + r].x);
       const float ref = mm == -INFINITY ? 0.0f : mm;
-      float sum = 0.0f, acc = 0.0f;
+      float sum = 0.0f, acc0 = 0.0f, acc1 = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 s = stats[w * R + r];
+        const float2 s = stats[w * R + r], v = *pair_of(w, r, i);
         const float f = ex2(s.x - ref);
         sum += s.y * f;
-        acc += s.x == -INFINITY ? 0.0f : merge[(w * R + r) * D + d] * f;
+        acc0 += s.x == -INFINITY ? 0.0f : v.x * f;
+        acc1 += s.x == -INFINITY ? 0.0f : v.y * f;
       }
       const bool gone = tail && parent && lost[(rt * R + r) / group - node0];   // a row of zeros
       if (whole) {
         const int row = rt * R + r;
-        T y;
-        from_float(gone || sum == 0.0f ? 0.0f : acc / sum, y);
-        static_cast<T*>(a.out)[((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + d] = y;
+        const bool none = gone || sum == 0.0f;
+        T y0, y1;
+        from_float(none ? 0.0f : acc0 / sum, y0);
+        from_float(none ? 0.0f : acc1 / sum, y1);
+        T* out = static_cast<T*>(a.out) + ((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + d;
+        out[0] = y0;
+        out[NEXT] = y1;
       } else {
-        part.sums[(slot * R + r) * D + d] = acc;
-        if (d == 0) part.stats[slot * R + r] = make_float2(mm, gone ? kLostRow : sum);
+        float* sums = part.sums + (slot * R + r) * D + d;
+        sums[0] = acc0;
+        sums[NEXT] = acc1;
+        if (i == 0) part.stats[slot * R + r] = make_float2(mm, gone ? kLostRow : sum);
       }
     }
   }
+  copy_wait<0>();
   if (bad) atomicOr(c.err, bad);
 }
 
