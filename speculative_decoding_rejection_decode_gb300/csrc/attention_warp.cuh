@@ -6,11 +6,12 @@
 // Few rows per request (16 a tile).  The pass is
 // bound by reading the cache once; each warp streams its own 16 or 32 keys of
 // a tile through a ring in shared memory (asynchronous 16-byte copies, three
-// blocks deep, no block-wide barrier), keeps the running maximum, sum and
+// blocks deep, no block-wide barrier, on from one item to the next), keeps the running maximum, sum and
 // weighted sum of its keys in registers, and the warps meet once per segment.
-// Measured (32 query and 8 kv heads of 128, bf16): one node over 500 keys 12 us, all
-// of it latency; 64 nodes over up to 4000 keys 593 MB in 111 us, 5.4 TB/s, the copies
-// of a CTA not deep enough at its first and last blocks (70 % of DRAM's cycles).
+// Measured (bf16, 32 query heads of 128): one node over 500 keys 12 us, all of it latency;
+// 8 kv heads, 64 nodes over up to 8191 keys 1.10 GB in 180 us, 6.1 TB/s; 32 kv heads, 64
+// requests of 1 row over 1000 states 6.3 TB/s, of 2 to 9 rows over up to 2047 states, a
+// tenth masked, 1.16 GB in 197 us, 5.9 TB/s.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -205,15 +206,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
 
   // ---- the warp's blocks: tile t, keys [t TK + warp KB, + KB).  They are asked for two
   // ahead of the one that is worked on, across the items of the range: a new item's first
-  // blocks are on their way while the last one's rows are joined (64 requests of 2 to 9
-  // rows, 32 heads of their own, up to 2047 states: WARP_FIGURES) -------------------------
+  // blocks are on their way while the last one's rows are joined (64 requests of 4 rows
+  // over 300 states 45 to 39 us) ---------------------------------------------------------
   uint32_t ignored = 0;
   Walk far = {u0, scan.before, scan.b, 0, 0, 0, 0, attend_request(plan, scan.b, R, TK, ignored)};
   bool more = next_segment(far);   // far.t0: the next tile to be looked up
   Walk now = far;
   // What leads to the cache row of this lane's key of that block is loaded while the block
   // before is worked on, and looked at behind it: a warp that met the mask and then the page
-  // table stood still for both (WARP_LOOK).
+  // table stood still for both (64 requests of 2 to 9 rows over up to 2047 states, 32 heads of
+  // their own: 217 to 197 us).
   struct Look {
     int page;        // as the table has it
     int row;         // the rest of the row
