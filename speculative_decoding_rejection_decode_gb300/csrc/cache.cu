@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) append_kernel(const A
     Values v = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (x.on && i < here && places[i].owned) {
       const T* from = x.from + i * x.stride;
-      v.a = __ldg(reinterpret_cast<const uint4*>(from));
-      v.b = __ldg(reinterpret_cast<const uint4*>(from + apart));
+      v.a = *reinterpret_cast<const uint4*>(from);    // (q may be turned in place)
+      v.b = *reinterpret_cast<const uint4*>(from + apart);
     }
     return v;
   };

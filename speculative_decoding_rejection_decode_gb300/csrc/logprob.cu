@@ -171,7 +171,7 @@ __device__ __forceinline__ void move_to(Sums& a, float rho, float c) {
     a.s = a.w = 0.0f;
   } else {
     const float d = (a.rho - rho) * c, f = ex2(d);
-    a.w = f * fmaf(d < kFloor ? kFloor : d, a.s, a.w);
+    a.w = f > 0.0f ? f * fmaf(d < kFloor ? kFloor : d, a.s, a.w) : 0.0f;   // (w: see the end of the kernel)
     a.s *= f;
   }
   a.rho = rho;
@@ -583,6 +583,10 @@ __global__ void __launch_bounds__(kNT, kBlocks) logprob_kernel(const LogprobArgs
   }
   if (warp) return;
   const bool fine = mine.s > 0.0f && mine.s < INFINITY;   // not: no distribution
+  // y of entries that are out of reach may pass 32 bits where the reference itself is near
+  // their end (0 x inf is NaN); the reference's neighbours are then 2^90 / T and more
+  // away, so that it and its equals have all the weight
+  if (!(mine.w == mine.w)) mine.w = 0.0f;
   const float none_f = __uint_as_float(0x7FC00000u);
   const float lg = log2f(mine.s);
   if (lane == 0) {
@@ -670,7 +674,7 @@ __global__ void __launch_bounds__(kGT) logprob_grad_kernel(const LogprobGradArgs
     for (; v + kGU * kGT <= v1; v += kGU * kGT) {
       uint4 w[kGU];
 #pragma unroll
-      for (int u = 0; u < kGU; ++u) w[u] = __ldg(xv + v + u * kGT + tid);
+      for (int u = 0; u < kGU; ++u) w[u] = xv[v + u * kGT + tid];   // (out may be x)
 #pragma unroll
       for (int u = 0; u < kGU; ++u) ov[v + u * kGT + tid] = turn(w[u]);
     }

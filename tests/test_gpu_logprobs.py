@@ -174,6 +174,33 @@ def test_largest_and_smallest_logits(V):
         assert got.top_ids[1].tolist() == [0, 1] and V.get_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_masks_of_the_lowest_value(V, dtype):
+    # beside entries of -inf, in rows with and without others; and references near the end
+    # of the type, where distances over T pass 32 bits
+    low, n = torch.finfo(dtype).min, 9000
+    x = (torch.randn(6, n, generator=gen(11), device="cuda") * 2).to(dtype)
+    x[0, ::2], x[0, 1::4] = low, -math.inf
+    x[1], x[1, 100:6000] = low, -math.inf
+    x[2, :7000], x[2, ::3] = low, -math.inf
+    x[3, 17] = -low
+    x[4, 4000:], x[4, 9] = -math.inf, -low
+    x[5], x[5, 5000], x[5, 5001] = low, -low, -low
+    for T in (1.0, 0.01, 1e-10, 100.0):
+        got = V.logprobs(x, i32([3, 50, 8999, 17, 9, 5001]), T=T, top=2)
+        grad = V.logprobs_grad(x, i32([3, 50, 8999, 17, 9, 5001]), got, grad_logprob=torch.ones(6, device="cuda"),
+                               grad_entropy=torch.ones(6, device="cuda"), T=T)
+        assert V.get_error() == 0 and grad.isfinite().all()
+        flat = math.log(n - 5900)
+        want = torch.tensor([-flat, 0, 0, -math.log(2)], device="cuda")
+        ent = torch.tensor([flat, 0, 0, math.log(2)], device="cuda")
+        rows = torch.tensor([1, 3, 4, 5], device="cuda")
+        assert ((got.logprob[rows] - want).abs() <= 1e-5).all() and ((got.entropy[rows] - ent).abs() <= 1e-4).all()
+        assert got.top_ids[5].tolist() == [5000, 5001] and got.top_ids[3, 0] == 17
+    check(V, x[[0, 2]], i32([3, 8999]), T=1.0, top=5)
+    check(V, x[[0, 2]], i32([3, 8999]), T=0.5, top=0)
+
+
 def test_rows_shared_missing_and_out_of_range(V):
     x = torch.randn(10, 4000, generator=gen(4), device="cuda").to(BF)
     rows, ids = i32([3, 3, 9, 0, 3]), i32([5, 6, 3999, 0, 5])
