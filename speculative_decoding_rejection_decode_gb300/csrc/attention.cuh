@@ -27,6 +27,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/specdec.h"
 #include "cache.cuh"
@@ -195,105 +196,112 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
 // becomes zeros.
 constexpr float kLostRow = -INFINITY;
 
-// Workspace: two partial slots per range, each R rows of D sums, then (max, sum).
-// A range may go on with an item that began earlier (slot 0) and leave another to
-// the next range (slot 1).
+// An item that range i leaves unfinished: what the join needs of it.
+struct alignas(16) OpenItem {
+  int64_t first;       // node row of its request
+  int64_t end, units;  // its last unit + 1; units of the call
+  int32_t rows, h, rt; // rows of its request (nodes x group), kv head, row tile
+  int32_t ranges;      // of the call; 0: the range leaves none
+};
+
+// Workspace: two partial slots per range, each R rows of D sums, then (max, sum); then what
+// the range leaves.  A range may go on with an item that began earlier (slot 0) and leave
+// another to the next range (slot 1).
 template <int R, int D>
 struct Partials {
   float* sums;
   float2* stats;
+  OpenItem* open;
   __host__ __device__ Partials(void* ws, int G)   // from a multiple of 32 bytes: rows are stored 32 at a time
       : sums(reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~(uintptr_t)31)),
-        stats(reinterpret_cast<float2*>(sums + (int64_t)2 * G * R * D)) {}
-  static constexpr int64_t bytes(int G) { return (int64_t)2 * G * R * (D * 4 + 8) + 32; }
+        stats(reinterpret_cast<float2*>(sums + (int64_t)2 * G * R * D)),
+        open(reinterpret_cast<OpenItem*>(stats + (int64_t)2 * G * R)) {}
+  static constexpr int64_t bytes(int G) { return (int64_t)2 * G * R * (D * 4 + 8) + G * (int64_t)sizeof(OpenItem) + 32; }
 };
 
-// Joins the partial results of the items that several ranges share.  An item
-// whose first tile is in range i - 1 and that goes on into range i belongs to blocks (i, *);
-// block (i, y) takes 8 of its rows, a warp two of them.
-template <typename T, int R, int TK, int D>
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, const int G) {
-  __shared__ ScanShared sh;
-  const int group = a.q_heads / a.c.geo.kv_heads;
-  const PlanArgs plan(a);
-  uint32_t why = 0;
-  int64_t u = 0;
-  int ranges = 0;
-  find_unit<128>(plan, R, TK,
-                 [&](int64_t units) {
-                   ranges = (int)min((int64_t)G, units);
-                   u = (int)blockIdx.x + 1 < ranges ? range_begin(units, ranges, blockIdx.x + 1) : units;
-                   return u;
-                 },
-                 sh, why);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if ((int)blockIdx.x + 1 >= ranges || sh.b < 0) return;
-  const int g0 = blockIdx.x;                     // the range before the boundary
-  const Request q = attend_request(plan, sh.b, R, TK, why);
-  if (q.units == 0) return;
-  const int64_t item = (u - sh.before) / (q.tiles + plan.item_cost);
-  const int64_t u0 = sh.before + item * (q.tiles + plan.item_cost) + plan.item_cost, u1 = u0 + q.tiles;   // its tiles
-  // not an item that begins at the boundary, nor one that range g0 also went on with
-  if (u0 >= u || range_begin(sh.total, ranges, g0) > u0) return;
-  const int h = (int)(item / q.rts), rt = (int)(item % q.rts);
-  const int g1 = range_of(sh.total, ranges, u1 - 1);
+// Joins the partial results of the items that several ranges share.  What range g leaves
+// unfinished belongs to blocks (g, *), of 16 rows each, a warp four of them.  No more
+// than this is done behind the attention kernel, whose ranges end together: with the plan
+// walked again here, and rows in turns, the join took 19 us of 207 (8-bit states, 32
+// requests of 29 nodes, 1500 to 12000 states), this form 13; the warp kernel's is hidden
+// by the launch.
+template <typename T, int R, int D>
+__global__ void __launch_bounds__(128, 8) attend_join_kernel(const AttendArgs a, const int G) {
+  constexpr int J = 4, U = 2, PER = D / 32;      // rows of a warp, partials under way together
+  using V = typename std::conditional<PER == 4, float4, float2>::type;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.q_heads / a.c.geo.kv_heads;
   const Partials<R, D> part(a.workspace, G);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = q.n * group;
-  constexpr int PER = D / 32;
-  for (int r = blockIdx.y * 8 + warp; r < (int)blockIdx.y * 8 + 8; r += 4) {
-    const int row = rt * R + r;
-    if (row >= rows) break;
-    // range g0 left the item in its second slot, the others began inside it
-    const int64_t at0 = (2 * (int64_t)g0 + 1) * R + r;
-    auto at_of = [&](int g) { return g == g0 ? at0 : 2 * (int64_t)g * R + r; };
-    float m = -INFINITY;
-    bool gone = false;
-    for (int g = g0 + lane; g <= g1; g += 32) {
-      const float2 s = part.stats[at_of(g)];
-      m = fmaxf(m, s.x);
-      gone |= s.y == kLostRow;
-    }
-    m = warp_max(m);
-    gone = __any_sync(0xFFFFFFFFu, gone);
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, acc[PER];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const OpenItem it = part.open[blockIdx.x];
+  if (it.ranges == 0) return;
+  const int g0 = blockIdx.x, g1 = range_of(it.units, it.ranges, it.end - 1), r0 = (int)blockIdx.y * 16 + warp * J;
+  const int live = min(J, it.rows - (it.rt * R + r0));
+  if (live <= 0) return;
+  // range g0 left the item in its second slot, the others began inside it
+  auto at_of = [&](int g, int j) { return (2 * (int64_t)g + (g == g0 ? 1 : 0)) * R + r0 + j; };
+  V v[U][J];
+  auto fetch = [&](int g) {
 #pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] = 0.0f;
-    constexpr int U = 4;
-    for (int g = g0; g <= g1; g += U) {      // four partials' loads under way together
-      float2 s[U];
-      float v[U][PER];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        s[u] = make_float2(-INFINITY, 0.0f);
-        if (g + u <= g1) {
-          const int64_t at = at_of(g + u);
-          s[u] = part.stats[at];
-          const float* p = part.sums + at * D + lane * PER;
-          if constexpr (PER == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(p);
-            v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(p);
-            v[u][0] = x.x; v[u][1] = x.y;
-          }
+      for (int j = 0; j < J; ++j) {
+        v[u][j] = V{};
+        if (g + u <= g1 && j < live) v[u][j] = *reinterpret_cast<const V*>(part.sums + at_of(g + u, j) * D + lane * PER);
+      }
+  };
+  fetch(g0);
+  // lane 8 j + p looks after row j in every eighth range
+  const int mine = lane >> 3, p = lane & 7;
+  auto stat = [&](int g) { return g <= g1 && mine < live ? part.stats[at_of(g, mine)] : make_float2(-INFINITY, 0.0f); };
+  float m = -INFINITY, l = 0.0f, acc[J][PER];
+  int gone = 0;
+  for (int g = g0 + p; g <= g1; g += 8) {
+    const float2 s = stat(g);
+    m = fmaxf(m, s.x);
+    gone |= s.y == kLostRow;
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    gone |= __shfl_xor_sync(0xFFFFFFFFu, gone, o);
+  }
+  if (m == -INFINITY) m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[j][k] = 0.0f;
+  for (int c = g0; c <= g1; c += 8) {
+    const float2 s = stat(c + p);
+    float w = ex2(s.x - m);
+    l += s.y * w;
+    if (s.x == -INFINITY) w = -1.0f;             // nothing there: its sums are not looked at
+    for (int i = 0; i < 8 && c + i <= g1; i += U) {
+      if (c + i > g0) fetch(c + i);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const float by = __shfl_sync(0xFFFFFFFFu, w, j * 8 + i + u);
+          const float* x = reinterpret_cast<const float*>(&v[u][j]);
+#pragma unroll
+          for (int k = 0; k < PER; ++k) acc[j][k] += by < 0.0f ? 0.0f : x[k] * by;
         }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float w = ex2(s[u].x - ref);
-        l += s[u].y * w;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] += s[u].x == -INFINITY ? 0.0f : v[u][k] * w;
-      }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+  const float inv_mine = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const float inv = __shfl_sync(0xFFFFFFFFu, inv_mine, j * 8);
+    const int lost = __shfl_sync(0xFFFFFFFFu, gone, j * 8);
+    if (j >= live) break;
+    const int row = it.rt * R + r0 + j;
     T* out = static_cast<T*>(a.out) +
-             ((q.first + row / group) * a.q_heads + h * group + row % group) * (int64_t)D + lane * PER;
+             ((it.first + row / group) * a.q_heads + it.h * group + row % group) * (int64_t)D + lane * PER;
 #pragma unroll
     for (int k = 0; k < PER; k += 2)
-      *reinterpret_cast<uint32_t*>(out + k) = gone ? 0u : pack2(acc[k] * inv, acc[k + 1] * inv, T());
+      *reinterpret_cast<uint32_t*>(out + k) = lost ? 0u : pack2(acc[j][k] * inv, acc[j][k + 1] * inv, T());
   }
 }
 
@@ -311,10 +319,10 @@ bool allow_shared(K kern, int bytes, std::atomic<uint64_t>& done) {
 }
 
 // Queues the join as a dependent of the attention kernel before it.
-template <typename T, int R, int TK, int D>
+template <typename T, int R, int D>
 int launch_join(const AttendArgs& a, int G, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)G, R / 8);
+  cfg.gridDim = dim3((unsigned)G, R / 16);
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -322,7 +330,7 @@ int launch_join(const AttendArgs& a, int G, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, R, TK, D>, a, G) == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, R, D>, a, G) == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
 #endif  // __CUDACC__

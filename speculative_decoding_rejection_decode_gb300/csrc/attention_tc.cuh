@@ -267,6 +267,12 @@ __device__ __forceinline__ void next_segment(Segments* s, const PlanArgs c) {
   s->more = true;
 }
 
+// Leaves a segment's item to the join if it begins here and goes on.
+__device__ __forceinline__ void leave_open(OpenItem* open, const Segments& s, int64_t units, int G, int group) {
+  if (s.whole || s.t0 > 0) return;
+  open[blockIdx.x] = {s.q.first, s.base + s.u, units, s.q.n * group, s.h, s.rt, (int)min((int64_t)G, units)};
+}
+
 inline decltype(&cuTensorMapEncodeTiled) tensor_map_encoder() {
   using Encode = decltype(&cuTensorMapEncodeTiled);
   static const Encode encode = [] {

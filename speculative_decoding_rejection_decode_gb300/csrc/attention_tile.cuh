@@ -23,10 +23,10 @@
 // The two groups' results are joined when a segment ends.
 //
 // Measured (32 or 64 query and 8 kv heads of 128): bf16, 2 to 9 nodes over up to 8191
-// keys, 64 requests, 1.30 GB in 217 us = 6.0 TB/s; 8 nodes over 100k and 131k keys 947
-// MB in 158 us = 6.0 TB/s: bound by memory.  e4m3, 29 nodes over 6000 to 16000 keys, 32
-// requests: 805 MB and 177 GFLOP in 300 us, bound by the chain of roles that a tile
-// passes (its scores, exponentials, weights and values widened: no unit above 37 % of
+// keys, 64 requests, 1.30 GB in 210 us = 6.2 TB/s; 8 nodes over 100k and 131k keys 947
+// MB in 157 us = 6.0 TB/s: bound by memory.  e4m3, 29 nodes over 6000 to 16000 keys, 32
+// requests: 805 MB and 177 GFLOP in 261 us, bound by the chain of roles that a tile
+// passes (its scores, exponentials, weights and values widened: no unit above 41 % of
 // its rate, the softmax's and finishers' instructions the largest part).
 //
 // 8-bit keys meet the queries in e4m3 products: a query is the sum of two (f16:
@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                           },
                           scan, why);
   if (blockIdx.x == 0 && why) atomicOr(c.err, why);
+  if (tid == 0 && !a.whole) Partials<kR, D>(a.workspace, G).open[blockIdx.x].ranges = 0;
   asm volatile("griddepcontrol.launch_dependents;");
   const int64_t units = scan.total;
   const int ranges = (int)min((int64_t)G, units);
@@ -994,7 +995,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       tc_fence_before();
       named_bar_sync(1, kSoftmaxThreads);   // the sums are read before queries lie over them
-      if (sid == 0) next_segment<kR>(&seg, plan);
+      if (sid == 0) {
+        leave_open(part.open, seg, scan.total, G, group);
+        next_segment<kR>(&seg, plan);
+      }
       named_bar_sync(1, kSoftmaxThreads);
       tile0 += n;
       ++g;
@@ -1033,7 +1037,7 @@ int launch_tile(const AttendArgs& a, int num_sms, cudaStream_t st) {
   if (box && (!encode_rows(&kmap, a.c.k, rows, D, box, FP8) || !encode_rows(&vmap, a.c.v, rows, D, box, FP8))) box = 0;
   kern<<<num_sms, kTileThreads, bytes, st>>>(a, box, grouped && box > 0, kmap, vmap);
   if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  return a.whole ? SPECDEC_OK : launch_join<T, kR, kTK, D>(a, num_sms, st);
+  return a.whole ? SPECDEC_OK : launch_join<T, kR, D>(a, num_sms, st);
 }
 
 template <bool CROSS, typename T, bool FP8>

@@ -158,12 +158,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
                       },
                       scan, why);
   if (blockIdx.x == 0 && why) atomicOr(c.err, why);
+  const Partials<R, D> part(a.workspace, G);
+  if (tid == 0 && !a.whole) part.open[blockIdx.x].ranges = 0;
   asm volatile("griddepcontrol.launch_dependents;");
   const int64_t units = scan.total;
   const int ranges = (int)min((int64_t)G, units);
   if ((int)blockIdx.x >= ranges || scan.b < 0) return;
   const int64_t uend = range_begin(units, ranges, blockIdx.x + 1);
-  const Partials<R, D> part(a.workspace, G);
   char* ring = smem + warp * (kStages * W::STAGE);
   const uint32_t ring_s = smem_addr(ring);
   const uint32_t q_s = smem_addr(smem + L::Q);
@@ -557,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
     }
     __syncthreads();
     const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 > 0 ? 0 : 1);
+    if (!whole && t0 == 0 && tid == 0) part.open[blockIdx.x] = {q.first, now.u, units, q.n * group, h, rt, ranges};
     for (int x = tid; x < rows * (D / 2); x += kThreads) {
       const int r = x / (D / 2), i = x % (D / 2), nt = i / 4;
       const int d = FP8 ? (nt >> 1) * 16 + i % 4 * 4 + (nt & 1) : 2 * i;
@@ -599,14 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
 template <bool CROSS, typename T, bool FP8, int D>
 int launch_warp(const AttendArgs& a, int num_sms, cudaStream_t st) {
   using L = WarpLayout<FP8, D, kRowsTile>;
-  constexpr int TK = WarpTile<FP8, D>::TK;
   auto kern = attend_warp_kernel<T, FP8, D, CROSS>;
   static std::atomic<uint64_t> done{0};
   if (!allow_shared(kern, L::BYTES, done)) return SPECDEC_ERR_CUDA;
   const int G = num_sms;
   kern<<<G, kThreads, L::BYTES, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  return a.whole ? SPECDEC_OK : launch_join<T, kRowsTile, TK, D>(a, G, st);
+  return a.whole ? SPECDEC_OK : launch_join<T, kRowsTile, D>(a, G, st);
 }
 
 template <bool CROSS, typename T, bool FP8>

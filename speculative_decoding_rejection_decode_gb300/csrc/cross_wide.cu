@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                           },
                           scan, why);
   if (blockIdx.x == 0 && why) atomicOr(c.err, why);
+  if (tid == 0 && !a.whole) Partials<kWideR, D>(a.workspace, G).open[blockIdx.x].ranges = 0;
   asm volatile("griddepcontrol.launch_dependents;");
   const int64_t units = scan.total;
   const int ranges = (int)min((int64_t)G, units);
@@ -426,7 +427,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (lane == 0) mbar_arrive(smem_addr(&sh.v_full[n % L::VS]));
       if (++t == seg.t1) {
         __syncwarp();
-        if (lane == 0) next_segment<kWideR>(&seg, plan);
+        if (lane == 0) {
+          leave_open(Partials<kWideR, D>(a.workspace, G).open, seg, scan.total, G, group);
+          next_segment<kWideR>(&seg, plan);
+        }
         __syncwarp();
         t = seg.t0;
       }
@@ -594,7 +598,7 @@ int launch_wide(const AttendArgs& a, int box, int num_sms, cudaStream_t st) {
   const bool qbox = kR % group == 0 && a.scale_log2 >= 0.0f && encode_queries(&qmap, a, D, group);
   kern<<<num_sms, kWideThreads, bytes, st>>>(a, box, qbox, kmap, vmap, qmap);
   if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  return a.whole ? SPECDEC_OK : launch_join<T, kWideR, kTK, D>(a, num_sms, st);
+  return a.whole ? SPECDEC_OK : launch_join<T, kWideR, D>(a, num_sms, st);
 }
 
 }  // namespace
