@@ -27,7 +27,8 @@
 // MB in 157 us = 6.0 TB/s: bound by memory.  e4m3, 29 nodes over 6000 to 16000 keys, 32
 // requests: 805 MB and 177 GFLOP in 261 us, bound by the chain of roles that a tile
 // passes (its scores, exponentials, weights and values widened: no unit above 41 % of
-// its rate, the softmax's and finishers' instructions the largest part).
+// its rate over 29 rows and 6000 states each, the softmax's and finishers' instructions
+// the largest part).
 //
 // 8-bit keys meet the queries in e4m3 products: a query is the sum of two (f16:
 // three) e4m3 parts of 4 bits each, q = hi + lo (+ lo2), which hold bf16's 8 (f16's
