@@ -293,8 +293,9 @@ int specdec_rejection_sample_given(specdec_handle_t h, const float* target_probs
  *                     what specdec_logprobs_grad needs of the row
  *   logits      device rows of V entries of `dtype` (SPECDEC_F32, _BF16 or _F16),
  *               row_stride elements apart (>= V), num_rows of them, of any alignment
- *   T           temperature, 2^-60 .. 2^60; finite logits lie below 2^60 T and 2^120
- *               in magnitude
+ *   T           temperature, 2^-60 .. 2^60; logits may be any finite numbers (the type's
+ *               lowest, as a mask): an entry so far below that its distance over T
+ *               passes 32 bits has ln p = -inf
  *   ids         device [n_tokens], or NULL: no given tokens (then out_logprob is
  *               NULL).  A token whose id is below 0 is skipped: its row is not read,
  *               its numbers are 0 and its alternatives -1 (specdec_rejection_sample

@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_warp_kernel(const AttendAr
           if constexpr (CROSS) return true;
           const int64_t j = key0 + key - q.len;
           if (j < 0) return true;
-          if (r >= rows) return false;
+          if (r >= rows || j >= q.n) return false;   // (j: where lengths change under the call)
           const int node = (rt * R + r) / group;
           return parent ? (anc[(node - node0) * words + (int)(j >> 5)] >> (j & 31)) & 1u : j <= node;
         };

@@ -197,6 +197,55 @@ def test_positions_and_offsets_that_say_what_slots_say(V, tree, cache):
     assert not torch.equal(moved[0], plain[0]) and torch.equal(moved[2], plain[2])
 
 
+@pytest.mark.parametrize("cache", [BF, E4])
+def test_append_in_place_and_captured(V, cache):
+    from speculative_decoding_rejection_decode_gb300 import rotary_axes, rotary_table
+    table, axes = rotary_table(300, 128), rotary_axes((24, 20, 20))
+    steps = [Step(ctx=[9, 70, 0], nodes=[33, 20, 5], cache=cache, seed=40 + i) for i in range(2)]
+    pos = [torch.randint(0, 300, (3, s.N), generator=torch.Generator("cuda").manual_seed(i), device="cuda", dtype=torch.int32)
+           for i, s in enumerate(steps)]
+    run = lambda s, p, q, **kw: s.cache(V).append(s.new_k, s.new_v, *args(s), q=q, rotary=table, positions=p, axes=axes, **kw)
+    want = []
+    for s, p in zip(steps, pos):
+        q = run(s, p, s.q)
+        want.append((q, *s.cache(V).read(*args(s)[:2], s.cu, n_rows=s.n_rows)))
+        own = s.q.clone()
+        assert torch.equal(run(s, p, own, out_q=own), q) and torch.equal(own, q)
+        s.k.zero_(), s.v.zero_()
+    graphs = []
+    for s, p in zip(steps, pos):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            q = run(s, p, s.q)
+            out = (q, *s.cache(V).read(*args(s)[:2], s.cu, n_rows=s.n_rows))
+        graphs.append((g, out, torch.cuda.Stream()))
+    for _ in range(5):
+        for g, _out, st in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_g, out, _st), w in zip(graphs, want):
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
+    assert V.get_error() == 0
+
+
+@pytest.mark.parametrize("heads,D,rotary", [(1, 1024, 128), (1, 16, 16), (300, 16, 16), (2, 24, 16), (3, 136, 128)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotate_few_and_many_pieces(V, heads, D, rotary, inter):
+    from speculative_decoding_rejection_decode_gb300 import rotary_table
+    g = torch.Generator("cuda").manual_seed(heads + D)
+    x = torch.randn(700, heads, D, generator=g, device="cuda").to(BF)
+    pos = torch.randint(0, 50, (700,), generator=g, device="cuda", dtype=torch.int32)
+    table = rotary_table(50, rotary)
+    want = plain_turn(x, pos[None], (0,) * (rotary // 2), table, inter).to(BF)
+    assert torch.equal(V.rotate(x, pos, table, interleaved=inter), want)
+    assert torch.equal(V.rotate(x, pos, table, interleaved=inter, out=x), want) and V.get_error() == 0
+    # one row for many: a broadcast input
+    wide = x[:1].expand(700, heads, D)
+    want = plain_turn(wide, pos[None], (0,) * (rotary // 2), table, inter).to(BF)
+    assert torch.equal(V.rotate(wide, pos, table, interleaved=inter), want) and V.get_error() == 0
+
+
 def test_rows_with_bad_positions_are_left_out(V):
     from speculative_decoding_rejection_decode_gb300 import rotary_table
     table = rotary_table(100, 128)
