@@ -8,14 +8,20 @@
 //
 // An item also counts item_cost units of its own: starting and ending it (queries,
 // an empty pipeline, results) takes about as long as that many tiles, and without
-// them the ranges that hold many short requests finished late.  us at a cost of 2, 4,
-// 5, 6 (32 query and 8 kv heads of 128): tile kernel, 64 requests of 2 to 9 nodes over up
-// to 8191 keys, bf16 237, 221, 219, 216; 32 of 29 over 6000 to 16000, e4m3 303, 298, 296,
-// 296; warp kernel at a cost of 1, 2, 3, 5, 64 of 1 over up to 8191, bf16 193, 183, 180,
-// 180; 200 of 1 to 4 over up to 1500, bf16 182, 170, 157, 151; 64 of 2 to 9 over up to
-// 2047, 32 kv heads, bf16 300, 256, 236, 216 (at 7 and more it rises again); e4m3 at 2, 3,
-// 4, 6: 178, 183, 185, 191; 173, 179, 183, 191; 258, 259, 269, 286 (its tiles are of 256
-// keys and take longer).
+// them the ranges that hold many short requests finished late.  us (32 query heads of 128;
+// requests of rows over keys or states, 8 kv heads unless said):
+//   tile, 16 bits, cost 2, 3, 5, 8: 64 of 2-9 over up to 8191 227, 219, 210, 211
+//   tile, 8 bits, 5, 8, 10, 12, 16: 32 of 29 over 1500-12000 202, 188, 186, 185, 188; 64 of 2-9
+//     over up to 8191 208, 193, 195, 198, 201; 200 of 5-29 over up to 1500 225, 218, 216, 218,
+//     224; 32 of 29 over 6000-16000 262, 257, 255, 255, 258
+//   wide, 2, 3, 4, 5, 7: 8 of 1000-2048 over 1500-4096 464, 441, 443, 448, 448; 64 of 100-200
+//     over 500-2000 252, 251, 249, 253, 252; 30 of 200-900 over 100-700 (16 kv heads of 64)
+//     110, 107, 106, 107, 108
+//   warp, 16 bits, 1, 2, 3, 5: 64 of 1 over up to 8191 193, 183, 180, 180; 200 of 1-4 over up to
+//     1500 182, 170, 157, 151; 64 of 2-9 over up to 2047 (32 kv heads) 300, 256, 236, 216
+//     (at 7 and more it rises again)
+//   warp, 8 bits, 2, 3, 4, 6: 178, 183, 185, 191; 173, 179, 183, 191; 258, 259, 269, 286 (its
+//     tiles are of 256 keys and take longer)
 //
 // Rows of an item: r = node * group + head within the group, so one read of a
 // key serves every node and every query head that shares it.
@@ -36,6 +42,8 @@
 namespace specdec {
 
 constexpr int kItemCost = 5;       // units of an item's own
+constexpr int kItemCostTile8 = 10;  // in the tile kernel over 8-bit caches
+constexpr int kItemCostWide = 4;    // in the wide kernel
 constexpr int kItemCostWarp8 = 2;  // the same in the warp kernel over 8-bit caches
 
 struct Request {

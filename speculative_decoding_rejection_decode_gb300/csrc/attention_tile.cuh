@@ -25,7 +25,7 @@
 // Measured (32 or 64 query and 8 kv heads of 128): bf16, 2 to 9 nodes over up to 8191
 // keys, 64 requests, 1.30 GB in 210 us = 6.2 TB/s; 8 nodes over 100k and 131k keys 947
 // MB in 157 us = 6.0 TB/s: bound by memory.  e4m3, 29 nodes over 6000 to 16000 keys, 32
-// requests: 805 MB and 177 GFLOP in 261 us, bound by the chain of roles that a tile
+// requests: 805 MB and 177 GFLOP in 255 us, bound by the chain of roles that a tile
 // passes (its scores, exponentials, weights and values widened: no unit above 41 % of
 // its rate over 29 rows and 6000 states each, the softmax's and finishers' instructions
 // the largest part).

@@ -21,7 +21,7 @@
 //
 // Measured (32 query and 8 kv heads of 128, bf16): 8 requests of 1536 rows over 2816 states
 // 566 GFLOP in 410 to 430 us = 1.3 PFLOP/s, the tensor pipe busy for 57 % of it; of 1000 to
-// 2048 rows over 1500 to 4096 states 1.17.  Bound by a group's scores, exponentials and
+// 2048 rows over 1500 to 4096 states 1.18.  Bound by a group's scores, exponentials and
 // weights in turn with its products; neither unit is full.
 #include "attention_tc.cuh"
 
