@@ -23,9 +23,9 @@
 // The two groups' results are joined when a segment ends.
 //
 // Measured (32 or 64 query and 8 kv heads of 128): bf16, 2 to 9 nodes over up to 8191
-// keys, 64 requests, 1.30 GB in 210 us = 6.2 TB/s; 8 nodes over 100k and 131k keys 947
+// keys, 64 requests, 1.30 GB in 208 us = 6.25 TB/s; 8 nodes over 100k and 131k keys 947
 // MB in 157 us = 6.0 TB/s: bound by memory.  e4m3, 29 nodes over 6000 to 16000 keys, 32
-// requests: 805 MB and 177 GFLOP in 255 us, bound by the chain of roles that a tile
+// requests: 805 MB and 177 GFLOP in 253 us, bound by the chain of roles that a tile
 // passes (its scores, exponentials, weights and values widened: no unit above 41 % of
 // its rate over 29 rows and 6000 states each, the softmax's and finishers' instructions
 // the largest part).
@@ -210,17 +210,18 @@ __device__ __noinline__ void left_out(const CacheArgs& c, const Segments& s, int
 }
 
 // One tile's scores of this thread's row become weights: one pass, kW keys at a time.
-// Weights are 2^(e - m), m a whole number that follows the running maximum only when
+// Weights are 2^(e - m), m the first maximum (so that a row that sees one key gets its
+// values as they are), which follows the running maximum by whole numbers and only when
 // that is kLazy above it: what has been summed, the row's O_w (`summed`: there is
-// one) and the tile's weights so far are then multiplied by a power of two, which is
-// exact.  The largest weight lies in [2^kHead, 2^(kHead + kLazy)]: f16 weights keep
+// one) and the tile's weights so far are then multiplied by a power of two, which
+// loses nothing.  The largest weight lies in [2^kHead, 2^(kHead + kLazy)]: f16 weights keep
 // their bits far below the largest, and the maximum may lag by 2^kLazy.
 template <typename T, bool FP8, int D, bool WIDE>
 __device__ __forceinline__ void tile_scores(uint32_t ts, uint32_t to, uint32_t base_s, int f, const float* vexp,
                                             const uint32_t* bits, bool masked, float rowf, bool summed, float& m, float& l) {
   using L = TileLayout<T, FP8, D>;
   using E = typename std::conditional<FP8, __half, T>::type;
-  constexpr float kLazy = 8.0f;
+  constexpr float kLazy = 9.0f;     // (8: 180 us where 9 took 175, 32 requests of 29 rows, 1500 to 12000 8-bit states)
   constexpr float kHead = std::is_same<E, __half>::value ? 6.0f : 0.0f;
 #pragma unroll 1
   for (int i = 0; i < kTK / kW; ++i) {
@@ -266,7 +267,7 @@ __device__ __forceinline__ void tile_scores(uint32_t ts, uint32_t to, uint32_t b
     const float most = mx == -INFINITY ? mx : fmaf(mx, of, shift);
     const bool move = most > m + kLazy || (m == -INFINITY && most != -INFINITY);
     if (__any_sync(0xFFFFFFFFu, move)) {
-      const float to_m = move ? ceilf(most) : m;
+      const float to_m = !move ? m : m == -INFINITY ? most : m + ceilf(most - m);
       const float fix = move ? ex2(m - to_m) : 1.0f;
       m = to_m;
       if (summed || i > 0) {
@@ -548,6 +549,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       Segments& seg = segs[3 + loader];
       int skip = loader, t = seg.t0;            // tiles of others before this loader's next
+      // The next item's queries on their way to L2 while this one's last tiles are worked on:
+      // 32 requests of 29 rows over 1500 to 12000 8-bit states 184 to 178 us, 64 of 2 to 9 over
+      // up to 8191 195 to 179 (but the 8-bit attention over context and nodes 255 to 271, whose
+      // roles' code is the longest: it goes without).
+      auto fetch_queries = [&](const Segments& s) {
+#pragma unroll 1
+        for (int i = lane; i < s.rows * (D / 64); i += 32) {
+          const int gr = s.rt * kR + i / (D / 64);
+          const T* src = static_cast<const T*>(a.q) + (s.q.first + gr / group) * a.q_row + (int64_t)(s.h * group + gr % group) * a.q_head + i % (D / 64) * 64;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+        }
+      };
       auto go = [&](Place& x) -> bool {         // this loader's next tile
         t += skip;
         while (seg.more && t >= seg.t1) {
@@ -556,6 +569,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (lane == 0) next_segment<kR>(&seg, plan);
           __syncwarp();
           t = seg.t0 + over;
+          if ((CROSS || !FP8) && loader == 0 && seg.more) fetch_queries(seg);
         }
         if (!seg.more) return false;
         skip = kLoaders;

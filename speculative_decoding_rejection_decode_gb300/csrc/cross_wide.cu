@@ -21,7 +21,7 @@
 //
 // Measured (32 query and 8 kv heads of 128, bf16): 8 requests of 1536 rows over 2816 states
 // 566 GFLOP in 410 to 430 us = 1.3 PFLOP/s, the tensor pipe busy for 57 % of it; of 1000 to
-// 2048 rows over 1500 to 4096 states 1.18.  Bound by a group's scores, exponentials and
+// 2048 rows over 1500 to 4096 states 1.2.  Bound by a group's scores, exponentials and
 // weights in turn with its products; neither unit is full.
 #include "attention_tc.cuh"
 
@@ -102,16 +102,20 @@ __device__ __noinline__ void rescale(uint32_t ts, uint32_t to, int parts, bool s
   }
 }
 
+// The reference of a row whose maximum has left the old one (-inf: none) behind.
+__device__ __noinline__ float follow(float m, float most) { return m == -INFINITY ? most : m + ceilf(most - m); }
+
 // A tile's scores of this thread's row become weights 2^(e - m), rounded to 16 bits for the
 // product with V (half a step each at most) and summed unrounded, 32 at a time; the
-// maximum of the next 32 is found beside the exponentials of these.  The reference m, a
-// whole number, follows the maximum only where that has passed it by kLazy: what has been
-// summed is then multiplied by a power of two, exactly.  (Handing on the first 96 keys'
+// maximum of the next 32 is found beside the exponentials of these.  The reference m, the
+// first maximum (so that a row that sees one state gets its values as they are), follows the
+// maximum by whole numbers and only where that has passed it by kLazy: what has been summed
+// is then multiplied by a power of two.  (Handing on the first 96 keys'
 // weights before the last 32 gained nothing.)
 template <typename T, int D, bool MASKED>
 __device__ __forceinline__ void tile_weights(uint32_t ts, uint32_t to, uint4 live, float rowf, bool summed,
                                              float& m, float& l, uint64_t* sum) {
-  constexpr float kLazy = 8.0f;
+  constexpr float kLazy = 9.0f;   // (8: 456 us where 9 took 434, 8 requests of 1000 to 2048 rows, 1500 to 4096 states)
   constexpr float kHead = std::is_same<T, __half>::value ? 6.0f : 0.0f;   // f16 weights keep their bits
   const uint64_t rowf2 = pair(rowf, rowf);
   uint32_t s[2][32];
@@ -134,7 +138,7 @@ __device__ __forceinline__ void tile_weights(uint32_t ts, uint32_t to, uint4 liv
     const float most = mx == -INFINITY ? mx : mx * rowf;
     const bool move = most > m + kLazy || (m == -INFINITY && most != -INFINITY);
     if (__any_sync(0xFFFFFFFFu, move)) {
-      const float to_m = move ? ceilf(most) : m;
+      const float to_m = move ? follow(m, most) : m;
       const float fix = move ? ex2(m - to_m) : 1.0f;
       m = to_m;
       l *= fix;

@@ -230,6 +230,22 @@ def test_infinite_values_reach_the_rows_that_see_them(V, nodes, kv):
     assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("rows,heads", [(1, {}), (20, {}), (300, {}), (300, MANY)])
+def test_a_row_that_sees_one_state_is_its_values(V, dtype, rows, heads):
+    # a weight of one, whatever the score
+    s = make([1, 40, 200], [rows] * 3, 0.0, dtype=dtype, cache=dtype, seed=13, **heads)
+    for b, slot in enumerate((0, 39, 130)):
+        s.mask[b] = False
+        s.mask[b, slot] = True
+    out = s.cache(V).cross_attend(s.q, s.table, s.lengths, s.cu, mask=s.mask)
+    assert V.get_error() == 0
+    for b, slot in enumerate((0, 39, 130)):
+        page, off = s.row(b, slot)
+        want = s.v[page, :, off].repeat_interleave(s.group, 0)
+        assert (out[b * rows:(b + 1) * rows] == want).all()
+
+
 def test_one_large_request_among_small_ones(V):
     s = make([3000, 50, 50, 50, 50], [900, 1, 1, 1, 1], kv_heads=2, group=1, seed=10)
     check(V, s)
