@@ -23,8 +23,8 @@
 // The two groups' results are joined when a segment ends.
 //
 // Measured (32 or 64 query and 8 kv heads of 128): bf16, 2 to 9 nodes over up to 8191
-// keys, 64 requests, 1.30 GB in 208 us = 6.25 TB/s; 8 nodes over 100k and 131k keys 947
-// MB in 157 us = 6.0 TB/s: bound by memory.  e4m3, 29 nodes over 6000 to 16000 keys, 32
+// keys, 64 requests, 1.30 GB in 205 us = 6.3 TB/s; 8 nodes over 100k and 131k keys 947
+// MB in 156 us = 6.1 TB/s: bound by memory.  e4m3, 29 nodes over 6000 to 16000 keys, 32
 // requests: 805 MB and 177 GFLOP in 253 us, bound by the chain of roles that a tile
 // passes (its scores, exponentials, weights and values widened: no unit above 41 % of
 // its rate over 29 rows and 6000 states each, the softmax's and finishers' instructions
@@ -221,7 +221,10 @@ __device__ __forceinline__ void tile_scores(uint32_t ts, uint32_t to, uint32_t b
                                             const uint32_t* bits, bool masked, float rowf, bool summed, float& m, float& l) {
   using L = TileLayout<T, FP8, D>;
   using E = typename std::conditional<FP8, __half, T>::type;
-  constexpr float kLazy = 9.0f;     // (8: 180 us where 9 took 175, 32 requests of 29 rows, 1500 to 12000 8-bit states)
+  // f16 ends at 2^16.  8-bit caches, 8 and 9: 180 and 175 us, 32 requests of 29 rows over 1500
+  // to 12000 states; bf16 weights, 9 and 16: 208 and 205, 64 of 2 to 9 over up to 8191 keys
+  // (sums of values below 2^90 stay in range).
+  constexpr float kLazy = std::is_same<E, __half>::value ? 9.0f : 16.0f;
   constexpr float kHead = std::is_same<E, __half>::value ? 6.0f : 0.0f;
 #pragma unroll 1
   for (int i = 0; i < kTK / kW; ++i) {

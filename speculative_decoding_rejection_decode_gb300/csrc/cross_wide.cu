@@ -21,7 +21,7 @@
 //
 // Measured (32 query and 8 kv heads of 128, bf16): 8 requests of 1536 rows over 2816 states
 // 566 GFLOP in 410 to 430 us = 1.3 PFLOP/s, the tensor pipe busy for 57 % of it; of 1000 to
-// 2048 rows over 1500 to 4096 states 1.2.  Bound by a group's scores, exponentials and
+// 2048 rows over 1500 to 4096 states 1.25.  Bound by a group's scores, exponentials and
 // weights in turn with its products; neither unit is full.
 #include "attention_tc.cuh"
 
@@ -115,7 +115,9 @@ __device__ __noinline__ float follow(float m, float most) { return m == -INFINIT
 template <typename T, int D, bool MASKED>
 __device__ __forceinline__ void tile_weights(uint32_t ts, uint32_t to, uint4 live, float rowf, bool summed,
                                              float& m, float& l, uint64_t* sum) {
-  constexpr float kLazy = 9.0f;   // (8: 456 us where 9 took 434, 8 requests of 1000 to 2048 rows, 1500 to 4096 states)
+  // f16 ends at 2^16; bf16, 8, 9 and 16: 456, 434 and 417 us, 8 requests of 1000 to 2048 rows
+  // over 1500 to 4096 states (sums of values below 2^90 stay in range).
+  constexpr float kLazy = std::is_same<T, __half>::value ? 9.0f : 16.0f;
   constexpr float kHead = std::is_same<T, __half>::value ? 6.0f : 0.0f;   // f16 weights keep their bits
   const uint64_t rowf2 = pair(rowf, rowf);
   uint32_t s[2][32];
