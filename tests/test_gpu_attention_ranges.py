@@ -1,0 +1,94 @@
+"""Attention at the ends of its types on the GPU: weights at the lag of their reference, values
+near the largest and smallest that bf16 holds, queries and keys that are no numbers."""
+import math
+
+import pytest
+import torch
+
+from cache_reference import Step, attend_tolerance
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, E4 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def V():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_rejection_decode_gb300 import Verifier
+    v = Verifier(0)
+    yield v
+    v.close()
+
+
+# rows of a request and heads that the three kernels serve: few, more, many for every SM
+KERNELS = [(2, {}), (40, {}), (300, {}), (300, dict(kv_heads=32, group=2))]
+
+
+def attend(V, s, cross, **kw):
+    c = s.cache(V)
+    if cross:
+        return c.cross_attend(s.q, s.table, s.lengths, s.cu, **kw)
+    return c.attend(s.q, s.table, s.lengths, s.cu, s.parent, **kw)
+
+
+def reference(s, cross, scale=None):
+    """float64 [n_rows, heads, head_dim] and, per row, the largest |v| seen; chains of nodes."""
+    scale = s.head_dim ** -0.5 if scale is None else scale
+    K, W = s.values("k"), s.values("v")
+    out, big = [], []
+    for b in range(s.B):
+        n = s.nodes[b]
+        slots = torch.arange(s.ctx[b] + (0 if cross else n), device=K.device)
+        pages = torch.tensor(s.pages[b], device=K.device)[slots // s.page]
+        k, v = K[pages, :, slots % s.page], W[pages, :, slots % s.page]
+        q = s.q[s.firsts[b]:s.firsts[b + 1]].double().view(n, s.kv_heads, s.group, s.head_dim)
+        z = torch.einsum("nhgd,shd->nhgs", q, k) * scale
+        later = slots[None] > s.ctx[b] + torch.arange(n, device=K.device)[:, None]
+        w = z.masked_fill(later[:, None, None], -math.inf).softmax(-1)
+        out.append(torch.einsum("nhgs,shd->nhgd", w, v).reshape(n, s.heads, s.head_dim))
+        most = v.abs().amax(2).cummax(0).values                       # [slots, kv_heads], seen up to a slot
+        seen = torch.full((n,), s.ctx[b] - 1, device=K.device) if cross else torch.arange(n, device=K.device) + s.ctx[b]
+        big.append(most[seen].repeat_interleave(s.group, 1))
+    return torch.cat(out), torch.cat(big)
+
+
+def one_higher(s, lag, slot):
+    """Every score 0 but those of `slot`, which are `lag` (times log 2, in base e) for the scale log 2."""
+    s.q.zero_()
+    s.q[..., 0] = 1.0
+    if s.ks is None:
+        s.k.zero_()
+    else:
+        s.k.view(torch.uint8).zero_()
+        s.ks.fill_(1.0)
+    for b in range(s.B):
+        page, off = s.row(b, slot)
+        if s.ks is None:
+            s.k[page, :, off, 0] = lag
+        else:
+            s.k[page, :, off, 0] = torch.tensor(8.0).to(E4)
+            s.ks[page, :, off] = lag / 8.0
+
+
+@pytest.mark.parametrize("cross", [False, True])
+@pytest.mark.parametrize("dtype,cache", [(HF, E4), (BF, E4), (HF, HF)])
+@pytest.mark.parametrize("rows,heads", KERNELS)
+def test_a_maximum_that_rises_by_the_lag(V, cross, dtype, cache, rows, heads):
+    # A reference may lag behind the maximum: weights just below, at and behind every lag that a
+    # kernel may leave, on a value whose scale has the largest mantissa.
+    s = Step(ctx=[200], nodes=[rows], dtype=dtype, cache=cache, seed=1, poison=False, **heads)
+    if s.vs is not None:
+        s.vs.fill_(2.0 - 2.0 ** -20)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    v = torch.rand(s.v.shape, generator=g, device="cuda") * 2 - 1      # up to the head room of the sums
+    s.v.copy_(v.to(s.v.dtype))
+    for lag in (7.9995, 8.0, 8.9995, 8.99999, 9.0, 9.0005, 9.9995, 15.9995):
+        one_higher(s, lag, 40)
+        out = attend(V, s, cross, scale=math.log(2.0))
+        assert V.get_error() == 0 and out.isfinite().all(), lag
+        want, big = reference(s, cross, math.log(2.0))
+        # scores up to 16 are off by less than 2^-18 (products of 32-bit factors), well within the tolerance
+        assert ((out.double() - want).abs() <= attend_tolerance(s, want, big)).all(), lag
