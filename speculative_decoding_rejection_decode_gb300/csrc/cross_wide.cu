@@ -534,8 +534,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           __syncwarp();
           tc_ld32(to + i * 32, x);
           if (!live) continue;
+          // (a reference of -inf may also mean that what the row saw was no number: inv is NaN then)
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = m == -INFINITY ? 0.0f : x[k] * inv;
+          for (int k = 0; k < 32; ++k) x[k] = (m == -INFINITY ? 0.0f : x[k]) * inv;
           // (a row's own lines: 32 bytes a store, half as many stores as of 16)
           if (seg.whole && aligned) {
             T* out = static_cast<T*>(a.out) + at * D + i * 32;

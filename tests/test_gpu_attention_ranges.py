@@ -92,3 +92,45 @@ def test_a_maximum_that_rises_by_the_lag(V, cross, dtype, cache, rows, heads):
         want, big = reference(s, cross, math.log(2.0))
         # scores up to 16 are off by less than 2^-18 (products of 32-bit factors), well within the tolerance
         assert ((out.double() - want).abs() <= attend_tolerance(s, want, big)).all(), lag
+
+
+def some_hidden(s):
+    """A mask with hidden slots among every 32."""
+    return (torch.arange(max(s.ctx), device="cuda") % 5 != 2).repeat(s.B, 1)
+
+
+@pytest.mark.parametrize("cross", [None, False, True])                # context and nodes; states; states with a mask
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (BF, E4), (HF, E4)])
+@pytest.mark.parametrize("ctx", [20, 60, 3000])                       # items whole, and split over ranges
+@pytest.mark.parametrize("rows,heads", KERNELS)
+def test_a_query_that_is_no_number(V, cross, dtype, cache, ctx, rows, heads):
+    s = Step(ctx=[ctx, ctx], nodes=[rows, rows], dtype=dtype, cache=cache, seed=5, poison=False, **heads)
+    kw = dict(mask=some_hidden(s)) if cross else {}
+    clean = attend(V, s, cross is not None, **kw)
+    s.q[1, 1, 3] = math.nan
+    out = attend(V, s, cross is not None, **kw)
+    assert V.get_error() == 0
+    assert out[1, 1].isnan().all()
+    out[1, 1] = clean[1, 1]
+    assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (BF, E4), (HF, E4)])
+@pytest.mark.parametrize("ctx", [20, 60, 3000])
+@pytest.mark.parametrize("rows,heads", KERNELS)
+def test_keys_that_are_no_numbers(V, masked, dtype, cache, ctx, rows, heads):
+    s = Step(ctx=[ctx, ctx], nodes=[rows, rows], dtype=dtype, cache=cache, seed=6, poison=False, **heads)
+    kw = dict(mask=some_hidden(s)) if masked else {}
+    clean = attend(V, s, True, **kw)
+    for slot in range(ctx):                                           # every key of request 1, kv head 0
+        page, off = s.row(1, slot)
+        if s.ks is None:
+            s.k[page, 0, off] = math.nan
+        else:
+            s.ks[page, 0, off] = math.nan
+    out = attend(V, s, True, **kw)
+    assert V.get_error() == 0
+    assert out[rows:2 * rows, :s.group].isnan().all()
+    out[rows:2 * rows, :s.group] = clean[rows:2 * rows, :s.group]
+    assert torch.equal(out, clean)
