@@ -472,7 +472,10 @@ int specdec_cache_read(specdec_handle_t h, const specdec_cache_t* cache,
  * q [N, q_heads, head_dim] strided, out contiguous [N, q_heads, head_dim], which
  * must not overlap q.
  * q_heads is a multiple of num_kv_heads.  Scores, maxima and sums are held in 32
- * bits; weights meet the values rounded to 16 bits (to f16 over e4m3 caches).
+ * bits; weights meet the values rounded to 16 bits (to f16 over e4m3 caches).  In bf16 the
+ * largest weight of a row lies in 2^-16 .. 1 before the division by their sum: values as
+ * large as 2^127 over the number of keys keep the sums finite, and values below 2^-118 may
+ * lose bits.
  * Keys in slots that the cache does not hold count as hidden (BAD_CACHE); a row
  * that sees no key is zeros, and so are the rows of a node whose own parent or an
  * ancestor's is no earlier node (BAD_TREE; the request's other nodes are not

@@ -224,9 +224,10 @@ __device__ __forceinline__ void tile_scores(uint32_t ts, uint32_t to, uint32_t b
   // f16 ends at 2^16: a weight of at most 2^15, or of 2^14 where it is yet to be multiplied with
   // the rest of a scale (EXACT, below 2).  8-bit caches, 8 and 9: 180 and 175 us, 32 requests of
   // 29 bf16 rows over 1500 to 12000 states; bf16 weights, 9 and 16: 208 and 205, 64 of 2 to 9
-  // over up to 8191 keys (sums of values below 2^90 stay in range).
+  // over up to 8191 keys.  bf16 weights end at 1, so that sums pass no further than the sum of
+  // the values' magnitudes.
   constexpr float kLazy = L::EXACT ? 8.0f : std::is_same<E, __half>::value ? 9.0f : 16.0f;
-  constexpr float kHead = std::is_same<E, __half>::value ? 6.0f : 0.0f;
+  constexpr float kHead = std::is_same<E, __half>::value ? 6.0f : -kLazy;
 #pragma unroll 1
   for (int i = 0; i < kTK / kW; ++i) {
     const float of = WIDE ? 1.0f : rowf;   // kWide: in the scores already

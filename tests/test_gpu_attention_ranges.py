@@ -134,3 +134,24 @@ def test_keys_that_are_no_numbers(V, masked, dtype, cache, ctx, rows, heads):
     assert out[rows:2 * rows, :s.group].isnan().all()
     out[rows:2 * rows, :s.group] = clean[rows:2 * rows, :s.group]
     assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("cross", [False, True])
+@pytest.mark.parametrize("rows,heads", KERNELS)
+@pytest.mark.parametrize("power", [-118, -100, -60, 60, 100, 119])
+def test_values_of_any_size(V, cross, rows, heads, power):
+    # 200 to 500 weights of at most 1 (the kernel's largest) and values below 2^119: sums below 2^128
+    s = Step(ctx=[200], nodes=[rows], seed=3, poison=False, **heads)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    s.v.copy_(torch.rand(s.v.shape, generator=g, device="cuda") * 2 - 1)
+    unit = s.v.clone()
+    for lag in (0.0, 7.96875, 15.9375):                              # what bf16 holds of 8 and 16
+        one_higher(s, lag, 40)
+        s.v.copy_(unit)
+        want, big = reference(s, cross, math.log(2.0))
+        s.v.mul_(2.0 ** power)                                        # exact
+        out = attend(V, s, cross, scale=math.log(2.0))
+        assert V.get_error() == 0 and out.isfinite().all(), lag
+        got = out.double() * 2.0 ** -power
+        assert ((got - want).abs() <= attend_tolerance(s, want, big)).all(), lag
