@@ -511,7 +511,7 @@ int64_t specdec_tree_attention_workspace(specdec_handle_t h, const specdec_cache
  * of a request sees the same ones.  nodes->parent is ignored.
  *   mask  device [B] rows of mask_slots bytes, mask_stride apart (>= mask_slots), or
  *         NULL: a slot whose byte is 0, or that lies at mask_slots or beyond, is hidden
- *         from the request's rows, whatever it holds
+ *         from the request's rows, whatever it holds, and needs no page
  * Everything else as for specdec_tree_attention: a row that sees no state (length 0, all
  * masked) is zeros. */
 int specdec_cross_attention(specdec_handle_t h, const specdec_cache_t* cache,

@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         x.end = CROSS ? x.len : x.len + (uint32_t)seg.q.n;      // within the table
         x.first = (uint32_t)t * kTK;
         x.h = seg.h;
-        x.id = -2;
+        x.id = -1;
         const uint32_t at = x.first + lane * 32;
         if (grouped && lane < 4 && at < x.end) x.id = __ldg(x.pages + at / page_size);
         if constexpr (CROSS) {
@@ -601,9 +601,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       // fewer than 2^31 rows in all; -1: the cache does not hold the slot
       auto row_at = [&](const Place& x, int id, uint32_t at) -> int {
-        if (id >= 0 && id < c.geo.num_pages) return (id * c.geo.kv_heads + x.h) * (int)page_size + (int)(at % page_size);
-        if (id != -2) bad |= SPECDEC_DEVERR_BAD_CACHE;
-        return -1;
+        return id >= 0 && id < c.geo.num_pages ? (id * c.geo.kv_heads + x.h) * (int)page_size + (int)(at % page_size) : -1;
       };
       // The rows of a tile of the array `src` (16-bit, or 8-bit as it is) to `dst`;
       // every lane arrives on `bar` when its copies have landed.  A box lies within
@@ -657,20 +655,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const Place now = ahead;
         const bool tail = now.first + kTK > now.len;
         int row = -1, rows[4] = {-1, -1, -1, -1};
-        uint32_t live = 0;                       // lanes 0 .. 3: of their 32 keys
+        uint32_t live = 0, missed = 0;           // lanes 0 .. 3: of their 32 keys; those without a page
         if (grouped) {
           const uint32_t at = now.first + lane * 32;
-          if (lane < 4) {
+          if (lane < 4 && at < now.end) {
             row = row_at(now, now.id, at);
-            if (row >= 0) live = now.end - at >= 32 ? 0xFFFFFFFFu : (1u << (now.end - at)) - 1u;
+            (row >= 0 ? live : missed) = now.end - at >= 32 ? 0xFFFFFFFFu : (1u << (now.end - at)) - 1u;
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t at = now.first + i * 32 + lane;
-            rows[i] = row_at(now, at < now.end ? __ldg(now.pages + at / page_size) : -2, at);
-            const uint32_t l = __ballot_sync(0xFFFFFFFFu, rows[i] >= 0);
-            if (lane == i) live = l;
+            rows[i] = row_at(now, at < now.end ? __ldg(now.pages + at / page_size) : -1, at);
+            const uint32_t l = __ballot_sync(0xFFFFFFFFu, rows[i] >= 0), m = __ballot_sync(0xFFFFFFFFu, at < now.end && rows[i] < 0);
+            if (lane == i) {
+              live = l;
+              missed = m;
+            }
           }
         }
         if constexpr (CROSS) {
@@ -678,10 +679,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t l = __ballot_sync(0xFFFFFFFFu, (now.see >> i) & 1u);
-              if (lane == i) live &= l;
+              if (lane == i) {
+                live &= l;
+                missed &= l;                     // a masked slot needs no page
+              }
             }
           }
         }
+        if (missed) bad |= SPECDEC_DEVERR_BAD_CACHE;
         const bool dirty = tail || __any_sync(0xFFFFFFFFu, lane < 4 && live != 0xFFFFFFFFu);
         // scales, 4 neighbouring keys a lane
         float4 ks = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vs = ks;

@@ -364,7 +364,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (key < len && t + lane / boxes < t1) {
             const int id = __ldg(pages + page);
             if (id >= 0 && id < c.geo.num_pages) row = (id * c.geo.kv_heads + h) * (int)page_size + (int)(key - page * page_size);
-            else bad |= SPECDEC_DEVERR_BAD_CACHE;
           }
         }
         const unsigned every = boxes == 32 ? 0xFFFFFFFFu : (1u << boxes) - 1u;
@@ -378,8 +377,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             const uint32_t in = i * 32 + lane, s = first + in;
-            const bool see = s < len && ((held >> (in >> shift)) & 1u) && (!mask || (s < a.mask_slots && __ldg(mask + s)));
-            const uint32_t live = __ballot_sync(0xFFFFFFFFu, see);
+            const bool shown = s < len && (!mask || (s < a.mask_slots && __ldg(mask + s))), here = (held >> (in >> shift)) & 1u;
+            if (shown && !here) bad |= SPECDEC_DEVERR_BAD_CACHE;   // (a masked slot needs no page)
+            const uint32_t live = __ballot_sync(0xFFFFFFFFu, shown && here);
             if (lane == 0) sh.live[f][i] = live;
           }
         }

@@ -155,3 +155,27 @@ def test_values_of_any_size(V, cross, rows, heads, power):
         assert V.get_error() == 0 and out.isfinite().all(), lag
         got = out.double() * 2.0 ** -power
         assert ((got - want).abs() <= attend_tolerance(s, want, big)).all(), lag
+
+
+@pytest.mark.parametrize("rows,heads", KERNELS)
+@pytest.mark.parametrize("cache", [BF, E4])
+@pytest.mark.parametrize("page", [12, 8, 16, 32, 64])                 # copies of 16 bytes, boxes of 8 to 64 rows
+def test_masked_slots_of_pages_that_are_not_held(V, rows, heads, cache, page):
+    # what a masked slot holds concerns no row, not even whether there is a page for it
+    s = Step(ctx=[200, 330], nodes=[rows, rows], cache=cache, page=page, seed=7, poison=False, **heads)
+    mask = torch.ones(2, 330, dtype=torch.bool, device="cuda")
+    mask[0, 128:] = False                                             # padding
+    mask[1, 2 * page:3 * page] = False                                # a page in the middle
+    mask[1, 256:256 + page // 2] = False                              # and half of one
+    want = attend(V, s, True, mask=mask)
+    assert V.get_error() == 0
+    table = s.table.clone()
+    table[0, -(-128 // page):] = -1
+    table[1, 2] = -2
+    s.table = table
+    assert torch.equal(attend(V, s, True, mask=mask), want)
+    assert V.get_error() == 0
+    # one slot of it shown: the page is missed
+    mask[1, 3 * page - 1] = True
+    assert torch.equal(attend(V, s, True, mask=mask), want)
+    assert V.get_error() == 32
