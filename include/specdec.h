@@ -446,8 +446,9 @@ int specdec_cache_append_positions(specdec_handle_t h, const specdec_cache_t* ca
  * and the arithmetic as in specdec_cache_append_positions, head_dim a multiple of 8 up to
  * 1024, rotary_dim a multiple of 16 up to head_dim and 128.
  *   inverse   not 0: turned back (sin negated), which is also the gradient of a turn
- *   out       the same shape, rows and heads that do not overlap one another; x itself
- *             (same address and strides), or no byte of x
+ *   out       the same shape, rows and heads that do not overlap one another (whole heads
+ *             within a row, or whole rows within a head, [heads, N, head_dim] in memory);
+ *             x itself (same address and strides), or no byte of x
  * A row one of whose positions lies outside the table becomes zeros
  * (SPECDEC_DEVERR_BAD_CACHE).  One launch, no workspace. */
 int specdec_rotate(specdec_handle_t h, int dtype, const void* x, int64_t x_row_stride,

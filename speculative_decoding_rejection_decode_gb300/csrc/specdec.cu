@@ -905,9 +905,11 @@ int specdec_rotate(specdec_handle_t h, int dtype, const void* x, int64_t x_row_s
   if (N > 0 && (!positions || !rows_ok(x, x_row_stride, x_head_stride) || !rows_ok(out, out_row_stride, out_head_stride)))
     return SPECDEC_ERR_INVALID_ARG;
   if (N > 0) {
-    // rows of the output of their own, over no input but the same values
-    if ((heads > 1 && (out_head_stride < head_dim)) || (N > 1 && out_row_stride < (heads - 1) * out_head_stride + head_dim))
-      return SPECDEC_ERR_INVALID_ARG;
+    // rows of the output of their own (heads within rows, or rows within heads), over no input
+    // but the same values
+    const bool by_row = (heads == 1 || out_head_stride >= head_dim) && (N == 1 || out_row_stride >= (heads - 1) * out_head_stride + head_dim);
+    const bool by_head = (N == 1 || out_row_stride >= head_dim) && (heads == 1 || out_head_stride >= (N - 1) * out_row_stride + head_dim);
+    if (!by_row && !by_head) return SPECDEC_ERR_INVALID_ARG;
     const int64_t bytes = 2 * ((N - 1) * out_row_stride + (heads - 1) * out_head_stride + head_dim);
     const bool itself = out == x && (heads == 1 || x_head_stride == out_head_stride) && (N == 1 || x_row_stride == out_row_stride);
     if ((!itself && meet_rows(out, bytes, x, x_row_stride, x_head_stride, N, heads, head_dim)) ||
