@@ -429,8 +429,9 @@ int specdec_cache_append(specdec_handle_t h, const specdec_cache_t* cache,
  *   offsets    device [B] or NULL, instead of positions: request b's nodes stand at
  *              lengths[b] + depth + offsets[b] on every axis (a prompt's images take
  *              more slots than positions)
- * A row one of whose positions, on any of the axes, lies outside the table is left out
- * as by specdec_cache_append (SPECDEC_DEVERR_BAD_CACHE). */
+ * out_q overlaps neither positions nor offsets.  A row one of whose positions, on any of
+ * the axes, lies outside the table is left out as by specdec_cache_append
+ * (SPECDEC_DEVERR_BAD_CACHE). */
 #define SPECDEC_MAX_AXES 4
 int specdec_cache_append_positions(specdec_handle_t h, const specdec_cache_t* cache,
                          const specdec_nodes_t* nodes, int dtype, const void* k,

@@ -221,6 +221,8 @@ class KVCache:
                 if t.dtype is not torch.int32 or t.get_device() != self._at or t.numel() != lengths.numel() \
                         or not t.is_contiguous():
                     raise ValueError("position_offsets must be a contiguous int32 tensor on the device, one entry per request")
+                if N and q is not None and _overlap(out_q, t):
+                    raise ValueError("out_q must not overlap position_offsets")
                 where = (None, 0, 1, None, t.data_ptr())
             if N:
                 _check(specdec_cache_append_positions(

@@ -734,6 +734,8 @@ static int append_rows(specdec_handle_t h, const specdec_cache_t* cache, const s
     return SPECDEC_ERR_INVALID_ARG;
   if (positions && offsets) return SPECDEC_ERR_INVALID_ARG;
   if ((positions || offsets) && !rotary) return SPECDEC_ERR_INVALID_ARG;
+  if (offsets && q && nodes->N > 0 && meet(out_q, 2 * nodes->N * q_heads * cache->head_dim, offsets, 4 * (int64_t)nodes->B))
+    return SPECDEC_ERR_INVALID_ARG;
   if (positions) {
     if (!pairs_of(axes, num_axes, rotary_dim, a.axes) || (num_axes > 1 && position_stride < nodes->N)) return SPECDEC_ERR_INVALID_ARG;
     const int64_t bytes = 4 * ((num_axes - 1) * position_stride + nodes->N);
