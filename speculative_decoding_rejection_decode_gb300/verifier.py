@@ -49,6 +49,7 @@ class LogprobOutput:
     top_ids: torch.Tensor | None        # int32 [M, top]; None where top is 0
     top_logprobs: torch.Tensor | None   # float32 [M, top]
     stats: torch.Tensor                 # float32 [M, 2] what the gradient needs of the rows
+    own_rows: bool = True               # token t's row is t (no `rows` were given): what the gradient takes
 
 
 _LOGITS = {torch.float32: SPECDEC_F32, torch.bfloat16: SPECDEC_BF16, torch.float16: SPECDEC_F16}
@@ -242,6 +243,7 @@ class Verifier:
                     raise ValueError(f"out.{name} does not go with ids and top")
                 if w:
                     self._flat(t, w[1], w[0], f"out.{name}")
+        out.own_rows = rows is None
         if M:
             if R == 0:
                 raise ValueError("logits has no rows")
@@ -262,8 +264,8 @@ class Verifier:
         f32 = torch.float32
         x, dt, stride = self._logit_rows(logits, "logits")
         (R, V), M = logits.shape, forward.stats.shape[0]
-        if M != R:
-            raise ValueError("the gradient needs a token for every row of the logits")
+        if M != R or not forward.own_rows:
+            raise ValueError("the gradient needs a token for every row of the logits, in their order (no rows)")
         if ids is not None:
             self._flat(ids, torch.int32, (M,), "ids")
         if (ids is None) != (forward.logprob is None):

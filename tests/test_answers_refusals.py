@@ -38,3 +38,16 @@ def test_the_library_refuses_them_too():
         assert call(q.data_ptr() + at) == -1
     assert v.get_error() == 0
     v.close()
+
+
+def test_a_gradient_of_rows_in_another_order_is_refused(lib):  # noqa: F811
+    from speculative_decoding_rejection_decode_gb300 import LogprobOutput
+    from test_answers_host import fake
+    v, f = fake(lib), torch.zeros
+    x, i = f(4, 10), lambda n: torch.zeros(n, dtype=torch.int32)
+    assert v.logprobs(x[:0], i(0)).own_rows and not v.logprobs(x, i(0), rows=i(0)).own_rows
+    out = LogprobOutput(f(0), f(0), None, None, f(0, 2))
+    assert not v.logprobs(x, i(0), rows=i(0), out=out).own_rows and v.logprobs(x, i(0), out=out).own_rows
+    # as many tokens as rows, but not their own: the gradient would be that of other rows
+    with pytest.raises(ValueError, match="order"):
+        v.logprobs_grad(x, i(4), LogprobOutput(f(4), f(4), None, None, f(4, 2), own_rows=False), grad_logprob=f(4))
