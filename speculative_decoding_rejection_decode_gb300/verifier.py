@@ -448,13 +448,14 @@ def rotary_axes(sections, *, spread: bool = False) -> tuple[int, ...]:
 def tree_rows(path: torch.Tensor, cu_num_nodes: torch.Tensor) -> torch.Tensor:
     """The target row (int32 [N]) that each slot of ``Verifier.tree``'s tokens comes
     from: node 0's for a request's first token, then those of the accepted nodes; -1
-    where no token stands."""
+    where no token stands, behind the last request too (``tree`` leaves path and tokens
+    there as they are)."""
     first = cu_num_nodes[:-1].long()
     slots = torch.arange(path.numel(), device=path.device)
     req = torch.searchsorted(cu_num_nodes[1:].contiguous(), slots.to(torch.int32), right=True).clamp(max=first.numel() - 1)
     before = torch.cat([path.new_zeros(1), path[:-1]])
     node = torch.where(slots == first[req], 0, before)
-    return torch.where(node >= 0, first[req] + node, -1).to(torch.int32)
+    return torch.where((node >= 0) & (slots < cu_num_nodes[-1]), first[req] + node, -1).to(torch.int32)
 
 
 @dataclass

@@ -51,3 +51,12 @@ def test_a_gradient_of_rows_in_another_order_is_refused(lib):  # noqa: F811
     # as many tokens as rows, but not their own: the gradient would be that of other rows
     with pytest.raises(ValueError, match="order"):
         v.logprobs_grad(x, i(4), LogprobOutput(f(4), f(4), None, None, f(4, 2), own_rows=False), grad_logprob=f(4))
+
+
+def test_slots_behind_the_last_request_have_no_row(lib):  # noqa: F811
+    from speculative_decoding_rejection_decode_gb300 import tree_rows
+    i = lambda x: torch.tensor(x, dtype=torch.int32)
+    # the verification leaves slots 5 .. 7 as they are: whatever lies there is no node
+    path = i([1, -1, -1, 1, -1, 3, 0, 900])
+    assert tree_rows(path, i([0, 3, 5])).tolist() == [0, 1, -1, 3, 4, -1, -1, -1]
+    assert tree_rows(path, i([0, 0])).tolist() == [-1] * 8
