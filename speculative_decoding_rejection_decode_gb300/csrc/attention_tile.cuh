@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const Place now = ahead;
         const bool tail = now.first + kTK > now.len;
         int row = -1, rows[4] = {-1, -1, -1, -1};
-        uint32_t live = 0, missed = 0;           // lanes 0 .. 3: of their 32 keys; those without a page
+        uint32_t live = 0, missed = 0;           // lanes 0 .. 3: of their 32 keys; grouped: those without a page
         if (grouped) {
           const uint32_t at = now.first + lane * 32;
           if (lane < 4 && at < now.end) {
@@ -667,11 +667,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int i = 0; i < 4; ++i) {
             const uint32_t at = now.first + i * 32 + lane;
             rows[i] = row_at(now, at < now.end ? __ldg(now.pages + at / page_size) : -1, at);
-            const uint32_t l = __ballot_sync(0xFFFFFFFFu, rows[i] >= 0), m = __ballot_sync(0xFFFFFFFFu, at < now.end && rows[i] < 0);
-            if (lane == i) {
-              live = l;
-              missed = m;
-            }
+            const uint32_t l = __ballot_sync(0xFFFFFFFFu, rows[i] >= 0);
+            if (lane == i) live = l;
+            if (at < now.end && rows[i] < 0 && (!CROSS || ((now.see >> i) & 1u))) bad |= SPECDEC_DEVERR_BAD_CACHE;
           }
         }
         if constexpr (CROSS) {
