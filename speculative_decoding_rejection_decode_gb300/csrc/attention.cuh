@@ -232,10 +232,15 @@ struct Partials {
 // than this is done behind the attention kernel, whose ranges end together: with the plan
 // walked again here, and rows in turns, the join took 19 us of 207 (8-bit states, 32
 // requests of 29 nodes, 1500 to 12000 states), this form 13; the warp kernel's is hidden
-// by the launch.
+// by the launch where requests are many.  Few of them have their items in many ranges, each
+// block alone on its SM, and then a row's partials are what takes time: 2, 4 and 8 of them
+// under way, 1 row over 2000 keys 16.5, 14.2, 13.6 us, 4000 17.2, 14.1, 13.5, 8000 in e4m3
+// 21.5, 18.3, 17.7, 64 of up to 8191 188.9, 187.4, 186.6.  Tiles of 128 and 256 rows want the
+// blocks on an SM: 2 and 4 (4 blocks), 32 requests of 29 nodes over 6000 to 16000 in e4m3 256
+// and 259, 8 prompts of 1000 to 2048 rows 415 and 420 (1 of 29 over 5000 keys 28.7 and 27.4).
 template <typename T, int R, int D>
-__global__ void __launch_bounds__(128, 8) attend_join_kernel(const AttendArgs a, const int G) {
-  constexpr int J = 4, U = 2, PER = D / 32;      // rows of a warp, partials under way together
+__global__ void __launch_bounds__(128, R == 16 ? 2 : 8) attend_join_kernel(const AttendArgs a, const int G) {
+  constexpr int J = 4, U = R == 16 ? 8 : 2, PER = D / 32;   // rows of a warp, partials under way together
   using V = typename std::conditional<PER == 4, float4, float2>::type;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.q_heads / a.c.geo.kv_heads;
   const Partials<R, D> part(a.workspace, G);

@@ -179,3 +179,18 @@ def test_masked_slots_of_pages_that_are_not_held(V, rows, heads, cache, page):
     mask[1, 3 * page - 1] = True
     assert torch.equal(attend(V, s, True, mask=mask), want)
     assert V.get_error() == 32
+
+
+@pytest.mark.parametrize("cross", [False, True])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (BF, E4)])
+@pytest.mark.parametrize("rows", [1, 3, 4, 29])
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_one_request_over_many_ranges(V, cross, dtype, cache, rows, head_dim):
+    # 2 to 152 partial results of every row
+    for kv_heads, ctx in ((8, 600), (8, 1500), (8, 1999), (1, 1999), (3, 5000), (2, 20000)):
+        s = Step(ctx=[ctx], nodes=[rows], kv_heads=kv_heads, group=4, head_dim=head_dim, dtype=dtype, cache=cache, page=64, seed=8, poison=False)
+        out = attend(V, s, cross)
+        assert V.get_error() == 0
+        want, big = reference(s, cross)
+        # (attend_tolerance: sums of up to 2^11 keys add 2^-13 of the largest value; of 2^15, 2^-9)
+        assert ((out.double() - want).abs() <= attend_tolerance(s, want, big) + (2.0 ** -9 * big[..., None] if ctx > 2000 else 0.0)).all()
