@@ -493,15 +493,21 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitArgs a, const i
 // Rows of an append's block, whose places are looked up together (a few dependent loads):
 // as many that the blocks fill whole waves of the resident ones.  40619 rows of 48 heads
 // into e4m3, 16, 24, 32 rows at most: 162, 160, 159 us, 15k (read back) 90, 88, 88; one
-// wave, or 16 rows whatever is left for the last wave, 167 and 104.
-inline int rows_per_block(int64_t N, int64_t blocks) {
-  const int64_t waves = (N + blocks * kRows - 1) / (blocks * kRows), r = (N + blocks * waves - 1) / (blocks * waves);
+// wave, or 16 rows whatever is left for the last wave, 167 and 104.  Wide rows of 16 bits are
+// bound by memory even within a wave, and two waves cover each other's starts: 15k of 128, 8,
+// 16, 24 rows at most 64.0, 62.9, 66.6 us (without a turn 60.4, 61.3, 73.7), 16k 67.6, 67.3,
+// 72.5; of 64 values 42.6, 40.4, 38.2.
+template <bool FP8, int D>
+constexpr int kMostRows = !FP8 && D == 128 ? 16 : kRows;
+
+inline int rows_per_block(int64_t N, int64_t blocks, int most) {
+  const int64_t waves = (N + blocks * most - 1) / (blocks * most), r = (N + blocks * waves - 1) / (blocks * waves);
   return (int)(r < 1 ? 1 : r);
 }
 
 template <typename T, bool FP8, int D>
 int append_dim(const AppendArgs& a, int num_sms, cudaStream_t st) {
-  const int rows = rows_per_block(a.c.N, (int64_t)num_sms * kAppendBlocks);
+  const int rows = rows_per_block(a.c.N, (int64_t)num_sms * kAppendBlocks, kMostRows<FP8, D>);
   const unsigned grid = (unsigned)((a.c.N + rows - 1) / rows);
   if (a.interleaved) append_kernel<T, FP8, D, true><<<grid, kThreads, 0, st>>>(a, rows);
   else append_kernel<T, FP8, D, false><<<grid, kThreads, 0, st>>>(a, rows);
