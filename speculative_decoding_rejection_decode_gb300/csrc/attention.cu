@@ -62,7 +62,9 @@ int launch_attend(const AttendArgs& args, int cache_dtype, int dtype, int num_sm
   const Kernel k = kernel_of(a.cross, cache_dtype, c.geo.page_size, c.B, c.N, c.geo.kv_heads, a.q_heads, num_sms);
   a.whole = whole_items(c.B, c.N, c.geo.kv_heads, a.q_heads, (int64_t)c.geo.max_pages * c.geo.page_size, rows_of(k), num_sms);
   const bool fp8 = cache_dtype == SPECDEC_E4M3;
-  a.item_cost = k == Kernel::kWide ? kItemCostWide : !fp8 ? kItemCost : k == Kernel::kTile ? kItemCostTile8 : kItemCostWarp8;
+  const bool brief = !a.cross && (int64_t)c.geo.max_pages * c.geo.page_size <= kShortSlots;
+  a.item_cost = k == Kernel::kWide ? kItemCostWide : !fp8 ? kItemCost : k == Kernel::kWarp ? kItemCostWarp8
+              : brief ? kItemCostTile8Short : kItemCostTile8;
   if (k == Kernel::kWide) return launch_cross_wide(a, dtype, num_sms, st);
   if (k == Kernel::kTile) return a.cross ? launch_cross_tile(a, cache_dtype, dtype, num_sms, st) : launch_attend_tile(a, cache_dtype, dtype, num_sms, st);
   return a.cross ? launch_cross_warp(a, cache_dtype, dtype, num_sms, st) : launch_warp_types<false>(a, cache_dtype, dtype, num_sms, st);

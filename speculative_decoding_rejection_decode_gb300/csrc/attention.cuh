@@ -14,6 +14,9 @@
 //   tile, 8 bits, 5, 8, 10, 12, 16: 32 of 29 over 1500-12000 202, 188, 186, 185, 188; 64 of 2-9
 //     over up to 8191 208, 193, 195, 198, 201; 200 of 5-29 over up to 1500 225, 218, 216, 218,
 //     224; 32 of 29 over 6000-16000 262, 257, 255, 255, 258
+//   the same over context and nodes, where the table holds 8192 slots at most, 5, 6, 7, 10: 64 of
+//     2-9 over up to 2000 113, 115, 120, 126; 128 of 9 over up to 1000 130, 132, 138, 146; 16 of 29
+//     f16 rows over up to 6000 96, 100, 101, 109 (1 of 29 over 2000 25.9, 25.5, 25.6, 24.4)
 //   wide, 2, 3, 4, 5, 7: 8 of 1000-2048 over 1500-4096 464, 441, 443, 448, 448; 64 of 100-200
 //     over 500-2000 252, 251, 249, 253, 252; 30 of 200-900 over 100-700 (16 kv heads of 64)
 //     110, 107, 106, 107, 108
@@ -43,6 +46,7 @@ namespace specdec {
 
 constexpr int kItemCost = 5;       // units of an item's own
 constexpr int kItemCostTile8 = 10;  // in the tile kernel over 8-bit caches
+constexpr int kItemCostTile8Short = 6, kShortSlots = 8192;   // the same over context and nodes, slots of a request
 constexpr int kItemCostWide = 4;    // in the wide kernel
 constexpr int kItemCostWarp8 = 2;  // the same in the warp kernel over 8-bit caches
 

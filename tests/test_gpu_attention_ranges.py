@@ -194,3 +194,16 @@ def test_one_request_over_many_ranges(V, cross, dtype, cache, rows, head_dim):
         want, big = reference(s, cross)
         # (attend_tolerance: sums of up to 2^11 keys add 2^-13 of the largest value; of 2^15, 2^-9)
         assert ((out.double() - want).abs() <= attend_tolerance(s, want, big) + (2.0 ** -9 * big[..., None] if ctx > 2000 else 0.0)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("width", [8192, 8193, 20000])                # slots that the table holds
+def test_ranges_of_short_and_long_tables(V, dtype, width):
+    # ragged requests over e4m3: the ranges of work are cut by the table's width, the result is not
+    s = Step(ctx=[0, 700, 2000, 3, 1300, 129] * 6, nodes=[9, 5, 9, 29, 6, 40] * 6, kv_heads=2, dtype=dtype, cache=E4, seed=10, page=64, poison=False)
+    pad = torch.full((s.B, -(-width // 64) - s.table.shape[1]), -1, dtype=torch.int32, device="cuda")
+    s.table = torch.cat([s.table, pad], 1)
+    out = attend(V, s, False)
+    assert V.get_error() == 0
+    want, big = reference(s, False)
+    assert ((out.double() - want).abs() <= attend_tolerance(s, want, big)).all()
