@@ -211,7 +211,10 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
 
 // A wait that gives up: the role goes on without waiting (its loops are finite
 // and its addresses do not depend on data), and the call reports the timeout.  A
-// try sleeps for a time that the hardware limits, so the wait ends within seconds.
+// try on a phase that does not complete returns after 4.0 us on this GPU (measured: 2048 tries
+// of 1, 32 and 128 threads, 4.2 us at most; the same with a time hint of 0.1 or 1 us, which
+// therefore is not given), so that 2^20 of them end after 4.3 seconds; the other roles'
+// waits end within 256 of theirs, a millisecond.
 // (Kept this small because it stands in many places: with a clock read in each,
 // the kernel's code passed the instruction cache.)
 __device__ __forceinline__ void wait_or_give_up(int& dead, uint32_t bar, uint32_t parity) {

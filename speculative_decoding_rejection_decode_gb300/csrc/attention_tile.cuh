@@ -213,8 +213,10 @@ __device__ __noinline__ void left_out(const CacheArgs& c, const Segments& s, int
 // Weights are 2^(e - m), m the first maximum (so that a row that sees one key gets its
 // values as they are), which follows the running maximum by whole numbers and only when
 // that is kLazy above it: what has been summed, the row's O_w (`summed`: there is
-// one) and the tile's weights so far are then multiplied by a power of two, which
-// loses nothing.  The largest weight lies in [2^kHead, 2^(kHead + kLazy)]: f16 weights keep
+// one) and the tile's weights so far are then multiplied by 2^(m - m').  m' = m + k is rounded to
+// 32 bits, so that the factor is a power of two but for |m'| 2^-24, as much as the scores of
+// that size are off by themselves; the weights' own factor is rounded to their 16 bits, to
+// the power of two.  The largest weight lies in [2^kHead, 2^(kHead + kLazy)]: f16 weights keep
 // their bits far below the largest, and the maximum may lag by 2^kLazy.
 template <typename T, bool FP8, int D, bool WIDE>
 __device__ __forceinline__ void tile_scores(uint32_t ts, uint32_t to, uint32_t base_s, int f, const float* vexp,
@@ -385,8 +387,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   extern __shared__ char smem_raw[];
   __shared__ ScanShared scan;
   __shared__ __align__(8) TileShared sh;
-  // segments of the softmax groups, the products, the loaders and the wideners
-  __shared__ Segments segs[4 + kLoaders];
+  // segments of the softmax groups, the products, the loaders and the finishers
+  __shared__ Segments segs[3 + kLoaders];
   char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t base_s = smem_addr(smem);
   const CacheArgs& c = a.c;
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   const uint32_t tm = sh.tmem;
   const int64_t uend = range_begin(units, ranges, blockIdx.x + 1);
-  if (tid < 4 + kLoaders) {
+  if (tid < 3 + kLoaders) {
     uint32_t ignored = 0;
     Segments& s = segs[tid];
     s.end = uend;
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int h, id;
         uint32_t see;                           // masks: bit i is key 32 i + lane's
       };
-      Segments& seg = segs[3 + loader];
+      Segments& seg = segs[2 + loader];
       int skip = loader, t = seg.t0;            // tiles of others before this loader's next
       // The next item's queries on their way to L2 while this one's last tiles are worked on:
       // 32 requests of 29 rows over 1500 to 12000 8-bit states 184 to 178 us, 64 of 2 to 9 over
@@ -787,7 +789,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---- finishers: 32 keys each.  8 lanes read and write one chunk of 8
     // neighbouring rows, without bank conflicts in any of the swizzles ------------
     const int pw = warp - 2 * kGroupWarps;
-    Segments& seg = segs[3 + kLoaders];
+    Segments& seg = segs[2 + kLoaders];
     for (int n = 0, t = seg.t0; seg.more; ++n) {
       const int f = n % kFactSlots;
       wait_use(sh.fact, kFactSlots, n);

@@ -56,7 +56,7 @@ struct alignas(16) WideShared {   // live is read 16 bytes at a time
   int dead;                                   // a wait ran out
 };
 
-// Two 16-bit weights times a power of two.
+// Two 16-bit weights times `by`, rounded to 16 bits as well.
 __device__ __forceinline__ uint32_t halves(uint32_t w, float by, __half) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(by));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -79,8 +79,9 @@ __device__ __forceinline__ void tc_arrived(uint32_t* r) {
       : "+r"(r[0]),"+r"(r[1]),"+r"(r[2]),"+r"(r[3]),"+r"(r[4]),"+r"(r[5]),"+r"(r[6]),"+r"(r[7]),"+r"(r[8]),"+r"(r[9]),"+r"(r[10]),"+r"(r[11]),"+r"(r[12]),"+r"(r[13]),"+r"(r[14]),"+r"(r[15]),"+r"(r[16]),"+r"(r[17]),"+r"(r[18]),"+r"(r[19]),"+r"(r[20]),"+r"(r[21]),"+r"(r[22]),"+r"(r[23]),"+r"(r[24]),"+r"(r[25]),"+r"(r[26]),"+r"(r[27]),"+r"(r[28]),"+r"(r[29]),"+r"(r[30]),"+r"(r[31]));
 }
 
-// What has been summed of a row so far times a power of two: the tile's weights that have
-// been stored (`parts` x 32) and, where there is one, O_w.  Out of line: rare.
+// What has been summed of a row so far times `fix`, a power of two (nearly, see below; weights
+// take it rounded to 16 bits, to the power of two): the tile's weights that have been stored
+// (`parts` x 32) and, where there is one, O_w.  Out of line: rare.
 template <typename T, int D>
 __device__ __noinline__ void rescale(uint32_t ts, uint32_t to, int parts, bool summed, float fix) {
   tc_wait_st();   // what is read back here has been stored
@@ -110,7 +111,8 @@ __device__ __noinline__ float follow(float m, float most) { return m == -INFINIT
 // maximum of the next 32 is found beside the exponentials of these.  The reference m, the
 // first maximum (so that a row that sees one state gets its values as they are), follows the
 // maximum by whole numbers and only where that has passed it by kLazy: what has been summed
-// is then multiplied by a power of two.  (Handing on the first 96 keys'
+// is then multiplied by 2^(m - m'), a power of two but for |m'| 2^-24 (the rounding of m', as
+// much as scores of that size are off by themselves).  (Handing on the first 96 keys'
 // weights before the last 32 gained nothing.)
 template <typename T, int D, bool MASKED>
 __device__ __forceinline__ void tile_weights(uint32_t ts, uint32_t to, uint4 live, float rowf, bool summed,
