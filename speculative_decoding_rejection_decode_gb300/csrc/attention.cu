@@ -13,10 +13,10 @@ int64_t average_rows(int B, int64_t N, int kv_heads, int q_heads) {
 // Up to these (a tile of the warp kernel) the warp kernel, above them the tile kernel.
 // One context of 500 / 64 up to 8191 / 4 of 30000 / 200 up to 1500, 8 kv heads of 128,
 // device us, warp and tile kernel:
-//   4 rows  bf16 14.9 18.1 / 179 184 / 87 90 / 127 150, e4m3 14.8 18.9 / 179 208 / 81 81 / 152 197
-//   12      bf16 16.8 18.8 / 183 185 / 92 92 / 144 151, e4m3 16.8 19.1 / 188 206 / 85 82 / 172 199
-//   16      bf16 17.3 18.8 / 182 185 / 93 92 / 148 151, e4m3 16.9 19.4 / 192 207 / 86 82 / 177 199
-//   20      bf16 17.0 18.9 / 340 189 / 165 94 / 255 153, e4m3 18.4 19.0 / 345 210 / 146 82 / 306 198
+//   4 rows  bf16 11.5 12.9 / 174 176 / 87 86 / 128 141, e4m3 12.5 15.2 / 184 199 / 83 82 / 153 196
+//   12      bf16 13.1 12.9 / 174 179 / 90 88 / 144 143, e4m3 13.7 15.4 / 187 205 / 84 84 / 169 198
+//   16      bf16 13.1 13.1 / 175 180 / 91 88 / 148 142, e4m3 14.1 15.4 / 189 206 / 84 85 / 174 198
+//   20      bf16 13.5 13.1 / 334 181 / 158 88 / 259 144, e4m3 14.3 15.2 / 356 206 / 150 85 / 313 200
 // The average decides: in a batch of one large request among many small ones, the
 // large one takes a tile of 16 rows at a time.
 constexpr int kWarpRows = 16;
@@ -28,10 +28,13 @@ constexpr int kTileRows = 128;   // rows of a tile of the tile kernel
 
 // The wide kernel (cross_wide.cu) reads a key for 256 rows, and is bound by the products; the
 // tile kernel divides a call's rows among more CTAs.  Tile and wide kernel, device us, 32
-// query and 8 kv heads of 128, bf16 states (rows of a request and kv head):
-//   1 request, 2816 states    128  29 29    160  27 31    256  29 36    512  31 37
-//   8 of 2816                 128  46 50    160  53 54    384  70 74    512  84 79
-//   64 of 1500                128 115 116   144 171 127   256 193 136   512 349 221
+// query and 8 kv heads of 128, bf16 states (rows of a request and kv head; f16 the same within
+// 4 %), and of 64:
+//   1 request, 2816 states    128  22 22    160  21 23    256  21 26    512  24 27
+//   8 of 2816                 128  37 38    160  42 41    384  58 60    512  72 63
+//   64 of 1500                128 100 103   160 156 115   256 176 123   512 324 210
+//   64: 8 of 2816             128  26 29    160  36 32    384  46 48    512  56 48
+//       64 of 1500            128  74 90    160 121 95    256 126 99    512 228 169
 // The wide one takes over where the rows pass a tile and the tiles are more than one and a
 // half for each SM.
 Kernel kernel_of(bool cross, int cache_dtype, int page_size, int B, int64_t N, int kv_heads, int q_heads, int num_sms) {

@@ -10,20 +10,20 @@
 // an empty pipeline, results) takes about as long as that many tiles, and without
 // them the ranges that hold many short requests finished late.  us (32 query heads of 128;
 // requests of rows over keys or states, 8 kv heads unless said):
-//   tile, 16 bits, cost 2, 3, 5, 8: 64 of 2-9 over up to 8191 227, 219, 210, 211
-//   tile, 8 bits, 5, 8, 10, 12, 16: 32 of 29 over 1500-12000 202, 188, 186, 185, 188; 64 of 2-9
-//     over up to 8191 208, 193, 195, 198, 201; 200 of 5-29 over up to 1500 225, 218, 216, 218,
-//     224; 32 of 29 over 6000-16000 262, 257, 255, 255, 258
-//   the same over context and nodes, where the table holds 8192 slots at most, 5, 6, 7, 10: 64 of
-//     2-9 over up to 2000 113, 115, 120, 126; 128 of 9 over up to 1000 130, 132, 138, 146; 16 of 29
-//     f16 rows over up to 6000 96, 100, 101, 109 (1 of 29 over 2000 25.9, 25.5, 25.6, 24.4)
-//   wide, 2, 3, 4, 5, 7: 8 of 1000-2048 over 1500-4096 464, 441, 443, 448, 448; 64 of 100-200
-//     over 500-2000 252, 251, 249, 253, 252; 30 of 200-900 over 100-700 (16 kv heads of 64)
-//     110, 107, 106, 107, 108
-//   warp, 16 bits, 1, 2, 3, 5: 64 of 1 over up to 8191 193, 183, 180, 180; 200 of 1-4 over up to
-//     1500 182, 170, 157, 151; 64 of 2-9 over up to 2047 (32 kv heads) 300, 256, 236, 216
+//   tile, 16 bits, cost 2, 3, 5, 8: 64 of 2-9 over up to 8191 205, 189, 180, 182
+//   tile, 8 bits, 5, 6, 8, 10, 12: 32 of 29 over 1500-12000 145, 145, 142, 145, 145; 64 of 2-9
+//     over up to 8191 185, 176, 179, 180, 183; 200 of 5-29 over up to 1500 223, 215, 211, 211, 213;
+//     32 of 29 over 6000-16000 (context and nodes) 250, 248, 247, 245, 244
+//   the same over context and nodes in pages of 16, where the table holds 8192 slots at most, 5, 6,
+//     7, 10: 64 of 2-9 over up to 2000 113, 115, 120, 126; 128 of 9 over up to 1000 130, 132, 138,
+//     146; 16 of 29 f16 rows over up to 6000 96, 100, 101, 109 (1 of 29 over 2000 25.9, 25.5, 25.6, 24.4)
+//   wide, 2, 3, 4, 5, 7: 8 of 1000-2048 over 1500-4096 391, 386, 388, 393, 401; 64 of 100-200
+//     over 500-2000 241, 236, 236, 242, 241; 30 of 200-900 over 100-700 (16 kv heads of 64)
+//     97, 95, 97, 99, 98
+//   warp, 16 bits, 1, 2, 3, 5: 64 of 1 over up to 8191 193, 176, 177, 174; 200 of 1-4 over up to
+//     1500 189, 157, 149, 145; 64 of 2-9 over up to 2047 (32 kv heads) 224, 192, 180, 174
 //     (at 7 and more it rises again)
-//   warp, 8 bits, 2, 3, 4, 6: 178, 183, 185, 191; 173, 179, 183, 191; 258, 259, 269, 286 (its
+//   warp, 8 bits, 2, 3, 4, 6: 184, 187, 189, 197; 171, 180, 188, 196; 173, 176, 179, 189 (its
 //     tiles are of 256 keys and take longer)
 //
 // Rows of an item: r = node * group + head within the group, so one read of a
@@ -76,10 +76,10 @@ struct PlanArgs {
 // table's width, and no more items than two for each CTA.  One launch and no
 // workspace then; splitting such items only pays where they are many and ragged.
 // Device us, whole and split, 32 query and 8 kv heads of 128, bf16: 1 request of 1 node
-// over 60 / 250 / 480 keys 7.5 and 8.9 / 9.3 and 10.9 / 11.6 and 11.0 (a call,
-// host included: 17.0 and 23.2, for the second launch and the workspace), of 29 nodes 12.3 and 15.6 /
-// 14.0 and 20.0 / 15.7 and 20.8; 32 requests of 1 node 12.3 and 13.8 / 15.8 and 19.8 /
-// 23.0 and 27.3, of 29 nodes 21.2 and 26.0 / 31.1 and 40.0 / 36.4 and 46.2.
+// over 60 / 250 / 480 keys 7.4 and 8.4 / 9.4 and 11.1 / 11.3 and 10.9 (a call,
+// host included: 17.0 and 23.2, for the second launch and the workspace), of 29 nodes 14.1 and 15.6 /
+// 17.6 and 20.0 / 19.5 and 20.1; 32 requests of 1 node 11.9 and 12.9 / 15.4 and 19.5 /
+// 19.3 and 24.0, of 29 nodes 22.9 and 24.2 / 28.9 and 34.6 / 34.2 and 42.0.
 inline bool whole_items(int B, int64_t N, int kv_heads, int q_heads, int64_t capacity, int rows, int num_sms) {
   const int64_t avg = (N + B - 1) / B * (q_heads / kv_heads);
   return capacity <= 512 && (int64_t)B * kv_heads * ((avg + rows - 1) / rows) <= 2 * (int64_t)num_sms;
