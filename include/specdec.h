@@ -446,7 +446,8 @@ int specdec_cache_append_positions(specdec_handle_t h, const specdec_cache_t* ca
  * rows before they are split) by positions on several axes; positions, axes, rotary
  * and the arithmetic as in specdec_cache_append_positions, head_dim a multiple of 8 up to
  * 1024, rotary_dim a multiple of 16 up to head_dim and 128.
- *   inverse   not 0: turned back (sin negated), which is also the gradient of a turn
+ *   inverse   not 0: turned back (sin negated), which is also the gradient of a turn (a
+ *             table's gain is applied, not taken back)
  *   out       the same shape, rows and heads that do not overlap one another (whole heads
  *             within a row, or whole rows within a head, [heads, N, head_dim] in memory);
  *             x itself (same address and strides), or no byte of x

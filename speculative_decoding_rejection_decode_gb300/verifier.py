@@ -217,7 +217,8 @@ class Verifier:
         float16, rows of any stride; ``ids`` (int32 [M], None: no given tokens), ids
         below 0 are skipped (zeros, alternatives -1), so the ``tokens`` of a
         verification can be given as they are; ``rows`` (int32 [M]) the row of each
-        token (``tree_rows`` for the tokens of ``tree``), None: its own."""
+        token (``tree_rows`` for the tokens of ``tree``), None: its own.  The results carry
+        no gradient: ``logprobs_grad`` gives that of the logits."""
         f32, i32 = torch.float32, torch.int32
         x, dt, stride = self._logit_rows(logits, "logits")
         R, V = logits.shape
@@ -304,8 +305,10 @@ class Verifier:
         """Dense rows x [N, heads, head_dim] (bfloat16 or float16, any row and head
         strides) turned by positions (int32 [N], or [axes, N] with ``axes``, the axis of
         each pair: ``rotary_axes``) of the table ``rotary`` (``rotary_table``), pairs as
-        in ``KVCache.append``: specdec_rotate.  ``inverse`` turns back, which is also
-        the gradient.  Returns contiguous rows, or ``out``: x itself or rows of their own."""
+        in ``KVCache.append``: specdec_rotate.  ``inverse`` turns back (a table with a gain,
+        ``scaling="by_parts"``, is applied once more, not taken back), which is also the
+        gradient of a turn; the result itself carries none.  Returns contiguous rows, or
+        ``out``: x itself or rows of their own."""
         if x.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float16) or x.get_device() != self._at:
             raise ValueError("x must be bfloat16 or float16 [N, heads, head_dim] on the device")
         N, heads, D = x.shape
