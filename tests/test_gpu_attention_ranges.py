@@ -207,3 +207,39 @@ def test_ranges_of_short_and_long_tables(V, dtype, width):
     assert V.get_error() == 0
     want, big = reference(s, False)
     assert ((out.double() - want).abs() <= attend_tolerance(s, want, big)).all()
+
+
+@pytest.mark.parametrize("cross", [False, True])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (BF, E4), (HF, E4)])
+@pytest.mark.parametrize("rows,heads", KERNELS)
+@pytest.mark.parametrize("rising", [False, True])
+def test_references_that_move_often(V, cross, dtype, cache, rows, heads, rising):
+    # scores tens of units of log 2 apart, in no order or rising along the keys: every lag is passed,
+    # in every part of a tile, while the next scores are under way
+    s = Step(ctx=[700], nodes=[rows], dtype=dtype, cache=cache, seed=11, poison=False, **heads)
+    s.q.mul_(8.0)
+    if rising:
+        s.q[..., :4] = s.q[..., :4].abs() + 4
+        for slot in range(s.ctx[0] + rows):
+            page, off = s.row(0, slot)
+            up = torch.tensor(0.008 * slot).to(dtype).float()
+            if s.ks is None:
+                s.k[page, :, off, :4] = up
+            else:
+                s.k[page, :, off, :4] = (up / s.ks[page, :, off])[:, None].clamp(max=448).to(E4)
+    out = attend(V, s, cross)
+    assert V.get_error() == 0
+    want, big = reference(s, cross)
+    # attend_tolerance with the scores' error of these inputs: float32 sums of D products, D 2^-24 of
+    # the sum of their magnitudes (twice that for a pair of weights), and over e4m3 keys in tiles the
+    # queries' parts, 2^-17 of a row's largest value
+    K = s.values("k").abs()
+    pages = torch.tensor(s.pages[0], device=K.device)[torch.arange(s.ctx[0] + rows, device=K.device) // s.page]
+    k = K[pages, :, torch.arange(s.ctx[0] + rows, device=K.device) % s.page]
+    q = s.q[:s.n_rows].double().abs().view(-1, s.kv_heads, s.group, s.head_dim)
+    size = torch.einsum("nhgd,shd->nhgs", q, k).amax(-1)
+    d = s.head_dim * 2.0 ** -24 * size
+    if s.ks is not None:
+        d = d + 2.0 ** -17 * q.amax(-1) * k.sum(-1).amax(0)[None, :, None]
+    d = (d * s.head_dim ** -0.5).view(-1, s.heads, 1)
+    assert ((out.double() - want).abs() <= attend_tolerance(s, want, big) + 2 * d * big[..., None]).all()
